@@ -10,6 +10,13 @@
  *   mep_prefetch    redundant experts' weights copied into their slots
  *   mep_dispatch_backward / mep_combine_backward   the two permutes' gradients
  *   mep_grouped_gemm  the grouped expert product that consumes the buffer
+ *   mep_grouped_wgrad the experts' weight gradients, from that buffer and the
+ *                   gradient of the product; what mep_reduce_grad folds
+ *   mep_layer_norm / mep_layer_norm_backward   the norm in front of the router
+ *   mep_swiglu / mep_swiglu_backward           the experts' gated activation
+ *   mep_ckpt_save / mep_ckpt_load   activations kept in 8 bits for the backward
+ *                   pass (the norm, the activation and mep_grouped_wgrad write
+ *                   or read them directly)
  *   mep_plan_remote_fallback / mep_plan_static_scratch   planner variants
  *   mep_wait_selftest  the kernels' bounded wait, run on a barrier that never completes
  *
@@ -75,6 +82,13 @@ typedef uint16_t mep_bf16;
 #define MEP_MAX_R 1024     /* ranks */
 #define MEP_MAX_K 64       /* experts per token */
 #define MEP_MAX_SLOTS 32768 /* R * B */
+#define MEP_MAX_NORM_H 16384      /* columns of a layer norm */
+#define MEP_MAX_CKPT_C (1 << 24)  /* columns of a checkpoint row, of a gated activation */
+
+/* Element types of the training operators' tensors. */
+#define MEP_BF16 0
+#define MEP_F32 1
+#define MEP_CKPT8 2  /* checkpoint rows, see mep_ckpt_save */
 
 /* Library version, (major << 16) | minor. */
 MEP_API int mep_version(void);
@@ -346,6 +360,140 @@ MEP_API int mep_grouped_gemm(const mep_bf16* x, const int32_t* cu_seqlens, const
                              const mep_bf16* w_slot, int32_t* status, int R, int S, int K, int E,
                              int B, int H, int Hp, void* ws, size_t ws_bytes, mep_bf16* y,
                              void* stream);
+
+/*
+ * mep_ckpt_save / mep_ckpt_load -- an activation kept in 8 bits between the
+ * forward and the backward pass, and its values back. (The pages keep the
+ * static buffer as it is and say nothing on checkpoints; the format is this
+ * library's.) A checkpoint row of C columns is mep_ckpt_row_bytes(C) bytes, a
+ * multiple of 32:
+ *   [0, C)                 q, signed bytes
+ *   [align16(C), + nb)     s, one scale byte per block of 128 columns,
+ *                          nb = ceil(C / 128) (the last block may be short)
+ *   the rest               zero
+ * and stands for the values q * 2^(s - 127). With a = the block's largest
+ * magnitude, k = max(floor(log2 a) - 6, -126), s = k + 127 and q = x * 2^-k
+ * rounded to nearest-even and kept within +-127: a bf16 x is kept to within
+ * 2^(k-1), at most a / 128. A block that holds an infinity or a NaN has
+ * s = 255 and stands for NaN throughout. The values are exact in bf16.
+ * Rows are plain bytes: mep_dispatch, given them as bf16 [R*S, row bytes / 2],
+ * permutes them into the buffer's order, so that a token is kept once, not K
+ * times, and permuted again in the backward pass.
+ *   x       bf16 or fp32 [N, C]   x_type MEP_BF16 or MEP_F32
+ *   C       1 .. MEP_MAX_CKPT_C
+ *   ckpt    uint8 [N, mep_ckpt_row_bytes(C)]   every byte written by save
+ * Input and output must not overlap.
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_ckpt_row_bytes(int64_t C, size_t* bytes);
+MEP_API int mep_ckpt_save(const void* x, int x_type, int64_t N, int64_t C, uint8_t* ckpt,
+                          void* stream);
+MEP_API int mep_ckpt_load(const uint8_t* ckpt, int64_t N, int64_t C, int x_type, void* x,
+                          void* stream);
+
+/*
+ * mep_layer_norm -- y = (x - mean) * rstd * weight + bias over each row, with
+ *   mean = sum_h x / H,  rstd = 1 / sqrt(sum_h (x - mean)^2 / H + eps),
+ * both in fp32 (the second sum over the centred row), y rounded once to x's
+ * type.
+ *   x        bf16 or fp32 [N, H]   x_type; 1 <= H <= MEP_MAX_NORM_H
+ *   weight   bf16 or fp32 [H]      p_type; NULL: 1
+ *   bias     the same              NULL: 0
+ *   y        x_type [N, H]         output
+ *   mean, rstd  fp32 [N]           outputs, for the backward pass
+ *   x_ckpt   uint8 [N, mep_ckpt_row_bytes(H)]   x in 8 bits, for
+ *            mep_layer_norm_backward; NULL: not kept
+ *   y_ckpt   the same              y (as rounded) in 8 bits, for
+ *            mep_grouped_wgrad after mep_dispatch; NULL: not kept
+ * Outputs must not overlap the inputs or one another.
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG (also for eps < 0), MEP_ERR_CUDA.
+ */
+MEP_API int mep_layer_norm(const void* x, int x_type, const void* weight, const void* bias,
+                           int p_type, float eps, int64_t N, int64_t H, void* y, float* mean,
+                           float* rstd, uint8_t* x_ckpt, uint8_t* y_ckpt, void* stream);
+
+/*
+ * mep_layer_norm_backward -- with xhat = (x - mean) * rstd and t = dy * weight,
+ *   dx      = rstd * (t - sum_h t / H - xhat * sum_h (t * xhat) / H)
+ *   dweight = sum_rows dy * xhat,   dbias = sum_rows dy,
+ * all sums in fp32, dx rounded once. The sums over rows go through partial
+ * sums in the workspace, added in a fixed order: the same call gives the same
+ * bits.
+ *   dy       bf16 or fp32 [N, H]   dy_type
+ *   x        [N, H] of dy_type, or checkpoint rows [N, mep_ckpt_row_bytes(H)]
+ *            (x_type MEP_CKPT8: the norm's x_ckpt)
+ *   weight   bf16 or fp32 [H]      p_type; NULL: 1
+ *   mean, rstd  fp32 [N]           from mep_layer_norm
+ *   ws       device scratch of >= mep_layer_norm_backward_workspace_bytes
+ *            bytes; may be NULL when dweight and dbias are
+ *   dx       dy_type [N, H]        output
+ *   dweight, dbias  fp32 [H]       outputs (accumulate != 0: added to); each
+ *                                  may be NULL
+ * Outputs must not overlap the inputs or one another. N == 0 leaves dx alone
+ * and makes dweight and dbias 0 (accumulate: leaves them alone).
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_layer_norm_backward_workspace_bytes(int64_t N, int64_t H, size_t* bytes);
+MEP_API int mep_layer_norm_backward(const void* dy, int dy_type, const void* x, int x_type,
+                                    const void* weight, int p_type, const float* mean,
+                                    const float* rstd, int64_t N, int64_t H, void* ws,
+                                    size_t ws_bytes, void* dx, float* dweight, float* dbias,
+                                    int accumulate, void* stream);
+
+/*
+ * mep_swiglu -- the experts' gated activation between the two projections:
+ * with g = gu[row, 0, :] and u = gu[row, 1, :],
+ *   a = bf16_rn( g * sigmoid(g) * u )       (fp32 inside)
+ *   gu     bf16 [rows, 2, F]    the first projection's output, H' = 2F
+ *   a      bf16 [rows, F]       output, the second projection's input
+ *   ckpt   uint8 [rows, 2, mep_ckpt_row_bytes(F)]   gu in 8 bits, as
+ *          mep_ckpt_save keeps it seen as [2 * rows, F]; NULL: not kept
+ * mep_swiglu_backward -- from da, and gu as it was or as it was kept:
+ *   dg = da * u * sigmoid(g) * (1 + g * (1 - sigmoid(g))),
+ *   du = da * g * sigmoid(g),   a as above, once more (the second
+ *   projection's mep_grouped_wgrad needs it)
+ *   da     bf16 [rows, F]
+ *   gu     bf16 [rows, 2, F] (gu_type MEP_BF16) or checkpoint rows (MEP_CKPT8)
+ *   dgu    bf16 [rows, 2, F]    output: dg, du
+ *   a      bf16 [rows, F]       output; NULL: not computed
+ * Outputs must not overlap the inputs. rows < 2^30.
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16* a, uint8_t* ckpt,
+                       void* stream);
+MEP_API int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_type, int64_t rows,
+                                int64_t F, mep_bf16* dgu, mep_bf16* a, void* stream);
+
+/*
+ * mep_grouped_wgrad -- gradients of mep_grouped_gemm's weights: the fp32
+ * tensors that mep_reduce_grad reads ("月之暗面开源MoonEP：面向MoE训练的专家并行
+ * 通信库", 内存契约与权重布局, gradient paragraph).
+ *   home_grad[e]    = sum over every rank's rows of group e of   x[row]^T dy[row]
+ *   slot_grad[r][b] = sum over rank r's rows of group E + b of   x[row]^T dy[row]
+ * (groups as in mep_grouped_gemm), products exact, sums in fp32. The order of
+ * the sums is fixed: the same call gives the same bits.
+ *   x          bf16 [R*S*K, H] (x_type MEP_BF16), or checkpoint rows
+ *              [R*S*K, mep_ckpt_row_bytes(H)] (MEP_CKPT8)
+ *   dy         bf16 [R*S*K, H']     gradient of the product
+ *   cu_seqlens int32 [R, E+B]       inclusive group ends, from mep_plan
+ *   status     int32 [1]            as for mep_grouped_gemm; may be NULL
+ *   H, Hp (= H')  multiples of 8
+ *   accumulate 0: home_grad is overwritten (0 where no rank has rows of the
+ *              expert), and so are the slots that have rows; slots without
+ *              rows are left alone. Not 0: added to what is there.
+ *   ws         device workspace of at least mep_grouped_wgrad_workspace_bytes
+ *              (rebuilt by every call)
+ *   home_grad  fp32 [E, H, H']      output
+ *   slot_grad  fp32 [R, B, H, H']   output; may be NULL when B == 0
+ * Outputs must not overlap the inputs.
+ * Host returns: as mep_grouped_gemm (x, dy and the gradients must be device
+ * memory of the current device).
+ */
+MEP_API int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int B, size_t* bytes);
+MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
+                              const int32_t* cu_seqlens, int32_t* status, int R, int S, int K, int E,
+                              int B, int H, int Hp, int accumulate, void* ws, size_t ws_bytes,
+                              float* home_grad, float* slot_grad, void* stream);
 
 /*
  * mep_wait_selftest -- exercises the bounded wait that every pipeline wait

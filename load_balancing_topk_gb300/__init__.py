@@ -18,7 +18,16 @@ Entry points (same names as the C ABI):
   slots zeroed;
 * :func:`mep_prefetch` -- redundant experts' weights copied into their slots;
 * :func:`mep_dispatch_backward` / :func:`mep_combine_backward` -- gradients of
-  the two permutes.
+  the two permutes;
+* :func:`mep_grouped_gemm` -- the experts' product over the buffer, and
+  :func:`mep_grouped_wgrad` -- its weight gradients, for mep_reduce_grad;
+* :func:`mep_layer_norm` / :func:`mep_layer_norm_backward` -- the norm in front
+  of the router;
+* :func:`mep_swiglu` / :func:`mep_swiglu_backward` -- the experts' gated
+  activation;
+* :func:`mep_ckpt_save` / :func:`mep_ckpt_load` -- activations kept in 8 bits
+  for the backward pass; the norm and the activation write them as they go, and
+  all three backward operators read them directly.
 """
 
 from __future__ import annotations
@@ -32,6 +41,9 @@ __all__ = [
     "MepError", "Plan", "library_path", "load_library", "status_string", "version",
     "plan_workspace_bytes", "plan_kernel_count", "mep_plan", "mep_plan_remote_fallback", "mep_dispatch", "mep_combine", "mep_reduce_grad",
     "mep_prefetch", "mep_dispatch_backward", "mep_combine_backward", "STATUS",
+    "grouped_gemm_workspace_bytes", "mep_grouped_gemm", "grouped_wgrad_workspace_bytes", "mep_grouped_wgrad",
+    "ckpt_row_bytes", "mep_ckpt_save", "mep_ckpt_load", "layer_norm_backward_workspace_bytes", "mep_layer_norm",
+    "mep_layer_norm_backward", "mep_swiglu", "mep_swiglu_backward",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -56,6 +68,9 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 # (name, restype, argtypes) of every function include/mep.h declares.
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+# element types of the training operators (MEP_BF16, MEP_F32, MEP_CKPT8)
+_BF16, _F32, _CKPT8 = 0, 1, 2
 SIGNATURES = [
     ("mep_version", _I, []),
     ("mep_status_string", ctypes.c_char_p, [_I]),
@@ -73,6 +88,18 @@ SIGNATURES = [
     ("mep_grouped_gemm_workspace_bytes", _I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     ("mep_grouped_gemm", _I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
                               _VP, _VP]),
+    ("mep_ckpt_row_bytes", _I, [_L, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_ckpt_save", _I, [_VP, _I, _L, _L, _VP, _VP]),
+    ("mep_ckpt_load", _I, [_VP, _L, _L, _I, _VP, _VP]),
+    ("mep_layer_norm", _I, [_VP, _I, _VP, _VP, _I, ctypes.c_float, _L, _L, _VP, _VP, _VP, _VP, _VP, _VP]),
+    ("mep_layer_norm_backward_workspace_bytes", _I, [_L, _L, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_layer_norm_backward", _I, [_VP, _I, _VP, _I, _VP, _I, _VP, _VP, _L, _L, _VP, ctypes.c_size_t, _VP,
+                                     _VP, _VP, _I, _VP]),
+    ("mep_swiglu", _I, [_VP, _L, _L, _VP, _VP, _VP]),
+    ("mep_swiglu_backward", _I, [_VP, _VP, _I, _L, _L, _VP, _VP, _VP]),
+    ("mep_grouped_wgrad_workspace_bytes", _I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_grouped_wgrad", _I, [_VP, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
+                               _VP, _VP, _VP]),
     ("mep_wait_selftest", _I, [_VP, ctypes.c_int64, _VP, _VP]),
 ]
 
@@ -433,6 +460,293 @@ def mep_grouped_gemm(x, cu_seqlens, w_home, w_slot, status, R: int, S: int, K: i
                                              _stream(dev))
     _check("mep_grouped_gemm", rc)
     return y
+
+
+def ckpt_row_bytes(C: int) -> int:
+    """Bytes of one checkpoint row of C columns (a multiple of 32)."""
+    out = ctypes.c_size_t(0)
+    _check("mep_ckpt_row_bytes", load_library().mep_ckpt_row_bytes(int(C), ctypes.byref(out)))
+    return int(out.value)
+
+
+def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("mep_layer_norm_backward_workspace_bytes",
+           load_library().mep_layer_norm_backward_workspace_bytes(int(N), int(H), ctypes.byref(out)))
+    return int(out.value)
+
+
+def grouped_wgrad_workspace_bytes(R: int, S: int, K: int, E: int, B: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("mep_grouped_wgrad_workspace_bytes",
+           load_library().mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, ctypes.byref(out)))
+    return int(out.value)
+
+
+def _float_type(t, name) -> int:
+    """MEP_BF16 or MEP_F32 of a tensor that may be either."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    return _BF16 if t.dtype == torch.bfloat16 else _F32
+
+
+def _need_params(weight, bias, H, dev) -> int:
+    """Checks a norm's weight and bias (each may be None); their type."""
+    kind = None
+    for name, p in (("weight", weight), ("bias", bias)):
+        if p is None:
+            continue
+        t = _float_type(p, name)
+        _need(p, name, p.dtype, (H,), dev)
+        if kind is not None and t != kind:
+            raise TypeError("weight and bias must have the same dtype")
+        kind = t
+    return _F32 if kind is None else kind
+
+
+def mep_ckpt_save(x, ckpt=None):
+    """x (bf16 or fp32 [N, C]) in 8 bits: checkpoint rows, uint8 [N, ckpt_row_bytes(C)].
+
+    Signed bytes with one power-of-two scale per 128 columns, in one row, so
+    that mep_dispatch can permute the rows seen as bf16.
+    """
+    torch = _torch()
+    kind = _float_type(x, "x")
+    _need(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, C]")
+    N, C = x.shape
+    rb = ckpt_row_bytes(C)
+    dev = x.device
+    if ckpt is None:
+        ckpt = torch.empty((N, rb), dtype=torch.uint8, device=dev)
+    else:
+        _need(ckpt, "ckpt", torch.uint8, (N, rb), dev)
+    with torch.cuda.device(dev):
+        rc = load_library().mep_ckpt_save(_ptr(x), kind, N, C, _ptr(ckpt), _stream(dev))
+    _check("mep_ckpt_save", rc)
+    return ckpt
+
+
+def mep_ckpt_load(ckpt, C: int, x=None, dtype=None):
+    """The values of checkpoint rows (uint8 [N, ckpt_row_bytes(C)]): [N, C] in x's
+    dtype, or ``dtype`` (bf16 unless given; both hold the values exactly)."""
+    torch = _torch()
+    _need(ckpt, "ckpt", torch.uint8)
+    rb = ckpt_row_bytes(C)
+    if ckpt.dim() != 2 or ckpt.shape[1] != rb:
+        raise ValueError(f"ckpt must be [N, {rb}] for {C} columns")
+    N, dev = ckpt.shape[0], ckpt.device
+    if x is None:
+        x = torch.empty((N, C), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+    kind = _float_type(x, "x")
+    _need(x, "x", x.dtype if dtype is None else dtype, (N, C), dev)
+    with torch.cuda.device(dev):
+        rc = load_library().mep_ckpt_load(_ptr(ckpt), N, C, kind, _ptr(x), _stream(dev))
+    _check("mep_ckpt_load", rc)
+    return x
+
+
+def mep_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=None, rstd=None,
+                   x_ckpt=None, y_ckpt=None):
+    """(y, mean, rstd) of the layer norm of every row of x (bf16 or fp32 [N, H]).
+
+    weight, bias: bf16 or fp32 [H], or None. y has x's dtype; mean and rstd are
+    fp32 [N]. x_ckpt, y_ckpt: uint8 [N, ckpt_row_bytes(H)] to keep x (for
+    mep_layer_norm_backward) and y (for mep_grouped_wgrad) in, or None.
+    """
+    torch = _torch()
+    kind = _float_type(x, "x")
+    _need(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, H]")
+    N, H = x.shape
+    dev = x.device
+    p_kind = _need_params(weight, bias, H, dev)
+    y = torch.empty_like(x) if y is None else _need(y, "y", x.dtype, (N, H), dev)
+    stats = []
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        stats.append(torch.empty(N, dtype=torch.float32, device=dev) if t is None
+                     else _need(t, name, torch.float32, (N,), dev))
+    mean, rstd = stats
+    for name, t in (("x_ckpt", x_ckpt), ("y_ckpt", y_ckpt)):
+        if t is not None:
+            _need(t, name, torch.uint8, (N, ckpt_row_bytes(H)), dev)
+    with torch.cuda.device(dev):
+        rc = load_library().mep_layer_norm(_ptr(x), kind, _ptr(weight), _ptr(bias), p_kind, eps, N, H,
+                                           _ptr(y), _ptr(mean), _ptr(rstd), _ptr(x_ckpt),
+                                           _ptr(y_ckpt), _stream(dev))
+    _check("mep_layer_norm", rc)
+    return y, mean, rstd
+
+
+def mep_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,
+                            accumulate: bool = False, params: bool = True, workspace=None):
+    """(dx, dweight, dbias) of mep_layer_norm.
+
+    dy: bf16 or fp32 [N, H]; x: the norm's input in dy's dtype, or its
+    checkpoint rows (uint8, the norm's x_ckpt); weight: as in the forward pass.
+    dx has dy's dtype, dweight and dbias are fp32 [H] (added to where
+    ``accumulate``). ``params=False``: dx alone, (dx, None, None).
+    """
+    torch = _torch()
+    kind = _float_type(dy, "dy")
+    _need(dy, "dy", dy.dtype)
+    if dy.dim() != 2:
+        raise ValueError("dy must be [N, H]")
+    N, H = dy.shape
+    dev = dy.device
+    if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
+        x_kind = _CKPT8
+        _need(x, "x", torch.uint8, (N, ckpt_row_bytes(H)), dev)
+    else:
+        x_kind = kind
+        _need(x, "x", dy.dtype, (N, H), dev)
+    p_kind = _need_params(weight, None, H, dev)
+    _need(mean, "mean", torch.float32, (N,), dev)
+    _need(rstd, "rstd", torch.float32, (N,), dev)
+    dx = torch.empty_like(dy) if dx is None else _need(dx, "dx", dy.dtype, (N, H), dev)
+    need = 0
+    if params:
+        if accumulate and (dweight is None or dbias is None):
+            raise ValueError("accumulate needs dweight and dbias to add to")
+        grads = []
+        for name, t in (("dweight", dweight), ("dbias", dbias)):
+            grads.append(torch.empty(H, dtype=torch.float32, device=dev) if t is None
+                         else _need(t, name, torch.float32, (H,), dev))
+        dweight, dbias = grads
+        need = layer_norm_backward_workspace_bytes(N, H)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            _need(workspace, "workspace", torch.uint8, None, dev)
+            if workspace.numel() < need:
+                raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
+    elif dweight is not None or dbias is not None:
+        raise ValueError("params=False computes neither dweight nor dbias")
+    with torch.cuda.device(dev):
+        rc = load_library().mep_layer_norm_backward(
+            _ptr(dy), kind, _ptr(x), x_kind, _ptr(weight), p_kind, _ptr(mean), _ptr(rstd), N, H,
+            _ptr(workspace) if params else None, need, _ptr(dx), _ptr(dweight), _ptr(dbias),
+            1 if accumulate else 0, _stream(dev))
+    _check("mep_layer_norm_backward", rc)
+    return dx, dweight, dbias
+
+
+def mep_swiglu(gu, a=None, ckpt=None):
+    """a = bf16(g * sigmoid(g) * u), g and u the two halves of every row of gu (bf16 [rows, 2F]).
+
+    ckpt: uint8 [rows, 2, ckpt_row_bytes(F)] to keep gu in for the backward pass, or None.
+    """
+    torch = _torch()
+    _need(gu, "gu", torch.bfloat16)
+    if gu.dim() != 2 or gu.shape[1] < 2 or gu.shape[1] % 2:
+        raise ValueError("gu must be [rows, 2F]")
+    rows, F = gu.shape[0], gu.shape[1] // 2
+    dev = gu.device
+    if a is None:
+        a = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(a, "a", torch.bfloat16, (rows, F), dev)
+    if ckpt is not None:
+        _need(ckpt, "ckpt", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
+    with torch.cuda.device(dev):
+        rc = load_library().mep_swiglu(_ptr(gu), rows, F, _ptr(a), _ptr(ckpt), _stream(dev))
+    _check("mep_swiglu", rc)
+    return a
+
+
+def mep_swiglu_backward(da, gu, dgu=None, a=None, again: bool = True):
+    """(dgu, a) of mep_swiglu from da (bf16 [rows, F]) and gu (bf16 [rows, 2F], or the
+    checkpoint rows kept of it, uint8 [rows, 2, ckpt_row_bytes(F)]).
+
+    dgu: bf16 [rows, 2F]. a: the activation once more, computed from what gu
+    stands for (None where ``again`` is false).
+    """
+    torch = _torch()
+    _need(da, "da", torch.bfloat16)
+    if da.dim() != 2:
+        raise ValueError("da must be [rows, F]")
+    rows, F = da.shape
+    dev = da.device
+    if isinstance(gu, torch.Tensor) and gu.dtype == torch.uint8:
+        kind = _CKPT8
+        _need(gu, "gu", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
+    else:
+        kind = _BF16
+        _need(gu, "gu", torch.bfloat16, (rows, 2 * F), dev)
+    if dgu is None:
+        dgu = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(dgu, "dgu", torch.bfloat16, (rows, 2 * F), dev)
+    if not again:
+        if a is not None:
+            raise ValueError("again=False does not compute a")
+    elif a is None:
+        a = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(a, "a", torch.bfloat16, (rows, F), dev)
+    with torch.cuda.device(dev):
+        rc = load_library().mep_swiglu_backward(_ptr(da), _ptr(gu), kind, rows, F, _ptr(dgu), _ptr(a),
+                                                _stream(dev))
+    _check("mep_swiglu_backward", rc)
+    return dgu, a
+
+
+def mep_grouped_wgrad(x, dy, cu_seqlens, home_grad, slot_grad, status, R: int, S: int, K: int,
+                      accumulate: bool = False, workspace=None):
+    """Weight gradients of mep_grouped_gemm, in place: home_grad[e] = sum of x[row]^T dy[row]
+    over the rows of group e of every rank, slot_grad[r, b] over rank r's rows of slot b.
+
+    x: bf16 [R*S*K, H], or checkpoint rows uint8 [R*S*K, ckpt_row_bytes(H)]; dy:
+    bf16 [R*S*K, H']; cu_seqlens: int32 [R, E+B]; home_grad: fp32 [E, H, H'];
+    slot_grad: fp32 [R, B, H, H'] (None when B == 0), as mep_reduce_grad reads
+    them. Slots without rows are left alone. Returns (home_grad, slot_grad).
+    """
+    torch = _torch()
+    _need(dy, "dy", torch.bfloat16)
+    dev = dy.device
+    _need(home_grad, "home_grad", torch.float32, None, dev)
+    if home_grad.dim() != 3:
+        raise ValueError("home_grad must be [E, H, H']")
+    E, H, Hp = home_grad.shape
+    _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
+    if cu_seqlens.dim() != 2 or cu_seqlens.shape[0] != R:
+        raise ValueError("cu_seqlens must be [R, E+B]")
+    B = cu_seqlens.shape[1] - E
+    if B < 0:
+        raise ValueError("cu_seqlens must have E+B columns")
+    rows = R * S * K
+    if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
+        kind, width = _CKPT8, ckpt_row_bytes(H)
+    else:
+        kind, width = _BF16, H
+    _need(x, "x", torch.uint8 if kind == _CKPT8 else torch.bfloat16, None, dev)
+    if x.numel() != rows * width:
+        raise ValueError(f"x must hold R*S*K rows of {width}")
+    if dy.numel() != rows * Hp:
+        raise ValueError("dy must hold R*S*K rows of H'")
+    if B > 0:
+        _need(slot_grad, "slot_grad", torch.float32, (R, B, H, Hp), dev)
+    if status is not None:
+        _need(status, "status", torch.int32, (1,), dev)
+    need = grouped_wgrad_workspace_bytes(R, S, K, E, B)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", torch.uint8, None, dev)
+        if workspace.numel() < need:
+            raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
+    with torch.cuda.device(dev):
+        rc = load_library().mep_grouped_wgrad(
+            _ptr(x), kind, _ptr(dy), _ptr(cu_seqlens), _ptr(status), R, S, K, E, B, H, Hp,
+            1 if accumulate else 0, _ptr(workspace), workspace.numel(), _ptr(home_grad),
+            _ptr(slot_grad) if B > 0 else None, _stream(dev))
+    _check("mep_grouped_wgrad", rc)
+    return home_grad, slot_grad
 
 
 def mep_wait_selftest(limit_ns: int, device=None):
