@@ -1,91 +1,609 @@
 // grouped_wgrad.cu -- the experts' weight gradients over the static buffer
-// (mep_grouped_wgrad).
+// (mep_grouped_wgrad), on the sm_100-family tensor cores (tcgen05 + TMA).
 //
 // Source: "月之暗面开源MoonEP：面向MoE训练的专家并行通信库", section
 // 内存契约与权重布局: the weights of one projection are one [E+B, H, H']
 // tensor, gradients are fp32, those of the prefetch slots lie in a buffer of
 // their own seen as [R, B, H, H'], which mep_reduce_grad folds into the home
 // experts' gradients.
+//
+// dW_j[h, n] = sum over the rows of group j of x[row, h] * dy[row, n]: a
+// product whose inner dimension is the ragged one. Both operands lie with the
+// outer dimension contiguous (M- and N-major), so TMA boxes of 64 rows x 64
+// columns are tensor-core operands as they come.
+//
+// Two launches on the caller's stream:
+//   k_wgrad_groups  (1 CTA) checks every cu_seqlens row and lists the weight
+//                   rows that have to be written, each with its row segments
+//                   (one per rank that has rows of it);
+//   k_wgrad_pair    persistent clusters of two CTAs, one per SM, 512 threads
+//                   each, over units (weight row, 256 rows of H, 256 columns
+//                   of H'), grid-stride. CTA r of a pair owns 128 of the 256
+//                   rows of H. Per step of 64 buffer rows:
+//     warp 0      TMA producer: this CTA's 128 columns of x (bf16 boxes, or
+//                 the checkpoint's bytes and their 64 scale bytes) and its
+//                 half of the 256 columns of dy, into a ring of stages;
+//     warps 4..7  converter: checkpoint bytes to bf16 operand boxes (exact:
+//                 q * 2^k has 8 significant bits), and zeros over the rows
+//                 that a segment's last step takes from the next group, in
+//                 both operands (a NaN there would survive a product with 0);
+//     warp 1      of CTA 0 issues the pair MMAs (tcgen05.mma.cta_group::2,
+//                 M = 256, N = 256 or 128, K = 16) into one of two TMEM
+//                 accumulators, which changes every kChunk steps;
+//     warps 8..15 add each finished accumulator to fp32 sums in registers
+//                 (128 a thread), and at the end of the unit write them
+//                 through shared memory with bulk tensor stores, or bulk
+//                 tensor additions.
+// The sums leave TMEM every kChunk * 64 rows because the tensor cores do not
+// round their fp32 additions to nearest: over a long group the error of one
+// accumulator grows with the number of steps, that of the registers' sums,
+// rounded to nearest, with its root.
+// Every wait is bounded as in grouped_gemm.cu.
 
 #include "ckpt.cuh"
+#include "tc.cuh"
+
+#ifndef MEP_WGRAD_CHUNK
+#define MEP_WGRAD_CHUNK 4
+#endif
 
 namespace mep {
 namespace {
 
-constexpr int kT = 64;   // tile edge
-constexpr int kRows = 16;
+constexpr int kBM = 128;                 // rows of H per CTA
+constexpr int kBN = 256;                 // columns of H' per pair
+constexpr int kBK = 64;                  // buffer rows per step
+constexpr int kBox = kBK * 64 * 2;       // one 64 x 64 bf16 box, 8 KB
+constexpr int kOp = 2 * kBox;            // an operand's two boxes, 16 KB
+constexpr int kQ = kBK * kBM;            // checkpoint bytes of a step, 8 KB
+constexpr int kScale = kBK * 16;         // their scale bytes, in 16-byte rows
+constexpr int kChunk = MEP_WGRAD_CHUNK;  // steps summed in TMEM
+constexpr int kThreads = 512;
+constexpr int kTmemCols = 2 * kBN;
+constexpr int kGroupThreads = 1024;
+constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
+constexpr int kEpiWarps = 8;
+constexpr int kPair = 2;
 
-__global__ void __launch_bounds__(1024)
-    k_wgrad_check(const int32_t* __restrict__ cu, int R, int G, int SK, int32_t* status, int* ok) {
+template <bool CKPT> struct Ring {
+  static constexpr int stage = 2 * kOp + (CKPT ? kQ + kScale : 0);
+  static constexpr int stages = CKPT ? 4 : 6;
+  static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * kStoreBox + 512;
+  static_assert(smem <= 232448, "the ring must fit in 227 KB of shared memory");
+};
+
+struct Smem {
+  uint64_t full[6], ready[6], empty[6], tfull[2], tempty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int count;
+};
+
+// wait_phase without a call: the converter and epilogue warps hold their
+// sums in registers across it. All lanes of the warp get the same answer.
+template <bool HONOR>
+__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort,
+                                            int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u) {
+      if (HONOR && *abort) return false;
+      const uint64_t now = globaltimer();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > MEP_GEMM_TIMEOUT_NS) {
+        *abort = 1;
+        set_status(status, MEP_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          int32_t* status) {
+  return __all_sync(MEP_FULL_MASK, wait_inline<true>(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z,
+                                             uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, int x, int y, int z,
+                                           uint32_t src) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read_0() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// bf16 in, fp32 accumulate, A and B both with their outer dimension contiguous.
+constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                            ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                             ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+
+// ---------------------------------------------------------------------------
+// The weight rows to write: entries[i] = {weight row, first segment, segments,
+// steps}, weight row < E a home expert and E + r*B + b slot b of rank r;
+// segs[j] = {first buffer row, rows}. Without `accumulate` a home expert is
+// listed even without rows (it is written as zero), a slot never is.
+__global__ void __launch_bounds__(kGroupThreads)
+    k_wgrad_groups(const int32_t* __restrict__ cu, int R, int E, int B, int SK, int accumulate,
+                   int32_t* status, int* __restrict__ count, int4* __restrict__ entries,
+                   int2* __restrict__ segs) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ int s_bad;
-  if (threadIdx.x == 0) s_bad = read_status(status) != 0 ? 2 : 0;
+  __shared__ int s_warp[33], s_entry[kGroupThreads + 1], s_seg[kGroupThreads + 1];
+  __shared__ int s_bad, s_entries, s_segs, s_stat;
+  const int G = E + B;
+  if (threadIdx.x == 0) {
+    s_bad = s_entries = s_segs = 0;
+    s_stat = read_status(status);
+  }
   __syncthreads();
+  if (s_stat != 0) {
+    if (threadIdx.x == 0) *count = 0;
+    return;
+  }
   for (long long p = threadIdx.x; p < (long long)R * G; p += blockDim.x) {
     const int j = int(p % G), v = cu[p], prev = j == 0 ? 0 : cu[p - 1];
-    if (v < prev || (j == G - 1 && v != SK)) s_bad = s_bad | 1;
+    if (v < prev || (j == G - 1 && v != SK)) s_bad = 1;
   }
   __syncthreads();
+  if (s_bad) {
+    if (threadIdx.x == 0) {
+      *count = 0;
+      set_status(status, MEP_ERR_BAD_SEQLENS);
+    }
+    return;
+  }
+  const int W = E + R * B;
+  for (int base = 0; base < W; base += blockDim.x) {
+    const int w = base + threadIdx.x;
+    const bool home = w < E;
+    const int j = home ? w : (w < W ? E + (w - E) % B : 0);
+    const int r0 = home ? 0 : (w < W ? (w - E) / B : 0), r1 = w < W ? (home ? R : r0 + 1) : r0;
+    int nseg = 0, steps = 0;
+    for (int r = r0; r < r1; ++r) {
+      const long long p = (long long)r * G + j;
+      const int len = cu[p] - (j == 0 ? 0 : cu[p - 1]);
+      nseg += len > 0;
+      steps += (len + kBK - 1) / kBK;
+    }
+    const bool listed = w < W && (nseg > 0 || (home && !accumulate));
+    s_entry[threadIdx.x] = listed;
+    s_seg[threadIdx.x] = nseg;
+    __syncthreads();
+    block_excl_scan(s_entry, s_entry, blockDim.x, s_warp, true);
+    block_excl_scan(s_seg, s_seg, blockDim.x, s_warp, true);
+    if (listed) {
+      int at = s_segs + s_seg[threadIdx.x];
+      entries[s_entries + s_entry[threadIdx.x]] = make_int4(w, at, nseg, steps);
+      for (int r = r0; r < r1; ++r) {
+        const long long p = (long long)r * G + j;
+        const int lo = j == 0 ? 0 : cu[p - 1], len = cu[p] - lo;
+        if (len > 0) segs[at++] = make_int2(int((long long)r * SK + lo), len);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s_entries += s_entry[blockDim.x];
+      s_segs += s_seg[blockDim.x];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *count = s_entries;
+}
+
+// Two signed bytes of w (chosen by sel) times a power of two, as two bf16.
+// The bytes are placed under 0x43 (bf16 128 + low seven bits, or 256 + ...
+// where the sign bit is set): v = 128 + low7, c = 128 or 256, v - c = q
+// exactly, and q * step has 8 significant bits.
+__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bfloat162 step) {
+  const uint32_t x = __byte_perm(w, 0x43434343u, sel);
+  const uint32_t v = x & 0xff7fff7fu, c = x & 0xff80ff80u;
+  const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
+  const __nv_bfloat162 r = __hmul2(q, step);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// ---------------------------------------------------------------------------
+template <bool CKPT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_wgrad_pair(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_s,
+                 const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_home,
+                 const __grid_constant__ CUtensorMap map_slot, const int* __restrict__ count_ptr,
+                 const int4* __restrict__ entries, const int2* __restrict__ segs, int32_t* status,
+                 int E, int H, int Hp, int accumulate) {
+  constexpr int kSt = Ring<CKPT>::stages, kStage = Ring<CKPT>::stage;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gen_base = smem_raw + (base - raw);
+  const uint32_t out_box = base + kSt * kStage;
+  Smem* S = reinterpret_cast<Smem*>(gen_base + kSt * kStage + kEpiWarps * kStoreBox);
+  volatile int* abort_flag = &S->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = int(cluster_rank());
+  const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    *ok = s_bad == 0;
-    if (s_bad == 1) set_status(status, MEP_ERR_BAD_SEQLENS);
+    for (int s = 0; s < kSt; ++s) {
+      mbar_init(smem_u32(&S->full[s]), 1);   // this CTA's producer and its bytes
+      mbar_init(smem_u32(&S->ready[s]), 8);  // CTA 0: four converter warps of each CTA
+      mbar_init(smem_u32(&S->empty[s]), 1);  // CTA 0's multicast commit
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(smem_u32(&S->tfull[a]), 1);
+      mbar_init(smem_u32(&S->tempty[a]), 2 * kEpiWarps);
+    }
+    mbar_init(smem_u32(&S->drain), 1);
+    S->abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_async_smem();
   }
-}
-
-template <bool CKPT>
-__device__ __forceinline__ float load_x(const void* x, long long r, int h, int H) {
-  if (!CKPT) return to_f32(static_cast<const __nv_bfloat16*>(x)[r * H + h]);
-  const uint8_t* row = static_cast<const uint8_t*>(x) + r * ckpt_row_bytes(H);
-  return float(int8_t(row[h])) * ckpt_step(row[ckpt_scale_at(H) + h / kCkptBlock]);
-}
-
-// One CTA per (weight row, 64 x 64 tile): 16 x 16 threads with 4 x 4 sums
-// each, 16 rows of x and dy at a time in shared memory.
-template <bool CKPT>
-__global__ void __launch_bounds__(256)
-    k_wgrad(const void* __restrict__ x, const __nv_bfloat16* __restrict__ dy,
-            const int32_t* __restrict__ cu, const int* __restrict__ ok, int R, int SK, int E, int B,
-            int H, int Hp, int accumulate, float* __restrict__ home, float* __restrict__ slot) {
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&S->tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   pdl_wait();
-  pdl_launch_dependents();
-  if (*ok == 0) return;
-  __shared__ float sx[kRows][kT], sd[kRows][kT];
-  const int G = E + B, wrow = blockIdx.z, h0 = blockIdx.y * kT, n0 = blockIdx.x * kT;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const bool is_home = wrow < E;
-  const int r0 = is_home ? 0 : (wrow - E) / B, r1 = is_home ? R : r0 + 1;
-  const int j = is_home ? wrow : E + (wrow - E) % B;
-  float acc[4][4] = {};
-  bool any = false;
-  for (int r = r0; r < r1; ++r) {
-    const int lo = j == 0 ? 0 : cu[r * G + j - 1], hi = cu[r * G + j];
-    for (int k0 = lo; k0 < hi; k0 += kRows) {
-      any = true;
-      for (int i = threadIdx.x; i < kRows * kT; i += 256) {
-        const int k = i / kT, c = i % kT;
-        const bool in = k0 + k < hi;
-        const long long row = (long long)r * SK + k0 + k;
-        sx[k][c] = in && h0 + c < H ? load_x<CKPT>(x, row, h0 + c, H) : 0.f;
-        sd[k][c] = in && n0 + c < Hp ? to_f32(dy[row * Hp + n0 + c]) : 0.f;
+  if (threadIdx.x == 0) S->count = read_status(status) != 0 ? 0 : *count_ptr;
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = S->tmem;
+  const int nM = (H + 2 * kBM - 1) / (2 * kBM), nN = (Hp + kBN - 1) / kBN;
+  const int tiles = nM * nN;
+  const long long units = (long long)S->count * tiles;
+  const long long u0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+
+  // the four warpgroups' registers: 40 + 88 + 192 + 192 = 4 x 128 at launch
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      if (lane == 0) {
+        // ---------------- TMA producer ----------------
+        uint32_t it = 0;
+        bool ok = true;
+        for (long long u = u0; ok && u < units; u += ustep) {
+          const int4 e = entries[u / tiles];
+          const int t = int(u % tiles);
+          const int h0 = t / nN * 2 * kBM + rank * kBM, n0 = t % nN * kBN;
+          const bool narrow = Hp - n0 <= 128;
+          const int c0 = n0 + rank * (narrow ? 64 : 128);
+          const int na = h0 >= H ? 0 : h0 + 64 < H ? 2 : 1;
+          const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
+          const uint32_t bytes = (CKPT ? (na > 0 ? kQ + kScale : 0) : na * kBox) + nb * kBox;
+          const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
+          for (int g = 0; ok && g < e.z; ++g) {
+            const int2 seg = segs[e.y + g];
+            for (int k = 0; k < seg.y; k += kBK, ++it) {
+              const int s = int(it % kSt);
+              if (!wait_phase(smem_u32(&S->empty[s]), ((it / kSt) & 1u) ^ 1u, abort_flag, status)) {
+                ok = false;
+                break;
+              }
+              const uint32_t bar = smem_u32(&S->full[s]), st = base + s * kStage;
+              mbar_expect_tx(bar, bytes);
+              if (CKPT) {
+                if (na > 0) {
+                  tma_load_2d(st + 2 * kOp, &map_x, h0, seg.x + k, bar);
+                  tma_load_2d(st + 2 * kOp + kQ, &map_s, sx, seg.x + k, bar);
+                }
+              } else {
+                for (int i = 0; i < na; ++i) tma_load_2d(st + i * kBox, &map_x, h0 + 64 * i, seg.x + k, bar);
+              }
+              for (int i = 0; i < nb; ++i)
+                tma_load_2d(st + kOp + i * kBox, &map_dy, c0 + 64 * i, seg.x + k, bar);
+            }
+          }
+        }
+        // this CTA's copies have landed, and every commit aimed at it has arrived
+        for (uint32_t j = it > kSt ? it - kSt : 0; j < it; ++j) {
+          wait_phase(smem_u32(&S->full[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
+          wait_phase(smem_u32(&S->empty[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
+        }
       }
-      __syncthreads();
-      for (int k = 0; k < kRows; ++k)
-        for (int a = 0; a < 4; ++a)
-          for (int b = 0; b < 4; ++b) acc[a][b] += sx[k][ty + 16 * a] * sd[k][tx + 16 * b];
-      __syncthreads();
+      __syncwarp();
+    } else if (warp == 1) {
+      if (lane == 0 && leader) {
+        // ---------------- MMA issuer (CTA 0 only) ----------------
+        uint32_t it = 0, ck = 0;
+        bool ok = true;
+        for (long long u = u0; ok && u < units; u += ustep) {
+          const int4 e = entries[u / tiles];
+          const int n0 = int(u % tiles) % nN * kBN;
+          const uint32_t idesc = Hp - n0 <= 128 ? kIdescN : kIdesc;
+          int step = 0;
+          for (int g = 0; ok && g < e.z; ++g) {
+            const int len = segs[e.y + g].y;
+            for (int k = 0; k < len; k += kBK, ++it, ++step) {
+              const uint32_t a = ck & 1u, d = tmem + a * kBN;
+              const int in_chunk = step % kChunk;
+              if (in_chunk == 0 &&
+                  !wait_phase(smem_u32(&S->tempty[a]), ((ck >> 1) & 1u) ^ 1u, abort_flag, status)) {
+                ok = false;
+                break;
+              }
+              const int s = int(it % kSt);
+              if (!wait_phase(smem_u32(&S->ready[s]), (it / kSt) & 1u, abort_flag, status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint32_t st = base + s * kStage;
+              const int left = len - k;
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk)
+                if (16 * kk < left)
+                  tc_mma2(d, sdesc(st + kk * 16 * 128, kBox, 1024),
+                          sdesc(st + kOp + kk * 16 * 128, kBox, 1024), (in_chunk | kk) != 0 ? 1u : 0u,
+                          idesc);
+              tc_commit2_mc(smem_u32(&S->empty[s]), 3);
+              if (in_chunk == kChunk - 1 || step == e.w - 1) {
+                tc_commit2_mc(smem_u32(&S->tfull[a]), 3);
+                ++ck;
+              }
+            }
+          }
+        }
+        tc_commit2(smem_u32(&S->drain));
+        wait_phase(smem_u32(&S->drain), 0u, abort_flag, status, false);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // ---------------- converter ----------------
+    // Thread t takes 16 columns (chunk t & 7) of rows t >> 3, + 16, + 32, + 48
+    // of the step. The bytes' box and the operand boxes are 128-byte
+    // swizzled; chunks 4..7 store their second half first, so that a quarter
+    // warp's stores cover all banks.
+    const int t = threadIdx.x - 128, chunk = t & 7, row0 = t >> 3;
+    uint32_t it = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < units; u += ustep) {
+      const int4 e = entries[u / tiles];
+      const int tile = int(u % tiles), h0 = tile / nN * 2 * kBM + rank * kBM;
+      const uint32_t sbyte = (uint32_t)(h0 / kCkptBlock) & 15u;
+      for (int g = 0; ok && g < e.z; ++g) {
+        const int len = segs[e.y + g].y;
+        for (int k = 0; k < len; k += kBK, ++it) {
+          const int s = int(it % kSt);
+          if (!warp_wait(smem_u32(&S->full[s]), (it / kSt) & 1u, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = base + s * kStage;
+          const int valid = min(kBK, len - k), need = (valid + 15) & ~15;
+          if (CKPT) {
+            if (h0 < H) {
+              const uint32_t q = st + 2 * kOp, sc = q + kQ;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 16 * i;
+                uint32_t v[4], sb;
+                lds128(q + row * 128 + ((chunk ^ (row & 7)) << 4), v);
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(sc + row * 16 + sbyte));
+                const uint32_t bits = (sb == (uint32_t)kCkptNan ? 0x7fffu : sb << 7) * 0x10001u;
+                const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&bits);
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const bool in = row < valid;
+                  o[2 * j] = in ? dequant2(v[j], 0x4140, step) : 0u;
+                  o[2 * j + 1] = in ? dequant2(v[j], 0x4342, step) : 0u;
+                }
+                const uint32_t dst = st + (chunk >> 2) * kBox + row * 128;
+                const int first = chunk >> 2, j0 = 2 * (chunk & 3) + first, j1 = 2 * (chunk & 3) + (first ^ 1);
+                sts128(dst + ((j0 ^ (row & 7)) << 4), first ? o[4] : o[0], first ? o[5] : o[1],
+                       first ? o[6] : o[2], first ? o[7] : o[3]);
+                sts128(dst + ((j1 ^ (row & 7)) << 4), first ? o[0] : o[4], first ? o[1] : o[5],
+                       first ? o[2] : o[6], first ? o[3] : o[7]);
+              }
+            }
+          }
+          if (valid < need)  // whole rows: the swizzle stays within a row
+            for (int i = t; i < (need - valid) * 32; i += 128) {
+              const int row = valid + (i >> 5), piece = i & 31;
+              if (CKPT && piece < 16) continue;
+              sts128(st + (piece >> 3) * kBox + row * 128 + ((piece & 7) << 4), 0u, 0u, 0u, 0u);
+            }
+          if (CKPT || valid < need) fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->ready[s]), 0));
+        }
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ---------------- sums and epilogue ----------------
+    // Warp q + 4 * half holds TMEM lanes (rows of H) [32q, 32q + 32) and
+    // columns [128 half, 128 half + 128) of the unit.
+    const int q = warp & 3, half = (warp - 8) >> 2;
+    const uint32_t box = out_box + (uint32_t)(warp - 8) * kStoreBox;
+    uint32_t ck = 0;
+    bool ok = true;
+    for (long long u = u0; ok && u < units; u += ustep) {
+      const int4 e = entries[u / tiles];
+      const int tile = int(u % tiles);
+      const int h = tile / nN * 2 * kBM + rank * kBM + 32 * q, n = tile % nN * kBN + 128 * half;
+      const int chunks = (e.w + kChunk - 1) / kChunk;
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int c = 0; c < chunks; ++c, ++ck) {
+        const uint32_t a = ck & 1u;
+        if (!warp_wait(smem_u32(&S->tfull[a]), (ck >> 1) & 1u, abort_flag, status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ta = tmem + a * kBN + 128 * half + ((uint32_t)(32 * q) << 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + 32 * i < Hp) {
+            uint32_t v[32];
+            tc_ld32_issue(ta + 32 * i, v);
+            tc_ld_wait(v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[32 * i + j] += __uint_as_float(v[j]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+      }
+      if (!ok) break;
+      const CUtensorMap* map = e.x < E ? &map_home : &map_slot;
+      const int z = e.x < E ? e.x : e.x - E;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (h < H && n + 32 * i < Hp) {
+          if (lane == 0) bulk_wait_read_0();
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            sts128(box + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(acc[32 * i + 4 * j]),
+                   __float_as_uint(acc[32 * i + 4 * j + 1]), __float_as_uint(acc[32 * i + 4 * j + 2]),
+                   __float_as_uint(acc[32 * i + 4 * j + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (accumulate)
+              tma_add_3d(map, n + 32 * i, h, z, box);
+            else
+              tma_store_3d(map, n + 32 * i, h, z, box);
+          }
+        }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (threadIdx.x == 0 && read_status(status) != 0) {
+    const uint64_t t0 = globaltimer();
+    while (globaltimer() - t0 < 100000ull) {
     }
   }
-  if (!any && (accumulate || !is_home)) return;
-  float* out = is_home ? home + (long long)wrow * H * Hp : slot + (long long)(wrow - E) * H * Hp;
-  for (int a = 0; a < 4; ++a)
-    for (int b = 0; b < 4; ++b) {
-      const int h = h0 + ty + 16 * a, n = n0 + tx + 16 * b;
-      if (h < H && n < Hp) {
-        float* o = out + (long long)h * Hp + n;
-        *o = accumulate ? *o + acc[a][b] : acc[a][b];
-      }
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// host side
+bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, unsigned long long rows,
+            unsigned long long cols, unsigned long long stride, unsigned box_cols, unsigned box_rows,
+            CUtensorMapSwizzle swizzle) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride};
+  const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// fp32 [n, H, H'], boxes of 32 x 32: a third dimension keeps a box that
+// hangs over the last rows of H out of the next matrix.
+bool map_grad(CUtensorMap* m, float* ptr, unsigned long long n, unsigned long long H,
+              unsigned long long Hp) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[3] = {Hp, H, n}, strides[2] = {Hp * 4, H * Hp * 4};
+  const cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool CKPT>
+cudaError_t launch_wgrad(cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& ms,
+                         const CUtensorMap& md, const CUtensorMap& mh, const CUtensorMap& msl,
+                         const int* count, const int4* entries, const int2* segs, int32_t* status,
+                         int E, int H, int Hp, int accumulate) {
+  static GridCache cache;
+  void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, const int*,
+                 const int4*, const int2*, int32_t*, int, int, int, int) = k_wgrad_pair<CKPT>;
+  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), Ring<CKPT>::smem))
+    return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPair;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Ring<CKPT>::smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int grid = 0;
+  {
+    std::lock_guard<std::mutex> lock(cache.mu);
+    if (cache.grid[dev] == 0) {
+      // The warpgroups share out 512 x 128 registers: with fewer at launch
+      // setmaxnreg would wait for ever.
+      cudaFuncAttributes fa;
+      cudaError_t e = cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kernel));
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
+      int nclusters = 0;
+      cfg.gridDim = dim3(sm_count() / kPair * kPair);
+      e = cudaOccupancyMaxActiveClusters(&nclusters, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (nclusters < 1) return cudaErrorInvalidConfiguration;
+      cache.grid[dev] = (nclusters * kPair < sm_count() ? nclusters : sm_count() / kPair) * kPair;
     }
+    grid = cache.grid[dev];
+  }
+  cfg.gridDim = dim3(grid);
+  return cudaLaunchKernelEx(&cfg, kernel, mx, ms, md, mh, msl, count, entries, segs, status, E, H, Hp,
+                            accumulate);
 }
 
 }  // namespace
@@ -97,7 +615,7 @@ extern "C" int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int
   if (bytes == nullptr || R < 1 || S < 0 || K < 1 || E < 1 || B < 0) return MEP_ERR_INVALID_ARG;
   if (R > MEP_MAX_R || E > MEP_MAX_E || K > MEP_MAX_K || (long long)R * B > MEP_MAX_SLOTS)
     return MEP_ERR_INVALID_ARG;
-  *bytes = 16;
+  *bytes = 16 + 16 * ((size_t)E + (size_t)R * B) + 8 * (size_t)R * (E + B);
   return MEP_OK;
 }
 
@@ -108,7 +626,8 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   size_t need = 0;
   if (mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, &need) != MEP_OK) return MEP_ERR_INVALID_ARG;
   if (x_type != MEP_BF16 && x_type != MEP_CKPT8) return MEP_ERR_INVALID_ARG;
-  if (H < 8 || H % 8 != 0 || Hp < 8 || Hp % 8 != 0) return MEP_ERR_INVALID_ARG;
+  if (H < 8 || H % 8 != 0 || Hp < 8 || Hp % 8 != 0 || H > MEP_MAX_CKPT_C || Hp > MEP_MAX_CKPT_C)
+    return MEP_ERR_INVALID_ARG;
   const long long SK = (long long)S * K, rows = (long long)R * SK;
   if (rows > 0x7fffff00LL) return MEP_ERR_INVALID_ARG;
   if (cu_seqlens == nullptr || home_grad == nullptr || ws == nullptr || ws_bytes < need ||
@@ -116,16 +635,37 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
     return MEP_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(dy) || !aligned16(home_grad) || !aligned16(slot_grad) || !aligned16(ws))
     return MEP_ERR_INVALID_ARG;
+  if ((rows > 0 && (!on_current_device(x) || !on_current_device(dy))) ||
+      !on_current_device(home_grad) || (B > 0 && !on_current_device(slot_grad)))
+    return MEP_ERR_INVALID_ARG;
+  CUtensorMap mx, ms, md, mh, msl;
+  if (!map_grad(&mh, home_grad, E, H, Hp)) return MEP_ERR_CUDA;
+  msl = mh;  // never used without slots
+  if (B > 0 && !map_grad(&msl, slot_grad, (unsigned long long)R * B, H, Hp)) return MEP_ERR_CUDA;
+  mx = ms = md = mh;  // never used without rows
+  if (rows > 0) {
+    const unsigned long long rb = ckpt_row_bytes(H);
+    bool ok = map_2d(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, rows, Hp, 2ull * Hp, 64, kBK,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (x_type == MEP_CKPT8)
+      ok = ok &&
+           map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, H, rb, kBM, kBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, rb, rb, 16, kBK, CU_TENSOR_MAP_SWIZZLE_NONE);
+    else
+      ok = ok && map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, rows, H, 2ull * H, 64, kBK,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!ok) return MEP_ERR_CUDA;
+  }
+  int* count = static_cast<int*>(ws);
+  int4* entries = reinterpret_cast<int4*>(static_cast<char*>(ws) + 16);
+  int2* segs = reinterpret_cast<int2*>(entries + (size_t)E + (size_t)R * B);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int* ok = static_cast<int*>(ws);
-  cudaError_t err = launch_pdl(k_wgrad_check, dim3(1), dim3(1024), 0, st, cu_seqlens, R, E + B,
-                               int(SK), status, ok);
+  cudaError_t err = launch_pdl(k_wgrad_groups, dim3(1), dim3(kGroupThreads), 0, st, cu_seqlens, R, E,
+                               B, int(SK), accumulate, status, count, entries, segs);
   if (err != cudaSuccess) return MEP_ERR_CUDA;
-  const dim3 grid((Hp + kT - 1) / kT, (H + kT - 1) / kT, E + R * B);
-  const __nv_bfloat16* d = reinterpret_cast<const __nv_bfloat16*>(dy);
-  err = x_type == MEP_CKPT8 ? launch_pdl(k_wgrad<true>, grid, dim3(256), 0, st, x, d, cu_seqlens, ok, R,
-                                         int(SK), E, B, H, Hp, accumulate, home_grad, slot_grad)
-                            : launch_pdl(k_wgrad<false>, grid, dim3(256), 0, st, x, d, cu_seqlens, ok, R,
-                                         int(SK), E, B, H, Hp, accumulate, home_grad, slot_grad);
+  err = x_type == MEP_CKPT8 ? launch_wgrad<true>(st, mx, ms, md, mh, msl, count, entries, segs, status,
+                                                 E, H, Hp, accumulate)
+                            : launch_wgrad<false>(st, mx, ms, md, mh, msl, count, entries, segs,
+                                                  status, E, H, Hp, accumulate);
   return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
 }
