@@ -130,6 +130,15 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, int x, int y,
       "r"(x), "r"(y), "r"(z), "r"(src)
       : "memory");
 }
+// Arrival on a barrier of another CTA of the cluster, ordered after this
+// thread's own work at CTA scope: what the other CTA's MMA issuer goes on to
+// start reads this CTA's operands and TMEM on this CTA's own SM, and the
+// writes to them were closed by fence.proxy.async or tcgen05.fence before. (A
+// release at cluster scope waits for a round trip to L2: 1250 cycles, on a
+// step of 512.)
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
 __device__ __forceinline__ void bulk_wait_read_0() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
@@ -415,23 +424,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (CKPT) {
             if (h0 < H) {
               const uint32_t q = st + 2 * kOp, sc = q + kQ;
+              uint32_t v[4][4], sb[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = row0 + 16 * i;
-                uint32_t v[4], sb;
-                lds128(q + row * 128 + ((chunk ^ (row & 7)) << 4), v);
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb) : "r"(sc + row * 16 + sbyte));
-                const uint32_t bits = (sb == (uint32_t)kCkptNan ? 0x7fffu : sb << 7) * 0x10001u;
+                lds128(q + row * 128 + ((chunk ^ (row & 7)) << 4), v[i]);
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[i]) : "r"(sc + row * 16 + sbyte));
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int row = row0 + 16 * i;
+                const uint32_t bits = (sb[i] == (uint32_t)kCkptNan ? 0x7fffu : sb[i] << 7) * 0x10001u;
                 const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&bits);
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const bool in = row < valid;
-                  o[2 * j] = in ? dequant2(v[j], 0x4140, step) : 0u;
-                  o[2 * j + 1] = in ? dequant2(v[j], 0x4342, step) : 0u;
+                  o[2 * j] = dequant2(v[i][j], 0x4140, step);
+                  o[2 * j + 1] = dequant2(v[i][j], 0x4342, step);
                 }
-                const uint32_t dst = st + (chunk >> 2) * kBox + row * 128;
-                const int first = chunk >> 2, j0 = 2 * (chunk & 3) + first, j1 = 2 * (chunk & 3) + (first ^ 1);
+                if (row >= valid) {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) o[j] = 0u;
+                }
+                const int first = chunk >> 2;
+                const uint32_t dst = st + first * kBox + row * 128;
+                const int j0 = 2 * (chunk & 3) + first, j1 = j0 ^ 1;
                 sts128(dst + ((j0 ^ (row & 7)) << 4), first ? o[4] : o[0], first ? o[5] : o[1],
                        first ? o[6] : o[2], first ? o[7] : o[3]);
                 sts128(dst + ((j1 ^ (row & 7)) << 4), first ? o[0] : o[4], first ? o[1] : o[5],
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           if (CKPT || valid < need) fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->ready[s]), 0));
+          if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->ready[s]), 0));
         }
       }
     }
@@ -487,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&S->tempty[a]), 0));
+        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[a]), 0));
       }
       if (!ok) break;
       const CUtensorMap* map = e.x < E ? &map_home : &map_slot;
