@@ -44,7 +44,7 @@
 #include "tc.cuh"
 
 #ifndef MEP_WGRAD_CHUNK
-#define MEP_WGRAD_CHUNK 4
+#define MEP_WGRAD_CHUNK 8
 #endif
 
 namespace mep {
@@ -153,8 +153,9 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
                              ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
 
 // ---------------------------------------------------------------------------
-// The weight rows to write: entries[i] = {weight row, first segment, segments,
-// steps}, weight row < E a home expert and E + r*B + b slot b of rank r;
+// The weight rows to write, weight row < E a home expert and E + r*B + b slot
+// b of rank r: entries[2i] = {weight row, first segment, segments, steps},
+// entries[2i + 1] = {first segment's first buffer row, its rows, 0, 0};
 // segs[j] = {first buffer row, rows}. Without `accumulate` a home expert is
 // listed even without rows (it is written as zero), a slot never is.
 __global__ void __launch_bounds__(kGroupThreads)
@@ -208,11 +209,17 @@ __global__ void __launch_bounds__(kGroupThreads)
     block_excl_scan(s_seg, s_seg, blockDim.x, s_warp, true);
     if (listed) {
       int at = s_segs + s_seg[threadIdx.x];
-      entries[s_entries + s_entry[threadIdx.x]] = make_int4(w, at, nseg, steps);
+      int4* entry = entries + 2 * (s_entries + s_entry[threadIdx.x]);
+      entry[0] = make_int4(w, at, nseg, steps);
+      entry[1] = make_int4(0, 0, 0, 0);
       for (int r = r0; r < r1; ++r) {
         const long long p = (long long)r * G + j;
         const int lo = j == 0 ? 0 : cu[p - 1], len = cu[p] - lo;
-        if (len > 0) segs[at++] = make_int2(int((long long)r * SK + lo), len);
+        if (len > 0) {
+          const int row = int((long long)r * SK + lo);
+          if (entry[1].y == 0) entry[1] = make_int4(row, len, 0, 0);
+          segs[at++] = make_int2(row, len);
+        }
       }
     }
     __syncthreads();
@@ -238,15 +245,65 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bflo
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&v)[4]) {
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(addr));
+__device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
+
+// The units of one CTA pair, in the order in which every role of both CTAs
+// walks them. The next unit's entry is loaded while f works on this one's;
+// f(entry, tile) returns false to stop.
+struct Entry {
+  int4 e;       // {weight row, first segment, segments, steps}
+  int row, len; // the first segment
+};
+__device__ __forceinline__ Entry load_entry(const int4* __restrict__ entries, int i) {
+  const int4 b = entries[2 * i + 1];
+  return {entries[2 * i], b.x, b.y};
+}
+template <typename F>
+__device__ __forceinline__ void for_units(const int4* __restrict__ entries, int count, int tiles, F f) {
+  const int step = gridDim.x / 2;
+  int i = (blockIdx.x / 2) / tiles, tile = (blockIdx.x / 2) % tiles;
+  if (i >= count) return;
+  Entry cur = load_entry(entries, i), next = cur;
+  for (;;) {
+    const int t = tile + step, ni = i + t / tiles;
+    if (ni < count) next = load_entry(entries, ni);
+    if (!f(cur, tile) || ni >= count) return;
+    cur = next;
+    i = ni;
+    tile = t % tiles;
+  }
+}
+// The steps of one unit: f(first buffer row, rows left from it on) per step.
+template <typename F>
+__device__ __forceinline__ bool for_steps(const Entry& en, const int2* __restrict__ segs, F f) {
+  int row = en.row, len = en.len;
+  for (int g = 0; g < en.e.z; ++g) {
+    if (g > 0) {
+      const int2 seg = segs[en.e.y + g];
+      row = seg.x;
+      len = seg.y;
+    }
+    for (int k = 0; k < len; k += kBK)
+      if (!f(row + k, len - k)) return false;
+  }
+  return true;
+}
+// A ring position: stage and the parity of its round.
+struct Pos {
+  uint32_t s = 0, parity = 0;
+  template <int N> __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      parity ^= 1u;
+    }
+  }
+};
 
 // ---------------------------------------------------------------------------
 template <bool CKPT>
@@ -298,21 +355,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = S->tmem;
   const int nM = (H + 2 * kBM - 1) / (2 * kBM), nN = (Hp + kBN - 1) / kBN;
-  const int tiles = nM * nN;
-  const long long units = (long long)S->count * tiles;
-  const long long u0 = blockIdx.x / 2, ustep = gridDim.x / 2;
+  const int tiles = nM * nN, count = S->count;
 
-  // the four warpgroups' registers: 40 + 88 + 192 + 192 = 4 x 128 at launch
+  // the four warpgroups' registers: 56 + 72 + 192 + 192 = 4 x 128 at launch
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       if (lane == 0) {
         // ---------------- TMA producer ----------------
-        uint32_t it = 0;
-        bool ok = true;
-        for (long long u = u0; ok && u < units; u += ustep) {
-          const int4 e = entries[u / tiles];
-          const int t = int(u % tiles);
+        Pos at;
+        uint32_t issued = 0;
+        for_units(entries, count, tiles, [&](const Entry& en, int t) {
           const int h0 = t / nN * 2 * kBM + rank * kBM, n0 = t % nN * kBN;
           const bool narrow = Hp - n0 <= 128;
           const int c0 = n0 + rank * (narrow ? 64 : 128);
@@ -320,31 +373,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
           const uint32_t bytes = (CKPT ? (na > 0 ? kQ + kScale : 0) : na * kBox) + nb * kBox;
           const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
-          for (int g = 0; ok && g < e.z; ++g) {
-            const int2 seg = segs[e.y + g];
-            for (int k = 0; k < seg.y; k += kBK, ++it) {
-              const int s = int(it % kSt);
-              if (!wait_phase(smem_u32(&S->empty[s]), ((it / kSt) & 1u) ^ 1u, abort_flag, status)) {
-                ok = false;
-                break;
+          return for_steps(en, segs, [&](int row, int) {
+            if (!wait_phase(smem_u32(&S->empty[at.s]), at.parity ^ 1u, abort_flag, status)) return false;
+            const uint32_t bar = smem_u32(&S->full[at.s]), st = base + at.s * kStage;
+            mbar_expect_tx(bar, bytes);
+            if (CKPT) {
+              if (na > 0) {
+                tma_load_2d(st + 2 * kOp, &map_x, h0, row, bar);
+                tma_load_2d(st + 2 * kOp + kQ, &map_s, sx, row, bar);
               }
-              const uint32_t bar = smem_u32(&S->full[s]), st = base + s * kStage;
-              mbar_expect_tx(bar, bytes);
-              if (CKPT) {
-                if (na > 0) {
-                  tma_load_2d(st + 2 * kOp, &map_x, h0, seg.x + k, bar);
-                  tma_load_2d(st + 2 * kOp + kQ, &map_s, sx, seg.x + k, bar);
-                }
-              } else {
-                for (int i = 0; i < na; ++i) tma_load_2d(st + i * kBox, &map_x, h0 + 64 * i, seg.x + k, bar);
-              }
-              for (int i = 0; i < nb; ++i)
-                tma_load_2d(st + kOp + i * kBox, &map_dy, c0 + 64 * i, seg.x + k, bar);
+            } else {
+              if (na > 0) tma_load_2d(st, &map_x, h0, row, bar);
+              if (na > 1) tma_load_2d(st + kBox, &map_x, h0 + 64, row, bar);
             }
-          }
-        }
+            if (nb > 0) tma_load_2d(st + kOp, &map_dy, c0, row, bar);
+            if (nb > 1) tma_load_2d(st + kOp + kBox, &map_dy, c0 + 64, row, bar);
+            at.template next<kSt>();
+            ++issued;
+            return true;
+          });
+        });
         // this CTA's copies have landed, and every commit aimed at it has arrived
-        for (uint32_t j = it > kSt ? it - kSt : 0; j < it; ++j) {
+        for (uint32_t j = issued > kSt ? issued - kSt : 0; j < issued; ++j) {
           wait_phase(smem_u32(&S->full[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
           wait_phase(smem_u32(&S->empty[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
         }
@@ -353,74 +403,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0 && leader) {
         // ---------------- MMA issuer (CTA 0 only) ----------------
-        uint32_t it = 0, ck = 0;
-        bool ok = true;
-        for (long long u = u0; ok && u < units; u += ustep) {
-          const int4 e = entries[u / tiles];
-          const int n0 = int(u % tiles) % nN * kBN;
-          const uint32_t idesc = Hp - n0 <= 128 ? kIdescN : kIdesc;
-          int step = 0;
-          for (int g = 0; ok && g < e.z; ++g) {
-            const int len = segs[e.y + g].y;
-            for (int k = 0; k < len; k += kBK, ++it, ++step) {
-              const uint32_t a = ck & 1u, d = tmem + a * kBN;
-              const int in_chunk = step % kChunk;
-              if (in_chunk == 0 &&
-                  !wait_phase(smem_u32(&S->tempty[a]), ((ck >> 1) & 1u) ^ 1u, abort_flag, status)) {
-                ok = false;
-                break;
-              }
-              const int s = int(it % kSt);
-              if (!wait_phase(smem_u32(&S->ready[s]), (it / kSt) & 1u, abort_flag, status)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint32_t st = base + s * kStage;
-              const int left = len - k;
+        Pos at, acc;  // stage; accumulator
+        const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + kOp, kBox, 1024);
+        for_units(entries, count, tiles, [&](const Entry& en, int t) {
+          const uint32_t idesc = Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc;
+          int steps = en.e.w, in_chunk = 0;
+          return for_steps(en, segs, [&](int, int left) {
+            if (in_chunk == 0 &&
+                !wait_phase(smem_u32(&S->tempty[acc.s]), acc.parity ^ 1u, abort_flag, status))
+              return false;
+            if (!wait_phase(smem_u32(&S->ready[at.s]), at.parity, abort_flag, status)) return false;
+            tc_fence_after();
+            const uint32_t d = tmem + acc.s * kBN;
+            const uint64_t ad = adesc + (at.s * kStage >> 4), bd = bdesc + (at.s * kStage >> 4);
+            if (left > kBK - 16) {
 #pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk)
-                if (16 * kk < left)
-                  tc_mma2(d, sdesc(st + kk * 16 * 128, kBox, 1024),
-                          sdesc(st + kOp + kk * 16 * 128, kBox, 1024), (in_chunk | kk) != 0 ? 1u : 0u,
-                          idesc);
-              tc_commit2_mc(smem_u32(&S->empty[s]), 3);
-              if (in_chunk == kChunk - 1 || step == e.w - 1) {
-                tc_commit2_mc(smem_u32(&S->tfull[a]), 3);
-                ++ck;
-              }
+                tc_mma2(d, ad + kk * 128, bd + kk * 128, kk > 0 ? 1u : (uint32_t)in_chunk, idesc);
+            } else {
+              for (int kk = 0; 16 * kk < left; ++kk)
+                tc_mma2(d, ad + kk * 128, bd + kk * 128, uint32_t(kk + in_chunk), idesc);
             }
-          }
-        }
+            tc_commit2_mc(smem_u32(&S->empty[at.s]), 3);
+            at.template next<kSt>();
+            --steps;
+            if (++in_chunk == kChunk || steps == 0) {
+              tc_commit2_mc(smem_u32(&S->tfull[acc.s]), 3);
+              acc.template next<2>();
+              in_chunk = 0;
+            }
+            return true;
+          });
+        });
         tc_commit2(smem_u32(&S->drain));
         wait_phase(smem_u32(&S->drain), 0u, abort_flag, status, false);
       }
       __syncwarp();
     }
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- converter ----------------
-    // Thread t takes 16 columns (chunk t & 7) of rows t >> 3, + 16, + 32, + 48
-    // of the step. The bytes' box and the operand boxes are 128-byte
-    // swizzled; chunks 4..7 store their second half first, so that a quarter
-    // warp's stores cover all banks.
-    const int t = threadIdx.x - 128, chunk = t & 7, row0 = t >> 3;
-    uint32_t it = 0;
-    bool ok = true;
-    for (long long u = u0; ok && u < units; u += ustep) {
-      const int4 e = entries[u / tiles];
-      const int tile = int(u % tiles), h0 = tile / nN * 2 * kBM + rank * kBM;
+    // Thread t takes columns [8c, 8c + 8) and [64 + 8c, 64 + 8c + 8), c = t & 7,
+    // of four rows: two 8-byte reads and two 16-byte stores, chunk c of either
+    // operand box. All boxes are 128-byte swizzled. A quarter warp stores to
+    // the eight chunks of one row; a half warp reads half of two rows that
+    // differ in bit 2, whose swizzle puts them into different halves.
+    const int t = threadIdx.x - 128, c8 = t & 7;
+    const int row0 = (lane >> 4) + ((lane >> 3) & 1) * 4 + (warp & 1) * 2 + ((warp >> 1) & 1) * 8;
+    Pos at;
+    for_units(entries, count, tiles, [&](const Entry& en, int tile) {
+      const int h0 = tile / nN * 2 * kBM + rank * kBM;
       const uint32_t sbyte = (uint32_t)(h0 / kCkptBlock) & 15u;
-      for (int g = 0; ok && g < e.z; ++g) {
-        const int len = segs[e.y + g].y;
-        for (int k = 0; k < len; k += kBK, ++it) {
-          const int s = int(it % kSt);
-          if (!warp_wait(smem_u32(&S->full[s]), (it / kSt) & 1u, abort_flag, status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + s * kStage;
-          const int valid = min(kBK, len - k), need = (valid + 15) & ~15;
+      return for_steps(en, segs, [&](int, int left) {
+          if (!warp_wait(smem_u32(&S->full[at.s]), at.parity, abort_flag, status)) return false;
+          const uint32_t st = base + at.s * kStage;
+          const int valid = min(kBK, left), need = (valid + 15) & ~15;
           if (CKPT) {
             if (h0 < H) {
               const uint32_t q = st + 2 * kOp, sc = q + kQ;
@@ -428,31 +465,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = row0 + 16 * i;
-                lds128(q + row * 128 + ((chunk ^ (row & 7)) << 4), v[i]);
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                  lds64(q + row * 128 + (((4 * half + (c8 >> 1)) ^ (row & 7)) << 4) + (c8 & 1) * 8,
+                        v[i][2 * half], v[i][2 * half + 1]);
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[i]) : "r"(sc + row * 16 + sbyte));
               }
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int row = row0 + 16 * i;
-                const uint32_t bits = (sb[i] == (uint32_t)kCkptNan ? 0x7fffu : sb[i] << 7) * 0x10001u;
+                // rows of the next group: q times 0
+                const uint32_t bits =
+                    row < valid ? (sb[i] == (uint32_t)kCkptNan ? 0x7fffu : sb[i] << 7) * 0x10001u : 0u;
                 const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&bits);
-                uint32_t o[8];
+                const uint32_t dst = st + row * 128 + ((c8 ^ (row & 7)) << 4);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  o[2 * j] = dequant2(v[i][j], 0x4140, step);
-                  o[2 * j + 1] = dequant2(v[i][j], 0x4342, step);
-                }
-                if (row >= valid) {
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) o[j] = 0u;
-                }
-                const int first = chunk >> 2;
-                const uint32_t dst = st + first * kBox + row * 128;
-                const int j0 = 2 * (chunk & 3) + first, j1 = j0 ^ 1;
-                sts128(dst + ((j0 ^ (row & 7)) << 4), first ? o[4] : o[0], first ? o[5] : o[1],
-                       first ? o[6] : o[2], first ? o[7] : o[3]);
-                sts128(dst + ((j1 ^ (row & 7)) << 4), first ? o[0] : o[4], first ? o[1] : o[5],
-                       first ? o[2] : o[6], first ? o[3] : o[7]);
+                for (int half = 0; half < 2; ++half)
+                  sts128(dst + half * kBox, dequant2(v[i][2 * half], 0x4140, step),
+                         dequant2(v[i][2 * half], 0x4342, step),
+                         dequant2(v[i][2 * half + 1], 0x4140, step),
+                         dequant2(v[i][2 * half + 1], 0x4342, step));
               }
             }
           }
@@ -464,10 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           if (CKPT || valid < need) fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->ready[s]), 0));
-        }
-      }
-    }
+          if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->ready[at.s]), 0));
+          at.template next<kSt>();
+          return true;
+      });
+    });
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ---------------- sums and epilogue ----------------
@@ -475,24 +508,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // columns [128 half, 128 half + 128) of the unit.
     const int q = warp & 3, half = (warp - 8) >> 2;
     const uint32_t box = out_box + (uint32_t)(warp - 8) * kStoreBox;
-    uint32_t ck = 0;
-    bool ok = true;
-    for (long long u = u0; ok && u < units; u += ustep) {
-      const int4 e = entries[u / tiles];
-      const int tile = int(u % tiles);
+    Pos at;
+    for_units(entries, count, tiles, [&](const Entry& en, int tile) {
+      const int4 e = en.e;
       const int h = tile / nN * 2 * kBM + rank * kBM + 32 * q, n = tile % nN * kBN + 128 * half;
       const int chunks = (e.w + kChunk - 1) / kChunk;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int c = 0; c < chunks; ++c, ++ck) {
-        const uint32_t a = ck & 1u;
-        if (!warp_wait(smem_u32(&S->tfull[a]), (ck >> 1) & 1u, abort_flag, status)) {
-          ok = false;
-          break;
-        }
+      for (int c = 0; c < chunks; ++c) {
+        if (!warp_wait(smem_u32(&S->tfull[at.s]), at.parity, abort_flag, status)) return false;
         tc_fence_after();
-        const uint32_t ta = tmem + a * kBN + 128 * half + ((uint32_t)(32 * q) << 16);
+        const uint32_t ta = tmem + at.s * kBN + 128 * half + ((uint32_t)(32 * q) << 16);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (n + 32 * i < Hp) {
@@ -504,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[a]), 0));
+        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[at.s]), 0));
+        at.template next<2>();
       }
-      if (!ok) break;
       const CUtensorMap* map = e.x < E ? &map_home : &map_slot;
       const int z = e.x < E ? e.x : e.x - E;
 #pragma unroll
@@ -528,7 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_store_3d(map, n + 32 * i, h, z, box);
           }
         }
-    }
+      return true;
+    });
     if (lane == 0) bulk_wait_all();
     __syncwarp();
   }
@@ -632,7 +660,7 @@ extern "C" int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int
   if (bytes == nullptr || R < 1 || S < 0 || K < 1 || E < 1 || B < 0) return MEP_ERR_INVALID_ARG;
   if (R > MEP_MAX_R || E > MEP_MAX_E || K > MEP_MAX_K || (long long)R * B > MEP_MAX_SLOTS)
     return MEP_ERR_INVALID_ARG;
-  *bytes = 16 + 16 * ((size_t)E + (size_t)R * B) + 8 * (size_t)R * (E + B);
+  *bytes = 16 + 32 * ((size_t)E + (size_t)R * B) + 8 * (size_t)R * (E + B);
   return MEP_OK;
 }
 
@@ -646,7 +674,9 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   if (H < 8 || H % 8 != 0 || Hp < 8 || Hp % 8 != 0 || H > MEP_MAX_CKPT_C || Hp > MEP_MAX_CKPT_C)
     return MEP_ERR_INVALID_ARG;
   const long long SK = (long long)S * K, rows = (long long)R * SK;
-  if (rows > 0x7fffff00LL) return MEP_ERR_INVALID_ARG;
+  const long long tiles = (long long)((H + 2 * kBM - 1) / (2 * kBM)) * ((Hp + kBN - 1) / kBN);
+  if (rows > 0x7fffff00LL || tiles * ((long long)E + (long long)R * B) > 0x7fff0000LL)
+    return MEP_ERR_INVALID_ARG;
   if (cu_seqlens == nullptr || home_grad == nullptr || ws == nullptr || ws_bytes < need ||
       (B > 0 && slot_grad == nullptr) || (rows > 0 && (x == nullptr || dy == nullptr)))
     return MEP_ERR_INVALID_ARG;
@@ -675,7 +705,7 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   }
   int* count = static_cast<int*>(ws);
   int4* entries = reinterpret_cast<int4*>(static_cast<char*>(ws) + 16);
-  int2* segs = reinterpret_cast<int2*>(entries + (size_t)E + (size_t)R * B);
+  int2* segs = reinterpret_cast<int2*>(entries + 2 * ((size_t)E + (size_t)R * B));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err = launch_pdl(k_wgrad_groups, dim3(1), dim3(kGroupThreads), 0, st, cu_seqlens, R, E,
                                B, int(SK), accumulate, status, count, entries, segs);
