@@ -1,142 +1,180 @@
 // act_ckpt.cu -- 8-bit activation checkpoints (mep_ckpt_save, mep_ckpt_load)
 // and the experts' gated activation that writes and reads them (mep_swiglu,
 // mep_swiglu_backward).
+//
+// All four are one pass over memory: each byte is read once and written once
+// (save 2 + 1.01 bytes a bf16 value, load the reverse; per value of the
+// activation 4 in, 2 + 2.02 out forward, 2 + 2.02 in, 4 + 2 out backward).
+// A half warp takes a block of 128 columns, eight values a lane, and gets the
+// block's largest magnitude in four shuffles; a thread holds kUnroll blocks
+// at a time, all loaded before the first is used. Where a row is a multiple of
+// 8 columns a lane's values are one 16-byte vector; otherwise they are
+// fetched one by one, coalesced over the half warp.
 
 #include "ckpt.cuh"
+
+#ifndef MEP_CKPT_UNROLL
+#define MEP_CKPT_UNROLL 4
+#endif
+#ifndef MEP_SWIGLU_UNROLL
+#define MEP_SWIGLU_UNROLL 2
+#endif
 
 namespace mep {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 256;
 
-__device__ __forceinline__ float warp_max_nan(float v) {
+// Calls f(row, block, in) for U blocks of this half warp at a time; the loads
+// of all U come first. Blocks are numbered over the whole tensor; a call's
+// are kThreads / 16 apart.
+struct Where {
+  long long row;
+  int block;
+  bool in;
+};
+template <int U> __device__ __forceinline__ void where(Where (&w)[U], uint32_t blocks, uint32_t nb) {
+  const uint32_t first = blockIdx.x * uint32_t(U * kThreads / kHalf) + threadIdx.x / kHalf;
 #pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v = max_nan(v, __shfl_xor_sync(MEP_FULL_MASK, v, d));
-  return v;
-}
-
-// One warp per (row, block of 128 columns).
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_ckpt_save(const T* __restrict__ x, long long N, int C, uint8_t* __restrict__ ckpt) {
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int nb = (C + kCkptBlock - 1) / kCkptBlock;
-  const long long rb = ckpt_row_bytes(C), items = N * nb;
-  for (long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items;
-       i += (long long)gridDim.x * kWarps) {
-    const long long r = i / nb;
-    const int b = int(i % nb), c0 = b * kCkptBlock;
-    float v[4], top = 0.f;
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 32 * j + lane;
-      v[j] = c < C ? to_f32(x[r * C + c]) : 0.f;
-      top = max_nan(top, fabsf(v[j]));
-    }
-    const int s = ckpt_scale(warp_max_nan(top));
-    const float inv = ckpt_inv_step(s);
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 32 * j + lane;
-      if (c < C) ckpt[r * rb + c] = uint8_t(ckpt_q(v[j], inv));
-    }
-    if (lane == 0) ckpt[r * rb + ckpt_scale_at(C) + b] = uint8_t(s);
-    if (b == nb - 1)
-      for (int p = ckpt_scale_at(C) + nb + lane; p < rb; p += 32) ckpt[r * rb + p] = 0;
-    if (b == nb - 1 && C + lane < ckpt_scale_at(C)) ckpt[r * rb + C + lane] = 0;
+  for (int u = 0; u < U; ++u) {
+    const uint32_t i = first + u * (kThreads / kHalf);
+    w[u].in = i < blocks;
+    w[u].row = i / nb;
+    w[u].block = int(i % nb);
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_ckpt_load(const uint8_t* __restrict__ ckpt, long long N, int C, T* __restrict__ x) {
+template <int KIND, bool VEC, int U>
+__global__ void __launch_bounds__(kThreads)
+    k_ckpt_save(const void* __restrict__ x, uint32_t blocks, int C, uint8_t* __restrict__ ckpt) {
   pdl_wait();
   pdl_launch_dependents();
-  const long long rb = ckpt_row_bytes(C), n = N * C;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (long long)gridDim.x * blockDim.x) {
-    const long long r = i / C;
-    const int c = int(i % C);
-    const uint8_t* row = ckpt + r * rb;
-    x[i] = from_f32<T>(float(int8_t(row[c])) * ckpt_step(row[ckpt_scale_at(C) + c / kCkptBlock]));
+  const int l = threadIdx.x % kHalf;
+  Where w[U];
+  where<U>(w, blocks, (C + kCkptBlock - 1) / kCkptBlock);
+  Pack<KIND> p[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (w[u].in)
+      p[u].template load<VEC>(x, w[u].row, C, w[u].block, l);
+    else
+      p[u].clear();
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = p[u].get(j);
+    save8<VEC>(ckpt, w[u].row, C, w[u].block, l, w[u].in, v);
   }
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return 1.f / (1.f + __expf(-g)); }
+template <typename T, bool VEC, int U>
+__global__ void __launch_bounds__(kThreads)
+    k_ckpt_load(const uint8_t* __restrict__ ckpt, uint32_t blocks, int C, T* __restrict__ x) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int l = threadIdx.x % kHalf;
+  Where w[U];
+  where<U>(w, blocks, (C + kCkptBlock - 1) / kCkptBlock);
+  Pack<MEP_CKPT8> p[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (w[u].in) p[u].template load<VEC>(ckpt, w[u].row, C, w[u].block, l);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (w[u].in) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = p[u].get(j);
+      store8<T, VEC>(x, w[u].row, C, w[u].block, l, v);
+    }
+}
 
-template <bool CKPT>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_swiglu(const __nv_bfloat16* __restrict__ gu, long long rows, int F,
+// 1 / (1 + e^-g); the quotient to 2 ulp (0 where e^-g overflows)
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+template <bool VEC, bool CKPT, int U>
+__global__ void __launch_bounds__(kThreads)
+    k_swiglu(const __nv_bfloat16* __restrict__ gu, uint32_t blocks, int F,
              __nv_bfloat16* __restrict__ a, uint8_t* __restrict__ ckpt) {
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int nb = (F + kCkptBlock - 1) / kCkptBlock;
-  const long long rb = ckpt_row_bytes(F), items = rows * nb;
-  for (long long i = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < items;
-       i += (long long)gridDim.x * kWarps) {
-    const long long r = i / nb;
-    const int b = int(i % nb), c0 = b * kCkptBlock;
-    float v[2][4], top[2] = {0.f, 0.f};
-    for (int h = 0; h < 2; ++h)
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + 32 * j + lane;
-        v[h][j] = c < F ? to_f32(gu[(2 * r + h) * F + c]) : 0.f;
-        top[h] = max_nan(top[h], fabsf(v[h][j]));
-      }
-    for (int j = 0; j < 4; ++j) {
-      const int c = c0 + 32 * j + lane;
-      if (c < F) a[r * F + c] = from_f32<__nv_bfloat16>(v[0][j] * sigmoid(v[0][j]) * v[1][j]);
+  const int l = threadIdx.x % kHalf;
+  Where w[U];
+  where<U>(w, blocks, (F + kCkptBlock - 1) / kCkptBlock);
+  Pack<MEP_BF16> p[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (w[u].in)
+        p[u][h].template load<VEC>(gu, 2 * w[u].row + h, F, w[u].block, l);
+      else
+        p[u][h].clear();
     }
-    if (CKPT)
-      for (int h = 0; h < 2; ++h) {
-        uint8_t* row = ckpt + (2 * r + h) * rb;
-        const int s = ckpt_scale(warp_max_nan(top[h]));
-        const float inv = ckpt_inv_step(s);
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + 32 * j + lane;
-          if (c < F) row[c] = uint8_t(ckpt_q(v[h][j], inv));
-        }
-        if (lane == 0) row[ckpt_scale_at(F) + b] = uint8_t(s);
-        if (b == nb - 1) {
-          for (int p = ckpt_scale_at(F) + nb + lane; p < rb; p += 32) row[p] = 0;
-          if (F + lane < ckpt_scale_at(F)) row[F + lane] = 0;
-        }
-      }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float v[2][8], o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      v[0][j] = p[u][0].get(j);
+      v[1][j] = p[u][1].get(j);
+      o[j] = v[0][j] * sigmoid(v[0][j]) * v[1][j];
+    }
+    if (w[u].in) store8<__nv_bfloat16, VEC>(a, w[u].row, F, w[u].block, l, o);
+    if (CKPT) {
+      save8<VEC>(ckpt, 2 * w[u].row, F, w[u].block, l, w[u].in, v[0]);
+      save8<VEC>(ckpt, 2 * w[u].row + 1, F, w[u].block, l, w[u].in, v[1]);
+    }
   }
 }
 
-template <bool CKPT>
-__global__ void __launch_bounds__(32 * kWarps)
-    k_swiglu_backward(const __nv_bfloat16* __restrict__ da, const void* __restrict__ gu_,
-                      long long rows, int F, __nv_bfloat16* __restrict__ dgu,
+template <int KIND, bool VEC, int U>
+__global__ void __launch_bounds__(kThreads)
+    k_swiglu_backward(const __nv_bfloat16* __restrict__ da, const void* __restrict__ gu,
+                      uint32_t blocks, int F, __nv_bfloat16* __restrict__ dgu,
                       __nv_bfloat16* __restrict__ a) {
   pdl_wait();
   pdl_launch_dependents();
-  const long long rb = ckpt_row_bytes(F), n = rows * F;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n;
-       i += (long long)gridDim.x * blockDim.x) {
-    const long long r = i / F;
-    const int c = int(i % F);
-    float v[2];
-    for (int h = 0; h < 2; ++h) {
-      if (CKPT) {
-        const uint8_t* row = static_cast<const uint8_t*>(gu_) + (2 * r + h) * rb;
-        v[h] = float(int8_t(row[c])) * ckpt_step(row[ckpt_scale_at(F) + c / kCkptBlock]);
-      } else {
-        v[h] = to_f32(static_cast<const __nv_bfloat16*>(gu_)[(2 * r + h) * F + c]);
-      }
+  const int l = threadIdx.x % kHalf;
+  Where w[U];
+  where<U>(w, blocks, (F + kCkptBlock - 1) / kCkptBlock);
+  Pack<KIND> p[U][2];
+  Pack<MEP_BF16> d[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (w[u].in) {
+      p[u][0].template load<VEC>(gu, 2 * w[u].row, F, w[u].block, l);
+      p[u][1].template load<VEC>(gu, 2 * w[u].row + 1, F, w[u].block, l);
+      d[u].template load<VEC>(da, w[u].row, F, w[u].block, l);
     }
-    const float d = to_f32(da[i]), s = sigmoid(v[0]);
-    dgu[2 * r * F + c] = from_f32<__nv_bfloat16>(d * v[1] * s * (1.f + v[0] * (1.f - s)));
-    dgu[(2 * r + 1) * F + c] = from_f32<__nv_bfloat16>(d * v[0] * s);
-    if (a != nullptr) a[i] = from_f32<__nv_bfloat16>(v[0] * s * v[1]);
-  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (w[u].in) {
+      float dg[8], du[8], o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float g = p[u][0].get(j), up = p[u][1].get(j), dv = d[u].get(j), s = sigmoid(g);
+        dg[j] = dv * up * s * (1.f + g * (1.f - s));
+        du[j] = dv * (g * s);
+        o[j] = g * s * up;
+      }
+      store8<__nv_bfloat16, VEC>(dgu, 2 * w[u].row, F, w[u].block, l, dg);
+      store8<__nv_bfloat16, VEC>(dgu, 2 * w[u].row + 1, F, w[u].block, l, du);
+      if (a != nullptr) store8<__nv_bfloat16, VEC>(a, w[u].row, F, w[u].block, l, o);
+    }
 }
 
-int grid_for(long long items, int per) {
-  const long long want = (items + per - 1) / per, cap = (long long)sm_count() * 64;
-  return int(want < cap ? want : cap);
+// Runs f(first row, blocks, grid) over slices of rows whose blocks fit 32 bits.
+template <int U, typename F> int sliced(long long rows, long long C, F f) {
+  const long long nb = (C + kCkptBlock - 1) / kCkptBlock, most = 0x40000000LL / nb;
+  constexpr int per = U * kThreads / kHalf;
+  for (long long r = 0; r < rows; r += most) {
+    const long long n = (rows - r < most ? rows - r : most) * nb;
+    if (f(r, uint32_t(n), dim3(unsigned((n + per - 1) / per))) != cudaSuccess) return MEP_ERR_CUDA;
+  }
+  return MEP_OK;
 }
 
 }  // namespace
@@ -162,29 +200,39 @@ extern "C" int mep_ckpt_save(const void* x, int x_type, int64_t N, int64_t C, ui
                              void* stream) {
   const int rc = ckpt_check(x, x_type, N, C, ckpt);
   if (rc != MEP_OK || N == 0) return rc;
+  constexpr int U = MEP_CKPT_UNROLL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(N * ((C + kCkptBlock - 1) / kCkptBlock), kWarps);
-  const cudaError_t err =
-      x_type == MEP_BF16
-          ? launch_pdl(k_ckpt_save<__nv_bfloat16>, dim3(grid), dim3(32 * kWarps), 0, st,
-                       static_cast<const __nv_bfloat16*>(x), (long long)N, int(C), ckpt)
-          : launch_pdl(k_ckpt_save<float>, dim3(grid), dim3(32 * kWarps), 0, st,
-                       static_cast<const float*>(x), (long long)N, int(C), ckpt);
-  return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
+  const bool bf16 = x_type == MEP_BF16, vec = C % 8 == 0;
+  const auto kernel = bf16 ? (vec ? k_ckpt_save<MEP_BF16, true, U> : k_ckpt_save<MEP_BF16, false, 1>)
+                           : (vec ? k_ckpt_save<MEP_F32, true, U / 2> : k_ckpt_save<MEP_F32, false, 1>);
+  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+    const void* p = static_cast<const char*>(x) + r * C * (bf16 ? 2 : 4);
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, p, blocks, int(C), ckpt + r * ckpt_row_bytes(C));
+  };
+  return !vec ? sliced<1>(N, C, f) : bf16 ? sliced<U>(N, C, f) : sliced<U / 2>(N, C, f);
 }
 
 extern "C" int mep_ckpt_load(const uint8_t* ckpt, int64_t N, int64_t C, int x_type, void* x,
                              void* stream) {
   const int rc = ckpt_check(x, x_type, N, C, ckpt);
   if (rc != MEP_OK || N == 0) return rc;
+  constexpr int U = MEP_CKPT_UNROLL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(N * C, 32 * kWarps);
-  const cudaError_t err =
-      x_type == MEP_BF16 ? launch_pdl(k_ckpt_load<__nv_bfloat16>, dim3(grid), dim3(32 * kWarps), 0,
-                                      st, ckpt, (long long)N, int(C), static_cast<__nv_bfloat16*>(x))
-                         : launch_pdl(k_ckpt_load<float>, dim3(grid), dim3(32 * kWarps), 0, st, ckpt,
-                                      (long long)N, int(C), static_cast<float*>(x));
-  return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
+  const bool vec = C % 8 == 0;
+  const auto run = [&](auto* out, auto kernel) {
+    return [=](long long r, uint32_t blocks, dim3 grid) {
+      return launch_pdl(kernel, grid, dim3(kThreads), 0, st, ckpt + r * ckpt_row_bytes(C), blocks, int(C),
+                        out + r * C);
+    };
+  };
+  if (x_type == MEP_BF16) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(x);
+    return vec ? sliced<U>(N, C, run(o, k_ckpt_load<__nv_bfloat16, true, U>))
+               : sliced<1>(N, C, run(o, k_ckpt_load<__nv_bfloat16, false, 1>));
+  }
+  float* o = static_cast<float*>(x);
+  return vec ? sliced<U>(N, C, run(o, k_ckpt_load<float, true, U>))
+             : sliced<1>(N, C, run(o, k_ckpt_load<float, false, 1>));
 }
 
 extern "C" int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16* a, uint8_t* ckpt,
@@ -193,16 +241,18 @@ extern "C" int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16*
   if (rows == 0) return MEP_OK;
   if (gu == nullptr || a == nullptr || !aligned16(gu) || !aligned16(a) || !aligned16(ckpt))
     return MEP_ERR_INVALID_ARG;
+  constexpr int U = MEP_SWIGLU_UNROLL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(rows * ((F + kCkptBlock - 1) / kCkptBlock), kWarps);
   const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(gu);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a);
-  const cudaError_t err =
-      ckpt != nullptr ? launch_pdl(k_swiglu<true>, dim3(grid), dim3(32 * kWarps), 0, st, in,
-                                   (long long)rows, int(F), out, ckpt)
-                      : launch_pdl(k_swiglu<false>, dim3(grid), dim3(32 * kWarps), 0, st, in,
-                                   (long long)rows, int(F), out, ckpt);
-  return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
+  const bool vec = F % 8 == 0;
+  const auto kernel = vec ? (ckpt != nullptr ? k_swiglu<true, true, U> : k_swiglu<true, false, U>)
+                          : (ckpt != nullptr ? k_swiglu<false, true, 1> : k_swiglu<false, false, 1>);
+  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, in + 2 * r * F, blocks, int(F), out + r * F,
+                      ckpt == nullptr ? nullptr : ckpt + 2 * r * ckpt_row_bytes(F));
+  };
+  return vec ? sliced<U>(rows, F, f) : sliced<1>(rows, F, f);
 }
 
 extern "C" int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_type, int64_t rows,
@@ -213,14 +263,17 @@ extern "C" int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_ty
   if (da == nullptr || gu == nullptr || dgu == nullptr || !aligned16(da) || !aligned16(gu) ||
       !aligned16(dgu) || !aligned16(a))
     return MEP_ERR_INVALID_ARG;
+  constexpr int U = MEP_SWIGLU_UNROLL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int grid = grid_for(rows * F, 32 * kWarps);
   const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(da);
   __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16*>(dgu), *oa = reinterpret_cast<__nv_bfloat16*>(a);
-  const cudaError_t err =
-      gu_type == MEP_CKPT8 ? launch_pdl(k_swiglu_backward<true>, dim3(grid), dim3(32 * kWarps), 0, st,
-                                        in, gu, (long long)rows, int(F), o, oa)
-                           : launch_pdl(k_swiglu_backward<false>, dim3(grid), dim3(32 * kWarps), 0,
-                                        st, in, gu, (long long)rows, int(F), o, oa);
-  return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
+  const bool vec = F % 8 == 0, kept = gu_type == MEP_CKPT8;
+  const auto kernel = kept ? (vec ? k_swiglu_backward<MEP_CKPT8, true, U> : k_swiglu_backward<MEP_CKPT8, false, 1>)
+                           : (vec ? k_swiglu_backward<MEP_BF16, true, U> : k_swiglu_backward<MEP_BF16, false, 1>);
+  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+    const void* p = static_cast<const char*>(gu) + r * (kept ? 2 * ckpt_row_bytes(F) : 4 * F);
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, st, in + r * F, p, blocks, int(F), o + 2 * r * F,
+                      oa == nullptr ? nullptr : oa + r * F);
+  };
+  return vec ? sliced<U>(rows, F, f) : sliced<1>(rows, F, f);
 }

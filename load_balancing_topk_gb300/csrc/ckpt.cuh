@@ -44,11 +44,22 @@ __device__ __forceinline__ float ckpt_inv_step(int s) {
 __device__ __forceinline__ float ckpt_step(int s) {
   return __uint_as_float(s == kCkptNan ? 0x7fc00000u : uint32_t(s) << 23);
 }
-// One value as a byte. In a block with s = 255 every finite value becomes 0
-// (times 0) and the non-finite ones convert to some byte that is never read
-// as a value.
-__device__ __forceinline__ int ckpt_q(float x, float inv_step) {
-  return max(-127, min(127, __float2int_rn(x * inv_step)));
+// Eight values as bytes. A sum with 1.5 * 2^23 leaves the value rounded to
+// nearest-even in its low bits (a conversion instruction runs at an eighth of
+// the rate of an addition). In a block with s = 255 every finite value becomes
+// 0 (times 0), the others some byte that is never read as a value.
+__device__ __forceinline__ uint2 ckpt_pack8(const float (&v)[8], float inv_step) {
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    q[j] = __float_as_uint(fminf(fmaxf(v[j] * inv_step, -127.f), 127.f) + 12582912.f);
+  return make_uint2(
+      __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+}
+// Signed byte j of w as a float: its bits under 2^23, less 2^23 + 128.
+__device__ __forceinline__ float ckpt_byte(uint32_t w, int j) {
+  return __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 + j)) - 8388736.f;
 }
 // max that keeps a NaN (fmaxf drops it)
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -63,6 +74,170 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// Sixteen lanes share a block of 128 columns; each holds eight of them. VEC:
+// columns [8l, 8l + 8) of the block, whole 16-byte vectors (rows of a multiple
+// of 8 columns); else columns l, l + 16, ... one by one, which stay coalesced
+// where rows start anywhere.
+constexpr int kHalf = 16;
+
+template <bool VEC> __device__ __forceinline__ int half_col(int block, int l, int j) {
+  return block * kCkptBlock + (VEC ? 8 * l + j : l + kHalf * j);
+}
+__device__ __forceinline__ float half_max_nan(float v) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v = max_nan(v, __shfl_xor_sync(MEP_FULL_MASK, v, d));
+  return v;
+}
+
+// Eight values of a row as they lie in memory (columns beyond C are 0).
+template <int KIND> struct Pack;
+template <> struct Pack<MEP_BF16> {
+  uint32_t w[4];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void* base, long long row, int C, int block, int l) {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + row * C;
+    if (VEC) {
+      const int c = half_col<true>(block, l, 0);
+      const uint4 q = c < C ? ld_nc(reinterpret_cast<const uint4*>(p + c)) : make_uint4(0, 0, 0, 0);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c0 = half_col<false>(block, l, 2 * j), c1 = half_col<false>(block, l, 2 * j + 1);
+        w[j] = (c0 < C ? __ldg(p + c0) : 0u) | (c1 < C ? uint32_t(__ldg(p + c1)) << 16 : 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
+};
+template <> struct Pack<MEP_F32> {
+  float v[8];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void* base, long long row, int C, int block, int l) {
+    const float* p = static_cast<const float*>(base) + row * C;
+    if (VEC) {
+      const int c = half_col<true>(block, l, 0);
+      const bool in = c < C;
+      const float4* q = reinterpret_cast<const float4*>(p + c);
+      const float4 a = in ? __ldg(q) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 b = in ? __ldg(q + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = half_col<false>(block, l, j);
+        v[j] = c < C ? __ldg(p + c) : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const { return v[j]; }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+  }
+};
+template <> struct Pack<MEP_CKPT8> {
+  uint32_t w[2];
+  float step;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void* base, long long row, int C, int block, int l) {
+    const uint8_t* p = static_cast<const uint8_t*>(base) + row * ckpt_row_bytes(C);
+    const bool in = half_col<VEC>(block, l, 0) < C;
+    if (VEC) {
+      const uint2 q = in ? __ldg(reinterpret_cast<const uint2*>(p + half_col<true>(block, l, 0)))
+                         : make_uint2(0, 0);
+      w[0] = q.x, w[1] = q.y;
+    } else {
+      w[0] = w[1] = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = half_col<false>(block, l, j);
+        if (c < C) w[j >> 2] |= uint32_t(__ldg(p + c)) << (8 * (j & 3));
+      }
+    }
+    step = in ? ckpt_step(__ldg(p + ckpt_scale_at(C) + block)) : 0.f;
+  }
+  __device__ __forceinline__ float get(int j) const { return ckpt_byte(w[j >> 2], j & 3) * step; }
+  __device__ __forceinline__ void clear() { w[0] = w[1] = 0u, step = 0.f; }
+};
+
+// Eight values into a row, rounded to its type; v becomes what was stored.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* base, long long row, int C, int block, int l, float (&v)[8]) {
+  T* p = base + row * C;
+  if (sizeof(T) == 2) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      v[2 * j] = __uint_as_float(o[j] << 16);
+      v[2 * j + 1] = __uint_as_float(o[j] & 0xffff0000u);
+    }
+    if (VEC) {
+      const int c = half_col<true>(block, l, 0);
+      if (c < C) *reinterpret_cast<uint4*>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = half_col<false>(block, l, j);
+        if (c < C) reinterpret_cast<uint16_t*>(p)[c] = uint16_t(j & 1 ? o[j >> 1] >> 16 : o[j >> 1]);
+      }
+    }
+  } else {
+    if (VEC) {
+      const int c = half_col<true>(block, l, 0);
+      if (c < C) {
+        float4* q = reinterpret_cast<float4*>(p + c);
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = half_col<false>(block, l, j);
+        if (c < C) reinterpret_cast<float*>(p)[c] = v[j];
+      }
+    }
+  }
+}
+
+// One block of a checkpoint row from its sixteen lanes' values, all lanes of
+// the warp together (`in`: this half warp has a block). The lanes of a row's
+// last block also write its padding.
+template <bool VEC>
+__device__ __forceinline__ void save8(uint8_t* base, long long row, int C, int block, int l, bool in,
+                                      const float (&v)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[j]));
+  const int s = ckpt_scale(half_max_nan(top));
+  if (!in) return;
+  const uint2 q = ckpt_pack8(v, ckpt_inv_step(s));
+  uint8_t* p = base + row * ckpt_row_bytes(C);
+  if (VEC) {
+    const int c = half_col<true>(block, l, 0);
+    if (c < C) *reinterpret_cast<uint2*>(p + c) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = half_col<false>(block, l, j);
+      if (c < C) p[c] = uint8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+    }
+  }
+  const int at = ckpt_scale_at(C), nb = (C + kCkptBlock - 1) / kCkptBlock;
+  if (l == 0) p[at + block] = uint8_t(s);
+  if (block == nb - 1) {
+    if (C + l < at) p[C + l] = 0;
+    const int end = int(ckpt_row_bytes(C));
+    for (int i = at + nb + l; i < end; i += kHalf) p[i] = 0;
+  }
 }
 
 }  // namespace
