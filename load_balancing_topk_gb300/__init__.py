@@ -33,6 +33,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -462,6 +463,41 @@ def mep_grouped_gemm(x, cu_seqlens, w_home, w_slot, status, R: int, S: int, K: i
     return y
 
 
+# The calls below are short next to what a check or a launch costs on the host,
+# so their checks look at a good tensor once (_good) and name what is wrong
+# (_need) only when something is; sizes that the library computes are kept.
+def _good(t, name, dtype, shape, dev):
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t
+    except AttributeError:
+        pass
+    return _need(t, name, dtype, shape, dev)
+
+
+def _call(fn: str, dev, *args) -> None:
+    """Enqueue one library call on the current stream of dev."""
+    torch = _torch()
+    lib = _lib if _lib is not None else load_library()
+    if torch.cuda.current_device() == dev.index:
+        rc = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc != 0:
+        raise MepError(fn, rc)
+
+
+def _cuda_device(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+@functools.lru_cache(maxsize=256)
 def ckpt_row_bytes(C: int) -> int:
     """Bytes of one checkpoint row of C columns (a multiple of 32)."""
     out = ctypes.c_size_t(0)
@@ -469,6 +505,7 @@ def ckpt_row_bytes(C: int) -> int:
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
     out = ctypes.c_size_t(0)
     _check("mep_layer_norm_backward_workspace_bytes",
@@ -476,6 +513,7 @@ def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
     return int(out.value)
 
 
+@functools.lru_cache(maxsize=256)
 def grouped_wgrad_workspace_bytes(R: int, S: int, K: int, E: int, B: int) -> int:
     out = ctypes.c_size_t(0)
     _check("mep_grouped_wgrad_workspace_bytes",
@@ -488,22 +526,35 @@ def _float_type(t, name) -> int:
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    return _BF16 if t.dtype == torch.bfloat16 else _F32
+    if t.dtype is torch.bfloat16:
+        return _BF16
+    if t.dtype is torch.float32:
+        return _F32
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def _matrix(t, name) -> int:
+    """Type of a dense CUDA matrix in bf16 or fp32."""
+    kind = _float_type(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return kind
 
 
 def _need_params(weight, bias, H, dev) -> int:
     """Checks a norm's weight and bias (each may be None); their type."""
     kind = None
     for name, p in (("weight", weight), ("bias", bias)):
-        if p is None:
-            continue
-        t = _float_type(p, name)
-        _need(p, name, p.dtype, (H,), dev)
-        if kind is not None and t != kind:
-            raise TypeError("weight and bias must have the same dtype")
-        kind = t
+        if p is not None:
+            t = _float_type(p, name)
+            _good(p, name, p.dtype, (H,), dev)
+            if kind is not None and t != kind:
+                raise TypeError("weight and bias must have the same dtype")
+            kind = t
     return _F32 if kind is None else kind
 
 
@@ -514,20 +565,14 @@ def mep_ckpt_save(x, ckpt=None):
     that mep_dispatch can permute the rows seen as bf16.
     """
     torch = _torch()
-    kind = _float_type(x, "x")
-    _need(x, "x", x.dtype)
-    if x.dim() != 2:
-        raise ValueError("x must be [N, C]")
+    kind = _matrix(x, "x")
     N, C = x.shape
-    rb = ckpt_row_bytes(C)
-    dev = x.device
+    dev, rb = x.device, ckpt_row_bytes(C)
     if ckpt is None:
         ckpt = torch.empty((N, rb), dtype=torch.uint8, device=dev)
     else:
-        _need(ckpt, "ckpt", torch.uint8, (N, rb), dev)
-    with torch.cuda.device(dev):
-        rc = load_library().mep_ckpt_save(_ptr(x), kind, N, C, _ptr(ckpt), _stream(dev))
-    _check("mep_ckpt_save", rc)
+        _good(ckpt, "ckpt", torch.uint8, (N, rb), dev)
+    _call("mep_ckpt_save", dev, x.data_ptr(), kind, N, C, ckpt.data_ptr())
     return ckpt
 
 
@@ -535,18 +580,18 @@ def mep_ckpt_load(ckpt, C: int, x=None, dtype=None):
     """The values of checkpoint rows (uint8 [N, ckpt_row_bytes(C)]): [N, C] in x's
     dtype, or ``dtype`` (bf16 unless given; both hold the values exactly)."""
     torch = _torch()
-    _need(ckpt, "ckpt", torch.uint8)
-    rb = ckpt_row_bytes(C)
+    dev, rb = _cuda_device(ckpt, "ckpt"), ckpt_row_bytes(C)
     if ckpt.dim() != 2 or ckpt.shape[1] != rb:
         raise ValueError(f"ckpt must be [N, {rb}] for {C} columns")
-    N, dev = ckpt.shape[0], ckpt.device
+    N = ckpt.shape[0]
+    _good(ckpt, "ckpt", torch.uint8, (N, rb), dev)
     if x is None:
         x = torch.empty((N, C), dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
-    kind = _float_type(x, "x")
-    _need(x, "x", x.dtype if dtype is None else dtype, (N, C), dev)
-    with torch.cuda.device(dev):
-        rc = load_library().mep_ckpt_load(_ptr(ckpt), N, C, kind, _ptr(x), _stream(dev))
-    _check("mep_ckpt_load", rc)
+        kind = _float_type(x, "x")
+    else:
+        kind = _float_type(x, "x")
+        _good(x, "x", x.dtype if dtype is None else dtype, (N, C), dev)
+    _call("mep_ckpt_load", dev, ckpt.data_ptr(), N, C, kind, x.data_ptr())
     return x
 
 
@@ -559,27 +604,19 @@ def mep_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=No
     mep_layer_norm_backward) and y (for mep_grouped_wgrad) in, or None.
     """
     torch = _torch()
-    kind = _float_type(x, "x")
-    _need(x, "x", x.dtype)
-    if x.dim() != 2:
-        raise ValueError("x must be [N, H]")
+    kind = _matrix(x, "x")
     N, H = x.shape
     dev = x.device
     p_kind = _need_params(weight, bias, H, dev)
-    y = torch.empty_like(x) if y is None else _need(y, "y", x.dtype, (N, H), dev)
-    stats = []
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        stats.append(torch.empty(N, dtype=torch.float32, device=dev) if t is None
-                     else _need(t, name, torch.float32, (N,), dev))
-    mean, rstd = stats
+    y = torch.empty_like(x) if y is None else _good(y, "y", x.dtype, (N, H), dev)
+    f32 = torch.float32
+    mean = torch.empty(N, dtype=f32, device=dev) if mean is None else _good(mean, "mean", f32, (N,), dev)
+    rstd = torch.empty(N, dtype=f32, device=dev) if rstd is None else _good(rstd, "rstd", f32, (N,), dev)
     for name, t in (("x_ckpt", x_ckpt), ("y_ckpt", y_ckpt)):
         if t is not None:
-            _need(t, name, torch.uint8, (N, ckpt_row_bytes(H)), dev)
-    with torch.cuda.device(dev):
-        rc = load_library().mep_layer_norm(_ptr(x), kind, _ptr(weight), _ptr(bias), p_kind, eps, N, H,
-                                           _ptr(y), _ptr(mean), _ptr(rstd), _ptr(x_ckpt),
-                                           _ptr(y_ckpt), _stream(dev))
-    _check("mep_layer_norm", rc)
+            _good(t, name, torch.uint8, (N, ckpt_row_bytes(H)), dev)
+    _call("mep_layer_norm", dev, x.data_ptr(), kind, _ptr(weight), _ptr(bias), p_kind, eps, N, H,
+          y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(x_ckpt), _ptr(y_ckpt))
     return y, mean, rstd
 
 
@@ -593,31 +630,25 @@ def mep_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     ``accumulate``). ``params=False``: dx alone, (dx, None, None).
     """
     torch = _torch()
-    kind = _float_type(dy, "dy")
-    _need(dy, "dy", dy.dtype)
-    if dy.dim() != 2:
-        raise ValueError("dy must be [N, H]")
+    kind = _matrix(dy, "dy")
     N, H = dy.shape
-    dev = dy.device
-    if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
+    dev, f32 = dy.device, torch.float32
+    if isinstance(x, torch.Tensor) and x.dtype is torch.uint8:
         x_kind = _CKPT8
-        _need(x, "x", torch.uint8, (N, ckpt_row_bytes(H)), dev)
+        _good(x, "x", torch.uint8, (N, ckpt_row_bytes(H)), dev)
     else:
         x_kind = kind
-        _need(x, "x", dy.dtype, (N, H), dev)
+        _good(x, "x", dy.dtype, (N, H), dev)
     p_kind = _need_params(weight, None, H, dev)
-    _need(mean, "mean", torch.float32, (N,), dev)
-    _need(rstd, "rstd", torch.float32, (N,), dev)
-    dx = torch.empty_like(dy) if dx is None else _need(dx, "dx", dy.dtype, (N, H), dev)
+    _good(mean, "mean", f32, (N,), dev)
+    _good(rstd, "rstd", f32, (N,), dev)
+    dx = torch.empty_like(dy) if dx is None else _good(dx, "dx", dy.dtype, (N, H), dev)
     need = 0
     if params:
         if accumulate and (dweight is None or dbias is None):
             raise ValueError("accumulate needs dweight and dbias to add to")
-        grads = []
-        for name, t in (("dweight", dweight), ("dbias", dbias)):
-            grads.append(torch.empty(H, dtype=torch.float32, device=dev) if t is None
-                         else _need(t, name, torch.float32, (H,), dev))
-        dweight, dbias = grads
+        dweight = torch.empty(H, dtype=f32, device=dev) if dweight is None else _good(dweight, "dweight", f32, (H,), dev)
+        dbias = torch.empty(H, dtype=f32, device=dev) if dbias is None else _good(dbias, "dbias", f32, (H,), dev)
         need = layer_norm_backward_workspace_bytes(N, H)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -627,12 +658,9 @@ def mep_layer_norm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
                 raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
     elif dweight is not None or dbias is not None:
         raise ValueError("params=False computes neither dweight nor dbias")
-    with torch.cuda.device(dev):
-        rc = load_library().mep_layer_norm_backward(
-            _ptr(dy), kind, _ptr(x), x_kind, _ptr(weight), p_kind, _ptr(mean), _ptr(rstd), N, H,
-            _ptr(workspace) if params else None, need, _ptr(dx), _ptr(dweight), _ptr(dbias),
-            1 if accumulate else 0, _stream(dev))
-    _check("mep_layer_norm_backward", rc)
+    _call("mep_layer_norm_backward", dev, dy.data_ptr(), kind, x.data_ptr(), x_kind, _ptr(weight), p_kind,
+          mean.data_ptr(), rstd.data_ptr(), N, H, _ptr(workspace) if params else None, need, dx.data_ptr(),
+          _ptr(dweight), _ptr(dbias), 1 if accumulate else 0)
     return dx, dweight, dbias
 
 
@@ -642,20 +670,15 @@ def mep_swiglu(gu, a=None, ckpt=None):
     ckpt: uint8 [rows, 2, ckpt_row_bytes(F)] to keep gu in for the backward pass, or None.
     """
     torch = _torch()
-    _need(gu, "gu", torch.bfloat16)
+    dev, bf16 = _cuda_device(gu, "gu"), torch.bfloat16
     if gu.dim() != 2 or gu.shape[1] < 2 or gu.shape[1] % 2:
         raise ValueError("gu must be [rows, 2F]")
     rows, F = gu.shape[0], gu.shape[1] // 2
-    dev = gu.device
-    if a is None:
-        a = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(a, "a", torch.bfloat16, (rows, F), dev)
+    _good(gu, "gu", bf16, (rows, 2 * F), dev)
+    a = torch.empty((rows, F), dtype=bf16, device=dev) if a is None else _good(a, "a", bf16, (rows, F), dev)
     if ckpt is not None:
-        _need(ckpt, "ckpt", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
-    with torch.cuda.device(dev):
-        rc = load_library().mep_swiglu(_ptr(gu), rows, F, _ptr(a), _ptr(ckpt), _stream(dev))
-    _check("mep_swiglu", rc)
+        _good(ckpt, "ckpt", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
+    _call("mep_swiglu", dev, gu.data_ptr(), rows, F, a.data_ptr(), _ptr(ckpt))
     return a
 
 
@@ -667,32 +690,27 @@ def mep_swiglu_backward(da, gu, dgu=None, a=None, again: bool = True):
     stands for (None where ``again`` is false).
     """
     torch = _torch()
-    _need(da, "da", torch.bfloat16)
+    dev, bf16 = _cuda_device(da, "da"), torch.bfloat16
     if da.dim() != 2:
         raise ValueError("da must be [rows, F]")
     rows, F = da.shape
-    dev = da.device
-    if isinstance(gu, torch.Tensor) and gu.dtype == torch.uint8:
+    _good(da, "da", bf16, (rows, F), dev)
+    if isinstance(gu, torch.Tensor) and gu.dtype is torch.uint8:
         kind = _CKPT8
-        _need(gu, "gu", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
+        _good(gu, "gu", torch.uint8, (rows, 2, ckpt_row_bytes(F)), dev)
     else:
         kind = _BF16
-        _need(gu, "gu", torch.bfloat16, (rows, 2 * F), dev)
-    if dgu is None:
-        dgu = torch.empty((rows, 2 * F), dtype=torch.bfloat16, device=dev)
-    else:
-        _need(dgu, "dgu", torch.bfloat16, (rows, 2 * F), dev)
+        _good(gu, "gu", bf16, (rows, 2 * F), dev)
+    dgu = (torch.empty((rows, 2 * F), dtype=bf16, device=dev) if dgu is None
+           else _good(dgu, "dgu", bf16, (rows, 2 * F), dev))
     if not again:
         if a is not None:
             raise ValueError("again=False does not compute a")
     elif a is None:
-        a = torch.empty((rows, F), dtype=torch.bfloat16, device=dev)
+        a = torch.empty((rows, F), dtype=bf16, device=dev)
     else:
-        _need(a, "a", torch.bfloat16, (rows, F), dev)
-    with torch.cuda.device(dev):
-        rc = load_library().mep_swiglu_backward(_ptr(da), _ptr(gu), kind, rows, F, _ptr(dgu), _ptr(a),
-                                                _stream(dev))
-    _check("mep_swiglu_backward", rc)
+        _good(a, "a", bf16, (rows, F), dev)
+    _call("mep_swiglu_backward", dev, da.data_ptr(), gu.data_ptr(), kind, rows, F, dgu.data_ptr(), _ptr(a))
     return dgu, a
 
 
@@ -707,32 +725,33 @@ def mep_grouped_wgrad(x, dy, cu_seqlens, home_grad, slot_grad, status, R: int, S
     them. Slots without rows are left alone. Returns (home_grad, slot_grad).
     """
     torch = _torch()
-    _need(dy, "dy", torch.bfloat16)
-    dev = dy.device
-    _need(home_grad, "home_grad", torch.float32, None, dev)
-    if home_grad.dim() != 3:
+    dev = _cuda_device(dy, "dy")
+    if not isinstance(home_grad, torch.Tensor) or home_grad.dim() != 3:
         raise ValueError("home_grad must be [E, H, H']")
     E, H, Hp = home_grad.shape
-    _need(cu_seqlens, "cu_seqlens", torch.int32, None, dev)
-    if cu_seqlens.dim() != 2 or cu_seqlens.shape[0] != R:
+    _good(home_grad, "home_grad", torch.float32, (E, H, Hp), dev)
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 2 or cu_seqlens.shape[0] != R:
         raise ValueError("cu_seqlens must be [R, E+B]")
     B = cu_seqlens.shape[1] - E
     if B < 0:
         raise ValueError("cu_seqlens must have E+B columns")
+    _good(cu_seqlens, "cu_seqlens", torch.int32, (R, E + B), dev)
     rows = R * S * K
-    if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
+    _good(dy, "dy", torch.bfloat16, dy.shape, dev)
+    if isinstance(x, torch.Tensor) and x.dtype is torch.uint8:
         kind, width = _CKPT8, ckpt_row_bytes(H)
+        _good(x, "x", torch.uint8, x.shape, dev)
     else:
         kind, width = _BF16, H
-    _need(x, "x", torch.uint8 if kind == _CKPT8 else torch.bfloat16, None, dev)
+        _need(x, "x", torch.bfloat16, None, dev)
     if x.numel() != rows * width:
         raise ValueError(f"x must hold R*S*K rows of {width}")
     if dy.numel() != rows * Hp:
         raise ValueError("dy must hold R*S*K rows of H'")
     if B > 0:
-        _need(slot_grad, "slot_grad", torch.float32, (R, B, H, Hp), dev)
+        _good(slot_grad, "slot_grad", torch.float32, (R, B, H, Hp), dev)
     if status is not None:
-        _need(status, "status", torch.int32, (1,), dev)
+        _good(status, "status", torch.int32, (1,), dev)
     need = grouped_wgrad_workspace_bytes(R, S, K, E, B)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
@@ -740,12 +759,9 @@ def mep_grouped_wgrad(x, dy, cu_seqlens, home_grad, slot_grad, status, R: int, S
         _need(workspace, "workspace", torch.uint8, None, dev)
         if workspace.numel() < need:
             raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
-    with torch.cuda.device(dev):
-        rc = load_library().mep_grouped_wgrad(
-            _ptr(x), kind, _ptr(dy), _ptr(cu_seqlens), _ptr(status), R, S, K, E, B, H, Hp,
-            1 if accumulate else 0, _ptr(workspace), workspace.numel(), _ptr(home_grad),
-            _ptr(slot_grad) if B > 0 else None, _stream(dev))
-    _check("mep_grouped_wgrad", rc)
+    _call("mep_grouped_wgrad", dev, x.data_ptr(), kind, dy.data_ptr(), cu_seqlens.data_ptr(), _ptr(status),
+          R, S, K, E, B, H, Hp, 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(),
+          home_grad.data_ptr(), slot_grad.data_ptr() if B > 0 else None)
     return home_grad, slot_grad
 
 
