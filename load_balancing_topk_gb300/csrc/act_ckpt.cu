@@ -62,10 +62,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float v[8];
+    F2 v[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = p[u].get(j);
-    save8<VEC>(ckpt, w[u].row, C, w[u].block, l, w[u].in, v);
+    for (int j = 0; j < 4; ++j) v[j] = p[u].at(j);
+    save8<VEC>(ckpt + w[u].row * ckpt_row_bytes(C), C, w[u].block, l, w[u].in, v);
   }
 }
 
@@ -84,15 +84,16 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (w[u].in) {
-      float v[8];
+      F2 v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[u].get(j);
-      store8<T, VEC>(x, w[u].row, C, w[u].block, l, v);
+      for (int j = 0; j < 4; ++j) v[j] = p[u].at(j);
+      store8<T, VEC>(x + w[u].row * C, C, w[u].block, l, v);
     }
 }
 
 // 1 / (1 + e^-g); the quotient to 2 ulp (0 where e^-g overflows)
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+__device__ __forceinline__ F2 sigmoid2(F2 g) { return pair(sigmoid(g.x()), sigmoid(g.y())); }
 
 template <bool VEC, bool CKPT, int U>
 __global__ void __launch_bounds__(kThreads)
@@ -115,17 +116,17 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float v[2][8], o[8];
+    F2 v[2][4], o[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      v[0][j] = p[u][0].get(j);
-      v[1][j] = p[u][1].get(j);
-      o[j] = v[0][j] * sigmoid(v[0][j]) * v[1][j];
+    for (int j = 0; j < 4; ++j) {
+      v[0][j] = p[u][0].at(j);
+      v[1][j] = p[u][1].at(j);
+      o[j] = mul2(mul2(v[0][j], sigmoid2(v[0][j])), v[1][j]);
     }
-    if (w[u].in) store8<__nv_bfloat16, VEC>(a, w[u].row, F, w[u].block, l, o);
+    if (w[u].in) store8<__nv_bfloat16, VEC>(a + w[u].row * F, F, w[u].block, l, o);
     if (CKPT) {
-      save8<VEC>(ckpt, 2 * w[u].row, F, w[u].block, l, w[u].in, v[0]);
-      save8<VEC>(ckpt, 2 * w[u].row + 1, F, w[u].block, l, w[u].in, v[1]);
+      save8<VEC>(ckpt + 2 * w[u].row * ckpt_row_bytes(F), F, w[u].block, l, w[u].in, v[0]);
+      save8<VEC>(ckpt + (2 * w[u].row + 1) * ckpt_row_bytes(F), F, w[u].block, l, w[u].in, v[1]);
     }
   }
 }
@@ -152,17 +153,18 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (w[u].in) {
-      float dg[8], du[8], o[8];
+      F2 dg[4], du[4], o[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float g = p[u][0].get(j), up = p[u][1].get(j), dv = d[u].get(j), s = sigmoid(g);
-        dg[j] = dv * up * s * (1.f + g * (1.f - s));
-        du[j] = dv * (g * s);
-        o[j] = g * s * up;
+      for (int j = 0; j < 4; ++j) {
+        const F2 g = p[u][0].at(j), up = p[u][1].at(j), dv = d[u].at(j), s = sigmoid2(g);
+        const F2 one = both(1.f), gs = mul2(g, s), rest = fma2(both(-1.f), s, one);  // 1 - s
+        dg[j] = mul2(mul2(mul2(dv, up), s), fma2(g, rest, one));
+        du[j] = mul2(dv, gs);
+        o[j] = mul2(gs, up);
       }
-      store8<__nv_bfloat16, VEC>(dgu, 2 * w[u].row, F, w[u].block, l, dg);
-      store8<__nv_bfloat16, VEC>(dgu, 2 * w[u].row + 1, F, w[u].block, l, du);
-      if (a != nullptr) store8<__nv_bfloat16, VEC>(a, w[u].row, F, w[u].block, l, o);
+      store8<__nv_bfloat16, VEC>(dgu + 2 * w[u].row * F, F, w[u].block, l, dg);
+      store8<__nv_bfloat16, VEC>(dgu + (2 * w[u].row + 1) * F, F, w[u].block, l, du);
+      if (a != nullptr) store8<__nv_bfloat16, VEC>(a + w[u].row * F, F, w[u].block, l, o);
     }
 }
 

@@ -44,22 +44,10 @@ __device__ __forceinline__ float ckpt_inv_step(int s) {
 __device__ __forceinline__ float ckpt_step(int s) {
   return __uint_as_float(s == kCkptNan ? 0x7fc00000u : uint32_t(s) << 23);
 }
-// Eight values as bytes. A sum with 1.5 * 2^23 leaves the value rounded to
-// nearest-even in its low bits (a conversion instruction runs at an eighth of
-// the rate of an addition). In a block with s = 255 every finite value becomes
-// 0 (times 0), the others some byte that is never read as a value.
-__device__ __forceinline__ uint2 ckpt_pack8(const float (&v)[8], float inv_step) {
-  uint32_t q[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    q[j] = __float_as_uint(fminf(fmaxf(v[j] * inv_step, -127.f), 127.f) + 12582912.f);
-  return make_uint2(
-      __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
-      __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
-}
 // Signed byte j of w as a float: its bits under 2^23, less 2^23 + 128.
+// (w here with its bytes' sign bits flipped.)
 __device__ __forceinline__ float ckpt_byte(uint32_t w, int j) {
-  return __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7440 + j)) - 8388736.f;
+  return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + j));
 }
 // max that keeps a NaN (fmaxf drops it)
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -74,6 +62,63 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
+}
+
+// ---------------------------------------------------------------------------
+// Two fp32 values in one 64-bit register, and operations on both at once, each
+// rounded as the single form is.
+struct F2 {
+  unsigned long long v;
+  __device__ __forceinline__ float x() const { return __uint_as_float(uint32_t(v)); }
+  __device__ __forceinline__ float y() const { return __uint_as_float(uint32_t(v >> 32)); }
+};
+__device__ __forceinline__ F2 pair(float x, float y) {
+  F2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d.v) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ F2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+// Two bf16 of a word, widened.
+__device__ __forceinline__ F2 widen(uint32_t w) {
+  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Four pairs of values as eight bytes. x * 2^-k + 1.5 * 2^23 in one rounding
+// leaves x * 2^-k rounded to nearest-even in the low bits (a conversion
+// instruction runs at an eighth of the rate). Only a block whose largest value
+// is at least 127.5 steps can round to 128: `full`, one in a hundred. In a
+// block with s = 255 every finite value becomes 0 (times 0), the others some
+// byte that is never read as a value.
+__device__ __forceinline__ uint2 ckpt_pack8(const F2 (&v)[4], float inv_step, bool full) {
+  F2 r[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) r[j] = fma2(v[j], both(inv_step), both(12582912.f));
+  if (full) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r[j] = pair(fminf(fmaxf(r[j].x(), 12582912.f - 127.f), 12582912.f + 127.f),
+                  fminf(fmaxf(r[j].y(), 12582912.f - 127.f), 12582912.f + 127.f));
+    }
+  }
+  uint32_t q[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) q[j] = __byte_perm(uint32_t(r[j].v), uint32_t(r[j].v >> 32), 0x0040);
+  return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
 // ---------------------------------------------------------------------------
@@ -111,8 +156,8 @@ template <> struct Pack<MEP_BF16> {
       }
     }
   }
-  __device__ __forceinline__ float get(int j) const {
-    return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  __device__ __forceinline__ F2 at(int j) const {  // values 2j and 2j + 1
+    return widen(w[j]);
   }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
 };
@@ -136,7 +181,7 @@ template <> struct Pack<MEP_F32> {
       }
     }
   }
-  __device__ __forceinline__ float get(int j) const { return v[j]; }
+  __device__ __forceinline__ F2 at(int j) const { return pair(v[2 * j], v[2 * j + 1]); }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -163,22 +208,24 @@ template <> struct Pack<MEP_CKPT8> {
     }
     step = in ? ckpt_step(__ldg(p + ckpt_scale_at(C) + block)) : 0.f;
   }
-  __device__ __forceinline__ float get(int j) const { return ckpt_byte(w[j >> 2], j & 3) * step; }
+  __device__ __forceinline__ F2 at(int j) const {
+    const uint32_t u = w[j >> 1] ^ 0x80808080u;
+    const int b = 2 * (j & 1);
+    return mul2(add2(pair(ckpt_byte(u, b), ckpt_byte(u, b + 1)), both(-8388736.f)), both(step));
+  }
   __device__ __forceinline__ void clear() { w[0] = w[1] = 0u, step = 0.f; }
 };
 
-// Eight values into a row, rounded to its type; v becomes what was stored.
+// Four pairs of values into the row at p, rounded to its type; v becomes what was stored.
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* base, long long row, int C, int block, int l, float (&v)[8]) {
-  T* p = base + row * C;
+__device__ __forceinline__ void store8(T* p, int C, int block, int l, F2 (&v)[4]) {
   if (sizeof(T) == 2) {
     uint32_t o[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x(), v[j].y());
       o[j] = *reinterpret_cast<const uint32_t*>(&h);
-      v[2 * j] = __uint_as_float(o[j] << 16);
-      v[2 * j + 1] = __uint_as_float(o[j] & 0xffff0000u);
+      v[j] = widen(o[j]);
     }
     if (VEC) {
       const int c = half_col<true>(block, l, 0);
@@ -195,32 +242,32 @@ __device__ __forceinline__ void store8(T* base, long long row, int C, int block,
       const int c = half_col<true>(block, l, 0);
       if (c < C) {
         float4* q = reinterpret_cast<float4*>(p + c);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        q[0] = make_float4(v[0].x(), v[0].y(), v[1].x(), v[1].y());
+        q[1] = make_float4(v[2].x(), v[2].y(), v[3].x(), v[3].y());
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = half_col<false>(block, l, j);
-        if (c < C) reinterpret_cast<float*>(p)[c] = v[j];
+        if (c < C) reinterpret_cast<float*>(p)[c] = j & 1 ? v[j >> 1].y() : v[j >> 1].x();
       }
     }
   }
 }
 
-// One block of a checkpoint row from its sixteen lanes' values, all lanes of
+// One block of the checkpoint row at p from its sixteen lanes' values, all lanes of
 // the warp together (`in`: this half warp has a block). The lanes of a row's
 // last block also write its padding.
 template <bool VEC>
-__device__ __forceinline__ void save8(uint8_t* base, long long row, int C, int block, int l, bool in,
-                                      const float (&v)[8]) {
+__device__ __forceinline__ void save8(uint8_t* p, int C, int block, int l, bool in, const F2 (&v)[4]) {
   float top = 0.f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[j]));
-  const int s = ckpt_scale(half_max_nan(top));
+  for (int j = 0; j < 4; ++j) top = max_nan(top, max_nan(fabsf(v[j].x()), fabsf(v[j].y())));
+  top = half_max_nan(top);
   if (!in) return;
-  const uint2 q = ckpt_pack8(v, ckpt_inv_step(s));
-  uint8_t* p = base + row * ckpt_row_bytes(C);
+  const int s = ckpt_scale(top);
+  const float inv = ckpt_inv_step(s);
+  const uint2 q = ckpt_pack8(v, inv, top * inv >= 127.5f);
   if (VEC) {
     const int c = half_col<true>(block, l, 0);
     if (c < C) *reinterpret_cast<uint2*>(p + c) = q;

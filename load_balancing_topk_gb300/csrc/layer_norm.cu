@@ -7,6 +7,11 @@
 // (the checkpoint's blocks, so that a block's largest magnitude is four
 // shuffles away). Sums over a row go through shuffles and, for W > 1, a few
 // words of shared memory.
+// A row of a multiple of 8 columns is fetched ahead: every thread copies its
+// own vectors of the rows of the next turns into its own slots of shared memory
+// (cp.async), so that the next rows' loads are under way while a row's sums
+// are, and no thread waits for another's copies. Registers alone (rows loaded
+// as they are used) held too few loads in flight: see the figures below.
 //   k_norm       the mean first, then the sum of the centred squares: with
 //                the row in registers the second pass costs no memory, and a
 //                row far from zero loses nothing to cancellation.
@@ -23,6 +28,11 @@ namespace {
 
 constexpr int kMaxH = MEP_MAX_NORM_H;
 constexpr int kMaxWarps = 32;
+// Turns whose rows are on their way: up to four, as many as fit `room` bytes of
+// slots a thread.
+__host__ __device__ constexpr int ahead_of(int bytes, int room) {
+  return room / bytes >= 4 ? 4 : room / bytes > 1 ? room / bytes : 1;
+}
 
 // ---------------------------------------------------------------------------
 // Barrier of one row group: W warps (of a CTA that may hold several groups).
@@ -30,116 +40,33 @@ __device__ __forceinline__ void group_sync(int group, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ float param(const void* p, int type, int h) {
-  return type == MEP_F32 ? __ldg(static_cast<const float*>(p) + h)
-                         : to_f32(static_cast<const __nv_bfloat16*>(p)[h]);
-}
 // Eight parameters of a block; `none` without the tensor, 0 beyond H.
 template <bool VEC>
 __device__ __forceinline__ void load_params(const void* p, int type, int H, int block, int l,
-                                            float none, float (&v)[8]) {
+                                            float none, F2 (&v)[4]) {
   if (p == nullptr) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = none;
-  } else if (VEC && type == MEP_F32) {
+    for (int j = 0; j < 4; ++j) v[j] = both(none);
+  } else if (type == MEP_F32) {
     Pack<MEP_F32> q;
-    q.load<true>(p, 0, H, block, l);
+    q.load<VEC>(p, 0, H, block, l);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = q.get(j);
-  } else if (VEC) {
-    Pack<MEP_BF16> q;
-    q.load<true>(p, 0, H, block, l);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = q.get(j);
+    for (int j = 0; j < 4; ++j) v[j] = q.at(j);
   } else {
+    Pack<MEP_BF16> q;
+    q.load<VEC>(p, 0, H, block, l);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int h = half_col<false>(block, l, j);
-      v[j] = h < H ? param(p, type, h) : 0.f;
-    }
+    for (int j = 0; j < 4; ++j) v[j] = q.at(j);
   }
 }
 
-// Sum of v over the W warps of a group; s holds W words, not in use elsewhere
-// before the next barrier of the group.
-__device__ __forceinline__ float group_sum(float v, float* s, int W, int warp, int group) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(MEP_FULL_MASK, v, d);
-  if (W == 1) return v;
-  if (lane == 0) s[warp] = v;
-  group_sync(group, 32 * W);
-  v = lane < W ? s[lane] : 0.f;
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(MEP_FULL_MASK, v, d);
-  return v;
-}
-
-// J blocks a half warp, W warps a row: 2 J W >= blocks of a row.
-template <typename T, int KIND, bool VEC, int J>
-__global__ void __launch_bounds__(32 * kMaxWarps / (J > 2 ? 2 : 1))
-    k_norm(const T* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b, int p_type,
-           float eps, long long N, int H, int W, T* __restrict__ y, float* __restrict__ mean,
-           float* __restrict__ rstd, uint8_t* __restrict__ x_ckpt, uint8_t* __restrict__ y_ckpt) {
-  pdl_wait();
-  pdl_launch_dependents();
-  __shared__ float s_sum[4][kMaxWarps];  // [mean and square, twice][warps of all groups]
-  const int l = threadIdx.x % kHalf;
-  const int group = (threadIdx.x >> 5) / W, groups = blockDim.x / (32 * W);
-  const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
-  const int nb = (H + kCkptBlock - 1) / kCkptBlock;
-  const float inv_h = 1.f / H;
-  int turn = 0;
-  for (long long r = (long long)blockIdx.x * groups + group; r < N;
-       r += (long long)gridDim.x * groups, turn ^= 2) {
-    Pack<KIND> p[J];
-#pragma unroll
-    for (int i = 0; i < J; ++i) p[i].template load<VEC>(x, r, H, half + 2 * W * i, l);
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < J; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += p[i].get(j);
-    const float m = group_sum(sum, &s_sum[turn][group * W], W, warp, group) * inv_h;
-    float sq = 0.f;
-#pragma unroll
-    for (int i = 0; i < J; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float c = half_col<VEC>(half + 2 * W * i, l, j) < H ? p[i].get(j) - m : 0.f;
-        sq = fmaf(c, c, sq);
-      }
-    const float rs = 1.f / sqrtf(group_sum(sq, &s_sum[turn + 1][group * W], W, warp, group) * inv_h + eps);
-    if (warp == 0 && (threadIdx.x & 31) == 0) {
-      mean[r] = m;
-      rstd[r] = rs;
-    }
-#pragma unroll
-    for (int i = 0; i < J; ++i) {
-      const int block = half + 2 * W * i;
-      const bool in = block < nb;
-      float v[8], wv[8], bv[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = p[i].get(j);
-      if (x_ckpt != nullptr) save8<VEC>(x_ckpt, r, H, block, l, in, v);
-      load_params<VEC>(w, p_type, H, block, l, 1.f, wv);
-      load_params<VEC>(b, p_type, H, block, l, 0.f, bv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = half_col<VEC>(block, l, j) < H ? fmaf((v[j] - m) * rs, wv[j], bv[j]) : 0.f;
-      store8<T, VEC>(y, r, H, block, l, v);
-      if (y_ckpt != nullptr) save8<VEC>(y_ckpt, r, H, block, l, in, v);
-    }
-  }
-}
-
-// Sums over a group of 2U values a thread, two for each of U rows: the lanes
+// Sums of n (2 or 4) values a thread over the W warps of a group. The lanes
 // first share the values out among themselves (each step halves the values a
-// lane still carries), so that a warp needs 2U + 5 - log2(2U) - 1 shuffles
-// and not 10U.
-template <int U>
-__device__ __forceinline__ void group_sums(float (&v)[2 * U], float* s, int W, int warp, int group) {
-  constexpr int n = 2 * U;
+// lane still carries): 6 or 7 shuffles a warp, not 10 or 20. s holds n words a
+// warp, not in use elsewhere before the group's next barrier but one.
+template <int n>
+__device__ __forceinline__ void group_sums(float (&v)[n], float* s, int W, int warp, int group) {
+  constexpr int lanes = 32 / n;  // that carry the same value in the end
   const int lane = threadIdx.x & 31;
   int d = 16;
 #pragma unroll
@@ -151,109 +78,416 @@ __device__ __forceinline__ void group_sums(float (&v)[2 * U], float* s, int W, i
       v[i] = keep + __shfl_xor_sync(MEP_FULL_MASK, give, d);
     }
   }
-  float t = v[0];  // of value `mine`, over the lanes that share d's remaining bits
-  for (; d >= 1; d >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, d);
-  // lane bits 4, 3, ... choose the value, high bit first
-  const int mine = lane / (32 / n);
+  float t = v[0];
+#pragma unroll
+  for (int e = lanes / 2; e >= 1; e >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, e);
+  // the lane's bits 4, 3, ... say which value it has, high bit first
   if (W > 1) {
-    if (lane % (32 / n) == 0) s[warp * n + mine] = t;
+    const int mine = lane / lanes, k0 = lane % lanes;
+    if (k0 == 0) s[warp * n + mine] = t;
     group_sync(group, 32 * W);
     t = 0.f;
-    for (int k = lane % (32 / n); k < W; k += 32 / n) t += s[k * n + mine];
+    for (int k = k0; k < W; k += lanes) t += s[k * n + mine];
 #pragma unroll
-    for (int e = 16 / n; e >= 1; e >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, e);
+    for (int e = lanes / 2; e >= 1; e >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, e);
   }
 #pragma unroll
-  for (int i = 0; i < n; ++i) v[i] = __shfl_sync(MEP_FULL_MASK, t, i * (32 / n));
+  for (int i = 0; i < n; ++i) v[i] = __shfl_sync(MEP_FULL_MASK, t, i * lanes);
 }
 
-template <typename T, int KIND, int XKIND, bool VEC, int J, int U>
-__global__ void __launch_bounds__(U == 4 ? 512 : 1024)
+// ---------------------------------------------------------------------------
+// A thread's slots. Piece i of thread t lies at (i * threads + t) * 16 bytes
+// (8 for checkpoint bytes): neighbours side by side.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest `left` groups of this thread's copies have landed.
+template <int left> __device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(left) : "memory");
+}
+
+template <int KIND> struct Slot {
+  static constexpr int bytes = KIND == MEP_BF16 ? 16 : KIND == MEP_F32 ? 32 : 8;  // per thread and block
+  // Address of the eight columns from c of row 0, and the bytes from row to row.
+  static __device__ __forceinline__ const char* at(const void* base, int c) {
+    return static_cast<const char*>(base) + (long long)c * (bytes / 8);
+  }
+  static __device__ __forceinline__ long long pitch(int H) {
+    return KIND == MEP_CKPT8 ? ckpt_row_bytes(H) : (long long)H * (bytes / 8);
+  }
+  static __device__ __forceinline__ void copy(uint32_t slot, int threads, const char* src) {
+    const int t = threadIdx.x;
+    if (KIND == MEP_CKPT8) {
+      copy_async8(slot + t * 8, src);
+    } else {
+      copy_async16(slot + t * 16, src);
+      if (KIND == MEP_F32) copy_async16(slot + (threads + t) * 16, src + 16);
+    }
+  }
+  static __device__ __forceinline__ void zero(uint32_t slot, int threads) {
+    const int t = threadIdx.x;
+    if (KIND == MEP_CKPT8) {
+      asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(slot + t * 8), "r"(0) : "memory");
+    } else {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot + t * 16), "r"(0) : "memory");
+      if (KIND == MEP_F32)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(slot + (threads + t) * 16), "r"(0)
+                     : "memory");
+    }
+  }
+  static __device__ __forceinline__ void fetch(uint32_t slot, int threads, Pack<KIND>& p) {
+    const int t = threadIdx.x;
+    if constexpr (KIND == MEP_CKPT8) {
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(p.w[0]), "=r"(p.w[1]) : "r"(slot + t * 8));
+    } else if constexpr (KIND == MEP_BF16) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3])
+                   : "r"(slot + t * 16));
+    } else {
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(p.v[0]), "=f"(p.v[1]), "=f"(p.v[2]), "=f"(p.v[3])
+                   : "r"(slot + t * 16));
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(p.v[4]), "=f"(p.v[5]), "=f"(p.v[6]), "=f"(p.v[7])
+                   : "r"(slot + (threads + t) * 16));
+    }
+  }
+};
+
+// MAXT is the number of threads of an SM: 512 with 128 registers each, in
+// CTAs of up to 512, or 1024 with 64 for the backward pass of rows of more than
+// 8192 columns.
+template <int KIND, int J, int U, int MAXT> __host__ __device__ constexpr int norm_ahead() {
+  return ahead_of(U * J * Slot<KIND>::bytes, 196608 / MAXT);
+}
+template <int KIND, int XKIND, int J, int U, int MAXT> __host__ __device__ constexpr int dx_ahead() {
+  return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / MAXT);
+}
+
+// J blocks a half warp, W warps a row (2 J W >= blocks of a row), U rows a turn.
+template <typename T, int KIND, bool VEC, int J, int U, int MAXT>
+__global__ void __launch_bounds__(MAXT)
+    k_norm(const T* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b, int p_type,
+           float eps, unsigned N, int H, int W, T* __restrict__ y, float* __restrict__ mean,
+           float* __restrict__ rstd, uint8_t* __restrict__ x_ckpt, uint8_t* __restrict__ y_ckpt) {
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int A = norm_ahead<KIND, J, U, MAXT>();
+  extern __shared__ __align__(16) float s_dyn[];  // slots
+  __shared__ float s_sum[4][kMaxWarps * 2];       // [mean and square, twice][two values a warp]
+  const int l = threadIdx.x % kHalf;
+  const int group = (threadIdx.x >> 5) / W, groups = blockDim.x / (32 * W);
+  const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
+  const int nb = (H + kCkptBlock - 1) / kCkptBlock, threads = blockDim.x;
+  const float inv_h = 1.f / H;
+  const unsigned first = (blockIdx.x * groups + group) * U, step = gridDim.x * groups * U;
+  const long long row_bytes = ckpt_row_bytes(H);
+  uint32_t slots = 0;
+  constexpr int turn_bytes = J * U * Slot<KIND>::bytes;  // a thread's, of all threads' turn
+  const char* src = nullptr;
+  long long src_step = 0;
+  bool there[J];
+#pragma unroll
+  for (int i = 0; i < J; ++i) there[i] = half_col<VEC>(half + 2 * W * i, l, 0) < H;
+  const auto ahead = [&](unsigned r, uint32_t slot) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (r + u < N) {
+        const char* row = src + u * Slot<KIND>::pitch(H);
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+          if (there[i])
+            Slot<KIND>::copy(slot + (u * J + i) * threads * Slot<KIND>::bytes, threads,
+                             row + 2 * W * i * 16 * Slot<KIND>::bytes);
+      }
+    src += src_step;
+    copy_async_commit();
+  };
+  if (VEC) {
+    slots = uint32_t(__cvta_generic_to_shared(s_dyn));
+    src = Slot<KIND>::at(x, half_col<true>(half, l, 0)) + first * Slot<KIND>::pitch(H);
+    src_step = step * Slot<KIND>::pitch(H);
+#pragma unroll
+    for (int i = 0; i < J; ++i)
+      if (!there[i])
+        for (int k = 0; k < A * U; ++k) Slot<KIND>::zero(slots + (k * J + i) * threads * Slot<KIND>::bytes, threads);
+    for (int k = 0; k < A; ++k) ahead(first + k * step, slots + k * turn_bytes * threads);
+  }
+  T* out = y + (long long)first * H;
+  uint8_t* xc = x_ckpt == nullptr ? nullptr : x_ckpt + first * row_bytes;
+  uint8_t* yc = y_ckpt == nullptr ? nullptr : y_ckpt + first * row_bytes;
+  int at = 0, turn = 0;  // slot, pair of sums
+  for (unsigned r = first; r < N; r += step, turn ^= 2) {
+    Pack<KIND> p[U][J];
+    if (VEC) {
+      const uint32_t slot = slots + at * turn_bytes * threads;
+      copy_async_wait<A - 1>();
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+          Slot<KIND>::fetch(slot + (u * J + i) * threads * Slot<KIND>::bytes, threads, p[u][i]);
+      ahead(r + A * step, slot);
+      at = at + 1 == A ? 0 : at + 1;
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+          if (r + u < N)
+            p[u][i].template load<false>(x, r + u, H, half + 2 * W * i, l);
+          else
+            p[u][i].clear();
+        }
+    }
+    float m[2] = {0.f, 0.f}, rs[2] = {0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      F2 sum = both(0.f);
+#pragma unroll
+      for (int i = 0; i < J; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = add2(sum, p[u][i].at(j));
+      m[u] = sum.x() + sum.y();
+    }
+    group_sums<2>(m, &s_sum[turn][group * W * 2], W, warp, group);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m[u] *= inv_h;
+      F2 sq = both(0.f);
+#pragma unroll
+      for (int i = 0; i < J; ++i) {
+        const int block = half + 2 * W * i;
+        if (!there[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          F2 c = add2(p[u][i].at(j), both(-m[u]));
+          if (!VEC)
+            c = pair(half_col<false>(block, l, 2 * j) < H ? c.x() : 0.f,
+                     half_col<false>(block, l, 2 * j + 1) < H ? c.y() : 0.f);
+          sq = fma2(c, c, sq);
+        }
+      }
+      rs[u] = sq.x() + sq.y();
+    }
+    group_sums<2>(rs, &s_sum[turn + 1][group * W * 2], W, warp, group);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rs[u] = 1.f / sqrtf(rs[u] * inv_h + eps);
+      if (threadIdx.x % (32 * W) == u && r + u < N) {
+        mean[r + u] = m[u];
+        rstd[r + u] = rs[u];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      const int block = half + 2 * W * i;
+      const bool in = block < nb;
+      F2 wv[4], bv[4];
+      load_params<VEC>(w, p_type, H, block, l, 1.f, wv);
+      load_params<VEC>(b, p_type, H, block, l, 0.f, bv);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (U > 1 && r + u >= N) continue;
+        F2 v[4];
+        if (x_ckpt != nullptr) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = p[u][i].at(j);
+          save8<VEC>(xc + u * row_bytes, H, block, l, in, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = fma2(mul2(add2(p[u][i].at(j), both(-m[u])), both(rs[u])), wv[j], bv[j]);
+          if (!VEC)
+            v[j] = pair(half_col<false>(block, l, 2 * j) < H ? v[j].x() : 0.f,
+                        half_col<false>(block, l, 2 * j + 1) < H ? v[j].y() : 0.f);
+          else if (!there[i])
+            v[j] = both(0.f);
+        }
+        store8<T, VEC>(out + (long long)u * H, H, block, l, v);
+        if (y_ckpt != nullptr) save8<VEC>(yc + u * row_bytes, H, block, l, in, v);
+      }
+    }
+    out += (long long)step * H;
+    if (x_ckpt != nullptr) xc += step * row_bytes;
+    if (y_ckpt != nullptr) yc += step * row_bytes;
+  }
+}
+
+template <typename T, int KIND, int XKIND, bool VEC, int J, int U, int MAXT>
+__global__ void __launch_bounds__(MAXT)
     k_norm_dx(const T* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ w,
-              int p_type, const float* __restrict__ mean, const float* __restrict__ rstd, long long N,
+              int p_type, const float* __restrict__ mean, const float* __restrict__ rstd, unsigned N,
               int H, int W, T* __restrict__ dx, float* __restrict__ ws) {
   pdl_wait();
   pdl_launch_dependents();
-  extern __shared__ float s_part[];                   // [groups][2][columns of a group]
+  constexpr int A = dx_ahead<KIND, XKIND, J, U, MAXT>();
+  extern __shared__ __align__(16) float s_dyn[];  // slots; at the end the groups' column sums
   __shared__ float s_sum[2][kMaxWarps * 2 * U];
   const int l = threadIdx.x % kHalf;
   const int group = (threadIdx.x >> 5) / W, groups = blockDim.x / (32 * W);
   const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
+  const int threads = blockDim.x;
   const float inv_h = 1.f / H;
-  float dw[J][8], db[J][8], wv[J][8];
+  F2 dw[J][4], db[J][4], wv[J][4];
+  bool there[J];
 #pragma unroll
   for (int i = 0; i < J; ++i) {
+    there[i] = half_col<VEC>(half + 2 * W * i, l, 0) < H;
     load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, wv[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = db[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = both(0.f);
   }
-  int turn = 0;
-  for (long long r0 = ((long long)blockIdx.x * groups + group) * U; r0 < N;
-       r0 += (long long)gridDim.x * groups * U, turn ^= 1) {
-    Pack<KIND> d[U][J];
-    Pack<XKIND> p[U][J];
-    float m[U], rs[U], sums[2 * U];
+  const unsigned first = (blockIdx.x * groups + group) * U, step = gridDim.x * groups * U;
+  constexpr int piece = Slot<KIND>::bytes + Slot<XKIND>::bytes;  // a thread's bytes of a block
+  const uint32_t slots = uint32_t(__cvta_generic_to_shared(s_dyn));
+  const char* dsrc = Slot<KIND>::at(dy, half_col<true>(half, l, 0)) + first * Slot<KIND>::pitch(H);
+  const char* xsrc = Slot<XKIND>::at(x, half_col<true>(half, l, 0)) + first * Slot<XKIND>::pitch(H);
+  const long long dstep = step * Slot<KIND>::pitch(H), xstep = step * Slot<XKIND>::pitch(H);
+  const auto ahead = [&](unsigned r, uint32_t slot) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool in = r0 + u < N;
+    for (int u = 0; u < U; ++u)
+      if (r + u < N) {
+        const char *drow = dsrc + u * Slot<KIND>::pitch(H), *xrow = xsrc + u * Slot<XKIND>::pitch(H);
 #pragma unroll
-      for (int i = 0; i < J; ++i) {
-        if (in) {
-          d[u][i].template load<VEC>(dy, r0 + u, H, half + 2 * W * i, l);
-          p[u][i].template load<VEC>(x, r0 + u, H, half + 2 * W * i, l);
-        } else {
-          d[u][i].clear();
-          p[u][i].clear();
-        }
+        for (int i = 0; i < J; ++i)
+          if (there[i]) {
+            const uint32_t s = slot + (u * J + i) * threads * piece;
+            Slot<KIND>::copy(s, threads, drow + 2 * W * i * 16 * Slot<KIND>::bytes);
+            Slot<XKIND>::copy(s + threads * Slot<KIND>::bytes, threads, xrow + 2 * W * i * 16 * Slot<XKIND>::bytes);
+          }
       }
-      m[u] = in ? __ldg(mean + r0 + u) : 0.f;
-      rs[u] = in ? __ldg(rstd + r0 + u) : 0.f;
-    }
+    dsrc += dstep;
+    xsrc += xstep;
+    copy_async_commit();
+  };
+  // what is one value a row, a turn ahead in registers
+  float m1[U], rs1[U];
+  int sb1[U][J];
+  const float *mp = mean + first, *rp = rstd + first;
+  const uint8_t* sp = static_cast<const uint8_t*>(x) + first * ckpt_row_bytes(H) + ckpt_scale_at(H) + half;
+  const auto scalars = [&](unsigned r) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float s1 = 0.f, s2 = 0.f;
+      const bool in = r + u < N;
+      m1[u] = in ? __ldg(mp + u) : 0.f;
+      rs1[u] = in ? __ldg(rp + u) : 0.f;
+      if (VEC && XKIND == MEP_CKPT8)
 #pragma unroll
-      for (int i = 0; i < J; ++i)
+        for (int i = 0; i < J; ++i)
+          sb1[u][i] = in && there[i] ? __ldg(sp + u * ckpt_row_bytes(H) + 2 * W * i) : 1;
+    }
+    mp += step;
+    rp += step;
+    if (VEC && XKIND == MEP_CKPT8) sp += step * ckpt_row_bytes(H);
+  };
+  if (VEC) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float g = d[u][i].get(j);
-          const float xhat = (p[u][i].get(j) - m[u]) * rs[u], t = g * wv[i][j];
-          s1 += t;
-          s2 = fmaf(t, xhat, s2);
-          dw[i][j] = fmaf(g, xhat, dw[i][j]);
-          db[i][j] += g;
+    for (int i = 0; i < J; ++i)
+      if (!there[i])
+        for (int k = 0; k < A * U; ++k) {
+          const uint32_t s = slots + (k * J + i) * threads * piece;
+          Slot<KIND>::zero(s, threads);
+          Slot<XKIND>::zero(s + threads * Slot<KIND>::bytes, threads);
         }
-      sums[u] = s1;
-      sums[U + u] = s2;
-    }
-    group_sums<U>(sums, &s_sum[turn][group * W * 2 * U], W, warp, group);
+    for (int k = 0; k < A; ++k) ahead(first + k * step, slots + k * U * J * threads * piece);
+  }
+  scalars(first);
+  T* out = dx + (long long)first * H;
+  int at = 0, turn = 0;  // slot, sums
+  for (unsigned r = first; r < N; r += step, turn ^= 1) {
+    const uint32_t slot = slots + at * U * J * threads * piece;
+    float m[U], rs[U], sums[2 * U];
+    int sb[U][J];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float c1 = sums[u] * inv_h, c2 = sums[U + u] * inv_h;
-      if (r0 + u < N) {
+      m[u] = m1[u];
+      rs[u] = rs1[u];
+#pragma unroll
+      for (int i = 0; i < J; ++i) sb[u][i] = sb1[u][i];
+    }
+    // both passes fetch a row's values anew (from the slots: two loads a vector)
+    const auto fetch = [&](int u, int i, Pack<KIND>& d, Pack<XKIND>& p) {
+      if (VEC) {
+        const uint32_t s = slot + (u * J + i) * threads * piece;
+        Slot<KIND>::fetch(s, threads, d);
+        Slot<XKIND>::fetch(s + threads * Slot<KIND>::bytes, threads, p);
+        if constexpr (XKIND == MEP_CKPT8) p.step = ckpt_step(sb[u][i]);
+      } else {
+        d.template load<false>(dy, r + u, H, half + 2 * W * i, l);
+        p.template load<false>(x, r + u, H, half + 2 * W * i, l);
+      }
+    };
+    if (VEC) copy_async_wait<A - 1>();
+    scalars(r + step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      F2 s1 = both(0.f), s2 = both(0.f);
+      if (U == 1 || r + u < N) {
+        const F2 k1 = both(rs[u]), k0 = both(-m[u] * rs[u]);
 #pragma unroll
         for (int i = 0; i < J; ++i) {
-          float v[8];
+          Pack<KIND> d;
+          Pack<XKIND> p;
+          fetch(u, i, d, p);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float xhat = (p[u][i].get(j) - m[u]) * rs[u];
-            v[j] = rs[u] * (fmaf(d[u][i].get(j), wv[i][j], -c1) - xhat * c2);
+          for (int j = 0; j < 4; ++j) {
+            const F2 g = d.at(j), xhat = fma2(p.at(j), k1, k0), t = mul2(g, wv[i][j]);
+            s1 = add2(s1, t);
+            s2 = fma2(t, xhat, s2);
+            dw[i][j] = fma2(g, xhat, dw[i][j]);
+            db[i][j] = add2(db[i][j], g);
           }
-          store8<T, VEC>(dx, r0 + u, H, half + 2 * W * i, l, v);
         }
       }
+      sums[u] = s1.x() + s1.y();
+      sums[U + u] = s2.x() + s2.y();
+    }
+    group_sums<2 * U>(sums, &s_sum[turn][group * W * 2 * U], W, warp, group);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (U == 1 || r + u < N) {
+        // rs (t - c1 - xhat c2), xhat = x rs - m rs
+        const F2 k1 = both(rs[u]), k0 = both(-m[u] * rs[u]);
+        const F2 a = both(-rs[u] * sums[u] * inv_h), c = both(-rs[u] * sums[U + u] * inv_h);
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+          Pack<KIND> d;
+          Pack<XKIND> p;
+          fetch(u, i, d, p);
+          F2 v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            v[j] = fma2(fma2(p.at(j), k1, k0), c, fma2(mul2(d.at(j), wv[i][j]), k1, a));
+          store8<T, VEC>(out + (long long)u * H, H, half + 2 * W * i, l, v);
+        }
+      }
+    }
+    out += (long long)step * H;
+    if (VEC) {
+      ahead(r + A * step, slot);
+      at = at + 1 == A ? 0 : at + 1;
     }
   }
   if (ws == nullptr) return;
   // join the groups' column sums: laid out by thread, then by value
-  const int tid = threadIdx.x - group * 32 * W, threads = 32 * W, cols = threads * 8 * J;
+  const int mine = 32 * W, tid = threadIdx.x - group * mine, cols = mine * 8 * J;
   if (groups > 1) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < J; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s_part[(2 * group) * cols + (8 * i + j) * threads + tid] = dw[i][j];
-        s_part[(2 * group + 1) * cols + (8 * i + j) * threads + tid] = db[i][j];
+      for (int j = 0; j < 4; ++j) {
+        float* a = s_dyn + (2 * group) * cols + (8 * i + 2 * j) * mine + tid;
+        a[0] = dw[i][j].x(), a[mine] = dw[i][j].y();
+        a[cols] = db[i][j].x(), a[cols + mine] = db[i][j].y();
       }
     __syncthreads();
     if (group != 0) return;
@@ -261,16 +495,17 @@ __global__ void __launch_bounds__(U == 4 ? 512 : 1024)
 #pragma unroll
       for (int i = 0; i < J; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dw[i][j] += s_part[(2 * g) * cols + (8 * i + j) * threads + tid];
-          db[i][j] += s_part[(2 * g + 1) * cols + (8 * i + j) * threads + tid];
+        for (int j = 0; j < 4; ++j) {
+          const float* a = s_dyn + (2 * g) * cols + (8 * i + 2 * j) * mine + tid;
+          dw[i][j] = add2(dw[i][j], pair(a[0], a[mine]));
+          db[i][j] = add2(db[i][j], pair(a[cols], a[cols + mine]));
         }
   }
-  float* out = ws + (long long)blockIdx.x * 2 * H;
+  float* part = ws + (long long)blockIdx.x * 2 * H;
 #pragma unroll
   for (int i = 0; i < J; ++i) {
-    store8<float, VEC>(out, 0, H, half + 2 * W * i, l, dw[i]);
-    store8<float, VEC>(out + H, 0, H, half + 2 * W * i, l, db[i]);
+    store8<float, VEC>(part, H, half + 2 * W * i, l, dw[i]);
+    store8<float, VEC>(part + H, H, half + 2 * W * i, l, db[i]);
   }
 }
 
@@ -307,65 +542,87 @@ int norm_check(int type, int64_t N, int64_t H, int p_type) {
 
 int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
-// How the backward pass lays a row out: J blocks a half warp, W warps a row,
-// U rows at a time, `groups` rows' worth of warps in a CTA.
+// The default limit of 48 KB holds for dynamic and static shared memory together.
+int allow_smem(const void* kernel, int bytes) {
+  return set_max_dynamic_smem(kernel, bytes > 44 * 1024 && bytes <= 48 * 1024 ? 48 * 1024 + 1 : bytes);
+}
+
+// How a row is laid out: J blocks a half warp, W warps a row, U rows a turn,
+// `groups` rows' worth of warps in a CTA.
 struct Shape {
-  int J, U, W, groups, parts;
+  int J, U, W, groups, threads, maxt, parts;
 };
-Shape backward_shape(long long N, int H, int type) {
+Shape shape_of(int H, int J, int U) {
   Shape s;
-  const int nb = ceil_div(H, kCkptBlock);
-  s.J = nb > 64 ? 2 : 1;
-  s.U = s.J == 2 ? 1 : (type == MEP_F32 ? 2 : 4);
-  if (nb > 32 && s.U > 2) s.U = 2;
-  s.W = ceil_div(nb, 2 * s.J);
-  s.groups = s.W >= 4 ? 1 : 8 / s.W;
-  const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups);
-  const int warps = s.W * s.groups, cap = 152 * (warps > 16 ? 1 : warps > 8 ? 2 : 4);
+  s.J = J;
+  s.U = U;
+  s.W = ceil_div(ceil_div(H, kCkptBlock), 2 * J);
+  s.groups = s.W >= 4 ? 1 : 4 / s.W;
+  s.threads = 32 * s.W * s.groups;
+  s.maxt = s.threads <= 512 ? 512 : 1024;
+  return s;
+}
+// Two rows a turn where a slot of 128 bytes a thread holds them: in bf16, up to
+// 512 threads a row. The number of CTAs must not depend on the device: the
+// workspace is sized by it.
+Shape backward_shape(long long N, int H, int type) {
+  const int J = H > 2 * kCkptBlock ? 2 : 1;
+  Shape s = shape_of(H, J, 1);
+  if (s.maxt <= 512 && type == MEP_BF16 && H % 8 == 0) s.U = 2;
+  const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups), cap = 152 * (s.maxt / s.threads);
   s.parts = want < cap ? want : cap;
   return s;
 }
 
-template <typename T, int KIND, bool VEC, int J>
-cudaError_t run_norm(const void* x, const void* w, const void* b, int p_type, float eps, long long N,
-                     int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
+template <typename T, int KIND, bool VEC, int J, int U, int MAXT>
+cudaError_t run_norm(const Shape& s, const void* x, const void* w, const void* b, int p_type, float eps,
+                     unsigned N, int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                      cudaStream_t st) {
-  const int W = ceil_div(ceil_div(H, kCkptBlock), 2 * J), groups = W >= 4 ? 1 : 4 / W;
-  const int want = ceil_div(N, groups), cap = sm_count() * (64 / (W * groups));
-  return launch_pdl(k_norm<T, KIND, VEC, J>, dim3(want < cap ? want : cap), dim3(32 * W * groups), 0, st,
-                    static_cast<const T*>(x), w, b, p_type, eps, N, H, W, static_cast<T*>(y), mean, rstd,
-                    xc, yc);
+  const int want = ceil_div(N, s.groups * U), cap = sm_count() * (MAXT / s.threads);
+  const int smem = VEC ? norm_ahead<KIND, J, U, MAXT>() * U * J * s.threads * Slot<KIND>::bytes : 0;
+  const auto kernel = k_norm<T, KIND, VEC, J, U, MAXT>;
+  if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
+  return launch_pdl(kernel, dim3(want < cap ? want : cap), dim3(s.threads), smem, st,
+                    static_cast<const T*>(x), w, b, p_type, eps, N, H, s.W, static_cast<T*>(y), mean,
+                    rstd, xc, yc);
 }
 
 template <typename T, int KIND, bool VEC>
-cudaError_t pick_norm(const void* x, const void* w, const void* b, int p_type, float eps, long long N,
+cudaError_t pick_norm(const void* x, const void* w, const void* b, int p_type, float eps, unsigned N,
                       int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                       cudaStream_t st) {
-  const auto run = H <= 2 * kCkptBlock   ? run_norm<T, KIND, VEC, 1>
-                   : H <= 4 * kCkptBlock ? run_norm<T, KIND, VEC, 2>
-                                         : run_norm<T, KIND, VEC, 4>;
-  return run(x, w, b, p_type, eps, N, H, y, mean, rstd, xc, yc, st);
+  constexpr int U = KIND == MEP_BF16 ? 2 : 1;
+  const int J = H <= 2 * kCkptBlock ? 1 : H <= 4 * kCkptBlock ? 2 : 4;
+  const Shape s = shape_of(H, J, U);
+  const auto run = J == 1   ? run_norm<T, KIND, VEC, 1, U, 512>
+                   : J == 2 ? run_norm<T, KIND, VEC, 2, U, 512>
+                            : run_norm<T, KIND, VEC, 4, U, 512>;
+  return run(s, x, w, b, p_type, eps, N, H, y, mean, rstd, xc, yc, st);
 }
 
-template <typename T, int KIND, int XKIND, bool VEC, int J, int U>
+template <typename T, int KIND, int XKIND, bool VEC, int J, int U, int MAXT>
 cudaError_t run_dx(const Shape& s, const void* dy, const void* x, const void* w, int p_type,
-                   const float* mean, const float* rstd, long long N, int H, void* dx, float* ws,
+                   const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                    cudaStream_t st) {
-  const int threads = 32 * s.W * s.groups;
-  const int smem = s.groups > 1 ? s.groups * 2 * 32 * s.W * 8 * J * 4 : 0;
-  const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U>;
-  if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
+  const int threads = s.threads;
+  const int slots = VEC ? dx_ahead<KIND, XKIND, J, U, MAXT>() * U * J * threads *
+                              (Slot<KIND>::bytes + Slot<XKIND>::bytes)
+                        : 0;
+  const int join = s.groups > 1 ? 2 * threads * 8 * J * 4 : 0, smem = slots > join ? slots : join;
+  const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U, MAXT>;
+  if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(s.parts), dim3(threads), smem, st, static_cast<const T*>(dy), x, w,
                     p_type, mean, rstd, N, H, s.W, static_cast<T*>(dx), ws);
 }
 
 template <typename T, int KIND, int XKIND, bool VEC>
 cudaError_t pick_dx(const Shape& s, const void* dy, const void* x, const void* w, int p_type,
-                    const float* mean, const float* rstd, long long N, int H, void* dx, float* ws,
+                    const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                     cudaStream_t st) {
-  const auto run = s.J == 2   ? run_dx<T, KIND, XKIND, VEC, 2, 1>
-                   : s.U == 2 ? run_dx<T, KIND, XKIND, VEC, 1, 2>
-                              : run_dx<T, KIND, XKIND, VEC, 1, 4>;
+  constexpr int U = KIND == MEP_BF16 && VEC ? 2 : 1;  // backward_shape's, up to 512 threads
+  const auto run = s.J == 1        ? run_dx<T, KIND, XKIND, VEC, 1, U, 512>
+                   : s.maxt == 512 ? run_dx<T, KIND, XKIND, VEC, 2, U, 512>
+                                   : run_dx<T, KIND, XKIND, VEC, 2, 1, 1024>;
   return run(s, dy, x, w, p_type, mean, rstd, N, H, dx, ws, st);
 }
 
