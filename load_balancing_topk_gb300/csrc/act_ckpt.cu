@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads)
     F2 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = p[u].at(j);
-    save8<VEC>(ckpt + w[u].row * ckpt_row_bytes(C), C, w[u].block, l, w[u].in, v);
+    save8<VEC>(ckpt + w[u].row * ckpt_row_bytes(C), C, w[u].block, l, w[u].in, p[u].top(), v);
   }
 }
 
@@ -125,8 +125,10 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (w[u].in) store8<__nv_bfloat16, VEC>(a + w[u].row * F, F, w[u].block, l, o);
     if (CKPT) {
-      save8<VEC>(ckpt + 2 * w[u].row * ckpt_row_bytes(F), F, w[u].block, l, w[u].in, v[0]);
-      save8<VEC>(ckpt + (2 * w[u].row + 1) * ckpt_row_bytes(F), F, w[u].block, l, w[u].in, v[1]);
+      save8<VEC>(ckpt + 2 * w[u].row * ckpt_row_bytes(F), F, w[u].block, l, w[u].in,
+                 p[u][0].top(), v[0]);
+      save8<VEC>(ckpt + (2 * w[u].row + 1) * ckpt_row_bytes(F), F, w[u].block, l, w[u].in,
+                 p[u][1].top(), v[1]);
     }
   }
 }

@@ -31,10 +31,11 @@ __host__ __device__ __forceinline__ long long ckpt_row_bytes(long long C) {
   return (((C + 15) & ~15LL) + (C + kCkptBlock - 1) / kCkptBlock + 31) & ~31LL;
 }
 
-// Scale byte of a block whose largest magnitude is `amax` (a NaN or an
-// infinity anywhere in the block must arrive here as one).
-__device__ __forceinline__ int ckpt_scale(float amax) {
-  const int e = int(__float_as_uint(amax) >> 23);  // biased exponent; 0 also for zero and subnormals
+// Scale byte of a block from the bits of its largest magnitude (as unsigned
+// integers, magnitudes compare as they do as numbers, with infinity and then
+// NaN above them all).
+__device__ __forceinline__ int ckpt_scale(uint32_t top) {
+  const int e = int(top >> 23);  // biased exponent; 0 also for zero and subnormals
   return e == 255 ? kCkptNan : max(e - 6, 1);
 }
 // 2^-k and 2^k of a scale byte s = k + 127, 1 <= s <= 248; 0 and NaN for 255.
@@ -49,13 +50,6 @@ __device__ __forceinline__ float ckpt_step(int s) {
 __device__ __forceinline__ float ckpt_byte(uint32_t w, int j) {
   return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + j));
 }
-// max that keeps a NaN (fmaxf drops it)
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T> __device__ __forceinline__ T from_f32(float v);
@@ -131,10 +125,28 @@ constexpr int kHalf = 16;
 template <bool VEC> __device__ __forceinline__ int half_col(int block, int l, int j) {
   return block * kCkptBlock + (VEC ? 8 * l + j : l + kHalf * j);
 }
-__device__ __forceinline__ float half_max_nan(float v) {
+// Bits of the largest magnitude of four words of two bf16, of four pairs of fp32.
+// (a maximum that keeps a NaN; on the packed words with integer instructions
+// the gated activation ran 4% slower)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t top_of(const F2 (&v)[4]) {
+  float t = 0.f;
 #pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) v = max_nan(v, __shfl_xor_sync(MEP_FULL_MASK, v, d));
-  return v;
+  for (int j = 0; j < 4; ++j) t = max_nan(t, max_nan(fabsf(v[j].x()), fabsf(v[j].y())));
+  return __float_as_uint(t);
+}
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[4]) {
+  const F2 v[4] = {widen(w[0]), widen(w[1]), widen(w[2]), widen(w[3])};
+  return top_of(v);
+}
+__device__ __forceinline__ uint32_t half_top(uint32_t t) {
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) t = max(t, __shfl_xor_sync(MEP_FULL_MASK, t, d));
+  return t;
 }
 
 // Eight values of a row as they lie in memory (columns beyond C are 0).
@@ -159,6 +171,7 @@ template <> struct Pack<MEP_BF16> {
   __device__ __forceinline__ F2 at(int j) const {  // values 2j and 2j + 1
     return widen(w[j]);
   }
+  __device__ __forceinline__ uint32_t top() const { return top_of(w); }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
 };
 template <> struct Pack<MEP_F32> {
@@ -182,6 +195,10 @@ template <> struct Pack<MEP_F32> {
     }
   }
   __device__ __forceinline__ F2 at(int j) const { return pair(v[2 * j], v[2 * j + 1]); }
+  __device__ __forceinline__ uint32_t top() const {
+    const F2 a[4] = {at(0), at(1), at(2), at(3)};
+    return top_of(a);
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -216,9 +233,10 @@ template <> struct Pack<MEP_CKPT8> {
   __device__ __forceinline__ void clear() { w[0] = w[1] = 0u, step = 0.f; }
 };
 
-// Four pairs of values into the row at p, rounded to its type; v becomes what was stored.
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int C, int block, int l, F2 (&v)[4]) {
+// Four pairs of values into the row at p, rounded to its type (FULL: the block
+// is known to lie within the row); v becomes what was stored. Returns the bits of its largest magnitude.
+template <typename T, bool VEC, bool FULL = false>
+__device__ __forceinline__ uint32_t store8(T* p, int C, int block, int l, F2 (&v)[4]) {
   if (sizeof(T) == 2) {
     uint32_t o[4];
 #pragma unroll
@@ -229,7 +247,7 @@ __device__ __forceinline__ void store8(T* p, int C, int block, int l, F2 (&v)[4]
     }
     if (VEC) {
       const int c = half_col<true>(block, l, 0);
-      if (c < C) *reinterpret_cast<uint4*>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (FULL || c < C) *reinterpret_cast<uint4*>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -237,10 +255,11 @@ __device__ __forceinline__ void store8(T* p, int C, int block, int l, F2 (&v)[4]
         if (c < C) reinterpret_cast<uint16_t*>(p)[c] = uint16_t(j & 1 ? o[j >> 1] >> 16 : o[j >> 1]);
       }
     }
+    return top_of(o);
   } else {
     if (VEC) {
       const int c = half_col<true>(block, l, 0);
-      if (c < C) {
+      if (FULL || c < C) {
         float4* q = reinterpret_cast<float4*>(p + c);
         q[0] = make_float4(v[0].x(), v[0].y(), v[1].x(), v[1].y());
         q[1] = make_float4(v[2].x(), v[2].y(), v[3].x(), v[3].y());
@@ -252,25 +271,25 @@ __device__ __forceinline__ void store8(T* p, int C, int block, int l, F2 (&v)[4]
         if (c < C) reinterpret_cast<float*>(p)[c] = j & 1 ? v[j >> 1].y() : v[j >> 1].x();
       }
     }
+    return top_of(v);
   }
 }
 
 // One block of the checkpoint row at p from its sixteen lanes' values, all lanes of
-// the warp together (`in`: this half warp has a block). The lanes of a row's
+// the warp together (`in`: this half warp has a block; `top`: the bits of this
+// lane's largest magnitude). The lanes of a row's
 // last block also write its padding.
-template <bool VEC>
-__device__ __forceinline__ void save8(uint8_t* p, int C, int block, int l, bool in, const F2 (&v)[4]) {
-  float top = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) top = max_nan(top, max_nan(fabsf(v[j].x()), fabsf(v[j].y())));
-  top = half_max_nan(top);
-  if (!in) return;
+template <bool VEC, bool FULL = false>
+__device__ __forceinline__ void save8(uint8_t* p, int C, int block, int l, bool in, uint32_t top,
+                                      const F2 (&v)[4]) {
+  top = half_top(top);
+  if (!FULL && !in) return;
   const int s = ckpt_scale(top);
   const float inv = ckpt_inv_step(s);
-  const uint2 q = ckpt_pack8(v, inv, top * inv >= 127.5f);
+  const uint2 q = ckpt_pack8(v, inv, __uint_as_float(top) * inv >= 127.5f);
   if (VEC) {
     const int c = half_col<true>(block, l, 0);
-    if (c < C) *reinterpret_cast<uint2*>(p + c) = q;
+    if (FULL || c < C) *reinterpret_cast<uint2*>(p + c) = q;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -12,9 +12,11 @@
 // (cp.async), so that the next rows' loads are under way while a row's sums
 // are, and no thread waits for another's copies. Registers alone (rows loaded
 // as they are used) held too few loads in flight: see the figures below.
-//   k_norm       the mean first, then the sum of the centred squares: with
-//                the row in registers the second pass costs no memory, and a
-//                row far from zero loses nothing to cancellation.
+//   k_norm       every warp takes the mean of its part of a row, then the
+//                squares around that mean; joined after one barrier, as
+//                var H = sum of the warps' squares + n_w (mean_w - mean)^2.
+//                All squares are of differences: a row far from zero loses
+//                nothing to cancellation.
 //   k_norm_dx    dx of U rows at a time; every thread also keeps the sums
 //                over its rows for its own columns of dweight and dbias, which
 //                the CTA's row groups join at the end and write to the
@@ -64,8 +66,7 @@ __device__ __forceinline__ void load_params(const void* p, int type, int H, int 
 // first share the values out among themselves (each step halves the values a
 // lane still carries): 6 or 7 shuffles a warp, not 10 or 20. s holds n words a
 // warp, not in use elsewhere before the group's next barrier but one.
-template <int n>
-__device__ __forceinline__ void group_sums(float (&v)[n], float* s, int W, int warp, int group) {
+template <int n> __device__ __forceinline__ float warp_sums(float (&v)[n]) {
   constexpr int lanes = 32 / n;  // that carry the same value in the end
   const int lane = threadIdx.x & 31;
   int d = 16;
@@ -81,7 +82,13 @@ __device__ __forceinline__ void group_sums(float (&v)[n], float* s, int W, int w
   float t = v[0];
 #pragma unroll
   for (int e = lanes / 2; e >= 1; e >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, e);
-  // the lane's bits 4, 3, ... say which value it has, high bit first
+  return t;  // of value lane / lanes: the lane's bits 4, 3, ... chose it, high bit first
+}
+template <int n>
+__device__ __forceinline__ void group_sums(float (&v)[n], float* s, int W, int warp, int group) {
+  constexpr int lanes = 32 / n;
+  const int lane = threadIdx.x & 31;
+  float t = warp_sums<n>(v);
   if (W > 1) {
     const int mine = lane / lanes, k0 = lane % lanes;
     if (k0 == 0) s[warp * n + mine] = t;
@@ -170,8 +177,9 @@ template <int KIND, int XKIND, int J, int U, int MAXT> __host__ __device__ const
   return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / MAXT);
 }
 
-// J blocks a half warp, W warps a row (2 J W >= blocks of a row), U rows a turn.
-template <typename T, int KIND, bool VEC, int J, int U, int MAXT>
+// J blocks a half warp, W warps a row (2 J W >= blocks of a row; FULL: equal,
+// and no block is cut), U rows a turn, KEEP: a checkpoint is written.
+template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U, int MAXT>
 __global__ void __launch_bounds__(MAXT)
     k_norm(const T* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b, int p_type,
            float eps, unsigned N, int H, int W, T* __restrict__ y, float* __restrict__ mean,
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(MAXT)
   pdl_launch_dependents();
   constexpr int A = norm_ahead<KIND, J, U, MAXT>();
   extern __shared__ __align__(16) float s_dyn[];  // slots
-  __shared__ float s_sum[4][kMaxWarps * 2];       // [mean and square, twice][two values a warp]
+  __shared__ float2 s_part[2][kMaxWarps * 2];     // two rows' mean and squares of a warp, twice
   const int l = threadIdx.x % kHalf;
   const int group = (threadIdx.x >> 5) / W, groups = blockDim.x / (32 * W);
   const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(MAXT)
   long long src_step = 0;
   bool there[J];
 #pragma unroll
-  for (int i = 0; i < J; ++i) there[i] = half_col<VEC>(half + 2 * W * i, l, 0) < H;
+  for (int i = 0; i < J; ++i) there[i] = FULL || half_col<VEC>(half + 2 * W * i, l, 0) < H;
   const auto ahead = [&](unsigned r, uint32_t slot) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -219,11 +227,29 @@ __global__ void __launch_bounds__(MAXT)
         for (int k = 0; k < A * U; ++k) Slot<KIND>::zero(slots + (k * J + i) * threads * Slot<KIND>::bytes, threads);
     for (int k = 0; k < A; ++k) ahead(first + k * step, slots + k * turn_bytes * threads);
   }
+  // columns of this warp, and of the warps whose parts this lane joins
+  const auto columns = [&](int k) {
+    int n = 0;
+    for (int i = 0; i < J; ++i) n += max(0, min(2 * kCkptBlock, H - (2 * k + 2 * W * i) * kCkptBlock));
+    return n;
+  };
+  const int k16 = threadIdx.x & 15;
+  const float inv_mine = 1.f / max(1, columns(warp));
+  const float n_a = k16 < W ? columns(k16) : 0, n_c = k16 + 16 < W ? columns(k16 + 16) : 0;
+  // up to two blocks a half warp the parameters stay in registers; loaded turn
+  // by turn they came from L2, the slots leave L1 little room
+  F2 wv[J > 2 ? 1 : J][4], bv[J > 2 ? 1 : J][4];
+  if (J <= 2) {
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, wv[J > 2 ? 0 : i]);
+      load_params<VEC>(b, p_type, H, half + 2 * W * i, l, 0.f, bv[J > 2 ? 0 : i]);
+    }
+  }
   T* out = y + (long long)first * H;
-  uint8_t* xc = x_ckpt == nullptr ? nullptr : x_ckpt + first * row_bytes;
-  uint8_t* yc = y_ckpt == nullptr ? nullptr : y_ckpt + first * row_bytes;
-  int at = 0, turn = 0;  // slot, pair of sums
-  for (unsigned r = first; r < N; r += step, turn ^= 2) {
+  uint8_t *xc = x_ckpt + first * row_bytes, *yc = y_ckpt + first * row_bytes;
+  int at = 0, turn = 0;  // slot, sums
+  for (unsigned r = first; r < N; r += step, turn ^= 1) {
     Pack<KIND> p[U][J];
     if (VEC) {
       const uint32_t slot = slots + at * turn_bytes * threads;
@@ -256,10 +282,11 @@ __global__ void __launch_bounds__(MAXT)
         for (int j = 0; j < 4; ++j) sum = add2(sum, p[u][i].at(j));
       m[u] = sum.x() + sum.y();
     }
-    group_sums<2>(m, &s_sum[turn][group * W * 2], W, warp, group);
+    // lane's row of the two is lane / 16 from here on
+    const float mw = warp_sums<2>(m) * inv_mine;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      m[u] *= inv_h;
+      m[u] = __shfl_sync(MEP_FULL_MASK, mw, 16 * u);
       F2 sq = both(0.f);
 #pragma unroll
       for (int i = 0; i < J; ++i) {
@@ -276,7 +303,28 @@ __global__ void __launch_bounds__(MAXT)
       }
       rs[u] = sq.x() + sq.y();
     }
-    group_sums<2>(rs, &s_sum[turn + 1][group * W * 2], W, warp, group);
+    float sq = warp_sums<2>(rs), mean_all = mw;
+    if (W > 1) {
+      float2* s = &s_part[turn][group * W * 2];
+      if ((threadIdx.x & 15) == 0) s[2 * warp + ((threadIdx.x >> 4) & 1)] = make_float2(mw, sq);
+      group_sync(group, 32 * W);
+      const int lane = threadIdx.x & 31, k = lane & 15;
+      const float2 none = make_float2(0.f, 0.f);
+      const float2 a = k < W ? s[2 * k + (lane >> 4)] : none, c = k + 16 < W ? s[2 * (k + 16) + (lane >> 4)] : none;
+      float t = fmaf(a.x, n_a, c.x * n_c);
+#pragma unroll
+      for (int e = 8; e >= 1; e >>= 1) t += __shfl_xor_sync(MEP_FULL_MASK, t, e);
+      mean_all = t * inv_h;
+      const float da = a.x - mean_all, dc = c.x - mean_all;
+      sq = (a.y + c.y) + fmaf(n_a * da, da, n_c * dc * dc);
+#pragma unroll
+      for (int e = 8; e >= 1; e >>= 1) sq += __shfl_xor_sync(MEP_FULL_MASK, sq, e);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      m[u] = __shfl_sync(MEP_FULL_MASK, mean_all, 16 * u);
+      rs[u] = __shfl_sync(MEP_FULL_MASK, sq, 16 * u);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rs[u] = 1.f / sqrtf(rs[u] * inv_h + eps);
@@ -288,35 +336,39 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
     for (int i = 0; i < J; ++i) {
       const int block = half + 2 * W * i;
-      const bool in = block < nb;
-      F2 wv[4], bv[4];
-      load_params<VEC>(w, p_type, H, block, l, 1.f, wv);
-      load_params<VEC>(b, p_type, H, block, l, 0.f, bv);
+      const bool in = FULL || block < nb;
+      if (J > 2) {
+        load_params<VEC>(w, p_type, H, block, l, 1.f, wv[0]);
+        load_params<VEC>(b, p_type, H, block, l, 0.f, bv[0]);
+      }
+      const F2(&wi)[4] = wv[J > 2 ? 0 : i], (&bi)[4] = bv[J > 2 ? 0 : i];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (U > 1 && r + u >= N) continue;
         F2 v[4];
-        if (x_ckpt != nullptr) {
+        if (KEEP && x_ckpt != nullptr) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[j] = p[u][i].at(j);
-          save8<VEC>(xc + u * row_bytes, H, block, l, in, v);
+          save8<VEC, FULL>(xc + u * row_bytes, H, block, l, in, p[u][i].top(), v);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[j] = fma2(mul2(add2(p[u][i].at(j), both(-m[u])), both(rs[u])), wv[j], bv[j]);
+          v[j] = fma2(mul2(add2(p[u][i].at(j), both(-m[u])), both(rs[u])), wi[j], bi[j]);
           if (!VEC)
             v[j] = pair(half_col<false>(block, l, 2 * j) < H ? v[j].x() : 0.f,
                         half_col<false>(block, l, 2 * j + 1) < H ? v[j].y() : 0.f);
           else if (!there[i])
             v[j] = both(0.f);
         }
-        store8<T, VEC>(out + (long long)u * H, H, block, l, v);
-        if (y_ckpt != nullptr) save8<VEC>(yc + u * row_bytes, H, block, l, in, v);
+        const uint32_t top = store8<T, VEC, FULL>(out + (long long)u * H, H, block, l, v);
+        if (KEEP && y_ckpt != nullptr) save8<VEC, FULL>(yc + u * row_bytes, H, block, l, in, top, v);
       }
     }
     out += (long long)step * H;
-    if (x_ckpt != nullptr) xc += step * row_bytes;
-    if (y_ckpt != nullptr) yc += step * row_bytes;
+    if (KEEP) {
+      xc += step * row_bytes;
+      yc += step * row_bytes;
+    }
   }
 }
 
@@ -430,7 +482,7 @@ __global__ void __launch_bounds__(MAXT)
     for (int u = 0; u < U; ++u) {
       F2 s1 = both(0.f), s2 = both(0.f);
       if (U == 1 || r + u < N) {
-        const F2 k1 = both(rs[u]), k0 = both(-m[u] * rs[u]);
+        const F2 k1 = both(rs[u]), k0 = both(-m[u]);
 #pragma unroll
         for (int i = 0; i < J; ++i) {
           Pack<KIND> d;
@@ -438,7 +490,8 @@ __global__ void __launch_bounds__(MAXT)
           fetch(u, i, d, p);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const F2 g = d.at(j), xhat = fma2(p.at(j), k1, k0), t = mul2(g, wv[i][j]);
+            // (x - mean) first: exact where the row is far from zero
+            const F2 g = d.at(j), xhat = mul2(add2(p.at(j), k0), k1), t = mul2(g, wv[i][j]);
             s1 = add2(s1, t);
             s2 = fma2(t, xhat, s2);
             dw[i][j] = fma2(g, xhat, dw[i][j]);
@@ -453,9 +506,9 @@ __global__ void __launch_bounds__(MAXT)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (U == 1 || r + u < N) {
-        // rs (t - c1 - xhat c2), xhat = x rs - m rs
-        const F2 k1 = both(rs[u]), k0 = both(-m[u] * rs[u]);
-        const F2 a = both(-rs[u] * sums[u] * inv_h), c = both(-rs[u] * sums[U + u] * inv_h);
+        // rs (t - c1 - xhat c2), with xhat rs = (x - m) rs^2
+        const F2 k1 = both(rs[u]), k0 = both(-m[u]);
+        const F2 a = both(-rs[u] * sums[u] * inv_h), c = both(-rs[u] * sums[U + u] * inv_h * rs[u]);
 #pragma unroll
         for (int i = 0; i < J; ++i) {
           Pack<KIND> d;
@@ -464,7 +517,7 @@ __global__ void __launch_bounds__(MAXT)
           F2 v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            v[j] = fma2(fma2(p.at(j), k1, k0), c, fma2(mul2(d.at(j), wv[i][j]), k1, a));
+            v[j] = fma2(add2(p.at(j), k0), c, fma2(mul2(d.at(j), wv[i][j]), k1, a));
           store8<T, VEC>(out + (long long)u * H, H, half + 2 * W * i, l, v);
         }
       }
@@ -552,12 +605,14 @@ int allow_smem(const void* kernel, int bytes) {
 struct Shape {
   int J, U, W, groups, threads, maxt, parts;
 };
-Shape shape_of(int H, int J, int U) {
+Shape shape_of(long long N, int H, int J, int U) {
   Shape s;
   s.J = J;
   s.U = U;
   s.W = ceil_div(ceil_div(H, kCkptBlock), 2 * J);
-  s.groups = s.W >= 4 ? 1 : 4 / s.W;
+  // as many rows as fit 512 threads, but rather a CTA for every SM
+  s.groups = s.W >= 16 ? 1 : 16 / s.W;
+  while (s.groups > 1 && N < 152ll * U * s.groups) s.groups /= 2;
   s.threads = 32 * s.W * s.groups;
   s.maxt = s.threads <= 512 ? 512 : 1024;
   return s;
@@ -567,20 +622,20 @@ Shape shape_of(int H, int J, int U) {
 // workspace is sized by it.
 Shape backward_shape(long long N, int H, int type) {
   const int J = H > 2 * kCkptBlock ? 2 : 1;
-  Shape s = shape_of(H, J, 1);
-  if (s.maxt <= 512 && type == MEP_BF16 && H % 8 == 0) s.U = 2;
+  const int U = type == MEP_BF16 && H % 8 == 0 && H <= 64 * kCkptBlock ? 2 : 1;
+  Shape s = shape_of(N, H, J, U);
   const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups), cap = 152 * (s.maxt / s.threads);
   s.parts = want < cap ? want : cap;
   return s;
 }
 
-template <typename T, int KIND, bool VEC, int J, int U, int MAXT>
+template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U, int MAXT>
 cudaError_t run_norm(const Shape& s, const void* x, const void* w, const void* b, int p_type, float eps,
                      unsigned N, int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                      cudaStream_t st) {
   const int want = ceil_div(N, s.groups * U), cap = sm_count() * (MAXT / s.threads);
   const int smem = VEC ? norm_ahead<KIND, J, U, MAXT>() * U * J * s.threads * Slot<KIND>::bytes : 0;
-  const auto kernel = k_norm<T, KIND, VEC, J, U, MAXT>;
+  const auto kernel = k_norm<T, KIND, VEC, FULL, KEEP, J, U, MAXT>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(want < cap ? want : cap), dim3(s.threads), smem, st,
                     static_cast<const T*>(x), w, b, p_type, eps, N, H, s.W, static_cast<T*>(y), mean,
@@ -592,11 +647,17 @@ cudaError_t pick_norm(const void* x, const void* w, const void* b, int p_type, f
                       int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                       cudaStream_t st) {
   constexpr int U = KIND == MEP_BF16 ? 2 : 1;
-  const int J = H <= 2 * kCkptBlock ? 1 : H <= 4 * kCkptBlock ? 2 : 4;
-  const Shape s = shape_of(H, J, U);
-  const auto run = J == 1   ? run_norm<T, KIND, VEC, 1, U, 512>
-                   : J == 2 ? run_norm<T, KIND, VEC, 2, U, 512>
-                            : run_norm<T, KIND, VEC, 4, U, 512>;
+  const int J = H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4;
+  const Shape s = shape_of(N, H, J, U);
+  // Without the edge and checkpoint tests the forward pass issues a fifth less
+  // ([32768, 2048] 61 -> 51 us, [65536, 7168] 404 -> 334 us); the backward
+  // pass, which waits for memory, ran the same either way.
+  const bool full = VEC && H == s.W * 2 * J * kCkptBlock, keep = xc != nullptr || yc != nullptr;
+  const auto run = J == 1   ? run_norm<T, KIND, VEC, false, true, 1, U, 512>
+                   : J == 4 ? run_norm<T, KIND, VEC, false, true, 4, U, 512>
+                   : full   ? (keep ? run_norm<T, KIND, VEC, VEC, true, 2, U, 512>
+                                    : run_norm<T, KIND, VEC, VEC, false, 2, U, 512>)
+                            : run_norm<T, KIND, VEC, false, true, 2, U, 512>;
   return run(s, x, w, b, p_type, eps, N, H, y, mean, rstd, xc, yc, st);
 }
 
@@ -620,9 +681,9 @@ cudaError_t pick_dx(const Shape& s, const void* dy, const void* x, const void* w
                     const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                     cudaStream_t st) {
   constexpr int U = KIND == MEP_BF16 && VEC ? 2 : 1;  // backward_shape's, up to 512 threads
-  const auto run = s.J == 1        ? run_dx<T, KIND, XKIND, VEC, 1, U, 512>
-                   : s.maxt == 512 ? run_dx<T, KIND, XKIND, VEC, 2, U, 512>
-                                   : run_dx<T, KIND, XKIND, VEC, 2, 1, 1024>;
+  const auto run = s.J == 1         ? run_dx<T, KIND, XKIND, VEC, 1, U, 512>
+                   : s.maxt == 1024 ? run_dx<T, KIND, XKIND, VEC, 2, 1, 1024>
+                                    : run_dx<T, KIND, XKIND, VEC, 2, U, 512>;
   return run(s, dy, x, w, p_type, mean, rstd, N, H, dx, ws, st);
 }
 
