@@ -79,31 +79,36 @@ struct Smem {
   int count;
 };
 
-// wait_phase without a call: the converter and epilogue warps hold their
-// sums in registers across it. All lanes of the warp get the same answer.
-template <bool HONOR>
-__device__ __forceinline__ bool wait_inline(uint32_t bar, uint32_t parity, volatile int* abort,
-                                            int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u) {
-      if (HONOR && *abort) return false;
-      const uint64_t now = globaltimer();
-      if (t0 == 0) {
-        t0 = now;
-      } else if (now - t0 > MEP_GEMM_TIMEOUT_NS) {
-        *abort = 1;
-        set_status(status, MEP_ERR_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
+// wait_phase for a whole warp, without a call (the roles hold their state in
+// registers across it), with long tries and the same answer for all lanes.
+template <bool HONOR = true>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                           int32_t* status) {
-  return __all_sync(MEP_FULL_MASK, wait_inline<true>(bar, parity, abort, status));
+  bool ok = mbar_try_wait_long(bar, parity);
+  uint64_t t0 = 0;
+  while (!ok) {
+#pragma unroll 1
+    for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait_long(bar, parity);
+    if (ok || (HONOR && *abort)) break;
+    const uint64_t now = globaltimer();
+    if (t0 == 0) {
+      t0 = now;
+    } else if (now - t0 > MEP_GEMM_TIMEOUT_NS) {
+      *abort = 1;
+      set_status(status, MEP_ERR_TIMEOUT);
+      break;
+    }
+  }
+  return __all_sync(MEP_FULL_MASK, ok);
+}
+// Lane 0's value: the same for the warp, and known to be.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(MEP_FULL_MASK, v, 0); }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -254,27 +259,33 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 }
 
 // The units of one CTA pair, in the order in which every role of both CTAs
-// walks them. The next unit's entry is loaded while f works on this one's;
+// walks them (whole warps: what steers the loops is the same for all lanes,
+// and known to be, so that addresses and descriptors stay in uniform
+// registers). The next unit's entry is loaded while f works on this one's;
 // f(entry, tile) returns false to stop.
 struct Entry {
   int4 e;       // {weight row, first segment, segments, steps}
   int row, len; // the first segment
 };
 __device__ __forceinline__ Entry load_entry(const int4* __restrict__ entries, int i) {
-  const int4 b = entries[2 * i + 1];
-  return {entries[2 * i], b.x, b.y};
+  const int4 a = entries[2 * i], b = entries[2 * i + 1];
+  return {a, b.x, b.y};
+}
+__device__ __forceinline__ Entry uniform(const Entry& e) {
+  return {make_int4(uniform(e.e.x), uniform(e.e.y), uniform(e.e.z), uniform(e.e.w)), uniform(e.row),
+          uniform(e.len)};
 }
 template <typename F>
 __device__ __forceinline__ void for_units(const int4* __restrict__ entries, int count, int tiles, F f) {
   const int step = gridDim.x / 2;
   int i = (blockIdx.x / 2) / tiles, tile = (blockIdx.x / 2) % tiles;
   if (i >= count) return;
-  Entry cur = load_entry(entries, i), next = cur;
+  Entry cur = uniform(load_entry(entries, i)), next = cur;
   for (;;) {
     const int t = tile + step, ni = i + t / tiles;
     if (ni < count) next = load_entry(entries, ni);
     if (!f(cur, tile) || ni >= count) return;
-    cur = next;
+    cur = uniform(next);
     i = ni;
     tile = t % tiles;
   }
@@ -286,8 +297,8 @@ __device__ __forceinline__ bool for_steps(const Entry& en, const int2* __restric
   for (int g = 0; g < en.e.z; ++g) {
     if (g > 0) {
       const int2 seg = segs[en.e.y + g];
-      row = seg.x;
-      len = seg.y;
+      row = uniform(seg.x);
+      len = uniform(seg.y);
     }
     for (int k = 0; k < len; k += kBK)
       if (!f(row + k, len - k)) return false;
@@ -322,8 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem* S = reinterpret_cast<Smem*>(gen_base + kSt * kStage + kEpiWarps * kStoreBox);
   volatile int* abort_flag = &S->abort;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = int(cluster_rank());
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int rank = uniform(int(cluster_rank()));
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSt; ++s) {
@@ -353,29 +364,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = S->tmem;
+  const uint32_t tmem = uniform(S->tmem);
   const int nM = (H + 2 * kBM - 1) / (2 * kBM), nN = (Hp + kBN - 1) / kBN;
-  const int tiles = nM * nN, count = S->count;
+  const int tiles = nM * nN, count = uniform(S->count);
 
   // the four warpgroups' registers: 56 + 72 + 192 + 192 = 4 x 128 at launch
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
-      if (lane == 0) {
-        // ---------------- TMA producer ----------------
-        Pos at;
-        uint32_t issued = 0;
-        for_units(entries, count, tiles, [&](const Entry& en, int t) {
-          const int h0 = t / nN * 2 * kBM + rank * kBM, n0 = t % nN * kBN;
-          const bool narrow = Hp - n0 <= 128;
-          const int c0 = n0 + rank * (narrow ? 64 : 128);
-          const int na = h0 >= H ? 0 : h0 + 64 < H ? 2 : 1;
-          const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
-          const uint32_t bytes = (CKPT ? (na > 0 ? kQ + kScale : 0) : na * kBox) + nb * kBox;
-          const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
-          return for_steps(en, segs, [&](int row, int) {
-            if (!wait_phase(smem_u32(&S->empty[at.s]), at.parity ^ 1u, abort_flag, status)) return false;
-            const uint32_t bar = smem_u32(&S->full[at.s]), st = base + at.s * kStage;
+      // ---------------- TMA producer ----------------
+      Pos at;
+      uint32_t issued = 0;
+      for_units(entries, count, tiles, [&](const Entry& en, int t) {
+        const int h0 = t / nN * 2 * kBM + rank * kBM, n0 = t % nN * kBN;
+        const bool narrow = Hp - n0 <= 128;
+        const int c0 = n0 + rank * (narrow ? 64 : 128);
+        const int na = h0 >= H ? 0 : h0 + 64 < H ? 2 : 1;
+        const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
+        const uint32_t bytes = (CKPT ? (na > 0 ? kQ + kScale : 0) : na * kBox) + nb * kBox;
+        const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
+        return for_steps(en, segs, [&](int row, int) {
+          if (!warp_wait(smem_u32(&S->empty[at.s]), at.parity ^ 1u, abort_flag, status)) return false;
+          const uint32_t bar = smem_u32(&S->full[at.s]), st = base + at.s * kStage;
+          if (elected()) {
             mbar_expect_tx(bar, bytes);
             if (CKPT) {
               if (na > 0) {
@@ -388,34 +399,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (nb > 0) tma_load_2d(st + kOp, &map_dy, c0, row, bar);
             if (nb > 1) tma_load_2d(st + kOp + kBox, &map_dy, c0 + 64, row, bar);
-            at.template next<kSt>();
-            ++issued;
-            return true;
-          });
+          }
+          __syncwarp();
+          at.template next<kSt>();
+          ++issued;
+          return true;
         });
-        // this CTA's copies have landed, and every commit aimed at it has arrived
-        for (uint32_t j = issued > kSt ? issued - kSt : 0; j < issued; ++j) {
-          wait_phase(smem_u32(&S->full[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
-          wait_phase(smem_u32(&S->empty[j % kSt]), (j / kSt) & 1u, abort_flag, status, false);
-        }
+      });
+      // this CTA's copies have landed, and every commit aimed at it has arrived
+      for (uint32_t j = issued > kSt ? issued - kSt : 0; j < issued; ++j) {
+        warp_wait<false>(smem_u32(&S->full[j % kSt]), (j / kSt) & 1u, abort_flag, status);
+        warp_wait<false>(smem_u32(&S->empty[j % kSt]), (j / kSt) & 1u, abort_flag, status);
       }
-      __syncwarp();
-    } else if (warp == 1) {
-      if (lane == 0 && leader) {
-        // ---------------- MMA issuer (CTA 0 only) ----------------
-        Pos at, acc;  // stage; accumulator
-        const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + kOp, kBox, 1024);
-        for_units(entries, count, tiles, [&](const Entry& en, int t) {
-          const uint32_t idesc = Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc;
-          int steps = en.e.w, in_chunk = 0;
-          return for_steps(en, segs, [&](int, int left) {
-            if (in_chunk == 0 &&
-                !wait_phase(smem_u32(&S->tempty[acc.s]), acc.parity ^ 1u, abort_flag, status))
-              return false;
-            if (!wait_phase(smem_u32(&S->ready[at.s]), at.parity, abort_flag, status)) return false;
-            tc_fence_after();
-            const uint32_t d = tmem + acc.s * kBN;
-            const uint64_t ad = adesc + (at.s * kStage >> 4), bd = bdesc + (at.s * kStage >> 4);
+    } else if (warp == 1 && leader) {
+      // ---------------- MMA issuer (CTA 0 only) ----------------
+      Pos at, acc;  // stage; accumulator
+      const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + kOp, kBox, 1024);
+      for_units(entries, count, tiles, [&](const Entry& en, int t) {
+        const uint32_t idesc = Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc;
+        int steps = en.e.w, in_chunk = 0;
+        return for_steps(en, segs, [&](int, int left) {
+          if (in_chunk == 0 &&
+              !warp_wait(smem_u32(&S->tempty[acc.s]), acc.parity ^ 1u, abort_flag, status))
+            return false;
+          if (!warp_wait(smem_u32(&S->ready[at.s]), at.parity, abort_flag, status)) return false;
+          tc_fence_after();
+          const uint32_t d = tmem + acc.s * kBN;
+          const uint64_t ad = adesc + (at.s * kStage >> 4), bd = bdesc + (at.s * kStage >> 4);
+          const bool last = in_chunk == kChunk - 1 || steps == 1;
+          if (elected()) {
             if (left > kBK - 16) {
 #pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk)
@@ -425,20 +437,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_mma2(d, ad + kk * 128, bd + kk * 128, uint32_t(kk + in_chunk), idesc);
             }
             tc_commit2_mc(smem_u32(&S->empty[at.s]), 3);
-            at.template next<kSt>();
-            --steps;
-            if (++in_chunk == kChunk || steps == 0) {
-              tc_commit2_mc(smem_u32(&S->tfull[acc.s]), 3);
-              acc.template next<2>();
-              in_chunk = 0;
-            }
-            return true;
-          });
+            if (last) tc_commit2_mc(smem_u32(&S->tfull[acc.s]), 3);
+          }
+          __syncwarp();
+          at.template next<kSt>();
+          --steps;
+          ++in_chunk;
+          if (last) {
+            acc.template next<2>();
+            in_chunk = 0;
+          }
+          return true;
         });
-        tc_commit2(smem_u32(&S->drain));
-        wait_phase(smem_u32(&S->drain), 0u, abort_flag, status, false);
-      }
+      });
+      if (elected()) tc_commit2(smem_u32(&S->drain));
       __syncwarp();
+      warp_wait<false>(smem_u32(&S->drain), 0u, abort_flag, status);
     }
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
