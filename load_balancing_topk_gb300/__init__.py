@@ -172,10 +172,16 @@ def grouped_gemm_workspace_bytes(R: int, S: int, K: int, E: int, B: int) -> int:
 
 
 # ---------------------------------------------------------------------------
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _need(t, name, dtype, shape=None, device=None):
@@ -468,7 +474,7 @@ def mep_grouped_gemm(x, cu_seqlens, w_home, w_slot, status, R: int, S: int, K: i
 # (_need) only when something is; sizes that the library computes are kept.
 def _good(t, name, dtype, shape, dev):
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == dev:
             return t
     except AttributeError:
         pass
@@ -547,15 +553,19 @@ def _matrix(t, name) -> int:
 
 def _need_params(weight, bias, H, dev) -> int:
     """Checks a norm's weight and bias (each may be None); their type."""
-    kind = None
-    for name, p in (("weight", weight), ("bias", bias)):
-        if p is not None:
-            t = _float_type(p, name)
-            _good(p, name, p.dtype, (H,), dev)
-            if kind is not None and t != kind:
+    if weight is not None:
+        kind = _float_type(weight, "weight")
+        _good(weight, "weight", weight.dtype, (H,), dev)
+        if bias is not None:
+            if _float_type(bias, "bias") != kind:
                 raise TypeError("weight and bias must have the same dtype")
-            kind = t
-    return _F32 if kind is None else kind
+            _good(bias, "bias", bias.dtype, (H,), dev)
+        return kind
+    if bias is not None:
+        kind = _float_type(bias, "bias")
+        _good(bias, "bias", bias.dtype, (H,), dev)
+        return kind
+    return _F32
 
 
 def mep_ckpt_save(x, ckpt=None):
@@ -612,9 +622,10 @@ def mep_layer_norm(x, weight=None, bias=None, eps: float = 1e-5, y=None, mean=No
     f32 = torch.float32
     mean = torch.empty(N, dtype=f32, device=dev) if mean is None else _good(mean, "mean", f32, (N,), dev)
     rstd = torch.empty(N, dtype=f32, device=dev) if rstd is None else _good(rstd, "rstd", f32, (N,), dev)
-    for name, t in (("x_ckpt", x_ckpt), ("y_ckpt", y_ckpt)):
-        if t is not None:
-            _good(t, name, torch.uint8, (N, ckpt_row_bytes(H)), dev)
+    if x_ckpt is not None:
+        _good(x_ckpt, "x_ckpt", torch.uint8, (N, ckpt_row_bytes(H)), dev)
+    if y_ckpt is not None:
+        _good(y_ckpt, "y_ckpt", torch.uint8, (N, ckpt_row_bytes(H)), dev)
     _call("mep_layer_norm", dev, x.data_ptr(), kind, _ptr(weight), _ptr(bias), p_kind, eps, N, H,
           y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(x_ckpt), _ptr(y_ckpt))
     return y, mean, rstd
