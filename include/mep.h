@@ -482,14 +482,16 @@ MEP_API int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_type,
  *              expert), and so are the slots that have rows; slots without
  *              rows are left alone. Not 0: added to what is there.
  *   ws         device workspace of at least mep_grouped_wgrad_workspace_bytes
- *              (rebuilt by every call)
+ *              (the list of groups, and up to 80 MB of partial sums of groups
+ *              that are long next to the others; rebuilt by every call)
  *   home_grad  fp32 [E, H, H']      output
  *   slot_grad  fp32 [R, B, H, H']   output; may be NULL when B == 0
  * Outputs must not overlap the inputs.
  * Host returns: as mep_grouped_gemm (x, dy and the gradients must be device
  * memory of the current device).
  */
-MEP_API int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int B, size_t* bytes);
+MEP_API int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int B, int H, int Hp,
+                                              size_t* bytes);
 MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
                               const int32_t* cu_seqlens, int32_t* status, int R, int S, int K, int E,
                               int B, int H, int Hp, int accumulate, void* ws, size_t ws_bytes,

@@ -98,7 +98,7 @@ SIGNATURES = [
                                      _VP, _VP, _I, _VP]),
     ("mep_swiglu", _I, [_VP, _L, _L, _VP, _VP, _VP]),
     ("mep_swiglu_backward", _I, [_VP, _VP, _I, _L, _L, _VP, _VP, _VP]),
-    ("mep_grouped_wgrad_workspace_bytes", _I, [_I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_grouped_wgrad_workspace_bytes", _I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     ("mep_grouped_wgrad", _I, [_VP, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
                                _VP, _VP, _VP]),
     ("mep_wait_selftest", _I, [_VP, ctypes.c_int64, _VP, _VP]),
@@ -520,10 +520,10 @@ def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def grouped_wgrad_workspace_bytes(R: int, S: int, K: int, E: int, B: int) -> int:
+def grouped_wgrad_workspace_bytes(R: int, S: int, K: int, E: int, B: int, H: int, Hp: int) -> int:
     out = ctypes.c_size_t(0)
     _check("mep_grouped_wgrad_workspace_bytes",
-           load_library().mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, ctypes.byref(out)))
+           load_library().mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, H, Hp, ctypes.byref(out)))
     return int(out.value)
 
 
@@ -763,7 +763,7 @@ def mep_grouped_wgrad(x, dy, cu_seqlens, home_grad, slot_grad, status, R: int, S
         _good(slot_grad, "slot_grad", torch.float32, (R, B, H, Hp), dev)
     if status is not None:
         _good(status, "status", torch.int32, (1,), dev)
-    need = grouped_wgrad_workspace_bytes(R, S, K, E, B)
+    need = grouped_wgrad_workspace_bytes(R, S, K, E, B, H, Hp)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:

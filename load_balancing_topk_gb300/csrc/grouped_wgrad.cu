@@ -15,10 +15,11 @@
 // Two launches on the caller's stream:
 //   k_wgrad_groups  (1 CTA) checks every cu_seqlens row and lists the weight
 //                   rows that have to be written, each with its row segments
-//                   (one per rank that has rows of it);
+//                   (one per rank that has rows of it), cut into parts where
+//                   a group is long next to all the work, the longest first;
 //   k_wgrad_pair    persistent clusters of two CTAs, one per SM, 512 threads
-//                   each, over units (weight row, 256 rows of H, 256 columns
-//                   of H'), grid-stride. CTA r of a pair owns 128 of the 256
+//                   each, over units (part of a weight row's group, 256 rows
+//                   of H, 256 columns of H'), to and fro over the pairs. CTA r of a pair owns 128 of the 256
 //                   rows of H. Per step of 64 buffer rows:
 //     warp 0      TMA producer: this CTA's 128 columns of x (bf16 boxes, or
 //                 the checkpoint's bytes and their 64 scale bytes) and its
@@ -64,6 +65,11 @@ constexpr int kGroupThreads = 1024;
 constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
 constexpr int kEpiWarps = 8;
 constexpr int kPair = 2;
+constexpr int kPairs = 76;       // a fixed number, so that the parts do not depend on the device
+constexpr int kLeastSteps = 8;
+constexpr int kMostParts = 8;
+constexpr int kMostPartials = 4 * kPairs;  // parts * tiles of all entries with several parts: see partials_of
+constexpr int kTile = 2 * kBM * kBN;       // fp32 values of a partial sum
 
 template <bool CKPT> struct Ring {
   static constexpr int stage = 2 * kOp + (CKPT ? kQ + kScale : 0);
@@ -159,21 +165,33 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 
 // ---------------------------------------------------------------------------
 // The weight rows to write, weight row < E a home expert and E + r*B + b slot
-// b of rank r: entries[2i] = {weight row, first segment, segments, steps},
-// entries[2i + 1] = {first segment's first buffer row, its rows, 0, 0};
+// b of rank r: entries[i] = {weight row, first segment, segments, steps};
 // segs[j] = {first buffer row, rows}. Without `accumulate` a home expert is
 // listed even without rows (it is written as zero), a slot never is.
+//
+// Their parts: parts[2i] = {weight row, first segment, 0, steps}, parts[2i + 1] =
+// {first buffer row, rows from there to the segment's end, parts of this entry
+// + 256 * number of this one, index of the entry's first partial sum}. A part
+// is at most half of what a pair has to do in all, so that few, uneven groups
+// still fill the pairs; a group has at most kMostParts (the last of them adds
+// the partial sums of all up), and a part at least kLeastSteps. The longest
+// come first. With more weight rows than threads the list stays as it is: that
+// many fill the pairs.
+__device__ __forceinline__ int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
+
 __global__ void __launch_bounds__(kGroupThreads)
-    k_wgrad_groups(const int32_t* __restrict__ cu, int R, int E, int B, int SK, int accumulate,
-                   int32_t* status, int* __restrict__ count, int4* __restrict__ entries,
-                   int2* __restrict__ segs) {
+    k_wgrad_groups(const int32_t* __restrict__ cu, int R, int E, int B, int SK, int tiles, int accumulate,
+                   int32_t* status, int* __restrict__ count, int4* __restrict__ parts,
+                   int4* __restrict__ entries, int2* __restrict__ segs, int* __restrict__ arrived) {
   pdl_wait();
   pdl_launch_dependents();
   __shared__ int s_warp[33], s_entry[kGroupThreads + 1], s_seg[kGroupThreads + 1];
-  __shared__ int s_bad, s_entries, s_segs, s_stat;
+  __shared__ int s_bad, s_entries, s_segs, s_stat, s_partials;
+  __shared__ unsigned long long s_steps;
   const int G = E + B;
   if (threadIdx.x == 0) {
-    s_bad = s_entries = s_segs = 0;
+    s_bad = s_entries = s_segs = s_partials = 0;
+    s_steps = 0;
     s_stat = read_status(status);
   }
   __syncthreads();
@@ -204,27 +222,22 @@ __global__ void __launch_bounds__(kGroupThreads)
       const long long p = (long long)r * G + j;
       const int len = cu[p] - (j == 0 ? 0 : cu[p - 1]);
       nseg += len > 0;
-      steps += (len + kBK - 1) / kBK;
+      steps += ceil_div(len, kBK);
     }
     const bool listed = w < W && (nseg > 0 || (home && !accumulate));
     s_entry[threadIdx.x] = listed;
     s_seg[threadIdx.x] = nseg;
+    if (steps > 0) atomicAdd(&s_steps, (unsigned long long)steps);
     __syncthreads();
     block_excl_scan(s_entry, s_entry, blockDim.x, s_warp, true);
     block_excl_scan(s_seg, s_seg, blockDim.x, s_warp, true);
     if (listed) {
       int at = s_segs + s_seg[threadIdx.x];
-      int4* entry = entries + 2 * (s_entries + s_entry[threadIdx.x]);
-      entry[0] = make_int4(w, at, nseg, steps);
-      entry[1] = make_int4(0, 0, 0, 0);
+      entries[s_entries + s_entry[threadIdx.x]] = make_int4(w, at, nseg, steps);
       for (int r = r0; r < r1; ++r) {
         const long long p = (long long)r * G + j;
         const int lo = j == 0 ? 0 : cu[p - 1], len = cu[p] - lo;
-        if (len > 0) {
-          const int row = int((long long)r * SK + lo);
-          if (entry[1].y == 0) entry[1] = make_int4(row, len, 0, 0);
-          segs[at++] = make_int2(row, len);
-        }
+        if (len > 0) segs[at++] = make_int2(int((long long)r * SK + lo), len);
       }
     }
     __syncthreads();
@@ -234,7 +247,60 @@ __global__ void __launch_bounds__(kGroupThreads)
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) *count = s_entries;
+  // this CTA's own global writes are read again below
+  __threadfence_block();
+  const int n = s_entries;
+  const bool sorted = n <= int(blockDim.x);
+  const int most = max(kLeastSteps, ceil_div((long long)s_steps * tiles, 2 * kPairs));
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int4 e = entries[i];
+    const int len = sorted && e.w > most ? max(ceil_div(e.w, kMostParts), ceil_div(e.w, ceil_div(e.w, most))) : e.w;
+    if (sorted) {
+      s_entry[i] = len;                                // steps of a part
+      s_seg[i] = e.w > 0 ? ceil_div(e.w, len) : 1;     // parts
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int4 e = entries[i];
+    const int len = sorted ? s_entry[i] : e.w, np = sorted ? s_seg[i] : 1;
+    int pos = i, partial = 0;
+    if (sorted) {
+      pos = 0;
+      for (int j = 0; j < n; ++j) {
+        if (s_entry[j] > len || (s_entry[j] == len && j < i)) pos += s_seg[j];
+        if (j < i && s_seg[j] > 1) partial += s_seg[j];
+      }
+      if (i == n - 1) s_partials = partial + (np > 1 ? np : 0);
+    }
+    int g = e.y, done = 0;  // segment, its steps that are behind
+    for (int k = 0; k < np; ++k) {
+      int2 seg = e.z > 0 ? segs[g] : make_int2(0, 0);
+      const int steps = min(len, e.w - k * len);
+      parts[2 * (pos + k)] = make_int4(e.x, g, 0, steps);
+      parts[2 * (pos + k) + 1] = make_int4(seg.x + done * kBK, seg.y - done * kBK, np + 256 * k, partial);
+      for (int left = k + 1 < np ? steps : 0; left > 0;) {  // on to the next part's first step
+        const int here = ceil_div(seg.y, kBK) - done;
+        if (left < here) {
+          done += left;
+          left = 0;
+        } else {
+          left -= here;
+          done = 0;
+          ++g;
+          if (left > 0) seg = segs[g];
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int total = n;
+    if (sorted)
+      for (int i = 0; i < n; ++i) total += s_seg[i] - 1;
+    *count = total;
+  }
+  for (int i = threadIdx.x; i < s_partials * tiles * 2 * kEpiWarps; i += blockDim.x) arrived[i] = 0;
 }
 
 // Two signed bytes of w (chosen by sel) times a power of two, as two bf16.
@@ -261,47 +327,51 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, ui
 // The units of one CTA pair, in the order in which every role of both CTAs
 // walks them (whole warps: what steers the loops is the same for all lanes,
 // and known to be, so that addresses and descriptors stay in uniform
-// registers). The next unit's entry is loaded while f works on this one's;
-// f(entry, tile) returns false to stop.
-struct Entry {
-  int4 e;       // {weight row, first segment, segments, steps}
-  int row, len; // the first segment
+// registers): round by round over the pairs, to and fro, since the list goes
+// from long to short. The next unit's part is loaded while f works on this
+// one's; f(part, tile) returns false to stop.
+struct Part {
+  int w, seg, steps;  // weight row, first segment
+  int row, len;       // first row, rows to the segment's end
+  int of, partial;
 };
-__device__ __forceinline__ Entry load_entry(const int4* __restrict__ entries, int i) {
-  const int4 a = entries[2 * i], b = entries[2 * i + 1];
-  return {a, b.x, b.y};
+__device__ __forceinline__ Part load_part(const int4* __restrict__ parts, int i) {
+  const int4 a = parts[2 * i], b = parts[2 * i + 1];
+  return {a.x, a.y, a.w, b.x, b.y, b.z, b.w};
 }
-__device__ __forceinline__ Entry uniform(const Entry& e) {
-  return {make_int4(uniform(e.e.x), uniform(e.e.y), uniform(e.e.z), uniform(e.e.w)), uniform(e.row),
-          uniform(e.len)};
+__device__ __forceinline__ Part uniform(const Part& p) {
+  return {uniform(p.w), uniform(p.seg), uniform(p.steps), uniform(p.row), uniform(p.len), uniform(p.of),
+          uniform(p.partial)};
 }
 template <typename F>
-__device__ __forceinline__ void for_units(const int4* __restrict__ entries, int count, int tiles, F f) {
-  const int step = gridDim.x / 2;
-  int i = (blockIdx.x / 2) / tiles, tile = (blockIdx.x / 2) % tiles;
-  if (i >= count) return;
-  Entry cur = uniform(load_entry(entries, i)), next = cur;
+__device__ __forceinline__ void for_units(const int4* __restrict__ parts, int count, int tiles, F f) {
+  const int pairs = gridDim.x / 2, units = count * tiles, me = blockIdx.x / 2;
+  int base = 0, u = me;
+  if (u >= units) return;
+  Part cur = uniform(load_part(parts, u / tiles)), next = cur;
   for (;;) {
-    const int t = tile + step, ni = i + t / tiles;
-    if (ni < count) next = load_entry(entries, ni);
-    if (!f(cur, tile) || ni >= count) return;
+    base += pairs;
+    const int nu = base / pairs % 2 == 0 ? base + me : base + pairs - 1 - me;
+    const bool more = nu < units;
+    if (more) next = load_part(parts, nu / tiles);
+    if (!f(cur, u % tiles) || !more) return;  // (only the last round is short)
     cur = uniform(next);
-    i = ni;
-    tile = t % tiles;
+    u = nu;
   }
 }
-// The steps of one unit: f(first buffer row, rows left from it on) per step.
+// The steps of one unit: f(first buffer row, rows left in the segment from it on) per step.
 template <typename F>
-__device__ __forceinline__ bool for_steps(const Entry& en, const int2* __restrict__ segs, F f) {
-  int row = en.row, len = en.len;
-  for (int g = 0; g < en.e.z; ++g) {
-    if (g > 0) {
-      const int2 seg = segs[en.e.y + g];
+__device__ __forceinline__ bool for_steps(const Part& part, const int2* __restrict__ segs, F f) {
+  int row = part.row, len = part.len, g = part.seg;
+  for (int steps = part.steps; steps > 0; --steps) {
+    if (len <= 0) {
+      const int2 seg = segs[++g];
       row = uniform(seg.x);
       len = uniform(seg.y);
     }
-    for (int k = 0; k < len; k += kBK)
-      if (!f(row + k, len - k)) return false;
+    if (!f(row, len)) return false;
+    row += kBK;
+    len -= kBK;
   }
   return true;
 }
@@ -322,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_wgrad_pair(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_s,
                  const __grid_constant__ CUtensorMap map_dy, const __grid_constant__ CUtensorMap map_home,
                  const __grid_constant__ CUtensorMap map_slot, const int* __restrict__ count_ptr,
-                 const int4* __restrict__ entries, const int2* __restrict__ segs, int32_t* status,
-                 int E, int H, int Hp, int accumulate) {
+                 const int4* __restrict__ parts, const int2* __restrict__ segs, int* __restrict__ arrived,
+                 float4* __restrict__ partials, int32_t* status, int E, int H, int Hp, int accumulate) {
   constexpr int kSt = Ring<CKPT>::stages, kStage = Ring<CKPT>::stage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -375,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- TMA producer ----------------
       Pos at;
       uint32_t issued = 0;
-      for_units(entries, count, tiles, [&](const Entry& en, int t) {
+      for_units(parts, count, tiles, [&](const Part& en, int t) {
         const int h0 = t / nN * 2 * kBM + rank * kBM, n0 = t % nN * kBN;
         const bool narrow = Hp - n0 <= 128;
         const int c0 = n0 + rank * (narrow ? 64 : 128);
@@ -415,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- MMA issuer (CTA 0 only) ----------------
       Pos at, acc;  // stage; accumulator
       const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + kOp, kBox, 1024);
-      for_units(entries, count, tiles, [&](const Entry& en, int t) {
+      for_units(parts, count, tiles, [&](const Part& en, int t) {
         const uint32_t idesc = Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc;
-        int steps = en.e.w, in_chunk = 0;
+        int steps = en.steps, in_chunk = 0;
         return for_steps(en, segs, [&](int, int left) {
           if (in_chunk == 0 &&
               !warp_wait(smem_u32(&S->tempty[acc.s]), acc.parity ^ 1u, abort_flag, status))
@@ -465,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = threadIdx.x - 128, c8 = t & 7;
     const int row0 = (lane >> 4) + ((lane >> 3) & 1) * 4 + (warp & 1) * 2 + ((warp >> 1) & 1) * 8;
     Pos at;
-    for_units(entries, count, tiles, [&](const Entry& en, int tile) {
+    for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h0 = tile / nN * 2 * kBM + rank * kBM;
       const uint32_t sbyte = (uint32_t)(h0 / kCkptBlock) & 15u;
       return for_steps(en, segs, [&](int, int left) {
@@ -523,10 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = (warp - 8) >> 2;
     const uint32_t box = out_box + (uint32_t)(warp - 8) * kStoreBox;
     Pos at;
-    for_units(entries, count, tiles, [&](const Entry& en, int tile) {
-      const int4 e = en.e;
+    for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h = tile / nN * 2 * kBM + rank * kBM + 32 * q, n = tile % nN * kBN + 128 * half;
-      const int chunks = (e.w + kChunk - 1) / kChunk;
+      const int chunks = (en.steps + kChunk - 1) / kChunk;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -548,8 +617,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[at.s]), 0));
         at.template next<2>();
       }
-      const CUtensorMap* map = e.x < E ? &map_home : &map_slot;
-      const int z = e.x < E ? e.x : e.x - E;
+      if ((en.of & 255) > 1 && h < H && n < Hp) {
+        // This part's sums go to the workspace, in the order of the threads
+        // that will read them; the warp that comes last adds up all parts', in
+        // their order: the same bits whoever is last.
+        const int np = en.of & 255, mine = (rank * kEpiWarps + warp - 8) * 32 * 32 + lane;
+        const long long part0 = (long long)en.partial * tiles + tile;
+        float4* own = partials + (part0 + (long long)(en.of >> 8) * tiles) * (kTile / 4) + mine;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          __stcg(own + 32 * i, make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(arrived + part0 * 2 * kEpiWarps + rank * kEpiWarps + warp - 8, 1);
+        if (uniform(before) != np - 1) return true;
+        __threadfence();
+#pragma unroll
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+        for (int k = 0; k < np; ++k) {
+          const float4* from = partials + (part0 + (long long)k * tiles) * (kTile / 4) + mine;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float4 v = __ldcg(from + 32 * i);
+            acc[4 * i] += v.x;
+            acc[4 * i + 1] += v.y;
+            acc[4 * i + 2] += v.z;
+            acc[4 * i + 3] += v.w;
+          }
+        }
+      }
+      const CUtensorMap* map = en.w < E ? &map_home : &map_slot;
+      const int z = en.w < E ? en.w : en.w - E;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (h < H && n + 32 * i < Hp) {
@@ -619,11 +718,11 @@ bool map_grad(CUtensorMap* m, float* ptr, unsigned long long n, unsigned long lo
 template <bool CKPT>
 cudaError_t launch_wgrad(cudaStream_t st, const CUtensorMap& mx, const CUtensorMap& ms,
                          const CUtensorMap& md, const CUtensorMap& mh, const CUtensorMap& msl,
-                         const int* count, const int4* entries, const int2* segs, int32_t* status,
-                         int E, int H, int Hp, int accumulate) {
+                         const int* count, const int4* parts, const int2* segs, int* arrived,
+                         float4* partials, int32_t* status, int E, int H, int Hp, int accumulate) {
   static GridCache cache;
   void (*kernel)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, const int*,
-                 const int4*, const int2*, int32_t*, int, int, int, int) = k_wgrad_pair<CKPT>;
+                 const int4*, const int2*, int*, float4*, int32_t*, int, int, int, int) = k_wgrad_pair<CKPT>;
   if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), Ring<CKPT>::smem))
     return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -661,8 +760,40 @@ cudaError_t launch_wgrad(cudaStream_t st, const CUtensorMap& mx, const CUtensorM
     grid = cache.grid[dev];
   }
   cfg.gridDim = dim3(grid);
-  return cudaLaunchKernelEx(&cfg, kernel, mx, ms, md, mh, msl, count, entries, segs, status, E, H, Hp,
-                            accumulate);
+  return cudaLaunchKernelEx(&cfg, kernel, mx, ms, md, mh, msl, count, parts, segs, arrived, partials, status,
+                            E, H, Hp, accumulate);
+}
+
+// The workspace: count | parts | entries | arrivals | segments | partial sums.
+struct Layout {
+  size_t parts, entries, arrived, segs, partials, bytes;
+};
+long long tiles_of(int H, int Hp) {
+  return (long long)((H + 2 * kBM - 1) / (2 * kBM)) * ((Hp + kBN - 1) / kBN);
+}
+// Partial sums at most: an entry of s steps is cut into at most s / most + 1 <=
+// 2 s / most parts, and most >= steps * tiles / (2 kPairs) over all entries;
+// only entries of more than kLeastSteps steps are cut, into at most s / 4 parts;
+// and every segment of rows has one step that is not full.
+long long partials_of(int R, long long rows, int G, int H, int Hp) {
+  const long long segments = rows < (long long)R * G ? rows : (long long)R * G;
+  const long long steps = rows / kBK + segments;
+  if (steps <= kLeastSteps) return 0;
+  const long long by_steps = tiles_of(H, Hp) * (steps / 4 + 1);
+  return by_steps < kMostPartials ? by_steps : kMostPartials;
+}
+Layout layout_of(int R, long long SK, int E, int B, int H, int Hp) {
+  const auto up = [](size_t v) { return (v + 255) & ~size_t(255); };
+  const size_t W = (size_t)E + (size_t)R * B;
+  const long long np = partials_of(R, (long long)R * SK, E + B, H, Hp);
+  Layout l;
+  l.parts = 16;
+  l.entries = l.parts + 32 * (W + kMostPartials);
+  l.arrived = l.entries + 16 * W;
+  l.segs = l.arrived + 4 * (size_t)np * 2 * kEpiWarps;
+  l.partials = up(l.segs + 8 * (size_t)R * (E + B));
+  l.bytes = l.partials + 4 * (size_t)np * kTile;
+  return l;
 }
 
 }  // namespace
@@ -670,11 +801,18 @@ cudaError_t launch_wgrad(cudaStream_t st, const CUtensorMap& mx, const CUtensorM
 
 using namespace mep;
 
-extern "C" int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int B, size_t* bytes) {
+extern "C" int mep_grouped_wgrad_workspace_bytes(int R, int S, int K, int E, int B, int H, int Hp,
+                                                 size_t* bytes) {
   if (bytes == nullptr || R < 1 || S < 0 || K < 1 || E < 1 || B < 0) return MEP_ERR_INVALID_ARG;
   if (R > MEP_MAX_R || E > MEP_MAX_E || K > MEP_MAX_K || (long long)R * B > MEP_MAX_SLOTS)
     return MEP_ERR_INVALID_ARG;
-  *bytes = 16 + 32 * ((size_t)E + (size_t)R * B) + 8 * (size_t)R * (E + B);
+  if (H < 8 || H % 8 != 0 || Hp < 8 || Hp % 8 != 0 || H > MEP_MAX_CKPT_C || Hp > MEP_MAX_CKPT_C)
+    return MEP_ERR_INVALID_ARG;
+  const long long SK = (long long)S * K;
+  if (R * SK > 0x7fffff00LL ||
+      tiles_of(H, Hp) > 0x7fff0000LL / (2 * kMostPartials + (long long)E + (long long)R * B))
+    return MEP_ERR_INVALID_ARG;
+  *bytes = layout_of(R, SK, E, B, H, Hp).bytes;
   return MEP_OK;
 }
 
@@ -683,14 +821,9 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
                                  int E, int B, int H, int Hp, int accumulate, void* ws,
                                  size_t ws_bytes, float* home_grad, float* slot_grad, void* stream) {
   size_t need = 0;
-  if (mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, &need) != MEP_OK) return MEP_ERR_INVALID_ARG;
+  if (mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, H, Hp, &need) != MEP_OK) return MEP_ERR_INVALID_ARG;
   if (x_type != MEP_BF16 && x_type != MEP_CKPT8) return MEP_ERR_INVALID_ARG;
-  if (H < 8 || H % 8 != 0 || Hp < 8 || Hp % 8 != 0 || H > MEP_MAX_CKPT_C || Hp > MEP_MAX_CKPT_C)
-    return MEP_ERR_INVALID_ARG;
   const long long SK = (long long)S * K, rows = (long long)R * SK;
-  const long long tiles = (long long)((H + 2 * kBM - 1) / (2 * kBM)) * ((Hp + kBN - 1) / kBN);
-  if (rows > 0x7fffff00LL || tiles * ((long long)E + (long long)R * B) > 0x7fff0000LL)
-    return MEP_ERR_INVALID_ARG;
   if (cu_seqlens == nullptr || home_grad == nullptr || ws == nullptr || ws_bytes < need ||
       (B > 0 && slot_grad == nullptr) || (rows > 0 && (x == nullptr || dy == nullptr)))
     return MEP_ERR_INVALID_ARG;
@@ -717,16 +850,20 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
                         CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return MEP_ERR_CUDA;
   }
-  int* count = static_cast<int*>(ws);
-  int4* entries = reinterpret_cast<int4*>(static_cast<char*>(ws) + 16);
-  int2* segs = reinterpret_cast<int2*>(entries + 2 * ((size_t)E + (size_t)R * B));
+  const Layout l = layout_of(R, SK, E, B, H, Hp);
+  char* p = static_cast<char*>(ws);
+  int *count = reinterpret_cast<int*>(p), *arrived = reinterpret_cast<int*>(p + l.arrived);
+  int4 *parts = reinterpret_cast<int4*>(p + l.parts), *entries = reinterpret_cast<int4*>(p + l.entries);
+  int2* segs = reinterpret_cast<int2*>(p + l.segs);
+  float4* partials = reinterpret_cast<float4*>(p + l.partials);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t err = launch_pdl(k_wgrad_groups, dim3(1), dim3(kGroupThreads), 0, st, cu_seqlens, R, E,
-                               B, int(SK), accumulate, status, count, entries, segs);
+  cudaError_t err =
+      launch_pdl(k_wgrad_groups, dim3(1), dim3(kGroupThreads), 0, st, cu_seqlens, R, E, B, int(SK),
+                 int(tiles_of(H, Hp)), accumulate, status, count, parts, entries, segs, arrived);
   if (err != cudaSuccess) return MEP_ERR_CUDA;
-  err = x_type == MEP_CKPT8 ? launch_wgrad<true>(st, mx, ms, md, mh, msl, count, entries, segs, status,
-                                                 E, H, Hp, accumulate)
-                            : launch_wgrad<false>(st, mx, ms, md, mh, msl, count, entries, segs,
-                                                  status, E, H, Hp, accumulate);
+  err = x_type == MEP_CKPT8 ? launch_wgrad<true>(st, mx, ms, md, mh, msl, count, parts, segs, arrived,
+                                                 partials, status, E, H, Hp, accumulate)
+                            : launch_wgrad<false>(st, mx, ms, md, mh, msl, count, parts, segs, arrived,
+                                                  partials, status, E, H, Hp, accumulate);
   return err == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
 }

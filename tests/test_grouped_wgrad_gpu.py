@@ -100,6 +100,24 @@ def test_wgrad_random_tables(seed):
     _case(cu, E, H, Hp, seed, seed % 2 == 0, seed % 3 == 0)
 
 
+@pytest.mark.parametrize("kept", [False, True], ids=["as_it_was", "kept"])
+@pytest.mark.parametrize("sizes", [
+    [[1500, 3, 0, 0, 40]],                                    # one group of 24 steps beside short ones
+    [[0, 5000, 0, 0, 0], [0, 0, 700, 4300, 0]],               # three long ones, one of them of two parts' length
+    [[9 * 64, 8 * 64, 64, 1, 9 * 64 + 1]],                    # at the shortest length that is cut, and beside it
+    [[600, 100, 70, 30, 0], [650, 20, 30, 100, 0], [64, 0, 36, 700, 0]],  # parts that begin inside a rank's rows
+])
+def test_wgrad_groups_in_parts(sizes, kept):
+    _case(_cu(sizes), 3, 264, 136, 5, True, kept)
+    _case(_cu(sizes), 3, 72, 520, 6, False, kept, accumulate=True, before=2.0)
+
+
+def test_wgrad_more_weight_rows_than_a_block_of_threads():
+    n = np.random.default_rng(0).integers(0, 3, (2, 1100))
+    n[:, -1] += 3000 - n.sum(1)  # every rank has 3000 rows
+    _case(_cu(n), 1090, 8, 16, 7, True, False)
+
+
 def test_wgrad_wide():
     _case(_cu([[100, 28]]), 1, 7168, 72, 1, True, True)
     _case(_cu([[100, 28]]), 1, 72, 7168, 1, True, False)

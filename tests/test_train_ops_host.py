@@ -81,7 +81,7 @@ def test_swiglu_rejects_bad_args(lib):
 
 
 def test_grouped_wgrad_rejects_bad_args(lib):
-    need = mep.grouped_wgrad_workspace_bytes(2, 4, 2, 8, 4)
+    need = mep.grouped_wgrad_workspace_bytes(2, 4, 2, 8, 4, 64, 64)
 
     def f(x=16, xt=BF16, dy=16, cu=16, R=2, S=4, K=2, E=8, B=4, H=64, Hp=64, ws=256, wb=None, home=16, slot=16):
         return lib.mep_grouped_wgrad(x, xt, dy, cu, None, R, S, K, E, B, H, Hp, 0, ws, need if wb is None else wb, home, slot,
@@ -93,5 +93,5 @@ def test_grouped_wgrad_rejects_bad_args(lib):
                dict(dy=24), dict(home=20), dict(slot=20), dict(ws=260)):
         assert f(**kw) == BAD, kw
     out = ctypes.c_size_t(0)
-    assert lib.mep_grouped_wgrad_workspace_bytes(2, 4, 2, 8, 4, None) == BAD
-    assert lib.mep_grouped_wgrad_workspace_bytes(0, 4, 2, 8, 4, ctypes.byref(out)) == BAD
+    assert lib.mep_grouped_wgrad_workspace_bytes(2, 4, 2, 8, 4, 64, 64, None) == BAD
+    assert lib.mep_grouped_wgrad_workspace_bytes(0, 4, 2, 8, 4, 64, 64, ctypes.byref(out)) == BAD
