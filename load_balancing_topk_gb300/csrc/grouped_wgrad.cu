@@ -165,119 +165,100 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 
 // ---------------------------------------------------------------------------
 // The weight rows to write, weight row < E a home expert and E + r*B + b slot
-// b of rank r: entries[i] = {weight row, first segment, segments, steps};
-// segs[j] = {first buffer row, rows}. Without `accumulate` a home expert is
-// listed even without rows (it is written as zero), a slot never is.
+// b of rank r, in parts: parts[2i] = {weight row, first segment, 0, steps},
+// parts[2i + 1] = {first buffer row, rows from there to the segment's end,
+// parts of this weight row + 256 * number of this one, index of the weight
+// row's first partial sum}; segs[j] = {first buffer row, rows}, R places for a
+// home expert and one for a slot. Without `accumulate` a home expert is listed
+// even without rows (it is written as zero), a slot never is.
 //
-// Their parts: parts[2i] = {weight row, first segment, 0, steps}, parts[2i + 1] =
-// {first buffer row, rows from there to the segment's end, parts of this entry
-// + 256 * number of this one, index of the entry's first partial sum}. A part
-// is at most half of what a pair has to do in all, so that few, uneven groups
-// still fill the pairs; a group has at most kMostParts (the last of them adds
-// the partial sums of all up), and a part at least kLeastSteps. The longest
-// come first. With more weight rows than threads the list stays as it is: that
-// many fill the pairs.
+// A part is at most half of what a pair has to do in all, so that few, uneven
+// groups still fill the pairs; a group has at most kMostParts (the last of them
+// adds the partial sums of all up), and only one of more than kLeastSteps is
+// cut. The longest come first. A thread has one weight row, reads its group
+// ends once (together the threads read, and check, all of cu_seqlens), and
+// places its parts by counting over the others' lengths in shared memory. With
+// more weight rows than threads the list is in their order and nothing is cut:
+// that many fill the pairs.
 __device__ __forceinline__ int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
+
+struct Row {  // a weight row's group
+  int segments = 0, steps = 0;
+  int2 first = {0, 0};  // its first segment
+  bool bad = false;
+};
+// Reads the group ends of weight row w, checks them, lists the segments.
+__device__ __forceinline__ Row read_row(const int32_t* __restrict__ cu, int w, int R, int E, int B, int SK,
+                                        int2* __restrict__ segs) {
+  Row row;
+  const int G = E + B;
+  const bool home = w < E;
+  const int j = home ? w : E + (w - E) % B, r0 = home ? 0 : (w - E) / B, r1 = home ? R : r0 + 1;
+  int2* to = segs + (home ? (long long)w * R : (long long)E * R + (w - E));
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    const long long p = (long long)r * G + j;
+    const int hi = cu[p], lo = j == 0 ? 0 : cu[p - 1], len = hi - lo;
+    if (len < 0 || (j == G - 1 && hi != SK)) row.bad = true;
+    if (len > 0) {
+      const int2 seg = make_int2(int((long long)r * SK + lo), len);
+      if (row.segments == 0) row.first = seg;
+      to[row.segments++] = seg;
+      row.steps += ceil_div(len, kBK);
+    }
+  }
+  return row;
+}
 
 __global__ void __launch_bounds__(kGroupThreads)
     k_wgrad_groups(const int32_t* __restrict__ cu, int R, int E, int B, int SK, int tiles, int accumulate,
                    int32_t* status, int* __restrict__ count, int4* __restrict__ parts,
-                   int4* __restrict__ entries, int2* __restrict__ segs, int* __restrict__ arrived) {
+                   int2* __restrict__ segs, int* __restrict__ arrived) {
   pdl_wait();
   pdl_launch_dependents();
-  __shared__ int s_warp[33], s_entry[kGroupThreads + 1], s_seg[kGroupThreads + 1];
-  __shared__ int s_bad, s_entries, s_segs, s_stat, s_partials;
-  __shared__ unsigned long long s_steps;
-  const int G = E + B;
-  if (threadIdx.x == 0) {
-    s_bad = s_entries = s_segs = s_partials = 0;
-    s_steps = 0;
-    s_stat = read_status(status);
-  }
-  __syncthreads();
-  if (s_stat != 0) {
-    if (threadIdx.x == 0) *count = 0;
-    return;
-  }
-  for (long long p = threadIdx.x; p < (long long)R * G; p += blockDim.x) {
-    const int j = int(p % G), v = cu[p], prev = j == 0 ? 0 : cu[p - 1];
-    if (v < prev || (j == G - 1 && v != SK)) s_bad = 1;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (threadIdx.x == 0) {
-      *count = 0;
-      set_status(status, MEP_ERR_BAD_SEQLENS);
+  __shared__ int s_warp[33], s_listed[kGroupThreads + 1];
+  __shared__ int2 s_rows[kGroupThreads];  // {steps of a part, parts}
+  __shared__ int s_steps;
+  const int W = E + R * B, t = threadIdx.x;
+  const auto seg0 = [&](int w) { return w < E ? w * R : E * R + (w - E); };
+  if (t == 0) s_steps = 0;
+  const int stat = read_status(status);
+  if (W <= int(blockDim.x)) {
+    const Row row = t < W ? read_row(cu, t, R, E, B, SK, segs) : Row();
+    const int stop = __syncthreads_or((stat != 0 ? 2 : 0) | (row.bad ? 1 : 0));
+    if (stop) {  // (what is read from a malformed table is not used)
+      if (t == 0) {
+        *count = 0;
+        if (stat == 0) set_status(status, MEP_ERR_BAD_SEQLENS);
+      }
+      return;
     }
-    return;
-  }
-  const int W = E + R * B;
-  for (int base = 0; base < W; base += blockDim.x) {
-    const int w = base + threadIdx.x;
-    const bool home = w < E;
-    const int j = home ? w : (w < W ? E + (w - E) % B : 0);
-    const int r0 = home ? 0 : (w < W ? (w - E) / B : 0), r1 = w < W ? (home ? R : r0 + 1) : r0;
-    int nseg = 0, steps = 0;
-    for (int r = r0; r < r1; ++r) {
-      const long long p = (long long)r * G + j;
-      const int len = cu[p] - (j == 0 ? 0 : cu[p - 1]);
-      nseg += len > 0;
-      steps += ceil_div(len, kBK);
-    }
-    const bool listed = w < W && (nseg > 0 || (home && !accumulate));
-    s_entry[threadIdx.x] = listed;
-    s_seg[threadIdx.x] = nseg;
-    if (steps > 0) atomicAdd(&s_steps, (unsigned long long)steps);
+    const int warp_steps = __reduce_add_sync(MEP_FULL_MASK, row.steps);
+    if ((t & 31) == 0 && warp_steps > 0) atomicAdd(&s_steps, warp_steps);
     __syncthreads();
-    block_excl_scan(s_entry, s_entry, blockDim.x, s_warp, true);
-    block_excl_scan(s_seg, s_seg, blockDim.x, s_warp, true);
-    if (listed) {
-      int at = s_segs + s_seg[threadIdx.x];
-      entries[s_entries + s_entry[threadIdx.x]] = make_int4(w, at, nseg, steps);
-      for (int r = r0; r < r1; ++r) {
-        const long long p = (long long)r * G + j;
-        const int lo = j == 0 ? 0 : cu[p - 1], len = cu[p] - lo;
-        if (len > 0) segs[at++] = make_int2(int((long long)r * SK + lo), len);
+    const int most = max(kLeastSteps, ceil_div((long long)s_steps * tiles, 2 * kPairs)), s = row.steps;
+    const bool listed = t < W && (s > 0 || (t < E && !accumulate));
+    const int len = s > most ? max(ceil_div(s, kMostParts), ceil_div(s, ceil_div(s, most))) : s;
+    const int np = !listed ? 0 : s > 0 ? ceil_div(s, len) : 1;
+    if (t < W) s_rows[t] = make_int2(len, np);
+    __syncthreads();
+    int pos = 0, partial = 0, all = 0, partials = 0;
+    for (int j = 0; j < W; ++j) {
+      const int2 o = s_rows[j];
+      all += o.y;
+      if (o.x > len || (o.x == len && j < t)) pos += o.y;
+      if (o.y > 1) {
+        partials += o.y;
+        if (j < t) partial += o.y;
       }
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s_entries += s_entry[blockDim.x];
-      s_segs += s_seg[blockDim.x];
-    }
-    __syncthreads();
-  }
-  // this CTA's own global writes are read again below
-  __threadfence_block();
-  const int n = s_entries;
-  const bool sorted = n <= int(blockDim.x);
-  const int most = max(kLeastSteps, ceil_div((long long)s_steps * tiles, 2 * kPairs));
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int4 e = entries[i];
-    const int len = sorted && e.w > most ? max(ceil_div(e.w, kMostParts), ceil_div(e.w, ceil_div(e.w, most))) : e.w;
-    if (sorted) {
-      s_entry[i] = len;                                // steps of a part
-      s_seg[i] = e.w > 0 ? ceil_div(e.w, len) : 1;     // parts
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int4 e = entries[i];
-    const int len = sorted ? s_entry[i] : e.w, np = sorted ? s_seg[i] : 1;
-    int pos = i, partial = 0;
-    if (sorted) {
-      pos = 0;
-      for (int j = 0; j < n; ++j) {
-        if (s_entry[j] > len || (s_entry[j] == len && j < i)) pos += s_seg[j];
-        if (j < i && s_seg[j] > 1) partial += s_seg[j];
-      }
-      if (i == n - 1) s_partials = partial + (np > 1 ? np : 0);
-    }
-    int g = e.y, done = 0;  // segment, its steps that are behind
+    if (t == 0) *count = all;
+    for (int i = t; i < partials * tiles * 2 * kEpiWarps; i += blockDim.x) arrived[i] = 0;
+    int g = seg0(t), done = 0;  // segment, its steps that are behind
+    int2 seg = row.first;
     for (int k = 0; k < np; ++k) {
-      int2 seg = e.z > 0 ? segs[g] : make_int2(0, 0);
-      const int steps = min(len, e.w - k * len);
-      parts[2 * (pos + k)] = make_int4(e.x, g, 0, steps);
+      const int steps = min(len, s - k * len);
+      parts[2 * (pos + k)] = make_int4(t, g, 0, steps);
       parts[2 * (pos + k) + 1] = make_int4(seg.x + done * kBK, seg.y - done * kBK, np + 256 * k, partial);
       for (int left = k + 1 < np ? steps : 0; left > 0;) {  // on to the next part's first step
         const int here = ceil_div(seg.y, kBK) - done;
@@ -287,20 +268,34 @@ __global__ void __launch_bounds__(kGroupThreads)
         } else {
           left -= here;
           done = 0;
-          ++g;
-          if (left > 0) seg = segs[g];
+          seg = segs[++g];
         }
       }
     }
+    return;
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int total = n;
-    if (sorted)
-      for (int i = 0; i < n; ++i) total += s_seg[i] - 1;
-    *count = total;
+  int bad = 0, listed_before = 0;
+  for (int base = 0; base < W; base += blockDim.x) {
+    const int w = base + t;
+    const Row row = w < W ? read_row(cu, w, R, E, B, SK, segs) : Row();
+    bad |= row.bad;
+    const bool listed = w < W && (row.steps > 0 || (w < E && !accumulate));
+    s_listed[t] = listed;
+    __syncthreads();
+    block_excl_scan(s_listed, s_listed, blockDim.x, s_warp, true);
+    if (listed) {
+      int4* part = parts + 2 * (listed_before + s_listed[t]);
+      part[0] = make_int4(w, seg0(w), 0, row.steps);
+      part[1] = make_int4(row.first.x, row.first.y, 1, 0);
+    }
+    listed_before += s_listed[blockDim.x];
+    __syncthreads();
   }
-  for (int i = threadIdx.x; i < s_partials * tiles * 2 * kEpiWarps; i += blockDim.x) arrived[i] = 0;
+  bad = __syncthreads_or(bad);
+  if (t == 0) {
+    *count = bad || stat != 0 ? 0 : listed_before;
+    if (bad && stat == 0) set_status(status, MEP_ERR_BAD_SEQLENS);
+  }
 }
 
 // Two signed bytes of w (chosen by sel) times a power of two, as two bf16.
@@ -764,9 +759,9 @@ cudaError_t launch_wgrad(cudaStream_t st, const CUtensorMap& mx, const CUtensorM
                             E, H, Hp, accumulate);
 }
 
-// The workspace: count | parts | entries | arrivals | segments | partial sums.
+// The workspace: count | parts | arrivals | segments | partial sums.
 struct Layout {
-  size_t parts, entries, arrived, segs, partials, bytes;
+  size_t parts, arrived, segs, partials, bytes;
 };
 long long tiles_of(int H, int Hp) {
   return (long long)((H + 2 * kBM - 1) / (2 * kBM)) * ((Hp + kBN - 1) / kBN);
@@ -788,8 +783,7 @@ Layout layout_of(int R, long long SK, int E, int B, int H, int Hp) {
   const long long np = partials_of(R, (long long)R * SK, E + B, H, Hp);
   Layout l;
   l.parts = 16;
-  l.entries = l.parts + 32 * (W + kMostPartials);
-  l.arrived = l.entries + 16 * W;
+  l.arrived = l.parts + 32 * (W + kMostPartials);
   l.segs = l.arrived + 4 * (size_t)np * 2 * kEpiWarps;
   l.partials = up(l.segs + 8 * (size_t)R * (E + B));
   l.bytes = l.partials + 4 * (size_t)np * kTile;
@@ -853,13 +847,15 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   const Layout l = layout_of(R, SK, E, B, H, Hp);
   char* p = static_cast<char*>(ws);
   int *count = reinterpret_cast<int*>(p), *arrived = reinterpret_cast<int*>(p + l.arrived);
-  int4 *parts = reinterpret_cast<int4*>(p + l.parts), *entries = reinterpret_cast<int4*>(p + l.entries);
+  int4* parts = reinterpret_cast<int4*>(p + l.parts);
   int2* segs = reinterpret_cast<int2*>(p + l.segs);
   float4* partials = reinterpret_cast<float4*>(p + l.partials);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // a small block: its barriers are most of what this kernel takes
+  const int W = E + R * B, group_threads = W >= kGroupThreads ? kGroupThreads : W < 128 ? 128 : (W + 31) / 32 * 32;
   cudaError_t err =
-      launch_pdl(k_wgrad_groups, dim3(1), dim3(kGroupThreads), 0, st, cu_seqlens, R, E, B, int(SK),
-                 int(tiles_of(H, Hp)), accumulate, status, count, parts, entries, segs, arrived);
+      launch_pdl(k_wgrad_groups, dim3(1), dim3(group_threads), 0, st, cu_seqlens, R, E, B, int(SK),
+                 int(tiles_of(H, Hp)), accumulate, status, count, parts, segs, arrived);
   if (err != cudaSuccess) return MEP_ERR_CUDA;
   err = x_type == MEP_CKPT8 ? launch_wgrad<true>(st, mx, ms, md, mh, msl, count, parts, segs, arrived,
                                                  partials, status, E, H, Hp, accumulate)
