@@ -482,7 +482,7 @@ MEP_API int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_type,
  *              expert), and so are the slots that have rows; slots without
  *              rows are left alone. Not 0: added to what is there.
  *   ws         device workspace of at least mep_grouped_wgrad_workspace_bytes
- *              (the list of groups, and up to 80 MB of partial sums of groups
+ *              (the list of groups, and up to 40 MB of partial sums of groups
  *              that are long next to the others; rebuilt by every call)
  *   home_grad  fp32 [E, H, H']      output
  *   slot_grad  fp32 [R, B, H, H']   output; may be NULL when B == 0

@@ -65,10 +65,15 @@ constexpr int kGroupThreads = 1024;
 constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
 constexpr int kEpiWarps = 8;
 constexpr int kPair = 2;
-constexpr int kPairs = 76;       // a fixed number, so that the parts do not depend on the device
-constexpr int kLeastSteps = 8;
+// How long groups are cut into parts (k_wgrad_groups). At H 512, H' 512 one
+// group of 4096 rows took 31 us whole, 31 in parts of 8 steps and 28 in parts
+// of 16, which is no loss at 1024 rows either (18 against 22 us); two groups of
+// 16384 rows at 256 x 256 took 156 us whole, 59 in four parts, 47 in eight and
+// 50 in sixteen (the last of them adds all up).
+constexpr int kPairs = 76;  // a fixed number, so that the parts do not depend on the device
+constexpr int kLeastSteps = 16;
 constexpr int kMostParts = 8;
-constexpr int kMostPartials = 4 * kPairs;  // parts * tiles of all entries with several parts: see partials_of
+constexpr int kMostPartials = 2 * kPairs;  // parts * tiles of all entries with several parts: see partials_of
 constexpr int kTile = 2 * kBM * kBN;       // fp32 values of a partial sum
 
 template <bool CKPT> struct Ring {
@@ -172,8 +177,9 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 // home expert and one for a slot. Without `accumulate` a home expert is listed
 // even without rows (it is written as zero), a slot never is.
 //
-// A part is at most half of what a pair has to do in all, so that few, uneven
-// groups still fill the pairs; a group has at most kMostParts (the last of them
+// A part is at most what a pair has to do in all, so that few, uneven groups
+// still fill the pairs (half of that cost more in joins than it evened out: 58
+// against 48 us at 22220 rows in 18 groups, 1160 x 520); a group has at most kMostParts (the last of them
 // adds the partial sums of all up), and only one of more than kLeastSteps is
 // cut. The longest come first. A thread has one weight row, reads its group
 // ends once (together the threads read, and check, all of cu_seqlens), and
@@ -236,7 +242,7 @@ __global__ void __launch_bounds__(kGroupThreads)
     const int warp_steps = __reduce_add_sync(MEP_FULL_MASK, row.steps);
     if ((t & 31) == 0 && warp_steps > 0) atomicAdd(&s_steps, warp_steps);
     __syncthreads();
-    const int most = max(kLeastSteps, ceil_div((long long)s_steps * tiles, 2 * kPairs)), s = row.steps;
+    const int most = max(kLeastSteps, ceil_div((long long)s_steps * tiles, kPairs)), s = row.steps;
     const bool listed = t < W && (s > 0 || (t < E && !accumulate));
     const int len = s > most ? max(ceil_div(s, kMostParts), ceil_div(s, ceil_div(s, most))) : s;
     const int np = !listed ? 0 : s > 0 ? ceil_div(s, len) : 1;
@@ -767,14 +773,13 @@ long long tiles_of(int H, int Hp) {
   return (long long)((H + 2 * kBM - 1) / (2 * kBM)) * ((Hp + kBN - 1) / kBN);
 }
 // Partial sums at most: an entry of s steps is cut into at most s / most + 1 <=
-// 2 s / most parts, and most >= steps * tiles / (2 kPairs) over all entries;
-// only entries of more than kLeastSteps steps are cut, into at most s / 4 parts;
-// and every segment of rows has one step that is not full.
+// 2 s / most parts, and most >= steps * tiles / kPairs over all entries; only
+// entries of more than kLeastSteps steps are cut, into at most s / 8 parts; and every segment of rows has one step that is not full.
 long long partials_of(int R, long long rows, int G, int H, int Hp) {
   const long long segments = rows < (long long)R * G ? rows : (long long)R * G;
   const long long steps = rows / kBK + segments;
   if (steps <= kLeastSteps) return 0;
-  const long long by_steps = tiles_of(H, Hp) * (steps / 4 + 1);
+  const long long by_steps = tiles_of(H, Hp) * (steps / 8 + 1);
   return by_steps < kMostPartials ? by_steps : kMostPartials;
 }
 Layout layout_of(int R, long long SK, int E, int B, int H, int Hp) {

@@ -102,10 +102,10 @@ def test_wgrad_random_tables(seed):
 
 @pytest.mark.parametrize("kept", [False, True], ids=["as_it_was", "kept"])
 @pytest.mark.parametrize("sizes", [
-    [[1500, 3, 0, 0, 40]],                                    # one group of 24 steps beside short ones
+    [[3000, 3, 0, 0, 40]],                                    # one group of 47 steps beside short ones
     [[0, 5000, 0, 0, 0], [0, 0, 700, 4300, 0]],               # three long ones, one of them of two parts' length
-    [[9 * 64, 8 * 64, 64, 1, 9 * 64 + 1]],                    # at the shortest length that is cut, and beside it
-    [[600, 100, 70, 30, 0], [650, 20, 30, 100, 0], [64, 0, 36, 700, 0]],  # parts that begin inside a rank's rows
+    [[17 * 64, 16 * 64, 64, 1, 17 * 64 + 1]],                 # at the shortest length that is cut, and beside it
+    [[900, 100, 70, 130, 0], [950, 20, 30, 200, 0], [64, 0, 36, 1100, 0]],  # parts that begin inside a rank's rows
 ])
 def test_wgrad_groups_in_parts(sizes, kept):
     _case(_cu(sizes), 3, 264, 136, 5, True, kept)
