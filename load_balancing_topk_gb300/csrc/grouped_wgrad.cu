@@ -61,6 +61,7 @@ constexpr int kScale = kBK * 16;         // their scale bytes, in 16-byte rows
 constexpr int kChunk = MEP_WGRAD_CHUNK;  // steps summed in TMEM
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 2 * kBN;
+constexpr int kACols = kBK / 2;          // TMEM columns of an A of one step
 constexpr int kGroupThreads = 1024;
 constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
 constexpr int kEpiWarps = 8;
@@ -76,15 +77,21 @@ constexpr int kMostParts = 8;
 constexpr int kMostPartials = 2 * kPairs;  // parts * tiles of all entries with several parts: see partials_of
 constexpr int kTile = 2 * kBM * kBN;       // fp32 values of a partial sum
 
+// A step's stage: from bf16 rows the operands A and B; from checkpoint rows B and
+// the bytes, which become an A in TMEM.
 template <bool CKPT> struct Ring {
-  static constexpr int stage = 2 * kOp + (CKPT ? kQ + kScale : 0);
-  static constexpr int stages = CKPT ? 4 : 6;
+  static constexpr int stage = kOp + (CKPT ? kQ + kScale : kOp);
+  static constexpr int stages = CKPT ? 7 : 6;
+  static constexpr int b0 = CKPT ? 0 : kOp;     // B within a stage
+  static constexpr int accs = CKPT ? 1 : 2;     // accumulators
+  static constexpr int chunk = CKPT ? 2 * kChunk : kChunk;
   static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * kStoreBox + 512;
   static_assert(smem <= 232448, "the ring must fit in 227 KB of shared memory");
+  static_assert(accs * kBN + (CKPT ? stages * kACols : 0) <= kTmemCols, "TMEM");
 };
 
 struct Smem {
-  uint64_t full[6], ready[6], empty[6], tfull[2], tempty[2], drain;
+  uint64_t full[8], ready[8], empty[8], tfull[2], tempty[2], drain;
   uint32_t tmem;
   int abort;
   int count;
@@ -304,6 +311,37 @@ __global__ void __launch_bounds__(kGroupThreads)
   }
 }
 
+// Four TMEM columns of A for 16 rows, eight times over (16x128b): thread T of the
+// warp writes register 2i to row T / 4, column 4i + T % 4, register 2i + 1 to
+// the row eight further.
+__device__ __forceinline__ void tc_st16x128(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+// The pair MMA with A (each CTA's 128 rows) in TMEM.
+__device__ __forceinline__ void tc_mma2_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                           uint32_t accumulate, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Four 8 x 8 matrices of 16-bit elements, transposed: thread T gets of each the
+// elements of column T / 4 in rows 2 (T % 4) and the next. Lane l gives the
+// address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+
 // Two signed bytes of w (chosen by sel) times a power of two, as two bf16.
 // The bytes are placed under 0x43 (bf16 128 + low seven bits, or 256 + ...
 // where the sign bit is set): v = 128 + low7, c = 128 or 256, v - c = q
@@ -317,9 +355,6 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bflo
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ void lds64(uint32_t addr, uint32_t& a, uint32_t& b) {
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-}
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
@@ -435,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = uniform(S->tmem);
+  const uint32_t tmem = uniform(S->tmem), a_ring = tmem + Ring<CKPT>::accs * kBN;
   const int nM = (H + 2 * kBM - 1) / (2 * kBM), nN = (Hp + kBN - 1) / kBN;
   const int tiles = nM * nN, count = uniform(S->count);
 
@@ -461,15 +496,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(bar, bytes);
             if (CKPT) {
               if (na > 0) {
-                tma_load_2d(st + 2 * kOp, &map_x, h0, row, bar);
-                tma_load_2d(st + 2 * kOp + kQ, &map_s, sx, row, bar);
+                tma_load_2d(st + kOp, &map_x, h0, row, bar);
+                tma_load_2d(st + kOp + kQ, &map_s, sx, row, bar);
               }
             } else {
               if (na > 0) tma_load_2d(st, &map_x, h0, row, bar);
               if (na > 1) tma_load_2d(st + kBox, &map_x, h0 + 64, row, bar);
             }
-            if (nb > 0) tma_load_2d(st + kOp, &map_dy, c0, row, bar);
-            if (nb > 1) tma_load_2d(st + kOp + kBox, &map_dy, c0 + 64, row, bar);
+            if (nb > 0) tma_load_2d(st + Ring<CKPT>::b0, &map_dy, c0, row, bar);
+            if (nb > 1) tma_load_2d(st + Ring<CKPT>::b0 + kBox, &map_dy, c0 + 64, row, bar);
           }
           __syncwarp();
           at.template next<kSt>();
@@ -485,9 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && leader) {
       // ---------------- MMA issuer (CTA 0 only) ----------------
       Pos at, acc;  // stage; accumulator
-      const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + kOp, kBox, 1024);
+      const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + Ring<CKPT>::b0, kBox, 1024);
       for_units(parts, count, tiles, [&](const Part& en, int t) {
-        const uint32_t idesc = Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc;
+        // A in TMEM has its rows in its lanes: not transposed (bit 15)
+        const uint32_t idesc = (Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc) & (CKPT ? ~(1u << 15) : ~0u);
         int steps = en.steps, in_chunk = 0;
         return for_steps(en, segs, [&](int, int left) {
           if (in_chunk == 0 &&
@@ -497,15 +533,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem + acc.s * kBN;
           const uint64_t ad = adesc + (at.s * kStage >> 4), bd = bdesc + (at.s * kStage >> 4);
-          const bool last = in_chunk == kChunk - 1 || steps == 1;
+          const uint32_t at_col = a_ring + at.s * kACols;
+          const bool last = in_chunk == Ring<CKPT>::chunk - 1 || steps == 1;
           if (elected()) {
             if (left > kBK - 16) {
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk)
-                tc_mma2(d, ad + kk * 128, bd + kk * 128, kk > 0 ? 1u : (uint32_t)in_chunk, idesc);
+              for (int kk = 0; kk < kBK / 16; ++kk) {
+                if (CKPT)
+                  tc_mma2_ta(d, at_col + kk * 8, bd + kk * 128, kk > 0 ? 1u : (uint32_t)in_chunk, idesc);
+                else
+                  tc_mma2(d, ad + kk * 128, bd + kk * 128, kk > 0 ? 1u : (uint32_t)in_chunk, idesc);
+              }
             } else {
-              for (int kk = 0; 16 * kk < left; ++kk)
-                tc_mma2(d, ad + kk * 128, bd + kk * 128, uint32_t(kk + in_chunk), idesc);
+              for (int kk = 0; 16 * kk < left; ++kk) {
+                if (CKPT)
+                  tc_mma2_ta(d, at_col + kk * 8, bd + kk * 128, uint32_t(kk + in_chunk), idesc);
+                else
+                  tc_mma2(d, ad + kk * 128, bd + kk * 128, uint32_t(kk + in_chunk), idesc);
+              }
             }
             tc_commit2_mc(smem_u32(&S->empty[at.s]), 3);
             if (last) tc_commit2_mc(smem_u32(&S->tfull[acc.s]), 3);
@@ -515,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           --steps;
           ++in_chunk;
           if (last) {
-            acc.template next<2>();
+            acc.template next<Ring<CKPT>::accs>();
             in_chunk = 0;
           }
           return true;
@@ -528,13 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- converter ----------------
-    // Thread t takes columns [8c, 8c + 8) and [64 + 8c, 64 + 8c + 8), c = t & 7,
-    // of four rows: two 8-byte reads and two 16-byte stores, chunk c of either
-    // operand box. All boxes are 128-byte swizzled. A quarter warp stores to
-    // the eight chunks of one row; a half warp reads half of two rows that
-    // differ in bit 2, whose swizzle puts them into different halves.
-    const int t = threadIdx.x - 128, c8 = t & 7;
-    const int row0 = (lane >> 4) + ((lane >> 3) & 1) * 4 + (warp & 1) * 2 + ((warp >> 1) & 1) * 8;
+    // Warp q makes the TMEM lanes [32q, 32q + 32) of A, 16 at a time. Of the
+    // bytes [64 rows][128 columns] (128-byte swizzled) it reads 8 rows x 16
+    // columns as an 8 x 8 matrix of byte pairs, transposed: a thread's word
+    // holds columns 2c and 2c + 1 (c = lane / 4) of two consecutive rows --
+    // and a TMEM word of A is two consecutive steps of K, here rows. So the
+    // bytes go from registers to TMEM without an exchange between threads
+    // or a way through shared memory. Column 2c becomes lane c of the 16,
+    // column 2c + 1 lane 8 + c: the epilogue puts the rows of D right.
+    const int t = threadIdx.x - 128, q4 = warp & 3;
     Pos at;
     for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h0 = tile / nN * 2 * kBM + rank * kBM;
@@ -543,43 +590,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!warp_wait(smem_u32(&S->full[at.s]), at.parity, abort_flag, status)) return false;
           const uint32_t st = base + at.s * kStage;
           const int valid = min(kBK, left), need = (valid + 15) & ~15;
-          if (CKPT) {
-            if (h0 < H) {
-              const uint32_t q = st + 2 * kOp, sc = q + kQ;
-              uint32_t v[4][4], sb[4];
+          if (CKPT && h0 < H) {
+            const uint32_t q = st + kOp, sc = q + kQ;
+            tc_fence_after();  // the MMAs that read this A last are done: `empty` let the producer go on
+            // lane l has the steps of rows 2l and 2l + 1 (0 for rows of the next group: q times 0)
+            uint32_t s0, s1;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s0) : "r"(sc + 2 * lane * 16 + sbyte));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s1) : "r"(sc + (2 * lane + 1) * 16 + sbyte));
+            s0 = 2 * lane >= valid ? 0u : s0 == (uint32_t)kCkptNan ? 0x7fffu : s0 << 7;
+            s1 = 2 * lane + 1 >= valid ? 0u : s1 == (uint32_t)kCkptNan ? 0x7fffu : s1 << 7;
+            const uint32_t pairs = s0 | s1 << 16;
+            uint32_t step[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 16 * i;
+            for (int i = 0; i < 8; ++i) step[i] = __shfl_sync(MEP_FULL_MASK, pairs, 4 * i + (lane & 3));
 #pragma unroll
-                for (int half = 0; half < 2; ++half)
-                  lds64(q + row * 128 + (((4 * half + (c8 >> 1)) ^ (row & 7)) << 4) + (c8 & 1) * 8,
-                        v[i][2 * half], v[i][2 * half + 1]);
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sb[i]) : "r"(sc + row * 16 + sbyte));
+            for (int half = 0; half < 2; ++half) {
+              uint32_t v[8], o[16];
+#pragma unroll
+              for (int i = 0; i < 8; i += 4) {
+                const int row = 8 * (i + (lane >> 3)) + (lane & 7);
+                ldsm4_trans(q + row * 128 + (((2 * q4 + half) ^ (row & 7)) << 4), v[i], v[i + 1], v[i + 2],
+                            v[i + 3]);
               }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 16 * i;
-                // rows of the next group: q times 0
-                const uint32_t bits =
-                    row < valid ? (sb[i] == (uint32_t)kCkptNan ? 0x7fffu : sb[i] << 7) * 0x10001u : 0u;
-                const __nv_bfloat162 step = *reinterpret_cast<const __nv_bfloat162*>(&bits);
-                const uint32_t dst = st + row * 128 + ((c8 ^ (row & 7)) << 4);
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                  sts128(dst + half * kBox, dequant2(v[i][2 * half], 0x4140, step),
-                         dequant2(v[i][2 * half], 0x4342, step),
-                         dequant2(v[i][2 * half + 1], 0x4140, step),
-                         dequant2(v[i][2 * half + 1], 0x4342, step));
+              for (int i = 0; i < 8; ++i) {
+                const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&step[i]);
+                o[2 * i] = dequant2(v[i], 0x4240, f);
+                o[2 * i + 1] = dequant2(v[i], 0x4341, f);
               }
+              tc_st16x128(a_ring + at.s * kACols + ((uint32_t)(32 * q4 + 16 * half) << 16), o);
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
           }
           if (valid < need)  // whole rows: the swizzle stays within a row
             for (int i = t; i < (need - valid) * 32; i += 128) {
               const int row = valid + (i >> 5), piece = i & 31;
-              if (CKPT && piece < 16) continue;
+              if (CKPT && piece >= 16) continue;  // there B alone lies in shared memory
               sts128(st + (piece >> 3) * kBox + row * 128 + ((piece & 7) << 4), 0u, 0u, 0u, 0u);
             }
-          if (CKPT || valid < need) fence_async_smem();
+          if (valid < need) fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->ready[at.s]), 0));
           at.template next<kSt>();
@@ -593,10 +643,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // columns [128 half, 128 half + 128) of the unit.
     const int q = warp & 3, half = (warp - 8) >> 2;
     const uint32_t box = out_box + (uint32_t)(warp - 8) * kStoreBox;
+    // the row of H, of these 32, in this lane: the converter's order
+    const int row = CKPT ? (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1) : lane;
     Pos at;
     for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h = tile / nN * 2 * kBM + rank * kBM + 32 * q, n = tile % nN * kBN + 128 * half;
-      const int chunks = (en.steps + kChunk - 1) / kChunk;
+      const int chunks = (en.steps + Ring<CKPT>::chunk - 1) / Ring<CKPT>::chunk;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
@@ -616,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[at.s]), 0));
-        at.template next<2>();
+        at.template next<Ring<CKPT>::accs>();
       }
       if ((en.of & 255) > 1 && h < H && n < Hp) {
         // This part's sums go to the workspace, in the order of the threads
@@ -657,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            sts128(box + lane * 128 + ((j ^ (lane & 7)) << 4), __float_as_uint(acc[32 * i + 4 * j]),
+            sts128(box + row * 128 + ((j ^ (row & 7)) << 4), __float_as_uint(acc[32 * i + 4 * j]),
                    __float_as_uint(acc[32 * i + 4 * j + 1]), __float_as_uint(acc[32 * i + 4 * j + 2]),
                    __float_as_uint(acc[32 * i + 4 * j + 3]));
           fence_async_smem();
