@@ -53,15 +53,9 @@ namespace {
 
 constexpr int kBM = 128;                 // rows of H per CTA
 constexpr int kBN = 256;                 // columns of H' per pair
-constexpr int kBK = 64;                  // buffer rows per step
-constexpr int kBox = kBK * 64 * 2;       // one 64 x 64 bf16 box, 8 KB
-constexpr int kOp = 2 * kBox;            // an operand's two boxes, 16 KB
-constexpr int kQ = kBK * kBM;            // checkpoint bytes of a step, 8 KB
-constexpr int kScale = kBK * 16;         // their scale bytes, in 16-byte rows
-constexpr int kChunk = MEP_WGRAD_CHUNK;  // steps summed in TMEM
+constexpr int kBK = 64;                  // buffer rows that the list of parts counts in
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 2 * kBN;
-constexpr int kACols = kBK / 2;          // TMEM columns of an A of one step
 constexpr int kGroupThreads = 1024;
 constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
 constexpr int kEpiWarps = 8;
@@ -77,17 +71,23 @@ constexpr int kMostParts = 8;
 constexpr int kMostPartials = 2 * kPairs;  // parts * tiles of all entries with several parts: see partials_of
 constexpr int kTile = 2 * kBM * kBN;       // fp32 values of a partial sum
 
-// A step's stage: from bf16 rows the operands A and B; from checkpoint rows B and
-// the bytes, which become an A in TMEM.
+// A step of K buffer rows and its stage: from bf16 rows the operands A and B;
+// from checkpoint rows B and the bytes, which become an A in TMEM. There a step
+// is 128 rows, as what it costs a converter to start one is spread further
+// (medium layer 847 -> 823 us; the bf16 form, which has more stages of 64,
+// 672 us against 694).
 template <bool CKPT> struct Ring {
-  static constexpr int stage = kOp + (CKPT ? kQ + kScale : kOp);
-  static constexpr int stages = CKPT ? 7 : 6;
-  static constexpr int b0 = CKPT ? 0 : kOp;     // B within a stage
-  static constexpr int accs = CKPT ? 1 : 2;     // accumulators
-  static constexpr int chunk = CKPT ? 2 * kChunk : kChunk;
+  static constexpr int K = CKPT ? 128 : 64;
+  static constexpr int box = K * 64 * 2, op = 2 * box;      // a bf16 box of 64 columns; an operand's two
+  static constexpr int q = K * kBM, scales = K * 16;        // checkpoint bytes; scale bytes, in 16-byte rows
+  static constexpr int stage = op + (CKPT ? q + scales : op), stages = CKPT ? 3 : 6;
+  static constexpr int b0 = CKPT ? 0 : op;                  // B within a stage
+  static constexpr int accs = CKPT ? 1 : 2;                 // accumulators
+  static constexpr int a_cols = K / 2;                      // TMEM columns of an A
+  static constexpr int chunk = MEP_WGRAD_CHUNK;             // steps summed in TMEM
   static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * kStoreBox + 512;
   static_assert(smem <= 232448, "the ring must fit in 227 KB of shared memory");
-  static_assert(accs * kBN + (CKPT ? stages * kACols : 0) <= kTmemCols, "TMEM");
+  static_assert(accs * kBN + (CKPT ? stages * a_cols : 0) <= kTmemCols, "TMEM");
 };
 
 struct Smem {
@@ -342,10 +342,12 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t& a, uint32_t
                : "memory");
 }
 
-// Two signed bytes of w (chosen by sel) times a power of two, as two bf16.
-// The bytes are placed under 0x43 (bf16 128 + low seven bits, or 256 + ...
-// where the sign bit is set): v = 128 + low7, c = 128 or 256, v - c = q
-// exactly, and q * step has 8 significant bits.
+// The four signed bytes of w times a power of two each, as bf16: bytes 0 and 2
+// by the halves of step, into even, bytes 1 and 3 into odd. A byte under 0x43
+// is bf16 128 + its low seven bits, or, where its sign bit falls into the
+// exponent, 256 + ...: v = 128 + low7, c = 128 or 256, v - c = q exactly, and
+// q * step has 8 significant bits. (A byte permutation first: masks on w
+// itself save an instruction and ran 6% slower.)
 __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bfloat162 step) {
   const uint32_t x = __byte_perm(w, 0x43434343u, sel);
   const uint32_t v = x & 0xff7fff7fu, c = x & 0xff80ff80u;
@@ -353,6 +355,10 @@ __device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bflo
                                    *reinterpret_cast<const __nv_bfloat162*>(&c));
   const __nv_bfloat162 r = __hmul2(q, step);
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void dequant4(uint32_t w, __nv_bfloat162 step, uint32_t& even, uint32_t& odd) {
+  even = dequant2(w, 0x4240, step);
+  odd = dequant2(w, 0x4341, step);
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -395,19 +401,22 @@ __device__ __forceinline__ void for_units(const int4* __restrict__ parts, int co
     u = nu;
   }
 }
-// The steps of one unit: f(first buffer row, rows left in the segment from it on) per step.
-template <typename F>
+// The steps of one unit, of up to K rows: f(first buffer row, rows left from it
+// on, whether it is the unit's last).
+template <int K, typename F>
 __device__ __forceinline__ bool for_steps(const Part& part, const int2* __restrict__ segs, F f) {
   int row = part.row, len = part.len, g = part.seg;
-  for (int steps = part.steps; steps > 0; --steps) {
+  for (int steps = part.steps; steps > 0;) {
     if (len <= 0) {
       const int2 seg = segs[++g];
       row = uniform(seg.x);
       len = uniform(seg.y);
     }
-    if (!f(row, len)) return false;
-    row += kBK;
-    len -= kBK;
+    const int left = min(len, steps * kBK);
+    steps -= K > kBK && left > kBK ? 2 : 1;
+    if (!f(row, left, steps == 0)) return false;
+    row += K;
+    len -= K;
   }
   return true;
 }
@@ -430,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  const __grid_constant__ CUtensorMap map_slot, const int* __restrict__ count_ptr,
                  const int4* __restrict__ parts, const int2* __restrict__ segs, int* __restrict__ arrived,
                  float4* __restrict__ partials, int32_t* status, int E, int H, int Hp, int accumulate) {
-  constexpr int kSt = Ring<CKPT>::stages, kStage = Ring<CKPT>::stage;
+  using Rg = Ring<CKPT>;
+  constexpr int kSt = Rg::stages, kStage = Rg::stage;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -470,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = uniform(S->tmem), a_ring = tmem + Ring<CKPT>::accs * kBN;
+  const uint32_t tmem = uniform(S->tmem), a_ring = tmem + Rg::accs * kBN;
   const int nM = (H + 2 * kBM - 1) / (2 * kBM), nN = (Hp + kBN - 1) / kBN;
   const int tiles = nM * nN, count = uniform(S->count);
 
@@ -487,24 +497,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = n0 + rank * (narrow ? 64 : 128);
         const int na = h0 >= H ? 0 : h0 + 64 < H ? 2 : 1;
         const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
-        const uint32_t bytes = (CKPT ? (na > 0 ? kQ + kScale : 0) : na * kBox) + nb * kBox;
+        const uint32_t bytes = (CKPT ? (na > 0 ? Rg::q + Rg::scales : 0) : na * Rg::box) + nb * Rg::box;
         const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
-        return for_steps(en, segs, [&](int row, int) {
+        return for_steps<Rg::K>(en, segs, [&](int row, int, bool) {
           if (!warp_wait(smem_u32(&S->empty[at.s]), at.parity ^ 1u, abort_flag, status)) return false;
           const uint32_t bar = smem_u32(&S->full[at.s]), st = base + at.s * kStage;
           if (elected()) {
             mbar_expect_tx(bar, bytes);
             if (CKPT) {
               if (na > 0) {
-                tma_load_2d(st + kOp, &map_x, h0, row, bar);
-                tma_load_2d(st + kOp + kQ, &map_s, sx, row, bar);
+                tma_load_2d(st + Rg::op, &map_x, h0, row, bar);
+                tma_load_2d(st + Rg::op + Rg::q, &map_s, sx, row, bar);
               }
             } else {
               if (na > 0) tma_load_2d(st, &map_x, h0, row, bar);
-              if (na > 1) tma_load_2d(st + kBox, &map_x, h0 + 64, row, bar);
+              if (na > 1) tma_load_2d(st + Rg::box, &map_x, h0 + 64, row, bar);
             }
-            if (nb > 0) tma_load_2d(st + Ring<CKPT>::b0, &map_dy, c0, row, bar);
-            if (nb > 1) tma_load_2d(st + Ring<CKPT>::b0 + kBox, &map_dy, c0 + 64, row, bar);
+            if (nb > 0) tma_load_2d(st + Rg::b0, &map_dy, c0, row, bar);
+            if (nb > 1) tma_load_2d(st + Rg::b0 + Rg::box, &map_dy, c0 + 64, row, bar);
           }
           __syncwarp();
           at.template next<kSt>();
@@ -520,12 +530,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1 && leader) {
       // ---------------- MMA issuer (CTA 0 only) ----------------
       Pos at, acc;  // stage; accumulator
-      const uint64_t adesc = sdesc(base, kBox, 1024), bdesc = sdesc(base + Ring<CKPT>::b0, kBox, 1024);
+      const uint64_t adesc = sdesc(base, Rg::box, 1024), bdesc = sdesc(base + Rg::b0, Rg::box, 1024);
       for_units(parts, count, tiles, [&](const Part& en, int t) {
         // A in TMEM has its rows in its lanes: not transposed (bit 15)
         const uint32_t idesc = (Hp - t % nN * kBN <= 128 ? kIdescN : kIdesc) & (CKPT ? ~(1u << 15) : ~0u);
-        int steps = en.steps, in_chunk = 0;
-        return for_steps(en, segs, [&](int, int left) {
+        int in_chunk = 0;
+        return for_steps<Rg::K>(en, segs, [&](int, int left, bool end) {
           if (in_chunk == 0 &&
               !warp_wait(smem_u32(&S->tempty[acc.s]), acc.parity ^ 1u, abort_flag, status))
             return false;
@@ -533,12 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           const uint32_t d = tmem + acc.s * kBN;
           const uint64_t ad = adesc + (at.s * kStage >> 4), bd = bdesc + (at.s * kStage >> 4);
-          const uint32_t at_col = a_ring + at.s * kACols;
-          const bool last = in_chunk == Ring<CKPT>::chunk - 1 || steps == 1;
+          const uint32_t at_col = a_ring + at.s * Rg::a_cols;
+          const bool last = in_chunk == Rg::chunk - 1 || end;
           if (elected()) {
-            if (left > kBK - 16) {
+            if (left > Rg::K - 16) {
 #pragma unroll
-              for (int kk = 0; kk < kBK / 16; ++kk) {
+              for (int kk = 0; kk < Rg::K / 16; ++kk) {
                 if (CKPT)
                   tc_mma2_ta(d, at_col + kk * 8, bd + kk * 128, kk > 0 ? 1u : (uint32_t)in_chunk, idesc);
                 else
@@ -557,10 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           at.template next<kSt>();
-          --steps;
           ++in_chunk;
           if (last) {
-            acc.template next<Ring<CKPT>::accs>();
+            acc.template next<Rg::accs>();
             in_chunk = 0;
           }
           return true;
@@ -586,39 +595,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h0 = tile / nN * 2 * kBM + rank * kBM;
       const uint32_t sbyte = (uint32_t)(h0 / kCkptBlock) & 15u;
-      return for_steps(en, segs, [&](int, int left) {
+      return for_steps<Rg::K>(en, segs, [&](int, int left, bool) {
           if (!warp_wait(smem_u32(&S->full[at.s]), at.parity, abort_flag, status)) return false;
           const uint32_t st = base + at.s * kStage;
-          const int valid = min(kBK, left), need = (valid + 15) & ~15;
+          const int valid = min(Rg::K, left), need = (valid + 15) & ~15;
           if (CKPT && h0 < H) {
-            const uint32_t q = st + kOp, sc = q + kQ;
+            const uint32_t q = st + Rg::op, sc = q + Rg::q;
             tc_fence_after();  // the MMAs that read this A last are done: `empty` let the producer go on
             // lane l has the steps of rows 2l and 2l + 1 (0 for rows of the next group: q times 0)
-            uint32_t s0, s1;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s0) : "r"(sc + 2 * lane * 16 + sbyte));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s1) : "r"(sc + (2 * lane + 1) * 16 + sbyte));
-            s0 = 2 * lane >= valid ? 0u : s0 == (uint32_t)kCkptNan ? 0x7fffu : s0 << 7;
-            s1 = 2 * lane + 1 >= valid ? 0u : s1 == (uint32_t)kCkptNan ? 0x7fffu : s1 << 7;
-            const uint32_t pairs = s0 | s1 << 16;
-            uint32_t step[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) step[i] = __shfl_sync(MEP_FULL_MASK, pairs, 4 * i + (lane & 3));
+            for (int k0 = 0; k0 < Rg::K; k0 += 64) {
+              if (k0 >= valid) break;
+              uint32_t s0, s1, v[16];
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s0) : "r"(sc + (k0 + 2 * lane) * 16 + sbyte));
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s1) : "r"(sc + (k0 + 2 * lane + 1) * 16 + sbyte));
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t v[8], o[16];
-#pragma unroll
-              for (int i = 0; i < 8; i += 4) {
-                const int row = 8 * (i + (lane >> 3)) + (lane & 7);
-                ldsm4_trans(q + row * 128 + (((2 * q4 + half) ^ (row & 7)) << 4), v[i], v[i + 1], v[i + 2],
+              for (int i = 0; i < 16; i += 4) {  // eight words for either 16 columns
+                const int row = k0 + 8 * ((i & 7) + (lane >> 3)) + (lane & 7);
+                ldsm4_trans(q + row * 128 + (((2 * q4 + (i >> 3)) ^ (row & 7)) << 4), v[i], v[i + 1], v[i + 2],
                             v[i + 3]);
               }
+              s0 = k0 + 2 * lane >= valid ? 0u : s0 == (uint32_t)kCkptNan ? 0x7fffu : s0 << 7;
+              s1 = k0 + 2 * lane + 1 >= valid ? 0u : s1 == (uint32_t)kCkptNan ? 0x7fffu : s1 << 7;
+              const uint32_t pairs = s0 | s1 << 16;
+              uint32_t step[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&step[i]);
-                o[2 * i] = dequant2(v[i], 0x4240, f);
-                o[2 * i + 1] = dequant2(v[i], 0x4341, f);
+              for (int i = 0; i < 8; ++i) step[i] = __shfl_sync(MEP_FULL_MASK, pairs, 4 * i + (lane & 3));
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t o[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162*>(&step[i]);
+                  dequant4(v[8 * half + i], f, o[2 * i], o[2 * i + 1]);
+                }
+                tc_st16x128(a_ring + at.s * Rg::a_cols + k0 / 2 + ((uint32_t)(32 * q4 + 16 * half) << 16), o);
               }
-              tc_st16x128(a_ring + at.s * kACols + ((uint32_t)(32 * q4 + 16 * half) << 16), o);
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
@@ -627,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = t; i < (need - valid) * 32; i += 128) {
               const int row = valid + (i >> 5), piece = i & 31;
               if (CKPT && piece >= 16) continue;  // there B alone lies in shared memory
-              sts128(st + (piece >> 3) * kBox + row * 128 + ((piece & 7) << 4), 0u, 0u, 0u, 0u);
+              sts128(st + (piece >> 3) * Rg::box + row * 128 + ((piece & 7) << 4), 0u, 0u, 0u, 0u);
             }
           if (valid < need) fence_async_smem();
           __syncwarp();
@@ -648,11 +660,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     Pos at;
     for_units(parts, count, tiles, [&](const Part& en, int tile) {
       const int h = tile / nN * 2 * kBM + rank * kBM + 32 * q, n = tile % nN * kBN + 128 * half;
-      const int chunks = (en.steps + Ring<CKPT>::chunk - 1) / Ring<CKPT>::chunk;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int c = 0; c < chunks; ++c) {
+      int in_chunk = 0;
+      const bool ok = for_steps<Rg::K>(en, segs, [&](int, int, bool end) {
+        if (++in_chunk < Rg::chunk && !end) return true;
+        in_chunk = 0;
         if (!warp_wait(smem_u32(&S->tfull[at.s]), at.parity, abort_flag, status)) return false;
         tc_fence_after();
         const uint32_t ta = tmem + at.s * kBN + 128 * half + ((uint32_t)(32 * q) << 16);
@@ -668,8 +682,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(map_to_rank(smem_u32(&S->tempty[at.s]), 0));
-        at.template next<Ring<CKPT>::accs>();
-      }
+        at.template next<Rg::accs>();
+        return true;
+      });
+      if (!ok) return false;
       if ((en.of & 255) > 1 && h < H && n < Hp) {
         // This part's sums go to the workspace, in the order of the threads
         // that will read them; the warp that comes last adds up all parts', in
@@ -826,7 +842,8 @@ long long tiles_of(int H, int Hp) {
 }
 // Partial sums at most: an entry of s steps is cut into at most s / most + 1 <=
 // 2 s / most parts, and most >= steps * tiles / kPairs over all entries; only
-// entries of more than kLeastSteps steps are cut, into at most s / 8 parts; and every segment of rows has one step that is not full.
+// entries of more than kLeastSteps steps are cut, into at most s / 8 parts; and
+// every segment of rows has one step that is not full.
 long long partials_of(int R, long long rows, int G, int H, int Hp) {
   const long long segments = rows < (long long)R * G ? rows : (long long)R * G;
   const long long steps = rows / kBK + segments;
@@ -890,14 +907,15 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   mx = ms = md = mh;  // never used without rows
   if (rows > 0) {
     const unsigned long long rb = ckpt_row_bytes(H);
-    bool ok = map_2d(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, rows, Hp, 2ull * Hp, 64, kBK,
+    bool ok = map_2d(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, rows, Hp, 2ull * Hp, 64, x_type == MEP_CKPT8 ? Ring<true>::K : Ring<false>::K,
                      CU_TENSOR_MAP_SWIZZLE_128B);
     if (x_type == MEP_CKPT8)
       ok = ok &&
-           map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, H, rb, kBM, kBK, CU_TENSOR_MAP_SWIZZLE_128B) &&
-           map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, rb, rb, 16, kBK, CU_TENSOR_MAP_SWIZZLE_NONE);
+           map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, H, rb, kBM, Ring<true>::K, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           map_2d(&ms, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, rb, rb, 16, Ring<true>::K,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
     else
-      ok = ok && map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, rows, H, 2ull * H, 64, kBK,
+      ok = ok && map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, rows, H, 2ull * H, 64, Ring<false>::K,
                         CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return MEP_ERR_CUDA;
   }
