@@ -171,6 +171,7 @@ template <> struct Pack<MEP_BF16> {
   __device__ __forceinline__ F2 at(int j) const {  // values 2j and 2j + 1
     return widen(w[j]);
   }
+  __device__ __forceinline__ F2 plus(int j, F2 c) const { return add2(at(j), c); }  // at(j) + c
   __device__ __forceinline__ uint32_t top() const { return top_of(w); }
   __device__ __forceinline__ void clear() { w[0] = w[1] = w[2] = w[3] = 0u; }
 };
@@ -195,6 +196,7 @@ template <> struct Pack<MEP_F32> {
     }
   }
   __device__ __forceinline__ F2 at(int j) const { return pair(v[2 * j], v[2 * j + 1]); }
+  __device__ __forceinline__ F2 plus(int j, F2 c) const { return add2(at(j), c); }
   __device__ __forceinline__ uint32_t top() const {
     const F2 a[4] = {at(0), at(1), at(2), at(3)};
     return top_of(a);
@@ -225,11 +227,13 @@ template <> struct Pack<MEP_CKPT8> {
     }
     step = in ? ckpt_step(__ldg(p + ckpt_scale_at(C) + block)) : 0.f;
   }
-  __device__ __forceinline__ F2 at(int j) const {
+  __device__ __forceinline__ F2 q(int j) const {
     const uint32_t u = w[j >> 1] ^ 0x80808080u;
     const int b = 2 * (j & 1);
-    return mul2(add2(pair(ckpt_byte(u, b), ckpt_byte(u, b + 1)), both(-8388736.f)), both(step));
+    return add2(pair(ckpt_byte(u, b), ckpt_byte(u, b + 1)), both(-8388736.f));
   }
+  __device__ __forceinline__ F2 at(int j) const { return mul2(q(j), both(step)); }
+  __device__ __forceinline__ F2 plus(int j, F2 c) const { return fma2(q(j), both(step), c); }
   __device__ __forceinline__ void clear() { w[0] = w[1] = 0u, step = 0.f; }
 };
 

@@ -167,26 +167,27 @@ template <int KIND> struct Slot {
   }
 };
 
-// MAXT is the number of threads of an SM: 512 with 128 registers each, in
-// CTAs of up to 512, or 1024 with 64 for the backward pass of rows of more than
-// 8192 columns.
-template <int KIND, int J, int U, int MAXT> __host__ __device__ constexpr int norm_ahead() {
-  return ahead_of(U * J * Slot<KIND>::bytes, 196608 / MAXT);
+// An SM has 512 threads with 128 registers each, in CTAs of up to 512: what they
+// wait for is copied ahead, and more of them with fewer registers issued more
+// for the same work (backward [65536, 7168]: 434 us, 665 with 896 threads).
+constexpr int kSmThreads = 512;
+template <int KIND, int J, int U> __host__ __device__ constexpr int norm_ahead() {
+  return ahead_of(U * J * Slot<KIND>::bytes, 196608 / kSmThreads);
 }
-template <int KIND, int XKIND, int J, int U, int MAXT> __host__ __device__ constexpr int dx_ahead() {
-  return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / MAXT);
+template <int KIND, int XKIND, int J, int U> __host__ __device__ constexpr int dx_ahead() {
+  return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / kSmThreads);
 }
 
 // J blocks a half warp, W warps a row (2 J W >= blocks of a row; FULL: equal,
 // and no block is cut), U rows a turn, KEEP: a checkpoint is written.
-template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U>
+__global__ void __launch_bounds__(kSmThreads)
     k_norm(const T* __restrict__ x, const void* __restrict__ w, const void* __restrict__ b, int p_type,
            float eps, unsigned N, int H, int W, T* __restrict__ y, float* __restrict__ mean,
            float* __restrict__ rstd, uint8_t* __restrict__ x_ckpt, uint8_t* __restrict__ y_ckpt) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int A = norm_ahead<KIND, J, U, MAXT>();
+  constexpr int A = norm_ahead<KIND, J, U>();
   extern __shared__ __align__(16) float s_dyn[];  // slots
   __shared__ float2 s_part[2][kMaxWarps * 2];     // two rows' mean and squares of a warp, twice
   const int l = threadIdx.x % kHalf;
@@ -372,14 +373,14 @@ __global__ void __launch_bounds__(MAXT)
   }
 }
 
-template <typename T, int KIND, int XKIND, bool VEC, int J, int U, int MAXT>
-__global__ void __launch_bounds__(MAXT)
+template <typename T, int KIND, int XKIND, bool VEC, int J, int U>
+__global__ void __launch_bounds__(kSmThreads)
     k_norm_dx(const T* __restrict__ dy, const void* __restrict__ x, const void* __restrict__ w,
               int p_type, const float* __restrict__ mean, const float* __restrict__ rstd, unsigned N,
               int H, int W, T* __restrict__ dx, float* __restrict__ ws) {
   pdl_wait();
   pdl_launch_dependents();
-  constexpr int A = dx_ahead<KIND, XKIND, J, U, MAXT>();
+  constexpr int A = dx_ahead<KIND, XKIND, J, U>();
   extern __shared__ __align__(16) float s_dyn[];  // slots; at the end the groups' column sums
   __shared__ float s_sum[2][kMaxWarps * 2 * U];
   const int l = threadIdx.x % kHalf;
@@ -387,12 +388,17 @@ __global__ void __launch_bounds__(MAXT)
   const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
   const int threads = blockDim.x;
   const float inv_h = 1.f / H;
-  F2 dw[J][4], db[J][4], wv[J][4];
+  // the weight stays in registers up to two blocks a half warp
+  F2 dw[J][4], db[J][4], held_w[J > 2 ? 1 : J][4];
   bool there[J];
+  const auto weight = [&](int i) -> const F2(&)[4] {
+    if (J > 2) load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, held_w[0]);
+    return held_w[J > 2 ? 0 : i];
+  };
 #pragma unroll
   for (int i = 0; i < J; ++i) {
     there[i] = half_col<VEC>(half + 2 * W * i, l, 0) < H;
-    load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, wv[i]);
+    if (J <= 2) load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, held_w[J > 2 ? 0 : i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = both(0.f);
   }
@@ -488,10 +494,11 @@ __global__ void __launch_bounds__(MAXT)
           Pack<KIND> d;
           Pack<XKIND> p;
           fetch(u, i, d, p);
+          const F2(&wv)[4] = weight(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             // (x - mean) first: exact where the row is far from zero
-            const F2 g = d.at(j), xhat = mul2(add2(p.at(j), k0), k1), t = mul2(g, wv[i][j]);
+            const F2 g = d.at(j), xhat = mul2(p.plus(j, k0), k1), t = mul2(g, wv[j]);
             s1 = add2(s1, t);
             s2 = fma2(t, xhat, s2);
             dw[i][j] = fma2(g, xhat, dw[i][j]);
@@ -514,10 +521,11 @@ __global__ void __launch_bounds__(MAXT)
           Pack<KIND> d;
           Pack<XKIND> p;
           fetch(u, i, d, p);
+          const F2(&wv)[4] = weight(i);
           F2 v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            v[j] = fma2(add2(p.at(j), k0), c, fma2(mul2(d.at(j), wv[i][j]), k1, a));
+            v[j] = fma2(p.plus(j, k0), c, fma2(mul2(d.at(j), wv[j]), k1, a));
           store8<T, VEC>(out + (long long)u * H, H, half + 2 * W * i, l, v);
         }
       }
@@ -603,7 +611,7 @@ int allow_smem(const void* kernel, int bytes) {
 // How a row is laid out: J blocks a half warp, W warps a row, U rows a turn,
 // `groups` rows' worth of warps in a CTA.
 struct Shape {
-  int J, U, W, groups, threads, maxt, parts;
+  int J, U, W, groups, threads, parts;
 };
 Shape shape_of(long long N, int H, int J, int U) {
   Shape s;
@@ -614,28 +622,28 @@ Shape shape_of(long long N, int H, int J, int U) {
   s.groups = s.W >= 16 ? 1 : 16 / s.W;
   while (s.groups > 1 && N < 152ll * U * s.groups) s.groups /= 2;
   s.threads = 32 * s.W * s.groups;
-  s.maxt = s.threads <= 512 ? 512 : 1024;
   return s;
 }
-// Two rows a turn where a slot of 128 bytes a thread holds them: in bf16, up to
-// 512 threads a row. The number of CTAs must not depend on the device: the
+// Blocks a half warp: one or two, and four for rows of more than 8192 columns.
+int blocks_of(int H) { return H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4; }
+// Two rows a turn in bf16, whose slots are half as wide, where there are
+// registers for them. The number of CTAs must not depend on the device: the
 // workspace is sized by it.
 Shape backward_shape(long long N, int H, int type) {
-  const int J = H > 2 * kCkptBlock ? 2 : 1;
-  const int U = type == MEP_BF16 && H % 8 == 0 && H <= 64 * kCkptBlock ? 2 : 1;
-  Shape s = shape_of(N, H, J, U);
-  const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups), cap = 152 * (s.maxt / s.threads);
+  const int J = blocks_of(H);
+  Shape s = shape_of(N, H, J, type == MEP_BF16 && H % 8 == 0 && J <= 2 ? 2 : 1);
+  const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups), cap = 152 * (kSmThreads / s.threads);
   s.parts = want < cap ? want : cap;
   return s;
 }
 
-template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U, int MAXT>
+template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U>
 cudaError_t run_norm(const Shape& s, const void* x, const void* w, const void* b, int p_type, float eps,
                      unsigned N, int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                      cudaStream_t st) {
-  const int want = ceil_div(N, s.groups * U), cap = sm_count() * (MAXT / s.threads);
-  const int smem = VEC ? norm_ahead<KIND, J, U, MAXT>() * U * J * s.threads * Slot<KIND>::bytes : 0;
-  const auto kernel = k_norm<T, KIND, VEC, FULL, KEEP, J, U, MAXT>;
+  const int want = ceil_div(N, s.groups * U), cap = sm_count() * (kSmThreads / s.threads);
+  const int smem = VEC ? norm_ahead<KIND, J, U>() * U * J * s.threads * Slot<KIND>::bytes : 0;
+  const auto kernel = k_norm<T, KIND, VEC, FULL, KEEP, J, U>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(want < cap ? want : cap), dim3(s.threads), smem, st,
                     static_cast<const T*>(x), w, b, p_type, eps, N, H, s.W, static_cast<T*>(y), mean,
@@ -647,30 +655,30 @@ cudaError_t pick_norm(const void* x, const void* w, const void* b, int p_type, f
                       int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                       cudaStream_t st) {
   constexpr int U = KIND == MEP_BF16 ? 2 : 1;
-  const int J = H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4;
+  const int J = blocks_of(H);
   const Shape s = shape_of(N, H, J, U);
   // Without the edge and checkpoint tests the forward pass issues a fifth less
   // ([32768, 2048] 61 -> 51 us, [65536, 7168] 404 -> 334 us); the backward
   // pass, which waits for memory, ran the same either way.
   const bool full = VEC && H == s.W * 2 * J * kCkptBlock, keep = xc != nullptr || yc != nullptr;
-  const auto run = J == 1   ? run_norm<T, KIND, VEC, false, true, 1, U, 512>
-                   : J == 4 ? run_norm<T, KIND, VEC, false, true, 4, U, 512>
-                   : full   ? (keep ? run_norm<T, KIND, VEC, VEC, true, 2, U, 512>
-                                    : run_norm<T, KIND, VEC, VEC, false, 2, U, 512>)
-                            : run_norm<T, KIND, VEC, false, true, 2, U, 512>;
+  const auto run = J == 1   ? run_norm<T, KIND, VEC, false, true, 1, U>
+                   : J == 4 ? run_norm<T, KIND, VEC, false, true, 4, U>
+                   : full   ? (keep ? run_norm<T, KIND, VEC, VEC, true, 2, U>
+                                    : run_norm<T, KIND, VEC, VEC, false, 2, U>)
+                            : run_norm<T, KIND, VEC, false, true, 2, U>;
   return run(s, x, w, b, p_type, eps, N, H, y, mean, rstd, xc, yc, st);
 }
 
-template <typename T, int KIND, int XKIND, bool VEC, int J, int U, int MAXT>
+template <typename T, int KIND, int XKIND, bool VEC, int J, int U>
 cudaError_t run_dx(const Shape& s, const void* dy, const void* x, const void* w, int p_type,
                    const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                    cudaStream_t st) {
   const int threads = s.threads;
-  const int slots = VEC ? dx_ahead<KIND, XKIND, J, U, MAXT>() * U * J * threads *
+  const int slots = VEC ? dx_ahead<KIND, XKIND, J, U>() * U * J * threads *
                               (Slot<KIND>::bytes + Slot<XKIND>::bytes)
                         : 0;
   const int join = s.groups > 1 ? 2 * threads * 8 * J * 4 : 0, smem = slots > join ? slots : join;
-  const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U, MAXT>;
+  const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(s.parts), dim3(threads), smem, st, static_cast<const T*>(dy), x, w,
                     p_type, mean, rstd, N, H, s.W, static_cast<T*>(dx), ws);
@@ -680,10 +688,10 @@ template <typename T, int KIND, int XKIND, bool VEC>
 cudaError_t pick_dx(const Shape& s, const void* dy, const void* x, const void* w, int p_type,
                     const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                     cudaStream_t st) {
-  constexpr int U = KIND == MEP_BF16 && VEC ? 2 : 1;  // backward_shape's, up to 512 threads
-  const auto run = s.J == 1         ? run_dx<T, KIND, XKIND, VEC, 1, U, 512>
-                   : s.maxt == 1024 ? run_dx<T, KIND, XKIND, VEC, 2, 1, 1024>
-                                    : run_dx<T, KIND, XKIND, VEC, 2, U, 512>;
+  constexpr int U = KIND == MEP_BF16 && VEC ? 2 : 1;  // as backward_shape has it
+  const auto run = s.J == 1   ? run_dx<T, KIND, XKIND, VEC, 1, U>
+                   : s.J == 2 ? run_dx<T, KIND, XKIND, VEC, 2, U>
+                              : run_dx<T, KIND, XKIND, VEC, 4, 1>;
   return run(s, dy, x, w, p_type, mean, rstd, N, H, dx, ws, st);
 }
 
