@@ -19,26 +19,43 @@
 //                   a group is long next to all the work, the longest first;
 //   k_wgrad_pair    persistent clusters of two CTAs, one per SM, 512 threads
 //                   each, over units (part of a weight row's group, 256 rows
-//                   of H, 256 columns of H'), to and fro over the pairs. CTA r of a pair owns 128 of the 256
-//                   rows of H. Per step of 64 buffer rows:
-//     warp 0      TMA producer: this CTA's 128 columns of x (bf16 boxes, or
-//                 the checkpoint's bytes and their 64 scale bytes) and its
-//                 half of the 256 columns of dy, into a ring of stages;
-//     warps 4..7  converter: checkpoint bytes to bf16 operand boxes (exact:
+//                   of H, 256 columns of H'), to and fro over the pairs. CTA r
+//                   of a pair owns 128 of the 256 rows of H. Per step of 64
+//                   buffer rows (128 from checkpoint rows):
+//     warp 0      TMA producer: its half of the 256 columns of dy and this
+//                 CTA's 128 columns of x (bf16 boxes, or the checkpoint's bytes
+//                 and the rows' scale bytes), into a ring of stages;
+//     warps 4..7  converter: checkpoint bytes to a bf16 operand A in TMEM (exact:
 //                 q * 2^k has 8 significant bits), and zeros over the rows
 //                 that a segment's last step takes from the next group, in
 //                 both operands (a NaN there would survive a product with 0);
 //     warp 1      of CTA 0 issues the pair MMAs (tcgen05.mma.cta_group::2,
-//                 M = 256, N = 256 or 128, K = 16) into one of two TMEM
-//                 accumulators, which changes every kChunk steps;
-//     warps 8..15 add each finished accumulator to fp32 sums in registers
-//                 (128 a thread), and at the end of the unit write them
-//                 through shared memory with bulk tensor stores, or bulk
-//                 tensor additions.
-// The sums leave TMEM every kChunk * 64 rows because the tensor cores do not
-// round their fp32 additions to nearest: over a long group the error of one
-// accumulator grows with the number of steps, that of the registers' sums,
-// rounded to nearest, with its root.
+//                 M = 256, N = 256 or 128, K = 16; A from shared memory, or
+//                 from TMEM) into an accumulator in TMEM: one of two in turn,
+//                 or the only one where A takes the room of the other;
+//     warps 8..15 add each accumulator, once Ring::chunk steps are in it, to
+//                 fp32 sums in registers (128 a thread), and at the end of
+//                 the unit write them through shared memory with bulk tensor
+//                 stores, or bulk tensor additions.
+//
+// Why the sums leave TMEM: the tensor cores do not round their fp32 additions
+// to nearest, and the error of one accumulator grows with the number of
+// steps. Over some 3000 rows of normal bf16 values it was 3.2e-6 of the result
+// with a single accumulator, and 0.9, 0.5 and 0.2e-6 with sums moved (and then
+// rounded to nearest) every 1024, 512 and 256 rows; fp32 products are off by
+// 0.2 to 0.4e-6. 512 cost 3% over 1024 and saves 6% over 256. A checkpoint's
+// bytes have fewer bits to lose: 0.2e-6 at 1024.
+//
+// What bounds it. From bf16 rows the feed: per step an SM takes in 32 KB and
+// its MMAs read as much of shared memory, all of its 128 bytes a cycle. The
+// medium layer ([196608, 2048] x [196608, 1408], 67 groups) takes 672 to 702
+// us by the box, 1614 to 1688 TFLOP/s, against 1694 to 1739 of a dense library
+// product of the same size. From checkpoint rows the converter, whose 160
+// integer and bf16 instructions a step and warp nothing else can share: 823
+// us, 1377 TFLOP/s (with them left out, 680). Its first form wrote the operand
+// to shared memory (940 us: 82 KB a step through shared memory, where it is
+// now half that). Waiting with short tries cost 7%, addresses in ordinary
+// instead of uniform registers 4%, a release at cluster scope per step half.
 // Every wait is bounded as in grouped_gemm.cu.
 
 #include "ckpt.cuh"
