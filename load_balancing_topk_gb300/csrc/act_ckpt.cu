@@ -62,10 +62,10 @@ __global__ void __launch_bounds__(kThreads)
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    F2 v[4];
+    Kept<1> k{{ckpt + w[u].row * ckpt_row_bytes(C)}, {w[u].block}, {w[u].in}, {p[u].top()}};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = p[u].at(j);
-    save8<VEC>(ckpt + w[u].row * ckpt_row_bytes(C), C, w[u].block, l, w[u].in, p[u].top(), v);
+    for (int j = 0; j < 4; ++j) k.v[0][j] = p[u].at(j);
+    save8<VEC>(k, C, l);
   }
 }
 
@@ -116,19 +116,24 @@ __global__ void __launch_bounds__(kThreads)
     }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    F2 v[2][4], o[4];
+    F2 o[4];
+    Kept<2> k;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[0][j] = p[u][0].at(j);
-      v[1][j] = p[u][1].at(j);
-      o[j] = mul2(mul2(v[0][j], sigmoid2(v[0][j])), v[1][j]);
+      k.v[0][j] = p[u][0].at(j);
+      k.v[1][j] = p[u][1].at(j);
+      o[j] = mul2(mul2(k.v[0][j], sigmoid2(k.v[0][j])), k.v[1][j]);
     }
     if (w[u].in) store8<__nv_bfloat16, VEC>(a + w[u].row * F, F, w[u].block, l, o);
     if (CKPT) {
-      save8<VEC>(ckpt + 2 * w[u].row * ckpt_row_bytes(F), F, w[u].block, l, w[u].in,
-                 p[u][0].top(), v[0]);
-      save8<VEC>(ckpt + (2 * w[u].row + 1) * ckpt_row_bytes(F), F, w[u].block, l, w[u].in,
-                 p[u][1].top(), v[1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        k.row[h] = ckpt + (2 * w[u].row + h) * ckpt_row_bytes(F);
+        k.block[h] = w[u].block;
+        k.in[h] = w[u].in;
+        k.top[h] = p[u][h].top();
+      }
+      save8<VEC>(k, F, l);
     }
   }
 }

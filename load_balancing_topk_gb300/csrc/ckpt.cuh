@@ -92,23 +92,12 @@ __device__ __forceinline__ F2 widen(uint32_t w) {
   return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// Four pairs of values as eight bytes. x * 2^-k + 1.5 * 2^23 in one rounding
-// leaves x * 2^-k rounded to nearest-even in the low bits (a conversion
-// instruction runs at an eighth of the rate). Only a block whose largest value
-// is at least 127.5 steps can round to 128: `full`, one in a hundred. In a
-// block with s = 255 every finite value becomes 0 (times 0), the others some
+// x * 2^-k + 1.5 * 2^23 in one rounding leaves x * 2^-k rounded to nearest-even
+// in the low bits (a conversion instruction runs at an eighth of the rate). In
+// a block with s = 255 every finite value becomes 0 (times 0), the others some
 // byte that is never read as a value.
-__device__ __forceinline__ uint2 ckpt_pack8(const F2 (&v)[4], float inv_step, bool full) {
-  F2 r[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = fma2(v[j], both(inv_step), both(12582912.f));
-  if (full) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r[j] = pair(fminf(fmaxf(r[j].x(), 12582912.f - 127.f), 12582912.f + 127.f),
-                  fminf(fmaxf(r[j].y(), 12582912.f - 127.f), 12582912.f + 127.f));
-    }
-  }
+constexpr float kRound = 12582912.f;
+__device__ __forceinline__ uint2 ckpt_bytes(const F2 (&r)[4]) {
   uint32_t q[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) q[j] = __byte_perm(uint32_t(r[j].v), uint32_t(r[j].v >> 32), 0x0040);
@@ -142,11 +131,6 @@ __device__ __forceinline__ uint32_t top_of(const F2 (&v)[4]) {
 __device__ __forceinline__ uint32_t top_of(const uint32_t (&w)[4]) {
   const F2 v[4] = {widen(w[0]), widen(w[1]), widen(w[2]), widen(w[3])};
   return top_of(v);
-}
-__device__ __forceinline__ uint32_t half_top(uint32_t t) {
-#pragma unroll
-  for (int d = 8; d >= 1; d >>= 1) t = max(t, __shfl_xor_sync(MEP_FULL_MASK, t, d));
-  return t;
 }
 
 // Eight values of a row as they lie in memory (columns beyond C are 0).
@@ -238,9 +222,10 @@ template <> struct Pack<MEP_CKPT8> {
 };
 
 // Four pairs of values into the row at p, rounded to its type (FULL: the block
-// is known to lie within the row); v becomes what was stored. Returns the bits of its largest magnitude.
+// is known to lie within the row; `in`: there is such a row); v becomes what
+// was stored. Returns the bits of its largest magnitude.
 template <typename T, bool VEC, bool FULL = false>
-__device__ __forceinline__ uint32_t store8(T* p, int C, int block, int l, F2 (&v)[4]) {
+__device__ __forceinline__ uint32_t store8(T* p, int C, int block, int l, F2 (&v)[4], bool in = true) {
   if (sizeof(T) == 2) {
     uint32_t o[4];
 #pragma unroll
@@ -251,19 +236,19 @@ __device__ __forceinline__ uint32_t store8(T* p, int C, int block, int l, F2 (&v
     }
     if (VEC) {
       const int c = half_col<true>(block, l, 0);
-      if (FULL || c < C) *reinterpret_cast<uint4*>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (in && (FULL || c < C)) *reinterpret_cast<uint4*>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = half_col<false>(block, l, j);
-        if (c < C) reinterpret_cast<uint16_t*>(p)[c] = uint16_t(j & 1 ? o[j >> 1] >> 16 : o[j >> 1]);
+        if (in && c < C) reinterpret_cast<uint16_t*>(p)[c] = uint16_t(j & 1 ? o[j >> 1] >> 16 : o[j >> 1]);
       }
     }
     return top_of(o);
   } else {
     if (VEC) {
       const int c = half_col<true>(block, l, 0);
-      if (FULL || c < C) {
+      if (in && (FULL || c < C)) {
         float4* q = reinterpret_cast<float4*>(p + c);
         q[0] = make_float4(v[0].x(), v[0].y(), v[1].x(), v[1].y());
         q[1] = make_float4(v[2].x(), v[2].y(), v[3].x(), v[3].y());
@@ -272,41 +257,77 @@ __device__ __forceinline__ uint32_t store8(T* p, int C, int block, int l, F2 (&v
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = half_col<false>(block, l, j);
-        if (c < C) reinterpret_cast<float*>(p)[c] = j & 1 ? v[j >> 1].y() : v[j >> 1].x();
+        if (in && c < C) reinterpret_cast<float*>(p)[c] = j & 1 ? v[j >> 1].y() : v[j >> 1].x();
       }
     }
     return top_of(v);
   }
 }
 
-// One block of the checkpoint row at p from its sixteen lanes' values, all lanes of
-// the warp together (`in`: this half warp has a block; `top`: the bits of this
-// lane's largest magnitude). The lanes of a row's
-// last block also write its padding.
-template <bool VEC, bool FULL = false>
-__device__ __forceinline__ void save8(uint8_t* p, int C, int block, int l, bool in, uint32_t top,
-                                      const F2 (&v)[4]) {
-  top = half_top(top);
-  if (!FULL && !in) return;
-  const int s = ckpt_scale(top);
-  const float inv = ckpt_inv_step(s);
-  const uint2 q = ckpt_pack8(v, inv, __uint_as_float(top) * inv >= 127.5f);
-  if (VEC) {
-    const int c = half_col<true>(block, l, 0);
-    if (FULL || c < C) *reinterpret_cast<uint2*>(p + c) = q;
-  } else {
+// n blocks on their way into checkpoint rows: for each its row, its number
+// in the row, whether this half warp has it at all, the bits of this lane's
+// largest magnitude, and this lane's values.
+template <int n> struct Kept {
+  uint8_t* row[n];
+  int block[n];
+  bool in[n];
+  uint32_t top[n];
+  F2 v[n][4];
+};
+// Writes them, all lanes of the warp together; the lanes of a row's last block
+// also write its padding. The blocks go through each stage side by side: one by
+// one, with their branches between them, hardly two of their instructions
+// overlapped.
+template <bool VEC, bool FULL = false, int n>
+__device__ __forceinline__ void save8(Kept<n>& k, int C, int l) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = half_col<false>(block, l, j);
-      if (c < C) p[c] = uint8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
-    }
+  for (int d = 8; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) k.top[i] = max(k.top[i], __shfl_xor_sync(MEP_FULL_MASK, k.top[i], d));
+  int s[n];
+  bool cut = false;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    s[i] = ckpt_scale(k.top[i]);
+    const float inv = ckpt_inv_step(s[i]);
+    cut |= __uint_as_float(k.top[i]) * inv >= 127.5f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k.v[i][j] = fma2(k.v[i][j], both(inv), both(kRound));
+  }
+  if (cut) {  // only a block whose largest value is at least 127.5 steps can round to 128: one in a hundred
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k.v[i][j] = pair(fminf(fmaxf(k.v[i][j].x(), kRound - 127.f), kRound + 127.f),
+                         fminf(fmaxf(k.v[i][j].y(), kRound - 127.f), kRound + 127.f));
   }
   const int at = ckpt_scale_at(C), nb = (C + kCkptBlock - 1) / kCkptBlock;
-  if (l == 0) p[at + block] = uint8_t(s);
-  if (block == nb - 1) {
-    if (C + l < at) p[C + l] = 0;
+  bool last = false;
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const uint2 q = ckpt_bytes(k.v[i]);
+    if (VEC) {
+      const int c = half_col<true>(k.block[i], l, 0);
+      if (k.in[i] && (FULL || c < C)) *reinterpret_cast<uint2*>(k.row[i] + c) = q;
+    } else if (k.in[i]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = half_col<false>(k.block[i], l, j);
+        if (c < C) k.row[i][c] = uint8_t((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+      }
+    }
+    if (l == 0 && k.in[i]) k.row[i][at + k.block[i]] = uint8_t(s[i]);
+    last |= k.block[i] == nb - 1;
+  }
+  if (last) {
     const int end = int(ckpt_row_bytes(C));
-    for (int i = at + nb + l; i < end; i += kHalf) p[i] = 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i)
+      if (k.in[i] && k.block[i] == nb - 1) {
+        if (C + l < at) k.row[i][C + l] = 0;
+        for (int e = at + nb + l; e < end; e += kHalf) k.row[i][e] = 0;
+      }
   }
 }
 

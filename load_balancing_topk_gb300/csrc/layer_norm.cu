@@ -321,49 +321,58 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
       for (int e = 8; e >= 1; e >>= 1) sq += __shfl_xor_sync(MEP_FULL_MASK, sq, e);
     }
+    const float rstd_all = 1.f / sqrtf(sq * inv_h + eps);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       m[u] = __shfl_sync(MEP_FULL_MASK, mean_all, 16 * u);
-      rs[u] = __shfl_sync(MEP_FULL_MASK, sq, 16 * u);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rs[u] = 1.f / sqrtf(rs[u] * inv_h + eps);
+      rs[u] = __shfl_sync(MEP_FULL_MASK, rstd_all, 16 * u);
       if (threadIdx.x % (32 * W) == u && r + u < N) {
         mean[r + u] = m[u];
         rstd[r + u] = rs[u];
       }
     }
+    constexpr int JJ = J < 2 ? J : 2;  // blocks side by side
 #pragma unroll
-    for (int i = 0; i < J; ++i) {
-      const int block = half + 2 * W * i;
-      const bool in = FULL || block < nb;
-      if (J > 2) {
-        load_params<VEC>(w, p_type, H, block, l, 1.f, wv[0]);
-        load_params<VEC>(b, p_type, H, block, l, 0.f, bv[0]);
+    for (int i0 = 0; i0 < J; i0 += JJ) {
+      Kept<JJ * U> k;
+#pragma unroll
+      for (int e = 0; e < JJ * U; ++e) {
+        k.block[e] = half + 2 * W * (i0 + e / U);
+        k.in[e] = (U == 1 || r + e % U < N) && (FULL || k.block[e] < nb);
       }
-      const F2(&wi)[4] = wv[J > 2 ? 0 : i], (&bi)[4] = bv[J > 2 ? 0 : i];
+      if (KEEP && x_ckpt != nullptr) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (U > 1 && r + u >= N) continue;
-        F2 v[4];
-        if (KEEP && x_ckpt != nullptr) {
+        for (int e = 0; e < JJ * U; ++e) {
+          const Pack<KIND>& q = p[e % U][i0 + e / U];
+          k.row[e] = xc + e % U * row_bytes;
+          k.top[e] = q.top();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] = p[u][i].at(j);
-          save8<VEC, FULL>(xc + u * row_bytes, H, block, l, in, p[u][i].top(), v);
+          for (int j = 0; j < 4; ++j) k.v[e][j] = q.at(j);
         }
+        save8<VEC, FULL>(k, H, l);
+      }
+#pragma unroll
+      for (int e = 0; e < JJ * U; ++e) {
+        const int u = e % U, i = i0 + e / U;
+        if (J > 2 && u == 0) {
+          load_params<VEC>(w, p_type, H, k.block[e], l, 1.f, wv[0]);
+          load_params<VEC>(b, p_type, H, k.block[e], l, 0.f, bv[0]);
+        }
+        const F2(&wi)[4] = wv[J > 2 ? 0 : i], (&bi)[4] = bv[J > 2 ? 0 : i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[j] = fma2(mul2(add2(p[u][i].at(j), both(-m[u])), both(rs[u])), wi[j], bi[j]);
+          F2 v = fma2(mul2(add2(p[u][i].at(j), both(-m[u])), both(rs[u])), wi[j], bi[j]);
           if (!VEC)
-            v[j] = pair(half_col<false>(block, l, 2 * j) < H ? v[j].x() : 0.f,
-                        half_col<false>(block, l, 2 * j + 1) < H ? v[j].y() : 0.f);
+            v = pair(half_col<false>(k.block[e], l, 2 * j) < H ? v.x() : 0.f,
+                     half_col<false>(k.block[e], l, 2 * j + 1) < H ? v.y() : 0.f);
           else if (!there[i])
-            v[j] = both(0.f);
+            v = both(0.f);
+          k.v[e][j] = v;
         }
-        const uint32_t top = store8<T, VEC, FULL>(out + (long long)u * H, H, block, l, v);
-        if (KEEP && y_ckpt != nullptr) save8<VEC, FULL>(yc + u * row_bytes, H, block, l, in, top, v);
+        k.row[e] = yc + u * row_bytes;
+        k.top[e] = store8<T, VEC, FULL>(out + (long long)u * H, H, k.block[e], l, k.v[e], k.in[e]);
       }
+      if (KEEP && y_ckpt != nullptr) save8<VEC, FULL>(k, H, l);
     }
     out += (long long)step * H;
     if (KEEP) {
@@ -410,17 +419,24 @@ __global__ void __launch_bounds__(kSmThreads)
   const long long dstep = step * Slot<KIND>::pitch(H), xstep = step * Slot<XKIND>::pitch(H);
   const auto ahead = [&](unsigned r, uint32_t slot) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (r + u < N) {
+    for (int u = 0; u < U; ++u) {
+      const bool in = r + u < N;
+      if (in || u > 0) {  // (a row beyond the last beside one before it: zeros, so that no sum has to ask)
         const char *drow = dsrc + u * Slot<KIND>::pitch(H), *xrow = xsrc + u * Slot<XKIND>::pitch(H);
 #pragma unroll
         for (int i = 0; i < J; ++i)
           if (there[i]) {
-            const uint32_t s = slot + (u * J + i) * threads * piece;
-            Slot<KIND>::copy(s, threads, drow + 2 * W * i * 16 * Slot<KIND>::bytes);
-            Slot<XKIND>::copy(s + threads * Slot<KIND>::bytes, threads, xrow + 2 * W * i * 16 * Slot<XKIND>::bytes);
+            const uint32_t s = slot + (u * J + i) * threads * piece, sx = s + threads * Slot<KIND>::bytes;
+            if (u > 0 && !in) {
+              Slot<KIND>::zero(s, threads);
+              Slot<XKIND>::zero(sx, threads);
+            } else {
+              Slot<KIND>::copy(s, threads, drow + 2 * W * i * 16 * Slot<KIND>::bytes);
+              Slot<XKIND>::copy(sx, threads, xrow + 2 * W * i * 16 * Slot<XKIND>::bytes);
+            }
           }
       }
+    }
     dsrc += dstep;
     xsrc += xstep;
     copy_async_commit();
@@ -487,7 +503,7 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       F2 s1 = both(0.f), s2 = both(0.f);
-      if (U == 1 || r + u < N) {
+      {
         const F2 k1 = both(rs[u]), k0 = both(-m[u]);
 #pragma unroll
         for (int i = 0; i < J; ++i) {
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__(kSmThreads)
     group_sums<2 * U>(sums, &s_sum[turn][group * W * 2 * U], W, warp, group);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (U == 1 || r + u < N) {
+      {
         // rs (t - c1 - xhat c2), with xhat rs = (x - m) rs^2
         const F2 k1 = both(rs[u]), k0 = both(-m[u]);
         const F2 a = both(-rs[u] * sums[u] * inv_h), c = both(-rs[u] * sums[U + u] * inv_h * rs[u]);
@@ -526,7 +542,7 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             v[j] = fma2(p.plus(j, k0), c, fma2(mul2(d.at(j), wv[j]), k1, a));
-          store8<T, VEC>(out + (long long)u * H, H, half + 2 * W * i, l, v);
+          store8<T, VEC>(out + (long long)u * H, H, half + 2 * W * i, l, v, U == 1 || r + u < N);
         }
       }
     }
