@@ -484,12 +484,13 @@ def _good(t, name, dtype, shape, dev):
 def _call(fn: str, dev, *args) -> None:
     """Enqueue one library call on the current stream of dev."""
     torch = _torch()
-    lib = _lib if _lib is not None else load_library()
-    if torch.cuda.current_device() == dev.index:
-        rc = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    entry = getattr(_lib if _lib is not None else load_library(), fn)
+    index = dev.index
+    if torch._C._cuda_getDevice() == index:
+        rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(dev):
-            rc = getattr(lib, fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            rc = entry(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc != 0:
         raise MepError(fn, rc)
 
