@@ -74,7 +74,6 @@ constexpr int kBK = 64;                  // buffer rows that the list of parts c
 constexpr int kThreads = 512;
 constexpr int kTmemCols = 2 * kBN;
 constexpr int kGroupThreads = 1024;
-constexpr int kStoreBox = 32 * 32 * 4;   // 32 rows x 32 fp32 columns
 constexpr int kEpiWarps = 8;
 constexpr int kPair = 2;
 // How long groups are cut into parts (k_wgrad_groups). At H 512, H' 512 one
@@ -97,12 +96,13 @@ template <bool CKPT> struct Ring {
   static constexpr int K = CKPT ? 128 : 64;
   static constexpr int box = K * 64 * 2, op = 2 * box;      // a bf16 box of 64 columns; an operand's two
   static constexpr int q = K * kBM, scales = K * 16;        // checkpoint bytes; scale bytes, in 16-byte rows
-  static constexpr int stage = op + (CKPT ? q + scales : op), stages = CKPT ? 3 : 6;
+  static constexpr int stage = op + (CKPT ? q + scales : op), stages = CKPT ? 4 : 6;
+  static constexpr int out = CKPT ? 16 : 32, out_box = 32 * out * 4;  // columns of an output box of 32 rows; its bytes
   static constexpr int b0 = CKPT ? 0 : op;                  // B within a stage
   static constexpr int accs = CKPT ? 1 : 2;                 // accumulators
   static constexpr int a_cols = K / 2;                      // TMEM columns of an A
   static constexpr int chunk = MEP_WGRAD_CHUNK;             // steps summed in TMEM
-  static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * kStoreBox + 512;
+  static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * out_box + 512;
   static_assert(smem <= 232448, "the ring must fit in 227 KB of shared memory");
   static_assert(accs * kBN + (CKPT ? stages * a_cols : 0) <= kTmemCols, "TMEM");
 };
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gen_base = smem_raw + (base - raw);
   const uint32_t out_box = base + kSt * kStage;
-  Smem* S = reinterpret_cast<Smem*>(gen_base + kSt * kStage + kEpiWarps * kStoreBox);
+  Smem* S = reinterpret_cast<Smem*>(gen_base + kSt * kStage + kEpiWarps * Rg::out_box);
   volatile int* abort_flag = &S->abort;
 
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warp q + 4 * half holds TMEM lanes (rows of H) [32q, 32q + 32) and
     // columns [128 half, 128 half + 128) of the unit.
     const int q = warp & 3, half = (warp - 8) >> 2;
-    const uint32_t box = out_box + (uint32_t)(warp - 8) * kStoreBox;
+    const uint32_t box = out_box + (uint32_t)(warp - 8) * Rg::out_box;
     // the row of H, of these 32, in this lane: the converter's order
     const int row = CKPT ? (lane & 16) + ((lane & 7) << 1) + ((lane >> 3) & 1) : lane;
     Pos at;
@@ -736,22 +736,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* map = en.w < E ? &map_home : &map_slot;
       const int z = en.w < E ? en.w : en.w - E;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (h < H && n + 32 * i < Hp) {
+      for (int i = 0; i < 128 / Rg::out; ++i)
+        if (h < H && n + Rg::out * i < Hp) {
           if (lane == 0) bulk_wait_read_0();
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sts128(box + row * 128 + ((j ^ (row & 7)) << 4), __float_as_uint(acc[32 * i + 4 * j]),
-                   __float_as_uint(acc[32 * i + 4 * j + 1]), __float_as_uint(acc[32 * i + 4 * j + 2]),
-                   __float_as_uint(acc[32 * i + 4 * j + 3]));
+          for (int j = 0; j < Rg::out / 4; ++j) {
+            const float* v = &acc[Rg::out * i + 4 * j];
+            sts128(box + row * (4 * Rg::out) + ((j ^ (Rg::out == 32 ? row & 7 : (row >> 1) & 3)) << 4),
+                   __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
             if (accumulate)
-              tma_add_3d(map, n + 32 * i, h, z, box);
+              tma_add_3d(map, n + Rg::out * i, h, z, box);
             else
-              tma_store_3d(map, n + 32 * i, h, z, box);
+              tma_store_3d(map, n + Rg::out * i, h, z, box);
           }
         }
       return true;
@@ -788,16 +789,16 @@ bool map_2d(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, unsigned 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// fp32 [n, H, H'], boxes of 32 x 32: a third dimension keeps a box that
+// fp32 [n, H, H'], boxes of 32 x `cols`: a third dimension keeps a box that
 // hangs over the last rows of H out of the next matrix.
 bool map_grad(CUtensorMap* m, float* ptr, unsigned long long n, unsigned long long H,
-              unsigned long long Hp) {
+              unsigned long long Hp, unsigned cols) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {Hp, H, n}, strides[2] = {Hp * 4, H * Hp * 4};
-  const cuuint32_t box[3] = {32, 32, 1}, estr[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {cols, 32, 1}, estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, ptr, dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, cols == 32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -918,9 +919,10 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
       !on_current_device(home_grad) || (B > 0 && !on_current_device(slot_grad)))
     return MEP_ERR_INVALID_ARG;
   CUtensorMap mx, ms, md, mh, msl;
-  if (!map_grad(&mh, home_grad, E, H, Hp)) return MEP_ERR_CUDA;
+  const unsigned out_cols = x_type == MEP_CKPT8 ? Ring<true>::out : Ring<false>::out;
+  if (!map_grad(&mh, home_grad, E, H, Hp, out_cols)) return MEP_ERR_CUDA;
   msl = mh;  // never used without slots
-  if (B > 0 && !map_grad(&msl, slot_grad, (unsigned long long)R * B, H, Hp)) return MEP_ERR_CUDA;
+  if (B > 0 && !map_grad(&msl, slot_grad, (unsigned long long)R * B, H, Hp, out_cols)) return MEP_ERR_CUDA;
   mx = ms = md = mh;  // never used without rows
   if (rows > 0) {
     const unsigned long long rb = ckpt_row_bytes(H);
