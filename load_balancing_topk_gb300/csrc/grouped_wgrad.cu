@@ -50,12 +50,19 @@
 // its MMAs read as much of shared memory, all of its 128 bytes a cycle. The
 // medium layer ([196608, 2048] x [196608, 1408], 67 groups) takes 672 to 702
 // us by the box, 1614 to 1688 TFLOP/s, against 1694 to 1739 of a dense library
-// product of the same size. From checkpoint rows the converter, whose 160
-// integer and bf16 instructions a step and warp nothing else can share: 823
-// us, 1377 TFLOP/s (with them left out, 680). Its first form wrote the operand
-// to shared memory (940 us: 82 KB a step through shared memory, where it is
-// now half that). Waiting with short tries cost 7%, addresses in ordinary
-// instead of uniform registers 4%, a release at cluster scope per step half.
+// product of the same size (and some 745 us once the GPU is hot). From
+// checkpoint rows the converter: 740 us, 1532 TFLOP/s (hot: 813). Of the 1450
+// cycles of a step of 128 rows (1024 of MMAs) its warps work 1000, wait 160 for
+// the copies, and the MMAs wait 220 for the sums to leave the one accumulator.
+// What it took to get there: the operand in TMEM (through shared memory 940
+// us), 128 rows a step, for what each step costs a converter to start (847 ->
+// 823 us; with the ring below, 750 against 893 at 64), a fourth stage, so that
+// copies, conversion and products of a stage may follow each other without
+// holding up the next (825 -> 752), and seven instructions for four bytes
+// instead of ten (762 -> 740). Loading a step's bytes before converting any,
+// or a step ahead, ran slower (773, 1007).
+// Waiting with short tries cost 7%, addresses in ordinary instead of uniform
+// registers 4%, a release at cluster scope per step half.
 // Every wait is bounded as in grouped_gemm.cu.
 
 #include "ckpt.cuh"
@@ -88,16 +95,14 @@ constexpr int kMostPartials = 2 * kPairs;  // parts * tiles of all entries with 
 constexpr int kTile = 2 * kBM * kBN;       // fp32 values of a partial sum
 
 // A step of K buffer rows and its stage: from bf16 rows the operands A and B;
-// from checkpoint rows B and the bytes, which become an A in TMEM. There a step
-// is 128 rows, as what it costs a converter to start one is spread further
-// (medium layer 847 -> 823 us; the bf16 form, which has more stages of 64,
-// 672 us against 694).
+// from checkpoint rows B and the bytes, which become an A in TMEM, in steps of
+// 128 rows, with output boxes half as large, for a fourth stage.
 template <bool CKPT> struct Ring {
   static constexpr int K = CKPT ? 128 : 64;
   static constexpr int box = K * 64 * 2, op = 2 * box;      // a bf16 box of 64 columns; an operand's two
   static constexpr int q = K * kBM, scales = K * 16;        // checkpoint bytes; scale bytes, in 16-byte rows
   static constexpr int stage = op + (CKPT ? q + scales : op), stages = CKPT ? 4 : 6;
-  static constexpr int out = CKPT ? 16 : 32, out_box = 32 * out * 4;  // columns of an output box of 32 rows; its bytes
+  static constexpr int out = CKPT ? 16 : 32, out_box = 32 * out * 4;  // an output box: columns; bytes of 32 rows
   static constexpr int b0 = CKPT ? 0 : op;                  // B within a stage
   static constexpr int accs = CKPT ? 1 : 2;                 // accumulators
   static constexpr int a_cols = K / 2;                      // TMEM columns of an A
@@ -203,9 +208,9 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 //
 // A part is at most what a pair has to do in all, so that few, uneven groups
 // still fill the pairs (half of that cost more in joins than it evened out: 58
-// against 48 us at 22220 rows in 18 groups, 1160 x 520); a group has at most kMostParts (the last of them
-// adds the partial sums of all up), and only one of more than kLeastSteps is
-// cut. The longest come first. A thread has one weight row, reads its group
+// against 48 us at 22220 rows in 18 groups, 1160 x 520); a group has at most
+// kMostParts (the last of them adds the partial sums of all up), and only one
+// of more than kLeastSteps is cut. The longest come first. A thread has one weight row, reads its group
 // ends once (together the threads read, and check, all of cu_seqlens), and
 // places its parts by counting over the others' lengths in shared memory. With
 // more weight rows than threads the list is in their order and nothing is cut:
@@ -359,23 +364,25 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t& a, uint32_t
                : "memory");
 }
 
-// The four signed bytes of w times a power of two each, as bf16: bytes 0 and 2
-// by the halves of step, into even, bytes 1 and 3 into odd. A byte under 0x43
-// is bf16 128 + its low seven bits, or, where its sign bit falls into the
-// exponent, 256 + ...: v = 128 + low7, c = 128 or 256, v - c = q exactly, and
-// q * step has 8 significant bits. (A byte permutation first: masks on w
-// itself save an instruction and ran 6% slower.)
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, __nv_bfloat162 step) {
-  const uint32_t x = __byte_perm(w, 0x43434343u, sel);
-  const uint32_t v = x & 0xff7fff7fu, c = x & 0xff80ff80u;
-  const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
+// The four signed bytes q of w times a power of two each, as bf16: bytes 0 and
+// 2 by the halves of `step` (which holds it times 2^6) into even, bytes 1 and 3
+// into odd. With its sign bit flipped a byte is u = q + 128, and sixteen bits
+// that hold u alone are bf16 u * 2^-133, below and above the smallest normal
+// number alike (u = 128) as its spacing stays the same. u * 2^127 in one step
+// less 2 is q * 2^-6, which has eight bits, and so has q times the power of two.
+__device__ __forceinline__ uint32_t dequant2(uint32_t u, __nv_bfloat162 step) {
+  constexpr uint32_t kUp = 0x7f007f00u, kBack = 0xc000c000u;  // 2^127, -2
+  const uint32_t up = kUp, back = kBack;
+  const __nv_bfloat162 q = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&up),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&back));
   const __nv_bfloat162 r = __hmul2(q, step);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 __device__ __forceinline__ void dequant4(uint32_t w, __nv_bfloat162 step, uint32_t& even, uint32_t& odd) {
-  even = dequant2(w, 0x4240, step);
-  odd = dequant2(w, 0x4341, step);
+  const uint32_t u = w ^ 0x80808080u;
+  even = dequant2(__byte_perm(u, 0u, 0x4240), step);
+  odd = dequant2(__byte_perm(u, 0u, 0x4341), step);
 }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -632,8 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ldsm4_trans(q + row * 128 + (((2 * q4 + (i >> 3)) ^ (row & 7)) << 4), v[i], v[i + 1], v[i + 2],
                             v[i + 3]);
               }
-              s0 = k0 + 2 * lane >= valid ? 0u : s0 == (uint32_t)kCkptNan ? 0x7fffu : s0 << 7;
-              s1 = k0 + 2 * lane + 1 >= valid ? 0u : s1 == (uint32_t)kCkptNan ? 0x7fffu : s1 << 7;
+              s0 = k0 + 2 * lane >= valid ? 0u : s0 == (uint32_t)kCkptNan ? 0x7fffu : (s0 + 6) << 7;
+              s1 = k0 + 2 * lane + 1 >= valid ? 0u : s1 == (uint32_t)kCkptNan ? 0x7fffu : (s1 + 6) << 7;
               const uint32_t pairs = s0 | s1 << 16;
               uint32_t step[8];
 #pragma unroll
@@ -926,8 +933,8 @@ extern "C" int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
   mx = ms = md = mh;  // never used without rows
   if (rows > 0) {
     const unsigned long long rb = ckpt_row_bytes(H);
-    bool ok = map_2d(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, rows, Hp, 2ull * Hp, 64, x_type == MEP_CKPT8 ? Ring<true>::K : Ring<false>::K,
-                     CU_TENSOR_MAP_SWIZZLE_128B);
+    bool ok = map_2d(&md, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dy, rows, Hp, 2ull * Hp, 64,
+                     x_type == MEP_CKPT8 ? Ring<true>::K : Ring<false>::K, CU_TENSOR_MAP_SWIZZLE_128B);
     if (x_type == MEP_CKPT8)
       ok = ok &&
            map_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, rows, H, rb, kBM, Ring<true>::K, CU_TENSOR_MAP_SWIZZLE_128B) &&
