@@ -22,9 +22,9 @@
 //                   of H, 256 columns of H'), to and fro over the pairs. CTA r
 //                   of a pair owns 128 of the 256 rows of H. Per step of 64
 //                   buffer rows (128 from checkpoint rows):
-//     warp 0      TMA producer: its half of the 256 columns of dy and this
-//                 CTA's 128 columns of x (bf16 boxes, or the checkpoint's bytes
-//                 and the rows' scale bytes), into a ring of stages;
+//     warps 0, 2  TMA producers: this CTA's 128 columns of x (bf16 boxes, or
+//                 the checkpoint's bytes and the rows' scale bytes), and its
+//                 half of the 256 columns of dy, into a ring of stages;
 //     warps 4..7  converter: checkpoint bytes to a bf16 operand A in TMEM (exact:
 //                 q * 2^k has 8 significant bits), and zeros over the rows
 //                 that a segment's last step takes from the next group, in
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSt; ++s) {
-      mbar_init(smem_u32(&S->full[s]), 1);   // this CTA's producer and its bytes
+      mbar_init(smem_u32(&S->full[s]), 2);   // this CTA's producers and their bytes
       mbar_init(smem_u32(&S->ready[s]), 8);  // CTA 0: four converter warps of each CTA
       mbar_init(smem_u32(&S->empty[s]), 1);  // CTA 0's multicast commit
     }
@@ -510,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the four warpgroups' registers: 56 + 72 + 192 + 192 = 4 x 128 at launch
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
-      // ---------------- TMA producer ----------------
+    if (warp == 0 || warp == 2) {
+      // ---------------- TMA producers: x, dy ----------------
+      const bool of_x = warp == 0;
       Pos at;
       uint32_t issued = 0;
       for_units(parts, count, tiles, [&](const Part& en, int t) {
@@ -520,24 +521,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c0 = n0 + rank * (narrow ? 64 : 128);
         const int na = h0 >= H ? 0 : h0 + 64 < H ? 2 : 1;
         const int nb = c0 >= Hp ? 0 : !narrow && c0 + 64 < Hp ? 2 : 1;
-        const uint32_t bytes = (CKPT ? (na > 0 ? Rg::q + Rg::scales : 0) : na * Rg::box) + nb * Rg::box;
+        const uint32_t bytes = !of_x ? nb * Rg::box : !CKPT ? na * Rg::box : na > 0 ? Rg::q + Rg::scales : 0;
         const int sx = ckpt_scale_at(H) + ((h0 / kCkptBlock) & ~15);
         return for_steps<Rg::K>(en, segs, [&](int row, int, bool) {
           if (!warp_wait(smem_u32(&S->empty[at.s]), at.parity ^ 1u, abort_flag, status)) return false;
           const uint32_t bar = smem_u32(&S->full[at.s]), st = base + at.s * kStage;
           if (elected()) {
             mbar_expect_tx(bar, bytes);
-            if (CKPT) {
-              if (na > 0) {
-                tma_load_2d(st + Rg::op, &map_x, h0, row, bar);
-                tma_load_2d(st + Rg::op + Rg::q, &map_s, sx, row, bar);
-              }
+            if (!of_x) {
+              if (nb > 0) tma_load_2d(st + Rg::b0, &map_dy, c0, row, bar);
+              if (nb > 1) tma_load_2d(st + Rg::b0 + Rg::box, &map_dy, c0 + 64, row, bar);
+            } else if (CKPT) {
+              if (na > 0) tma_load_2d(st + Rg::op, &map_x, h0, row, bar);
+              if (na > 0) tma_load_2d(st + Rg::op + Rg::q, &map_s, sx, row, bar);
             } else {
               if (na > 0) tma_load_2d(st, &map_x, h0, row, bar);
               if (na > 1) tma_load_2d(st + Rg::box, &map_x, h0 + 64, row, bar);
             }
-            if (nb > 0) tma_load_2d(st + Rg::b0, &map_dy, c0, row, bar);
-            if (nb > 1) tma_load_2d(st + Rg::b0 + Rg::box, &map_dy, c0 + 64, row, bar);
           }
           __syncwarp();
           at.template next<kSt>();
