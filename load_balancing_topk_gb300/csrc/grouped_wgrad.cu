@@ -45,16 +45,16 @@
 // rounded to nearest) every 1024, 512 and 256 rows; fp32 products are off by
 // 0.2 to 0.4e-6. 512 cost 3% over 1024 and saves 6% over 256. A checkpoint's
 // bytes have fewer bits to lose: 1.7, 2.6 and 3.5e-7 at 1024, 1536 and 2048
-// rows (5.4e-7 with a single accumulator). So there 2048 costs no more than 512
-// does here, and the MMAs wait less often for the one accumulator to empty:
-// 724, 707 and 702 us on the medium layer (696).
+// rows (5.4e-7 with a single accumulator). The longer a chunk, the less often
+// the MMAs wait for the one accumulator to empty: 724, 707 and 702 us on the
+// medium layer (696). 1536 has most of that.
 //
 // What bounds it. From bf16 rows the feed: per step an SM takes in 32 KB and
 // its MMAs read as much of shared memory, all of its 128 bytes a cycle. The
 // medium layer ([196608, 2048] x [196608, 1408], 67 groups) takes 672 to 702
 // us by the box, 1614 to 1688 TFLOP/s, against 1694 to 1739 of a dense library
 // product of the same size (and some 745 us once the GPU is hot). From
-// checkpoint rows 702 us too, 1614 TFLOP/s: of the 1310 cycles of a step of 128
+// checkpoint rows 707 us, 1605 TFLOP/s: of the 1310 cycles of a step of 128
 // rows (1024 of MMAs) a converter warp works 825 and waits 160 for the copies,
 // and the MMAs wait 135 for the sums to leave the one accumulator.
 // What it took to get there: the operand in TMEM (through shared memory 940
@@ -105,7 +105,7 @@ template <bool CKPT> struct Ring {
   static constexpr int b0 = CKPT ? 0 : op;                  // B within a stage
   static constexpr int accs = CKPT ? 1 : 2;                 // accumulators
   static constexpr int a_cols = K / 2;                      // TMEM columns of an A
-  static constexpr int chunk = CKPT ? 16 : 8;               // steps summed in TMEM
+  static constexpr int chunk = CKPT ? 12 : 8;               // steps summed in TMEM
   static constexpr int smem = 1024 /* alignment slack */ + stages * stage + kEpiWarps * out_box + 512;
   static_assert(smem <= 232448, "the ring must fit in 227 KB of shared memory");
   static_assert(accs * kBN + (CKPT ? stages * a_cols : 0) <= kTmemCols, "TMEM");
