@@ -25,33 +25,46 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Calls f(row, block, in) for U blocks of this half warp at a time; the loads
-// of all U come first. Blocks are numbered over the whole tensor; a call's
+// Where the U blocks of this half warp are. Blocks are numbered over the whole tensor; a call's
 // are kThreads / 16 apart.
 struct Where {
   long long row;
   int block;
   bool in;
 };
-template <int U> __device__ __forceinline__ void where(Where (&w)[U], uint32_t blocks, uint32_t nb) {
+// Blocks: how many there are, how many a row has, and the quotient i / per_row
+// of i < 2^31 by a product: with 2^l >= per_row and m = floor(2^(31+l) /
+// per_row) + 1, m * per_row is off 2^(31+l) by at most 2^l, too little to
+// reach the next quotient. (Divisions were a tenth of what the kernels issue.)
+struct Blocks {
+  uint32_t all, per_row, m;
+  int shift;
+};
+Blocks blocks_of(uint32_t all, int C) {
+  const uint32_t d = (C + kCkptBlock - 1) / kCkptBlock;
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  return {all, d, d == 1 ? 0u : uint32_t((1ull << (31 + l)) / d + 1), l - 1};
+}
+template <int U> __device__ __forceinline__ void where(Where (&w)[U], const Blocks& b) {
   const uint32_t first = blockIdx.x * uint32_t(U * kThreads / kHalf) + threadIdx.x / kHalf;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint32_t i = first + u * (kThreads / kHalf);
-    w[u].in = i < blocks;
-    w[u].row = i / nb;
-    w[u].block = int(i % nb);
+    const uint32_t i = first + u * (kThreads / kHalf), row = b.per_row == 1 ? i : __umulhi(i, b.m) >> b.shift;
+    w[u].in = i < b.all;
+    w[u].row = row;
+    w[u].block = int(i - row * b.per_row);
   }
 }
 
 template <int KIND, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
-    k_ckpt_save(const void* __restrict__ x, uint32_t blocks, int C, uint8_t* __restrict__ ckpt) {
+    k_ckpt_save(const void* __restrict__ x, Blocks blocks, int C, uint8_t* __restrict__ ckpt) {
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % kHalf;
   Where w[U];
-  where<U>(w, blocks, (C + kCkptBlock - 1) / kCkptBlock);
+  where<U>(w, blocks);
   Pack<KIND> p[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -71,12 +84,12 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
-    k_ckpt_load(const uint8_t* __restrict__ ckpt, uint32_t blocks, int C, T* __restrict__ x) {
+    k_ckpt_load(const uint8_t* __restrict__ ckpt, Blocks blocks, int C, T* __restrict__ x) {
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % kHalf;
   Where w[U];
-  where<U>(w, blocks, (C + kCkptBlock - 1) / kCkptBlock);
+  where<U>(w, blocks);
   Pack<MEP_CKPT8> p[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -97,13 +110,13 @@ __device__ __forceinline__ F2 sigmoid2(F2 g) { return pair(sigmoid(g.x()), sigmo
 
 template <bool VEC, bool CKPT, int U>
 __global__ void __launch_bounds__(kThreads)
-    k_swiglu(const __nv_bfloat16* __restrict__ gu, uint32_t blocks, int F,
+    k_swiglu(const __nv_bfloat16* __restrict__ gu, Blocks blocks, int F,
              __nv_bfloat16* __restrict__ a, uint8_t* __restrict__ ckpt) {
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % kHalf;
   Where w[U];
-  where<U>(w, blocks, (F + kCkptBlock - 1) / kCkptBlock);
+  where<U>(w, blocks);
   Pack<MEP_BF16> p[U][2];
 #pragma unroll
   for (int u = 0; u < U; ++u)
@@ -141,13 +154,13 @@ __global__ void __launch_bounds__(kThreads)
 template <int KIND, bool VEC, int U>
 __global__ void __launch_bounds__(kThreads)
     k_swiglu_backward(const __nv_bfloat16* __restrict__ da, const void* __restrict__ gu,
-                      uint32_t blocks, int F, __nv_bfloat16* __restrict__ dgu,
+                      Blocks blocks, int F, __nv_bfloat16* __restrict__ dgu,
                       __nv_bfloat16* __restrict__ a) {
   pdl_wait();
   pdl_launch_dependents();
   const int l = threadIdx.x % kHalf;
   Where w[U];
-  where<U>(w, blocks, (F + kCkptBlock - 1) / kCkptBlock);
+  where<U>(w, blocks);
   Pack<KIND> p[U][2];
   Pack<MEP_BF16> d[U];
 #pragma unroll
@@ -181,7 +194,7 @@ template <int U, typename F> int sliced(long long rows, long long C, F f) {
   constexpr int per = U * kThreads / kHalf;
   for (long long r = 0; r < rows; r += most) {
     const long long n = (rows - r < most ? rows - r : most) * nb;
-    if (f(r, uint32_t(n), dim3(unsigned((n + per - 1) / per))) != cudaSuccess) return MEP_ERR_CUDA;
+    if (f(r, blocks_of(uint32_t(n), int(C)), dim3(unsigned((n + per - 1) / per))) != cudaSuccess) return MEP_ERR_CUDA;
   }
   return MEP_OK;
 }
@@ -214,7 +227,7 @@ extern "C" int mep_ckpt_save(const void* x, int x_type, int64_t N, int64_t C, ui
   const bool bf16 = x_type == MEP_BF16, vec = C % 8 == 0;
   const auto kernel = bf16 ? (vec ? k_ckpt_save<MEP_BF16, true, U> : k_ckpt_save<MEP_BF16, false, 1>)
                            : (vec ? k_ckpt_save<MEP_F32, true, U / 2> : k_ckpt_save<MEP_F32, false, 1>);
-  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+  const auto f = [&](long long r, Blocks blocks, dim3 grid) {
     const void* p = static_cast<const char*>(x) + r * C * (bf16 ? 2 : 4);
     return launch_pdl(kernel, grid, dim3(kThreads), 0, st, p, blocks, int(C), ckpt + r * ckpt_row_bytes(C));
   };
@@ -229,7 +242,7 @@ extern "C" int mep_ckpt_load(const uint8_t* ckpt, int64_t N, int64_t C, int x_ty
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool vec = C % 8 == 0;
   const auto run = [&](auto* out, auto kernel) {
-    return [=](long long r, uint32_t blocks, dim3 grid) {
+    return [=](long long r, Blocks blocks, dim3 grid) {
       return launch_pdl(kernel, grid, dim3(kThreads), 0, st, ckpt + r * ckpt_row_bytes(C), blocks, int(C),
                         out + r * C);
     };
@@ -257,7 +270,7 @@ extern "C" int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16*
   const bool vec = F % 8 == 0;
   const auto kernel = vec ? (ckpt != nullptr ? k_swiglu<true, true, U> : k_swiglu<true, false, U>)
                           : (ckpt != nullptr ? k_swiglu<false, true, 1> : k_swiglu<false, false, 1>);
-  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+  const auto f = [&](long long r, Blocks blocks, dim3 grid) {
     return launch_pdl(kernel, grid, dim3(kThreads), 0, st, in + 2 * r * F, blocks, int(F), out + r * F,
                       ckpt == nullptr ? nullptr : ckpt + 2 * r * ckpt_row_bytes(F));
   };
@@ -279,7 +292,7 @@ extern "C" int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_ty
   const bool vec = F % 8 == 0, kept = gu_type == MEP_CKPT8;
   const auto kernel = kept ? (vec ? k_swiglu_backward<MEP_CKPT8, true, U> : k_swiglu_backward<MEP_CKPT8, false, 1>)
                            : (vec ? k_swiglu_backward<MEP_BF16, true, U> : k_swiglu_backward<MEP_BF16, false, 1>);
-  const auto f = [&](long long r, uint32_t blocks, dim3 grid) {
+  const auto f = [&](long long r, Blocks blocks, dim3 grid) {
     const void* p = static_cast<const char*>(gu) + r * (kept ? 2 * ckpt_row_bytes(F) : 4 * F);
     return launch_pdl(kernel, grid, dim3(kThreads), 0, st, in + r * F, p, blocks, int(F), o + 2 * r * F,
                       oa == nullptr ? nullptr : oa + r * F);
