@@ -6,27 +6,33 @@
 // (save 2 + 1.01 bytes a bf16 value, load the reverse; per value of the
 // activation 4 in, 2 + 2.02 out forward, 2 + 2.02 in, 4 + 2 out backward).
 // A half warp takes a block of 128 columns, eight values a lane, and gets the
-// block's largest magnitude in four shuffles; a thread holds kUnroll blocks
-// at a time, all loaded before the first is used. Where a row is a multiple of
-// 8 columns a lane's values are one 16-byte vector; otherwise they are
-// fetched one by one, coalesced over the half warp.
+// block's largest magnitude in four shuffles; a thread holds a few blocks at a
+// time, all loaded before the first is used. Where a row is a multiple of 8
+// columns a lane's values are one 16-byte vector; otherwise they are fetched
+// one by one, coalesced over the half warp.
+// What bounds them is DRAM, and in small calls the launch. The activation
+// forward and backward on [196608, 2, 1408] takes 742 us, 6.7 TB/s (a copy
+// runs at 6.8); saving and loading [32768, 2048] 71 us, 5.7 TB/s, of which some
+// 4 us a launch are its start and end. Rows one by one issue two to three times
+// as much: [32768, 2047] 108 us, the activation on [65536, 2, 1407] 408
+// where 1408 columns take 250.
 
 #include "ckpt.cuh"
-
-#ifndef MEP_CKPT_UNROLL
-#define MEP_CKPT_UNROLL 4
-#endif
-#ifndef MEP_SWIGLU_UNROLL
-#define MEP_SWIGLU_UNROLL 2
-#endif
 
 namespace mep {
 namespace {
 
 constexpr int kThreads = 256;
+// Blocks a thread holds. Saving and loading [32768, 2048] in bf16 with 2, 4, 6
+// and 8: 76, 76, 85 and 101 us, more registers and so fewer warps; the
+// activation on [196608, 2, 1408] with 1, 2, 3 and 4: 798, 762, 791 and 822. fp32
+// has half as many (1, 2, 4: 128, 126, 126 us). Without vectors one, as eight
+// loads are under way then: the activation on [65536, 2, 1407] with 1, 2 and 4:
+// 408, 432 and 568 us.
+constexpr int kCkptUnroll = 4, kSwigluUnroll = 2;
 
-// Where the U blocks of this half warp are. Blocks are numbered over the whole tensor; a call's
-// are kThreads / 16 apart.
+// Where the U blocks of this half warp are. Blocks are numbered over the whole
+// tensor; a thread's are kThreads / 16 apart.
 struct Where {
   long long row;
   int block;
@@ -222,7 +228,7 @@ extern "C" int mep_ckpt_save(const void* x, int x_type, int64_t N, int64_t C, ui
                              void* stream) {
   const int rc = ckpt_check(x, x_type, N, C, ckpt);
   if (rc != MEP_OK || N == 0) return rc;
-  constexpr int U = MEP_CKPT_UNROLL;
+  constexpr int U = kCkptUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = x_type == MEP_BF16, vec = C % 8 == 0;
   const auto kernel = bf16 ? (vec ? k_ckpt_save<MEP_BF16, true, U> : k_ckpt_save<MEP_BF16, false, 1>)
@@ -238,7 +244,7 @@ extern "C" int mep_ckpt_load(const uint8_t* ckpt, int64_t N, int64_t C, int x_ty
                              void* stream) {
   const int rc = ckpt_check(x, x_type, N, C, ckpt);
   if (rc != MEP_OK || N == 0) return rc;
-  constexpr int U = MEP_CKPT_UNROLL;
+  constexpr int U = kCkptUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool vec = C % 8 == 0;
   const auto run = [&](auto* out, auto kernel) {
@@ -263,7 +269,7 @@ extern "C" int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16*
   if (rows == 0) return MEP_OK;
   if (gu == nullptr || a == nullptr || !aligned16(gu) || !aligned16(a) || !aligned16(ckpt))
     return MEP_ERR_INVALID_ARG;
-  constexpr int U = MEP_SWIGLU_UNROLL;
+  constexpr int U = kSwigluUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(gu);
   __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a);
@@ -285,7 +291,7 @@ extern "C" int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_ty
   if (da == nullptr || gu == nullptr || dgu == nullptr || !aligned16(da) || !aligned16(gu) ||
       !aligned16(dgu) || !aligned16(a))
     return MEP_ERR_INVALID_ARG;
-  constexpr int U = MEP_SWIGLU_UNROLL;
+  constexpr int U = kSwigluUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const __nv_bfloat16* in = reinterpret_cast<const __nv_bfloat16*>(da);
   __nv_bfloat16 *o = reinterpret_cast<__nv_bfloat16*>(dgu), *oa = reinterpret_cast<__nv_bfloat16*>(a);

@@ -10,8 +10,12 @@
 // A row of a multiple of 8 columns is fetched ahead: every thread copies its
 // own vectors of the rows of the next turns into its own slots of shared memory
 // (cp.async), so that the next rows' loads are under way while a row's sums
-// are, and no thread waits for another's copies. Registers alone (rows loaded
-// as they are used) held too few loads in flight: see the figures below.
+// are, and no thread waits for another's copies. What a thread has to issue
+// bounds them, most of all narrow rows. The backward pass of [65536, 7168] took
+// 820 us with the rows in flight in registers, 665 copied ahead and in pairs of
+// fp32, 444 with two rows of 16 columns a thread, 128 registers and addresses
+// that step, and takes 437 now (95% of the copy rate); [32768, 2048] takes 49
+// us forward (81%), 68 with y in 8 bits (73%), 70 backward from x in 8 bits (71%).
 //   k_norm       every warp takes the mean of its part of a row, then the
 //                squares around that mean; joined after one barrier, as
 //                var H = sum of the warps' squares + n_w (mean_w - mean)^2.
@@ -168,8 +172,9 @@ template <int KIND> struct Slot {
 };
 
 // An SM has 512 threads with 128 registers each, in CTAs of up to 512: what they
-// wait for is copied ahead, and more of them with fewer registers issued more
-// for the same work (backward [65536, 7168]: 434 us, 665 with 896 threads).
+// wait for is copied ahead, and more of them with fewer registers issue more
+// for the same work (forward [32768, 2048] with 1024 threads, one block a half
+// warp: 62 us against 52, with y in 8 bits and that read back 131 against 115).
 constexpr int kSmThreads = 512;
 template <int KIND, int J, int U> __host__ __device__ constexpr int norm_ahead() {
   return ahead_of(U * J * Slot<KIND>::bytes, 196608 / kSmThreads);
