@@ -109,8 +109,15 @@ __device__ __forceinline__ void group_sums(float (&v)[n], float* s, int W, int w
 // ---------------------------------------------------------------------------
 // A thread's slots. Piece i of thread t lies at (i * threads + t) * 16 bytes
 // (8 for checkpoint bytes): neighbours side by side.
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Past L1 where a warp's 16-byte pieces lie side by side; through it where every
+// other piece is another copy's (32 bytes a lane), or L2 is asked for each
+// sector twice: [32768, 2048] fp32 forward 134 us past it, 100 through it,
+// backward 207 and 135; bf16 forward 49 and 51.
+template <bool L1> __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  if (L1)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -137,8 +144,8 @@ template <int KIND> struct Slot {
     if (KIND == MEP_CKPT8) {
       copy_async8(slot + t * 8, src);
     } else {
-      copy_async16(slot + t * 16, src);
-      if (KIND == MEP_F32) copy_async16(slot + (threads + t) * 16, src + 16);
+      copy_async16<KIND == MEP_F32>(slot + t * 16, src);
+      if (KIND == MEP_F32) copy_async16<true>(slot + (threads + t) * 16, src + 16);
     }
   }
   static __device__ __forceinline__ void zero(uint32_t slot, int threads) {
@@ -645,11 +652,15 @@ Shape shape_of(long long N, int H, int J, int U) {
   s.threads = 32 * s.W * s.groups;
   return s;
 }
-// Blocks a half warp: one or two, and four for rows of more than 8192 columns.
+// Blocks a half warp: one where a row has no more than two, else two, and four
+// for rows of more than 8192 columns (backward [16384, 12288] 359 us; with two
+// blocks, 1024 threads and half the registers 483).
 int blocks_of(int H) { return H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4; }
-// Two rows a turn in bf16, whose slots are half as wide, where there are
-// registers for them. The number of CTAs must not depend on the device: the
-// workspace is sized by it.
+// Two rows a turn in bf16, up to two blocks: their sums share one barrier and
+// most of their shuffles (forward [32768, 2048] 49 us, one row a turn 62;
+// backward [65536, 7168] 443 and 552). In fp32 a row is twice the bytes and two
+// gain nothing (134 and 135 us). The number of CTAs must not depend on the
+// device: the workspace is sized by it.
 Shape backward_shape(long long N, int H, int type) {
   const int J = blocks_of(H);
   Shape s = shape_of(N, H, J, type == MEP_BF16 && H % 8 == 0 && J <= 2 ? 2 : 1);
