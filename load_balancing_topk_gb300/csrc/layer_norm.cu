@@ -34,6 +34,10 @@ namespace {
 
 constexpr int kMaxH = MEP_MAX_NORM_H;
 constexpr int kMaxWarps = 32;
+// Rows of other widths are loaded as they are used, value by value, but L2 is
+// asked for them two turns before: [32768, 2047] bf16 forward 123 -> 100 us,
+// backward 168 -> 122 (131 with one turn).
+constexpr int kTurnsToL2 = 2;
 // Turns whose rows are on their way: up to four, as many as fit `room` bytes of
 // slots a thread.
 __host__ __device__ constexpr int ahead_of(int bytes, int room) {
@@ -159,6 +163,22 @@ template <int KIND> struct Slot {
                      : "memory");
     }
   }
+  static __device__ __forceinline__ void put(uint32_t slot, int threads, const Pack<KIND>& p) {
+    const int t = threadIdx.x;
+    if constexpr (KIND == MEP_CKPT8) {
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(slot + t * 8), "r"(p.w[0]), "r"(p.w[1]) : "memory");
+    } else if constexpr (KIND == MEP_BF16) {
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot + t * 16), "r"(p.w[0]), "r"(p.w[1]),
+                   "r"(p.w[2]), "r"(p.w[3])
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(slot + (h * threads + t) * 16),
+                     "f"(p.v[4 * h]), "f"(p.v[4 * h + 1]), "f"(p.v[4 * h + 2]), "f"(p.v[4 * h + 3])
+                     : "memory");
+    }
+  }
   static __device__ __forceinline__ void fetch(uint32_t slot, int threads, Pack<KIND>& p) {
     const int t = threadIdx.x;
     if constexpr (KIND == MEP_CKPT8) {
@@ -177,6 +197,15 @@ template <int KIND> struct Slot {
     }
   }
 };
+
+// Asks L2 for the rows from r on, U or as many as there are, of `pitch` bytes
+// each, by the threads (t of n) of a group.
+template <int U>
+__device__ __forceinline__ void rows_to_l2(const void* p, unsigned r, unsigned N, long long pitch, int t, int n) {
+  const char* row = static_cast<const char*>(p) + r * pitch;
+  const long long end = (r >= N ? 0 : min(unsigned(U), N - r)) * pitch;
+  for (long long o = 128ll * t; o < end; o += 128ll * n) prefetch_l2(row + o);
+}
 
 // An SM has 512 threads with 128 registers each, in CTAs of up to 512: what they
 // wait for is copied ahead, and more of them with fewer registers issue more
@@ -275,6 +304,7 @@ __global__ void __launch_bounds__(kSmThreads)
       ahead(r + A * step, slot);
       at = at + 1 == A ? 0 : at + 1;
     } else {
+      rows_to_l2<U>(x, r + kTurnsToL2 * step, N, Slot<KIND>::pitch(H), threadIdx.x - group * 32 * W, 32 * W);
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -464,14 +494,14 @@ __global__ void __launch_bounds__(kSmThreads)
       const bool in = r + u < N;
       m1[u] = in ? __ldg(mp + u) : 0.f;
       rs1[u] = in ? __ldg(rp + u) : 0.f;
-      if (VEC && XKIND == MEP_CKPT8)
+      if (XKIND == MEP_CKPT8)
 #pragma unroll
         for (int i = 0; i < J; ++i)
           sb1[u][i] = in && there[i] ? __ldg(sp + u * ckpt_row_bytes(H) + 2 * W * i) : 1;
     }
     mp += step;
     rp += step;
-    if (VEC && XKIND == MEP_CKPT8) sp += step * ckpt_row_bytes(H);
+    if (XKIND == MEP_CKPT8) sp += step * ckpt_row_bytes(H);
   };
   if (VEC) {
 #pragma unroll
@@ -498,19 +528,28 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
       for (int i = 0; i < J; ++i) sb[u][i] = sb1[u][i];
     }
-    // both passes fetch a row's values anew (from the slots: two loads a vector)
-    const auto fetch = [&](int u, int i, Pack<KIND>& d, Pack<XKIND>& p) {
-      if (VEC) {
-        const uint32_t s = slot + (u * J + i) * threads * piece;
+    // both passes fetch a row's values anew from the slots (two loads a vector);
+    // values that had to be loaded one by one are put there by the first (fp32
+    // [32768, 2047] 195 -> 148 us)
+    const auto fetch = [&](int u, int i, bool first_pass, Pack<KIND>& d, Pack<XKIND>& p) {
+      const uint32_t s = slot + (u * J + i) * threads * piece, sx = s + threads * Slot<KIND>::bytes;
+      if (VEC || !first_pass) {
         Slot<KIND>::fetch(s, threads, d);
-        Slot<XKIND>::fetch(s + threads * Slot<KIND>::bytes, threads, p);
+        Slot<XKIND>::fetch(sx, threads, p);
         if constexpr (XKIND == MEP_CKPT8) p.step = ckpt_step(sb[u][i]);
       } else {
         d.template load<false>(dy, r + u, H, half + 2 * W * i, l);
         p.template load<false>(x, r + u, H, half + 2 * W * i, l);
+        Slot<KIND>::put(s, threads, d);
+        Slot<XKIND>::put(sx, threads, p);
       }
     };
-    if (VEC) copy_async_wait<A - 1>();
+    if (VEC) {
+      copy_async_wait<A - 1>();
+    } else {
+      rows_to_l2<U>(dy, r + kTurnsToL2 * step, N, Slot<KIND>::pitch(H), threadIdx.x - group * 32 * W, 32 * W);
+      rows_to_l2<U>(x, r + kTurnsToL2 * step, N, Slot<XKIND>::pitch(H), threadIdx.x - group * 32 * W, 32 * W);
+    }
     scalars(r + step);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -521,7 +560,7 @@ __global__ void __launch_bounds__(kSmThreads)
         for (int i = 0; i < J; ++i) {
           Pack<KIND> d;
           Pack<XKIND> p;
-          fetch(u, i, d, p);
+          fetch(u, i, true, d, p);
           const F2(&wv)[4] = weight(i);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -548,7 +587,7 @@ __global__ void __launch_bounds__(kSmThreads)
         for (int i = 0; i < J; ++i) {
           Pack<KIND> d;
           Pack<XKIND> p;
-          fetch(u, i, d, p);
+          fetch(u, i, false, d, p);
           const F2(&wv)[4] = weight(i);
           F2 v[4];
 #pragma unroll
@@ -706,9 +745,8 @@ cudaError_t run_dx(const Shape& s, const void* dy, const void* x, const void* w,
                    const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                    cudaStream_t st) {
   const int threads = s.threads;
-  const int slots = VEC ? dx_ahead<KIND, XKIND, J, U>() * U * J * threads *
-                              (Slot<KIND>::bytes + Slot<XKIND>::bytes)
-                        : 0;
+  const int slots = (VEC ? dx_ahead<KIND, XKIND, J, U>() : 1) * U * J * threads *
+                    (Slot<KIND>::bytes + Slot<XKIND>::bytes);
   const int join = s.groups > 1 ? 2 * threads * 8 * J * 4 : 0, smem = slots > join ? slots : join;
   const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
