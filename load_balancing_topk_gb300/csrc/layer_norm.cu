@@ -212,11 +212,27 @@ __device__ __forceinline__ void rows_to_l2(const void* p, unsigned r, unsigned N
 // for the same work (forward [32768, 2048] with 1024 threads, one block a half
 // warp: 62 us against 52, with y in 8 bits and that read back 131 against 115).
 constexpr int kSmThreads = 512;
+// Beyond two blocks a half warp the parameters have no room in registers: a
+// thread keeps its own in shared memory, 32 bytes a block, beside the slots
+// (from L2 they were more bytes than the rows: bf16 [16384, 12288] forward 280
+// us, 191 so, backward 345 and 222).
+template <int J> constexpr int kParamBytes = J > 2 ? 32 * J : 0;
 template <int KIND, int J, int U> __host__ __device__ constexpr int norm_ahead() {
-  return ahead_of(U * J * Slot<KIND>::bytes, 196608 / kSmThreads);
+  return ahead_of(U * J * Slot<KIND>::bytes, 196608 / kSmThreads - 2 * kParamBytes<J>);
 }
 template <int KIND, int XKIND, int J, int U> __host__ __device__ constexpr int dx_ahead() {
-  return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / kSmThreads);
+  return ahead_of(U * J * (Slot<KIND>::bytes + Slot<XKIND>::bytes), 196608 / kSmThreads - kParamBytes<J>);
+}
+__device__ __forceinline__ void put_params(uint32_t at, int threads, const F2 (&v)[4]) {
+  asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + threadIdx.x * 16), "l"(v[0].v), "l"(v[1].v) : "memory");
+  asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + (threads + threadIdx.x) * 16), "l"(v[2].v), "l"(v[3].v)
+               : "memory");
+}
+__device__ __forceinline__ void get_params(uint32_t at, int threads, F2 (&v)[4]) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v[0].v), "=l"(v[1].v) : "r"(at + threadIdx.x * 16));
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+               : "=l"(v[2].v), "=l"(v[3].v)
+               : "r"(at + (threads + threadIdx.x) * 16));
 }
 
 // J blocks a half warp, W warps a row (2 J W >= blocks of a row; FULL: equal,
@@ -278,14 +294,16 @@ __global__ void __launch_bounds__(kSmThreads)
   const int k16 = threadIdx.x & 15;
   const float inv_mine = 1.f / max(1, columns(warp));
   const float n_a = k16 < W ? columns(k16) : 0, n_c = k16 + 16 < W ? columns(k16 + 16) : 0;
-  // up to two blocks a half warp the parameters stay in registers; loaded turn
-  // by turn they came from L2, the slots leave L1 little room
   F2 wv[J > 2 ? 1 : J][4], bv[J > 2 ? 1 : J][4];
-  if (J <= 2) {
+  const uint32_t params = uint32_t(__cvta_generic_to_shared(s_dyn)) + (VEC ? A * turn_bytes * threads : 0);
 #pragma unroll
-    for (int i = 0; i < J; ++i) {
-      load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, wv[J > 2 ? 0 : i]);
-      load_params<VEC>(b, p_type, H, half + 2 * W * i, l, 0.f, bv[J > 2 ? 0 : i]);
+  for (int i = 0; i < J; ++i) {
+    const int k = J > 2 ? 0 : i;
+    load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, wv[k]);
+    load_params<VEC>(b, p_type, H, half + 2 * W * i, l, 0.f, bv[k]);
+    if (J > 2) {
+      put_params(params + (2 * i) * threads * 32, threads, wv[k]);
+      put_params(params + (2 * i + 1) * threads * 32, threads, bv[k]);
     }
   }
   T* out = y + (long long)first * H;
@@ -397,8 +415,8 @@ __global__ void __launch_bounds__(kSmThreads)
       for (int e = 0; e < JJ * U; ++e) {
         const int u = e % U, i = i0 + e / U;
         if (J > 2 && u == 0) {
-          load_params<VEC>(w, p_type, H, k.block[e], l, 1.f, wv[0]);
-          load_params<VEC>(b, p_type, H, k.block[e], l, 0.f, bv[0]);
+          get_params(params + (2 * i) * threads * 32, threads, wv[0]);
+          get_params(params + (2 * i + 1) * threads * 32, threads, bv[0]);
         }
         const F2(&wi)[4] = wv[J > 2 ? 0 : i], (&bi)[4] = bv[J > 2 ? 0 : i];
 #pragma unroll
@@ -439,23 +457,24 @@ __global__ void __launch_bounds__(kSmThreads)
   const int warp = (threadIdx.x >> 5) - group * W, half = 2 * warp + ((threadIdx.x >> 4) & 1);
   const int threads = blockDim.x;
   const float inv_h = 1.f / H;
-  // the weight stays in registers up to two blocks a half warp
   F2 dw[J][4], db[J][4], held_w[J > 2 ? 1 : J][4];
   bool there[J];
+  constexpr int piece = Slot<KIND>::bytes + Slot<XKIND>::bytes;  // a thread's bytes of a block
+  const uint32_t slots = uint32_t(__cvta_generic_to_shared(s_dyn));
+  const uint32_t params = slots + (VEC ? A : 1) * U * J * threads * piece;
   const auto weight = [&](int i) -> const F2(&)[4] {
-    if (J > 2) load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, held_w[0]);
+    if (J > 2) get_params(params + i * threads * 32, threads, held_w[0]);
     return held_w[J > 2 ? 0 : i];
   };
 #pragma unroll
   for (int i = 0; i < J; ++i) {
     there[i] = half_col<VEC>(half + 2 * W * i, l, 0) < H;
-    if (J <= 2) load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, held_w[J > 2 ? 0 : i]);
+    load_params<VEC>(w, p_type, H, half + 2 * W * i, l, 1.f, held_w[J > 2 ? 0 : i]);
+    if (J > 2) put_params(params + i * threads * 32, threads, held_w[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = db[i][j] = both(0.f);
   }
   const unsigned first = (blockIdx.x * groups + group) * U, step = gridDim.x * groups * U;
-  constexpr int piece = Slot<KIND>::bytes + Slot<XKIND>::bytes;  // a thread's bytes of a block
-  const uint32_t slots = uint32_t(__cvta_generic_to_shared(s_dyn));
   const char* dsrc = Slot<KIND>::at(dy, half_col<true>(half, l, 0)) + first * Slot<KIND>::pitch(H);
   const char* xsrc = Slot<XKIND>::at(x, half_col<true>(half, l, 0)) + first * Slot<XKIND>::pitch(H);
   const long long dstep = step * Slot<KIND>::pitch(H), xstep = step * Slot<XKIND>::pitch(H);
@@ -692,8 +711,9 @@ Shape shape_of(long long N, int H, int J, int U) {
   return s;
 }
 // Blocks a half warp: one where a row has no more than two, else two, and four
-// for rows of more than 8192 columns (backward [16384, 12288] 359 us; with two
-// blocks, 1024 threads and half the registers 483).
+// for rows of more than 8192 columns (backward [16384, 12288] 345 us before the
+// weights went to shared memory; with two blocks, 1024 threads and half the
+// registers 483).
 int blocks_of(int H) { return H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4; }
 // Two rows a turn in bf16, up to two blocks: their sums share one barrier and
 // most of their shuffles (forward [32768, 2048] 49 us, one row a turn 62;
@@ -713,7 +733,7 @@ cudaError_t run_norm(const Shape& s, const void* x, const void* w, const void* b
                      unsigned N, int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                      cudaStream_t st) {
   const int want = ceil_div(N, s.groups * U), cap = sm_count() * (kSmThreads / s.threads);
-  const int smem = VEC ? norm_ahead<KIND, J, U>() * U * J * s.threads * Slot<KIND>::bytes : 0;
+  const int smem = s.threads * ((VEC ? norm_ahead<KIND, J, U>() * U * J * Slot<KIND>::bytes : 0) + 2 * kParamBytes<J>);
   const auto kernel = k_norm<T, KIND, VEC, FULL, KEEP, J, U>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
   return launch_pdl(kernel, dim3(want < cap ? want : cap), dim3(s.threads), smem, st,
@@ -745,8 +765,8 @@ cudaError_t run_dx(const Shape& s, const void* dy, const void* x, const void* w,
                    const float* mean, const float* rstd, unsigned N, int H, void* dx, float* ws,
                    cudaStream_t st) {
   const int threads = s.threads;
-  const int slots = (VEC ? dx_ahead<KIND, XKIND, J, U>() : 1) * U * J * threads *
-                    (Slot<KIND>::bytes + Slot<XKIND>::bytes);
+  const int slots = threads * ((VEC ? dx_ahead<KIND, XKIND, J, U>() : 1) * U * J *
+                                   (Slot<KIND>::bytes + Slot<XKIND>::bytes) + kParamBytes<J>);
   const int join = s.groups > 1 ? 2 * threads * 8 * J * 4 : 0, smem = slots > join ? slots : join;
   const auto kernel = k_norm_dx<T, KIND, XKIND, VEC, J, U>;
   if (allow_smem(reinterpret_cast<const void*>(kernel), smem)) return cudaErrorInvalidValue;
