@@ -713,8 +713,14 @@ Shape shape_of(long long N, int H, int J, int U) {
 // Blocks a half warp: one where a row has no more than two, else two, and four
 // for rows of more than 8192 columns (backward [16384, 12288] 345 us before the
 // weights went to shared memory; with two blocks, 1024 threads and half the
-// registers 483).
-int blocks_of(int H) { return H <= 2 * kCkptBlock ? 1 : H <= 64 * kCkptBlock ? 2 : 4; }
+// registers 483). Four also where a row would take 9 or 10 warps, of which an SM
+// has room for 16: bf16 [20000, 5120] backward 121 us, with two 133, forward
+// with a checkpoint and its reading 174 and 189 (without 91 and 89), fp32 forward
+// 133 and 154; at 12 warps, [20000, 6144], backward 152 and 142.
+int blocks_of(int H) {
+  const int nb = ceil_div(H, kCkptBlock), warps = ceil_div(nb, 4);
+  return nb <= 2 ? 1 : warps > 16 || warps == 9 || warps == 10 ? 4 : 2;
+}
 // Two rows a turn in bf16, up to two blocks: their sums share one barrier and
 // most of their shuffles (forward [32768, 2048] 49 us, one row a turn 62;
 // backward [65536, 7168] 443 and 552). In fp32 a row is twice the bytes and two

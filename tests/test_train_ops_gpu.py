@@ -257,6 +257,23 @@ def test_norm_backward(H, dt, ckpt):
     _check_backward(dy, x, w, mean, rstd, dt, ckpt)
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [2050, 4099, 4104, 5120, 5128, 8200])
+def test_norm_wide_rows_over_many_turns(H, dt):
+    N = 1501
+    x, dy = _x(N, H, dt, H, shift=0.5), _x(N, H, dt, H + 1)
+    w = 1 + 0.3 * torch.randn(H, generator=torch.Generator().manual_seed(H))
+    yc = torch.full((N, mep.ckpt_row_bytes(H)), 77, dtype=torch.uint8, device=DEV)
+    y, mean, rstd = mep.mep_layer_norm(x.to(DEV), w.to(DEV), None, y_ckpt=yc)
+    want, m, r, ty, tm, tr = _norm_tol(_np(x), _np(w), np.zeros(H), 1e-5, dt)
+    _within(mean, m, tm, "mean")
+    _within(rstd, r, tr, "rstd")
+    _within(y, want, ty, "y")
+    assert torch.equal(yc, mep.mep_ckpt_save(y))  # (rows against the plain form: test_ckpt_rows_and_values)
+    for ckpt in (False, True):
+        _check_backward(dy, x, w, mean, rstd, dt, ckpt)
+
+
 def test_norm_rows_16_bytes_into_their_storage():
     N, H = 70, 272
     x, y, dy, dx = (_rows_view((N, H), BF16, 16) for _ in range(4))
