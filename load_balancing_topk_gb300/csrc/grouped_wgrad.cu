@@ -232,8 +232,11 @@ __device__ __forceinline__ Row read_row(const int32_t* __restrict__ cu, int w, i
 #pragma unroll 4
   for (int r = r0; r < r1; ++r) {
     const long long p = (long long)r * G + j;
-    const int hi = cu[p], lo = j == 0 ? 0 : cu[p - 1], len = hi - lo;
-    if (len < 0 || (j == G - 1 && hi != SK)) row.bad = true;
+    // (compared, not subtracted: the difference of two ends of a corrupt row may wrap)
+    const int hi = cu[p], lo = j == 0 ? 0 : cu[p - 1];
+    const bool bad = lo < 0 || hi < lo || hi > SK || (j == G - 1 && hi != SK);
+    row.bad |= bad;
+    const int len = bad ? 0 : hi - lo;
     if (len > 0) {
       const int2 seg = make_int2(int((long long)r * SK + lo), len);
       if (row.segments == 0) row.first = seg;

@@ -219,6 +219,23 @@ def test_wgrad_malformed_tables(rows):
     assert (home == 5).all() and int(status.item()) == mep.STATUS_CODE["MEP_ERR_BAD_SEQLENS"]
 
 
+@pytest.mark.parametrize("E,B", [(3, 1), (2, 2), (1100, 0)], ids=["a_slot", "two_slots", "more_weight_rows_than_threads"])
+def test_wgrad_malformed_tables_whose_differences_wrap(E, B):
+    """Ends far apart: taken in 32 bits, every difference of this row is positive and its last end is S*K."""
+    ends = [2 ** 31 - 1, -2 ** 31, -1, 64]
+    differences = np.diff(np.array([0] + ends, np.int64)).astype(np.int32)
+    assert (differences > 0).all()
+    # (further groups without rows in front, where the table has more than four)
+    cu = torch.tensor([[0] * (E + B - 4) + ends], dtype=torch.int32, device=DEV)
+    home = torch.full((E, 16, 8), 5.0, device=DEV)
+    slot = torch.full((1, B, 16, 8), 5.0, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x, dy = torch.ones(64, 16, dtype=BF16, device=DEV), torch.ones(64, 8, dtype=BF16, device=DEV)
+    mep.mep_grouped_wgrad(x, dy, cu, home, slot if B else None, status, 1, 64, 1)
+    assert int(status.item()) == mep.STATUS_CODE["MEP_ERR_BAD_SEQLENS"]
+    assert (home == 5).all() and (slot == 5).all()
+
+
 def test_wgrad_refusals():
     x, dy = torch.ones(64, 16, dtype=BF16, device=DEV), torch.ones(64, 8, dtype=BF16, device=DEV)
     cu = torch.tensor([[10, 20, 64]], dtype=torch.int32, device=DEV)
