@@ -425,7 +425,8 @@ MEP_API int mep_layer_norm(const void* x, int x_type, const void* weight, const 
  *   weight   bf16 or fp32 [H]      p_type; NULL: 1
  *   mean, rstd  fp32 [N]           from mep_layer_norm
  *   ws       device scratch of >= mep_layer_norm_backward_workspace_bytes
- *            bytes; may be NULL when dweight and dbias are
+ *            bytes; may be NULL when dweight and dbias are. The size does not
+ *            fall with N: scratch for N rows serves every call of fewer
  *   dx       dy_type [N, H]        output
  *   dweight, dbias  fp32 [H]       outputs (accumulate != 0: added to); each
  *                                  may be NULL

@@ -514,6 +514,7 @@ def ckpt_row_bytes(C: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
+    """Bytes of mep_layer_norm_backward's workspace for up to N rows of H columns."""
     out = ctypes.c_size_t(0)
     _check("mep_layer_norm_backward_workspace_bytes",
            load_library().mep_layer_norm_backward_workspace_bytes(int(N), int(H), ctypes.byref(out)))
@@ -522,6 +523,7 @@ def layer_norm_backward_workspace_bytes(N: int, H: int) -> int:
 
 @functools.lru_cache(maxsize=256)
 def grouped_wgrad_workspace_bytes(R: int, S: int, K: int, E: int, B: int, H: int, Hp: int) -> int:
+    """Bytes of mep_grouped_wgrad's workspace for up to S tokens a rank."""
     out = ctypes.c_size_t(0)
     _check("mep_grouped_wgrad_workspace_bytes",
            load_library().mep_grouped_wgrad_workspace_bytes(R, S, K, E, B, H, Hp, ctypes.byref(out)))

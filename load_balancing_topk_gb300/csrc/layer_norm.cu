@@ -733,6 +733,18 @@ Shape backward_shape(long long N, int H, int type) {
   s.parts = want < cap ? want : cap;
   return s;
 }
+// The most CTAs of any call of up to N rows. They are not most at N itself:
+// with fewer rows a CTA holds fewer row groups, and up to three times as many
+// CTAs fit. A workspace for the longest batch has to serve every shorter one.
+int backward_parts(long long N, int H, int type) {
+  int most = 0;
+  for (;;) {
+    const Shape s = backward_shape(N, H, type);
+    most = s.parts > most ? s.parts : most;
+    if (s.groups == 1) return most;
+    N = 152ll * s.U * s.groups - 1;  // the longest call of smaller CTAs: with as large ones, fewer rows take fewer
+  }
+}
 
 template <typename T, int KIND, bool VEC, bool FULL, bool KEEP, int J, int U>
 cudaError_t run_norm(const Shape& s, const void* x, const void* w, const void* b, int p_type, float eps,
@@ -817,7 +829,7 @@ extern "C" int mep_layer_norm(const void* x, int x_type, const void* weight, con
 
 extern "C" int mep_layer_norm_backward_workspace_bytes(int64_t N, int64_t H, size_t* bytes) {
   if (bytes == nullptr || norm_check(MEP_F32, N, H, MEP_F32) != MEP_OK) return MEP_ERR_INVALID_ARG;
-  const int a = backward_shape(N, int(H), MEP_BF16).parts, b = backward_shape(N, int(H), MEP_F32).parts;
+  const int a = backward_parts(N, int(H), MEP_BF16), b = backward_parts(N, int(H), MEP_F32);
   *bytes = size_t(a > b ? a : b) * 2 * H * sizeof(float);
   return MEP_OK;
 }

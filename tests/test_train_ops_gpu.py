@@ -335,6 +335,20 @@ def test_norm_gradients_add_to_what_is_there_and_repeat_their_bits():
     assert torch.equal(w2, 3.0 + dw) and torch.equal(b2, -5.0 + db)
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("H", [128, 2048, 4099])
+def test_norm_one_workspace_for_batches_of_any_length(H, dt):
+    long = 20000
+    ws = torch.empty(mep.layer_norm_backward_workspace_bytes(long, H), dtype=torch.uint8, device=DEV)
+    x, dy = (torch.randn(long, H, device=DEV, generator=torch.Generator(DEV).manual_seed(i)).to(dt) for i in (1, 2))
+    _, mean, rstd = mep.mep_layer_norm(x)
+    for n in (long, 4863, 1300, 607, 455, 3):
+        ws.fill_(255)  # NaN, were any of it read before it is written
+        got = mep.mep_layer_norm_backward(dy[:n], x[:n], None, mean[:n], rstd[:n], workspace=ws)
+        want = mep.mep_layer_norm_backward(dy[:n], x[:n], None, mean[:n], rstd[:n])
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and not got[1].isnan().any()
+
+
 def test_norm_without_rows():
     x = torch.empty(0, 64, dtype=BF16, device=DEV)
     y, mean, rstd = mep.mep_layer_norm(x)

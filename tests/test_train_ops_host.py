@@ -66,6 +66,22 @@ def test_layer_norm_rejects_bad_args(lib):
     assert bwd(N=0, dw=None, db=None) == 0
 
 
+# around every length at which the backward pass goes over to larger CTAs (152 * rows a turn * row groups), and beyond
+LENGTHS = sorted({0, 1, 2, 1 << 20, (1 << 31) - 1, *(max(0, 152 * k + d) for k in range(1, 33) for d in (-1, 0, 1)), *range(5, 40000, 997)})
+
+
+@pytest.mark.parametrize("H", [1, 128, 257, 640, 1001, 1408, 2048, 4099, 4104, 5120, 6144, 7168, 12288, 16384])
+def test_a_norm_workspace_for_many_rows_serves_fewer(lib, H):
+    sizes = [mep.layer_norm_backward_workspace_bytes(n, H) for n in LENGTHS]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("H,Hp", [(8, 8), (128, 64), (520, 1160), (2048, 1408)])
+def test_a_wgrad_workspace_for_many_rows_serves_fewer(lib, H, Hp):
+    sizes = [mep.grouped_wgrad_workspace_bytes(4, S, 2, 8, 4, H, Hp) for S in (0, 1, 2, 63, 64, 65, 500, 4096, 1 << 20)]
+    assert sizes == sorted(sizes)
+
+
 def test_swiglu_rejects_bad_args(lib):
     for args in ((None, 4, 64, 16, None), (16, 4, 64, None, None), (24, 4, 64, 16, None), (16, 4, 64, 24, None),
                  (16, 4, 64, 16, 24), (16, -1, 64, 16, None), (16, 1 << 30, 64, 16, None), (16, 4, 0, 16, None),
