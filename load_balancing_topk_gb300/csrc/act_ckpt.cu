@@ -112,12 +112,37 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// 1 / (1 + e^-g); the quotient to 2 ulp (0 where e^-g overflows)
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-__device__ __forceinline__ F2 sigmoid2(F2 g) { return pair(sigmoid(g.x()), sigmoid(g.y())); }
+// sigmoid(g) = k / (k + k e^-g) with k = 2^-24: e^-g stays below 2^126, where
+// the reciprocal instruction still has a result, down to g = -104, where
+// sigmoid itself leaves fp32's range. Without k it was flushed to 0 below g =
+// -87.3 already, which u = 1e38 makes an activation of -87; to scale costs
+// nothing, as k e^-g = 2^(-g log2 e - 24) is one fma where e^-g is a product.
+// (e^-|g| and its numerator by the sign of g: 780 us for the activation forward
+// and backward on [196608, 2, 1408], this 745.) Relative error, in units of
+// 2^-24: 17 + 2 |g| of the exponent, 3 of ex2, 1 of the sum, 2 of the reciprocal.
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ F2 sigmoid2(F2 g) {
+  constexpr float kLog2e = 1.44269504f, k = 1.f / (1 << 24);
+  const F2 v = fma2(g, both(-kLog2e), both(-24.f));
+  const F2 y = add2(pair(ex2(v.x()), ex2(v.y())), both(k));
+  return mul2(pair(rcp(y.x()), rcp(y.y())), both(k));
+}
 
+// (five CTAs an SM for both: 48 registers, left to themselves 50, four CTAs:
+// forward with a checkpoint on [196608, 2, 1408] 338 us and 352, backward from
+// it 409 and 432; without vectors the forward pass has 40, six CTAs, and given
+// more ran slower, on [65536, 2, 1407] 190 us for 176)
 template <bool VEC, bool CKPT, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, VEC ? 5 : 6)
     k_swiglu(const __nv_bfloat16* __restrict__ gu, Blocks blocks, int F,
              __nv_bfloat16* __restrict__ a, uint8_t* __restrict__ ckpt) {
   pdl_wait();
@@ -160,7 +185,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 template <int KIND, bool VEC, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, KIND == MEP_CKPT8 ? 5 : 1)
     k_swiglu_backward(const __nv_bfloat16* __restrict__ da, const void* __restrict__ gu,
                       Blocks blocks, int F, __nv_bfloat16* __restrict__ dgu,
                       __nv_bfloat16* __restrict__ a) {

@@ -464,6 +464,32 @@ def test_swiglu_far_values():
     _within(dgu[:, F:], du, tu, "du")
 
 
+def test_swiglu_gates_whose_sigmoid_is_tiny():
+    """Gates down to -104, where sigmoid leaves fp32's range, beside values that make their products large again.
+
+    sigmoid(g) = k / (k + 2^(-g log2 e - 24)): the exponent is off by its rounding, 2^-24 (24 + 1.45 |g|), and that of
+    log2 e, 2^-24 * 1.45 |g|, both times ln 2 in the result; ex2 adds 2^-22.5, the sum 2^-24, the reciprocal 2^-23: at most
+    U (23 + 2 |g|). Subnormal results are off by 2^-149 at most instead, and so are products of them."""
+    g = torch.linspace(-104, -80, 97)
+    u = torch.tensor([1.0, -1e30, 1e38])
+    G, Uu = torch.meshgrid(g, u, indexing="ij")
+    F = G.numel()
+    gu = torch.cat([G.reshape(-1), Uu.reshape(-1)]).view(1, 2 * F).bfloat16()
+    gn, un = _np(gu)[:, :F], _np(gu)[:, F:]
+    es, sub = U * (23 + 2 * np.abs(gn)), (1 + np.abs(gn)) * 2.0 ** -149
+    want = ref.swiglu(gn, un)
+    e = np.abs(want) * (es + 3 * U) + 2 * np.abs(un) * sub
+    for a in (mep.mep_swiglu(gu.to(DEV)), mep.mep_swiglu_backward(torch.ones(1, F, dtype=BF16, device=DEV), gu.to(DEV))[1]):
+        _within(a, want, e + _round(BF16, np.abs(want) + e), "a")
+    dgu, _ = mep.mep_swiglu_backward(torch.ones(1, F, dtype=BF16, device=DEV), gu.to(DEV))
+    dg, du = ref.swiglu_backward(np.ones_like(gn), gn, un)
+    eg = np.abs(un) * ref.sigmoid(gn) * (1 + np.abs(gn)) * (es + 6 * U) + 2 * (1 + np.abs(un)) * sub
+    eu = np.abs(du) * (es + 3 * U) + 2 * sub
+    _within(dgu[:, :F], dg, eg + _round(BF16, np.abs(dg) + eg), "dg")
+    _within(dgu[:, F:], du, eu + _round(BF16, np.abs(du) + eu), "du")
+    assert (_np(dgu)[:, F:][gn > -90] != 0).all()
+
+
 def test_swiglu_overflow_stays_visible():
     gu = torch.randn(4, 512, generator=torch.Generator().manual_seed(0)).bfloat16().to(DEV)
     gu[1, 5], gu[2, 256 + 200] = float("inf"), float("nan")
