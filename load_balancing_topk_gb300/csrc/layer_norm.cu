@@ -713,21 +713,28 @@ Shape shape_of(long long N, int H, int J, int U) {
 // Blocks a half warp: one where a row has no more than two, else two, and four
 // for rows of more than 8192 columns (backward [16384, 12288] 345 us before the
 // weights went to shared memory; with two blocks, 1024 threads and half the
-// registers 483). Four also where a row would take 9 or 10 warps, of which an SM
-// has room for 16: bf16 [20000, 5120] backward 121 us, with two 133, forward
-// with a checkpoint and its reading 174 and 189 (without 91 and 89), fp32 forward
-// 133 and 154; at 12 warps, [20000, 6144], backward 152 and 142.
-int blocks_of(int H) {
+// registers 483). Four also (`four`) where a row would take 9 or 10 warps, 4097
+// to 5120 columns, of which an SM has room for 16; at 12 warps, [20000,
+// 6144], bf16 backward from 8 bits 152 us and with two 142. Over those widths, of 20000 rows, in
+// us with four and with two blocks:
+//   forward     bf16 84-91 and 88-113, fp32 115-133 and 147-162, odd widths
+//               137-158 and 215-240; with one or two checkpoints alike
+//   backward    bf16 103-115 and 111-125, from 8 bits 117-122 and 131-135,
+//               odd widths 201-223 and 257-281, but from 8 bits 303-317 and
+//               275-297: two
+//               fp32 179-197 and 177-197, from 8 bits 193-211 and 162-177,
+//               odd widths 255-332 and 234-262: two
+int blocks_of(int H, bool four) {
   const int nb = ceil_div(H, kCkptBlock), warps = ceil_div(nb, 4);
-  return nb <= 2 ? 1 : warps > 16 || warps == 9 || warps == 10 ? 4 : 2;
+  return nb <= 2 ? 1 : warps > 16 || (four && (warps == 9 || warps == 10)) ? 4 : 2;
 }
 // Two rows a turn in bf16, up to two blocks: their sums share one barrier and
 // most of their shuffles (forward [32768, 2048] 49 us, one row a turn 62;
 // backward [65536, 7168] 443 and 552). In fp32 a row is twice the bytes and two
 // gain nothing (134 and 135 us). The number of CTAs must not depend on the
 // device: the workspace is sized by it.
-Shape backward_shape(long long N, int H, int type) {
-  const int J = blocks_of(H);
+Shape backward_shape(long long N, int H, int type, int x_type) {
+  const int J = blocks_of(H, type == MEP_BF16 && (H % 8 == 0 || x_type != MEP_CKPT8));
   Shape s = shape_of(N, H, J, type == MEP_BF16 && H % 8 == 0 && J <= 2 ? 2 : 1);
   const int want = ceil_div(N < 1 ? 1 : N, s.U * s.groups), cap = 152 * (kSmThreads / s.threads);
   s.parts = want < cap ? want : cap;
@@ -736,10 +743,10 @@ Shape backward_shape(long long N, int H, int type) {
 // The most CTAs of any call of up to N rows. They are not most at N itself:
 // with fewer rows a CTA holds fewer row groups, and up to three times as many
 // CTAs fit. A workspace for the longest batch has to serve every shorter one.
-int backward_parts(long long N, int H, int type) {
+int backward_parts(long long N, int H, int type, int x_type) {
   int most = 0;
   for (;;) {
-    const Shape s = backward_shape(N, H, type);
+    const Shape s = backward_shape(N, H, type, x_type);
     most = s.parts > most ? s.parts : most;
     if (s.groups == 1) return most;
     N = 152ll * s.U * s.groups - 1;  // the longest call of smaller CTAs: with as large ones, fewer rows take fewer
@@ -764,7 +771,7 @@ cudaError_t pick_norm(const void* x, const void* w, const void* b, int p_type, f
                       int H, void* y, float* mean, float* rstd, uint8_t* xc, uint8_t* yc,
                       cudaStream_t st) {
   constexpr int U = KIND == MEP_BF16 ? 2 : 1;
-  const int J = blocks_of(H);
+  const int J = blocks_of(H, true);
   const Shape s = shape_of(N, H, J, U);
   // Without the edge and checkpoint tests the forward pass issues a fifth less
   // ([32768, 2048] 61 -> 51 us, [65536, 7168] 404 -> 334 us); the backward
@@ -829,8 +836,13 @@ extern "C" int mep_layer_norm(const void* x, int x_type, const void* weight, con
 
 extern "C" int mep_layer_norm_backward_workspace_bytes(int64_t N, int64_t H, size_t* bytes) {
   if (bytes == nullptr || norm_check(MEP_F32, N, H, MEP_F32) != MEP_OK) return MEP_ERR_INVALID_ARG;
-  const int a = backward_parts(N, int(H), MEP_BF16), b = backward_parts(N, int(H), MEP_F32);
-  *bytes = size_t(a > b ? a : b) * 2 * H * sizeof(float);
+  int most = 0;
+  for (int type : {MEP_BF16, MEP_F32})
+    for (int x_type : {type, MEP_CKPT8}) {
+      const int n = backward_parts(N, int(H), type, x_type);
+      most = n > most ? n : most;
+    }
+  *bytes = size_t(most) * 2 * H * sizeof(float);
   return MEP_OK;
 }
 
@@ -852,7 +864,7 @@ extern "C" int mep_layer_norm_backward(const void* dy, int dy_type, const void* 
                         static_cast<const void*>(dweight), static_cast<const void*>(dbias)})
     if (!aligned16(p)) return MEP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const Shape s = backward_shape(N, int(H), dy_type);
+  const Shape s = backward_shape(N, int(H), dy_type, x_type);
   float* part = params ? static_cast<float*>(ws) : nullptr;
   const bool vec = H % 8 == 0, kept = x_type == MEP_CKPT8;
   if (N > 0) {
