@@ -40,6 +40,10 @@
  *     the host. Work is enqueued on `stream` (a cudaStream_t passed as void*;
  *     NULL = the legacy default stream) and runs asynchronously.
  *   - Tensors are dense, row-major, and must start on a 16-byte boundary.
+ *     Exception: in mep_ckpt_save / load, mep_layer_norm and mep_swiglu and
+ *     their backward passes, where the columns (C, H, F) are not a multiple of
+ *     8, tensors need only start on a boundary of their element (any run of
+ *     rows of a larger tensor does), except for checkpoint rows and workspaces.
  *   - bf16 data is passed as 16-bit bit patterns (mep_bf16).
  *   - The int return value reports only the checks made on the host before
  *     anything is enqueued (MEP_ERR_INVALID_ARG) and launch failures

@@ -247,7 +247,7 @@ static int ckpt_check(const void* x, int type, int64_t N, int64_t C, const void*
   if (N < 0 || N > 0x7fffffffLL || C < 1 || C > MEP_MAX_CKPT_C) return MEP_ERR_INVALID_ARG;
   if (type != MEP_BF16 && type != MEP_F32) return MEP_ERR_INVALID_ARG;
   if (N == 0) return MEP_OK;
-  if (x == nullptr || ckpt == nullptr || !aligned16(x) || !aligned16(ckpt)) return MEP_ERR_INVALID_ARG;
+  if (x == nullptr || ckpt == nullptr || !may_start(x, type, C) || !aligned16(ckpt)) return MEP_ERR_INVALID_ARG;
   return MEP_OK;
 }
 
@@ -294,7 +294,7 @@ extern "C" int mep_swiglu(const mep_bf16* gu, int64_t rows, int64_t F, mep_bf16*
                           void* stream) {
   if (rows < 0 || rows > 0x3fffffffLL || F < 1 || F > MEP_MAX_CKPT_C) return MEP_ERR_INVALID_ARG;
   if (rows == 0) return MEP_OK;
-  if (gu == nullptr || a == nullptr || !aligned16(gu) || !aligned16(a) || !aligned16(ckpt))
+  if (gu == nullptr || a == nullptr || !may_start(gu, MEP_BF16, F) || !may_start(a, MEP_BF16, F) || !aligned16(ckpt))
     return MEP_ERR_INVALID_ARG;
   constexpr int U = kSwigluUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -315,8 +315,8 @@ extern "C" int mep_swiglu_backward(const mep_bf16* da, const void* gu, int gu_ty
   if (rows < 0 || rows > 0x3fffffffLL || F < 1 || F > MEP_MAX_CKPT_C) return MEP_ERR_INVALID_ARG;
   if (gu_type != MEP_BF16 && gu_type != MEP_CKPT8) return MEP_ERR_INVALID_ARG;
   if (rows == 0) return MEP_OK;
-  if (da == nullptr || gu == nullptr || dgu == nullptr || !aligned16(da) || !aligned16(gu) ||
-      !aligned16(dgu) || !aligned16(a))
+  if (da == nullptr || gu == nullptr || dgu == nullptr || !may_start(da, MEP_BF16, F) ||
+      !may_start(gu, gu_type, F) || !may_start(dgu, MEP_BF16, F) || !may_start(a, MEP_BF16, F))
     return MEP_ERR_INVALID_ARG;
   constexpr int U = kSwigluUnroll;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

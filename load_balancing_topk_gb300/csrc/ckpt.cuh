@@ -58,6 +58,15 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
   return __float2bfloat16_rn(v);
 }
 
+// Where a tensor of `type` with these columns may start: rows of a multiple of
+// 8 columns are read and written in 16-byte vectors, others element by element,
+// so that any run of their rows is as good; checkpoint rows are whole vectors
+// at any width.
+inline bool may_start(const void* p, int type, long long columns) {
+  const uintptr_t step = columns % 8 == 0 || type == MEP_CKPT8 ? 16 : type == MEP_BF16 ? 2 : 4;
+  return reinterpret_cast<uintptr_t>(p) % step == 0;
+}
+
 // ---------------------------------------------------------------------------
 // Two fp32 values in one 64-bit register, and operations on both at once, each
 // rounded as the single form is.

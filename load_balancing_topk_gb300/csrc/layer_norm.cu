@@ -821,10 +821,10 @@ extern "C" int mep_layer_norm(const void* x, int x_type, const void* weight, con
   if (norm_check(x_type, N, H, p_type) != MEP_OK || !(eps >= 0.f)) return MEP_ERR_INVALID_ARG;
   if (N == 0) return MEP_OK;
   if (x == nullptr || y == nullptr || mean == nullptr || rstd == nullptr) return MEP_ERR_INVALID_ARG;
-  for (const void* p : {x, weight, bias, static_cast<const void*>(y), static_cast<const void*>(mean),
-                        static_cast<const void*>(rstd), static_cast<const void*>(x_ckpt),
-                        static_cast<const void*>(y_ckpt)})
-    if (!aligned16(p)) return MEP_ERR_INVALID_ARG;
+  if (!may_start(x, x_type, H) || !may_start(y, x_type, H) || !may_start(weight, p_type, H) ||
+      !may_start(bias, p_type, H) || !may_start(mean, MEP_F32, H) || !may_start(rstd, MEP_F32, H) ||
+      !aligned16(x_ckpt) || !aligned16(y_ckpt))
+    return MEP_ERR_INVALID_ARG;
   const bool vec = H % 8 == 0;
   const auto run = x_type == MEP_BF16
                        ? (vec ? pick_norm<__nv_bfloat16, MEP_BF16, true> : pick_norm<__nv_bfloat16, MEP_BF16, false>)
@@ -859,10 +859,10 @@ extern "C" int mep_layer_norm_backward(const void* dy, int dy_type, const void* 
     return MEP_ERR_INVALID_ARG;
   const bool params = dweight != nullptr || dbias != nullptr;
   if (params && (ws == nullptr || ws_bytes < need)) return MEP_ERR_INVALID_ARG;
-  for (const void* p : {dy, x, weight, static_cast<const void*>(mean), static_cast<const void*>(rstd),
-                        static_cast<const void*>(ws), static_cast<const void*>(dx),
-                        static_cast<const void*>(dweight), static_cast<const void*>(dbias)})
-    if (!aligned16(p)) return MEP_ERR_INVALID_ARG;
+  if (!may_start(dy, dy_type, H) || !may_start(x, x_type, H) || !may_start(dx, dy_type, H) ||
+      !may_start(weight, p_type, H) || !may_start(mean, MEP_F32, H) || !may_start(rstd, MEP_F32, H) ||
+      !may_start(dweight, MEP_F32, H) || !may_start(dbias, MEP_F32, H) || !aligned16(ws))
+    return MEP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Shape s = backward_shape(N, int(H), dy_type, x_type);
   float* part = params ? static_cast<float*>(ws) : nullptr;

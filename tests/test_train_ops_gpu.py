@@ -511,6 +511,55 @@ def test_swiglu_gradients_against_differences():
     assert abs(num - (_np(dgu) * d).sum()) <= 2.0 ** -8 * np.abs(_np(dgu) * d).sum()
 
 
+# ------------------------------------------------------------------------------------------------ runs of rows
+
+
+@pytest.mark.parametrize("first", range(1, 8))
+@pytest.mark.parametrize("C", [9, 333, 2050])
+def test_a_run_of_rows_of_a_larger_tensor(C, first):
+    """Rows [first, first + n) of odd-width tensors, in place: results of the same rows on their own, nothing else touched."""
+    n, total = 21, 40
+    run = slice(first, first + n)
+
+    def own(t):
+        return t[run].clone()
+
+    def untouched(t, v):
+        return (t[:first] == v).all() and (t[first + n:] == v).all()
+
+    for dt in (BF16, F32):
+        x, dy = _x(total, C, dt, C + first).to(DEV), _x(total, C, dt, C + first + 1).to(DEV)
+        params = torch.randn(2 * C, generator=torch.Generator().manual_seed(C)).to(DEV)
+        w, b = params[:C], params[C:]  # one behind the other in one buffer
+        y, dx = torch.full_like(x, 3.0), torch.full_like(x, 3.0)
+        mean, rstd = torch.full((2, total), 3.0, device=DEV)
+        xc = torch.empty((n, mep.ckpt_row_bytes(C)), dtype=torch.uint8, device=DEV)
+        mep.mep_layer_norm(x[run], w, b, y=y[run], mean=mean[run], rstd=rstd[run], x_ckpt=xc)
+        want = mep.mep_layer_norm(own(x), w.clone(), b.clone())
+        assert all(torch.equal(a[run], v) and untouched(a, 3.0) for a, v in zip((y, mean, rstd), want))
+        assert torch.equal(xc, mep.mep_ckpt_save(x[run])) and torch.equal(xc, mep.mep_ckpt_save(own(x)))
+        back = torch.full_like(x, 3.0)
+        mep.mep_ckpt_load(xc, C, back[run])
+        assert torch.equal(back[run], mep.mep_ckpt_load(xc, C, dtype=dt)) and untouched(back, 3.0)
+        for src in (x[run], xc):
+            grads = torch.full((2 * C + 1,), 3.0, device=DEV)
+            mep.mep_layer_norm_backward(dy[run], src, w, mean[run], rstd[run], dx=dx[run], dweight=grads[:C],
+                                        dbias=grads[C:2 * C])
+            want = mep.mep_layer_norm_backward(own(dy), src.clone(), w.clone(), own(mean), own(rstd))
+            assert torch.equal(dx[run], want[0]) and untouched(dx, 3.0)
+            assert torch.equal(grads[:C], want[1]) and torch.equal(grads[C:2 * C], want[2]) and grads[2 * C] == 3
+    gu, da = _x(total, 2 * C, BF16, C + first + 2).to(DEV), _x(total, C, BF16, C + first + 3).to(DEV)
+    a, again, dgu = torch.full_like(da, 3.0), torch.full_like(da, 3.0), torch.full_like(gu, 3.0)
+    gc = torch.empty((n, 2, mep.ckpt_row_bytes(C)), dtype=torch.uint8, device=DEV)
+    mep.mep_swiglu(gu[run], a=a[run], ckpt=gc)
+    assert torch.equal(a[run], mep.mep_swiglu(own(gu))) and untouched(a, 3.0)
+    for src in (gu[run], gc):
+        mep.mep_swiglu_backward(da[run], src, dgu=dgu[run], a=again[run])
+        want = mep.mep_swiglu_backward(own(da), src.clone())
+        assert torch.equal(dgu[run], want[0]) and torch.equal(again[run], want[1])
+        assert untouched(dgu, 3.0) and untouched(again, 3.0)
+
+
 # ------------------------------------------------------------------------------------------------ streams, graphs, refusals
 
 

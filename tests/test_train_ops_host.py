@@ -111,3 +111,27 @@ def test_grouped_wgrad_rejects_bad_args(lib):
     out = ctypes.c_size_t(0)
     assert lib.mep_grouped_wgrad_workspace_bytes(2, 4, 2, 8, 4, 64, 64, None) == BAD
     assert lib.mep_grouped_wgrad_workspace_bytes(0, 4, 2, 8, 4, 64, 64, ctypes.byref(out)) == BAD
+
+
+def test_where_tensors_may_start(lib):
+    """Whole vectors (a multiple of 8 columns): 16 bytes; other widths: the element; checkpoint rows and workspaces 16.
+    (Only refusals: what is allowed is launched in the GPU tests.)"""
+    for C in (63, 65, 1):
+        assert lib.mep_ckpt_save(17, BF16, 4, C, 32, None) == BAD
+        assert lib.mep_ckpt_save(18, F32, 4, C, 32, None) == BAD
+        assert lib.mep_ckpt_save(16, BF16, 4, C, 34, None) == BAD
+        assert lib.mep_ckpt_load(40, 4, C, BF16, 16, None) == BAD
+        assert lib.mep_swiglu(17, 4, C, 16, None, None) == BAD
+        assert lib.mep_swiglu(16, 4, C, 17, None, None) == BAD
+        assert lib.mep_swiglu(16, 4, C, 16, 24, None) == BAD
+        assert lib.mep_swiglu_backward(16, 24, CKPT8, 4, C, 16, 16, None) == BAD
+        assert lib.mep_swiglu_backward(16, 17, BF16, 4, C, 16, 16, None) == BAD
+        for at in range(4):  # x, y, mean, rstd
+            p = [16] * 4
+            p[at] = 18
+            assert lib.mep_layer_norm(p[0], F32, 16, 16, F32, 1e-5, 4, C, p[1], p[2], p[3], None, None, None) == BAD
+        for w, b, xc, yc in ((18, 16, None, None), (16, 18, None, None), (16, 16, 36, None), (16, 16, None, 36)):
+            assert lib.mep_layer_norm(16, BF16, w, b, F32, 1e-5, 4, C, 16, 16, 16, xc, yc, None) == BAD
+        assert lib.mep_layer_norm_backward(16, BF16, 24, CKPT8, 16, F32, 16, 16, 4, C, 256, 1 << 20, 16, 16, 16, 0, None) == BAD
+        assert lib.mep_layer_norm_backward(16, BF16, 16, BF16, 16, F32, 16, 16, 4, C, 260, 1 << 20, 16, 16, 16, 0, None) == BAD
+        assert lib.mep_layer_norm_backward(16, BF16, 16, BF16, 16, F32, 16, 16, 4, C, 256, 1 << 20, 16, 18, 16, 0, None) == BAD
