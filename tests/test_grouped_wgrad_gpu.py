@@ -123,6 +123,97 @@ def test_wgrad_wide():
     _case(_cu([[100, 28]]), 1, 72, 7168, 1, True, False)
 
 
+@pytest.mark.parametrize("kept", [False, True], ids=["as_it_was", "kept"])
+@pytest.mark.parametrize("rows,H,Hp", [
+    (30000, 264, 136),   # one group in eight parts of 59 steps: from 8 bits every part empties its one accumulator twice
+    (13000, 1160, 520),  # eight parts of 26 steps over 15 tiles
+    (5000, 2048, 2560),  # 80 tiles, more than there are pairs: one part of 79 steps
+])
+def test_wgrad_of_more_steps_than_an_accumulator_takes(rows, H, Hp, kept):
+    """Integers, bit for bit. (Sums of 30000 products of at most 4 stay below 2^24, so that the fp32 product compared
+    with is exact as well.)"""
+    x, dy = _rows(rows + 70, H, 1, True).to(DEV), _rows(rows + 70, Hp, 2, True).to(DEV)
+    cu = torch.tensor([[30, 30 + rows, rows + 70]], dtype=torch.int32, device=DEV)
+    home, slot = torch.zeros(2, H, Hp, device=DEV), torch.zeros(1, 1, H, Hp, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mep.mep_grouped_wgrad(mep.mep_ckpt_save(x) if kept else x, dy, cu, home, slot, status, 1, rows + 70, 1)
+    assert int(status.item()) == 0
+    for got, a, b in ((home[0], 0, 30), (home[1], 30, 30 + rows), (slot[0, 0], 30 + rows, rows + 70)):
+        assert torch.equal(got, x[a:b].float().t() @ dy[a:b].float())
+
+
+@pytest.mark.parametrize("kept", [False, True], ids=["as_it_was", "kept"])
+def test_wgrad_sums_leave_the_tensor_cores_in_time(kept):
+    """2-norm error over 3000 rows in one part (80 tiles, so that nothing is cut).
+
+    The tensor cores' additions, one for 16 rows, cut off up to an ulp: half of one on average, and an ulp is 0.72 * 2^-23
+    of a value on average; a running sum of random terms has on average 2/3 of its last size. After n additions that is
+    n * 2^-25 of the sum: 32 (512 rows) 0.95e-6, 188 (all of them) 5.6e-6. From 8 bits there are fewer bits to cut off."""
+    rows, H, Hp = 3000, 2048, 2560
+    x, dy = _rows(rows, H, 1, False).to(DEV), _rows(rows, Hp, 2, False).to(DEV)
+    cu = torch.tensor([[rows]], dtype=torch.int32, device=DEV)
+    home = torch.zeros(1, H, Hp, device=DEV)
+    ck = mep.mep_ckpt_save(x)
+    mep.mep_grouped_wgrad(ck if kept else x, dy, cu, home, None, None, 1, rows, 1)
+    want = (mep.mep_ckpt_load(ck, H) if kept else x).double().t() @ dy.double()
+    assert float((home[0] - want).norm() / want.norm()) < 1e-6
+
+
+def _room(nbytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 1.2 * nbytes:
+        pytest.skip("not enough memory")
+
+
+@pytest.mark.parametrize("kept", [False, True], ids=["as_it_was", "kept"])
+def test_wgrad_of_more_than_2_31_elements(kept):
+    """Two ranks of 150001 rows of 7168 columns (the second's rows lie beyond 2^31 bytes and elements), integers."""
+    _room(8 << 30)
+    R, S, E, H, Hp = 2, 150001, 2, 7168, 136
+    g = torch.Generator(DEV).manual_seed(1)
+    x = torch.randint(-2, 3, (R * S, H), generator=g, device=DEV, dtype=torch.int8).to(BF16)
+    dy = torch.randint(-2, 3, (R * S, Hp), generator=g, device=DEV, dtype=torch.int8).to(BF16)
+    assert x.numel() > 2 ** 31
+    ends = [[S - 70, S - 70, S], [100, S - 40, S]]
+    cu = torch.tensor(ends, dtype=torch.int32, device=DEV)
+    home, slot = torch.zeros(E, H, Hp, device=DEV), torch.zeros(R, 1, H, Hp, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mep.mep_grouped_wgrad(mep.mep_ckpt_save(x) if kept else x, dy, cu, home, slot, status, R, S, 1)
+    assert int(status.item()) == 0
+
+    def product(a, b):
+        return x[a:b].float().t() @ dy[a:b].float()
+
+    assert torch.equal(home[0], product(0, S - 70) + product(S, S + 100))
+    assert torch.equal(home[1], product(S + 100, 2 * S - 40))
+    assert torch.equal(slot[0, 0], product(S - 70, S)) and torch.equal(slot[1, 0], product(2 * S - 40, 2 * S))
+
+
+def test_wgrad_gradients_of_more_than_2_31_elements():
+    """The large workload's experts (256 of 7168 x 1408): the last ones' gradients lie beyond 2^31 elements."""
+    E, H, Hp, SK = 256, 7168, 1408, 640
+    _room(4 * E * H * Hp)
+    home = torch.full((E, H, Hp), 7.0, device=DEV)
+    assert home.numel() > 2 ** 31
+    x, dy = _rows(2 * SK, H, 1, True).to(DEV), _rows(2 * SK, Hp, 2, True).to(DEV)
+    n = torch.zeros(2, E, dtype=torch.int64)
+    n[0, 0], n[0, 200], n[0, 254] = 300, 40, 300
+    n[1, 1], n[1, 213], n[1, 255] = 17, 500, 123
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mep.mep_grouped_wgrad(x, dy, n.cumsum(1).int().to(DEV), home, None, status, 2, SK, 1)
+    assert int(status.item()) == 0
+    at = 0
+    for e in range(E):  # (no expert has rows of both ranks)
+        assert not n[0, e] or not n[1, e]
+    for r in range(2):
+        for e in n[r].nonzero().flatten().tolist():
+            c = int(n[r, e])
+            assert torch.equal(home[e], x[at:at + c].float().t() @ dy[at:at + c].float()), e
+            at += c
+    empty = (n.sum(0) == 0).nonzero().flatten()
+    assert all(not home[e].any() for e in empty.tolist())
+
+
 def test_wgrad_of_no_rows():
     home, slot = torch.full((2, 16, 8), 5.0, device=DEV), torch.full((1, 1, 16, 8), 5.0, device=DEV)
     cu = torch.zeros((1, 3), dtype=torch.int32, device=DEV)

@@ -511,6 +511,135 @@ def test_swiglu_gradients_against_differences():
     assert abs(num - (_np(dgu) * d).sum()) <= 2.0 ** -8 * np.abs(_np(dgu) * d).sum()
 
 
+# ------------------------------------------------------------------------------------------------ many rows, large tensors
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("N,H", [(30001, 128), (30001, 256), (20001, 512), (9001, 1408), (8001, 2048)])
+def test_norm_over_many_turns(N, H, dt):
+    """So many rows that every CTA goes round its slots of rows copied ahead more than once."""
+    x, dy = _x(N, H, dt, H, shift=0.5), _x(N, H, dt, H + 1)
+    g = torch.Generator().manual_seed(H)
+    w, b = 1 + 0.3 * torch.randn(H, generator=g), torch.randn(H, generator=g)
+    rb = mep.ckpt_row_bytes(H)
+    xc, yc = (torch.full((N, rb), 77, dtype=torch.uint8, device=DEV) for _ in range(2))
+    y, mean, rstd = mep.mep_layer_norm(x.to(DEV), w.to(DEV), b.to(DEV))
+    want, m, r, ty, tm, tr = _norm_tol(_np(x), _np(w), _np(b), 1e-5, dt)
+    _within(mean, m, tm, "mean")
+    _within(rstd, r, tr, "rstd")
+    _within(y, want, ty, "y")
+    again = mep.mep_layer_norm(x.to(DEV), w.to(DEV), b.to(DEV), x_ckpt=xc, y_ckpt=yc)
+    assert all(torch.equal(p, q) for p, q in zip(again, (y, mean, rstd)))
+    assert torch.equal(xc, mep.mep_ckpt_save(x.to(DEV))) and torch.equal(yc, mep.mep_ckpt_save(y))
+    dx, dw, db = mep.mep_layer_norm_backward(dy.to(DEV), x.to(DEV), w.to(DEV), mean, rstd)
+    want = _backward_tol(_np(dy), _np(x), _np(w), _np(mean), _np(rstd), dt)
+    for got, v, tol, what in zip((dx, dw, db), want[:3], want[3:], ("dx", "dweight", "dbias")):
+        _within(got, v, tol, what)
+
+
+@pytest.mark.parametrize("H", [128, 264, 2048, 8200])
+def test_fp32_rows_16_bytes_into_their_storage(H):
+    """16 bytes off a 32-byte boundary: eight values go out in two pieces."""
+    N = 45
+    x, y, dy, dx, back = (_rows_view((N, H), F32, 16) for _ in range(5))
+    assert x.data_ptr() % 32 == 16
+    x.copy_(_x(N, H, F32, 1))
+    dy.copy_(_x(N, H, F32, 2))
+    w = _rows_view((H,), F32, 16)
+    w.copy_(1 + 0.3 * torch.randn(H, generator=torch.Generator().manual_seed(3)))
+    dw, db = _rows_view((H,), F32, 16), _rows_view((H,), F32, 16)
+    xc = _rows_view((N, mep.ckpt_row_bytes(H)), torch.uint8, 16)
+    _, mean, rstd = mep.mep_layer_norm(x, w, w, 1e-5, y=y, x_ckpt=xc)
+    want, m, r, ty, tm, tr = _norm_tol(_np(x), _np(w), _np(w), 1e-5, F32)
+    _within(y, want, ty, "y")
+    _assert_rows(xc, _np(x), "x_ckpt")
+    mep.mep_ckpt_load(xc, H, back)
+    np.testing.assert_array_equal(_np(back), ref.kept(_np(x)))
+    for src, xn in ((x, _np(x)), (xc, ref.kept(_np(x)))):
+        got = mep.mep_layer_norm_backward(dy, src, w, mean, rstd, dx=dx, dweight=dw, dbias=db)
+        want = _backward_tol(_np(dy), xn, _np(w), _np(mean), _np(rstd), F32)
+        for v, e, t, what in zip(got, want[:3], want[3:], ("dx", "dweight", "dbias")):
+            _within(v, e, t, what)
+
+
+def _room(nbytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 1.2 * nbytes:
+        pytest.skip("not enough memory")
+
+
+def _runs(N, columns):
+    """First, middle and last rows, and those around the 2^31st element."""
+    at = 2 ** 31 // columns
+    assert 4 < at < N - 5
+    return [slice(0, 9), slice(N // 2, N // 2 + 9), slice(at - 4, at + 5), slice(N - 300, N)]
+
+
+@pytest.mark.parametrize("N,H", [(300001, 7168), (1048201, 2049)])
+def test_norm_of_more_than_2_31_elements(N, H):
+    """Rows beyond 2^31 elements come out as they do on their own (tested above), bit for bit."""
+    _room(22 << 30)
+    assert N * H > 2 ** 31
+    g = torch.Generator(DEV).manual_seed(1)
+    x = torch.randn(N, H, generator=g, device=DEV, dtype=BF16)
+    w, b = torch.randn(H, generator=g, device=DEV), torch.randn(H, generator=g, device=DEV)
+    xc, yc = (torch.empty((N, mep.ckpt_row_bytes(H)), dtype=torch.uint8, device=DEV) for _ in range(2))
+    y, mean, rstd = mep.mep_layer_norm(x, w, b, x_ckpt=xc, y_ckpt=yc)
+    dy = torch.randint(-1, 2, (N, H), generator=g, device=DEV, dtype=torch.int8).to(BF16)
+    for run in _runs(N, H):
+        want = mep.mep_layer_norm(x[run].clone(), w, b)
+        assert all(torch.equal(p[run], q) for p, q in zip((y, mean, rstd), want))
+        assert torch.equal(xc[run], mep.mep_ckpt_save(x[run].clone()))
+        assert torch.equal(yc[run], mep.mep_ckpt_save(y[run].clone()))
+    for src in (x, xc):
+        dx, _, db = mep.mep_layer_norm_backward(dy, src, w, mean, rstd, dx=y)
+        for run in _runs(N, H):
+            want = mep.mep_layer_norm_backward(dy[run].clone(), src[run].clone(), w, mean[run].clone(), rstd[run].clone())
+            assert torch.equal(dx[run], want[0])
+        # -1, 0 and 1 add up to integers below 2^24: exact in any order
+        assert torch.equal(db, dy.sum(0, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("rows,F", [(800001, 1408), (800001, 1407)])
+def test_swiglu_of_more_than_2_31_elements(rows, F):
+    _room(20 << 30)
+    g = torch.Generator(DEV).manual_seed(1)
+    gu = torch.randn(rows, 2 * F, generator=g, device=DEV, dtype=BF16)
+    da = torch.randn(rows, F, generator=g, device=DEV, dtype=BF16)
+    assert gu.numel() > 2 ** 31
+    ck = torch.empty((rows, 2, mep.ckpt_row_bytes(F)), dtype=torch.uint8, device=DEV)
+    a = mep.mep_swiglu(gu, ckpt=ck)
+    for src in (gu, ck):
+        dgu, again = mep.mep_swiglu_backward(da, src)
+        for run in _runs(rows, 2 * F):
+            want = mep.mep_swiglu_backward(da[run].clone(), src[run].clone())
+            assert torch.equal(dgu[run], want[0]) and torch.equal(again[run], want[1])
+        del dgu, again
+    for run in _runs(rows, 2 * F):
+        kept = torch.empty((ck[run].shape), dtype=torch.uint8, device=DEV)
+        assert torch.equal(a[run], mep.mep_swiglu(gu[run].clone(), ckpt=kept)) and torch.equal(ck[run], kept)
+
+
+@pytest.mark.parametrize("C", [8, 1])
+def test_ckpt_of_more_blocks_than_a_launch_takes(C):
+    """2^30 + 12345 rows of one block each: two launches."""
+    N = 2 ** 30 + 12345
+    _room(N * (32 + 4 * C))
+    x = torch.zeros((N, C), dtype=BF16, device=DEV)
+    runs = [slice(0, 100), slice(2 ** 30 - 50, 2 ** 30 + 50), slice(N - 100, N)]
+    for run in runs:
+        x[run] = torch.randn(100, C, device=DEV)
+    ck = mep.mep_ckpt_save(x)
+    for run in runs:
+        assert torch.equal(ck[run], mep.mep_ckpt_save(x[run].clone()))
+    back = mep.mep_ckpt_load(ck, C)
+    assert back.numel() == x.numel()
+    for run in runs:
+        assert torch.equal(back[run], mep.mep_ckpt_load(ck[run].clone(), C))
+        back[run] = 0
+    assert not back.any()
+
+
 # ------------------------------------------------------------------------------------------------ runs of rows
 
 
