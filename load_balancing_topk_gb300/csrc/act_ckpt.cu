@@ -11,11 +11,11 @@
 // columns a lane's values are one 16-byte vector; otherwise they are fetched
 // one by one, coalesced over the half warp.
 // What bounds them is DRAM, and in small calls the launch. The activation
-// forward and backward on [196608, 2, 1408] takes 742 us, 6.7 TB/s (a copy
-// runs at 6.8); saving and loading [32768, 2048] 71 us, 5.7 TB/s, of which some
+// forward and backward on [196608, 2, 1408] takes 737 us, 6.8 TB/s (a copy
+// runs at 6.8); saving and loading [32768, 2048] 70 us, 5.8 TB/s, of which some
 // 4 us a launch are its start and end. Rows one by one issue two to three times
-// as much: [32768, 2047] 108 us, the activation on [65536, 2, 1407] 408
-// where 1408 columns take 250.
+// as much: [32768, 2047] 108 us, the activation on [65536, 2, 1407] 398
+// where 1408 columns take 255.
 
 #include "ckpt.cuh"
 
@@ -25,10 +25,10 @@ namespace {
 constexpr int kThreads = 256;
 // Blocks a thread holds. Saving and loading [32768, 2048] in bf16 with 2, 4, 6
 // and 8: 76, 76, 85 and 101 us, more registers and so fewer warps; the
-// activation on [196608, 2, 1408] with 1, 2, 3 and 4: 798, 762, 791 and 822. fp32
+// activation on [196608, 2, 1408] with 1, 2, 3 and 4: 781, 740, 750 and 876. fp32
 // has half as many (1, 2, 4: 128, 126, 126 us). Without vectors one, as eight
 // loads are under way then: the activation on [65536, 2, 1407] with 1, 2 and 4:
-// 408, 432 and 568 us.
+// 399, 398 and 573 us.
 constexpr int kCkptUnroll = 4, kSwigluUnroll = 2;
 
 // Where the U blocks of this half warp are. Blocks are numbered over the whole
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads)
 // -87.3 already, which u = 1e38 makes an activation of -87; to scale costs
 // nothing, as k e^-g = 2^(-g log2 e - 24) is one fma where e^-g is a product.
 // (e^-|g| and its numerator by the sign of g: 780 us for the activation forward
-// and backward on [196608, 2, 1408], this 745.) Relative error, in units of
+// and backward on [196608, 2, 1408], this 740.) Relative error, in units of
 // 2^-24: 17 + 2 |g| of the exponent, 3 of ex2, 1 of the sum, 2 of the reciprocal.
 __device__ __forceinline__ float ex2(float v) {
   float r;

@@ -49,14 +49,22 @@
 // the MMAs wait for the one accumulator to empty: 724, 707 and 702 us on the
 // medium layer (696). 1536 has most of that.
 //
-// What bounds it. From bf16 rows the feed: per step an SM takes in 32 KB and
-// its MMAs read as much of shared memory, all of its 128 bytes a cycle. The
-// medium layer ([196608, 2048] x [196608, 1408], 67 groups) takes 672 to 702
-// us by the box, 1614 to 1688 TFLOP/s, against 1694 to 1739 of a dense library
-// product of the same size (and some 745 us once the GPU is hot). From
-// checkpoint rows 707 us, 1605 TFLOP/s: of the 1310 cycles of a step of 128
-// rows (1024 of MMAs) a converter warp works 825 and waits 160 for the copies,
-// and the MMAs wait 135 for the sums to leave the one accumulator.
+// What bounds it, on the medium layer ([196608, 2048] x [196608, 1408], 67
+// groups). Back to back the power limit: from bf16 rows 778 to 788 us (1440 to
+// 1460 TFLOP/s) at an SM clock of 1470 MHz, from checkpoint rows 798 to 819
+// (1385 to 1420) at 1590, a dense library product of the size 790 at 1670. So a
+// pass from checkpoint rows takes 12% more cycles, of which the power they do
+// not draw gives back all but 3%.
+// In single passes the cycles: 672 to 759 us from bf16 rows by the box, 707 to
+// 737 from checkpoint rows (1494 to 1688 and 1538 to 1605 TFLOP/s; the library
+// product 1694 to 1739). From bf16 rows they are the feed: per step an SM takes
+// in 32 KB and its MMAs read as much of shared memory, all of its 128 bytes a
+// cycle. From checkpoint rows, of the 1310 cycles of a step of 128 rows (1024
+// of MMAs) a converter warp works 825 and waits 160 for the copies, and the
+// MMAs wait 135 for the sums to leave the one accumulator.
+// The large workload's layer ([524288, 7168] x [524288, 1408], 256 experts)
+// takes 6.28 ms from bf16 rows and 6.48 from checkpoint rows in single passes
+// (1686 and 1635 TFLOP/s), 7.35 and 7.62 back to back.
 // What it took to get there: the operand in TMEM (through shared memory 940
 // us), 128 rows a step, for what each step costs a converter to start (847 ->
 // 823 us; with the ring below, 750 against 893 at 64), a fourth stage, so that
@@ -212,8 +220,12 @@ constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (
 // of more than kLeastSteps is cut. The longest come first. A thread has one weight row, reads its group
 // ends once (together the threads read, and check, all of cu_seqlens), and
 // places its parts by counting over the others' lengths in shared memory. With
-// more weight rows than threads the list is in their order and nothing is cut:
-// that many fill the pairs.
+// more weight rows than threads, empty slots among them, the list is in their
+// order and nothing is cut. That serves calls whose rows are spread (64 ranks
+// of 2 experts and 1000 rows, each with a slot in use, at 512 x 512: 117 us
+// with 16 slots a rank, 1152 weight rows; 187 with 14, 1024 weight rows, of
+// which the counting is some 90), but not those with one expert hot (the same
+// with 64600 rows of one expert: 357 and 212).
 __device__ __forceinline__ int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
 struct Row {  // a weight row's group

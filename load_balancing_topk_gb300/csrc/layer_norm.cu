@@ -714,9 +714,9 @@ Shape shape_of(long long N, int H, int J, int U) {
 // for rows of more than 8192 columns (backward [16384, 12288] 345 us before the
 // weights went to shared memory; with two blocks, 1024 threads and half the
 // registers 483). Four also (`four`) where a row would take 9 or 10 warps, 4097
-// to 5120 columns, of which an SM has room for 16; at 12 warps, [20000,
-// 6144], bf16 backward from 8 bits 152 us and with two 142. Over those widths, of 20000 rows, in
-// us with four and with two blocks:
+// to 5120 columns, of which an SM has room for 16; at 12 warps, [20000, 6144],
+// the bf16 backward pass from 8 bits took 152 us with four and 142 with two.
+// Over those widths, of 20000 rows, in us with four and with two:
 //   forward     bf16 84-91 and 88-113, fp32 115-133 and 147-162, odd widths
 //               137-158 and 215-240; with one or two checkpoints alike
 //   backward    bf16 103-115 and 111-125, from 8 bits 117-122 and 131-135,
