@@ -55,8 +55,8 @@
 // (1385 to 1420) at 1590, a dense library product of the size 790 at 1670. So a
 // pass from checkpoint rows takes 12% more cycles, of which the power they do
 // not draw gives back all but 3%.
-// In single passes the cycles: 672 to 759 us from bf16 rows by the box, 707 to
-// 737 from checkpoint rows (1494 to 1688 and 1538 to 1605 TFLOP/s; the library
+// In single passes the cycles: 672 to 759 us from bf16 rows by the GPU, 707 to
+// 749 from checkpoint rows (1494 to 1688 and 1515 to 1605 TFLOP/s; the library
 // product 1694 to 1739). From bf16 rows they are the feed: per step an SM takes
 // in 32 KB and its MMAs read as much of shared memory, all of its 128 bytes a
 // cycle. From checkpoint rows, of the 1310 cycles of a step of 128 rows (1024
