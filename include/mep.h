@@ -17,6 +17,13 @@
  *   mep_ckpt_save / mep_ckpt_load   activations kept in 8 bits for the backward
  *                   pass (the norm, the activation and mep_grouped_wgrad write
  *                   or read them directly)
+ *   mep_route / mep_route_backward  the router's choice: logits to topk_idx and
+ *                   topk_w, and their gradient
+ *   mep_expert_layer the whole layer for a few tokens: what plan .. combine
+ *                   compute, without a plan or a buffer
+ *   mep_w4_save / mep_w4_load / mep_w4_product   weights held in 4 bits, and
+ *                   their product with a few rows (mep_expert_layer reads them
+ *                   too)
  *   mep_plan_remote_fallback / mep_plan_static_scratch   planner variants
  *   mep_wait_selftest  the kernels' bounded wait, run on a barrier that never completes
  *
@@ -44,6 +51,10 @@
  *     their backward passes, where the columns (C, H, F) are not a multiple of
  *     8, tensors need only start on a boundary of their element (any run of
  *     rows of a larger tensor does), except for checkpoint rows and workspaces.
+ *     The same holds in mep_route and mep_route_backward (for every tensor, at
+ *     any width), in mep_w4_save / load (w, at any width), in mep_w4_product
+ *     (x, where K is not a multiple of 8; y) and for mep_expert_layer's
+ *     topk_idx and topk_w.
  *   - bf16 data is passed as 16-bit bit patterns (mep_bf16).
  *   - The int return value reports only the checks made on the host before
  *     anything is enqueued (MEP_ERR_INVALID_ARG) and launch failures
@@ -74,11 +85,11 @@ typedef uint16_t mep_bf16;
 #define MEP_OK 0
 #define MEP_ERR_INVALID_ARG 1   /* host check failed: null pointer, bad size, misalignment */
 #define MEP_ERR_CUDA 2          /* a CUDA launch or attribute call failed */
-#define MEP_ERR_BAD_ROUTING 3   /* device: an expert index out of [0,E) or repeated in a token's row */
+#define MEP_ERR_BAD_ROUTING 3   /* device: an expert index out of range or repeated in a token's row */
 #define MEP_ERR_CAPACITY 4      /* device: some rank needs more than B redundant slots */
 #define MEP_ERR_BAD_POSITION 5  /* device: a dst_pos entry outside [0, R*S*K) */
 #define MEP_ERR_BAD_SLOT_MAP 6  /* device: a slot_expert entry outside [-1, E) */
-#define MEP_ERR_TIMEOUT 7       /* device: a bounded pipeline wait inside mep_grouped_gemm or mep_grouped_wgrad gave up */
+#define MEP_ERR_TIMEOUT 7       /* device: a bounded pipeline wait inside a kernel gave up */
 #define MEP_ERR_BAD_SEQLENS 8   /* device: a cu_seqlens row decreases, is negative or does not end at S*K */
 
 /* Size limits checked on the host. */
@@ -88,11 +99,14 @@ typedef uint16_t mep_bf16;
 #define MEP_MAX_SLOTS 32768 /* R * B */
 #define MEP_MAX_NORM_H 16384      /* columns of a layer norm */
 #define MEP_MAX_CKPT_C (1 << 24)  /* columns of a checkpoint row, of a gated activation */
+#define MEP_MAX_FEW 64     /* tokens of mep_expert_layer, rows of mep_w4_product */
+#define MEP_MAX_W4 (1 << 20)      /* rows and columns of a matrix in 4 bits */
 
 /* Element types of the training operators' tensors. */
 #define MEP_BF16 0
 #define MEP_F32 1
 #define MEP_CKPT8 2  /* checkpoint rows, see mep_ckpt_save */
+#define MEP_W4 3     /* matrices in 4 bits, see mep_w4_save */
 
 /* Library version, (major << 16) | minor. */
 MEP_API int mep_version(void);
@@ -504,6 +518,137 @@ MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
                               const int32_t* cu_seqlens, int32_t* status, int R, int S, int K, int E,
                               int B, int H, int Hp, int accumulate, void* ws, size_t ws_bytes,
                               float* home_grad, float* slot_grad, void* stream);
+
+/*
+ * mep_route -- the router's choice from its logits: what mep_plan, mep_combine
+ * and mep_expert_layer take. (The pages start from "the current router
+ * output"; the reading is the one the synthetic inputs follow.) For every token
+ *   topk_idx = the K experts of the largest logits[e] + bias[e] (added in
+ *              fp32), in descending order, ties to the lower index, NaN above
+ *              everything;
+ *   topk_w   = softmax over the chosen experts' logits (without the bias), in
+ *              fp32.
+ * A logit of -infinity masks its expert: it is chosen last and its weight is 0;
+ * a token without any other logit has weights 0 throughout. With skip_masked
+ * a masked expert's index is -1, which mep_expert_layer passes over (mep_plan
+ * wants K experts of every token). An infinity or a NaN among the chosen
+ * makes the token's weights NaN.
+ *   logits   bf16 or fp32 [N, E]   type
+ *   bias     fp32 [E]              NULL: 0
+ *   E, K     1 <= K <= min(E, MEP_MAX_K), E <= MEP_MAX_E
+ *   topk_idx int32 [N, K]          output
+ *   topk_w   fp32 [N, K]           output
+ * mep_route_backward -- the logits' gradient (the choice itself, and so the
+ * bias, has none):
+ *   dlogits[t, topk_idx[t,k]] = topk_w[t,k] * (dtopk_w[t,k] - sum_j topk_w[t,j] dtopk_w[t,j])
+ * in fp32, rounded once, and 0 for every other expert. An expert that stands
+ * twice in a row gets both; -1 gets none.
+ *   dtopk_w, topk_w  fp32 [N, K];  topk_idx int32 [N, K]
+ *   status   int32 [1]             read on entry (nonzero: no-op); set to
+ *                                  MEP_ERR_BAD_ROUTING if an index is outside
+ *                                  [-1, E) (it gets none). May be NULL.
+ *   dlogits  bf16 or fp32 [N, E]   type; output, every element written
+ * Outputs must not overlap the inputs or one another. N < 2^31.
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_route(const void* logits, int type, const float* bias, int64_t N, int E, int K,
+                      int skip_masked, int32_t* topk_idx, float* topk_w, void* stream);
+MEP_API int mep_route_backward(const float* dtopk_w, const float* topk_w, const int32_t* topk_idx,
+                               int32_t* status, int64_t N, int E, int K, int type, void* dlogits,
+                               void* stream);
+
+/*
+ * mep_w4_save / mep_w4_load -- weight matrices in 4 bits with a scale for each
+ * group of rows of a column, and their values back. (The pages keep weights in
+ * one type; the format is this library's.) A column's rows are taken in groups
+ * of 32, 64 or 128. With a = the group's largest magnitude its scale is
+ * s = bf16_rn(a / 7), q = w / s rounded to nearest-even and kept within +-7,
+ * and the value is q * s (0 where s is 0; NaN where the group holds an
+ * infinity or a NaN).
+ * A matrix of K rows and N columns is mep_w4_bytes(K, N, group) bytes: panels
+ * of 64 columns one after another, a panel's blocks of 128 rows one after
+ * another, rows and columns that are not there filled up with q = 0, s = 0. A
+ * block is 4096 bytes of pairs and then its scales, bf16 [128 / group][64].
+ * Row k = 64 h + 16 j + 8 i + 2 t + e of the block and column n = 16 c + 8 l + g
+ * of the panel: q + 8 is the low (l = 0) or high half of the byte
+ * ((((4 h + c) * 8 + g) * 4 + t) * 4 + j) * 4 + 2 e + i, and the column's scale
+ * is number 16 c + 2 g + l of its group's 64. (A lane's 16 bytes are then four
+ * steps of one tensor-core operand.)
+ *   w       bf16 or fp32 [M, K, N]   w_type; M matrices
+ *   parts   each matrix is kept as `parts` matrices of N / parts columns
+ *           (N % parts == 0): 2 for the gate and up halves of an expert's
+ *           first projection, as mep_expert_layer reads them
+ *   group   32, 64 or 128
+ *   w4      uint8 [M, parts, mep_w4_bytes(K, N / parts, group)]
+ * mep_w4_load rounds q * s once to bf16; fp32 holds it exactly.
+ * Input and output must not overlap. 1 <= K, N / parts <= MEP_MAX_W4,
+ * M * parts < 2^31.
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_w4_bytes(int64_t K, int64_t N, int group, size_t* bytes);
+MEP_API int mep_w4_save(const void* w, int w_type, int64_t M, int64_t K, int64_t N, int parts,
+                        int group, uint8_t* w4, void* stream);
+MEP_API int mep_w4_load(const uint8_t* w4, int64_t M, int64_t K, int64_t N, int parts, int group,
+                        int w_type, void* w, void* stream);
+
+/*
+ * mep_w4_product -- y[t, n] = sum_k x[t, k] * W[k, n] for a few rows and one
+ * matrix in 4 bits. The products x * q are exact, a group's are added in fp32
+ * (by the tensor cores, order fixed), times its scale and added up in fp32; y
+ * is rounded once. The same call gives the same bits.
+ *   x       bf16 [T, K]    0 <= T <= MEP_MAX_FEW
+ *   w4      uint8 [mep_w4_bytes(K, N, group)]   from mep_w4_save, parts 1
+ *   status  int32 [1]      read on entry (nonzero: no-op); set to
+ *                          MEP_ERR_TIMEOUT if a pipeline wait gives up. May be NULL.
+ *   ws      device scratch of >= mep_w4_product_workspace_bytes bytes; the
+ *           size does not fall with T. Calls that overlap on the GPU need
+ *           one each
+ *   y       bf16 or fp32 [T, N]    y_type; output; must not overlap the inputs
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_w4_product_workspace_bytes(int T, int64_t K, int64_t N, int group, size_t* bytes);
+MEP_API int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* status, int T, int64_t K,
+                           int64_t N, int group, void* ws, size_t ws_bytes, int y_type, void* y,
+                           void* stream);
+
+/*
+ * mep_expert_layer -- the whole layer for a few tokens, such as the next token
+ * of each of up to 64 sequences: what mep_plan .. mep_combine compute with the
+ * two projections and mep_swiglu between them, from the home experts' weights,
+ * without plan, buffer or slots (with so few tokens the path's time is the
+ * weights' bytes, and every expert's are read once whatever the balance). With
+ * e = topk_idx[t,k]:
+ *   a[t,k] = bf16_rn( silu(x[t] . w1[e][:, :F]) * (x[t] . w1[e][:, F:]) )
+ *   out[t] = bf16_rn( sum_k topk_w[t,k] * (a[t,k] . w2[e]) )      k ascending
+ * with sums in fp32 (the tensor cores', order fixed: the same call gives the
+ * same bits). a is rounded as mep_swiglu's output is, since the second product
+ * takes it as an operand; nothing else is rounded before out.
+ *   x        bf16 [T, H]     0 <= T <= MEP_MAX_FEW
+ *   topk_idx int32 [T, K]    in [-1, E), distinct per row but for -1, which
+ *                            stands for no expert (the empty places of a padded
+ *                            batch); a token without any gets zeros
+ *   topk_w   fp32 [T, K]     used as given
+ *   w1, w2   w_type MEP_BF16: bf16 [E, H, 2F] (gate columns, then up columns)
+ *            and [E, F, H], as mep_grouped_gemm takes them (device memory of
+ *            the current device); MEP_W4: uint8
+ *            [E, 2, mep_w4_bytes(H, F, group)] and [E, mep_w4_bytes(F, H, group)]
+ *   group    of MEP_W4; not read for MEP_BF16
+ *   status   int32 [1]       read on entry (nonzero: no-op); set to
+ *                            MEP_ERR_BAD_ROUTING (out untouched) or
+ *                            MEP_ERR_TIMEOUT. May be NULL.
+ *   H, F     multiples of 8, H <= MEP_MAX_W4, F <= MEP_MAX_W4 / 2
+ *   ws       device scratch of >= mep_expert_layer_workspace_bytes bytes; the
+ *            size does not fall with T. Calls that overlap on the GPU need one
+ *            each
+ *   out      bf16 [T, H]     output; must not overlap the inputs
+ * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
+ */
+MEP_API int mep_expert_layer_workspace_bytes(int T, int K, int E, int64_t H, int64_t F, int w_type,
+                                             int group, size_t* bytes);
+MEP_API int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, const float* topk_w,
+                             const void* w1, const void* w2, int w_type, int group, int32_t* status,
+                             int T, int K, int E, int64_t H, int64_t F, void* ws, size_t ws_bytes,
+                             mep_bf16* out, void* stream);
 
 /*
  * mep_wait_selftest -- exercises the bounded wait that every pipeline wait

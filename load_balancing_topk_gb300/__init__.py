@@ -27,7 +27,14 @@ Entry points (same names as the C ABI):
   activation;
 * :func:`mep_ckpt_save` / :func:`mep_ckpt_load` -- activations kept in 8 bits
   for the backward pass; the norm and the activation write them as they go, and
-  all three backward operators read them directly.
+  all three backward operators read them directly;
+* :func:`mep_route` / :func:`mep_route_backward` -- the router's choice from its
+  logits, and their gradient;
+* :func:`mep_expert_layer` -- the whole layer for up to 64 tokens, without a
+  plan or a buffer;
+* :func:`mep_w4_save` / :func:`mep_w4_load` / :func:`mep_w4_product` -- weights
+  held in 4 bits, which mep_expert_layer reads too, and their product with a few
+  rows.
 """
 
 from __future__ import annotations
@@ -45,6 +52,8 @@ __all__ = [
     "grouped_gemm_workspace_bytes", "mep_grouped_gemm", "grouped_wgrad_workspace_bytes", "mep_grouped_wgrad",
     "ckpt_row_bytes", "mep_ckpt_save", "mep_ckpt_load", "layer_norm_backward_workspace_bytes", "mep_layer_norm",
     "mep_layer_norm_backward", "mep_swiglu", "mep_swiglu_backward",
+    "mep_route", "mep_route_backward", "w4_bytes", "mep_w4_save", "mep_w4_load", "w4_product_workspace_bytes",
+    "mep_w4_product", "expert_layer_workspace_bytes", "mep_expert_layer", "MAX_FEW",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -70,8 +79,10 @@ STATUS_CODE = {v: k for k, v in STATUS.items()}
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
-# element types of the training operators (MEP_BF16, MEP_F32, MEP_CKPT8)
-_BF16, _F32, _CKPT8 = 0, 1, 2
+# element types of the training operators (MEP_BF16, MEP_F32, MEP_CKPT8, MEP_W4)
+_BF16, _F32, _CKPT8, _W4 = 0, 1, 2, 3
+# tokens that mep_expert_layer takes, rows that mep_w4_product takes (MEP_MAX_FEW)
+MAX_FEW = 64
 SIGNATURES = [
     ("mep_version", _I, []),
     ("mep_status_string", ctypes.c_char_p, [_I]),
@@ -101,6 +112,15 @@ SIGNATURES = [
     ("mep_grouped_wgrad_workspace_bytes", _I, [_I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
     ("mep_grouped_wgrad", _I, [_VP, _I, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _I, _I, _VP, ctypes.c_size_t,
                                _VP, _VP, _VP]),
+    ("mep_route", _I, [_VP, _I, _VP, _L, _I, _I, _I, _VP, _VP, _VP]),
+    ("mep_route_backward", _I, [_VP, _VP, _VP, _VP, _L, _I, _I, _I, _VP, _VP]),
+    ("mep_w4_bytes", _I, [_L, _L, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_w4_save", _I, [_VP, _I, _L, _L, _L, _I, _I, _VP, _VP]),
+    ("mep_w4_load", _I, [_VP, _L, _L, _L, _I, _I, _I, _VP, _VP]),
+    ("mep_w4_product_workspace_bytes", _I, [_I, _L, _L, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_w4_product", _I, [_VP, _VP, _VP, _I, _L, _L, _I, _VP, ctypes.c_size_t, _I, _VP, _VP]),
+    ("mep_expert_layer_workspace_bytes", _I, [_I, _I, _I, _L, _L, _I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    ("mep_expert_layer", _I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _VP, _I, _I, _I, _L, _L, _VP, ctypes.c_size_t, _VP, _VP]),
     ("mep_wait_selftest", _I, [_VP, ctypes.c_int64, _VP, _VP]),
 ]
 
@@ -777,6 +797,219 @@ def mep_grouped_wgrad(x, dy, cu_seqlens, home_grad, slot_grad, status, R: int, S
           R, S, K, E, B, H, Hp, 1 if accumulate else 0, workspace.data_ptr(), workspace.numel(),
           home_grad.data_ptr(), slot_grad.data_ptr() if B > 0 else None)
     return home_grad, slot_grad
+
+
+def mep_route(logits, K: int, bias=None, topk_idx=None, topk_w=None, skip_masked: bool = False):
+    """(topk_idx, topk_w) of every token: the K experts of the largest logits + bias (descending, ties to
+    the lower index), and the softmax of their logits.
+
+    logits: bf16 or fp32 [N, E]; bias: fp32 [E], for the choice alone, or None. A logit of -inf masks its
+    expert: chosen last, weight 0, index -1 where ``skip_masked`` (mep_expert_layer passes over those;
+    mep_plan wants K experts). topk_idx: int32 [N, K]; topk_w: fp32 [N, K].
+    """
+    torch = _torch()
+    kind = _matrix(logits, "logits")
+    N, E = logits.shape
+    dev, f32 = logits.device, torch.float32
+    if not 1 <= K <= E:
+        raise ValueError(f"K must be in [1, {E}]")
+    if bias is not None:
+        _good(bias, "bias", f32, (E,), dev)
+    topk_idx = (torch.empty((N, K), dtype=torch.int32, device=dev) if topk_idx is None
+                else _good(topk_idx, "topk_idx", torch.int32, (N, K), dev))
+    topk_w = torch.empty((N, K), dtype=f32, device=dev) if topk_w is None else _good(topk_w, "topk_w", f32, (N, K), dev)
+    _call("mep_route", dev, logits.data_ptr(), kind, _ptr(bias), N, E, K, 1 if skip_masked else 0, topk_idx.data_ptr(),
+          topk_w.data_ptr())
+    return topk_idx, topk_w
+
+
+def mep_route_backward(dtopk_w, topk_w, topk_idx, E: int, dlogits=None, dtype=None, status=None):
+    """dlogits [N, E] of mep_route from dtopk_w (fp32 [N, K]) and what mep_route gave.
+
+    dlogits: bf16 or fp32, ``dtype`` (fp32 unless given). Indices of -1 get nothing; one outside [-1, E)
+    sets status (int32 [1], or None) to MEP_ERR_BAD_ROUTING.
+    """
+    torch = _torch()
+    dev, f32 = _cuda_device(dtopk_w, "dtopk_w"), torch.float32
+    if dtopk_w.dim() != 2:
+        raise ValueError("dtopk_w must be [N, K]")
+    N, K = dtopk_w.shape
+    _good(dtopk_w, "dtopk_w", f32, (N, K), dev)
+    _good(topk_w, "topk_w", f32, (N, K), dev)
+    _good(topk_idx, "topk_idx", torch.int32, (N, K), dev)
+    if status is not None:
+        _good(status, "status", torch.int32, (1,), dev)
+    if dlogits is None:
+        dlogits = torch.empty((N, E), dtype=f32 if dtype is None else dtype, device=dev)
+        kind = _float_type(dlogits, "dlogits")
+    else:
+        kind = _float_type(dlogits, "dlogits")
+        _good(dlogits, "dlogits", dlogits.dtype if dtype is None else dtype, (N, E), dev)
+    _call("mep_route_backward", dev, dtopk_w.data_ptr(), topk_w.data_ptr(), topk_idx.data_ptr(), _ptr(status), N, E, K,
+          kind, dlogits.data_ptr())
+    return dlogits
+
+
+@functools.lru_cache(maxsize=256)
+def w4_bytes(K: int, N: int, group: int = 128) -> int:
+    """Bytes of a matrix [K, N] in 4 bits, in groups of ``group`` (32, 64 or 128) rows."""
+    out = ctypes.c_size_t(0)
+    _check("mep_w4_bytes", load_library().mep_w4_bytes(int(K), int(N), int(group), ctypes.byref(out)))
+    return int(out.value)
+
+
+@functools.lru_cache(maxsize=256)
+def w4_product_workspace_bytes(T: int, K: int, N: int, group: int = 128) -> int:
+    """Bytes of mep_w4_product's workspace for up to T rows."""
+    out = ctypes.c_size_t(0)
+    _check("mep_w4_product_workspace_bytes",
+           load_library().mep_w4_product_workspace_bytes(int(T), int(K), int(N), int(group), ctypes.byref(out)))
+    return int(out.value)
+
+
+@functools.lru_cache(maxsize=256)
+def expert_layer_workspace_bytes(T: int, K: int, E: int, H: int, F: int, w4: bool = False, group: int = 128) -> int:
+    """Bytes of mep_expert_layer's workspace for up to T tokens."""
+    out = ctypes.c_size_t(0)
+    _check("mep_expert_layer_workspace_bytes",
+           load_library().mep_expert_layer_workspace_bytes(int(T), int(K), int(E), int(H), int(F), _W4 if w4 else _BF16,
+                                                           int(group), ctypes.byref(out)))
+    return int(out.value)
+
+
+def _scratch(workspace, need, dev):
+    """The workspace given, if it is good and large enough, or one of ``need`` bytes."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    if workspace.numel() < need:
+        raise ValueError(f"workspace has {workspace.numel()} bytes, needs {need}")
+    return workspace
+
+
+def mep_w4_save(w, group: int = 128, parts: int = 1, w4=None):
+    """w (bf16 or fp32 [..., K, N]) in 4 bits: uint8 [..., parts, w4_bytes(K, N / parts, group)].
+
+    One scale for each ``group`` (32, 64 or 128) rows of a column. parts: 2 for the gate and up halves of an
+    expert's first projection, as mep_expert_layer reads them.
+    """
+    torch = _torch()
+    kind = _float_type(w, "w")
+    if w.dim() < 2:
+        raise ValueError("w must be [..., K, N]")
+    K, N = w.shape[-2:]
+    if parts < 1 or N % parts:
+        raise ValueError("N must be a multiple of parts")
+    dev = _cuda_device(w, "w")
+    _good(w, "w", w.dtype, w.shape, dev)
+    shape = tuple(w.shape[:-2]) + (parts, w4_bytes(K, N // parts, group))
+    M = 1
+    for n in w.shape[:-2]:
+        M *= n
+    w4 = torch.empty(shape, dtype=torch.uint8, device=dev) if w4 is None else _good(w4, "w4", torch.uint8, shape, dev)
+    _call("mep_w4_save", dev, w.data_ptr(), kind, M, K, N, parts, group, w4.data_ptr())
+    return w4
+
+
+def mep_w4_load(w4, K: int, N: int, group: int = 128, w=None, dtype=None):
+    """The values of matrices in 4 bits (uint8 [..., parts, bytes], as mep_w4_save gives them): [..., K, N] in
+    w's dtype, or ``dtype`` (bf16 unless given, rounded once; fp32 holds the values exactly)."""
+    torch = _torch()
+    dev = _cuda_device(w4, "w4")
+    if w4.dim() < 2 or w4.shape[-2] < 1 or N % w4.shape[-2] or w4.shape[-1] != w4_bytes(K, N // w4.shape[-2], group):
+        raise ValueError("w4 must be [..., parts, w4_bytes(K, N / parts, group)]")
+    _good(w4, "w4", torch.uint8, w4.shape, dev)
+    shape, parts, M = tuple(w4.shape[:-2]) + (K, N), w4.shape[-2], 1
+    for n in w4.shape[:-2]:
+        M *= n
+    if w is None:
+        w = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=dev)
+        kind = _float_type(w, "w")
+    else:
+        kind = _float_type(w, "w")
+        _good(w, "w", w.dtype if dtype is None else dtype, shape, dev)
+    _call("mep_w4_load", dev, w4.data_ptr(), M, K, N, parts, group, kind, w.data_ptr())
+    return w
+
+
+def mep_w4_product(x, w4, N: int, group: int = 128, y=None, dtype=None, status=None, workspace=None):
+    """y = x @ W for up to 64 rows x (bf16 [T, K]) and one matrix W [K, N] in 4 bits.
+
+    w4: uint8 of w4_bytes(K, N, group) bytes (mep_w4_save of one matrix, parts 1). y: [T, N] in bf16 or fp32,
+    ``dtype`` (bf16 unless given); sums in fp32, rounded once. status: int32 [1] or None.
+    """
+    torch = _torch()
+    dev, bf16 = _cuda_device(x, "x"), torch.bfloat16
+    if x.dim() != 2 or x.shape[0] > MAX_FEW:
+        raise ValueError(f"x must be [T, K] with T of {MAX_FEW} at most")
+    T, K = x.shape
+    _good(x, "x", bf16, (T, K), dev)
+    _need(w4, "w4", torch.uint8, None, dev)
+    if w4.numel() != w4_bytes(K, N, group):
+        raise ValueError(f"w4 must hold one matrix of {w4_bytes(K, N, group)} bytes")
+    if status is not None:
+        _good(status, "status", torch.int32, (1,), dev)
+    if y is None:
+        y = torch.empty((T, N), dtype=bf16 if dtype is None else dtype, device=dev)
+        kind = _float_type(y, "y")
+    else:
+        kind = _float_type(y, "y")
+        _good(y, "y", y.dtype if dtype is None else dtype, (T, N), dev)
+    workspace = _scratch(workspace, w4_product_workspace_bytes(T, K, N, group), dev)
+    _call("mep_w4_product", dev, x.data_ptr(), w4.data_ptr(), _ptr(status), T, K, N, group, workspace.data_ptr(),
+          workspace.numel(), kind, y.data_ptr())
+    return y
+
+
+def mep_expert_layer(x, topk_idx, topk_w, w1, w2, status=None, F: Optional[int] = None, group: int = 128, out=None,
+                     workspace=None):
+    """out[t] = sum_k topk_w[t, k] * (swiglu(x[t] @ w1[e]) @ w2[e]), e = topk_idx[t, k], for up to 64 tokens
+    x (bf16 [T, H]): plan, dispatch, both products, the activation and combine in one call.
+
+    topk_idx: int32 [T, K], distinct per row; -1 stands for no expert. topk_w: fp32 [T, K]. w1, w2: bf16
+    [E, H, 2F] (gate columns first) and [E, F, H], or in 4 bits: ``mep_w4_save(w1, group, parts=2)`` and
+    ``mep_w4_save(w2, group)``, with F given. status (int32 [1] or None) gets MEP_ERR_BAD_ROUTING for a bad
+    index; out is then left as it was. Returns out, bf16 [T, H].
+    """
+    torch = _torch()
+    dev, bf16 = _cuda_device(x, "x"), torch.bfloat16
+    if x.dim() != 2 or x.shape[0] > MAX_FEW:
+        raise ValueError(f"x must be [T, H] with T of {MAX_FEW} at most (mep_plan and mep_dispatch take more)")
+    T, H = x.shape
+    _good(x, "x", bf16, (T, H), dev)
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        raise ValueError("topk_idx must be [T, K]")
+    K = topk_idx.shape[1]
+    _good(topk_idx, "topk_idx", torch.int32, (T, K), dev)
+    _good(topk_w, "topk_w", torch.float32, (T, K), dev)
+    if not isinstance(w1, torch.Tensor):
+        raise TypeError("w1 must be a torch.Tensor")
+    in4 = w1.dtype is torch.uint8
+    if in4:
+        if F is None:
+            raise ValueError("weights in 4 bits need F")
+        if w1.dim() != 3:
+            raise ValueError("w1 must be [E, 2, w4_bytes(H, F, group)]")
+        E = w1.shape[0]
+        _good(w1, "w1", torch.uint8, (E, 2, w4_bytes(H, F, group)), dev)
+        _need(w2, "w2", torch.uint8, None, dev)
+        if w2.numel() != E * w4_bytes(F, H, group) or w2.shape[0] != E:
+            raise ValueError("w2 must be [E, 1, w4_bytes(F, H, group)]")
+    else:
+        if w1.dim() != 3 or w1.shape[2] % 2 or (F is not None and w1.shape[2] != 2 * F):
+            raise ValueError("w1 must be [E, H, 2F]")
+        E, F = w1.shape[0], w1.shape[2] // 2
+        _good(w1, "w1", bf16, (E, H, 2 * F), dev)
+        _good(w2, "w2", bf16, (E, F, H), dev)
+    if status is not None:
+        _good(status, "status", torch.int32, (1,), dev)
+    out = torch.empty_like(x) if out is None else _good(out, "out", bf16, (T, H), dev)
+    workspace = _scratch(workspace, expert_layer_workspace_bytes(T, K, E, H, F, in4, group), dev)
+    _call("mep_expert_layer", dev, x.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), w1.data_ptr(), w2.data_ptr(),
+          _W4 if in4 else _BF16, group, _ptr(status), T, K, E, H, F, workspace.data_ptr(), workspace.numel(),
+          out.data_ptr())
+    return out
 
 
 def mep_wait_selftest(limit_ns: int, device=None):
