@@ -100,6 +100,7 @@ typedef uint16_t mep_bf16;
 #define MEP_MAX_NORM_H 16384      /* columns of a layer norm */
 #define MEP_MAX_CKPT_C (1 << 24)  /* columns of a checkpoint row, of a gated activation */
 #define MEP_MAX_FEW 64     /* tokens of mep_expert_layer, rows of mep_w4_product */
+#define MEP_MAX_FEW_H 65536       /* hidden width of mep_expert_layer; F up to half of it */
 #define MEP_MAX_W4 (1 << 20)      /* rows and columns of a matrix in 4 bits */
 
 /* Element types of the training operators' tensors. */
@@ -618,11 +619,12 @@ MEP_API int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* status
  * without plan, buffer or slots (with so few tokens the path's time is the
  * weights' bytes, and every expert's are read once whatever the balance). With
  * e = topk_idx[t,k]:
- *   a[t,k] = bf16_rn( silu(x[t] . w1[e][:, :F]) * (x[t] . w1[e][:, F:]) )
- *   out[t] = bf16_rn( sum_k topk_w[t,k] * (a[t,k] . w2[e]) )      k ascending
+ *   a[t,k] = silu(x[t] . w1[e][:, :F]) * (x[t] . w1[e][:, F:])
+ *   out[t] = bf16_rn( sum_k topk_w[t,k] * (a[t,k] . w2[e]) )
  * with sums in fp32 (the tensor cores', order fixed: the same call gives the
- * same bits). a is rounded as mep_swiglu's output is, since the second product
- * takes it as an operand; nothing else is rounded before out.
+ * same bits). The second product takes a as two bf16, the value rounded and
+ * what that left over, so that a is off by 2^-16 of itself at most; nothing
+ * else is rounded to fewer than 32 bits before out.
  *   x        bf16 [T, H]     0 <= T <= MEP_MAX_FEW
  *   topk_idx int32 [T, K]    in [-1, E), distinct per row but for -1, which
  *                            stands for no expert (the empty places of a padded
@@ -636,7 +638,7 @@ MEP_API int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* status
  *   status   int32 [1]       read on entry (nonzero: no-op); set to
  *                            MEP_ERR_BAD_ROUTING (out untouched) or
  *                            MEP_ERR_TIMEOUT. May be NULL.
- *   H, F     multiples of 8, H <= MEP_MAX_W4, F <= MEP_MAX_W4 / 2
+ *   H, F     multiples of 8, H <= MEP_MAX_FEW_H, F <= MEP_MAX_FEW_H / 2
  *   ws       device scratch of >= mep_expert_layer_workspace_bytes bytes; the
  *            size does not fall with T. Calls that overlap on the GPU need one
  *            each

@@ -67,8 +67,8 @@ def test_expert_layer_rejects_bad_args(lib):
 
     for kw in (dict(x=None), dict(i=None), dict(w=None), dict(w1=None), dict(w2=None), dict(ws=None), dict(o=None), dict(wb=need - 1),
                dict(t=F32), dict(t=CKPT8), dict(t=4), dict(t=W4, group=0), dict(t=W4, group=48), dict(T=-1), dict(T=65), dict(K=0),
-               dict(K=65), dict(E=0), dict(E=4097), dict(H=4), dict(H=60), dict(F=0), dict(F=12), dict(H=(1 << 20) + 8),
-               dict(F=(1 << 19) + 8), dict(x=24), dict(i=18), dict(w=18), dict(w1=24), dict(w2=24), dict(ws=260), dict(o=24)):
+               dict(K=65), dict(E=0), dict(E=4097), dict(H=4), dict(H=60), dict(F=0), dict(F=12), dict(H=65544),
+               dict(F=32776), dict(x=24), dict(i=18), dict(w=18), dict(w1=24), dict(w2=24), dict(ws=260), dict(o=24)):
         assert f(**kw) == BAD, kw
     assert f(T=0, x=None, i=None, w=None, w1=None, w2=None, ws=None, wb=0, o=None) == 0
     out = ctypes.c_size_t(0)
