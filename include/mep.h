@@ -563,9 +563,9 @@ MEP_API int mep_route_backward(const float* dtopk_w, const float* topk_w, const 
  * group of rows of a column, and their values back. (The pages keep weights in
  * one type; the format is this library's.) A column's rows are taken in groups
  * of 32, 64 or 128. With a = the group's largest magnitude its scale is
- * s = bf16_rn(a / 7), q = w / s rounded to nearest-even and kept within +-7,
- * and the value is q * s (0 where s is 0; NaN where the group holds an
- * infinity or a NaN).
+ * s = bf16_rn(a * (1/7)) (a product in fp32, by fp32's 1/7), q = w / s rounded
+ * to nearest-even and kept within +-7, and the value is q * s (0 where s is 0;
+ * NaN where the group holds an infinity or a NaN).
  * A matrix of K rows and N columns is mep_w4_bytes(K, N, group) bytes: panels
  * of 64 columns one after another, a panel's blocks of 128 rows one after
  * another, rows and columns that are not there filled up with q = 0, s = 0. A

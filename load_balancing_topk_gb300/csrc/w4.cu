@@ -3,7 +3,8 @@
 // A warp holds 16 columns of a block, a lane columns g and g + 8 at the rows
 // whose pairs it writes (w4.cuh): 32 rows, of which every group has its share
 // in each of the four lanes t, so that a group's largest magnitude is two
-// shuffles away. q = w / s is a division, as the format is defined by it.
+// shuffles away. q = w / s is a division, as the format is defined by it; the
+// scale itself is a product by fp32's 1/7.
 
 #include "ckpt.cuh"
 #include "w4.cuh"
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, M
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       scale[q][l] = m[q] >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                        : __bfloat162float(__float2bfloat16_rn(__uint_as_float(m[q]) / kW4Top));
+                                        : __bfloat162float(__float2bfloat16_rn(__uint_as_float(m[q]) * (1.f / kW4Top)));
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

@@ -32,7 +32,7 @@ def w4_quantise(w, group):
         v = w[i * group:(i + 1) * group]
         top = np.abs(v).max(0)
         fine = np.isfinite(top)
-        s[i] = np.where(fine, bf16(np.where(fine, top, 0).astype(np.float32) / np.float32(7)), np.nan)
+        s[i] = np.where(fine, bf16(np.where(fine, top, 0).astype(np.float32) * (np.float32(1) / np.float32(7))), np.nan)
         ok = s[i] > 0
         d = np.where(ok, s[i], 1)
         r = np.rint(np.where(ok, np.where(np.isfinite(v), v, 0) / d, 0))
