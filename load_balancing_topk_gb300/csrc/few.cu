@@ -42,43 +42,84 @@ namespace mep {
 namespace {
 
 constexpr int kMaxCtas = 152;       // SMs of a GB300; more are not used, the workspace counts on it
-constexpr int kM = 4;               // warps across a unit's columns, 32 each
-constexpr int kUnit = 128;          // columns of a unit
+constexpr int kM = 8;               // warps across a unit's columns: 16 of its first half and 16 of its second
+constexpr int kUnit = 256;          // columns of a unit
+constexpr int kPanels = kUnit / kW4Cols;
 constexpr int kPanelRow = 128;      // bytes of a stage's row of 64 bf16 columns
 constexpr int kMaxStages = 16;
 constexpr int kSmem = 225 * 1024;
 constexpr int kChunk = 32;          // tokens of an expert that one unit takes in the layer
+constexpr uint32_t kEnd = 0xffffffffu;
 
-__host__ __device__ constexpr int step_rows(int fmt) { return fmt == MEP_BF16 ? 128 : 256; }
-__host__ __device__ constexpr int threads_of(int slices) { return 32 * (kM * slices + 2); }
+__host__ __device__ constexpr int step_rows(int fmt) { return fmt == MEP_BF16 ? 64 : 256; }
+__host__ __device__ constexpr int threads_of(int slices) { return 32 * (kM * slices + 1); }
 
 // ---------------------------------------------------------------------------
-// A product's units and this CTA's run of steps.
-struct Phase {
-  uint32_t ks, nb;      // steps of a unit, units of an expert
-  uint32_t per;         // steps of a CTA
-  uint32_t parts;       // CTAs that a unit may be cut over
-  uint32_t begin, n;    // this CTA's
+// n / d by a product, n < 2^31: with 2^l >= d, m = floor(2^(31+l) / d) + 1 the
+// product is off by too little to reach the next quotient.
+struct Div {
+  uint32_t m;
+  int shift;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return m == 0 ? n : __umulhi(n, m) >> shift; }
 };
-// Units are cut where a CTA's run ends: unit u is in CTAs u * ks / per up to
-// ((u + 1) * ks - 1) / per.
-__host__ __device__ __forceinline__ uint32_t parts_of(uint32_t ks, uint32_t per) {
-  const uint32_t p = (ks - 1) / per + 2;
+Div div_of(uint32_t d) {
+  int l = 0;
+  while ((1u << l) < d) ++l;
+  return {d == 1 ? 0u : uint32_t((1ull << (31 + l)) / d + 1), l - 1};
+}
+// A product's sizes, known on the host: steps of a unit, units of an expert.
+struct Shape {
+  uint32_t ks, nb;
+  Div by_ks, by_nb;
+};
+Shape shape_of(long long ks, long long nb) {
+  return {uint32_t(ks), uint32_t(nb), div_of(uint32_t(ks)), div_of(uint32_t(nb))};
+}
+// Its units' steps in a row, cut into runs of `run` steps. Up to kOneRun steps a
+// CTA: one run each, equal ones. More: runs of a power of two, sixteen to 32 a
+// CTA, taken as they come: some SMs are a fifth slower than others at reading
+// (64 tokens of the large layer: 2.72 ms with equal shares, 2.32 this way). Runs
+// of a sixteenth of a unit or more, which bounds the partial sums.
+constexpr uint32_t kOneRun = 32;
+struct Phase {
+  uint32_t ks, nb;
+  uint32_t total, run, runs;
+  uint32_t parts;  // runs that a unit may be cut over
+  uint32_t by_run; // n / run: 2^32 / run + 1, exact for powers of two and for n * run < 2^32
+  Div by_ks, by_nb;
+};
+__host__ __device__ __forceinline__ uint32_t least_run(uint32_t ks) {
+  uint32_t run = 4;
+  while (run * 16 < ks) run *= 2;
+  return run;
+}
+__host__ __device__ __forceinline__ uint32_t run_of(uint32_t total, uint32_t ks) {
+  const uint32_t per = (total + kMaxCtas - 1) / kMaxCtas;
+  if (per <= kOneRun) return per > 1 ? per : 1;
+  uint32_t run = least_run(ks);
+  while (run * 32 <= per) run *= 2;
+  return run;
+}
+// Unit u is in runs u * ks / run up to ((u + 1) * ks - 1) / run, so many at most:
+__host__ __device__ __forceinline__ uint32_t parts_of(uint32_t ks, uint32_t run) {
+  const uint32_t p = (ks - 1) / run + 2;
   return p < ks ? p : ks;
 }
-__device__ __forceinline__ Phase make_phase(uint32_t experts, uint32_t nb, uint32_t ks) {
+__device__ __forceinline__ Phase make_phase(uint32_t experts, const Shape& s) {
   Phase p;
-  p.ks = ks, p.nb = nb;
-  const uint32_t total = experts * nb * ks;
-  p.per = max(1u, (total + gridDim.x - 1) / gridDim.x);
-  p.parts = parts_of(ks, p.per);
-  p.begin = min(total, blockIdx.x * p.per);
-  p.n = min(total, p.begin + p.per) - p.begin;
+  p.ks = s.ks, p.nb = s.nb, p.by_ks = s.by_ks, p.by_nb = s.by_nb;
+  p.total = experts * s.nb * s.ks;
+  p.run = run_of(p.total, s.ks);
+  p.by_run = 0xffffffffu / p.run + 1;
+  p.parts = p.run % s.ks == 0 ? 1 : parts_of(s.ks, p.run);
+  p.runs = (p.total + p.run - 1) / p.run;
   return p;
 }
-__device__ __forceinline__ uint32_t first_cta(const Phase& p, uint32_t unit) { return unit * p.ks / p.per; }
+__device__ __forceinline__ uint32_t run_at(const Phase& p, uint32_t step) {
+  return p.by_run == 0 ? step : __umulhi(step, p.by_run);
+}
 __device__ __forceinline__ uint32_t parts_in(const Phase& p, uint32_t unit) {
-  return ((unit + 1) * p.ks - 1) / p.per - first_cta(p, unit) + 1;
+  return p.parts == 1 ? 1 : run_at(p, (unit + 1) * p.ks - 1) - run_at(p, unit * p.ks) + 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -88,6 +129,7 @@ struct Ring {
   uint32_t stage0, stage_bytes; // first stage
   uint32_t x_at, plane;         // of a stage: where the rows of x start; bytes of a plane of them
   int stages;
+  volatile uint32_t* step;      // of a stage: which step it holds, or kEnd
   volatile int* abort;
   int32_t* status;
 };
@@ -98,25 +140,22 @@ struct Cursor {
     if (++slot == stages) slot = 0, parity ^= 1;
   }
 };
-// Where a product's weights lie: expert e's first panel of unit j, and the second panel of the unit.
+// Where a product's weights lie. A unit's four panels of 64 columns are two and
+// two: of the first and the second half of its columns.
 struct Weights {
-  const CUtensorMap* map;                // bf16
-  const uint8_t* w4;                     // 4 bits
-  long long expert, panel, second;       //   bytes
-  int col, col_second;                   // bf16: columns of the same
-  int limit;                             // units whose j * 128 + 64 reaches it have no second panel
-  int K;                                 // rows
+  const CUtensorMap* map;           // bf16
+  const uint8_t* w4;                // 4 bits
+  long long expert, panel, second;  //   bytes of an expert, of a panel; from a unit's first to its third panel
+  int unit, col_second;             // panels from unit to unit; bf16: columns from the first to the third
+  int columns;                      // of a half that there are (both products have the first panel of a unit)
+  bool gated;                       // the halves are gate and up columns, each counted to `columns`
+  int K;                            // rows
 };
 // Rows of x: `planes` of them after one another (the activation's two).
 struct Rows {
   const char* p;
   long long pitch;  // bytes
   int K;            // bf16 of a row
-};
-struct List {
-  const uint16_t *expert, *start;  // of an entry: its expert, its first row
-  const uint16_t* row;             // of a row: t * K + k
-  int entries;
 };
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -131,70 +170,166 @@ __device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t byt
                : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
-
-// One thread: weights of steps [from, to) of this CTA's run.
-template <int FMT>
-__device__ __forceinline__ void produce_weights(const Phase& p, uint32_t from, uint32_t to, const Ring& r, Cursor& c,
-                                                const Weights& w, const uint16_t* expert, int block) {
-  uint32_t s = (p.begin + from) % p.ks, u = (p.begin + from) / p.ks;
-  uint32_t j = u % p.nb, e = u / p.nb;
-  for (uint32_t i = from; i < to; ++i) {
-    const uint32_t bar = r.full + 8 * c.slot, dst = r.stage0 + c.slot * r.stage_bytes;
-    if (!wait_phase(r.empty + 8 * c.slot, c.parity ^ 1, r.abort, r.status)) return;
-    const bool two = int(j * kUnit + kW4Cols) < w.limit;
-    if (FMT == MEP_BF16) {
-      const uint32_t bytes = step_rows(FMT) * kPanelRow;
-      mbar_expect_tx(bar, two ? 2 * bytes : bytes);
-      tma_3d(dst, w.map, j * w.col, s * step_rows(FMT), expert[e], bar);
-      if (two) tma_3d(dst + bytes, w.map, j * w.col + w.col_second, s * step_rows(FMT), expert[e], bar);
-    } else {
-      const int left = (w.K + kW4Rows - 1) / kW4Rows - 2 * int(s);
-      const uint32_t bytes = (left < 2 ? 1 : 2) * block;
-      const uint8_t* src = w.w4 + expert[e] * w.expert + j * w.panel + (long long)s * (2 * block);
-      mbar_expect_tx(bar, two ? 2 * bytes : bytes);
-      bulk(dst, src, bytes, bar);
-      if (two) bulk(dst + 2 * block, src + w.second, bytes, bar);
-    }
-    c.next(r.stages);
-    if (++s == p.ks) {
-      s = 0;
-      if (++j == p.nb) j = 0, ++e;
-    }
-  }
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A whole warp waits; the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Ring& r) {
+  if (__all_sync(MEP_FULL_MASK, mbar_try_wait_long(bar, parity))) return true;
+  return __all_sync(MEP_FULL_MASK, wait_phase(bar, parity, r.abort, r.status));
 }
 
-// One warp: the rows of x of all steps of this CTA's run. ROW(entry's row number) -> row of x.
-template <int FMT, int PLANES, typename RowOf>
-__device__ __forceinline__ void produce_rows(const Phase& p, const Ring& r, Cursor& c, const Rows& x,
-                                             const uint16_t* start, RowOf row_of) {
-  constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
-  const int lane = threadIdx.x & 31;
-  uint32_t s = p.begin % p.ks, u = p.begin / p.ks;
-  uint32_t j = u % p.nb, e = u / p.nb;
-  for (uint32_t i = 0; i < p.n; ++i) {
-    const uint32_t bar = r.full + 8 * c.slot, dst = r.stage0 + c.slot * r.stage_bytes + r.x_at;
-    const int first = start[e], m = start[e + 1] - first, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
-    if (!__all_sync(MEP_FULL_MASK, wait_phase(r.empty + 8 * c.slot, c.parity ^ 1, r.abort, r.status))) return;
+// ---------------------------------------------------------------------------
+// The producer warp's side. A step's stage is full once its weights have come
+// and its rows have: two arrivals. What a step needs is worked out where its
+// unit begins; a step itself has to cost less than its bytes take to come (a
+// stage of 32 KB in 0.75 us).
+template <int FMT, int PLANES> struct Stream {
+  static constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
+  uint32_t step, end;      // of the run
+  uint32_t s, j, entry;    // step of the unit, unit of the expert, the expert's entry
+  uint32_t tx;             // bytes of a full step's weights
+  int e, m, panels;        // panels: a bit for each that is there
+  const uint8_t* w;        // 4 bits: the unit's first panel
+  const char* row[2];      // this lane's rows of x
+  uint32_t at[2];          // and where they go in a stage
+
+  __device__ __forceinline__ void init(const Ring& r) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = lane + 32 * i;
+      at[i] = r.x_at + (q % PLANES) * r.plane + (q / PLANES) * pitch;
+    }
+  }
+  template <typename RowOf>
+  __device__ __forceinline__ void unit(const Weights& w_, const Rows& x, const uint16_t* expert, const uint16_t* start,
+                                       int block, RowOf row_of) {
+    const int lane = threadIdx.x & 31, first = start[entry], panel = j * w_.unit;
+    m = start[entry + 1] - first, e = expert[entry];
+    const int count = (w_.columns + kW4Cols - 1) / kW4Cols - panel;
+    panels = w_.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
+    tx = __popc(panels) * (FMT == MEP_BF16 ? step_rows(FMT) * kPanelRow : 2 * block);
+    if (FMT == MEP_W4) w = w_.w4 + e * w_.expert + panel * w_.panel;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int q = lane + 32 * i;
+      if (q < PLANES * m) row[i] = x.p + (row_of(first + q / PLANES) * PLANES + q % PLANES) * x.pitch;
+    }
+  }
+  template <typename RowOf>
+  __device__ __forceinline__ void seek(uint32_t to, const Phase& p, const Weights& w_, const Rows& x,
+                                       const uint16_t* expert, const uint16_t* start, int block, RowOf row_of) {
+    step = to, end = min(p.total, to + p.run);
+    if (step >= end) return;
+    const uint32_t u = p.by_ks(step);
+    s = step - u * p.ks, entry = p.by_nb(u), j = u - entry * p.nb;
+    unit(w_, x, expert, start, block, row_of);
+  }
+  template <typename RowOf>
+  __device__ __forceinline__ void next(const Phase& p, const Weights& w_, const Rows& x, const uint16_t* expert,
+                                       const uint16_t* start, int block, RowOf row_of) {
+    if (++step == end || ++s < p.ks) return;
+    s = 0;
+    if (++j == p.nb) j = 0, ++entry;
+    unit(w_, x, expert, start, block, row_of);
+  }
+  __device__ __forceinline__ void weights(const Ring& r, int slot, const Weights& w_, int block) const {  // one lane
+    const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
+    r.step[slot] = step;
+    if (FMT == MEP_BF16) {
+      constexpr uint32_t bytes = step_rows(FMT) * kPanelRow;
+      const int col = j * w_.unit * kW4Cols, k = s * BK;
+      mbar_expect_tx(bar, tx);
+#pragma unroll
+      for (int q = 0; q < kPanels; ++q)
+        if (panels >> q & 1) tma_3d(dst + q * bytes, w_.map, col + (q & 1) * kW4Cols + (q >> 1) * w_.col_second, k, e, bar);
+    } else {
+      const uint8_t* src = w + s * (2 * block);
+      const uint32_t half = 2 * int(s) + 1 == (w_.K + kW4Rows - 1) / kW4Rows;  // the last step may have one block
+      mbar_expect_tx(bar, tx >> half);
+#pragma unroll
+      for (int q = 0; q < kPanels; ++q)
+        if (panels >> q & 1)
+          bulk(dst + q * 2 * block, src + (q & 1) * w_.panel + (q >> 1) * w_.second, (2 * block) >> half, bar);
+    }
+  }
+  __device__ __forceinline__ void rows(const Ring& r, int slot, const Rows& x) const {  // the warp
+    const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
+    const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
     if (bytes < 2 * BK) {  // beyond the sum's end the weights are zeros: what they meet must be numbers
-      for (int q = lane; q < PLANES * m; q += 32) {
-        const uint32_t d = dst + (q % PLANES) * r.plane + (q / PLANES) * pitch;
-        for (int b = bytes; b < 2 * BK; b += 16)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(d + b), "r"(0) : "memory");
-      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < PLANES * m)
+          for (int b = bytes; b < 2 * BK; b += 16)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at[i] + b), "r"(0) : "memory");
       fence_async();
       __syncwarp();
     }
     if (lane == 0) mbar_expect_tx(bar, PLANES * m * bytes);
-    __syncwarp();
-    for (int q = lane; q < PLANES * m; q += 32)
-      bulk(dst + (q % PLANES) * r.plane + (q / PLANES) * pitch,
-           x.p + (row_of(first + q / PLANES) * PLANES + q % PLANES) * x.pitch + 2 * k0, bytes, bar);
-    c.next(r.stages);
-    if (++s == p.ks) {
-      s = 0;
-      if (++j == p.nb) j = 0, ++e;
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (lane + 32 * i < PLANES * m) bulk(dst + at[i], row[i] + 2 * k0, bytes, bar);
   }
+};
+
+// Before a barrier of the grid: the weights of as many steps of the CTA's own
+// run as the ring has room for, and their rows where these are there already.
+template <int FMT, bool ROWS, int PLANES, typename RowOf>
+__device__ __forceinline__ void feed_ahead(Stream<FMT, PLANES>& t, const Phase& p, const Ring& r, Cursor& c,
+                                           const Weights& w, const Rows& x, const uint16_t* expert,
+                                           const uint16_t* start, int block, RowOf row_of) {
+  t.init(r);
+  t.seek(min(p.total, blockIdx.x * p.run), p, w, x, expert, start, block, row_of);
+  for (int i = 0; i < r.stages && t.step < t.end; ++i) {
+    if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) break;
+    if ((threadIdx.x & 31) == 0) t.weights(r, c.slot, w, block);
+    if (ROWS) t.rows(r, c.slot, x);
+    c.next(r.stages);
+    t.next(p, w, x, expert, start, block, row_of);
+  }
+}
+// After it: the rest of the own run, further runs off the counter, the end's
+// mark. `behind`: the first stage fed ahead, whose rows are due.
+template <int FMT, bool ROWS, int PLANES, typename RowOf>
+__device__ __forceinline__ void feed(Stream<FMT, PLANES>& t, Cursor behind, const Phase& p, const Ring& r, Cursor& c,
+                                     const Weights& w, const Rows& x, const uint16_t* expert, const uint16_t* start,
+                                     int block, uint32_t* counter, RowOf row_of) {
+  const int lane = threadIdx.x & 31;
+  const bool more = p.runs > gridDim.x;
+  uint32_t next = 0;
+  if (more && lane == 0) next = atomicAdd(counter, 1u);  // on its way while the run is fed
+  if (!ROWS) {
+    const uint32_t to = t.step, end = t.end;
+    t.seek(min(p.total, blockIdx.x * p.run), p, w, x, expert, start, block, row_of);
+    while (t.step < to) {
+      t.rows(r, behind.slot, x);
+      behind.next(r.stages);
+      t.next(p, w, x, expert, start, block, row_of);
+    }
+    t.end = end;
+  }
+  while (true) {
+    if (t.step == t.end) {
+      const uint32_t run = more ? gridDim.x + __shfl_sync(MEP_FULL_MASK, next, 0) : p.runs;
+      if (run >= p.runs) break;
+      t.seek(run * p.run, p, w, x, expert, start, block, row_of);
+      if (lane == 0) next = atomicAdd(counter, 1u);
+    }
+    if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
+    if (lane == 0) t.weights(r, c.slot, w, block);
+    t.rows(r, c.slot, x);
+    c.next(r.stages);
+    t.next(p, w, x, expert, start, block, row_of);
+  }
+  if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
+  if (lane == 0) {
+    r.step[c.slot] = kEnd;
+    arrive(r.full + 8 * c.slot);
+    arrive(r.full + 8 * c.slot);
+  }
+  c.next(r.stages);
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -212,9 +347,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&v)[4], uint32_t addr)
                : "memory");
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -226,32 +361,37 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-// Operand of one step: two q at bits 4i and 16 + 4i of the word, behind the bits of bf16 128, less 136.
+// Operand of one step, over 64: the word's four pairs of q + 8 at bits 0, 4, 8
+// and 12 of either half. Bits 0-7 of a bf16 without more are that whole number
+// times 2^-133 (subnormal up to 127, the first binade above), so that one fused
+// multiply-add takes a pair to q / 64, exactly, wherever in the byte it was.
 __device__ __forceinline__ void widen_q(uint32_t word, uint32_t (&a)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = ((word >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(a[i]) : "r"(v), "r"(0x43084308u));
+  for (int i = 0; i < 2; ++i, word >>= 8) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[2 * i]) : "r"(word & 0x000f000fu), "r"(0x7f007f00u), "r"(0xbe00be00u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(a[2 * i + 1]) : "r"(word & 0x00f000f0u), "r"(0x7d007d00u), "r"(0xbe00be00u));
   }
 }
+constexpr float kQ = 64.f;
 
-// This warp's share of a stage: 16 columns of either panel, slice `sl` of the rows.
+// This warp's share of a stage: 16 columns of either half, slice `sl` of the rows.
 template <int FMT, int SLICES, int NT, int PLANES>
 __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t stage, const Ring& r, int mi, int sl,
-                                              int group, int block) {
+                                              int blocks, int group, int block) {
   constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
   const int lane = threadIdx.x & 31;
-  const uint32_t xb = stage + r.x_at + (lane & 7) * pitch + (sl * (BK / SLICES) + 8 * (lane >> 3)) * 2;
+  const uint32_t xb = stage + r.x_at + (lane & 7) * pitch + 16 * (lane >> 3);
   if (FMT == MEP_BF16) {
-    const uint32_t wa = stage + (sl * (BK / SLICES) + (lane >> 4) * 8 + (lane & 7)) * kPanelRow +
-                        (((2 * mi + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+    const uint32_t wa = stage + (mi >> 2) * (BK * kPanelRow) + ((lane >> 4) * 8 + (lane & 7)) * kPanelRow +
+                        (((2 * (mi & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
 #pragma unroll
-    for (int k = 0; k < BK / SLICES; k += 32) {
+    for (int i = 0; i < BK / SLICES; i += 32) {
+      const int k = sl * (BK / SLICES) + i;
       uint32_t a[2][2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) ldmatrix4_trans(a[q][s], wa + q * (BK * kPanelRow) + (k + 16 * s) * kPanelRow);
+        for (int s = 0; s < 2; ++s) ldmatrix4_trans(a[q][s], wa + q * (2 * BK * kPanelRow) + (k + 16 * s) * kPanelRow);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -266,56 +406,55 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
         }
     }
   } else {
-    // 64 rows at a time: a lane's 16 bytes of either panel
 #pragma unroll
-    for (int k = 0; k < BK / SLICES; k += 64) {
-      const int row = sl * (BK / SLICES) + k, b = row / kW4Rows, h = row / 64 % 2;
-      const uint32_t wb = stage + b * block;
-      uint4 words[2];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) words[q] = lds128(wb + q * 2 * block + ((h * 4 + mi) * 32 + lane) * 16);
-      const uint32_t sb = wb + kW4Pairs + (mi * 8 + (lane >> 2)) * 4;
-      // groups of 32 rows scale every 32, the others every 64 (128 is 64 twice, by the same scale)
-      const uint32_t g0 = 64 * h / group * 128, g1 = (64 * h + 32) / group * 128;
-      const bool split = group == 32;
+    for (int i = 0; i < 2 / SLICES; ++i) {
+      const int b = SLICES == 1 ? i : sl;  // block of 128 rows
+      if (b >= blocks) break;
+      const uint32_t wb = stage + (mi >> 2) * 2 * block + b * block;
+      const uint32_t at = wb + ((mi & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((mi & 3) * 8 + (lane >> 2)) * 4;
       float sum[2][NT][4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if (half == 0 || split) {
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+        for (int n = 0; n < NT; ++n) sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
-        }
-        uint32_t a[2][2][4];
+      for (int h = 0; h < 2; ++h) {
+        const uint4 w0 = lds128(at + h * 2048), w1 = lds128(at + h * 2048 + 4 * block);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          widen_q(half ? words[q].z : words[q].x, a[q][0]);
-          widen_q(half ? words[q].w : words[q].y, a[q][1]);
-        }
+        for (int half = 0; half < 2; ++half) {
+          const int k = 128 * b + 64 * h + 32 * half;
+          uint32_t a[2][2][4];
+          widen_q(half ? w0.z : w0.x, a[0][0]);
+          widen_q(half ? w0.w : w0.y, a[0][1]);
+          widen_q(half ? w1.z : w1.x, a[1][0]);
+          widen_q(half ? w1.w : w1.y, a[1][1]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int pl = 0; pl < PLANES; ++pl) {
-            uint32_t bx[4];
-            ldmatrix4(bx, xb + pl * r.plane + n * (8 * pitch) + 2 * (k + 32 * half));
+            for (int pl = 0; pl < PLANES; ++pl) {
+              uint32_t bx[4];
+              ldmatrix4(bx, xb + pl * r.plane + n * (8 * pitch) + 2 * k);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                mma(sum[q][n], a[q][0], bx[0], bx[1]);
+                mma(sum[q][n], a[q][1], bx[2], bx[3]);
+              }
+            }
+          const int end = 64 * h + 32 * half + 32;
+          if (end == 128 || (end == 64 && group <= 64) || group == 32) {  // a group ends here
+            const uint32_t row = (end - 1) / group * 128;
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              mma(sum[q][n], a[q][0], bx[0], bx[1]);
-              mma(sum[q][n], a[q][1], bx[2], bx[3]);
-            }
-          }
-        if (half == 1 || split) {
+              const uint32_t sc = lds32(sb + row + q * 4 * block);
+              const float lo = __uint_as_float(sc << 16), hi = __uint_as_float(sc & 0xffff0000u);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t sc = lds32(sb + q * 2 * block + (half ? g1 : g0));
-            const float lo = __uint_as_float(sc << 16), hi = __uint_as_float(sc & 0xffff0000u);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              acc[q][n][0] = fmaf(lo, sum[q][n][0], acc[q][n][0]);
-              acc[q][n][1] = fmaf(lo, sum[q][n][1], acc[q][n][1]);
-              acc[q][n][2] = fmaf(hi, sum[q][n][2], acc[q][n][2]);
-              acc[q][n][3] = fmaf(hi, sum[q][n][3], acc[q][n][3]);
+              for (int n = 0; n < NT; ++n) {
+                acc[q][n][0] = fmaf(lo, sum[q][n][0], acc[q][n][0]);
+                acc[q][n][1] = fmaf(lo, sum[q][n][1], acc[q][n][1]);
+                acc[q][n][2] = fmaf(hi, sum[q][n][2], acc[q][n][2]);
+                acc[q][n][3] = fmaf(hi, sum[q][n][3], acc[q][n][3]);
+                sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
+              }
             }
           }
         }
@@ -324,11 +463,17 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
   }
 }
 
-// Steps of one unit, then its partial sum: slices joined through shared memory
-// (in order), the first slice's warps write. PUT(panel, column of 64, token, value).
+struct Join {              // of two slices
+  float4* room;            // [kM][2][32]
+  uint32_t full, empty;    // barriers, one each a pair of warps
+};
+
+// `steps` steps of one unit from its step s on, then their sum: the slices are
+// joined, in order, and the first one's warps write it. PUT(half, column of the
+// half, token, value).
 template <int FMT, int SLICES, int NT, int PLANES, typename Put>
-__device__ __forceinline__ void unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int m,
-                                             int group, int block, float4* s_join, Put put) {
+__device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int m,
+                                             int group, int block, const Join& join, uint32_t& turn, Put put) {
   constexpr int BK = step_rows(FMT);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mi = warp % kM, sl = warp / kM;
   float acc[2][NT][4];
@@ -337,93 +482,108 @@ __device__ __forceinline__ void unit_product(uint32_t steps, uint32_t s, int K, 
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.f;
   for (; steps > 0; --steps, ++s) {
-    if (!__all_sync(MEP_FULL_MASK, wait_phase(r.full + 8 * c.slot, c.parity, r.abort, r.status))) break;
-    // a slice wholly beyond the sum's end has no weights (4 bits) or zeros
-    if (int(s * BK) + sl * (BK / SLICES) / kW4Rows * kW4Rows < K)
-      stage_product<FMT, SLICES, NT, PLANES>(acc, r.stage0 + c.slot * r.stage_bytes, r, mi, sl, group, block);
+    if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
+    const int blocks = FMT == MEP_W4 ? (K - int(s * BK) + kW4Rows - 1) / kW4Rows : 0;
+    stage_product<FMT, SLICES, NT, PLANES>(acc, r.stage0 + c.slot * r.stage_bytes, r, mi, sl, blocks, group, block);
     __syncwarp();
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(r.empty + 8 * c.slot) : "memory");
+    if (lane == 0) arrive(r.empty + 8 * c.slot);
     c.next(r.stages);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     if (8 * n >= m) break;
-    float4* mine = s_join + ((sl - 1) * kM + mi) * 64 + lane;
-    if (sl > 0) {
-      mine[0] = make_float4(acc[0][n][0], acc[0][n][1], acc[0][n][2], acc[0][n][3]);
-      mine[32] = make_float4(acc[1][n][0], acc[1][n][1], acc[1][n][2], acc[1][n][3]);
+    if (SLICES == 2) {
+      float4* mine = join.room + mi * 64 + lane;
+      if (sl == 1) {
+        if (!warp_wait(join.empty + 8 * mi, turn & 1 ^ 1, r)) return false;
+        mine[0] = make_float4(acc[0][n][0], acc[0][n][1], acc[0][n][2], acc[0][n][3]);
+        mine[32] = make_float4(acc[1][n][0], acc[1][n][1], acc[1][n][2], acc[1][n][3]);
+        __syncwarp();
+        if (lane == 0) arrive(join.full + 8 * mi);
+      } else {
+        if (!warp_wait(join.full + 8 * mi, turn & 1, r)) return false;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 f = mine[32 * q];
+          acc[q][n][0] += f.x, acc[q][n][1] += f.y, acc[q][n][2] += f.z, acc[q][n][3] += f.w;
+        }
+        __syncwarp();
+        if (lane == 0) arrive(join.empty + 8 * mi);
+      }
+      ++turn;
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + mi), "r"(32 * SLICES) : "memory");
     if (sl == 0) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float v[4] = {acc[q][n][0], acc[q][n][1], acc[q][n][2], acc[q][n][3]};
-#pragma unroll
-        for (int o = 1; o < SLICES; ++o) {
-          const float4 f = s_join[((o - 1) * kM + mi) * 64 + 32 * q + lane];
-          v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-        }
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = 8 * n + 2 * (lane & 3) + (i & 1);
-          if (t < m) put(q, 16 * mi + (lane >> 2) + 8 * (i >> 1), t, v[i]);
+          if (t < m) put(q, 16 * mi + (lane >> 2) + 8 * (i >> 1), t, FMT == MEP_W4 ? kQ * acc[q][n][i] : acc[q][n][i]);
         }
-      }
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + mi), "r"(32 * SLICES) : "memory");
   }
+  return true;
 }
 
-// All units of this CTA's run. PUT(entry, unit of the expert, part, panel, column, token, value).
+// All steps that this CTA is fed. PUT(first row, unit of the expert, part, half, column, token, value).
 template <int FMT, int SLICES, int NTMAX, int PLANES, typename Put>
 __device__ __forceinline__ void products(const Phase& p, int K, const Ring& r, Cursor& c, const uint16_t* start,
-                                         int group, int block, float4* s_join, Put put) {
-  uint32_t i = 0;
-  while (i < p.n) {  // after a wait that gave up too: the joins' barriers want every warp
-    const uint32_t at = p.begin + i, u = at / p.ks, s = at % p.ks, steps = min(p.ks - s, p.n - i);
-    const uint32_t e = u / p.nb, j = u % p.nb, part = blockIdx.x - first_cta(p, u);
-    const int m = start[e + 1] - start[e];
-    const auto f = [&](int q, int col, int t, float v) { put(e, j, part, q, col, t, v); };
+                                         int group, int block, const Join& join, uint32_t& turn, Put put) {
+  while (true) {
+    if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return;
+    const uint32_t at = r.step[c.slot];
+    if (at == kEnd) break;
+    const uint32_t u = p.by_ks(at), s = at - u * p.ks, run = run_at(p, at);
+    const uint32_t steps = min(min(p.ks - s, (run + 1) * p.run - at), p.total - at);
+    const uint32_t e = p.by_nb(u), j = u - e * p.nb, part = p.parts == 1 ? 0 : run - run_at(p, u * p.ks);
+    const int first = start[e], m = start[e + 1] - first;
+    const auto f = [&](int q, int col, int t, float v) { put(first, j, part, q, col, t, v); };
+    bool ok;
     if (m <= 8)
-      unit_product<FMT, SLICES, 1, PLANES>(steps, s, K, r, c, m, group, block, s_join, f);
+      ok = unit_product<FMT, SLICES, 1, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
     else if (m <= 16)
-      unit_product<FMT, SLICES, 2, PLANES>(steps, s, K, r, c, m, group, block, s_join, f);
+      ok = unit_product<FMT, SLICES, 2, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
     else if (NTMAX <= 4 || m <= 32)
-      unit_product<FMT, SLICES, 4, PLANES>(steps, s, K, r, c, m, group, block, s_join, f);
+      ok = unit_product<FMT, SLICES, 4, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
     else
-      unit_product<FMT, SLICES, NTMAX, PLANES>(steps, s, K, r, c, m, group, block, s_join, f);
-    i += steps;
+      ok = unit_product<FMT, SLICES, NTMAX, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
+    if (!ok) return;
   }
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(r.empty + 8 * c.slot);
+  c.next(r.stages);
 }
 
 // Stages for rows of up to m tokens (as many as a unit's instantiation computes).
 template <int FMT, int PLANES>
 __device__ __forceinline__ void size_ring(Ring& r, uint32_t room, int m, int block) {
   const int rows = m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64;
-  r.x_at = FMT == MEP_BF16 ? 2 * step_rows(FMT) * kPanelRow : 4 * block;
+  r.x_at = FMT == MEP_BF16 ? kPanels * step_rows(FMT) * kPanelRow : kPanels * 2 * block;
   r.plane = rows * (step_rows(FMT) * 2 + 16);
   r.stage_bytes = (r.x_at + PLANES * r.plane + 1023) / 1024 * 1024;
   r.stages = min(kMaxStages, int(room / r.stage_bytes));
 }
 
 struct Head {  // start of shared memory
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages], join_full[kM], join_empty[kM];
+  uint32_t step[kMaxStages];
   int warp_sums[32];
   int abort, bad, most, entries, rows, go;
 };
+constexpr uint32_t kHeadBytes = 1024;
+__host__ __device__ constexpr uint32_t join_bytes(int slices) { return (slices - 1) * kM * 64 * 16; }
 
-__device__ __forceinline__ void init_ring(Ring& r, Head* h, int consumers, int32_t* status) {
+__device__ __forceinline__ void init_ring(Ring& r, Join& join, Head* h, char* room, int consumers, int32_t* status) {
   r.full = smem_u32(h->full), r.empty = smem_u32(h->empty);
-  r.abort = &h->abort, r.status = status;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(r.full + 8 * i, 2);  // weights, rows
-      mbar_init(r.empty + 8 * i, consumers);
-    }
+  r.step = h->step, r.abort = &h->abort, r.status = status;
+  join.full = smem_u32(h->join_full), join.empty = smem_u32(h->join_empty), join.room = reinterpret_cast<float4*>(room);
+  if (threadIdx.x < kMaxStages) {
+    mbar_init(r.full + 8 * threadIdx.x, 2);  // weights, rows
+    mbar_init(r.empty + 8 * threadIdx.x, consumers);
+    if (threadIdx.x < kM) mbar_init(join.full + 8 * threadIdx.x, 1), mbar_init(join.empty + 8 * threadIdx.x, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    h->abort = h->bad = h->most = 0;
   }
+  if (threadIdx.x == 0) h->abort = h->bad = h->most = 0;
 }
 
 // After a wait that gave up: copies may be under way still; they land before the CTA's memory is another's.
@@ -437,6 +597,15 @@ __device__ __forceinline__ void settle(const Ring& r) {
   __syncthreads();
 }
 
+// Items [0, n) over the grid's warps, one CTA's after another's: a few items are on as many SMs.
+struct Spread {
+  uint32_t i, step;
+};
+__device__ __forceinline__ Spread spread() {
+  const uint32_t warps = blockDim.x / 32;
+  return {((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31), warps * gridDim.x * 32};
+}
+
 // ---------------------------------------------------------------------------
 struct LayerArgs {
   const __nv_bfloat16* x;
@@ -445,6 +614,9 @@ struct LayerArgs {
   const uint8_t *w1, *w2;
   int32_t* status;
   int T, K, E, H, F, group;
+  Shape s1, s2;
+  Div by_k;
+  uint32_t* counters;
   float *part1, *part2;
   __nv_bfloat16* act;
   __nv_bfloat16* out;
@@ -454,74 +626,88 @@ __host__ __device__ __forceinline__ int max_entries(int T, int K, int E) {
   return (E < T * K ? E : T * K) + T * K / kChunk;
 }
 __host__ __device__ __forceinline__ uint32_t list_bytes(int T, int K, int E) {
-  return (2u * (2 * max_entries(T, K, E) + 1 + 3 * T * K) + 1023) / 1024 * 1024;
+  return (2u * (2 * max_entries(T, K, E) + 1 + 3 * T * K) + 4u * T * K + 1023) / 1024 * 1024;
 }
-__host__ __device__ __forceinline__ uint32_t join_bytes(int slices) { return (slices - 1) * kM * 64 * 16; }
-constexpr uint32_t kHeadBytes = 1024;
-static_assert(sizeof(Head) <= kHeadBytes, "head");
+
+struct Lists {              // in shared memory
+  float* weight;            // of an assignment, as given
+  uint16_t *expert, *start; // of an entry: its expert, its first row (one more at the end)
+  uint16_t *entry, *token;  // of a row
+  uint16_t* row;            // of an assignment; kNone
+};
+constexpr uint16_t kNone = 0xffff;
 
 // The experts in use in ascending order, each one's tokens in order, more than
-// kChunk of them in several entries; where each assignment went.
-__device__ __forceinline__ void make_list(const LayerArgs& a, Head* h, char* scratch, uint16_t* expert, uint16_t* start,
-                                          uint16_t* row_entry, uint16_t* row_of, uint16_t* row_token) {
+// kChunk of them in several entries; where each assignment went. What comes from
+// memory is asked for at the start, the barriers' words are set up meanwhile.
+__device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Join& join, Head* h, char* room, int consumers,
+                                          char* scratch, const Lists& l) {
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
-  uint16_t* e_start = reinterpret_cast<uint16_t*>(mask + a.E);
-  uint16_t* e_entry = e_start + a.E;
+  uint32_t* e_at = reinterpret_cast<uint32_t*>(mask + a.E);  // entry and first row of an expert
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, A = a.T * a.K;
+  const int mine = tid < A ? __ldg(a.idx + tid) : -1;
+  const float weight = tid < A ? __ldg(a.topk_w + tid) : 0.f;
+  const int held = tid == 0 ? read_status(a.status) : 0;
+  init_ring(r, join, h, room, consumers, a.status);
   for (int e = tid; e < a.E; e += threads) mask[e] = 0;
+  if (tid == 0 && blockIdx.x == 0) a.counters[0] = a.counters[1] = 0;
   __syncthreads();
-  for (int i = tid; i < A; i += threads) {
-    const int e = a.idx[i];
+  if (tid == 0) h->go = held == 0;
+#pragma unroll 1
+  for (int i = tid, e = mine; i < A;) {
     if (e >= 0 && e < a.E) {
-      const unsigned long long bit = 1ull << (i / a.K);
+      const unsigned long long bit = 1ull << a.by_k(i);
       if (atomicOr(&mask[e], bit) & bit) h->bad = 1;
     } else if (e != -1) {
       h->bad = 1;
     }
+    if ((i += threads) < A) e = a.idx[i];
   }
   __syncthreads();
   // entries and rows before each thread's experts, in one word
-  const int per = (a.E + threads - 1) / threads, lo = min(a.E, tid * per), hi = min(a.E, lo + per);
-  int sum = 0, most = 0;
+  const int per = a.E <= threads ? 1 : (a.E + threads - 1) / threads, lo = min(a.E, tid * per), hi = min(a.E, lo + per);
+  uint32_t sum = 0;
+  int most = 0;
+#pragma unroll 1
   for (int e = lo; e < hi; ++e) {
     const int n = __popcll(mask[e]);
     sum += ((n + kChunk - 1) / kChunk << 16) + n;
     most = max(most, n);
   }
-  const int incl = warp_incl_scan(sum);
+  const uint32_t incl = warp_incl_scan(sum);
   most = __reduce_max_sync(MEP_FULL_MASK, most);
   if (lane == 31) h->warp_sums[warp] = incl;
-  if (lane == 0) atomicMax(&h->most, most);
+  if (lane == 0 && most > 0) atomicMax(&h->most, most);
   __syncthreads();
-  int before = 0, all = 0;
-  for (int w = 0; w < threads / 32; ++w) {
-    if (w < warp) before += h->warp_sums[w];
-    all += h->warp_sums[w];
-  }
-  before += incl - sum;
+  const uint32_t w = lane < threads / 32 ? h->warp_sums[lane] : 0;
+  const uint32_t all = __reduce_add_sync(MEP_FULL_MASK, w);
+  uint32_t before = __reduce_add_sync(MEP_FULL_MASK, lane < warp ? w : 0) + incl - sum;
+#pragma unroll 1
   for (int e = lo; e < hi; ++e) {
     const int n = __popcll(mask[e]);
-    int entry = before >> 16, row = before & 0xffff;
-    e_start[e] = row, e_entry[e] = entry;
-    for (int q = 0; q < n; q += kChunk, ++entry) expert[entry] = e, start[entry] = row + q;
+    int entry = before >> 16;
+    const int row = before & 0xffff;
+    e_at[e] = before;
+    for (int q = 0; q < n; q += kChunk, ++entry) l.expert[entry] = e, l.start[entry] = row + q;
     before += ((n + kChunk - 1) / kChunk << 16) + n;
   }
   if (tid == 0) {
     h->entries = all >> 16, h->rows = all & 0xffff;
-    start[all >> 16] = all & 0xffff;
+    l.start[all >> 16] = all & 0xffff;
   }
   __syncthreads();
-  for (int i = tid; i < A; i += threads) {
-    const int e = a.idx[i];
-    if (e < 0 || e >= a.E) {
-      row_of[i] = 0xffff;
-      continue;
+  if (!h->bad)
+#pragma unroll 1
+    for (int i = tid, e = mine; i < A;) {
+      l.weight[i] = i == tid ? weight : a.topk_w[i];
+      if (e < 0) {
+        l.row[i] = kNone;
+      } else {
+        const int t = a.by_k(i), rank = __popcll(mask[e] & ((1ull << t) - 1)), row = (e_at[e] & 0xffff) + rank;
+        l.row[i] = row, l.token[row] = t, l.entry[row] = (e_at[e] >> 16) + rank / kChunk;
+      }
+      if ((i += threads) < A) e = a.idx[i];
     }
-    const int t = i / a.K, rank = __popcll(mask[e] & ((1ull << t) - 1));
-    const int row = e_start[e] + rank;
-    row_of[i] = row;
-    if (!h->bad) row_token[row] = t, row_entry[row] = e_entry[e] + rank / kChunk;
-  }
   fence_async();  // the ring's copies come into the same memory
   __syncthreads();
 }
@@ -531,70 +717,74 @@ __global__ void __launch_bounds__(threads_of(SLICES), 1)
     k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const LayerArgs a) {
   extern __shared__ __align__(1024) char smem[];
   const auto grid = cooperative_groups::this_grid();
-  constexpr int BK = step_rows(FMT), NTMAX = kChunk / 8, kConsumers = kM * SLICES;
+  constexpr int NTMAX = kChunk / 8, kConsumers = kM * SLICES;
   Head* h = reinterpret_cast<Head*>(smem);
-  char* at = smem + kHeadBytes;
-  float4* s_join = reinterpret_cast<float4*>(at);
-  at += join_bytes(SLICES);
-  const int cap = max_entries(a.T, a.K, a.E), A = a.T * a.K;
-  uint16_t* expert = reinterpret_cast<uint16_t*>(at);
-  uint16_t* start = expert + cap;
-  uint16_t* row_entry = start + cap + 1;
-  uint16_t* row_of = row_entry + A;
-  uint16_t* row_token = row_of + A;
-  at += list_bytes(a.T, a.K, a.E);
-  Ring r;
-  init_ring(r, h, kConsumers, a.status);
+  Lists l;
+  {
+    const int cap = max_entries(a.T, a.K, a.E), A = a.T * a.K;
+    l.weight = reinterpret_cast<float*>(smem + kHeadBytes + join_bytes(SLICES));
+    l.expert = reinterpret_cast<uint16_t*>(l.weight + A);
+    l.start = l.expert + cap;
+    l.entry = l.start + cap + 1;
+    l.token = l.entry + A;
+    l.row = l.token + A;
+  }
+  const uint16_t *expert = l.expert, *start = l.start;
+  const uint32_t used = kHeadBytes + join_bytes(SLICES) + list_bytes(a.T, a.K, a.E);
   const int block = FMT == MEP_W4 ? w4_block_bytes(a.group) : 0;
-  if (threadIdx.x == 0) h->go = read_status(a.status) == 0;
-  __syncthreads();
-  make_list(a, h, at, expert, start, row_entry, row_of, row_token);
+  Ring r;
+  Join join;
+  make_list(a, r, join, h, smem + kHeadBytes, kConsumers, smem + used, l);
   const bool go = h->go && !h->bad;
   if (h->go && h->bad && threadIdx.x == 0) set_status(a.status, MEP_ERR_BAD_ROUTING);
-  r.stage0 = smem_u32(at);
-  size_ring<FMT, 2>(r, kSmem - uint32_t(at - smem), min(h->most, kChunk), block);
+  r.stage0 = smem_u32(smem + used);
+  size_ring<FMT, 2>(r, kSmem - used, min(h->most, kChunk), block);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t experts = go ? h->entries : 0, rows = go ? h->rows : 0;
-  const Phase p1 = make_phase(experts, (a.F + 63) / 64, (a.H + BK - 1) / BK);
-  const Phase p2 = make_phase(experts, (a.H + kUnit - 1) / kUnit, (a.F + BK - 1) / BK);
+  const Phase p1 = make_phase(experts, a.s1), p2 = make_phase(experts, a.s2);
   const long long m1 = FMT == MEP_W4 ? w4_matrix_bytes(a.H, a.F, a.group) : 0, q1 = FMT == MEP_W4 ? w4_panel_bytes(a.H, a.group) : 0;
   const long long m2 = FMT == MEP_W4 ? w4_matrix_bytes(a.F, a.H, a.group) : 0, q2 = FMT == MEP_W4 ? w4_panel_bytes(a.F, a.group) : 0;
-  const Weights w1 = {&map1, a.w1, 2 * m1, q1, m1, 64, a.F, 0x7fffffff, a.H};
-  const Weights w2 = {&map2, a.w2, m2, 2 * q2, q2, kUnit, 64, a.H, a.F};
+  const Weights w1 = {&map1, a.w1, 2 * m1, q1, m1, 2, a.F, a.F, true, a.H};
+  const Weights w2 = {&map2, a.w2, m2, q2, 2 * q2, 4, 2 * kW4Cols, a.H, false, a.F};
   const Rows x1 = {reinterpret_cast<const char*>(a.x), 2LL * a.H, a.H};
   const Rows x2 = {reinterpret_cast<const char*>(a.act), 2LL * a.F, a.F};
-  Cursor c;
-  const uint32_t ahead = min(p2.n, uint32_t(r.stages));
+  const auto token = [&](int row) { return (long long)l.token[row]; };
+  const auto same = [&](int row) { return (long long)row; };
+  Cursor c, behind;
+  uint32_t turn = 0;
+  Stream<FMT, 1> t1;
+  Stream<FMT, 2> t2;
 
+  if (warp == kConsumers) feed_ahead<FMT, true>(t1, p1, r, c, w1, x1, expert, start, block, token);
+  if (p1.runs > gridDim.x || p2.runs > gridDim.x) grid.sync();  // the counters are zero
   if (warp == kConsumers) {
-    if (lane == 0) {
-      produce_weights<FMT>(p1, 0, p1.n, r, c, w1, expert, block);
-      produce_weights<FMT>(p2, 0, ahead, r, c, w2, expert, block);  // filling while the activation is computed
-    }
-    __syncwarp();
-  } else if (warp == kConsumers + 1) {
-    produce_rows<FMT, 1>(p1, r, c, x1, start, [&](int row) { return (long long)row_token[row]; });
+    feed<FMT, true>(t1, behind, p1, r, c, w1, x1, expert, start, block, a.counters, token);
+    behind = c;  // the ring fills while the activation is computed
+    feed_ahead<FMT, false>(t2, p2, r, c, w2, x2, expert, start, block, same);
   } else {
-    products<FMT, SLICES, NTMAX, 1>(p1, a.H, r, c, start, a.group, block, s_join,
-                                    [&](uint32_t e, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int f = j * 64 + col;
-                                      if (f < a.F)
-                                        a.part1[((long long)(start[e] + t) * p1.parts + part) * (2 * a.F) + q * a.F + f] = v;
+    products<FMT, SLICES, NTMAX, 1>(p1, a.H, r, c, start, a.group, block, join, turn,
+                                    [&](int first, uint32_t j, uint32_t part, int q, int col, int t, float v) {
+                                      const int n = j * (kUnit / 2) + col;
+                                      if (n < a.F)
+                                        a.part1[((long long)(first + t) * p1.parts + part) * (2 * a.F) + q * a.F + n] = v;
                                     });
   }
   grid.sync();
   {
-    const uint32_t quads = a.F / 4, n = rows * quads, step = gridDim.x * blockDim.x;
-    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-      const uint32_t row = i / quads, f = i % quads * 4;
-      const uint32_t parts = parts_in(p1, row_entry[row] * p1.nb + f / 64);
-      const float* in = a.part1 + (long long)row * p1.parts * (2 * a.F) + f;
+    constexpr uint32_t quads = kUnit / 8;  // of a unit's gates, four and the four ups a lane
+    const uint32_t n = rows * p1.nb * quads;
+#pragma unroll 1
+    for (Spread s = spread(); s.i < n; s.i += s.step) {
+      const uint32_t unit = s.i / quads, row = p1.by_nb(unit), j = unit - row * p1.nb, col = j * (kUnit / 2) + s.i % quads * 4;
+      if (int(col) >= a.F) continue;
+      const uint32_t parts = parts_in(p1, l.entry[row] * p1.nb + j);
+      const float* in = a.part1 + (long long)row * p1.parts * (2 * a.F) + col;
       float g[4] = {}, u[4] = {};
 #pragma unroll 4
-      for (uint32_t q = 0; q < parts; ++q) {
-        const float4 vg = *reinterpret_cast<const float4*>(in + q * (2LL * a.F));
-        const float4 vu = *reinterpret_cast<const float4*>(in + q * (2LL * a.F) + a.F);
+      for (uint32_t q = 0; q < parts; ++q, in += 2 * a.F) {
+        const float4 vg = __ldcg(reinterpret_cast<const float4*>(in));
+        const float4 vu = __ldcg(reinterpret_cast<const float4*>(in + a.F));
         g[0] += vg.x, g[1] += vg.y, g[2] += vg.z, g[3] += vg.w;
         u[0] += vu.x, u[1] += vu.y, u[2] += vu.z, u[3] += vu.w;
       }
@@ -606,7 +796,7 @@ __global__ void __launch_bounds__(threads_of(SLICES), 1)
         const float rest = v - __bfloat162float(hi[k]);
         lo[k] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);  // an infinity stays one
       }
-      __nv_bfloat16* o = a.act + (long long)row * 2 * a.F + f;
+      __nv_bfloat16* o = a.act + (long long)row * 2 * a.F + col;
       *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(hi);
       *reinterpret_cast<uint2*>(o + a.F) = *reinterpret_cast<uint2*>(lo);
     }
@@ -614,50 +804,51 @@ __global__ void __launch_bounds__(threads_of(SLICES), 1)
   }
   grid.sync();
   if (warp == kConsumers) {
-    if (lane == 0) produce_weights<FMT>(p2, ahead, p2.n, r, c, w2, expert, block);
-    __syncwarp();
-  } else if (warp == kConsumers + 1) {
     fence_async();
-    produce_rows<FMT, 2>(p2, r, c, x2, start, [&](int row) { return (long long)row; });
+    feed<FMT, false>(t2, behind, p2, r, c, w2, x2, expert, start, block, a.counters + 1, same);
   } else {
-    products<FMT, SLICES, NTMAX, 2>(p2, a.F, r, c, start, a.group, block, s_join,
-                                    [&](uint32_t e, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int n = j * kUnit + 64 * q + col;
-                                      if (n < a.H) a.part2[((long long)(start[e] + t) * p2.parts + part) * a.H + n] = v;
+    products<FMT, SLICES, NTMAX, 2>(p2, a.F, r, c, start, a.group, block, join, turn,
+                                    [&](int first, uint32_t j, uint32_t part, int q, int col, int t, float v) {
+                                      const int n = j * kUnit + q * (kUnit / 2) + col;
+                                      if (n < a.H) a.part2[((long long)(first + t) * p2.parts + part) * a.H + n] = v;
                                     });
   }
   grid.sync();
   if (go) {
     // eight lanes share four outputs, each a part of the token's experts
-    const uint32_t quads = a.H / 4, n = a.T * quads * 8, step = gridDim.x * blockDim.x;
-    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-      const uint32_t o = i / 8, t = o / quads, col = o % quads * 4;
-      float s[4] = {};
-      for (int k = i % 8; k < a.K; k += 8) {
-        const uint32_t row = row_of[t * a.K + k];
-        if (row == 0xffff) continue;
-        const uint32_t parts = parts_in(p2, row_entry[row] * p2.nb + col / kUnit);
+    constexpr uint32_t items = kUnit / 4 * 8;
+    const uint32_t n = a.T * p2.nb * items;
+#pragma unroll 1
+    for (Spread s = spread(); s.i < n; s.i += s.step) {
+      const uint32_t u = s.i / items, t = p2.by_nb(u), j = u - t * p2.nb, col = j * kUnit + s.i % items / 8 * 4;
+      if (int(col) >= a.H) continue;
+      float v[4] = {};
+#pragma unroll 1
+      for (int k = s.i % 8; k < a.K; k += 8) {
+        const uint32_t row = l.row[t * a.K + k];
+        if (row == kNone) continue;
+        const float w = l.weight[t * a.K + k];
+        const uint32_t parts = parts_in(p2, l.entry[row] * p2.nb + j);
         const float* in = a.part2 + (long long)row * p2.parts * a.H + col;
         float y[4] = {};
 #pragma unroll 4
-        for (uint32_t q = 0; q < parts; ++q) {
-          const float4 v = *reinterpret_cast<const float4*>(in + q * (long long)a.H);
-          y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+        for (uint32_t q = 0; q < parts; ++q, in += a.H) {
+          const float4 part = __ldcg(reinterpret_cast<const float4*>(in));
+          y[0] += part.x, y[1] += part.y, y[2] += part.z, y[3] += part.w;
         }
-        const float w = a.topk_w[t * a.K + k];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] = fmaf(w, y[q], s[q]);
+        for (int q = 0; q < 4; ++q) v[q] = fmaf(w, y[q], v[q]);
       }
       const unsigned lanes = 0xffu << (threadIdx.x & 24);
 #pragma unroll
       for (int d = 4; d > 0; d >>= 1)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] += __shfl_xor_sync(lanes, s[q], d);
-      if (i % 8 == 0) {
-        __nv_bfloat16 v[4];
+        for (int q = 0; q < 4; ++q) v[q] += __shfl_xor_sync(lanes, v[q], d);
+      if (s.i % 8 == 0) {
+        __nv_bfloat16 b[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = __float2bfloat16_rn(s[q]);
-        *reinterpret_cast<uint2*>(a.out + (long long)t * a.H + col) = *reinterpret_cast<uint2*>(v);
+        for (int q = 0; q < 4; ++q) b[q] = __float2bfloat16_rn(v[q]);
+        *reinterpret_cast<uint2*>(a.out + (long long)t * a.H + col) = *reinterpret_cast<uint2*>(b);
       }
     }
   }
@@ -670,6 +861,8 @@ struct ProductArgs {
   const uint8_t* w4;
   int32_t* status;
   int T, K, N, group;
+  Shape shape;
+  uint32_t* counter;
   __nv_bfloat16* padded;  // rows of x that are whole 16-byte vectors, where K is not a multiple of 8
   float* part;
   void* y;
@@ -679,66 +872,80 @@ template <int SLICES, int NTMAX, typename T>
 __global__ void __launch_bounds__(threads_of(SLICES), 1) k_w4_product(const ProductArgs a) {
   extern __shared__ __align__(1024) char smem[];
   const auto grid = cooperative_groups::this_grid();
-  constexpr int FMT = MEP_W4, BK = step_rows(FMT), kConsumers = kM * SLICES;
+  constexpr int FMT = MEP_W4, kConsumers = kM * SLICES;
   Head* h = reinterpret_cast<Head*>(smem);
   uint16_t* start = reinterpret_cast<uint16_t*>(h + 1);  // one entry, all rows
   uint16_t* expert = start + 2;
   static_assert(sizeof(Head) + 8 <= kHeadBytes, "head");
-  float4* s_join = reinterpret_cast<float4*>(smem + kHeadBytes);
-  char* at = smem + kHeadBytes + join_bytes(SLICES);
+  const uint32_t used = kHeadBytes + join_bytes(SLICES);
   Ring r;
-  init_ring(r, h, kConsumers, a.status);
-  if (threadIdx.x == 0) {
+  Join join;
+  init_ring(r, join, h, smem + kHeadBytes, kConsumers, a.status);
+  if (threadIdx.x == 32) {
     h->go = read_status(a.status) == 0;
     start[0] = 0, start[1] = a.T, expert[0] = 0;
+    if (blockIdx.x == 0) *a.counter = 0;
   }
   __syncthreads();
   const bool go = h->go;
   const int block = w4_block_bytes(a.group);
-  r.stage0 = smem_u32(at);
-  size_ring<FMT, 1>(r, kSmem - uint32_t(at - smem), a.T, block);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Phase p = make_phase(go ? 1 : 0, (a.N + kUnit - 1) / kUnit, (a.K + BK - 1) / BK);
+  r.stage0 = smem_u32(smem + used);
+  size_ring<FMT, 1>(r, kSmem - used, a.T, block);
+  const int warp = threadIdx.x >> 5;
+  const Phase p = make_phase(go ? 1 : 0, a.shape);
   const long long panel = w4_panel_bytes(a.K, a.group);
-  const Weights w = {nullptr, a.w4, 0, 2 * panel, panel, 0, 0, a.N, a.K};
+  const Weights w = {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K};
   const bool pad = a.K % 8 != 0;
   const int K8 = (a.K + 7) / 8 * 8;
   const Rows x = {reinterpret_cast<const char*>(pad ? a.padded : a.x), 2LL * K8, K8};
+  const auto same = [&](int row) { return (long long)row; };
   Cursor c;
-  const uint32_t ahead = min(p.n, uint32_t(r.stages));
+  const Cursor behind;
+  uint32_t turn = 0;
+  Stream<FMT, 1> t1;
+  if (warp == kConsumers) {
+    if (pad)
+      feed_ahead<FMT, false>(t1, p, r, c, w, x, expert, start, block, same);
+    else
+      feed_ahead<FMT, true>(t1, p, r, c, w, x, expert, start, block, same);
+  }
   if (pad) {
-    if (threadIdx.x == 32 * kConsumers) produce_weights<FMT>(p, 0, ahead, r, c, w, expert, block);
-    __syncwarp();
     for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < uint32_t(a.T * K8); i += gridDim.x * blockDim.x) {
       const uint32_t t = i / K8, k = i % K8;
       a.padded[i] = int(k) < a.K ? a.x[(long long)t * a.K + k] : __float2bfloat16_rn(0.f);
     }
     fence_async();
-    grid.sync();
-    fence_async();
   }
+  if (pad || p.runs > gridDim.x) grid.sync();
   if (warp == kConsumers) {
-    if (lane == 0) produce_weights<FMT>(p, pad ? ahead : 0, p.n, r, c, w, expert, block);
-    __syncwarp();
-  } else if (warp == kConsumers + 1) {
-    produce_rows<FMT, 1>(p, r, c, x, start, [&](int row) { return (long long)row; });
+    fence_async();
+    if (pad)
+      feed<FMT, false>(t1, behind, p, r, c, w, x, expert, start, block, a.counter, same);
+    else
+      feed<FMT, true>(t1, behind, p, r, c, w, x, expert, start, block, a.counter, same);
   } else {
-    products<FMT, SLICES, NTMAX, 1>(p, a.K, r, c, start, a.group, block, s_join,
-                                    [&](uint32_t, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int n = j * kUnit + 64 * q + col;
-                                      if (n < a.N) a.part[((long long)t * p.parts + part) * a.N + n] = v;
+    products<FMT, SLICES, NTMAX, 1>(p, a.K, r, c, start, a.group, block, join, turn,
+                                    [&](int, uint32_t j, uint32_t part, int q, int col, int t, float v) {
+                                      const int n = j * kUnit + q * (kUnit / 2) + col;
+                                      if (n >= a.N) return;
+                                      if (p.parts == 1)
+                                        static_cast<T*>(a.y)[(long long)t * a.N + n] = from_f32<T>(v);
+                                      else
+                                        a.part[((long long)t * p.parts + part) * a.N + n] = v;
                                     });
   }
-  grid.sync();
-  if (go) {
-    const uint32_t n = uint32_t(a.T) * a.N, step = gridDim.x * blockDim.x;
-    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
-      const uint32_t t = i / a.N, col = i % a.N, parts = parts_in(p, col / kUnit);
-      const float* in = a.part + (long long)t * p.parts * a.N + col;
-      float s = 0.f;
+  if (p.parts > 1) {
+    grid.sync();
+    if (go) {
+      const uint32_t n = uint32_t(a.T) * a.N;
+      for (Spread s = spread(); s.i < n; s.i += s.step) {
+        const uint32_t t = s.i / a.N, col = s.i - t * a.N, parts = parts_in(p, col / kUnit);
+        const float* in = a.part + (long long)t * p.parts * a.N + col;
+        float v = 0.f;
 #pragma unroll 4
-      for (uint32_t q = 0; q < parts; ++q) s += in[q * (long long)a.N];
-      static_cast<T*>(a.y)[i] = from_f32<T>(s);
+        for (uint32_t q = 0; q < parts; ++q, in += a.N) v += __ldcg(in);
+        static_cast<T*>(a.y)[s.i] = from_f32<T>(v);
+      }
     }
   }
   settle(r);
@@ -765,19 +972,27 @@ int launch_all(void (*kernel)(KArgs...), long long most, int threads, cudaStream
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Most bytes of partial sums [rows][parts][columns] with 1 to `experts` of them
-// in use: the fewer, the more CTAs share a unit, and the fewer rows there are.
-size_t part_bytes(int experts, int T, int A, long long nb, long long ks, long long columns) {
+// Most bytes of partial sums [rows][parts][columns] with any number of entries
+// up to `most`, and T rows an entry at most, A in all. One run a CTA: the more
+// entries the longer the runs and the fewer the parts, and beyond `full` entries
+// no more rows. Several runs a CTA: the least run's parts.
+size_t part_bytes(int most, int full, int T, int A, long long nb, long long ks, long long columns) {
   size_t top = 0;
-  for (int n = 1; n <= experts; ++n) {
-    const long long per = ceil_div(n * nb * ks, kMaxCtas), rows = (long long)T * n < A ? (long long)T * n : A;
-    const size_t bytes = size_t(rows) * parts_of(uint32_t(ks), uint32_t(per)) * columns * 4;
-    if (bytes > top) top = bytes;
+  for (int n = 1; n <= full && n <= most; ++n) {
+    const uint32_t per = uint32_t(ceil_div(n * nb * ks, kMaxCtas));
+    if (per > kOneRun) break;
+    const long long rows = (long long)T * n < A ? (long long)T * n : A;
+    const size_t values = size_t(rows) * parts_of(uint32_t(ks), per) * columns;
+    if (values > top) top = values;
   }
-  return align256(top);
+  if (ceil_div(most * nb * ks, kMaxCtas) > kOneRun) {
+    const size_t values = size_t(A) * parts_of(uint32_t(ks), least_run(uint32_t(ks))) * columns;
+    if (values > top) top = values;
+  }
+  return align256(4 * top);
 }
 
-// 3D bf16 map over [E, K, N], box {64 columns, 128 rows, 1}, 128-byte swizzle; beyond a matrix's edges zeros.
+// 3D bf16 map over [E, K, N], box {64 columns, a step's rows, 1}, 128-byte swizzle; beyond a matrix's edges zeros.
 bool make_map3(CUtensorMap* m, const void* p, long long E, long long K, long long N) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
@@ -790,45 +1005,46 @@ bool make_map3(CUtensorMap* m, const void* p, long long E, long long K, long lon
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The layer's workspace: partial sums of the first product, the activation, partial sums of the second.
+constexpr size_t kCounters = 256;  // bytes at the start
+
+// The layer's workspace: counters, partial sums of the first product, the activation, partial sums of the second.
 struct LayerSpace {
   size_t part1, act, part2;
-  size_t all() const { return part1 + act + part2; }
+  size_t all() const { return kCounters + part1 + act + part2; }
 };
 bool layer_space(int T, int K, int E, long long H, long long F, int w_type, int group, LayerSpace* s) {
   if (T < 0 || T > MEP_MAX_FEW || K < 1 || K > MEP_MAX_K || E < 1 || E > MEP_MAX_E || H < 8 || F < 8 || H % 8 != 0 ||
       F % 8 != 0 || H > MEP_MAX_FEW_H || F > MEP_MAX_FEW_H / 2)
     return false;
   if (w_type != MEP_BF16 && (w_type != MEP_W4 || !w4_sizes_ok(H, F, group))) return false;
-  // beyond K experts there are no more rows, only fewer parts
-  const int A = T * K, experts = E < K ? E : K, bk = step_rows(w_type);
-  s->part1 = part_bytes(T > 0 ? experts : 0, T, A, ceil_div(F, 64), ceil_div(H, bk), 2 * F);
-  s->part2 = part_bytes(T > 0 ? experts : 0, T, A, ceil_div(H, kUnit), ceil_div(F, bk), H);
+  const int A = T * K, most = max_entries(T, K, E), bk = step_rows(w_type);
+  s->part1 = part_bytes(most, K, T, A, ceil_div(F, kUnit / 2), ceil_div(H, bk), 2 * F);
+  s->part2 = part_bytes(most, K, T, A, ceil_div(H, kUnit), ceil_div(F, bk), H);
   s->act = align256(size_t(A) * F * 4);
   return true;
 }
 
 struct ProductSpace {
   size_t padded, part;
-  size_t all() const { return padded + part; }
+  size_t all() const { return kCounters + padded + part; }
 };
 bool product_space(int T, long long K, long long N, int group, ProductSpace* s) {
   if (T < 0 || T > MEP_MAX_FEW || !w4_sizes_ok(K, N, group)) return false;
   s->padded = K % 8 == 0 ? 0 : align256(size_t(T) * ceil_div(K, 8) * 16);
-  s->part = part_bytes(1, T, T, ceil_div(N, kUnit), ceil_div(K, step_rows(MEP_W4)), N);
+  s->part = T == 0 ? 0 : part_bytes(1, 1, T, T, ceil_div(N, kUnit), ceil_div(K, step_rows(MEP_W4)), N);
   return true;
 }
 
 template <int FMT, int SLICES>
 int launch_layer(const CUtensorMap& m1, const CUtensorMap& m2, const LayerArgs& a, cudaStream_t st) {
   const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(FMT);
-  const long long n1 = experts * ceil_div(a.F, 64) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
+  const long long n1 = experts * ceil_div(a.F, kUnit / 2) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
   return launch_all(k_layer<FMT, SLICES>, n1 > n2 ? n1 : n2, threads_of(SLICES), st, m1, m2, a);
 }
 template <typename T> int launch_product(const ProductArgs& a, cudaStream_t st) {
   const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(MEP_W4));
-  return a.T <= 32 ? launch_all(k_w4_product<4, 4, T>, n, threads_of(4), st, a)
-                   : launch_all(k_w4_product<2, 8, T>, n, threads_of(2), st, a);
+  return a.T <= 32 ? launch_all(k_w4_product<2, 4, T>, n, threads_of(2), st, a)
+                   : launch_all(k_w4_product<1, 8, T>, n, threads_of(1), st, a);
 }
 
 }  // namespace
@@ -852,8 +1068,9 @@ extern "C" int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* sta
   if (!aligned16(w4) || !aligned16(ws) || reinterpret_cast<uintptr_t>(x) % (K % 8 == 0 ? 16 : 2) != 0 ||
       reinterpret_cast<uintptr_t>(y) % (y_type == MEP_BF16 ? 2 : 4) != 0)
     return MEP_ERR_INVALID_ARG;
-  char* p = static_cast<char*>(ws);
+  char* p = static_cast<char*>(ws) + kCounters;
   const ProductArgs a = {reinterpret_cast<const __nv_bfloat16*>(x), w4, status, T, int(K), int(N), group,
+                         shape_of(ceil_div(K, step_rows(MEP_W4)), ceil_div(N, kUnit)), static_cast<uint32_t*>(ws),
                          reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<float*>(p + s.padded), y};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return y_type == MEP_BF16 ? launch_product<__nv_bfloat16>(a, st) : launch_product<float>(a, st);
@@ -879,7 +1096,8 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
   if (!aligned16(x) || !aligned16(w1) || !aligned16(w2) || !aligned16(ws) || !aligned16(out) ||
       reinterpret_cast<uintptr_t>(topk_idx) % 4 != 0 || reinterpret_cast<uintptr_t>(topk_w) % 4 != 0)
     return MEP_ERR_INVALID_ARG;
-  char* p = static_cast<char*>(ws);
+  char* p = static_cast<char*>(ws) + kCounters;
+  const int bk = step_rows(w_type);
   const LayerArgs a = {reinterpret_cast<const __nv_bfloat16*>(x),
                        topk_idx,
                        topk_w,
@@ -892,14 +1110,18 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
                        int(H),
                        int(F),
                        group,
+                       shape_of(ceil_div(H, bk), ceil_div(F, kUnit / 2)),
+                       shape_of(ceil_div(F, bk), ceil_div(H, kUnit)),
+                       div_of(K),
+                       static_cast<uint32_t*>(ws),
                        reinterpret_cast<float*>(p),
                        reinterpret_cast<float*>(p + s.part1 + s.act),
                        reinterpret_cast<__nv_bfloat16*>(p + s.part1),
                        reinterpret_cast<__nv_bfloat16*>(out)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap m1 = {}, m2 = {};
-  if (w_type == MEP_W4) return launch_layer<MEP_W4, 4>(m1, m2, a, st);
+  if (w_type == MEP_W4) return launch_layer<MEP_W4, 2>(m1, m2, a, st);
   if (!on_current_device(w1) || !on_current_device(w2)) return MEP_ERR_INVALID_ARG;
   if (!make_map3(&m1, w1, E, H, 2 * F) || !make_map3(&m2, w2, E, F, H)) return MEP_ERR_CUDA;
-  return launch_layer<MEP_BF16, 4>(m1, m2, a, st);
+  return launch_layer<MEP_BF16, 2>(m1, m2, a, st);
 }

@@ -62,7 +62,8 @@ def agrees(layer, x, idx, w, **kw):
 
 SIZES = [(1, 1, 1, 8, 8), (1, 2, 3, 16, 8), (4, 2, 8, 128, 64), (1, 6, 64, 2048, 1408), (8, 6, 64, 2048, 1408), (64, 8, 16, 264, 72),
          (64, 1, 1, 136, 200), (17, 64, 64, 72, 40), (5, 4, 4096, 64, 32), (64, 8, 256, 512, 128), (2, 2, 4, 7168, 1408), (33, 3, 5, 104, 88),
-         (16, 2, 2, 640, 328), (64, 4, 4, 1000, 1000), (3, 3, 7, 4104, 8), (3, 3, 7, 8, 4104), (63, 5, 9, 200, 120), (48, 1, 2, 256, 256)]
+         (16, 2, 2, 640, 328), (64, 4, 4, 1000, 1000), (3, 3, 7, 4104, 8), (3, 3, 7, 8, 4104), (63, 5, 9, 200, 120), (48, 1, 2, 256, 256),
+         (64, 8, 256, 2048, 512), (16, 8, 128, 2048, 520)]
 
 
 @pytest.mark.parametrize("group", [0, 128, 64, 32])
@@ -159,6 +160,24 @@ def test_any_workspace_and_repeated_bits(group):
         out = torch.full((n + 1, 512), 7.0, dtype=torch.bfloat16, device="cuda")
         got = layer(x[:n], idx[:n].contiguous(), w[:n].contiguous(), workspace=ws, out=out[:n])
         assert torch.equal(got, layer(x[:n], idx[:n].contiguous(), w[:n].contiguous())) and (out[n] == 7).all()
+
+
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("T,K,E,H,F,same", [(1, 1, 1, 4096, 8, 1), (64, 1, 1, 2048, 64, 1), (64, 8, 8, 2048, 512, 1), (16, 8, 128, 2048, 512, 0),
+                                            (64, 8, 256, 2048, 512, 0), (64, 8, 256, 2048, 512, 1), (3, 8, 256, 1024, 512, 0),
+                                            (64, 2, 64, 8, 4096, 0), (40, 4, 16, 1000, 328, 0), (64, 64, 64, 264, 72, 0)])
+def test_nothing_is_written_behind_the_workspace(T, K, E, H, F, same, group):
+    """As many experts as can be in use and as few; one byte less is refused."""
+    layer = Layer(E, H, F, 26, group)
+    x, idx, w = tokens(T, K, E, H, 27, skew=0.0)
+    if same:
+        idx[:] = idx[0].clone()
+    need = mep.expert_layer_workspace_bytes(T, K, E, H, F, bool(group), group or 128)
+    ws = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    agrees(layer, x, idx, w, workspace=ws[:need])
+    assert (ws[need:] == 0xA5).all()
+    with pytest.raises(ValueError):
+        layer(x, idx, w, workspace=ws[:need - 1])
 
 
 def test_against_the_planned_path():

@@ -132,6 +132,18 @@ def test_product_repeats_its_bits_and_takes_any_workspace():
         assert torch.equal(got, mep.mep_w4_product(x[:t], w4, N))
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 7168, 256), (64, 7168, 200), (64, 2048, 40000), (5, 1001, 1407), (33, 257, 70000), (64, 40000, 8)])
+def test_product_writes_nothing_behind_its_workspace(T, K, N):
+    x = torch.randn(T, K, device="cuda").to(torch.bfloat16)
+    w4 = mep.mep_w4_save(torch.randn(K, N, device="cuda"))
+    need = mep.w4_product_workspace_bytes(T, K, N)
+    ws = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = mep.mep_w4_product(x, w4, N, workspace=ws[:need], dtype=torch.float32)
+    assert (ws[need:] == 0xA5).all()
+    want, mag = ref.product(x, mep.mep_w4_load(w4, K, N, dtype=torch.float32))
+    assert ((got.double() - want).abs() <= ref.product_bound(want, mag, K, 2.0 ** -24)).all()
+
+
 def test_product_special_values():
     """A NaN or an infinity in one row or one column's group stays there; so does a group of zeros."""
     T, K, N = 11, 300, 100
