@@ -815,14 +815,15 @@ __global__ void __launch_bounds__(threads_of(SLICES), 1)
   }
   grid.sync();
   if (go) {
-    // eight lanes share four outputs, each a part of the token's experts
-    constexpr uint32_t items = kUnit / 4 * 8;
+    // eight lanes share 16 outputs, each a part of the token's experts
+    constexpr uint32_t groups = kUnit / 16, items = groups * 8;
     const uint32_t n = a.T * p2.nb * items;
 #pragma unroll 1
     for (Spread s = spread(); s.i < n; s.i += s.step) {
-      const uint32_t u = s.i / items, t = p2.by_nb(u), j = u - t * p2.nb, col = j * kUnit + s.i % items / 8 * 4;
+      const uint32_t u = s.i / items, t = p2.by_nb(u), j = u - t * p2.nb, col = j * kUnit + s.i % items / 8 * 16;
       if (int(col) >= a.H) continue;
-      float v[4] = {};
+      const bool full = int(col) + 16 <= a.H;  // else eight columns
+      float v[16] = {};
 #pragma unroll 1
       for (int k = s.i % 8; k < a.K; k += 8) {
         const uint32_t row = l.row[t * a.K + k];
@@ -830,26 +831,33 @@ __global__ void __launch_bounds__(threads_of(SLICES), 1)
         const float w = l.weight[t * a.K + k];
         const uint32_t parts = parts_in(p2, l.entry[row] * p2.nb + j);
         const float* in = a.part2 + (long long)row * p2.parts * a.H + col;
-        float y[4] = {};
-#pragma unroll 4
+        float y[16] = {};
+#pragma unroll 2
         for (uint32_t q = 0; q < parts; ++q, in += a.H) {
-          const float4 part = __ldcg(reinterpret_cast<const float4*>(in));
-          y[0] += part.x, y[1] += part.y, y[2] += part.z, y[3] += part.w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= 2 && !full) break;
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(in) + i);
+            y[4 * i] += f.x, y[4 * i + 1] += f.y, y[4 * i + 2] += f.z, y[4 * i + 3] += f.w;
+          }
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = fmaf(w, y[q], v[q]);
+        for (int i = 0; i < 16; ++i) v[i] = fmaf(w, y[i], v[i]);
       }
+      // halves of the lanes' sums change hands: eight lanes end with two outputs each
       const unsigned lanes = 0xffu << (threadIdx.x & 24);
+      const int lane = threadIdx.x & 7;
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1)
+      for (int d = 4, left = 8; d > 0; d >>= 1, left >>= 1)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] += __shfl_xor_sync(lanes, v[q], d);
-      if (s.i % 8 == 0) {
-        __nv_bfloat16 b[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) b[q] = __float2bfloat16_rn(v[q]);
-        *reinterpret_cast<uint2*>(a.out + (long long)t * a.H + col) = *reinterpret_cast<uint2*>(b);
-      }
+        for (int i = 0; i < left; ++i) {
+          const bool up = lane & d;
+          const float mine = up ? v[left + i] : v[i], other = up ? v[i] : v[left + i];
+          v[i] = mine + __shfl_xor_sync(lanes, other, d);
+        }
+      const int at = (lane & 4 ? 8 : 0) + (lane & 2 ? 4 : 0) + (lane & 1 ? 2 : 0);
+      if (full || at < 8)
+        *reinterpret_cast<__nv_bfloat162*>(a.out + (long long)t * a.H + col + at) = __floats2bfloat162_rn(v[0], v[1]);
     }
   }
   settle(r);
