@@ -42,17 +42,17 @@ namespace mep {
 namespace {
 
 constexpr int kMaxCtas = 152;       // SMs of a GB300; more are not used, the workspace counts on it
-constexpr int kM = 8;               // warps across a unit's columns: 16 of its first half and 16 of its second
+constexpr int kWarps = 8;           // across a unit's columns: 16 of its first half and 16 of its second
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr int kUnit = 256;          // columns of a unit
 constexpr int kPanels = kUnit / kW4Cols;
 constexpr int kPanelRow = 128;      // bytes of a stage's row of 64 bf16 columns
 constexpr int kMaxStages = 16;
-constexpr int kSmem = 225 * 1024;
+constexpr int kSmem = 227 * 1024;
 constexpr int kChunk = 32;          // tokens of an expert that one unit takes in the layer
 constexpr uint32_t kEnd = 0xffffffffu;
 
 __host__ __device__ constexpr int step_rows(int fmt) { return fmt == MEP_BF16 ? 64 : 256; }
-__host__ __device__ constexpr int threads_of(int slices) { return 32 * (kM * slices + 1); }
 
 // ---------------------------------------------------------------------------
 // n / d by a product, n < 2^31: with 2^l >= d, m = floor(2^(31+l) / d) + 1 the
@@ -127,7 +127,7 @@ __device__ __forceinline__ uint32_t parts_in(const Phase& p, uint32_t unit) {
 struct Ring {
   uint32_t full, empty;         // barriers, 8 bytes each
   uint32_t stage0, stage_bytes; // first stage
-  uint32_t x_at, plane;         // of a stage: where the rows of x start; bytes of a plane of them
+  uint32_t x_at;                // of a stage: where the rows of x start
   int stages;
   volatile uint32_t* step;      // of a stage: which step it holds, or kEnd
   volatile int* abort;
@@ -154,25 +154,45 @@ struct Weights {
 // Rows of x: `planes` of them after one another (the activation's two).
 struct Rows {
   const char* p;
-  long long pitch;  // bytes
-  int K;            // bf16 of a row
+  const uint16_t* token;  // row of x of a row of the list; NULL: the same
+  long long pitch;        // bytes
+  int K;                  // bf16 of a row
+  int planes;
+};
+// Where a product's partial sums go: rows' parts of `pitch` floats.
+struct Sums {
+  float* p;
+  uint32_t pitch;
+  int unit, half;      // columns from unit to unit, from a unit's first half to its second
+  int limit, counted;  // j * unit + column + (half & counted) is below limit where a column is there
 };
 
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+// `live`: not executed where it is false, though fetched.
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, bool live) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "@p cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(int(live))
       : "memory");
 }
-__device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-               : "memory");
+__device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, bool live) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar), "r"(int(live))
+      : "memory");
+}
+__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes, bool live) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(int(live))
+      : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+__device__ __noinline__ void grid_barrier() { cooperative_groups::this_grid().sync(); }
 // A whole warp waits; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Ring& r) {
   if (__all_sync(MEP_FULL_MASK, mbar_try_wait_long(bar, parity))) return true;
@@ -184,153 +204,147 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const R
 // and its rows have: two arrivals. What a step needs is worked out where its
 // unit begins; a step itself has to cost less than its bytes take to come (a
 // stage of 32 KB in 0.75 us).
-template <int FMT, int PLANES> struct Stream {
+template <int FMT> struct Stream {
   static constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
-  uint32_t step, end;      // of the run
-  uint32_t s, j, entry;    // step of the unit, unit of the expert, the expert's entry
-  uint32_t tx;             // bytes of a full step's weights
-  int e, m, panels;        // panels: a bit for each that is there
-  const uint8_t* w;        // 4 bits: the unit's first panel
-  const char* row[2];      // this lane's rows of x
-  uint32_t at[2];          // and where they go in a stage
+  const Ring& r;
+  const uint16_t *expert, *start;
+  const int block;
+  Phase p;
+  Weights w;
+  Rows x;
+  uint32_t step = 0, end = 0;  // of the run
+  uint32_t s, j, entry;        // step of the unit, unit of the expert, the expert's entry
+  uint32_t tx;                 // bytes of a full step's weights
+  int e, m, panels;            // panels: a bit for each that is there
+  const uint8_t* unit_w;       // 4 bits: the unit's first panel
+  const char* row[2];          // this lane's rows of x
+  uint32_t at[2];              // and where they go in a stage
 
-  __device__ __forceinline__ void init(const Ring& r) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int q = lane + 32 * i;
-      at[i] = r.x_at + (q % PLANES) * r.plane + (q / PLANES) * pitch;
-    }
-  }
-  template <typename RowOf>
-  __device__ __forceinline__ void unit(const Weights& w_, const Rows& x, const uint16_t* expert, const uint16_t* start,
-                                       int block, RowOf row_of) {
-    const int lane = threadIdx.x & 31, first = start[entry], panel = j * w_.unit;
-    m = start[entry + 1] - first, e = expert[entry];
-    const int count = (w_.columns + kW4Cols - 1) / kW4Cols - panel;
-    panels = w_.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
+  __device__ __forceinline__ Stream(const Ring& ring, const uint16_t* e_, const uint16_t* s_, int b)
+      : r(ring), expert(e_), start(s_), block(b) {}
+  __device__ __forceinline__ void unit(bool live) {
+    const int lane = threadIdx.x & 31, first = live ? start[entry] : 0, panel = j * w.unit, pl = x.planes - 1;
+    m = live ? start[entry + 1] - first : 0, e = live ? expert[entry] : 0;
+    const int count = (w.columns + kW4Cols - 1) / kW4Cols - panel;
+    panels = w.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
     tx = __popc(panels) * (FMT == MEP_BF16 ? step_rows(FMT) * kPanelRow : 2 * block);
-    if (FMT == MEP_W4) w = w_.w4 + e * w_.expert + panel * w_.panel;
+    if (FMT == MEP_W4) unit_w = w.w4 + e * w.expert + panel * w.panel;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int q = lane + 32 * i;
-      if (q < PLANES * m) row[i] = x.p + (row_of(first + q / PLANES) * PLANES + q % PLANES) * x.pitch;
+      at[i] = r.x_at + q * pitch;
+      if (q < m << pl) {
+        const int of = first + (q >> pl);
+        row[i] = x.p + (((x.token == nullptr ? of : x.token[of]) << pl) + (q & pl)) * x.pitch;
+      }
     }
   }
-  template <typename RowOf>
-  __device__ __forceinline__ void seek(uint32_t to, const Phase& p, const Weights& w_, const Rows& x,
-                                       const uint16_t* expert, const uint16_t* start, int block, RowOf row_of) {
+  __device__ __forceinline__ void seek(uint32_t to, bool live = true) {
     step = to, end = min(p.total, to + p.run);
-    if (step >= end) return;
+    if (step >= end && live) return;
     const uint32_t u = p.by_ks(step);
     s = step - u * p.ks, entry = p.by_nb(u), j = u - entry * p.nb;
-    unit(w_, x, expert, start, block, row_of);
+    unit(live);
   }
-  template <typename RowOf>
-  __device__ __forceinline__ void next(const Phase& p, const Weights& w_, const Rows& x, const uint16_t* expert,
-                                       const uint16_t* start, int block, RowOf row_of) {
+  __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_, bool live = true) {
+    p = p_, w = w_, x = x_;
+    seek(min(p.total, blockIdx.x * p.run), live);
+  }
+  __device__ __forceinline__ void next() {
     if (++step == end || ++s < p.ks) return;
     s = 0;
     if (++j == p.nb) j = 0, ++entry;
-    unit(w_, x, expert, start, block, row_of);
+    unit(true);
   }
-  __device__ __forceinline__ void weights(const Ring& r, int slot, const Weights& w_, int block) const {  // one lane
+  __device__ __forceinline__ void weights(int slot, bool live = true) const {  // one lane
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
-    r.step[slot] = step;
+    if (live) r.step[slot] = step;
     if (FMT == MEP_BF16) {
       constexpr uint32_t bytes = step_rows(FMT) * kPanelRow;
-      const int col = j * w_.unit * kW4Cols, k = s * BK;
-      mbar_expect_tx(bar, tx);
+      const int col = j * w.unit * kW4Cols, k = s * BK;
+      expect(bar, tx, live);
 #pragma unroll
       for (int q = 0; q < kPanels; ++q)
-        if (panels >> q & 1) tma_3d(dst + q * bytes, w_.map, col + (q & 1) * kW4Cols + (q >> 1) * w_.col_second, k, e, bar);
+        tma_3d(dst + q * bytes, w.map, col + (q & 1) * kW4Cols + (q >> 1) * w.col_second, k, e, bar, live && panels >> q & 1);
     } else {
-      const uint8_t* src = w + s * (2 * block);
-      const uint32_t half = 2 * int(s) + 1 == (w_.K + kW4Rows - 1) / kW4Rows;  // the last step may have one block
-      mbar_expect_tx(bar, tx >> half);
+      const uint8_t* src = unit_w + s * (2 * block);
+      const uint32_t half = 2 * int(s) + 1 == (w.K + kW4Rows - 1) / kW4Rows;  // the last step may have one block
+      expect(bar, tx >> half, live);
 #pragma unroll
       for (int q = 0; q < kPanels; ++q)
-        if (panels >> q & 1)
-          bulk(dst + q * 2 * block, src + (q & 1) * w_.panel + (q >> 1) * w_.second, (2 * block) >> half, bar);
+        bulk(dst + q * 2 * block, src + (q & 1) * w.panel + (q >> 1) * w.second, (2 * block) >> half, bar,
+             live && panels >> q & 1);
     }
   }
-  __device__ __forceinline__ void rows(const Ring& r, int slot, const Rows& x) const {  // the warp
-    const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
+  __device__ __forceinline__ void rows(int slot, bool live = true) const {  // the warp
+    const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0), n = m << (x.planes - 1);
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
     if (bytes < 2 * BK) {  // beyond the sum's end the weights are zeros: what they meet must be numbers
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < PLANES * m)
+        if (lane + 32 * i < n)
           for (int b = bytes; b < 2 * BK; b += 16)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at[i] + b), "r"(0) : "memory");
       fence_async();
       __syncwarp();
     }
-    if (lane == 0) mbar_expect_tx(bar, PLANES * m * bytes);
+    if (lane == 0) expect(bar, n * bytes, live);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 32 * i < PLANES * m) bulk(dst + at[i], row[i] + 2 * k0, bytes, bar);
+    for (int i = 0; i < 2; ++i) bulk(dst + at[i], row[i] + 2 * k0, bytes, bar, lane + 32 * i < n);
   }
-};
-
-// Before a barrier of the grid: the weights of as many steps of the CTA's own
-// run as the ring has room for, and their rows where these are there already.
-template <int FMT, bool ROWS, int PLANES, typename RowOf>
-__device__ __forceinline__ void feed_ahead(Stream<FMT, PLANES>& t, const Phase& p, const Ring& r, Cursor& c,
-                                           const Weights& w, const Rows& x, const uint16_t* expert,
-                                           const uint16_t* start, int block, RowOf row_of) {
-  t.init(r);
-  t.seek(min(p.total, blockIdx.x * p.run), p, w, x, expert, start, block, row_of);
-  for (int i = 0; i < r.stages && t.step < t.end; ++i) {
-    if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) break;
-    if ((threadIdx.x & 31) == 0) t.weights(r, c.slot, w, block);
-    if (ROWS) t.rows(r, c.slot, x);
-    c.next(r.stages);
-    t.next(p, w, x, expert, start, block, row_of);
-  }
-}
-// After it: the rest of the own run, further runs off the counter, the end's
-// mark. `behind`: the first stage fed ahead, whose rows are due.
-template <int FMT, bool ROWS, int PLANES, typename RowOf>
-__device__ __forceinline__ void feed(Stream<FMT, PLANES>& t, Cursor behind, const Phase& p, const Ring& r, Cursor& c,
-                                     const Weights& w, const Rows& x, const uint16_t* expert, const uint16_t* start,
-                                     int block, uint32_t* counter, RowOf row_of) {
-  const int lane = threadIdx.x & 31;
-  const bool more = p.runs > gridDim.x;
-  uint32_t next = 0;
-  if (more && lane == 0) next = atomicAdd(counter, 1u);  // on its way while the run is fed
-  if (!ROWS) {
-    const uint32_t to = t.step, end = t.end;
-    t.seek(min(p.total, blockIdx.x * p.run), p, w, x, expert, start, block, row_of);
-    while (t.step < to) {
-      t.rows(r, behind.slot, x);
-      behind.next(r.stages);
-      t.next(p, w, x, expert, start, block, row_of);
+  // Before a barrier of the grid: the weights of as many steps of the CTA's own
+  // run as the ring has room for, and their rows where these are there already.
+  __device__ __forceinline__ void ahead(Cursor& c, bool with_rows) {
+#pragma unroll 1
+    for (int i = 0; i < r.stages && step < end; ++i) {
+      if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) break;
+      if ((threadIdx.x & 31) == 0) weights(c.slot);
+      if (with_rows) rows(c.slot);
+      c.next(r.stages);
+      next();
     }
-    t.end = end;
   }
-  while (true) {
-    if (t.step == t.end) {
-      const uint32_t run = more ? gridDim.x + __shfl_sync(MEP_FULL_MASK, next, 0) : p.runs;
-      if (run >= p.runs) break;
-      t.seek(run * p.run, p, w, x, expert, start, block, row_of);
-      if (lane == 0) next = atomicAdd(counter, 1u);
+  // After it: the rows that are due, of the stages from `behind` on; the rest of
+  // the own run, further runs off the counter, the end's mark.
+  __device__ __forceinline__ void feed(Cursor& c, Cursor behind, bool due, uint32_t* counter) {
+    const int lane = threadIdx.x & 31;
+    const bool more = p.runs > gridDim.x;
+    uint32_t taken = 0;
+    if (more && lane == 0) taken = atomicAdd(counter, 1u);  // on its way while the run is fed
+    if (due) {
+      const uint32_t to = step, stop = end;
+      seek(min(p.total, blockIdx.x * p.run));
+      while (step < to) {
+        rows(behind.slot);
+        behind.next(r.stages);
+        next();
+      }
+      end = stop;
+    }
+#pragma unroll 1
+    while (true) {
+      if (step == end) {
+        const uint32_t run = more ? gridDim.x + __shfl_sync(MEP_FULL_MASK, taken, 0) : p.runs;
+        if (run >= p.runs) break;
+        seek(run * p.run);
+        if (lane == 0) taken = atomicAdd(counter, 1u);
+      }
+      if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
+      if (lane == 0) weights(c.slot);
+      rows(c.slot);
+      c.next(r.stages);
+      next();
     }
     if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
-    if (lane == 0) t.weights(r, c.slot, w, block);
-    t.rows(r, c.slot, x);
+    if (lane == 0) {
+      r.step[c.slot] = kEnd;
+      arrive(r.full + 8 * c.slot);
+      arrive(r.full + 8 * c.slot);
+    }
     c.next(r.stages);
-    t.next(p, w, x, expert, start, block, row_of);
+    __syncwarp();
   }
-  if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
-  if (lane == 0) {
-    r.step[c.slot] = kEnd;
-    arrive(r.full + 8 * c.slot);
-    arrive(r.full + 8 * c.slot);
-  }
-  c.next(r.stages);
-  __syncwarp();
-}
+};
 
 // ---------------------------------------------------------------------------
 // Products.
@@ -374,87 +388,97 @@ __device__ __forceinline__ void widen_q(uint32_t word, uint32_t (&a)[4]) {
 }
 constexpr float kQ = 64.f;
 
-// This warp's share of a stage: 16 columns of either half, slice `sl` of the rows.
-template <int FMT, int SLICES, int NT, int PLANES>
-__device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t stage, const Ring& r, int mi, int sl,
+// This warp's share of a stage: 16 columns of either half.
+template <int FMT, int NT>
+__device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t stage, const Ring& r, int warp,
                                               int blocks, int group, int block) {
   constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
   const int lane = threadIdx.x & 31;
   const uint32_t xb = stage + r.x_at + (lane & 7) * pitch + 16 * (lane >> 3);
   if (FMT == MEP_BF16) {
-    const uint32_t wa = stage + (mi >> 2) * (BK * kPanelRow) + ((lane >> 4) * 8 + (lane & 7)) * kPanelRow +
-                        (((2 * (mi & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
+    const uint32_t wa = stage + (warp >> 2) * (BK * kPanelRow) + ((lane >> 4) * 8 + (lane & 7)) * kPanelRow +
+                        (((2 * (warp & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
 #pragma unroll
-    for (int i = 0; i < BK / SLICES; i += 32) {
-      const int k = sl * (BK / SLICES) + i;
+    for (int k = 0; k < BK; k += 32) {
       uint32_t a[2][2][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int s = 0; s < 2; ++s) ldmatrix4_trans(a[q][s], wa + q * (2 * BK * kPanelRow) + (k + 16 * s) * kPanelRow);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        uint32_t b[4];
+        ldmatrix4(b, xb + n * (8 * pitch) + 2 * k);
 #pragma unroll
-        for (int pl = 0; pl < PLANES; ++pl) {
-          uint32_t b[4];
-          ldmatrix4(b, xb + pl * r.plane + n * (8 * pitch) + 2 * k);
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            mma(acc[q][n], a[q][0], b[0], b[1]);
-            mma(acc[q][n], a[q][1], b[2], b[3]);
-          }
-        }
+          for (int q = 0; q < 2; ++q) mma(acc[q][n], a[q][s], b[2 * s], b[2 * s + 1]);
+      }
     }
   } else {
+    // With few columns everything that a block of 128 rows needs of the stage is
+    // asked for at once; with more than 32 the block is gone through again.
+    constexpr bool early = NT <= 2;
+    constexpr int NS = NT < 4 ? NT : 4;
 #pragma unroll
-    for (int i = 0; i < 2 / SLICES; ++i) {
-      const int b = SLICES == 1 ? i : sl;  // block of 128 rows
-      if (b >= blocks) break;
-      const uint32_t wb = stage + (mi >> 2) * 2 * block + b * block;
-      const uint32_t at = wb + ((mi & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((mi & 3) * 8 + (lane >> 2)) * 4;
-      float sum[2][NT][4];
+    for (int i = 0; i < 2 * (NT / NS); ++i) {
+      const int b = i & 1, n0 = (i >> 1) * NS;
+      if (b >= blocks) continue;
+      const uint32_t wb = stage + (warp >> 2) * 2 * block + b * block;
+      const uint32_t at = wb + ((warp & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((warp & 3) * 8 + (lane >> 2)) * 4;
+      const uint32_t xa = xb + n0 * (8 * pitch) + 256 * b;
+      uint4 w[2][2];
+      uint32_t x[4][early ? NS : 1][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[h][0] = lds128(at + 2048 * h), w[h][1] = lds128(at + 2048 * h + 4 * block);
+      if (early) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int n = 0; n < NS; ++n) ldmatrix4(x[k][n], xa + n * (8 * pitch) + 64 * k);
+      }
+      float sum[2][NS][4];
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
+        for (int n = 0; n < NS; ++n) sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint4 w0 = lds128(at + h * 2048), w1 = lds128(at + h * 2048 + 4 * block);
+      for (int k = 0; k < 4; ++k) {  // 32 rows
+        const bool ends = k == 3 || (k == 1 && group <= 64) || group == 32;  // a group
+        uint32_t scale[2];
+        if (ends) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int k = 128 * b + 64 * h + 32 * half;
-          uint32_t a[2][2][4];
-          widen_q(half ? w0.z : w0.x, a[0][0]);
-          widen_q(half ? w0.w : w0.y, a[0][1]);
-          widen_q(half ? w1.z : w1.x, a[1][0]);
-          widen_q(half ? w1.w : w1.y, a[1][1]);
+          for (int q = 0; q < 2; ++q) scale[q] = lds32(sb + (32 * k + 31) / group * 128 + q * 4 * block);
+        }
+        uint32_t a[2][2][4];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int pl = 0; pl < PLANES; ++pl) {
-              uint32_t bx[4];
-              ldmatrix4(bx, xb + pl * r.plane + n * (8 * pitch) + 2 * k);
+          for (int q = 0; q < 2; ++q) {
+            const uint4& v = w[k >> 1][q];
+            widen_q(k & 1 ? (s ? v.w : v.z) : (s ? v.y : v.x), a[q][s]);
+          }
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                mma(sum[q][n], a[q][0], bx[0], bx[1]);
-                mma(sum[q][n], a[q][1], bx[2], bx[3]);
-              }
-            }
-          const int end = 64 * h + 32 * half + 32;
-          if (end == 128 || (end == 64 && group <= 64) || group == 32) {  // a group ends here
-            const uint32_t row = (end - 1) / group * 128;
+        for (int n = 0; n < NS; ++n) {
+          if (!early) ldmatrix4(x[0][0], xa + n * (8 * pitch) + 64 * k);
+          const uint32_t(&f)[4] = early ? x[k][n] : x[0][0];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t sc = lds32(sb + row + q * 4 * block);
-              const float lo = __uint_as_float(sc << 16), hi = __uint_as_float(sc & 0xffff0000u);
+          for (int s = 0; s < 2; ++s)
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                acc[q][n][0] = fmaf(lo, sum[q][n][0], acc[q][n][0]);
-                acc[q][n][1] = fmaf(lo, sum[q][n][1], acc[q][n][1]);
-                acc[q][n][2] = fmaf(hi, sum[q][n][2], acc[q][n][2]);
-                acc[q][n][3] = fmaf(hi, sum[q][n][3], acc[q][n][3]);
-                sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
-              }
+            for (int q = 0; q < 2; ++q) mma(sum[q][n], a[q][s], f[2 * s], f[2 * s + 1]);
+        }
+        if (ends) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float lo = __uint_as_float(scale[q] << 16), hi = __uint_as_float(scale[q] & 0xffff0000u);
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+              float(&to)[4] = acc[q][n0 + n];
+              to[0] = fmaf(lo, sum[q][n][0], to[0]);
+              to[1] = fmaf(lo, sum[q][n][1], to[1]);
+              to[2] = fmaf(hi, sum[q][n][2], to[2]);
+              to[3] = fmaf(hi, sum[q][n][3], to[3]);
+              sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
             }
           }
         }
@@ -463,124 +487,107 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
   }
 }
 
-struct Join {              // of two slices
-  float4* room;            // [kM][2][32]
-  uint32_t full, empty;    // barriers, one each a pair of warps
-};
-
-// `steps` steps of one unit from its step s on, then their sum: the slices are
-// joined, in order, and the first one's warps write it. PUT(half, column of the
-// half, token, value).
-template <int FMT, int SLICES, int NT, int PLANES, typename Put>
-__device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int m,
-                                             int group, int block, const Join& join, uint32_t& turn, Put put) {
+// `steps` steps of one unit from its step s on, then their sums out. PUT(half,
+// column of the half, row, two values: of this row of x and the next one).
+// `dry`: see products().
+template <int FMT, int NT, typename Put>
+__device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int rows,
+                                             int group, int block, bool dry, Put put) {
   constexpr int BK = step_rows(FMT);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mi = warp % kM, sl = warp / kM;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[2][NT][4];
 #pragma unroll
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.f;
+#pragma unroll 1
   for (; steps > 0; --steps, ++s) {
-    if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
+    if (!dry && !warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
     const int blocks = FMT == MEP_W4 ? (K - int(s * BK) + kW4Rows - 1) / kW4Rows : 0;
-    stage_product<FMT, SLICES, NT, PLANES>(acc, r.stage0 + c.slot * r.stage_bytes, r, mi, sl, blocks, group, block);
+    stage_product<FMT, NT>(acc, r.stage0 + c.slot * r.stage_bytes, r, warp, blocks, group, block);
     __syncwarp();
+    if (dry) continue;
     if (lane == 0) arrive(r.empty + 8 * c.slot);
     c.next(r.stages);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (8 * n >= m) break;
-    if (SLICES == 2) {
-      float4* mine = join.room + mi * 64 + lane;
-      if (sl == 1) {
-        if (!warp_wait(join.empty + 8 * mi, turn & 1 ^ 1, r)) return false;
-        mine[0] = make_float4(acc[0][n][0], acc[0][n][1], acc[0][n][2], acc[0][n][3]);
-        mine[32] = make_float4(acc[1][n][0], acc[1][n][1], acc[1][n][2], acc[1][n][3]);
-        __syncwarp();
-        if (lane == 0) arrive(join.full + 8 * mi);
-      } else {
-        if (!warp_wait(join.full + 8 * mi, turn & 1, r)) return false;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 f = mine[32 * q];
-          acc[q][n][0] += f.x, acc[q][n][1] += f.y, acc[q][n][2] += f.z, acc[q][n][3] += f.w;
-        }
-        __syncwarp();
-        if (lane == 0) arrive(join.empty + 8 * mi);
-      }
-      ++turn;
-    }
-    if (sl == 0) {
+    if (8 * n >= rows) break;
+    const int row = 8 * n + 2 * (lane & 3);
+    if (row < rows && !dry) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 8 * n + 2 * (lane & 3) + (i & 1);
-          if (t < m) put(q, 16 * mi + (lane >> 2) + 8 * (i >> 1), t, FMT == MEP_W4 ? kQ * acc[q][n][i] : acc[q][n][i]);
+        for (int i = 0; i < 4; i += 2) {
+          const float f = FMT == MEP_W4 ? kQ : 1.f;
+          put(q, 16 * warp + (lane >> 2) + 4 * i, row, f * acc[q][n][i], f * acc[q][n][i + 1]);
         }
     }
   }
   return true;
 }
 
-// All steps that this CTA is fed. PUT(first row, unit of the expert, part, half, column, token, value).
-template <int FMT, int SLICES, int NTMAX, int PLANES, typename Put>
-__device__ __forceinline__ void products(const Phase& p, int K, const Ring& r, Cursor& c, const uint16_t* start,
-                                         int group, int block, const Join& join, uint32_t& turn, Put put) {
+// All steps that this CTA is fed, of `planes` rows of x a token. PUT(first row of
+// the list, unit of the expert, part, rows, and as above). What a kernel executes
+// for the first time comes from far away, at some 25 ns an instruction: with
+// `dry` the code is run through once, on whatever the first stage holds and to no
+// effect, while that stage's bytes are on their way.
+template <int FMT, int NTMAX, typename Put>
+__device__ __forceinline__ void products(const Phase& p, int K, int planes, const Ring& r, Cursor& c,
+                                         const uint16_t* start, int group, int block, bool dry, int most, Put put) {
+#pragma unroll 1
   while (true) {
-    if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return;
-    const uint32_t at = r.step[c.slot];
-    if (at == kEnd) break;
+    uint32_t at = 0;
+    if (!dry) {
+      if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return;
+      at = r.step[c.slot];
+      if (at == kEnd) break;
+    }
     const uint32_t u = p.by_ks(at), s = at - u * p.ks, run = run_at(p, at);
-    const uint32_t steps = min(min(p.ks - s, (run + 1) * p.run - at), p.total - at);
+    const uint32_t steps = dry ? 1 : min(min(p.ks - s, (run + 1) * p.run - at), p.total - at);
     const uint32_t e = p.by_nb(u), j = u - e * p.nb, part = p.parts == 1 ? 0 : run - run_at(p, u * p.ks);
-    const int first = start[e], m = start[e + 1] - first;
-    const auto f = [&](int q, int col, int t, float v) { put(first, j, part, q, col, t, v); };
+    const int first = start[e], rows = planes * (dry ? most : start[e + 1] - first);
+    const auto f = [&](int q, int col, int row, float v0, float v1) { put(first, j, part, rows, q, col, row, v0, v1); };
     bool ok;
-    if (m <= 8)
-      ok = unit_product<FMT, SLICES, 1, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
-    else if (m <= 16)
-      ok = unit_product<FMT, SLICES, 2, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
-    else if (NTMAX <= 4 || m <= 32)
-      ok = unit_product<FMT, SLICES, 4, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
+    if (rows <= 8)
+      ok = unit_product<FMT, 1>(steps, s, K, r, c, rows, group, block, dry, f);
+    else if (rows <= 16)
+      ok = unit_product<FMT, 2>(steps, s, K, r, c, rows, group, block, dry, f);
+    else if (NTMAX <= 4 || rows <= 32)
+      ok = unit_product<FMT, 4>(steps, s, K, r, c, rows, group, block, dry, f);
     else
-      ok = unit_product<FMT, SLICES, NTMAX, PLANES>(steps, s, K, r, c, m, group, block, join, turn, f);
+      ok = unit_product<FMT, NTMAX>(steps, s, K, r, c, rows, group, block, dry, f);
     if (!ok) return;
+    dry = false;
   }
   __syncwarp();
   if ((threadIdx.x & 31) == 0) arrive(r.empty + 8 * c.slot);
   c.next(r.stages);
 }
 
-// Stages for rows of up to m tokens (as many as a unit's instantiation computes).
-template <int FMT, int PLANES>
-__device__ __forceinline__ void size_ring(Ring& r, uint32_t room, int m, int block) {
-  const int rows = m <= 8 ? 8 : m <= 16 ? 16 : m <= 32 ? 32 : 64;
+// Stages for up to `rows` rows of x (as many as a unit's instantiation computes).
+template <int FMT> __device__ __forceinline__ void size_ring(Ring& r, uint32_t room, int rows, int block) {
+  const int n = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   r.x_at = FMT == MEP_BF16 ? kPanels * step_rows(FMT) * kPanelRow : kPanels * 2 * block;
-  r.plane = rows * (step_rows(FMT) * 2 + 16);
-  r.stage_bytes = (r.x_at + PLANES * r.plane + 1023) / 1024 * 1024;
+  r.stage_bytes = (r.x_at + n * (step_rows(FMT) * 2 + 16) + 1023) / 1024 * 1024;
   r.stages = min(kMaxStages, int(room / r.stage_bytes));
 }
 
 struct Head {  // start of shared memory
-  uint64_t full[kMaxStages], empty[kMaxStages], join_full[kM], join_empty[kM];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint32_t step[kMaxStages];
   int warp_sums[32];
-  int abort, bad, most, entries, rows, go;
+  int abort, bad, most, rows, go;
+  Phase phase[2];
 };
 constexpr uint32_t kHeadBytes = 1024;
-__host__ __device__ constexpr uint32_t join_bytes(int slices) { return (slices - 1) * kM * 64 * 16; }
 
-__device__ __forceinline__ void init_ring(Ring& r, Join& join, Head* h, char* room, int consumers, int32_t* status) {
+__device__ __forceinline__ void init_ring(Ring& r, Head* h, int32_t* status) {
   r.full = smem_u32(h->full), r.empty = smem_u32(h->empty);
   r.step = h->step, r.abort = &h->abort, r.status = status;
-  join.full = smem_u32(h->join_full), join.empty = smem_u32(h->join_empty), join.room = reinterpret_cast<float4*>(room);
   if (threadIdx.x < kMaxStages) {
     mbar_init(r.full + 8 * threadIdx.x, 2);  // weights, rows
-    mbar_init(r.empty + 8 * threadIdx.x, consumers);
-    if (threadIdx.x < kM) mbar_init(join.full + 8 * threadIdx.x, 1), mbar_init(join.empty + 8 * threadIdx.x, 1);
+    mbar_init(r.empty + 8 * threadIdx.x, kWarps);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (threadIdx.x == 0) h->abort = h->bad = h->most = 0;
@@ -597,12 +604,11 @@ __device__ __forceinline__ void settle(const Ring& r) {
   __syncthreads();
 }
 
-// Items [0, n) over the grid's warps, one CTA's after another's: a few items are on as many SMs.
+// Items [0, n) over `warps` warps of every CTA, one CTA's after another's: a few items are on as many SMs.
 struct Spread {
   uint32_t i, step;
 };
-__device__ __forceinline__ Spread spread() {
-  const uint32_t warps = blockDim.x / 32;
+__device__ __forceinline__ Spread spread(int warps) {
   return {((threadIdx.x >> 5) * gridDim.x + blockIdx.x) * 32 + (threadIdx.x & 31), warps * gridDim.x * 32};
 }
 
@@ -640,15 +646,14 @@ constexpr uint16_t kNone = 0xffff;
 // The experts in use in ascending order, each one's tokens in order, more than
 // kChunk of them in several entries; where each assignment went. What comes from
 // memory is asked for at the start, the barriers' words are set up meanwhile.
-__device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Join& join, Head* h, char* room, int consumers,
-                                          char* scratch, const Lists& l) {
+__device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, char* scratch, const Lists& l) {
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
   uint32_t* e_at = reinterpret_cast<uint32_t*>(mask + a.E);  // entry and first row of an expert
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, A = a.T * a.K;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = kThreads, A = a.T * a.K;
   const int mine = tid < A ? __ldg(a.idx + tid) : -1;
   const float weight = tid < A ? __ldg(a.topk_w + tid) : 0.f;
   const int held = tid == 0 ? read_status(a.status) : 0;
-  init_ring(r, join, h, room, consumers, a.status);
+  init_ring(r, h, a.status);
   for (int e = tid; e < a.E; e += threads) mask[e] = 0;
   if (tid == 0 && blockIdx.x == 0) a.counters[0] = a.counters[1] = 0;
   __syncthreads();
@@ -691,9 +696,13 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Join& joi
     for (int q = 0; q < n; q += kChunk, ++entry) l.expert[entry] = e, l.start[entry] = row + q;
     before += ((n + kChunk - 1) / kChunk << 16) + n;
   }
-  if (tid == 0) {
-    h->entries = all >> 16, h->rows = all & 0xffff;
-    l.start[all >> 16] = all & 0xffff;
+  if (lane == 0 && warp < 2) {
+    const bool run = h->go && !h->bad;
+    h->phase[warp] = make_phase(run ? all >> 16 : 0, warp == 0 ? a.s1 : a.s2);
+    if (warp == 0) {
+      h->rows = run ? all & 0xffff : 0;
+      l.start[all >> 16] = all & 0xffff;
+    }
   }
   __syncthreads();
   if (!h->bad)
@@ -712,152 +721,178 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Join& joi
   __syncthreads();
 }
 
-template <int FMT, int SLICES>
-__global__ void __launch_bounds__(threads_of(SLICES), 1)
+template <int FMT> __device__ __forceinline__ Weights first_weights(const LayerArgs& a, const CUtensorMap* map) {
+  const long long m = FMT == MEP_W4 ? w4_matrix_bytes(a.H, a.F, a.group) : 0, q = FMT == MEP_W4 ? w4_panel_bytes(a.H, a.group) : 0;
+  return {map, a.w1, 2 * m, q, m, 2, a.F, a.F, true, a.H};
+}
+template <int FMT> __device__ __forceinline__ Weights second_weights(const LayerArgs& a, const CUtensorMap* map) {
+  const long long m = FMT == MEP_W4 ? w4_matrix_bytes(a.F, a.H, a.group) : 0, q = FMT == MEP_W4 ? w4_panel_bytes(a.F, a.group) : 0;
+  return {map, a.w2, m, q, 2 * q, 4, 2 * kW4Cols, a.H, false, a.F};
+}
+
+// The activation of n quads of columns: the first product's parts added up, in
+// order, then silu(g) * u as two bf16.
+__device__ __forceinline__ void activate(const LayerArgs& a, const Phase& p, const Lists& l, uint32_t n, Spread s, bool dry) {
+  constexpr uint32_t quads = kUnit / 8;  // of a unit's gates
+#pragma unroll 1
+  for (; s.i < n; s.i += s.step) {
+    const uint32_t unit = s.i / quads, row = p.by_nb(unit), j = unit - row * p.nb, col = j * (kUnit / 2) + s.i % quads * 4;
+    if (int(col) >= a.F) continue;
+    const uint32_t parts = parts_in(p, l.entry[row] * p.nb + j);
+    const float* in = a.part1 + (long long)row * p.parts * (2 * a.F) + col;
+    float g[4] = {}, u[4] = {};
+#pragma unroll 4
+    for (uint32_t q = 0; q < parts; ++q, in += 2 * a.F) {
+      const float4 vg = __ldcg(reinterpret_cast<const float4*>(in));
+      const float4 vu = __ldcg(reinterpret_cast<const float4*>(in + a.F));
+      g[0] += vg.x, g[1] += vg.y, g[2] += vg.z, g[3] += vg.w;
+      u[0] += vu.x, u[1] += vu.y, u[2] += vu.z, u[3] += vu.w;
+    }
+    __nv_bfloat16 hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float v = g[k] / (1.f + expf(-g[k])) * u[k];
+      hi[k] = __float2bfloat16_rn(v);
+      const float rest = v - __bfloat162float(hi[k]);
+      lo[k] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);  // an infinity stays one
+    }
+    __nv_bfloat16* o = a.act + (long long)row * 2 * a.F + col;
+    if (!dry) {
+      *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(hi);
+      *reinterpret_cast<uint2*>(o + a.F) = *reinterpret_cast<uint2*>(lo);
+    }
+  }
+}
+
+// n lanes' items of the output: eight lanes share 16 columns, each a part of the
+// token's experts, whose parts are added up in order.
+__device__ __forceinline__ void combine(const LayerArgs& a, const Phase& p, const Lists& l, uint32_t n, Spread s, bool dry) {
+  constexpr uint32_t items = kUnit / 16 * 8;
+#pragma unroll 1
+  for (; s.i < n; s.i += s.step) {
+    const uint32_t u = s.i / items, t = p.by_nb(u), j = u - t * p.nb, col = j * kUnit + s.i % items / 8 * 16;
+    if (int(col) >= a.H) continue;
+    const bool full = int(col) + 16 <= a.H;  // else eight columns
+    float v[16] = {};
+#pragma unroll 1
+    for (int k = s.i % 8; k < a.K; k += 8) {
+      const uint32_t row = l.row[t * a.K + k];
+      if (row == kNone) continue;
+      const float w = l.weight[t * a.K + k];
+      const uint32_t parts = parts_in(p, l.entry[row] * p.nb + j);
+      const float* in = a.part2 + (long long)row * p.parts * a.H + col;
+      float y[16] = {};
+#pragma unroll 2
+      for (uint32_t q = 0; q < parts; ++q, in += a.H) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (i >= 2 && !full) break;
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(in) + i);
+          y[4 * i] += f.x, y[4 * i + 1] += f.y, y[4 * i + 2] += f.z, y[4 * i + 3] += f.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = fmaf(w, y[i], v[i]);
+    }
+    // halves of the lanes' sums change hands: eight lanes end with two outputs each
+    const unsigned lanes = 0xffu << (threadIdx.x & 24);
+    const int lane = threadIdx.x & 7;
+#pragma unroll
+    for (int d = 4, left = 8; d > 0; d >>= 1, left >>= 1)
+#pragma unroll
+      for (int i = 0; i < left; ++i) {
+        const bool up = lane & d;
+        const float mine = up ? v[left + i] : v[i], other = up ? v[i] : v[left + i];
+        v[i] = mine + __shfl_xor_sync(lanes, other, d);
+      }
+    const int at = (lane & 4 ? 8 : 0) + (lane & 2 ? 4 : 0) + (lane & 1 ? 2 : 0);
+    if ((full || at < 8) && !dry)
+      *reinterpret_cast<__nv_bfloat162*>(a.out + (long long)t * a.H + col + at) = __floats2bfloat162_rn(v[0], v[1]);
+  }
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
     k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const LayerArgs a) {
   extern __shared__ __align__(1024) char smem[];
-  const auto grid = cooperative_groups::this_grid();
-  constexpr int NTMAX = kChunk / 8, kConsumers = kM * SLICES;
   Head* h = reinterpret_cast<Head*>(smem);
   Lists l;
   {
     const int cap = max_entries(a.T, a.K, a.E), A = a.T * a.K;
-    l.weight = reinterpret_cast<float*>(smem + kHeadBytes + join_bytes(SLICES));
+    l.weight = reinterpret_cast<float*>(smem + kHeadBytes);
     l.expert = reinterpret_cast<uint16_t*>(l.weight + A);
     l.start = l.expert + cap;
     l.entry = l.start + cap + 1;
     l.token = l.entry + A;
     l.row = l.token + A;
   }
-  const uint16_t *expert = l.expert, *start = l.start;
-  const uint32_t used = kHeadBytes + join_bytes(SLICES) + list_bytes(a.T, a.K, a.E);
+  const uint32_t used = kHeadBytes + list_bytes(a.T, a.K, a.E);
   const int block = FMT == MEP_W4 ? w4_block_bytes(a.group) : 0;
   Ring r;
-  Join join;
-  make_list(a, r, join, h, smem + kHeadBytes, kConsumers, smem + used, l);
+  make_list(a, r, h, smem + used, l);
   const bool go = h->go && !h->bad;
   if (h->go && h->bad && threadIdx.x == 0) set_status(a.status, MEP_ERR_BAD_ROUTING);
   r.stage0 = smem_u32(smem + used);
-  size_ring<FMT, 2>(r, kSmem - used, min(h->most, kChunk), block);
+  const int most = min(h->most, kChunk);
+  size_ring<FMT>(r, kSmem - used, 2 * most, block);
 
   const int warp = threadIdx.x >> 5;
-  const uint32_t experts = go ? h->entries : 0, rows = go ? h->rows : 0;
-  const Phase p1 = make_phase(experts, a.s1), p2 = make_phase(experts, a.s2);
-  const long long m1 = FMT == MEP_W4 ? w4_matrix_bytes(a.H, a.F, a.group) : 0, q1 = FMT == MEP_W4 ? w4_panel_bytes(a.H, a.group) : 0;
-  const long long m2 = FMT == MEP_W4 ? w4_matrix_bytes(a.F, a.H, a.group) : 0, q2 = FMT == MEP_W4 ? w4_panel_bytes(a.F, a.group) : 0;
-  const Weights w1 = {&map1, a.w1, 2 * m1, q1, m1, 2, a.F, a.F, true, a.H};
-  const Weights w2 = {&map2, a.w2, m2, q2, 2 * q2, 4, 2 * kW4Cols, a.H, false, a.F};
-  const Rows x1 = {reinterpret_cast<const char*>(a.x), 2LL * a.H, a.H};
-  const Rows x2 = {reinterpret_cast<const char*>(a.act), 2LL * a.F, a.F};
-  const auto token = [&](int row) { return (long long)l.token[row]; };
-  const auto same = [&](int row) { return (long long)row; };
-  Cursor c, behind;
-  uint32_t turn = 0;
-  Stream<FMT, 1> t1;
-  Stream<FMT, 2> t2;
-
-  if (warp == kConsumers) feed_ahead<FMT, true>(t1, p1, r, c, w1, x1, expert, start, block, token);
-  if (p1.runs > gridDim.x || p2.runs > gridDim.x) grid.sync();  // the counters are zero
-  if (warp == kConsumers) {
-    feed<FMT, true>(t1, behind, p1, r, c, w1, x1, expert, start, block, a.counters, token);
-    behind = c;  // the ring fills while the activation is computed
-    feed_ahead<FMT, false>(t2, p2, r, c, w2, x2, expert, start, block, same);
-  } else {
-    products<FMT, SLICES, NTMAX, 1>(p1, a.H, r, c, start, a.group, block, join, turn,
-                                    [&](int first, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int n = j * (kUnit / 2) + col;
-                                      if (n < a.F)
-                                        a.part1[((long long)(first + t) * p1.parts + part) * (2 * a.F) + q * a.F + n] = v;
-                                    });
-  }
-  grid.sync();
-  {
-    constexpr uint32_t quads = kUnit / 8;  // of a unit's gates, four and the four ups a lane
-    const uint32_t n = rows * p1.nb * quads;
+  const uint32_t rows = h->rows;
+  const Phase &p1 = h->phase[0], &p2 = h->phase[1];
+  const bool counted = p1.runs > gridDim.x || p2.runs > gridDim.x;  // the counters are in use: zero after a barrier
+  Cursor c;
+  if (warp == kWarps) {
+    Stream<FMT> t(r, l.expert, l.start, block);
+    Cursor behind;
+    t.own(p1, first_weights<FMT>(a, &map1), {reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1});
+    t.ahead(c, true);
+    if (counted) grid_barrier();
 #pragma unroll 1
-    for (Spread s = spread(); s.i < n; s.i += s.step) {
-      const uint32_t unit = s.i / quads, row = p1.by_nb(unit), j = unit - row * p1.nb, col = j * (kUnit / 2) + s.i % quads * 4;
-      if (int(col) >= a.F) continue;
-      const uint32_t parts = parts_in(p1, l.entry[row] * p1.nb + j);
-      const float* in = a.part1 + (long long)row * p1.parts * (2 * a.F) + col;
-      float g[4] = {}, u[4] = {};
-#pragma unroll 4
-      for (uint32_t q = 0; q < parts; ++q, in += 2 * a.F) {
-        const float4 vg = __ldcg(reinterpret_cast<const float4*>(in));
-        const float4 vu = __ldcg(reinterpret_cast<const float4*>(in + a.F));
-        g[0] += vg.x, g[1] += vg.y, g[2] += vg.z, g[3] += vg.w;
-        u[0] += vu.x, u[1] += vu.y, u[2] += vu.z, u[3] += vu.w;
+    for (int phase = 0; phase < 2; ++phase) {
+      t.feed(c, behind, phase == 1, a.counters + phase);
+      if (phase == 0) {  // the ring fills while the activation is computed
+        behind = c;
+        t.own(p2, second_weights<FMT>(a, &map2), {reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2});
+        t.ahead(c, false);
+        grid_barrier();
       }
-      __nv_bfloat16 hi[4], lo[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = g[k] / (1.f + expf(-g[k])) * u[k];
-        hi[k] = __float2bfloat16_rn(v);
-        const float rest = v - __bfloat162float(hi[k]);
-        lo[k] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);  // an infinity stays one
-      }
-      __nv_bfloat16* o = a.act + (long long)row * 2 * a.F + col;
-      *reinterpret_cast<uint2*>(o) = *reinterpret_cast<uint2*>(hi);
-      *reinterpret_cast<uint2*>(o + a.F) = *reinterpret_cast<uint2*>(lo);
+      grid_barrier();
+      fence_async();
     }
-    fence_async();
-  }
-  grid.sync();
-  if (warp == kConsumers) {
-    fence_async();
-    feed<FMT, false>(t2, behind, p2, r, c, w2, x2, expert, start, block, a.counters + 1, same);
   } else {
-    products<FMT, SLICES, NTMAX, 2>(p2, a.F, r, c, start, a.group, block, join, turn,
-                                    [&](int first, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int n = j * kUnit + q * (kUnit / 2) + col;
-                                      if (n < a.H) a.part2[((long long)(first + t) * p2.parts + part) * a.H + n] = v;
-                                    });
-  }
-  grid.sync();
-  if (go) {
-    // eight lanes share 16 outputs, each a part of the token's experts
-    constexpr uint32_t groups = kUnit / 16, items = groups * 8;
-    const uint32_t n = a.T * p2.nb * items;
+    if (counted) grid_barrier();
+    // Two turns of product and sum. Two warps first run through the sums, dry.
 #pragma unroll 1
-    for (Spread s = spread(); s.i < n; s.i += s.step) {
-      const uint32_t u = s.i / items, t = p2.by_nb(u), j = u - t * p2.nb, col = j * kUnit + s.i % items / 8 * 16;
-      if (int(col) >= a.H) continue;
-      const bool full = int(col) + 16 <= a.H;  // else eight columns
-      float v[16] = {};
-#pragma unroll 1
-      for (int k = s.i % 8; k < a.K; k += 8) {
-        const uint32_t row = l.row[t * a.K + k];
-        if (row == kNone) continue;
-        const float w = l.weight[t * a.K + k];
-        const uint32_t parts = parts_in(p2, l.entry[row] * p2.nb + j);
-        const float* in = a.part2 + (long long)row * p2.parts * a.H + col;
-        float y[16] = {};
-#pragma unroll 2
-        for (uint32_t q = 0; q < parts; ++q, in += a.H) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i >= 2 && !full) break;
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(in) + i);
-            y[4 * i] += f.x, y[4 * i + 1] += f.y, y[4 * i + 2] += f.z, y[4 * i + 3] += f.w;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = fmaf(w, y[i], v[i]);
+    for (int phase = warp < 2 && rows > 0 ? -1 : 0; phase < 2; ++phase) {
+      const bool dry = phase < 0;
+      const bool second = dry ? warp == 1 : phase == 1;
+      const Phase& p = h->phase[second];
+      if (!dry) {
+        const Sums o = second ? Sums{a.part2, uint32_t(a.H), kUnit, kUnit / 2, a.H, -1}
+                              : Sums{a.part1, 2u * a.F, kUnit / 2, a.F, a.F, 0};
+        products<FMT, kChunk / 4>(
+            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, a.group, block, !second, most,
+            [&](int first, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
+              const int n = j * o.unit + col, off = q * o.half;
+              if (n + (off & o.counted) >= o.limit) return;
+              // the two rows: the activation's two of one token; else two tokens
+              float* to = o.p + ((long long)(first + (second ? row >> 1 : row)) * p.parts + part) * o.pitch + n + off;
+              *to = second ? v0 + v1 : v0;
+              if (!second && row + 1 < rows) to[p.parts * o.pitch] = v1;
+            });
+        grid_barrier();
       }
-      // halves of the lanes' sums change hands: eight lanes end with two outputs each
-      const unsigned lanes = 0xffu << (threadIdx.x & 24);
-      const int lane = threadIdx.x & 7;
-#pragma unroll
-      for (int d = 4, left = 8; d > 0; d >>= 1, left >>= 1)
-#pragma unroll
-        for (int i = 0; i < left; ++i) {
-          const bool up = lane & d;
-          const float mine = up ? v[left + i] : v[i], other = up ? v[i] : v[left + i];
-          v[i] = mine + __shfl_xor_sync(lanes, other, d);
+      Spread s = spread(kWarps);
+      if (dry) s.i = threadIdx.x & 31, s.step = 0x40000000;
+      if (!second) {
+        activate(a, p, l, dry ? 32 : rows * p.nb * (kUnit / 8), s, dry);
+        if (!dry) {
+          fence_async();
+          grid_barrier();
         }
-      const int at = (lane & 4 ? 8 : 0) + (lane & 2 ? 4 : 0) + (lane & 1 ? 2 : 0);
-      if (full || at < 8)
-        *reinterpret_cast<__nv_bfloat162*>(a.out + (long long)t * a.H + col + at) = __floats2bfloat162_rn(v[0], v[1]);
+      } else if (go) {
+        combine(a, p, l, dry ? 32 : a.T * p.nb * (kUnit / 16 * 8), s, dry);
+      }
     }
   }
   settle(r);
@@ -876,77 +911,76 @@ struct ProductArgs {
   void* y;
 };
 
-template <int SLICES, int NTMAX, typename T>
-__global__ void __launch_bounds__(threads_of(SLICES), 1) k_w4_product(const ProductArgs a) {
+template <int NTMAX, typename T>
+__global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a) {
   extern __shared__ __align__(1024) char smem[];
-  const auto grid = cooperative_groups::this_grid();
-  constexpr int FMT = MEP_W4, kConsumers = kM * SLICES;
+  constexpr int FMT = MEP_W4;
   Head* h = reinterpret_cast<Head*>(smem);
   uint16_t* start = reinterpret_cast<uint16_t*>(h + 1);  // one entry, all rows
   uint16_t* expert = start + 2;
   static_assert(sizeof(Head) + 8 <= kHeadBytes, "head");
-  const uint32_t used = kHeadBytes + join_bytes(SLICES);
+  constexpr uint32_t used = kHeadBytes;
+  const bool producer = threadIdx.x >> 5 == kWarps;
   Ring r;
-  Join join;
-  init_ring(r, join, h, smem + kHeadBytes, kConsumers, a.status);
-  if (threadIdx.x == 32) {
-    h->go = read_status(a.status) == 0;
+  const int held = threadIdx.x == 0 ? read_status(a.status) : 0;
+  init_ring(r, h, a.status);
+  if (threadIdx.x == 0) {
     start[0] = 0, start[1] = a.T, expert[0] = 0;
     if (blockIdx.x == 0) *a.counter = 0;
+    h->go = held == 0;
   }
   __syncthreads();
   const bool go = h->go;
   const int block = w4_block_bytes(a.group);
   r.stage0 = smem_u32(smem + used);
-  size_ring<FMT, 1>(r, kSmem - used, a.T, block);
-  const int warp = threadIdx.x >> 5;
+  size_ring<FMT>(r, kSmem - used, a.T, block);
   const Phase p = make_phase(go ? 1 : 0, a.shape);
-  const long long panel = w4_panel_bytes(a.K, a.group);
-  const Weights w = {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K};
   const bool pad = a.K % 8 != 0;
   const int K8 = (a.K + 7) / 8 * 8;
-  const Rows x = {reinterpret_cast<const char*>(pad ? a.padded : a.x), 2LL * K8, K8};
-  const auto same = [&](int row) { return (long long)row; };
-  Cursor c;
-  const Cursor behind;
-  uint32_t turn = 0;
-  Stream<FMT, 1> t1;
-  if (warp == kConsumers) {
-    if (pad)
-      feed_ahead<FMT, false>(t1, p, r, c, w, x, expert, start, block, same);
-    else
-      feed_ahead<FMT, true>(t1, p, r, c, w, x, expert, start, block, same);
-  }
-  if (pad) {
+  const bool first_barrier = pad || p.runs > gridDim.x;
+  const auto copy_rows = [&]() {  // to whole vectors
     for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < uint32_t(a.T * K8); i += gridDim.x * blockDim.x) {
       const uint32_t t = i / K8, k = i % K8;
       a.padded[i] = int(k) < a.K ? a.x[(long long)t * a.K + k] : __float2bfloat16_rn(0.f);
     }
     fence_async();
-  }
-  if (pad || p.runs > gridDim.x) grid.sync();
-  if (warp == kConsumers) {
+  };
+  Cursor c;
+  if (producer) {
+    Stream<FMT> t(r, expert, start, block);
+    const Cursor behind;
+    const long long panel = w4_panel_bytes(a.K, a.group);
+    t.own(p, {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K},
+          {reinterpret_cast<const char*>(pad ? a.padded : a.x), nullptr, 2LL * K8, K8, 1});
+    t.ahead(c, !pad);
+    if (pad) copy_rows();
+    if (first_barrier) grid_barrier();
     fence_async();
-    if (pad)
-      feed<FMT, false>(t1, behind, p, r, c, w, x, expert, start, block, a.counter, same);
-    else
-      feed<FMT, true>(t1, behind, p, r, c, w, x, expert, start, block, a.counter, same);
+    t.feed(c, behind, pad, a.counter);
   } else {
-    products<FMT, SLICES, NTMAX, 1>(p, a.K, r, c, start, a.group, block, join, turn,
-                                    [&](int, uint32_t j, uint32_t part, int q, int col, int t, float v) {
-                                      const int n = j * kUnit + q * (kUnit / 2) + col;
-                                      if (n >= a.N) return;
-                                      if (p.parts == 1)
-                                        static_cast<T*>(a.y)[(long long)t * a.N + n] = from_f32<T>(v);
-                                      else
-                                        a.part[((long long)t * p.parts + part) * a.N + n] = v;
-                                    });
+    if (pad) copy_rows();
+    if (first_barrier) grid_barrier();
+    products<FMT, NTMAX>(p, a.K, 1, r, c, start, a.group, block, true, a.T,
+                         [&](int, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
+                           const int n = j * kUnit + q * (kUnit / 2) + col;
+                           if (n >= a.N) return;
+                           if (p.parts == 1) {
+                             T* to = static_cast<T*>(a.y) + (long long)row * a.N + n;
+                             *to = from_f32<T>(v0);
+                             if (row + 1 < rows) to[a.N] = from_f32<T>(v1);
+                           } else {
+                             float* to = a.part + ((long long)row * p.parts + part) * a.N + n;
+                             *to = v0;
+                             if (row + 1 < rows) to[(long long)p.parts * a.N] = v1;
+                           }
+                         });
   }
   if (p.parts > 1) {
-    grid.sync();
+    grid_barrier();
     if (go) {
       const uint32_t n = uint32_t(a.T) * a.N;
-      for (Spread s = spread(); s.i < n; s.i += s.step) {
+#pragma unroll 1
+      for (Spread s = spread(kWarps + 1); s.i < n; s.i += s.step) {
         const uint32_t t = s.i / a.N, col = s.i - t * a.N, parts = parts_in(p, col / kUnit);
         const float* in = a.part + (long long)t * p.parts * a.N + col;
         float v = 0.f;
@@ -1043,16 +1077,15 @@ bool product_space(int T, long long K, long long N, int group, ProductSpace* s) 
   return true;
 }
 
-template <int FMT, int SLICES>
+template <int FMT>
 int launch_layer(const CUtensorMap& m1, const CUtensorMap& m2, const LayerArgs& a, cudaStream_t st) {
   const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(FMT);
   const long long n1 = experts * ceil_div(a.F, kUnit / 2) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
-  return launch_all(k_layer<FMT, SLICES>, n1 > n2 ? n1 : n2, threads_of(SLICES), st, m1, m2, a);
+  return launch_all(k_layer<FMT>, n1 > n2 ? n1 : n2, kThreads, st, m1, m2, a);
 }
 template <typename T> int launch_product(const ProductArgs& a, cudaStream_t st) {
   const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(MEP_W4));
-  return a.T <= 32 ? launch_all(k_w4_product<2, 4, T>, n, threads_of(2), st, a)
-                   : launch_all(k_w4_product<1, 8, T>, n, threads_of(1), st, a);
+  return a.T <= 32 ? launch_all(k_w4_product<4, T>, n, kThreads, st, a) : launch_all(k_w4_product<8, T>, n, kThreads, st, a);
 }
 
 }  // namespace
@@ -1128,8 +1161,8 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
                        reinterpret_cast<__nv_bfloat16*>(out)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap m1 = {}, m2 = {};
-  if (w_type == MEP_W4) return launch_layer<MEP_W4, 2>(m1, m2, a, st);
+  if (w_type == MEP_W4) return launch_layer<MEP_W4>(m1, m2, a, st);
   if (!on_current_device(w1) || !on_current_device(w2)) return MEP_ERR_INVALID_ARG;
   if (!make_map3(&m1, w1, E, H, 2 * F) || !make_map3(&m2, w2, E, F, H)) return MEP_ERR_CUDA;
-  return launch_layer<MEP_BF16, 2>(m1, m2, a, st);
+  return launch_layer<MEP_BF16>(m1, m2, a, st);
 }
