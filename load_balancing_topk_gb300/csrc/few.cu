@@ -167,26 +167,16 @@ struct Sums {
   int limit, counted;  // j * unit + column + (half & counted) is below limit where a column is there
 };
 
-// `live`: not executed where it is false, though fetched.
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar, bool live) {
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "@p cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(int(live))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, bool live) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
-      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar), "r"(int(live))
-      : "memory");
-}
-__device__ __forceinline__ void expect(uint32_t bar, uint32_t bytes, bool live) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(int(live))
-      : "memory");
+__device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void arrive(uint32_t bar) {
@@ -215,16 +205,16 @@ template <int FMT> struct Stream {
   uint32_t step = 0, end = 0;  // of the run
   uint32_t s, j, entry;        // step of the unit, unit of the expert, the expert's entry
   uint32_t tx;                 // bytes of a full step's weights
-  int e, m, panels;            // panels: a bit for each that is there
+  int e, rows_n, panels;       // expert, rows of x; a bit for each panel that is there
   const uint8_t* unit_w;       // 4 bits: the unit's first panel
   const char* row[2];          // this lane's rows of x
   uint32_t at[2];              // and where they go in a stage
 
   __device__ __forceinline__ Stream(const Ring& ring, const uint16_t* e_, const uint16_t* s_, int b)
       : r(ring), expert(e_), start(s_), block(b) {}
-  __device__ __forceinline__ void unit(bool live) {
-    const int lane = threadIdx.x & 31, first = live ? start[entry] : 0, panel = j * w.unit, pl = x.planes - 1;
-    m = live ? start[entry + 1] - first : 0, e = live ? expert[entry] : 0;
+  __device__ __forceinline__ void unit() {
+    const int lane = threadIdx.x & 31, first = start[entry], panel = j * w.unit, pl = x.planes - 1;
+    rows_n = (start[entry + 1] - first) << pl, e = expert[entry];
     const int count = (w.columns + kW4Cols - 1) / kW4Cols - panel;
     panels = w.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
     tx = __popc(panels) * (FMT == MEP_BF16 ? step_rows(FMT) * kPanelRow : 2 * block);
@@ -233,64 +223,64 @@ template <int FMT> struct Stream {
     for (int i = 0; i < 2; ++i) {
       const int q = lane + 32 * i;
       at[i] = r.x_at + q * pitch;
-      if (q < m << pl) {
+      if (q < rows_n) {
         const int of = first + (q >> pl);
         row[i] = x.p + (((x.token == nullptr ? of : x.token[of]) << pl) + (q & pl)) * x.pitch;
       }
     }
   }
-  __device__ __forceinline__ void seek(uint32_t to, bool live = true) {
+  __device__ __forceinline__ void seek(uint32_t to) {
     step = to, end = min(p.total, to + p.run);
-    if (step >= end && live) return;
+    if (step >= end) return;
     const uint32_t u = p.by_ks(step);
     s = step - u * p.ks, entry = p.by_nb(u), j = u - entry * p.nb;
-    unit(live);
+    unit();
   }
-  __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_, bool live = true) {
+  __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_) {
     p = p_, w = w_, x = x_;
-    seek(min(p.total, blockIdx.x * p.run), live);
+    seek(min(p.total, blockIdx.x * p.run));
   }
   __device__ __forceinline__ void next() {
     if (++step == end || ++s < p.ks) return;
     s = 0;
     if (++j == p.nb) j = 0, ++entry;
-    unit(true);
+    unit();
   }
-  __device__ __forceinline__ void weights(int slot, bool live = true) const {  // one lane
+  __device__ __forceinline__ void weights(int slot) const {  // one lane
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
-    if (live) r.step[slot] = step;
+    r.step[slot] = step;
     if (FMT == MEP_BF16) {
       constexpr uint32_t bytes = step_rows(FMT) * kPanelRow;
       const int col = j * w.unit * kW4Cols, k = s * BK;
-      expect(bar, tx, live);
+      mbar_expect_tx(bar, tx);
 #pragma unroll
       for (int q = 0; q < kPanels; ++q)
-        tma_3d(dst + q * bytes, w.map, col + (q & 1) * kW4Cols + (q >> 1) * w.col_second, k, e, bar, live && panels >> q & 1);
+        if (panels >> q & 1) tma_3d(dst + q * bytes, w.map, col + (q & 1) * kW4Cols + (q >> 1) * w.col_second, k, e, bar);
     } else {
       const uint8_t* src = unit_w + s * (2 * block);
       const uint32_t half = 2 * int(s) + 1 == (w.K + kW4Rows - 1) / kW4Rows;  // the last step may have one block
-      expect(bar, tx >> half, live);
+      mbar_expect_tx(bar, tx >> half);
 #pragma unroll
       for (int q = 0; q < kPanels; ++q)
-        bulk(dst + q * 2 * block, src + (q & 1) * w.panel + (q >> 1) * w.second, (2 * block) >> half, bar,
-             live && panels >> q & 1);
+        if (panels >> q & 1) bulk(dst + q * 2 * block, src + (q & 1) * w.panel + (q >> 1) * w.second, (2 * block) >> half, bar);
     }
   }
-  __device__ __forceinline__ void rows(int slot, bool live = true) const {  // the warp
-    const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0), n = m << (x.planes - 1);
+  __device__ __forceinline__ void rows(int slot) const {  // the warp
+    const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
     if (bytes < 2 * BK) {  // beyond the sum's end the weights are zeros: what they meet must be numbers
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        if (lane + 32 * i < n)
+        if (lane + 32 * i < rows_n)
           for (int b = bytes; b < 2 * BK; b += 16)
             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at[i] + b), "r"(0) : "memory");
       fence_async();
       __syncwarp();
     }
-    if (lane == 0) expect(bar, n * bytes, live);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) bulk(dst + at[i], row[i] + 2 * k0, bytes, bar, lane + 32 * i < n);
+    if (lane == 0) mbar_expect_tx(bar, rows_n * bytes);
+    // lanes' copies go out one after another: a branch leaves the others out
+    if (lane < rows_n) bulk(dst + at[0], row[0] + 2 * k0, bytes, bar);
+    if (rows_n > 32 && lane + 32 < rows_n) bulk(dst + at[1], row[1] + 2 * k0, bytes, bar);
   }
   // Before a barrier of the grid: the weights of as many steps of the CTA's own
   // run as the ring has room for, and their rows where these are there already.
