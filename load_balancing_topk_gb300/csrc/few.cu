@@ -52,7 +52,9 @@ constexpr int kSmem = 227 * 1024;
 constexpr int kChunk = 32;          // tokens of an expert that one unit takes in the layer
 constexpr uint32_t kEnd = 0xffffffffu;
 
-__host__ __device__ constexpr int step_rows(int fmt) { return fmt == MEP_BF16 ? 64 : 256; }
+// The kernels go by the weights' group: 0 for bf16, else 32, 64 or 128 rows of
+// a column in 4 bits.
+__host__ __device__ constexpr int step_rows(int group) { return group == 0 ? 64 : 256; }
 
 // ---------------------------------------------------------------------------
 // n / d by a product, n < 2^31: with 2^l >= d, m = floor(2^(31+l) / d) + 1 the
@@ -75,17 +77,22 @@ struct Shape {
 Shape shape_of(long long ks, long long nb) {
   return {uint32_t(ks), uint32_t(nb), div_of(uint32_t(ks)), div_of(uint32_t(nb))};
 }
-// Its units' steps in a row, cut into runs of `run` steps. Up to kOneRun steps a
-// CTA: one run each, equal ones. More: runs of a power of two, sixteen to 32 a
-// CTA, taken as they come: some SMs are a fifth slower than others at reading
-// (64 tokens of the large layer: 2.72 ms with equal shares, 2.32 this way). Runs
-// of a sixteenth of a unit or more, which bounds the partial sums.
+// Its units' steps in a row, cut into runs. Up to kOneRun steps a CTA: one run
+// each, equal ones. More: runs of a power of two, sixteen to 32 a CTA, taken as
+// they come, since some SMs are a fifth slower than others at reading (64 tokens
+// of the large layer: 2.72 ms with equal shares, 2.32 this way). In 4 bits, whose
+// panels are contiguous, three quarters of the steps are in one long run a CTA
+// (16 tokens of the large layer 357 -> 341 us); in bf16, whose rows' pieces lie
+// between the other columns', CTAs read faster side by side (1790 us; 1870 with
+// long runs). Short runs are a sixteenth of a unit or more, which bounds the
+// partial sums.
 constexpr uint32_t kOneRun = 32;
 struct Phase {
   uint32_t ks, nb;
-  uint32_t total, run, runs;
-  uint32_t parts;  // runs that a unit may be cut over
-  uint32_t by_run; // n / run: 2^32 / run + 1, exact for powers of two and for n * run < 2^32
+  uint32_t total, run;       // steps; of a short run
+  uint32_t q, first, runs;   // short runs in a CTA's own one, in all own ones; runs, the own ones counted as one each
+  uint32_t parts;            // runs that a unit may be cut over
+  uint32_t by_run, by_q;     // n / d: 2^32 / d + 1, exact for powers of two and for n * d < 2^32; 0: d is 1
   Div by_ks, by_nb;
 };
 __host__ __device__ __forceinline__ uint32_t least_run(uint32_t ks) {
@@ -100,24 +107,39 @@ __host__ __device__ __forceinline__ uint32_t run_of(uint32_t total, uint32_t ks)
   while (run * 32 <= per) run *= 2;
   return run;
 }
-// Unit u is in runs u * ks / run up to ((u + 1) * ks - 1) / run, so many at most:
+// A unit is cut where runs end, into so many parts at most:
 __host__ __device__ __forceinline__ uint32_t parts_of(uint32_t ks, uint32_t run) {
   const uint32_t p = (ks - 1) / run + 2;
   return p < ks ? p : ks;
 }
-__device__ __forceinline__ Phase make_phase(uint32_t experts, const Shape& s) {
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t m) { return m == 0 ? n : __umulhi(n, m); }
+__device__ __forceinline__ Phase make_phase(uint32_t experts, const Shape& s, bool long_run) {
   Phase p;
   p.ks = s.ks, p.nb = s.nb, p.by_ks = s.by_ks, p.by_nb = s.by_nb;
   p.total = experts * s.nb * s.ks;
   p.run = run_of(p.total, s.ks);
   p.by_run = 0xffffffffu / p.run + 1;
+  const uint32_t shorts = divide(p.total + p.run - 1, p.by_run), each = p.total / (gridDim.x * p.run);
+  p.q = long_run && each > 1 ? each * 3 / 4 : 1;
+  p.by_q = 0xffffffffu / p.q + 1;
+  p.first = gridDim.x * p.q;
+  p.runs = shorts <= p.first ? divide(shorts + p.q - 1, p.by_q) : gridDim.x + shorts - p.first;
   p.parts = p.run % s.ks == 0 ? 1 : parts_of(s.ks, p.run);
-  p.runs = (p.total + p.run - 1) / p.run;
   return p;
 }
-__device__ __forceinline__ uint32_t run_at(const Phase& p, uint32_t step) {
-  return p.by_run == 0 ? step : __umulhi(step, p.by_run);
+// Each run a unit: nothing is cut (and nothing asks run_at).
+__device__ __forceinline__ void whole_units(Phase& p) {
+  p.run = p.ks, p.q = 1, p.first = gridDim.x, p.runs = p.nb, p.parts = 1;
 }
+// The run of a step; the first step of a run.
+__device__ __forceinline__ uint32_t run_at(const Phase& p, uint32_t step) {
+  const uint32_t r = divide(step, p.by_run);
+  return r < p.first ? divide(r, p.by_q) : gridDim.x + r - p.first;
+}
+__device__ __forceinline__ uint32_t run_start(const Phase& p, uint32_t run) {
+  return min(p.total, (run < gridDim.x ? run * p.q : p.first + run - gridDim.x) * p.run);
+}
+// Unit u is in runs run_at(u * ks) up to run_at((u + 1) * ks - 1).
 __device__ __forceinline__ uint32_t parts_in(const Phase& p, uint32_t unit) {
   return p.parts == 1 ? 1 : run_at(p, (unit + 1) * p.ks - 1) - run_at(p, unit * p.ks) + 1;
 }
@@ -151,8 +173,10 @@ struct Weights {
   bool gated;                       // the halves are gate and up columns, each counted to `columns`
   int K;                            // rows
 };
-// Rows of x: `planes` of them after one another (the activation's two).
+// Rows of x: `planes` of them after one another (the activation's two). Given a
+// map, tiles of rows one after another instead of row by row.
 struct Rows {
+  const CUtensorMap* map;
   const char* p;
   const uint16_t* token;  // row of x of a row of the list; NULL: the same
   long long pitch;        // bytes
@@ -173,6 +197,12 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
@@ -183,6 +213,8 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __noinline__ void grid_barrier() { cooperative_groups::this_grid().sync(); }
+// Rows that a stage has room for (as many as a unit's instantiation computes).
+__device__ __forceinline__ int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 // A whole warp waits; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Ring& r) {
   if (__all_sync(MEP_FULL_MASK, mbar_try_wait_long(bar, parity))) return true;
@@ -194,11 +226,11 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const R
 // and its rows have: two arrivals. What a step needs is worked out where its
 // unit begins; a step itself has to cost less than its bytes take to come (a
 // stage of 32 KB in 0.75 us).
-template <int FMT> struct Stream {
-  static constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
+template <int G, bool TILES> struct Stream {
+  static constexpr int BK = step_rows(G), pitch = BK * 2 + 16;
   const Ring& r;
   const uint16_t *expert, *start;
-  const int block;
+  static constexpr int block = G == 0 ? 0 : w4_block_bytes(G);
   Phase p;
   Weights w;
   Rows x;
@@ -210,17 +242,18 @@ template <int FMT> struct Stream {
   const char* row[2];          // this lane's rows of x
   uint32_t at[2];              // and where they go in a stage
 
-  __device__ __forceinline__ Stream(const Ring& ring, const uint16_t* e_, const uint16_t* s_, int b)
-      : r(ring), expert(e_), start(s_), block(b) {}
+  __device__ __forceinline__ Stream(const Ring& ring, const uint16_t* e_, const uint16_t* s_)
+      : r(ring), expert(e_), start(s_) {}
   __device__ __forceinline__ void unit() {
     const int lane = threadIdx.x & 31, first = start[entry], panel = j * w.unit, pl = x.planes - 1;
     rows_n = (start[entry + 1] - first) << pl, e = expert[entry];
+    if (TILES) rows_n = tile_rows(rows_n);
     const int count = (w.columns + kW4Cols - 1) / kW4Cols - panel;
     panels = w.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
-    tx = __popc(panels) * (FMT == MEP_BF16 ? step_rows(FMT) * kPanelRow : 2 * block);
-    if (FMT == MEP_W4) unit_w = w.w4 + e * w.expert + panel * w.panel;
+    tx = __popc(panels) * (G == 0 ? step_rows(G) * kPanelRow : 2 * block);
+    if (G != 0) unit_w = w.w4 + e * w.expert + panel * w.panel;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 && !TILES; ++i) {
       const int q = lane + 32 * i;
       at[i] = r.x_at + q * pitch;
       if (q < rows_n) {
@@ -229,8 +262,8 @@ template <int FMT> struct Stream {
       }
     }
   }
-  __device__ __forceinline__ void seek(uint32_t to) {
-    step = to, end = min(p.total, to + p.run);
+  __device__ __forceinline__ void seek(uint32_t run) {
+    step = run_start(p, run), end = run_start(p, run + 1);
     if (step >= end) return;
     const uint32_t u = p.by_ks(step);
     s = step - u * p.ks, entry = p.by_nb(u), j = u - entry * p.nb;
@@ -238,7 +271,7 @@ template <int FMT> struct Stream {
   }
   __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_) {
     p = p_, w = w_, x = x_;
-    seek(min(p.total, blockIdx.x * p.run));
+    seek(blockIdx.x);
   }
   __device__ __forceinline__ void next() {
     if (++step == end || ++s < p.ks) return;
@@ -249,8 +282,8 @@ template <int FMT> struct Stream {
   __device__ __forceinline__ void weights(int slot) const {  // one lane
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
     r.step[slot] = step;
-    if (FMT == MEP_BF16) {
-      constexpr uint32_t bytes = step_rows(FMT) * kPanelRow;
+    if (G == 0) {
+      constexpr uint32_t bytes = step_rows(G) * kPanelRow;
       const int col = j * w.unit * kW4Cols, k = s * BK;
       mbar_expect_tx(bar, tx);
 #pragma unroll
@@ -268,6 +301,14 @@ template <int FMT> struct Stream {
   __device__ __forceinline__ void rows(int slot) const {  // the warp
     const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
+    if (TILES) {  // zeros beyond the rows and the sum's end
+      if (lane == 0) {
+        mbar_expect_tx(bar, rows_n * BK * 2);
+#pragma unroll
+        for (int i = 0; i < BK / 64; ++i) tma_2d(dst + r.x_at + i * rows_n * 128, x.map, k0 + 64 * i, 0, bar);
+      }
+      return;
+    }
     if (bytes < 2 * BK) {  // beyond the sum's end the weights are zeros: what they meet must be numbers
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -303,7 +344,7 @@ template <int FMT> struct Stream {
     if (more && lane == 0) taken = atomicAdd(counter, 1u);  // on its way while the run is fed
     if (due) {
       const uint32_t to = step, stop = end;
-      seek(min(p.total, blockIdx.x * p.run));
+      seek(blockIdx.x);
       while (step < to) {
         rows(behind.slot);
         behind.next(r.stages);
@@ -316,7 +357,7 @@ template <int FMT> struct Stream {
       if (step == end) {
         const uint32_t run = more ? gridDim.x + __shfl_sync(MEP_FULL_MASK, taken, 0) : p.runs;
         if (run >= p.runs) break;
-        seek(run * p.run);
+        seek(run);
         if (lane == 0) taken = atomicAdd(counter, 1u);
       }
       if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
@@ -355,6 +396,11 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
@@ -379,13 +425,19 @@ __device__ __forceinline__ void widen_q(uint32_t word, uint32_t (&a)[4]) {
 constexpr float kQ = 64.f;
 
 // This warp's share of a stage: 16 columns of either half.
-template <int FMT, int NT>
+template <int G, bool TILES, int NT>
 __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t stage, const Ring& r, int warp,
-                                              int blocks, int group, int block) {
-  constexpr int BK = step_rows(FMT), pitch = BK * 2 + 16;
+                                              int blocks, int tile) {
+  constexpr int BK = step_rows(G), pitch = BK * 2 + 16;
   const int lane = threadIdx.x & 31;
-  const uint32_t xb = stage + r.x_at + (lane & 7) * pitch + 16 * (lane >> 3);
-  if (FMT == MEP_BF16) {
+  // eight rows of x from row 8 n on, 32 columns from k on: where this lane's part starts
+  const auto x_at = [&](int n, int k) -> uint32_t {
+    if (TILES)
+      return stage + r.x_at + (k >> 6) * (tile * 128) + (8 * n + (lane & 7)) * 128 +
+             ((((k >> 3 & 7) + (lane >> 3)) ^ (lane & 7)) << 4);
+    return stage + r.x_at + (8 * n + (lane & 7)) * pitch + 16 * (lane >> 3) + 2 * k;
+  };
+  if (G == 0) {
     const uint32_t wa = stage + (warp >> 2) * (BK * kPanelRow) + ((lane >> 4) * 8 + (lane & 7)) * kPanelRow +
                         (((2 * (warp & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4);
 #pragma unroll
@@ -398,7 +450,7 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         uint32_t b[4];
-        ldmatrix4(b, xb + n * (8 * pitch) + 2 * k);
+        ldmatrix4(b, x_at(n, k));
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -406,61 +458,67 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
       }
     }
   } else {
-    // With few columns everything that a block of 128 rows needs of the stage is
-    // asked for at once; with more than 32 the block is gone through again.
-    constexpr bool early = NT <= 2;
-    constexpr int NS = NT < 4 ? NT : 4;
+    // Everything that a block of 128 rows needs of the stage is asked for at once
+    // (with more than 32 columns the block is gone through again), with eight
+    // columns both blocks' at once.
+    constexpr int NS = NT < 4 ? NT : 4, block = w4_block_bytes(G > 0 ? G : 128), per = G > 0 ? G / 32 : 1;  // groups: per * 32 rows
+    constexpr int ahead = 1;
+    uint4 w[ahead][2][2];
+    uint32_t x[ahead][4][NT <= 2 ? NS : 1][4], scale[ahead][4][2];
 #pragma unroll
     for (int i = 0; i < 2 * (NT / NS); ++i) {
-      const int b = i & 1, n0 = (i >> 1) * NS;
-      if (b >= blocks) continue;
-      const uint32_t wb = stage + (warp >> 2) * 2 * block + b * block;
-      const uint32_t at = wb + ((warp & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((warp & 3) * 8 + (lane >> 2)) * 4;
-      const uint32_t xa = xb + n0 * (8 * pitch) + 256 * b;
-      uint4 w[2][2];
-      uint32_t x[4][early ? NS : 1][4];
+      const int n0 = (i >> 1) * NS;
+      if ((i & 1) >= blocks) continue;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) w[h][0] = lds128(at + 2048 * h), w[h][1] = lds128(at + 2048 * h + 4 * block);
-      if (early) {
+      for (int o = 0; o < ahead; ++o) {
+        const int b = (i & 1) + o;
+        if (ahead == 2 && i > 0) break;
+        const uint32_t wb = stage + (warp >> 2) * 2 * block + b * block;
+        const uint32_t at = wb + ((warp & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((warp & 3) * 8 + (lane >> 2)) * 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[o][h][0] = lds128(at + 2048 * h), w[o][h][1] = lds128(at + 2048 * h + 4 * block);
+        if (NT <= 2) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int n = 0; n < NS; ++n) ldmatrix4(x[o][k][n], x_at(n0 + n, 128 * b + 32 * k));
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
+          if ((k + 1) % per == 0)
 #pragma unroll
-          for (int n = 0; n < NS; ++n) ldmatrix4(x[k][n], xa + n * (8 * pitch) + 64 * k);
+            for (int q = 0; q < 2; ++q) scale[o][k][q] = lds32(sb + k / per * 128 + q * 4 * block);
       }
+      const int o = ahead == 2 ? i & 1 : 0;
       float sum[2][NS][4];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int n = 0; n < NS; ++n) sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
-#pragma unroll
       for (int k = 0; k < 4; ++k) {  // 32 rows
-        const bool ends = k == 3 || (k == 1 && group <= 64) || group == 32;  // a group
-        uint32_t scale[2];
-        if (ends) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) scale[q] = lds32(sb + (32 * k + 31) / group * 128 + q * 4 * block);
-        }
         uint32_t a[2][2][4];
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const uint4& v = w[k >> 1][q];
+            const uint4& v = w[o][k >> 1][q];
             widen_q(k & 1 ? (s ? v.w : v.z) : (s ? v.y : v.x), a[q][s]);
           }
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          if (!early) ldmatrix4(x[0][0], xa + n * (8 * pitch) + 64 * k);
-          const uint32_t(&f)[4] = early ? x[k][n] : x[0][0];
+          if (NT > 2) ldmatrix4(x[0][0][0], x_at(n0 + n, 128 * (i & 1) + 32 * k));
+          const uint32_t(&f)[4] = NT <= 2 ? x[o][k][n] : x[0][0][0];
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) mma(sum[q][n], a[q][s], f[2 * s], f[2 * s + 1]);
+            for (int q = 0; q < 2; ++q) {
+              if (s == 0 && k % per == 0)
+                mma_first(sum[q][n], a[q][s], f[2 * s], f[2 * s + 1]);
+              else
+                mma(sum[q][n], a[q][s], f[2 * s], f[2 * s + 1]);
+            }
         }
-        if (ends) {
+        if ((k + 1) % per == 0) {  // a group ends
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float lo = __uint_as_float(scale[q] << 16), hi = __uint_as_float(scale[q] & 0xffff0000u);
+            const float lo = __uint_as_float(scale[o][k][q] << 16), hi = __uint_as_float(scale[o][k][q] & 0xffff0000u);
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
               float(&to)[4] = acc[q][n0 + n];
@@ -468,7 +526,6 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
               to[1] = fmaf(lo, sum[q][n][1], to[1]);
               to[2] = fmaf(hi, sum[q][n][2], to[2]);
               to[3] = fmaf(hi, sum[q][n][3], to[3]);
-              sum[q][n][0] = sum[q][n][1] = sum[q][n][2] = sum[q][n][3] = 0.f;
             }
           }
         }
@@ -480,10 +537,10 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
 // `steps` steps of one unit from its step s on, then their sums out. PUT(half,
 // column of the half, row, two values: of this row of x and the next one).
 // `dry`: see products().
-template <int FMT, int NT, typename Put>
+template <int G, bool TILES, int NT, typename Put>
 __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int rows,
-                                             int group, int block, bool dry, Put put) {
-  constexpr int BK = step_rows(FMT);
+                                             bool dry, Put put) {
+  constexpr int BK = step_rows(G);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[2][NT][4];
 #pragma unroll
@@ -493,8 +550,8 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
 #pragma unroll 1
   for (; steps > 0; --steps, ++s) {
     if (!dry && !warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
-    const int blocks = FMT == MEP_W4 ? (K - int(s * BK) + kW4Rows - 1) / kW4Rows : 0;
-    stage_product<FMT, NT>(acc, r.stage0 + c.slot * r.stage_bytes, r, warp, blocks, group, block);
+    const int blocks = G != 0 ? (K - int(s * BK) + kW4Rows - 1) / kW4Rows : 0;
+    stage_product<G, TILES, NT>(acc, r.stage0 + c.slot * r.stage_bytes, r, warp, blocks, tile_rows(rows));
     __syncwarp();
     if (dry) continue;
     if (lane == 0) arrive(r.empty + 8 * c.slot);
@@ -509,7 +566,7 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float f = FMT == MEP_W4 ? kQ : 1.f;
+          const float f = G != 0 ? kQ : 1.f;
           put(q, 16 * warp + (lane >> 2) + 4 * i, row, f * acc[q][n][i], f * acc[q][n][i + 1]);
         }
     }
@@ -522,9 +579,9 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
 // for the first time comes from far away, at some 25 ns an instruction: with
 // `dry` the code is run through once, on whatever the first stage holds and to no
 // effect, while that stage's bytes are on their way.
-template <int FMT, int NTMAX, typename Put>
+template <int G, bool TILES, int NTMAX, typename Put>
 __device__ __forceinline__ void products(const Phase& p, int K, int planes, const Ring& r, Cursor& c,
-                                         const uint16_t* start, int group, int block, bool dry, int most, Put put) {
+                                         const uint16_t* start, bool dry, int most, Put put) {
 #pragma unroll 1
   while (true) {
     uint32_t at = 0;
@@ -533,20 +590,20 @@ __device__ __forceinline__ void products(const Phase& p, int K, int planes, cons
       at = r.step[c.slot];
       if (at == kEnd) break;
     }
-    const uint32_t u = p.by_ks(at), s = at - u * p.ks, run = run_at(p, at);
-    const uint32_t steps = dry ? 1 : min(min(p.ks - s, (run + 1) * p.run - at), p.total - at);
+    const uint32_t u = p.by_ks(at), s = at - u * p.ks, run = p.parts == 1 ? 0 : run_at(p, at);
+    const uint32_t steps = dry ? 1 : p.parts == 1 ? p.ks - s : min(p.ks - s, run_start(p, run + 1) - at);
     const uint32_t e = p.by_nb(u), j = u - e * p.nb, part = p.parts == 1 ? 0 : run - run_at(p, u * p.ks);
     const int first = start[e], rows = planes * (dry ? most : start[e + 1] - first);
     const auto f = [&](int q, int col, int row, float v0, float v1) { put(first, j, part, rows, q, col, row, v0, v1); };
     bool ok;
     if (rows <= 8)
-      ok = unit_product<FMT, 1>(steps, s, K, r, c, rows, group, block, dry, f);
+      ok = unit_product<G, TILES, 1>(steps, s, K, r, c, rows, dry, f);
     else if (rows <= 16)
-      ok = unit_product<FMT, 2>(steps, s, K, r, c, rows, group, block, dry, f);
+      ok = unit_product<G, TILES, 2>(steps, s, K, r, c, rows, dry, f);
     else if (NTMAX <= 4 || rows <= 32)
-      ok = unit_product<FMT, 4>(steps, s, K, r, c, rows, group, block, dry, f);
+      ok = unit_product<G, TILES, 4>(steps, s, K, r, c, rows, dry, f);
     else
-      ok = unit_product<FMT, NTMAX>(steps, s, K, r, c, rows, group, block, dry, f);
+      ok = unit_product<G, TILES, NTMAX>(steps, s, K, r, c, rows, dry, f);
     if (!ok) return;
     dry = false;
   }
@@ -555,11 +612,11 @@ __device__ __forceinline__ void products(const Phase& p, int K, int planes, cons
   c.next(r.stages);
 }
 
-// Stages for up to `rows` rows of x (as many as a unit's instantiation computes).
-template <int FMT> __device__ __forceinline__ void size_ring(Ring& r, uint32_t room, int rows, int block) {
-  const int n = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  r.x_at = FMT == MEP_BF16 ? kPanels * step_rows(FMT) * kPanelRow : kPanels * 2 * block;
-  r.stage_bytes = (r.x_at + n * (step_rows(FMT) * 2 + 16) + 1023) / 1024 * 1024;
+// Stages for up to `rows` rows of x. Tiles start on a swizzle's boundary.
+template <int G, bool TILES> __device__ __forceinline__ void size_ring(Ring& r, uint32_t room, int rows) {
+  r.x_at = G == 0 ? kPanels * step_rows(G) * kPanelRow : kPanels * 2 * w4_block_bytes(G > 0 ? G : 128);
+  if (TILES) r.x_at = (r.x_at + 1023) / 1024 * 1024;
+  r.stage_bytes = (r.x_at + tile_rows(rows) * (step_rows(G) * 2 + (TILES ? 0 : 16)) + 1023) / 1024 * 1024;
   r.stages = min(kMaxStages, int(room / r.stage_bytes));
 }
 
@@ -609,8 +666,9 @@ struct LayerArgs {
   const float* topk_w;
   const uint8_t *w1, *w2;
   int32_t* status;
-  int T, K, E, H, F, group;
+  int T, K, E, H, F;
   Shape s1, s2;
+  int counted;  // the counters may be in use
   Div by_k;
   uint32_t* counters;
   float *part1, *part2;
@@ -636,7 +694,7 @@ constexpr uint16_t kNone = 0xffff;
 // The experts in use in ascending order, each one's tokens in order, more than
 // kChunk of them in several entries; where each assignment went. What comes from
 // memory is asked for at the start, the barriers' words are set up meanwhile.
-__device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, char* scratch, const Lists& l) {
+__device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, char* scratch, const Lists& l, bool long_run) {
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
   uint32_t* e_at = reinterpret_cast<uint32_t*>(mask + a.E);  // entry and first row of an expert
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = kThreads, A = a.T * a.K;
@@ -688,7 +746,7 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
   }
   if (lane == 0 && warp < 2) {
     const bool run = h->go && !h->bad;
-    h->phase[warp] = make_phase(run ? all >> 16 : 0, warp == 0 ? a.s1 : a.s2);
+    h->phase[warp] = make_phase(run ? all >> 16 : 0, warp == 0 ? a.s1 : a.s2, long_run);
     if (warp == 0) {
       h->rows = run ? all & 0xffff : 0;
       l.start[all >> 16] = all & 0xffff;
@@ -711,12 +769,12 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
   __syncthreads();
 }
 
-template <int FMT> __device__ __forceinline__ Weights first_weights(const LayerArgs& a, const CUtensorMap* map) {
-  const long long m = FMT == MEP_W4 ? w4_matrix_bytes(a.H, a.F, a.group) : 0, q = FMT == MEP_W4 ? w4_panel_bytes(a.H, a.group) : 0;
+template <int G> __device__ __forceinline__ Weights first_weights(const LayerArgs& a, const CUtensorMap* map) {
+  const long long m = G != 0 ? w4_matrix_bytes(a.H, a.F, G) : 0, q = G != 0 ? w4_panel_bytes(a.H, G) : 0;
   return {map, a.w1, 2 * m, q, m, 2, a.F, a.F, true, a.H};
 }
-template <int FMT> __device__ __forceinline__ Weights second_weights(const LayerArgs& a, const CUtensorMap* map) {
-  const long long m = FMT == MEP_W4 ? w4_matrix_bytes(a.F, a.H, a.group) : 0, q = FMT == MEP_W4 ? w4_panel_bytes(a.F, a.group) : 0;
+template <int G> __device__ __forceinline__ Weights second_weights(const LayerArgs& a, const CUtensorMap* map) {
+  const long long m = G != 0 ? w4_matrix_bytes(a.F, a.H, G) : 0, q = G != 0 ? w4_panel_bytes(a.F, G) : 0;
   return {map, a.w2, m, q, 2 * q, 4, 2 * kW4Cols, a.H, false, a.F};
 }
 
@@ -801,7 +859,7 @@ __device__ __forceinline__ void combine(const LayerArgs& a, const Phase& p, cons
   }
 }
 
-template <int FMT>
+template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
     k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const LayerArgs a) {
   extern __shared__ __align__(1024) char smem[];
@@ -817,24 +875,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     l.row = l.token + A;
   }
   const uint32_t used = kHeadBytes + list_bytes(a.T, a.K, a.E);
-  const int block = FMT == MEP_W4 ? w4_block_bytes(a.group) : 0;
   Ring r;
-  make_list(a, r, h, smem + used, l);
+  make_list(a, r, h, smem + used, l, G != 0);
   const bool go = h->go && !h->bad;
   if (h->go && h->bad && threadIdx.x == 0) set_status(a.status, MEP_ERR_BAD_ROUTING);
   r.stage0 = smem_u32(smem + used);
   const int most = min(h->most, kChunk);
-  size_ring<FMT>(r, kSmem - used, 2 * most, block);
+  size_ring<G, false>(r, kSmem - used, 2 * most);
 
   const int warp = threadIdx.x >> 5;
   const uint32_t rows = h->rows;
   const Phase &p1 = h->phase[0], &p2 = h->phase[1];
-  const bool counted = p1.runs > gridDim.x || p2.runs > gridDim.x;  // the counters are in use: zero after a barrier
+  // How many barriers there are does not depend on what is read: every CTA comes
+  // to all of them, whatever another stream does to the status word meanwhile.
+  const bool counted = a.counted;
   Cursor c;
   if (warp == kWarps) {
-    Stream<FMT> t(r, l.expert, l.start, block);
+    Stream<G, false> t(r, l.expert, l.start);
     Cursor behind;
-    t.own(p1, first_weights<FMT>(a, &map1), {reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1});
+    t.own(p1, first_weights<G>(a, &map1), {nullptr, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1});
     t.ahead(c, true);
     if (counted) grid_barrier();
 #pragma unroll 1
@@ -842,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.feed(c, behind, phase == 1, a.counters + phase);
       if (phase == 0) {  // the ring fills while the activation is computed
         behind = c;
-        t.own(p2, second_weights<FMT>(a, &map2), {reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2});
+        t.own(p2, second_weights<G>(a, &map2), {nullptr, reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2});
         t.ahead(c, false);
         grid_barrier();
       }
@@ -860,8 +919,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!dry) {
         const Sums o = second ? Sums{a.part2, uint32_t(a.H), kUnit, kUnit / 2, a.H, -1}
                               : Sums{a.part1, 2u * a.F, kUnit / 2, a.F, a.F, 0};
-        products<FMT, kChunk / 4>(
-            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, a.group, block, !second, most,
+        products<G, false, kChunk / 4>(
+            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, !second, most,
             [&](int first, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
               const int n = j * o.unit + col, off = q * o.half;
               if (n + (off & o.counted) >= o.limit) return;
@@ -893,18 +952,25 @@ struct ProductArgs {
   const __nv_bfloat16* x;
   const uint8_t* w4;
   int32_t* status;
-  int T, K, N, group;
+  int T, K, N, y_type;
   Shape shape;
+  int whole;  // a run is a unit
   uint32_t* counter;
   __nv_bfloat16* padded;  // rows of x that are whole 16-byte vectors, where K is not a multiple of 8
   float* part;
   void* y;
 };
 
-template <int NTMAX, typename T>
-__global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a) {
+__device__ __forceinline__ void put_y(const ProductArgs& a, long long at, float v) {
+  if (a.y_type == MEP_BF16)
+    static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(a.y)[at] = v;
+}
+
+template <int G, int NTMAX>
+__global__ void __launch_bounds__(kThreads, 1) k_w4_product(const __grid_constant__ CUtensorMap map_x, const ProductArgs a) {
   extern __shared__ __align__(1024) char smem[];
-  constexpr int FMT = MEP_W4;
   Head* h = reinterpret_cast<Head*>(smem);
   uint16_t* start = reinterpret_cast<uint16_t*>(h + 1);  // one entry, all rows
   uint16_t* expert = start + 2;
@@ -921,13 +987,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a)
   }
   __syncthreads();
   const bool go = h->go;
-  const int block = w4_block_bytes(a.group);
   r.stage0 = smem_u32(smem + used);
-  size_ring<FMT>(r, kSmem - used, a.T, block);
-  const Phase p = make_phase(go ? 1 : 0, a.shape);
+  size_ring<G, true>(r, kSmem - used, a.T);
+  Phase p = make_phase(1, a.shape, true);
+  if (a.whole) whole_units(p);
   const bool pad = a.K % 8 != 0;
+  // as in k_layer: no barrier goes by the status word
+  const bool first_barrier = pad || p.runs > gridDim.x, joined = p.parts > 1;
+  if (!go) p.total = p.runs = 0;
   const int K8 = (a.K + 7) / 8 * 8;
-  const bool first_barrier = pad || p.runs > gridDim.x;
   const auto copy_rows = [&]() {  // to whole vectors
     for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < uint32_t(a.T * K8); i += gridDim.x * blockDim.x) {
       const uint32_t t = i / K8, k = i % K8;
@@ -937,11 +1005,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a)
   };
   Cursor c;
   if (producer) {
-    Stream<FMT> t(r, expert, start, block);
+    Stream<G, true> t(r, expert, start);
     const Cursor behind;
-    const long long panel = w4_panel_bytes(a.K, a.group);
-    t.own(p, {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K},
-          {reinterpret_cast<const char*>(pad ? a.padded : a.x), nullptr, 2LL * K8, K8, 1});
+    const long long panel = w4_panel_bytes(a.K, G);
+    t.own(p, {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K}, {&map_x, nullptr, nullptr, 0, K8, 1});
     t.ahead(c, !pad);
     if (pad) copy_rows();
     if (first_barrier) grid_barrier();
@@ -950,33 +1017,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a)
   } else {
     if (pad) copy_rows();
     if (first_barrier) grid_barrier();
-    products<FMT, NTMAX>(p, a.K, 1, r, c, start, a.group, block, true, a.T,
-                         [&](int, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
-                           const int n = j * kUnit + q * (kUnit / 2) + col;
-                           if (n >= a.N) return;
-                           if (p.parts == 1) {
-                             T* to = static_cast<T*>(a.y) + (long long)row * a.N + n;
-                             *to = from_f32<T>(v0);
-                             if (row + 1 < rows) to[a.N] = from_f32<T>(v1);
-                           } else {
-                             float* to = a.part + ((long long)row * p.parts + part) * a.N + n;
-                             *to = v0;
-                             if (row + 1 < rows) to[(long long)p.parts * a.N] = v1;
-                           }
-                         });
+    products<G, true, NTMAX>(p, a.K, 1, r, c, start, true, a.T,
+                             [&](int, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
+                               const int n = j * kUnit + q * (kUnit / 2) + col;
+                               if (n >= a.N) return;
+                               if (p.parts == 1) {
+                                 put_y(a, (long long)row * a.N + n, v0);
+                                 if (row + 1 < rows) put_y(a, (row + 1LL) * a.N + n, v1);
+                               } else {
+                                 float* to = a.part + ((long long)row * p.parts + part) * a.N + n;
+                                 *to = v0;
+                                 if (row + 1 < rows) to[(long long)p.parts * a.N] = v1;
+                               }
+                             });
   }
-  if (p.parts > 1) {
+  if (joined) {
     grid_barrier();
     if (go) {
-      const uint32_t n = uint32_t(a.T) * a.N;
+      const uint32_t quads = (a.N + 3) / 4, n = uint32_t(a.T) * quads;
+      const bool vec = a.N % 4 == 0;
 #pragma unroll 1
       for (Spread s = spread(kWarps + 1); s.i < n; s.i += s.step) {
-        const uint32_t t = s.i / a.N, col = s.i - t * a.N, parts = parts_in(p, col / kUnit);
+        const uint32_t t = s.i / quads, col = (s.i - t * quads) * 4, parts = parts_in(p, col / kUnit);
         const float* in = a.part + (long long)t * p.parts * a.N + col;
-        float v = 0.f;
+        float v[4] = {};
 #pragma unroll 4
-        for (uint32_t q = 0; q < parts; ++q, in += a.N) v += __ldcg(in);
-        static_cast<T*>(a.y)[s.i] = from_f32<T>(v);
+        for (uint32_t q = 0; q < parts; ++q, in += a.N) {
+          if (vec) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(in));
+            v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += int(col) + i < a.N ? __ldcg(in + i) : 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (int(col) + i < a.N) put_y(a, (long long)t * a.N + col + i, v[i]);
       }
     }
   }
@@ -985,10 +1062,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const ProductArgs a)
 
 // ---------------------------------------------------------------------------
 // host side
+int ctas() { return sm_count() < kMaxCtas ? sm_count() : kMaxCtas; }
+
 template <typename... KArgs, typename... Args>
 int launch_all(void (*kernel)(KArgs...), long long most, int threads, cudaStream_t st, const Args&... args) {
   if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmem)) return MEP_ERR_CUDA;
-  const int sms = sm_count() < kMaxCtas ? sm_count() : kMaxCtas;
+  const int sms = ctas();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(most < 1 ? 1 : most < sms ? most : sms));
   cfg.blockDim = dim3(threads);
@@ -1030,7 +1109,7 @@ bool make_map3(CUtensorMap* m, const void* p, long long E, long long K, long lon
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {cuuint64_t(N), cuuint64_t(K), cuuint64_t(E)};
   const cuuint64_t strides[2] = {cuuint64_t(N) * 2, cuuint64_t(N) * K * 2};
-  const cuuint32_t box[3] = {64, cuuint32_t(step_rows(MEP_BF16)), 1};
+  const cuuint32_t box[3] = {64, cuuint32_t(step_rows(0)), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1049,13 +1128,20 @@ bool layer_space(int T, int K, int E, long long H, long long F, int w_type, int 
       F % 8 != 0 || H > MEP_MAX_FEW_H || F > MEP_MAX_FEW_H / 2)
     return false;
   if (w_type != MEP_BF16 && (w_type != MEP_W4 || !w4_sizes_ok(H, F, group))) return false;
-  const int A = T * K, most = max_entries(T, K, E), bk = step_rows(w_type);
+  const int A = T * K, most = max_entries(T, K, E), bk = step_rows(w_type == MEP_W4 ? group : 0);
   s->part1 = part_bytes(most, K, T, A, ceil_div(F, kUnit / 2), ceil_div(H, bk), 2 * F);
   s->part2 = part_bytes(most, K, T, A, ceil_div(H, kUnit), ceil_div(F, bk), H);
   s->act = align256(size_t(A) * F * 4);
   return true;
 }
 
+// Whether a product's runs are its units: where that leaves no more than a fifth
+// of the SMs idle in the last round, for partial sums cost a write and a read of
+// the output and a barrier ([64, 2048] x [2048, 65536]: DETAIL).
+bool whole_product(long long N) {
+  const long long units = ceil_div(N, kUnit), rounds = ceil_div(units, kMaxCtas);
+  return rounds * kMaxCtas * 4 <= units * 5;
+}
 struct ProductSpace {
   size_t padded, part;
   size_t all() const { return kCounters + padded + part; }
@@ -1063,19 +1149,19 @@ struct ProductSpace {
 bool product_space(int T, long long K, long long N, int group, ProductSpace* s) {
   if (T < 0 || T > MEP_MAX_FEW || !w4_sizes_ok(K, N, group)) return false;
   s->padded = K % 8 == 0 ? 0 : align256(size_t(T) * ceil_div(K, 8) * 16);
-  s->part = T == 0 ? 0 : part_bytes(1, 1, T, T, ceil_div(N, kUnit), ceil_div(K, step_rows(MEP_W4)), N);
+  s->part = T == 0 || whole_product(N) ? 0 : part_bytes(1, 1, T, T, ceil_div(N, kUnit), ceil_div(K, step_rows(128)), N);
   return true;
 }
 
-template <int FMT>
+template <int G>
 int launch_layer(const CUtensorMap& m1, const CUtensorMap& m2, const LayerArgs& a, cudaStream_t st) {
-  const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(FMT);
+  const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(G);
   const long long n1 = experts * ceil_div(a.F, kUnit / 2) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
-  return launch_all(k_layer<FMT>, n1 > n2 ? n1 : n2, kThreads, st, m1, m2, a);
+  return launch_all(k_layer<G>, n1 > n2 ? n1 : n2, kThreads, st, m1, m2, a);
 }
-template <typename T> int launch_product(const ProductArgs& a, cudaStream_t st) {
-  const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(MEP_W4));
-  return a.T <= 32 ? launch_all(k_w4_product<4, T>, n, kThreads, st, a) : launch_all(k_w4_product<8, T>, n, kThreads, st, a);
+template <int G> int launch_product(const CUtensorMap& x, const ProductArgs& a, cudaStream_t st) {
+  const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(G));
+  return a.T <= 32 ? launch_all(k_w4_product<G, 4>, n, kThreads, st, x, a) : launch_all(k_w4_product<G, 8>, n, kThreads, st, x, a);
 }
 
 }  // namespace
@@ -1100,11 +1186,24 @@ extern "C" int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* sta
       reinterpret_cast<uintptr_t>(y) % (y_type == MEP_BF16 ? 2 : 4) != 0)
     return MEP_ERR_INVALID_ARG;
   char* p = static_cast<char*>(ws) + kCounters;
-  const ProductArgs a = {reinterpret_cast<const __nv_bfloat16*>(x), w4, status, T, int(K), int(N), group,
-                         shape_of(ceil_div(K, step_rows(MEP_W4)), ceil_div(N, kUnit)), static_cast<uint32_t*>(ws),
+  const ProductArgs a = {reinterpret_cast<const __nv_bfloat16*>(x), w4, status, T, int(K), int(N), y_type,
+                         shape_of(ceil_div(K, step_rows(128)), ceil_div(N, kUnit)), whole_product(N), static_cast<uint32_t*>(ws),
                          reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<float*>(p + s.padded), y};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return y_type == MEP_BF16 ? launch_product<__nv_bfloat16>(a, st) : launch_product<float>(a, st);
+  // x as tiles of all its rows and 64 columns, 128-byte swizzle; beyond its edges zeros
+  CUtensorMap map = {};
+  EncodeTiledFn fn = encode_fn();
+  const long long K8 = ceil_div(K, 8) * 8;
+  const cuuint64_t dims[2] = {cuuint64_t(K8), cuuint64_t(T)}, strides[1] = {cuuint64_t(K8) * 2};
+  const cuuint32_t box[2] = {64, T <= 8 ? 8u : T <= 16 ? 16u : T <= 32 ? 32u : 64u}, estr[2] = {1, 1};
+  void* from = K % 8 == 0 ? const_cast<mep_bf16*>(x) : static_cast<void*>(p);
+  if (fn == nullptr || fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, from, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MEP_ERR_CUDA;
+  return group == 32   ? launch_product<32>(map, a, st)
+         : group == 64 ? launch_product<64>(map, a, st)
+                       : launch_product<128>(map, a, st);
 }
 
 extern "C" int mep_expert_layer_workspace_bytes(int T, int K, int E, int64_t H, int64_t F, int w_type, int group,
@@ -1128,7 +1227,9 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
       reinterpret_cast<uintptr_t>(topk_idx) % 4 != 0 || reinterpret_cast<uintptr_t>(topk_w) % 4 != 0)
     return MEP_ERR_INVALID_ARG;
   char* p = static_cast<char*>(ws) + kCounters;
-  const int bk = step_rows(w_type);
+  const int bk = step_rows(w_type == MEP_W4 ? group : 0);
+  const long long steps1 = ceil_div(H, bk) * ceil_div(F, kUnit / 2), steps2 = ceil_div(F, bk) * ceil_div(H, kUnit);
+  const int counted = max_entries(T, K, E) * (steps1 > steps2 ? steps1 : steps2) > kOneRun * (long long)ctas();
   const LayerArgs a = {reinterpret_cast<const __nv_bfloat16*>(x),
                        topk_idx,
                        topk_w,
@@ -1140,9 +1241,9 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
                        E,
                        int(H),
                        int(F),
-                       group,
                        shape_of(ceil_div(H, bk), ceil_div(F, kUnit / 2)),
                        shape_of(ceil_div(F, bk), ceil_div(H, kUnit)),
+                       counted,
                        div_of(K),
                        static_cast<uint32_t*>(ws),
                        reinterpret_cast<float*>(p),
@@ -1151,8 +1252,11 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
                        reinterpret_cast<__nv_bfloat16*>(out)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   CUtensorMap m1 = {}, m2 = {};
-  if (w_type == MEP_W4) return launch_layer<MEP_W4>(m1, m2, a, st);
+  if (w_type == MEP_W4)
+    return group == 32   ? launch_layer<32>(m1, m2, a, st)
+           : group == 64 ? launch_layer<64>(m1, m2, a, st)
+                         : launch_layer<128>(m1, m2, a, st);
   if (!on_current_device(w1) || !on_current_device(w2)) return MEP_ERR_INVALID_ARG;
   if (!make_map3(&m1, w1, E, H, 2 * F) || !make_map3(&m2, w2, E, F, H)) return MEP_ERR_CUDA;
-  return launch_layer<MEP_BF16>(m1, m2, a, st);
+  return launch_layer<0>(m1, m2, a, st);
 }

@@ -25,7 +25,7 @@ constexpr int kW4Rows = 128, kW4Cols = 64;          // of a block
 constexpr int kW4Pairs = kW4Rows * kW4Cols / 2;     // bytes of pairs
 constexpr float kW4Top = 7.f;                       // largest |q|
 
-__host__ __device__ __forceinline__ int w4_block_bytes(int group) {
+__host__ __device__ constexpr int w4_block_bytes(int group) {
   return kW4Pairs + kW4Rows / group * kW4Cols * 2;
 }
 __host__ __device__ __forceinline__ long long w4_panel_bytes(long long K, int group) {
