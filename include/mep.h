@@ -582,8 +582,8 @@ MEP_API int mep_route_backward(const float* dtopk_w, const float* topk_w, const 
  *   group   32, 64 or 128
  *   w4      uint8 [M, parts, mep_w4_bytes(K, N / parts, group)]
  * mep_w4_load rounds q * s once to bf16; fp32 holds it exactly.
- * Input and output must not overlap. 1 <= K, N / parts <= MEP_MAX_W4,
- * M * parts < 2^31.
+ * Input and output must not overlap. 1 <= K, N / parts <= MEP_MAX_W4, fewer
+ * than 2^31 blocks in all.
  * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
  */
 MEP_API int mep_w4_bytes(int64_t K, int64_t N, int group, size_t* bytes);

@@ -2,9 +2,16 @@
 // gradient (mep_route_backward).
 //
 // A warp takes a token's row. Forward, the logits become whole numbers of the
-// same order; K times the warp takes the largest one that is left (a maximum
-// over the lanes, then the lowest index that has it). Backward, the row is
-// zeros but for K places.
+// same order, and K times the warp takes the largest that is left: a maximum over
+// the lanes, a vote for whose it is. Up to 256 experts a lane has its values in
+// registers and knows the best two of them with their places, so that taking one
+// costs a dozen instructions; only a lane that loses both looks through its
+// values again (one row in five, of 256 normal logits and K = 8). What is taken
+// is told by its order, not marked: values behind the last one taken, by size
+// and place. What bounds it is what a warp has to issue. More experts: the orders
+// lie in shared memory and every lane looks through its own each time.
+// Backward, the row is zeros but for K places: built in shared memory, which
+// stays zero otherwise, and written out in vectors; bound by those bytes.
 
 #include <math.h>
 
@@ -20,6 +27,93 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
   if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Weights of the chosen: lane and lane + 32 have number lane and lane + 32, their
+// logits l.
+__device__ __forceinline__ void put_row(const float (&l)[2], const int (&at)[2], int K, int skip_masked, int32_t* idx,
+                                        float* w) {
+  const int lane = threadIdx.x & 31;
+  float m = fmaxf(l[0], l[1]);
+  bool nan = isnan(l[0]) || isnan(l[1]);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
+  nan = __any_sync(MEP_FULL_MASK, nan);
+  float ex[2], sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    ex[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+    sum += ex[i];
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, d);
+  if (nan) sum = __uint_as_float(0x7fc00000u);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = 32 * i + lane;
+    if (k < K) {
+      idx[k] = skip_masked && l[i] == -INFINITY ? -1 : at[i];
+      w[k] = sum == 0.f ? 0.f : ex[i] / sum;
+    }
+  }
+}
+
+// Up to 32 NV experts: expert lane + 32 i is value i of the lane.
+template <typename T, int NV>
+__global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ logits, const float* __restrict__ bias,
+                                                        long long N, int E, int K, int skip_masked,
+                                                        int32_t* __restrict__ idx, float* __restrict__ w) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (long long row = (long long)blockIdx.x * kWarps + warp; row < N; row += (long long)gridDim.x * kWarps) {
+    const T* in = logits + row * E;
+    uint32_t key[NV];  // 0: no expert
+    // the best two and their places: larger first, equal ones in order of place
+    uint32_t m1 = 0, m2 = 0;
+    int i1 = 0, i2 = 0, left = 2;
+    const auto offer = [&](uint32_t k, int i) {
+      const bool first = k > m1, second = k > m2;
+      const uint32_t m = first ? m1 : k;
+      const int at = first ? i1 : i;
+      m2 = second ? m : m2, i2 = second ? at : i2;
+      m1 = first ? k : m1, i1 = first ? i : i1;
+    };
+    float v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < E ? to_f32(in[lane + 32 * i]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < E ? order_of(bias == nullptr ? v[i] : v[i] + bias[e]) : 0u;
+      offer(key[i], i);
+    }
+    int mine[2] = {0, 0};  // chosen number lane, and lane + 32
+#pragma unroll 1
+    for (int k = 0; k < K; ++k) {
+      const uint32_t top = __reduce_max_sync(MEP_FULL_MASK, m1);
+      const unsigned who = __ballot_sync(MEP_FULL_MASK, m1 == top);
+      int at = 32 * i1 + lane;
+      if (who & (who - 1))  // several lanes: the lowest place
+        at = __reduce_min_sync(MEP_FULL_MASK, m1 == top ? at : 0x7fffffff);
+      else
+        at = __shfl_sync(MEP_FULL_MASK, at, __ffs(who) - 1);
+      if ((k & 31) == lane) mine[k >> 5] = at;
+      if ((at & 31) == lane) {
+        const int last = i1;
+        m1 = m2, i1 = i2, m2 = 0;
+        if (--left == 0) {
+          m1 = 0, left = 2;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) offer(key[i] < top || (key[i] == top && i > last) ? key[i] : 0u, i);
+        }
+      }
+    }
+    float l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l[i] = 32 * i + lane < K ? to_f32(in[mine[i]]) : -INFINITY;
+    put_row(l, mine, K, skip_masked, idx + row * K, w + row * K);
+  }
 }
 
 template <typename T>
@@ -50,51 +144,27 @@ __global__ void __launch_bounds__(kThreads) k_route(const T* __restrict__ logits
       if ((k & 31) == lane) mine[k >> 5] = at;
       __syncwarp();
     }
-    float l[2], m = -INFINITY;
-    bool nan = false;
+    float l[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] = 32 * i + lane < K ? to_f32(in[mine[i]]) : -INFINITY;
-      nan |= isnan(l[i]);
-      m = fmaxf(m, l[i]);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
-    nan = __any_sync(MEP_FULL_MASK, nan);
-    float ex[2], sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ex[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-      sum += ex[i];
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, d);
-    if (nan) sum = __uint_as_float(0x7fc00000u);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int k = 32 * i + lane;
-      if (k < K) {
-        idx[row * K + k] = skip_masked && l[i] == -INFINITY ? -1 : mine[i];
-        w[row * K + k] = sum == 0.f ? 0.f : ex[i] / sum;
-      }
-    }
+    for (int i = 0; i < 2; ++i) l[i] = 32 * i + lane < K ? to_f32(in[mine[i]]) : -INFINITY;
+    put_row(l, mine, K, skip_masked, idx + row * K, w + row * K);
     __syncwarp();
   }
 }
 
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_route_backward(const float* __restrict__ dw, const float* __restrict__ w,
                                                              const int32_t* __restrict__ idx, int32_t* status,
                                                              long long N, int E, int K, T* __restrict__ dlogits) {
-  extern __shared__ float s_rows[];
+  extern __shared__ __align__(16) float s_rows[];
   pdl_launch_dependents();
   pdl_wait();
   if (read_status(status) != 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* d = s_rows + warp * E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pitch = (E + 7) & ~7;
+  float* d = s_rows + warp * pitch;
+  for (int e = lane; e < pitch; e += 32) d[e] = 0.f;
   bool bad = false;
   for (long long row = (long long)blockIdx.x * kWarps + warp; row < N; row += (long long)gridDim.x * kWarps) {
-    for (int e = lane; e < E; e += 32) d[e] = 0.f;
     float wk[2], dk[2], sum = 0.f;
     int at[2];
 #pragma unroll
@@ -103,18 +173,44 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const float* __rest
       wk[i] = k < K ? w[row * K + k] : 0.f;
       dk[i] = k < K ? dw[row * K + k] : 0.f;
       at[i] = k < K ? idx[row * K + k] : -1;
-      bad |= at[i] < -1 || at[i] >= E;
+      if (at[i] < -1 || at[i] >= E) bad = true, at[i] = -1;
+      if (at[i] < 0) at[i] = -1;
       sum += k < K ? wk[i] * dk[i] : 0.f;
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, s);
+    // an expert that stands twice gets both, one after another
+    const unsigned same = __match_any_sync(MEP_FULL_MASK, at[0]);
+    const bool once = at[0] < 0 || (same & (same - 1)) == 0;
     __syncwarp();
-    for (int k = 0; k < K; ++k) {  // one after another: an expert that stands twice gets both, in order
-      const float v = wk[k >> 5] * (dk[k >> 5] - sum);
-      if ((k & 31) == lane && at[k >> 5] >= 0 && at[k >> 5] < E) d[at[k >> 5]] += v;
+    if (K <= 32 && __all_sync(MEP_FULL_MASK, once)) {
+      if (at[0] >= 0) d[at[0]] = wk[0] * (dk[0] - sum);
       __syncwarp();
+    } else {
+      for (int k = 0; k < K; ++k) {
+        const int i = k >> 5;
+        if ((k & 31) == lane && at[i] >= 0) d[at[i]] += wk[i] * (dk[i] - sum);
+        __syncwarp();
+      }
     }
-    for (int e = lane; e < E; e += 32) dlogits[row * E + e] = from_f32<T>(d[e]);
+    T* out = dlogits + row * E;
+    if (VEC) {
+      for (int e = 4 * lane; e < E; e += 128) {
+        const float4 v = *reinterpret_cast<const float4*>(d + e);
+        if (sizeof(T) == 4) {
+          __stcs(reinterpret_cast<float4*>(out + e), v);
+        } else {
+          __nv_bfloat162 p[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
+          __stcs(reinterpret_cast<uint2*>(out + e), *reinterpret_cast<const uint2*>(p));
+        }
+      }
+    } else {
+      for (int e = lane; e < E; e += 32) out[e] = from_f32<T>(d[e]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (at[i] >= 0) d[at[i]] = 0.f;
     __syncwarp();
   }
   if (bad) set_status(status, MEP_ERR_BAD_ROUTING);
@@ -127,14 +223,31 @@ bool sizes_ok(int64_t N, int E, int K, int type) {
 bool on(const void* p, unsigned size) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % size == 0; }
 
 template <typename Kernel, typename... Args>
-int launch_rows(Kernel kernel, int64_t N, int E, cudaStream_t st, Args... args) {
-  const int smem = kWarps * E * 4;
+int launch_rows(Kernel kernel, int64_t N, int smem, cudaStream_t st, Args... args) {
   if (set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem)) return MEP_ERR_CUDA;
   const long long blocks = (N + kWarps - 1) / kWarps, most = 16LL * sm_count();
   return launch_pdl(kernel, dim3(unsigned(blocks < most ? blocks : most)), dim3(kThreads), smem, st, args...) ==
                  cudaSuccess
              ? MEP_OK
              : MEP_ERR_CUDA;
+}
+template <typename T>
+int route(const T* logits, const float* bias, int64_t N, int E, int K, int skip_masked, int32_t* idx, float* w,
+          cudaStream_t st) {
+  const auto few = [&](auto kernel) { return launch_rows(kernel, N, 0, st, logits, bias, N, E, K, skip_masked, idx, w); };
+  if (E <= 32) return few(k_route_few<T, 1>);
+  if (E <= 64) return few(k_route_few<T, 2>);
+  if (E <= 128) return few(k_route_few<T, 4>);
+  if (E <= 256) return few(k_route_few<T, 8>);
+  return launch_rows(k_route<T>, N, kWarps * E * 4, st, logits, bias, N, E, K, skip_masked, idx, w);
+}
+template <typename T>
+int route_backward(const float* dw, const float* w, const int32_t* idx, int32_t* status, int64_t N, int E, int K, T* d,
+                   cudaStream_t st) {
+  const int smem = kWarps * ((E + 7) & ~7) * 4;
+  const bool vec = E % 4 == 0 && reinterpret_cast<uintptr_t>(d) % (4 * sizeof(T)) == 0;
+  return vec ? launch_rows(k_route_backward<T, true>, N, smem, st, dw, w, idx, status, N, E, K, d)
+             : launch_rows(k_route_backward<T, false>, N, smem, st, dw, w, idx, status, N, E, K, d);
 }
 
 }  // namespace
@@ -149,10 +262,9 @@ extern "C" int mep_route(const void* logits, int type, const float* bias, int64_
   if (!on(logits, type == MEP_BF16 ? 2 : 4) || (bias != nullptr && !on(bias, 4)) || !on(topk_idx, 4) || !on(topk_w, 4))
     return MEP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return type == MEP_BF16 ? launch_rows(k_route<__nv_bfloat16>, N, E, st, static_cast<const __nv_bfloat16*>(logits),
-                                        bias, N, E, K, skip_masked, topk_idx, topk_w)
-                          : launch_rows(k_route<float>, N, E, st, static_cast<const float*>(logits), bias, N, E, K,
-                                        skip_masked, topk_idx, topk_w);
+  return type == MEP_BF16
+             ? route(static_cast<const __nv_bfloat16*>(logits), bias, N, E, K, skip_masked, topk_idx, topk_w, st)
+             : route(static_cast<const float*>(logits), bias, N, E, K, skip_masked, topk_idx, topk_w, st);
 }
 
 extern "C" int mep_route_backward(const float* dtopk_w, const float* topk_w, const int32_t* topk_idx, int32_t* status,
@@ -162,8 +274,6 @@ extern "C" int mep_route_backward(const float* dtopk_w, const float* topk_w, con
   if (!on(dtopk_w, 4) || !on(topk_w, 4) || !on(topk_idx, 4) || !on(dlogits, type == MEP_BF16 ? 2 : 4))
     return MEP_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return type == MEP_BF16 ? launch_rows(k_route_backward<__nv_bfloat16>, N, E, st, dtopk_w, topk_w, topk_idx, status, N,
-                                        E, K, static_cast<__nv_bfloat16*>(dlogits))
-                          : launch_rows(k_route_backward<float>, N, E, st, dtopk_w, topk_w, topk_idx, status, N, E, K,
-                                        static_cast<float*>(dlogits));
+  return type == MEP_BF16 ? route_backward(dtopk_w, topk_w, topk_idx, status, N, E, K, static_cast<__nv_bfloat16*>(dlogits), st)
+                          : route_backward(dtopk_w, topk_w, topk_idx, status, N, E, K, static_cast<float*>(dlogits), st);
 }

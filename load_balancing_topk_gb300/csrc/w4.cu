@@ -1,10 +1,17 @@
 // w4.cu -- weight matrices to 4 bits and back (mep_w4_save, mep_w4_load).
 //
-// A warp holds 16 columns of a block, a lane columns g and g + 8 at the rows
-// whose pairs it writes (w4.cuh): 32 rows, of which every group has its share
-// in each of the four lanes t, so that a group's largest magnitude is two
-// shuffles away. q = w / s is a division, as the format is defined by it; the
-// scale itself is a product by fp32's 1/7.
+// One pass over memory, a CTA a block of 128 rows and 64 columns, which goes
+// through shared memory: rows outside in 16-byte vectors, inside the 32 rows of
+// two columns that a lane's pairs are of (w4.cuh). A warp holds 16 columns; a
+// group has its share in each of the four lanes t, so that its largest magnitude
+// is two shuffles away. Rows that do not start on 16-byte boundaries are read and
+// written element by element, coalesced over a row's 64 columns.
+// q = w / s is a division, as the format is defined by it. From bf16 it is a
+// product by 1 / s and a correction by the remainder, which two fused
+// multiply-adds give: the quotient of two numbers of eight bits is 2^-9 or more
+// from every half step unless it is one, and one it meets exactly. (Scales below
+// 2^-100, whose reciprocal leaves fp32, divide.) Adding 1.5 * 2^23 + 8 rounds to
+// a whole number, ties to even, and leaves q + 8 in the low bits.
 
 #include "ckpt.cuh"
 #include "w4.cuh"
@@ -22,31 +29,78 @@ struct Matrices {
 
 // Block number -> where its values lie: part p of matrix m, first row and column.
 struct At {
-  long long base, k0, n0, ld;  // element of (row 0, column 0) of the part; row pitch
+  long long base;  // element of the block's first row and column
+  long long ld;    // row pitch
+  int rows, cols;  // that there are
 };
-__device__ __forceinline__ At at_block(const Matrices& s, long long b) {
-  const long long kb = b % s.kb, panel = b / s.kb % s.panels, mp = b / s.kb / s.panels;
-  const long long m = mp / s.parts, p = mp % s.parts;
+__device__ __forceinline__ At at_block(const Matrices& s, uint32_t b) {
+  const uint32_t panel_all = b / uint32_t(s.kb), kb = b - panel_all * s.kb;
+  const uint32_t mp = panel_all / uint32_t(s.panels), panel = panel_all - mp * uint32_t(s.panels);
+  const uint32_t m = mp / uint32_t(s.parts), p = mp - m * s.parts;
   At a;
   a.ld = s.N * s.parts;
-  a.base = m * s.K * a.ld + p * s.N;
-  a.k0 = kb * kW4Rows;
-  a.n0 = panel * kW4Cols;
+  const long long k0 = (long long)kb * kW4Rows, n0 = (long long)panel * kW4Cols;
+  a.base = (m * s.K + k0) * a.ld + p * s.N + n0;
+  a.rows = int(min((long long)kW4Rows, s.K - k0)), a.cols = int(min((long long)kW4Cols, s.N - n0));
   return a;
 }
+// A block's values in shared memory: a row's pitch in elements, which puts the
+// four rows and eight columns of a warp's access into different banks.
+template <typename T> constexpr int kPitch = sizeof(T) == 2 ? 72 : 68;
 
-template <typename T>
+// A block's rows into shared memory, zeros where there are none.
+template <typename T, bool VEC> __device__ __forceinline__ void rows_in(const T* __restrict__ w, const At& a, T* tile) {
+  constexpr int V = VEC ? 16 / sizeof(T) : 1, per_row = kW4Cols / V;
+  if (VEC) {
+    uint4 v[kW4Rows * per_row / kThreads];
+#pragma unroll
+    for (int i = 0; i < kW4Rows * per_row / kThreads; ++i) {
+      const int q = i * kThreads + threadIdx.x, r = q / per_row, c = q % per_row * V;
+      v[i] = r < a.rows && c < a.cols ? __ldg(reinterpret_cast<const uint4*>(w + a.base + r * a.ld + c)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kW4Rows * per_row / kThreads; ++i) {
+      const int q = i * kThreads + threadIdx.x;
+      *reinterpret_cast<uint4*>(tile + q / per_row * kPitch<T> + q % per_row * V) = v[i];
+    }
+  } else {
+#pragma unroll 16
+    for (int q = threadIdx.x; q < kW4Rows * kW4Cols; q += kThreads) {
+      const int r = q / kW4Cols, c = q % kW4Cols;
+      tile[r * kPitch<T> + c] = r < a.rows && c < a.cols ? w[a.base + r * a.ld + c] : from_f32<T>(0.f);
+    }
+  }
+}
+template <typename T, bool VEC> __device__ __forceinline__ void rows_out(const T* tile, const At& a, T* __restrict__ w) {
+  constexpr int V = VEC ? 16 / sizeof(T) : 1, per_row = kW4Cols / V;
+#pragma unroll 8
+  for (int q = threadIdx.x; q < kW4Rows * per_row; q += kThreads) {
+    const int r = q / per_row, c = q % per_row * V;
+    if (r < a.rows && c < a.cols) {
+      if (VEC)
+        __stcs(reinterpret_cast<uint4*>(w + a.base + r * a.ld + c), *reinterpret_cast<const uint4*>(tile + r * kPitch<T> + c));
+      else
+        w[a.base + r * a.ld + c] = tile[r * kPitch<T> + c];
+    }
+  }
+}
+// Row of the block that pair (i, e) of word j of half h has in lane t.
+__device__ __forceinline__ constexpr int row_of(int h, int j, int r, int t) { return 64 * h + 16 * j + 8 * (r & 1) + 2 * t + (r >> 1); }
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, Matrices s, int group,
                                                       uint8_t* __restrict__ w4) {
+  __shared__ __align__(16) T tile[kW4Rows * kPitch<T>];
   pdl_launch_dependents();
   pdl_wait();
   const At a = at_block(s, blockIdx.x);
+  rows_in<T, VEC>(w, a, tile);
+  __syncthreads();
   const int c = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   uint8_t* out = w4 + (long long)blockIdx.x * w4_block_bytes(group);
-  float v[2][4][4][2];  // h, j, (i, e), l
-  float top[4][2];      // of 32 rows: h, j / 2
-#pragma unroll
-  for (int q = 0; q < 4; ++q) top[q][0] = top[q][1] = 0.f;
+  const T* mine = tile + 16 * c + g;
+  // the larger magnitude, as bits: an infinity and then a NaN above all numbers
+  uint32_t top[4][2] = {};  // of 32 rows
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -55,29 +109,18 @@ __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, M
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
-          const long long k = a.k0 + 64 * h + 16 * j + 8 * (r & 1) + 2 * t + (r >> 1);
-          const long long n = a.n0 + 16 * c + 8 * l + g;
-          const float x = k < s.K && n < s.N ? to_f32(w[a.base + k * a.ld + n]) : 0.f;
-          v[h][j][r][l] = x;
-          float& m = top[2 * h + j / 2][l];
-          // the larger magnitude, as bits: an infinity and then a NaN above all numbers
-          m = __uint_as_float(max(__float_as_uint(m), __float_as_uint(x) & 0x7fffffffu));
+          const float x = to_f32(mine[row_of(h, j, r, t) * kPitch<T> + 8 * l]);
+          top[2 * h + j / 2][l] = max(top[2 * h + j / 2][l], __float_as_uint(x) & 0x7fffffffu);
         }
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int l = 0; l < 2; ++l) {
-      uint32_t m = __float_as_uint(top[q][l]);
-      m = max(m, __shfl_xor_sync(MEP_FULL_MASK, m, 1));
-      m = max(m, __shfl_xor_sync(MEP_FULL_MASK, m, 2));
-      top[q][l] = __uint_as_float(m);
-    }
   float scale[4][2];
 #pragma unroll
   for (int l = 0; l < 2; ++l) {
     uint32_t m[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) m[q] = __float_as_uint(top[q][l]);
+    for (int q = 0; q < 4; ++q) {
+      m[q] = max(top[q][l], __shfl_xor_sync(MEP_FULL_MASK, top[q][l], 1));
+      m[q] = max(m[q], __shfl_xor_sync(MEP_FULL_MASK, m[q], 2));
+    }
     if (group >= 64) m[0] = m[1] = max(m[0], m[1]), m[2] = m[3] = max(m[2], m[3]);
     if (group >= 128) m[0] = m[1] = m[2] = m[3] = max(m[0], m[2]);
 #pragma unroll
@@ -85,6 +128,17 @@ __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, M
       scale[q][l] = m[q] >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
                                         : __bfloat162float(__float2bfloat16_rn(__uint_as_float(m[q]) * (1.f / kW4Top)));
   }
+  constexpr float kShift = 12582912.f + 8.f;
+  float inv[4][2];
+  bool divide = sizeof(T) == 4;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      // a scale of zero or NaN: every q is 0
+      inv[q][l] = scale[q][l] > 0.f ? 1.f / scale[q][l] : 0.f;
+      divide |= scale[q][l] > 0.f && scale[q][l] < 0x1p-100f;
+    }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     uint32_t word[4];
@@ -95,9 +149,17 @@ __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, M
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
-          const float sc = scale[2 * h + j / 2][l];
-          const float q = sc > 0.f ? rintf(v[h][j][r][l] / sc) : 0.f;
-          word[j] |= (uint32_t)(int(fminf(fmaxf(q, -kW4Top), kW4Top)) + 8) << (8 * r + 4 * l);
+          const float sc = scale[2 * h + j / 2][l], in = inv[2 * h + j / 2][l];
+          const float x = to_f32(mine[row_of(h, j, r, t) * kPitch<T> + 8 * l]);
+          float q;
+          if (divide) {
+            q = in > 0.f ? x / sc : 0.f;
+          } else {
+            q = in > 0.f ? x * in : 0.f;
+            q = in > 0.f ? fmaf(fmaf(-q, sc, x), in, q) : 0.f;
+          }
+          const uint32_t bits = __float_as_uint(fminf(fmaxf(q, -kW4Top), kW4Top) + kShift) & 15u;
+          word[j] |= bits << (8 * r + 4 * l);
         }
     }
     reinterpret_cast<uint4*>(out)[((h * 4 + c) * 8 + g) * 4 + t] = make_uint4(word[0], word[1], word[2], word[3]);
@@ -111,33 +173,40 @@ __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, M
   }
 }
 
-template <typename T>
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_w4_load(const uint8_t* __restrict__ w4, Matrices s, int group,
                                                       T* __restrict__ w) {
+  __shared__ __align__(16) T tile[kW4Rows * kPitch<T>];
   pdl_launch_dependents();
   pdl_wait();
   const At a = at_block(s, blockIdx.x);
   const int c = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const uint8_t* in = w4 + (long long)blockIdx.x * w4_block_bytes(group);
+  const __nv_bfloat162* scales = reinterpret_cast<const __nv_bfloat162*>(in + kW4Pairs) + c * 8 + g;
+  T* mine = tile + 16 * c + g;
+  uint4 pairs[2];
+  __nv_bfloat162 sc[4];  // of 32 rows
+#pragma unroll
+  for (int h = 0; h < 2; ++h) pairs[h] = __ldcs(reinterpret_cast<const uint4*>(in) + ((h * 4 + c) * 8 + g) * 4 + t);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sc[q] = scales[(group == 32 ? q : group == 64 ? q / 2 : 0) * 32];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 q4 = reinterpret_cast<const uint4*>(in)[((h * 4 + c) * 8 + g) * 4 + t];
-    const uint32_t word[4] = {q4.x, q4.y, q4.z, q4.w};
+    const uint32_t word[4] = {pairs[h].x, pairs[h].y, pairs[h].z, pairs[h].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 sc =
-          reinterpret_cast<const __nv_bfloat162*>(in + kW4Pairs)[(64 * h + 16 * j) / group * 32 + c * 8 + g];
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int l = 0; l < 2; ++l) {
-          const long long k = a.k0 + 64 * h + 16 * j + 8 * (r & 1) + 2 * t + (r >> 1);
-          const long long n = a.n0 + 16 * c + 8 * l + g;
-          const float q = float(int(word[j] >> (8 * r + 4 * l) & 15u) - 8);
-          if (k < s.K && n < s.N) w[a.base + k * a.ld + n] = from_f32<T>(q * __bfloat162float(l ? sc.y : sc.x));
+          // q + 8 under 2^23, less 2^23 + 8
+          const float q = __uint_as_float(((word[j] >> (8 * r + 4 * l)) & 15u) | 0x4b000000u) - 8388616.f;
+          const __nv_bfloat162 p = sc[2 * h + j / 2];
+          mine[row_of(h, j, r, t) * kPitch<T> + 8 * l] = from_f32<T>(q * __bfloat162float(l ? p.y : p.x));
         }
-    }
   }
+  __syncthreads();
+  rows_out<T, VEC>(tile, a, w);
 }
 
 int w4_check(const void* w, int type, int64_t M, int64_t K, int64_t N, int parts, int group, const void* w4,
@@ -148,7 +217,7 @@ int w4_check(const void* w, int type, int64_t M, int64_t K, int64_t N, int parts
   if (M > 0x7fffffffLL || M * parts > 0x7fffffffLL) return MEP_ERR_INVALID_ARG;
   s->K = K, s->N = N / parts, s->parts = parts;
   s->kb = int((K + kW4Rows - 1) / kW4Rows), s->panels = (s->N + kW4Cols - 1) / kW4Cols;
-  if (M * parts > (1LL << 46) / ((long long)s->kb * s->panels)) return MEP_ERR_INVALID_ARG;
+  if (M * parts > 0x7fffffffLL / ((long long)s->kb * s->panels)) return MEP_ERR_INVALID_ARG;
   *blocks = M * parts * s->kb * s->panels;
   if (M == 0) return MEP_OK;
   if (w == nullptr || w4 == nullptr || !aligned16(w4) ||
@@ -168,21 +237,32 @@ extern "C" int mep_w4_bytes(int64_t K, int64_t N, int group, size_t* bytes) {
   return MEP_OK;
 }
 
+namespace {
+// Whole vectors: every row of every part starts on a 16-byte boundary.
+bool vectors(const void* w, int type, const Matrices& s) {
+  const int v = type == MEP_BF16 ? 8 : 4;
+  return aligned16(w) && s.N % v == 0;
+}
+template <typename... KArgs, typename... Args>
+int launch_blocks(void (*kernel)(KArgs...), long long blocks, void* stream, Args... args) {
+  return launch_pdl(kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, static_cast<cudaStream_t>(stream), args...) == cudaSuccess
+             ? MEP_OK
+             : MEP_ERR_CUDA;
+}
+}  // namespace
+
 extern "C" int mep_w4_save(const void* w, int w_type, int64_t M, int64_t K, int64_t N, int parts, int group,
                            uint8_t* w4, void* stream) {
   Matrices s;
   long long blocks = 0;
   const int rc = w4_check(w, w_type, M, K, N, parts, group, w4, &s, &blocks);
   if (rc != MEP_OK || blocks == 0) return rc;
-  if (blocks > 0x7fffffffLL) return MEP_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      w_type == MEP_BF16
-          ? launch_pdl(k_w4_save<__nv_bfloat16>, dim3(unsigned(blocks)), dim3(kThreads), 0, st,
-                       static_cast<const __nv_bfloat16*>(w), s, group, w4)
-          : launch_pdl(k_w4_save<float>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, static_cast<const float*>(w), s,
+  const bool vec = vectors(w, w_type, s);
+  if (w_type == MEP_BF16)
+    return launch_blocks(vec ? k_w4_save<__nv_bfloat16, true> : k_w4_save<__nv_bfloat16, false>, blocks, stream,
+                         static_cast<const __nv_bfloat16*>(w), s, group, w4);
+  return launch_blocks(vec ? k_w4_save<float, true> : k_w4_save<float, false>, blocks, stream, static_cast<const float*>(w), s,
                        group, w4);
-  return e == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
 }
 
 extern "C" int mep_w4_load(const uint8_t* w4, int64_t M, int64_t K, int64_t N, int parts, int group, int w_type,
@@ -191,13 +271,10 @@ extern "C" int mep_w4_load(const uint8_t* w4, int64_t M, int64_t K, int64_t N, i
   long long blocks = 0;
   const int rc = w4_check(w, w_type, M, K, N, parts, group, w4, &s, &blocks);
   if (rc != MEP_OK || blocks == 0) return rc;
-  if (blocks > 0x7fffffffLL) return MEP_ERR_INVALID_ARG;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e =
-      w_type == MEP_BF16
-          ? launch_pdl(k_w4_load<__nv_bfloat16>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, w4, s, group,
-                       static_cast<__nv_bfloat16*>(w))
-          : launch_pdl(k_w4_load<float>, dim3(unsigned(blocks)), dim3(kThreads), 0, st, w4, s, group,
+  const bool vec = vectors(w, w_type, s);
+  if (w_type == MEP_BF16)
+    return launch_blocks(vec ? k_w4_load<__nv_bfloat16, true> : k_w4_load<__nv_bfloat16, false>, blocks, stream, w4, s, group,
+                         static_cast<__nv_bfloat16*>(w));
+  return launch_blocks(vec ? k_w4_load<float, true> : k_w4_load<float, false>, blocks, stream, w4, s, group,
                        static_cast<float*>(w));
-  return e == cudaSuccess ? MEP_OK : MEP_ERR_CUDA;
 }
