@@ -2,16 +2,23 @@
 //
 // One pass over memory, a CTA a block of 128 rows and 64 columns, which goes
 // through shared memory: rows outside in 16-byte vectors, inside the 32 rows of
-// two columns that a lane's pairs are of (w4.cuh). A warp holds 16 columns; a
-// group has its share in each of the four lanes t, so that its largest magnitude
-// is two shuffles away. Rows that do not start on 16-byte boundaries are read and
-// written element by element, coalesced over a row's 64 columns.
-// q = w / s is a division, as the format is defined by it. From bf16 it is a
-// product by 1 / s and a correction by the remainder, which two fused
-// multiply-adds give: the quotient of two numbers of eight bits is 2^-9 or more
-// from every half step unless it is one, and one it meets exactly. (Scales below
-// 2^-100, whose reciprocal leaves fp32, divide.) Adding 1.5 * 2^23 + 8 rounds to
-// a whole number, ties to even, and leaves q + 8 in the low bits.
+// two columns that a lane's pairs are of (w4.cuh). Rows that do not start on
+// 16-byte boundaries are read and written element by element, coalesced over a
+// row's 64 columns. What bounds it is what a lane has to issue for a weight.
+//   save  Largest magnitudes first, of 32 rows of two columns a thread (bf16, in
+//         packed maxima) or 64 of one; scales and their reciprocals, one thread
+//         each; then the pairs. q = w / s is a division, as the format is defined
+//         by it: a product by the correctly rounded 1 / s and corrections by the
+//         remainder, two fused multiply-adds each, after which the quotient is
+//         correctly rounded (Markstein, 1990: two from fp32; one from bf16, where
+//         a quotient of two numbers of eight bits is 2^-9 or more from every half
+//         step unless it is one, and one it meets exactly). 1.5 * 2^23 rounds to
+//         a whole number, ties to even, and four of them become 16 bits of pairs
+//         by multiply-adds. Scales below 2^-100, whose reciprocal or remainder
+//         may leave fp32, divide, and keep within +-7, which others do anyway.
+//   load  In bf16 two weights at once: the bits of q + 8 are a bf16 of q / 64
+//         after one multiply-add (few.cu), and that times 64 s is rounded once.
+//         Scales from 2^120 on go the other way, through fp32, like fp32 output.
 
 #include "ckpt.cuh"
 #include "w4.cuh"
@@ -64,9 +71,9 @@ template <typename T, bool VEC> __device__ __forceinline__ void rows_in(const T*
       *reinterpret_cast<uint4*>(tile + q / per_row * kPitch<T> + q % per_row * V) = v[i];
     }
   } else {
-#pragma unroll 16
-    for (int q = threadIdx.x; q < kW4Rows * kW4Cols; q += kThreads) {
-      const int r = q / kW4Cols, c = q % kW4Cols;
+#pragma unroll 32
+    for (int i = 0; i < kW4Rows * kW4Cols / kThreads; ++i) {
+      const int q = i * kThreads + threadIdx.x, r = q / kW4Cols, c = q % kW4Cols;
       tile[r * kPitch<T> + c] = r < a.rows && c < a.cols ? w[a.base + r * a.ld + c] : from_f32<T>(0.f);
     }
   }
@@ -87,89 +94,108 @@ template <typename T, bool VEC> __device__ __forceinline__ void rows_out(const T
 // Row of the block that pair (i, e) of word j of half h has in lane t.
 __device__ __forceinline__ constexpr int row_of(int h, int j, int r, int t) { return 64 * h + 16 * j + 8 * (r & 1) + 2 * t + (r >> 1); }
 
+constexpr float kRoundShift = 12582912.f;  // 1.5 * 2^23
+
+// q of x: x / s to the nearest whole number. `once`: one correction is enough.
+template <bool ONCE> __device__ __forceinline__ float quotient(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);
+  if (!ONCE) q = fmaf(fmaf(-q, s, x), inv, q);
+  return (q + kRoundShift) - kRoundShift;
+}
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_w4_save(const T* __restrict__ w, Matrices s, int group,
                                                       uint8_t* __restrict__ w4) {
   __shared__ __align__(16) T tile[kW4Rows * kPitch<T>];
+  __shared__ uint32_t s_top[4][kW4Cols];  // of 32 rows: the largest magnitude's bits
+  __shared__ float2 s_scale[4][kW4Cols];  // and the group's scale, and 1 / it
   pdl_launch_dependents();
   pdl_wait();
   const At a = at_block(s, blockIdx.x);
   rows_in<T, VEC>(w, a, tile);
   __syncthreads();
-  const int c = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x;
+  if (sizeof(T) == 2) {
+    const __nv_bfloat162* in = reinterpret_cast<const __nv_bfloat162*>(tile) + (tid >> 5) * 32 * (kPitch<T> / 2) + (tid & 31);
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 16
+    for (int r = 0; r < 32; ++r) m = __hmax2_nan(m, __habs2(in[r * (kPitch<T> / 2)]));
+    s_top[tid >> 5][2 * (tid & 31)] = __float_as_uint(__bfloat162float(m.x));
+    s_top[tid >> 5][2 * (tid & 31) + 1] = __float_as_uint(__bfloat162float(m.y));
+  } else {
+    const uint32_t* in = reinterpret_cast<const uint32_t*>(tile) + (tid >> 6) * 64 * kPitch<T> + (tid & 63);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t m = 0;  // an infinity and then a NaN lie above all numbers
+#pragma unroll 16
+      for (int r = 0; r < 32; ++r) m = max(m, in[(32 * q + r) * kPitch<T>] & 0x7fffffffu);
+      s_top[2 * (tid >> 6) + q][tid & 63] = m;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int q = 2 * (tid >> 6) + i, c = tid & 63, n = group / 32, q0 = q / n * n;
+    uint32_t m = s_top[q0][c];
+    for (int o = 1; o < n; ++o) m = max(m, s_top[q0 + o][c]);
+    const float sc = m >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                      : __bfloat162float(__float2bfloat16_rn(__uint_as_float(m) * (1.f / kW4Top)));
+    s_scale[q][c] = make_float2(sc, sc > 0.f ? 1.f / sc : 0.f);  // 0: every q is 0
+  }
+  __syncthreads();
+  const int c = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint8_t* out = w4 + (long long)blockIdx.x * w4_block_bytes(group);
   const T* mine = tile + 16 * c + g;
-  // the larger magnitude, as bits: an infinity and then a NaN above all numbers
-  uint32_t top[4][2] = {};  // of 32 rows
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          const float x = to_f32(mine[row_of(h, j, r, t) * kPitch<T> + 8 * l]);
-          top[2 * h + j / 2][l] = max(top[2 * h + j / 2][l], __float_as_uint(x) & 0x7fffffffu);
-        }
-  float scale[4][2];
-#pragma unroll
-  for (int l = 0; l < 2; ++l) {
-    uint32_t m[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      m[q] = max(top[q][l], __shfl_xor_sync(MEP_FULL_MASK, top[q][l], 1));
-      m[q] = max(m[q], __shfl_xor_sync(MEP_FULL_MASK, m[q], 2));
-    }
-    if (group >= 64) m[0] = m[1] = max(m[0], m[1]), m[2] = m[3] = max(m[2], m[3]);
-    if (group >= 128) m[0] = m[1] = m[2] = m[3] = max(m[0], m[2]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      scale[q][l] = m[q] >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                        : __bfloat162float(__float2bfloat16_rn(__uint_as_float(m[q]) * (1.f / kW4Top)));
-  }
-  constexpr float kShift = 12582912.f + 8.f;
-  float inv[4][2];
-  bool divide = sizeof(T) == 4;
+  bool slow = false;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int l = 0; l < 2; ++l) {
-      // a scale of zero or NaN: every q is 0
-      inv[q][l] = scale[q][l] > 0.f ? 1.f / scale[q][l] : 0.f;
-      divide |= scale[q][l] > 0.f && scale[q][l] < 0x1p-100f;
+      const float2 sc = s_scale[q][16 * c + 8 * l + g];
+      slow |= !(sc.x == 0.f) && !(sc.x >= 0x1p-100f);  // NaN too: what it meets may not be a number
     }
+  uint4* pairs = reinterpret_cast<uint4*>(out) + (c * 8 + g) * 4 + t;
+  if (!slow) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t word[4];
+    for (int h = 0; h < 2; ++h) {
+      uint32_t word[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      word[j] = 0;
+      for (int j = 0; j < 4; ++j) {
+        const float2 s0 = s_scale[2 * h + j / 2][16 * c + g], s1 = s_scale[2 * h + j / 2][16 * c + 8 + g];
+        float byte[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          const float sc = scale[2 * h + j / 2][l], in = inv[2 * h + j / 2][l];
-          const float x = to_f32(mine[row_of(h, j, r, t) * kPitch<T> + 8 * l]);
-          float q;
-          if (divide) {
-            q = in > 0.f ? x / sc : 0.f;
-          } else {
-            q = in > 0.f ? x * in : 0.f;
-            q = in > 0.f ? fmaf(fmaf(-q, sc, x), in, q) : 0.f;
-          }
-          const uint32_t bits = __float_as_uint(fminf(fmaxf(q, -kW4Top), kW4Top) + kShift) & 15u;
-          word[j] |= bits << (8 * r + 4 * l);
+        for (int r = 0; r < 4; ++r) {
+          const T* x = mine + row_of(h, j, r, t) * kPitch<T>;
+          byte[r] = fmaf(quotient<sizeof(T) == 2>(to_f32(x[8]), s1.x, s1.y), 16.f,
+                         quotient<sizeof(T) == 2>(to_f32(x[0]), s0.x, s0.y));
         }
+        // + 136 in every byte, and the bits of a whole number
+        const uint32_t low = __float_as_uint(fmaf(byte[1], 256.f, byte[0]) + (kRoundShift + 34952.f));
+        const uint32_t high = __float_as_uint(fmaf(byte[3], 256.f, byte[2]) + (kRoundShift + 34952.f));
+        word[j] = __byte_perm(low, high, 0x5410);
+      }
+      pairs[h * 128] = make_uint4(word[0], word[1], word[2], word[3]);
     }
-    reinterpret_cast<uint4*>(out)[((h * 4 + c) * 8 + g) * 4 + t] = make_uint4(word[0], word[1], word[2], word[3]);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      const int h = i >> 2, j = i & 3;
+      uint32_t word = 0;
+#pragma unroll 1
+      for (int o = 0; o < 8; ++o) {
+        const int r = o >> 1, l = o & 1;
+        const float2 sc = s_scale[2 * h + j / 2][16 * c + 8 * l + g];
+        const float q = sc.x > 0.f ? rintf(to_f32(mine[row_of(h, j, r, t) * kPitch<T> + 8 * l]) / sc.x) : 0.f;
+        word |= uint32_t(int(fminf(fmaxf(q, -kW4Top), kW4Top)) + 8) << (8 * r + 4 * l);
+      }
+      reinterpret_cast<uint32_t*>(pairs + h * 128)[j] = word;
+    }
   }
   if (t < kW4Rows / group) {
-    __nv_bfloat162 pair;
     const int q = t * (group / 32);
-    pair.x = __float2bfloat16_rn(q == 0 ? scale[0][0] : q == 1 ? scale[1][0] : q == 2 ? scale[2][0] : scale[3][0]);
-    pair.y = __float2bfloat16_rn(q == 0 ? scale[0][1] : q == 1 ? scale[1][1] : q == 2 ? scale[2][1] : scale[3][1]);
-    reinterpret_cast<__nv_bfloat162*>(out + kW4Pairs)[t * 32 + c * 8 + g] = pair;
+    reinterpret_cast<__nv_bfloat162*>(out + kW4Pairs)[t * 32 + c * 8 + g] =
+        __floats2bfloat162_rn(s_scale[q][16 * c + g].x, s_scale[q][16 * c + 8 + g].x);
   }
 }
 
@@ -186,24 +212,55 @@ __global__ void __launch_bounds__(kThreads) k_w4_load(const uint8_t* __restrict_
   T* mine = tile + 16 * c + g;
   uint4 pairs[2];
   __nv_bfloat162 sc[4];  // of 32 rows
+  bool wide = false;
 #pragma unroll
   for (int h = 0; h < 2; ++h) pairs[h] = __ldcs(reinterpret_cast<const uint4*>(in) + ((h * 4 + c) * 8 + g) * 4 + t);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sc[q] = scales[(group == 32 ? q : group == 64 ? q / 2 : 0) * 32];
+  for (int q = 0; q < 4; ++q) {
+    sc[q] = scales[(group == 32 ? q : group == 64 ? q / 2 : 0) * 32];
+    wide |= !(__bfloat162float(sc[q].x) < 0x1p120f) || !(__bfloat162float(sc[q].y) < 0x1p120f);
+  }
+  if (sizeof(T) == 2 && !wide) {
+    __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(mine);
+    const __nv_bfloat162 k64 = __floats2bfloat162_rn(64.f, 64.f);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t word[4] = {pairs[h].x, pairs[h].y, pairs[h].z, pairs[h].w};
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t word[4] = {pairs[h].x, pairs[h].y, pairs[h].z, pairs[h].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 s64 = __hmul2(sc[2 * h + j / 2], k64);
+        uint32_t v = word[j];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int i = 0; i < 2; ++i, v >>= 8)
 #pragma unroll
-        for (int l = 0; l < 2; ++l) {
-          // q + 8 under 2^23, less 2^23 + 8
-          const float q = __uint_as_float(((word[j] >> (8 * r + 4 * l)) & 15u) | 0x4b000000u) - 8388616.f;
-          const __nv_bfloat162 p = sc[2 * h + j / 2];
-          mine[row_of(h, j, r, t) * kPitch<T> + 8 * l] = from_f32<T>(q * __bfloat162float(l ? p.y : p.x));
-        }
+          for (int l = 0; l < 2; ++l) {
+            uint32_t q;
+            asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+                : "=r"(q)
+                : "r"(v & (l ? 0x00f000f0u : 0x000f000fu)), "r"(l ? 0x7d007d00u : 0x7f007f00u), "r"(0xbe00be00u));
+            const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&q), l ? __high2bfloat162(s64) : __low2bfloat162(s64));
+            // rows 8 i + 2 t and the next one
+            o[row_of(h, j, i, t) * kPitch<T> + 8 * l] = x.x;
+            o[row_of(h, j, i + 2, t) * kPitch<T> + 8 * l] = x.y;
+          }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t word[4] = {pairs[h].x, pairs[h].y, pairs[h].z, pairs[h].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int l = 0; l < 2; ++l) {
+            // q + 8 under 2^23, less 2^23 + 8
+            const float q = __uint_as_float(((word[j] >> (8 * r + 4 * l)) & 15u) | 0x4b000000u) - 8388616.f;
+            const __nv_bfloat162 p = sc[2 * h + j / 2];
+            mine[row_of(h, j, r, t) * kPitch<T> + 8 * l] = from_f32<T>(q * __bfloat162float(l ? p.y : p.x));
+          }
+    }
   }
   __syncthreads();
   rows_out<T, VEC>(tile, a, w);

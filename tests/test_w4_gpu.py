@@ -53,6 +53,28 @@ def test_bytes(K, N, kind, dtype, group):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("exponent", [0, 100, 117, -60, -90, -98, -100, -104, -115, -126, -130])
+def test_quotients_next_to_half_steps(dtype, exponent):
+    """w around (n + 1/2) s by single steps of fp32, scales of many sizes: q as the division in fp32 rounds it."""
+    K, N, group = 128, 4096, 32
+    g = torch.Generator(device="cuda").manual_seed(exponent + 200)
+    top = (1 + torch.rand(K // group, 1, N, generator=g, device="cuda")) * 2.0 ** exponent
+    scale = (top * (torch.ones(1, device="cuda") / 7)).to(torch.bfloat16).float()
+    n = torch.randint(-7, 7, (K // group, group, N), generator=g, device="cuda").float() + 0.5
+    w = n * scale
+    step = torch.randint(-3, 4, w.shape, generator=g, device="cuda", dtype=torch.int32)
+    w = torch.where(w.abs() > 2.0 ** -120, (w.view(torch.int32) + step).view(torch.float32), w)
+    w = torch.minimum(torch.maximum(w, -top), top)
+    w[:, 0] = top[:, 0]
+    w = w.reshape(K, N).to(dtype).reshape(K // group, group, N)
+    top = w.float().abs().amax(1, keepdim=True)
+    scale = (top * (torch.ones(1, device="cuda") / 7)).to(torch.bfloat16).float()
+    want = torch.round(w.float() / torch.where(scale > 0, scale, torch.ones_like(scale))).clamp(-7, 7) * scale
+    got = mep.mep_w4_load(mep.mep_w4_save(w.reshape(K, N), group=group), K, N, group=group, dtype=torch.float32)
+    assert torch.equal(got.reshape(w.shape), torch.where(scale > 0, want, torch.zeros_like(want)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_parts_and_batches(dtype):
     M, K, F, group = 3, 200, 72, 64
     w = torch.randn(M, K, 2 * F).to(dtype).cuda()
