@@ -2,14 +2,14 @@
 // gradient (mep_route_backward).
 //
 // A warp takes a token's row. Forward, the logits become whole numbers of the
-// same order, and K times the warp takes the largest that is left: a maximum over
-// the lanes, a vote for whose it is. Up to 256 experts a lane has its values in
-// registers and knows the best two of them with their places, so that taking one
-// costs a dozen instructions; only a lane that loses both looks through its
-// values again (one row in five, of 256 normal logits and K = 8). What is taken
-// is told by its order, not marked: values behind the last one taken, by size
-// and place. What bounds it is what a warp has to issue. More experts: the orders
-// lie in shared memory and every lane looks through its own each time.
+// same order. Up to 256 experts a lane has its values in registers: the K-th
+// largest of the lanes' maxima (K times a maximum over the warp, without whose it
+// is) is a bound that the K largest values and few others reach, a dozen of 256
+// normal logits with K = 8; those are put together, one a lane, and each finds
+// its place by comparing itself with the others. Only where more than 32 values
+// reach the bound (many equal ones) the warp takes the largest that is left K
+// times. What bounds it is what a warp has to issue. More experts: the orders lie
+// in shared memory, and the largest is taken K times.
 // Backward, the row is zeros but for K places: built in shared memory, which
 // stays zero otherwise, and written out in vectors; bound by those bytes.
 
@@ -58,61 +58,85 @@ __device__ __forceinline__ void put_row(const float (&l)[2], const int (&at)[2],
   }
 }
 
-// Up to 32 NV experts: expert lane + 32 i is value i of the lane.
+// Up to 32 NV experts, K <= 32: expert lane + 32 i is value i of the lane.
 template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ logits, const float* __restrict__ bias,
                                                         long long N, int E, int K, int skip_masked,
                                                         int32_t* __restrict__ idx, float* __restrict__ w) {
+  __shared__ uint2 s_found[kWarps][32];  // order, expert
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint2* found = s_found[warp];
   for (long long row = (long long)blockIdx.x * kWarps + warp; row < N; row += (long long)gridDim.x * kWarps) {
     const T* in = logits + row * E;
-    uint32_t key[NV];  // 0: no expert
-    // the best two and their places: larger first, equal ones in order of place
-    uint32_t m1 = 0, m2 = 0;
-    int i1 = 0, i2 = 0, left = 2;
-    const auto offer = [&](uint32_t k, int i) {
-      const bool first = k > m1, second = k > m2;
-      const uint32_t m = first ? m1 : k;
-      const int at = first ? i1 : i;
-      m2 = second ? m : m2, i2 = second ? at : i2;
-      m1 = first ? k : m1, i1 = first ? i : i1;
-    };
     float v[NV];
+    uint32_t key[NV], most = 0;  // 0: no expert
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < E ? to_f32(in[lane + 32 * i]) : 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
       key[i] = e < E ? order_of(bias == nullptr ? v[i] : v[i] + bias[e]) : 0u;
-      offer(key[i], i);
+      most = max(most, key[i]);
     }
-    int mine[2] = {0, 0};  // chosen number lane, and lane + 32
+    uint32_t bound = 0;
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
-      const uint32_t top = __reduce_max_sync(MEP_FULL_MASK, m1);
-      const unsigned who = __ballot_sync(MEP_FULL_MASK, m1 == top);
-      int at = 32 * i1 + lane;
-      if (who & (who - 1))  // several lanes: the lowest place
-        at = __reduce_min_sync(MEP_FULL_MASK, m1 == top ? at : 0x7fffffff);
-      else
-        at = __shfl_sync(MEP_FULL_MASK, at, __ffs(who) - 1);
-      if ((k & 31) == lane) mine[k >> 5] = at;
-      if ((at & 31) == lane) {
-        const int last = i1;
-        m1 = m2, i1 = i2, m2 = 0;
-        if (--left == 0) {
-          m1 = 0, left = 2;
+      bound = __reduce_max_sync(MEP_FULL_MASK, most);
+      if (most == bound) most = 0;
+    }
+    bound = max(bound, 1u);
+    int count = 0;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) offer(key[i] < top || (key[i] == top && i > last) ? key[i] : 0u, i);
+    for (int i = 0; i < NV; ++i) count += key[i] >= bound;
+    int at = warp_incl_scan(count);
+    const int all = __shfl_sync(MEP_FULL_MASK, at, 31);
+    int mine = 0, rank = 32;  // expert, and its place among the chosen
+    if (all <= 32) {
+      at -= count;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (key[i] >= bound) found[at++] = make_uint2(key[i], lane + 32 * i);
+      __syncwarp();
+      const uint2 f = lane < all ? found[lane] : make_uint2(0u, 0u);
+      mine = int(f.y), rank = lane < all ? 0 : 32;
+#pragma unroll 4
+      for (int o = 0; o < all; ++o) {
+        const uint2 other = found[o];
+        rank += other.x > f.x || (other.x == f.x && other.y < f.y);
+      }
+      __syncwarp();
+    } else {
+      uint32_t last = 0xffffffffu;  // order and place of the last one taken
+      int last_at = -1;
+#pragma unroll 1
+      for (int k = 0; k < K; ++k) {
+        uint32_t best = 0;
+        int e = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int here = lane + 32 * i;
+          if ((key[i] < last || (key[i] == last && here > last_at)) && key[i] > best) best = key[i], e = here;
         }
+        last = __reduce_max_sync(MEP_FULL_MASK, best);
+        last_at = __reduce_min_sync(MEP_FULL_MASK, best == last ? e : 0x7fffffff);
+        if (k == lane) mine = last_at, rank = k;
       }
     }
-    float l[2];
+    // the chosen, in any order of lanes: each one's weight goes to its place
+    const bool chosen = rank < K;
+    const float l = chosen ? to_f32(in[mine]) : -INFINITY;
+    float m = l;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) l[i] = 32 * i + lane < K ? to_f32(in[mine[i]]) : -INFINITY;
-    put_row(l, mine, K, skip_masked, idx + row * K, w + row * K);
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
+    float ex = l == -INFINITY ? 0.f : expf(l - m), sum = ex;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, d);
+    if (chosen) {
+      idx[row * K + rank] = skip_masked && l == -INFINITY ? -1 : mine;
+      w[row * K + rank] = sum == 0.f ? 0.f : ex / sum;
+    }
   }
 }
 
@@ -235,6 +259,7 @@ template <typename T>
 int route(const T* logits, const float* bias, int64_t N, int E, int K, int skip_masked, int32_t* idx, float* w,
           cudaStream_t st) {
   const auto few = [&](auto kernel) { return launch_rows(kernel, N, 0, st, logits, bias, N, E, K, skip_masked, idx, w); };
+  if (K > 32) return launch_rows(k_route<T>, N, kWarps * E * 4, st, logits, bias, N, E, K, skip_masked, idx, w);
   if (E <= 32) return few(k_route_few<T, 1>);
   if (E <= 64) return few(k_route_few<T, 2>);
   if (E <= 128) return few(k_route_few<T, 4>);

@@ -73,6 +73,16 @@ def test_values(kind, dtype, skip, N, E, K):
     check(t, x, K, None, skip)
 
 
+@pytest.mark.parametrize("E,K", [(256, 8), (64, 6), (128, 32), (100, 3), (200, 33)])
+@pytest.mark.parametrize("values", [1, 2, 3, 5, 9, 17, 33, 100])
+def test_few_different_values(E, K, values):
+    """From all equal (every value reaches any bound) to nearly all different; every choice by place."""
+    g = torch.Generator(device="cuda").manual_seed(E + values)
+    t = torch.randint(0, values, (400, E), generator=g, device="cuda").float()
+    idx, _ = mep.mep_route(t, K)
+    assert (idx.long() == torch.sort(t, dim=1, descending=True, stable=True)[1][:, :K]).all()
+
+
 @pytest.mark.parametrize("kind", ["normal", "masked", "ties"])
 def test_bias_chooses_but_does_not_weigh(kind):
     t, x = make(100, 64, 3, torch.float32, kind)
@@ -161,7 +171,8 @@ def test_many_rows_and_another_stream():
         idx, w = mep.mep_route(t, K)
         d = mep.mep_route_backward(w, w, idx, E)
     torch.cuda.current_stream().wait_stream(side)
-    top, at = torch.topk(t, K, dim=1)
+    top, at = torch.sort(t, dim=1, descending=True, stable=True)  # (topk leaves the order of equal values open)
+    top, at = top[:, :K], at[:, :K]
     assert (idx.long() == at).all()
     p = torch.softmax(top.double(), 1)
     want = torch.zeros(N, E, dtype=torch.float64, device="cuda").scatter_(1, at, p * (p - (p * p).sum(1, keepdim=True)))
