@@ -2,7 +2,7 @@
 // gradient (mep_route_backward).
 //
 // A warp takes a token's row. Forward, the logits become whole numbers of the
-// same order. Up to 256 experts a lane has its values in registers: the K-th
+// same order. Up to 512 experts a lane has its values in registers: the K-th
 // largest of the lanes' maxima (K times a maximum over the warp, without whose it
 // is) is a bound that the K largest values and few others reach, a dozen of 256
 // normal logits with K = 8; those are put together, one a lane, and each finds
@@ -28,6 +28,9 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
+
+// The value of an order (+0 for either zero).
+__device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
 // Weights of the chosen: lane and lane + 32 have number lane and lane + 32, their
 // logits l.
@@ -68,18 +71,23 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint2* found = s_found[warp];
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < N; row += (long long)gridDim.x * kWarps) {
-    const T* in = logits + row * E;
-    float v[NV];
-    uint32_t key[NV], most = 0;  // 0: no expert
+  const long long step = (long long)gridDim.x * kWarps;
+  long long row = (long long)blockIdx.x * kWarps + warp;
+  float v[NV];  // of the next row, on its way while this one is worked on
+  const auto load = [&](long long r) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < E ? to_f32(in[lane + 32 * i]) : 0.f;
+    for (int i = 0; i < NV; ++i) v[i] = r < N && lane + 32 * i < E ? to_f32(logits[r * E + lane + 32 * i]) : 0.f;
+  };
+  load(row);
+  for (; row < N; row += step) {
+    uint32_t key[NV], most = 0;  // 0: no expert
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
       key[i] = e < E ? order_of(bias == nullptr ? v[i] : v[i] + bias[e]) : 0u;
       most = max(most, key[i]);
     }
+    load(row + step);
     uint32_t bound = 0;
 #pragma unroll 1
     for (int k = 0; k < K; ++k) {
@@ -93,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
     int at = warp_incl_scan(count);
     const int all = __shfl_sync(MEP_FULL_MASK, at, 31);
     int mine = 0, rank = 32;  // expert, and its place among the chosen
+    uint32_t order = 0;
     if (all <= 32) {
       at -= count;
 #pragma unroll
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
         if (key[i] >= bound) found[at++] = make_uint2(key[i], lane + 32 * i);
       __syncwarp();
       const uint2 f = lane < all ? found[lane] : make_uint2(0u, 0u);
-      mine = int(f.y), rank = lane < all ? 0 : 32;
+      mine = int(f.y), order = f.x, rank = lane < all ? 0 : 32;
 #pragma unroll 4
       for (int o = 0; o < all; ++o) {
         const uint2 other = found[o];
@@ -121,12 +130,12 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
         }
         last = __reduce_max_sync(MEP_FULL_MASK, best);
         last_at = __reduce_min_sync(MEP_FULL_MASK, best == last ? e : 0x7fffffff);
-        if (k == lane) mine = last_at, rank = k;
+        if (k == lane) mine = last_at, order = last, rank = k;
       }
     }
     // the chosen, in any order of lanes: each one's weight goes to its place
     const bool chosen = rank < K;
-    const float l = chosen ? to_f32(in[mine]) : -INFINITY;
+    const float l = !chosen ? -INFINITY : bias == nullptr ? value_of(order) : to_f32(logits[row * E + mine]);
     float m = l;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
@@ -188,19 +197,29 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const float* __rest
   float* d = s_rows + warp * pitch;
   for (int e = lane; e < pitch; e += 32) d[e] = 0.f;
   bool bad = false;
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < N; row += (long long)gridDim.x * kWarps) {
+  const long long step = (long long)gridDim.x * kWarps;
+  long long row = (long long)blockIdx.x * kWarps + warp;
+  float wn[2], dn[2];  // of the next row
+  int an[2];
+  const auto load = [&](long long r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool there = r < N && 32 * i + lane < K;
+      const long long k = r * K + 32 * i + lane;
+      wn[i] = there ? w[k] : 0.f, dn[i] = there ? dw[k] : 0.f, an[i] = there ? idx[k] : -1;
+    }
+  };
+  load(row);
+  for (; row < N; row += step) {
     float wk[2], dk[2], sum = 0.f;
     int at[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int k = 32 * i + lane;
-      wk[i] = k < K ? w[row * K + k] : 0.f;
-      dk[i] = k < K ? dw[row * K + k] : 0.f;
-      at[i] = k < K ? idx[row * K + k] : -1;
+      wk[i] = wn[i], dk[i] = dn[i], at[i] = an[i];
       if (at[i] < -1 || at[i] >= E) bad = true, at[i] = -1;
-      if (at[i] < 0) at[i] = -1;
-      sum += k < K ? wk[i] * dk[i] : 0.f;
+      sum += 32 * i + lane < K ? wk[i] * dk[i] : 0.f;
     }
+    load(row + step);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, s);
     // an expert that stands twice gets both, one after another
@@ -264,6 +283,7 @@ int route(const T* logits, const float* bias, int64_t N, int E, int K, int skip_
   if (E <= 64) return few(k_route_few<T, 2>);
   if (E <= 128) return few(k_route_few<T, 4>);
   if (E <= 256) return few(k_route_few<T, 8>);
+  if (E <= 512) return few(k_route_few<T, 16>);
   return launch_rows(k_route<T>, N, kWarps * E * 4, st, logits, bias, N, E, K, skip_masked, idx, w);
 }
 template <typename T>
