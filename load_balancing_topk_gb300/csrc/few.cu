@@ -43,7 +43,8 @@ namespace {
 
 constexpr int kMaxCtas = 152;       // SMs of a GB300; more are not used, the workspace counts on it
 constexpr int kWarps = 8;           // across a unit's columns: 16 of its first half and 16 of its second
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kThreads = 32 * (kWarps + 1);       // a producer's warp beside them
+constexpr int kLayerThreads = 32 * (kWarps + 2);  // and one that runs ahead through the sums
 constexpr int kUnit = 256;          // columns of a unit
 constexpr int kPanels = kUnit / kW4Cols;
 constexpr int kPanelRow = 128;      // bytes of a stage's row of 64 bf16 columns
@@ -576,12 +577,14 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
 
 // All steps that this CTA is fed, of `planes` rows of x a token. PUT(first row of
 // the list, unit of the expert, part, rows, and as above). What a kernel executes
-// for the first time comes from far away, at some 25 ns an instruction: with
-// `dry` the code is run through once, on whatever the first stage holds and to no
-// effect, while that stage's bytes are on their way.
+// for the first time comes from far away, at some 25 ns an instruction: dry, the
+// code is run through once, on whatever the first stage holds and to no effect,
+// while that stage's bytes are on their way.
+enum Run { kReal, kDry, kDryThenReal };
 template <int G, bool TILES, int NTMAX, typename Put>
 __device__ __forceinline__ void products(const Phase& p, int K, int planes, const Ring& r, Cursor& c,
-                                         const uint16_t* start, bool dry, int most, Put put) {
+                                         const uint16_t* start, Run how, int most, Put put) {
+  bool dry = how != kReal;
 #pragma unroll 1
   while (true) {
     uint32_t at = 0;
@@ -604,7 +607,7 @@ __device__ __forceinline__ void products(const Phase& p, int K, int planes, cons
       ok = unit_product<G, TILES, 4>(steps, s, K, r, c, rows, dry, f);
     else
       ok = unit_product<G, TILES, NTMAX>(steps, s, K, r, c, rows, dry, f);
-    if (!ok) return;
+    if (!ok || how == kDry) return;
     dry = false;
   }
   __syncwarp();
@@ -629,9 +632,12 @@ struct Head {  // start of shared memory
 };
 constexpr uint32_t kHeadBytes = 1024;
 
-__device__ __forceinline__ void init_ring(Ring& r, Head* h, int32_t* status) {
+__device__ __forceinline__ void init_names(Ring& r, Head* h, int32_t* status) {
   r.full = smem_u32(h->full), r.empty = smem_u32(h->empty);
   r.step = h->step, r.abort = &h->abort, r.status = status;
+}
+__device__ __forceinline__ void init_ring(Ring& r, Head* h, int32_t* status) {
+  init_names(r, h, status);
   if (threadIdx.x < kMaxStages) {
     mbar_init(r.full + 8 * threadIdx.x, 2);  // weights, rows
     mbar_init(r.empty + 8 * threadIdx.x, kWarps);
@@ -694,17 +700,23 @@ constexpr uint16_t kNone = 0xffff;
 // The experts in use in ascending order, each one's tokens in order, more than
 // kChunk of them in several entries; where each assignment went. What comes from
 // memory is asked for at the start, the barriers' words are set up meanwhile.
+// The warps that make it: four of the products' and the producer.
+constexpr int kListWarps = 4;
+__device__ __forceinline__ void list_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * (kListWarps + 1)) : "memory"); }
+
 __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, char* scratch, const Lists& l, bool long_run) {
   unsigned long long* mask = reinterpret_cast<unsigned long long*>(scratch);
   uint32_t* e_at = reinterpret_cast<uint32_t*>(mask + a.E);  // entry and first row of an expert
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = kThreads, A = a.T * a.K;
+  constexpr int threads = 32 * (kListWarps + 1);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 == kWarps ? kListWarps : threadIdx.x >> 5;
+  const int tid = 32 * warp + lane, A = a.T * a.K;
   const int mine = tid < A ? __ldg(a.idx + tid) : -1;
   const float weight = tid < A ? __ldg(a.topk_w + tid) : 0.f;
   const int held = tid == 0 ? read_status(a.status) : 0;
   init_ring(r, h, a.status);
   for (int e = tid; e < a.E; e += threads) mask[e] = 0;
   if (tid == 0 && blockIdx.x == 0) a.counters[0] = a.counters[1] = 0;
-  __syncthreads();
+  list_sync();
   if (tid == 0) h->go = held == 0;
 #pragma unroll 1
   for (int i = tid, e = mine; i < A;) {
@@ -716,7 +728,7 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
     }
     if ((i += threads) < A) e = a.idx[i];
   }
-  __syncthreads();
+  list_sync();
   // entries and rows before each thread's experts, in one word
   const int per = a.E <= threads ? 1 : (a.E + threads - 1) / threads, lo = min(a.E, tid * per), hi = min(a.E, lo + per);
   uint32_t sum = 0;
@@ -731,7 +743,7 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
   most = __reduce_max_sync(MEP_FULL_MASK, most);
   if (lane == 31) h->warp_sums[warp] = incl;
   if (lane == 0 && most > 0) atomicMax(&h->most, most);
-  __syncthreads();
+  list_sync();
   const uint32_t w = lane < threads / 32 ? h->warp_sums[lane] : 0;
   const uint32_t all = __reduce_add_sync(MEP_FULL_MASK, w);
   uint32_t before = __reduce_add_sync(MEP_FULL_MASK, lane < warp ? w : 0) + incl - sum;
@@ -752,7 +764,7 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
       l.start[all >> 16] = all & 0xffff;
     }
   }
-  __syncthreads();
+  list_sync();
   if (!h->bad)
 #pragma unroll 1
     for (int i = tid, e = mine; i < A;) {
@@ -766,7 +778,6 @@ __device__ __forceinline__ void make_list(const LayerArgs& a, Ring& r, Head* h, 
       if ((i += threads) < A) e = a.idx[i];
     }
   fence_async();  // the ring's copies come into the same memory
-  __syncthreads();
 }
 
 template <int G> __device__ __forceinline__ Weights first_weights(const LayerArgs& a, const CUtensorMap* map) {
@@ -860,7 +871,7 @@ __device__ __forceinline__ void combine(const LayerArgs& a, const Phase& p, cons
 }
 
 template <int G>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kLayerThreads, 1)
     k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const LayerArgs a) {
   extern __shared__ __align__(1024) char smem[];
   Head* h = reinterpret_cast<Head*>(smem);
@@ -875,22 +886,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     l.row = l.token + A;
   }
   const uint32_t used = kHeadBytes + list_bytes(a.T, a.K, a.E);
-  Ring r;
-  make_list(a, r, h, smem + used, l, G != 0);
-  const bool go = h->go && !h->bad;
-  if (h->go && h->bad && threadIdx.x == 0) set_status(a.status, MEP_ERR_BAD_ROUTING);
-  r.stage0 = smem_u32(smem + used);
-  const int most = min(h->most, kChunk);
-  size_ring<G, false>(r, kSmem - used, 2 * most);
-
   const int warp = threadIdx.x >> 5;
-  const uint32_t rows = h->rows;
-  const Phase &p1 = h->phase[0], &p2 = h->phase[1];
+  Ring r;
+  // The list is made by some of the warps. The others meanwhile run through the
+  // product, dry; all meet at a barrier, where each has got to. Then the last warp
+  // runs through the two sums, dry (before, their first instructions took 2 to 4
+  // us each, most of it after a barrier when nothing else was under way).
+  if (warp < kListWarps || warp == kWarps) {
+    make_list(a, r, h, smem + used, l, G != 0);
+  } else {
+    r.stage0 = smem_u32(smem + used), r.stage_bytes = r.x_at = 0, r.stages = 1;
+  }
+  const auto list_made = [&]() {
+    asm volatile("barrier.sync 0;" ::: "memory");
+    init_names(r, h, a.status);
+    r.stage0 = smem_u32(smem + used);
+    size_ring<G, false>(r, kSmem - used, 2 * min(h->most, kChunk));
+  };
   // How many barriers there are does not depend on what is read: every CTA comes
   // to all of them, whatever another stream does to the status word meanwhile.
   const bool counted = a.counted;
   Cursor c;
   if (warp == kWarps) {
+    list_made();
+    if (h->go && h->bad && threadIdx.x == 32 * kWarps) set_status(a.status, MEP_ERR_BAD_ROUTING);
+    const Phase &p1 = h->phase[0], &p2 = h->phase[1];
     Stream<G, false> t(r, l.expert, l.start);
     Cursor behind;
     t.own(p1, first_weights<G>(a, &map1), {nullptr, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1});
@@ -909,18 +929,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async();
     }
   } else {
-    if (counted) grid_barrier();
-    // Two turns of product and sum. Two warps first run through the sums, dry.
+    // Two turns of product and sum; -1: the product, dry; -3, -2: the sums, dry.
+    const bool helper = warp > kWarps;
+    int phase = -1;
+    if (helper || warp < kListWarps) {
+      list_made();
+      if (counted) grid_barrier();
+      phase = !helper ? 0 : h->rows > 0 ? -3 : -1;
+    }
 #pragma unroll 1
-    for (int phase = warp < 2 && rows > 0 ? -1 : 0; phase < 2; ++phase) {
-      const bool dry = phase < 0;
-      const bool second = dry ? warp == 1 : phase == 1;
+    for (; phase < (helper ? -1 : 2); ++phase) {
+      const bool dry = phase < -1, second = dry ? phase == -2 : phase == 1;
       const Phase& p = h->phase[second];
       if (!dry) {
         const Sums o = second ? Sums{a.part2, uint32_t(a.H), kUnit, kUnit / 2, a.H, -1}
                               : Sums{a.part1, 2u * a.F, kUnit / 2, a.F, a.F, 0};
         products<G, false, kChunk / 4>(
-            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, !second, most,
+            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, phase < 0 ? kDry : kReal, 1,
             [&](int first, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
               const int n = j * o.unit + col, off = q * o.half;
               if (n + (off & o.counted) >= o.limit) return;
@@ -929,20 +954,27 @@ __global__ void __launch_bounds__(kThreads, 1)
               *to = second ? v0 + v1 : v0;
               if (!second && row + 1 < rows) to[p.parts * o.pitch] = v1;
             });
+        if (phase < 0) {
+          list_made();
+          if (counted) grid_barrier();
+          continue;
+        }
         grid_barrier();
       }
       Spread s = spread(kWarps);
       if (dry) s.i = threadIdx.x & 31, s.step = 0x40000000;
       if (!second) {
-        activate(a, p, l, dry ? 32 : rows * p.nb * (kUnit / 8), s, dry);
+        activate(a, p, l, dry ? 32 : h->rows * p.nb * (kUnit / 8), s, dry);
         if (!dry) {
           fence_async();
           grid_barrier();
         }
-      } else if (go) {
+      } else if (h->go && !h->bad) {
         combine(a, p, l, dry ? 32 : a.T * p.nb * (kUnit / 16 * 8), s, dry);
       }
     }
+    if (helper)
+      for (int i = 0; i < 3; ++i) grid_barrier();
   }
   settle(r);
 }
@@ -1017,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const __grid_constan
   } else {
     if (pad) copy_rows();
     if (first_barrier) grid_barrier();
-    products<G, true, NTMAX>(p, a.K, 1, r, c, start, true, a.T,
+    products<G, true, NTMAX>(p, a.K, 1, r, c, start, kDryThenReal, a.T,
                              [&](int, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
                                const int n = j * kUnit + q * (kUnit / 2) + col;
                                if (n >= a.N) return;
@@ -1157,7 +1189,7 @@ template <int G>
 int launch_layer(const CUtensorMap& m1, const CUtensorMap& m2, const LayerArgs& a, cudaStream_t st) {
   const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(G);
   const long long n1 = experts * ceil_div(a.F, kUnit / 2) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
-  return launch_all(k_layer<G>, n1 > n2 ? n1 : n2, kThreads, st, m1, m2, a);
+  return launch_all(k_layer<G>, n1 > n2 ? n1 : n2, kLayerThreads, st, m1, m2, a);
 }
 template <int G> int launch_product(const CUtensorMap& x, const ProductArgs& a, cudaStream_t st) {
   const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(G));
