@@ -22,11 +22,11 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 
-// A number whose order is that of the values, equal for both zeros, NaN on top.
+// A number whose order is that of the values, equal for both zeros and for all
+// NaN (a sum that is a NaN is the canonical one), NaN on top.
 __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  if ((b & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-  return b & 0x80000000u ? ~b : b | 0x80000000u;
+  return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
 }
 
 // The value of an order (+0 for either zero).
@@ -137,8 +137,12 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
     const bool chosen = rank < K;
     const float l = !chosen ? -INFINITY : bias == nullptr ? value_of(order) : to_f32(logits[row * E + mine]);
     float m = l;
+    if (bias == nullptr) {
+      m = value_of(__reduce_max_sync(MEP_FULL_MASK, chosen ? order : 0u));
+    } else {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(MEP_FULL_MASK, m, d));
+    }
     float ex = l == -INFINITY ? 0.f : expf(l - m), sum = ex;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(MEP_FULL_MASK, sum, d);

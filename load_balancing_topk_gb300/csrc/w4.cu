@@ -96,7 +96,8 @@ __device__ __forceinline__ constexpr int row_of(int h, int j, int r, int t) { re
 
 constexpr float kRoundShift = 12582912.f;  // 1.5 * 2^23
 
-// q of x: x / s to the nearest whole number. `once`: one correction is enough.
+// q of x: x / s to the nearest whole number. `ONCE`: one correction is enough.
+// (Two at a time in packed fp32 it took 279 us where this takes 255.)
 template <bool ONCE> __device__ __forceinline__ float quotient(float x, float s, float inv) {
   float q = x * inv;
   q = fmaf(fmaf(-q, s, x), inv, q);

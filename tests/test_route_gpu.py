@@ -73,6 +73,21 @@ def test_values(kind, dtype, skip, N, E, K):
     check(t, x, K, None, skip)
 
 
+@pytest.mark.parametrize("E", [20, 300, 700])
+def test_every_nan_is_the_same_and_on_top(E):
+    """Negative ones and ones with payloads too."""
+    x = torch.zeros(4, E)
+    bits = x.view(torch.int32)
+    bits[0, 5], bits[0, 3], bits[0, 7] = 0x7FC00000, -(1 << 22), 0x7F800001
+    x[1, 4], x[1, 2] = float("inf"), float("-inf")
+    bits[1, 6] = -1
+    bits[2, 0], bits[2, 1] = -(1 << 31), 0
+    bits[3, 9] = -(1 << 23) + 1
+    idx, w = mep.mep_route(x.cuda(), 3)
+    assert idx.tolist() == [[3, 5, 7], [6, 4, 0], [0, 1, 2], [9, 0, 1]]
+    assert torch.isnan(w[[0, 1, 3]]).all() and (w[2] - 1 / 3).abs().max() < 1e-6
+
+
 @pytest.mark.parametrize("E,K", [(256, 8), (64, 6), (128, 32), (100, 3), (200, 33)])
 @pytest.mark.parametrize("values", [1, 2, 3, 5, 9, 17, 33, 100])
 def test_few_different_values(E, K, values):
