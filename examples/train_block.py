@@ -2,7 +2,7 @@
 
     python examples/train_block.py [--steps 20] [--tokens 1024]
 
-Forward: layer norm -> router -> plan -> dispatch -> two grouped products with
+Forward: layer norm -> router product and choice -> plan -> dispatch -> two grouped products with
 the gated activation between them -> combine, added to the residual stream.
 Backward: the gradients of all of it; the experts' weight gradients land in the
 home experts' and slots' fp32 tensors and mep_reduce_grad folds them together.
@@ -73,8 +73,7 @@ class Block:
         P = self.params
         y, self.mean, self.rstd = mep.mep_layer_norm(x, P["norm_w"], P["norm_b"], x_ckpt=self.kept["x"],
                                                      y_ckpt=self.kept["y"])
-        top, idx = torch.topk(y.float() @ P["router"], self.K, dim=1)
-        self.idx, self.weight = idx.to(torch.int32), torch.softmax(top, 1)
+        self.idx, self.weight = mep.mep_route(y.float() @ P["router"], self.K)
         self.plan = p = mep.mep_plan(self.idx, self.R, self.S, self.K, self.E, self.B)
         buf = mep.mep_dispatch(y, p.dst_pos, p.status, self.R, self.S, self.K)
         a = mep.mep_swiglu(self._product(buf, "w1"), ckpt=self.kept["gu"])
@@ -97,8 +96,7 @@ class Block:
             mep.mep_reduce_grad(p.slot_expert, G[name], self.slot_grad[name], p.status, E)
         dy = mep.mep_dispatch_backward(dbuf, p.dst_pos, p.status, R, S, K).float()
         # the router: softmax over the chosen logits, then a dense product
-        dtop = self.weight * (dweight - (self.weight * dweight).sum(1, keepdim=True))
-        dlogits = torch.zeros(R * S, E, device=dy.device).scatter_(1, self.idx.long(), dtop)
+        dlogits = mep.mep_route_backward(dweight, self.weight, self.idx, E)
         y = mep.mep_ckpt_load(self.kept["y"], self.H)
         G["router"].copy_(y.float().t() @ dlogits)
         dy += dlogits @ P["router"].t()
