@@ -543,11 +543,12 @@ MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
  * bias, has none):
  *   dlogits[t, topk_idx[t,k]] = topk_w[t,k] * (dtopk_w[t,k] - sum_j topk_w[t,j] dtopk_w[t,j])
  * in fp32, rounded once, and 0 for every other expert. An expert that stands
- * twice in a row gets both; -1 gets none.
+ * twice in a row gets both; -1 gets none and is left out of the sum, whatever
+ * its dtopk_w holds.
  *   dtopk_w, topk_w  fp32 [N, K];  topk_idx int32 [N, K]
  *   status   int32 [1]             read on entry (nonzero: no-op); set to
  *                                  MEP_ERR_BAD_ROUTING if an index is outside
- *                                  [-1, E) (it gets none). May be NULL.
+ *                                  [-1, E) (it counts as -1). May be NULL.
  *   dlogits  bf16 or fp32 [N, E]   type; output, every element written
  * Outputs must not overlap the inputs or one another. N < 2^31.
  * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
@@ -597,7 +598,8 @@ MEP_API int mep_w4_load(const uint8_t* w4, int64_t M, int64_t K, int64_t N, int 
  * matrix in 4 bits. The products x * q are exact, a group's are added in fp32
  * (by the tensor cores, order fixed), times its scale and added up in fp32; y
  * is rounded once. The same call gives the same bits.
- *   x       bf16 [T, K]    0 <= T <= MEP_MAX_FEW
+ *   x       bf16 [T, K]    0 <= T <= MEP_MAX_FEW (device memory of the current
+ *                          device; ws too where K is not a multiple of 8)
  *   w4      uint8 [mep_w4_bytes(K, N, group)]   from mep_w4_save, parts 1
  *   status  int32 [1]      read on entry (nonzero: no-op); set to
  *                          MEP_ERR_TIMEOUT if a pipeline wait gives up. May be NULL.

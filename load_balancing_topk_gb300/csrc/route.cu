@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) k_route_backward(const float* __rest
     for (int i = 0; i < 2; ++i) {
       wk[i] = wn[i], dk[i] = dn[i], at[i] = an[i];
       if (at[i] < -1 || at[i] >= E) bad = true, at[i] = -1;
-      sum += 32 * i + lane < K ? wk[i] * dk[i] : 0.f;
+      sum += at[i] >= 0 ? wk[i] * dk[i] : 0.f;
     }
     load(row + step);
 #pragma unroll

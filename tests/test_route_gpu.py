@@ -177,6 +177,21 @@ def test_backward_repeated_and_bad_indices():
     assert (keep == 9).all()
 
 
+@pytest.mark.parametrize("E,K", [(8, 4), (40, 35)])
+def test_backward_leaves_out_what_was_not_chosen(E, K):
+    """A place of -1 may hold anything: NaN in its gradient or its weight reaches no logit."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = torch.randn(9, E, generator=g, device="cuda")
+    logits[2, 3:] = -float("inf")
+    logits[5] = -float("inf")
+    idx, w = mep.mep_route(logits, K, skip_masked=True)
+    dw = torch.randn(9, K, generator=g, device="cuda")
+    want = mep.mep_route_backward(dw, w, idx, E)
+    dw[idx < 0] = float("nan")
+    assert bool((idx < 0).any()) and torch.equal(mep.mep_route_backward(dw, w, idx, E), want)
+    assert torch.equal(mep.mep_route_backward(dw, w.masked_fill(idx < 0, float("nan")), idx, E), want)
+
+
 def test_many_rows_and_another_stream():
     N, E, K = 200003, 16, 2
     side = torch.cuda.Stream()
