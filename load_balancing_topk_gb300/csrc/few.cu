@@ -8,17 +8,19 @@
 // products, the joins and the barriers between the layer's two products happen
 // behind it.
 //
-// A unit of work is 128 columns of one expert (64 gate and the 64 matching up
-// columns, or 128 columns of the second product) times the expert's tokens; a
-// step is a stage's share of a unit's sum. The steps of all units in a row are
-// cut into equal runs, one a CTA, so that every SM reads as many bytes as the
-// others whatever the number of experts and columns; a unit that is cut leaves
-// a partial sum in each of its CTAs, in fp32 in the workspace, joined in order
-// after a barrier of the grid (1.3 us, and the ring of the second product fills
-// meanwhile). One cooperative launch for the layer: three barriers, in
-//   products 1 | activation | products 2 | weighted sum over the token's experts.
+// A unit of work is 256 columns of one expert (128 gate and the 128 matching up
+// columns, or 256 columns of the second product) times the expert's tokens, up
+// to 32 in the layer; a step is a stage's share of a unit's sum: 64 rows of bf16
+// (32 KB), 256 of 4 bits (34 to 40 KB). The steps of all units in a row are cut
+// into runs without regard to where units end, so that every SM reads about as
+// many bytes as the others whatever the number of experts and columns (Phase);
+// a unit that is cut leaves a partial sum for each of its runs, in fp32 in the
+// workspace, joined in order after a barrier of the grid (1.3 us, and the ring of
+// the second product fills meanwhile). One cooperative launch for the layer:
+//   products 1 | activation | products 2 | weighted sum over the token's experts
+// with a barrier at each stroke, and one more in front where runs are counted.
 // Which experts are in use and which tokens they have, every CTA finds out by
-// itself from topk_idx (a 64-bit mask of tokens for each expert).
+// itself from topk_idx (a 64-bit mask of tokens for each expert; 2.8 us).
 //
 // Tensor cores: mma.sync m16n8k16 with the weights as the 16-row operand and
 // eight tokens as the columns, fp32 sums. (tcgen05 takes its operands from
@@ -26,11 +28,31 @@
 // rate are short here; and weights in 4 bits have to pass through registers,
 // where this instruction takes them.) Weights in bf16 are read from the
 // swizzled stage by transposing ldmatrix; in 4 bits a lane's 16 bytes are its
-// operand of four steps (w4.cuh): a shift and a logic operation put two of them
-// behind bf16's 128, a packed subtraction of 136 leaves q exactly, and the
-// scale multiplies the group's fp32 sums.
+// operand of four steps (w4.cuh): a mask and a packed multiply-add make two of
+// them q / 64 exactly, and the scale multiplies the group's fp32 sums.
 // The activation is kept as two bf16, the value rounded and what that left
-// over, and the second product takes both: it is then off by 2^-17, not 2^-9.
+// over, and the second product takes both: it is then off by 2^-16 at most,
+// where one bf16 would be off by 2^-8. bf16 x bf16 is exact in fp32.
+//
+// Measured, as one node of a graph, L2 flushed before it (back to back):
+//   64 tokens, 256 experts, 7168 x 1408, 8 each, bf16: 12.2 GB of weights in
+//     1750 to 1790 us (1710 to 1750), 6.8 to 7.1 TB/s; the same without the products.
+//   16 tokens of it in 4 bits: 1.24 GB in 281 us (265). Without the products the
+//     copies take 226, without the copies the products 244: a stage's 65536
+//     weights keep eight warps busy for some 1200 clocks, in which they issue
+//     nine operations for eight weights to widen them, and a unit's sums cost 700
+//     to 2000 more. Sixteen warps of half the columns each took 294, where eight
+//     took 283; both blocks of a stage in one go 308, where one after another took
+//     302.
+//   1 token in 4 bits: 125 MB in 48 us (43); 1 token, 64 experts, 2048 x 1408, 6
+//     each, bf16: 104 MB in 40 us (32). A launch with its first loads is some 5,
+//     the list 2.8, a barrier 1.3; the rest is the stream with its start and its
+//     slowest SM (some read a fifth slower than others).
+//   A call of a few small experts 19 us (16): all latency. What helped there is
+//     that the code is run through before its data is there (products(), k_layer).
+//   [1, 7168] x [7168, 7168] in 4 bits 22 us (17.5), [64, 2048] x [2048, 65536]
+//     74 us (70), without the products 40: at 64 rows they are 34 us of the
+//     tensor pipe, and x comes from L2 once a step.
 
 #include <cooperative_groups.h>
 
@@ -48,10 +70,9 @@ constexpr int kLayerThreads = 32 * (kWarps + 2);  // and one that runs ahead thr
 constexpr int kUnit = 256;          // columns of a unit
 constexpr int kPanels = kUnit / kW4Cols;
 constexpr int kPanelRow = 128;      // bytes of a stage's row of 64 bf16 columns
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 8;
 constexpr int kSmem = 227 * 1024;
 constexpr int kChunk = 32;          // tokens of an expert that one unit takes in the layer
-constexpr uint32_t kEnd = 0xffffffffu;
 
 // The kernels go by the weights' group: 0 for bf16, else 32, 64 or 128 rows of
 // a column in 4 bits.
@@ -146,13 +167,22 @@ __device__ __forceinline__ uint32_t parts_in(const Phase& p, uint32_t unit) {
 }
 
 // ---------------------------------------------------------------------------
+// What a CTA's warps have to know of a unit, or of the part of one that is in a
+// run. The producer, which waits for room most of the time, works it out. Where
+// each of the eight other warps did, a part began with 1100 clocks, now 400, and a
+// step takes 1200 (16 tokens of the large layer in 4 bits 302 us, 285 this way).
+struct __align__(16) Part {
+  int steps, left, rows, columns;  // 0: the end; rows of the sum from its first step on; of x; columns of the unit on
+  long long to;                    // its first sum's number
+  long long none;
+};
 // The ring of stages.
 struct Ring {
   uint32_t full, empty;         // barriers, 8 bytes each
   uint32_t stage0, stage_bytes; // first stage
   uint32_t x_at;                // of a stage: where the rows of x start
   int stages;
-  volatile uint32_t* step;      // of a stage: which step it holds, or kEnd
+  struct Part* part;            // of a stage that a part starts with
   volatile int* abort;
   int32_t* status;
 };
@@ -184,12 +214,11 @@ struct Rows {
   int K;                  // bf16 of a row
   int planes;
 };
-// Where a product's partial sums go: rows' parts of `pitch` floats.
+// Where a product's sums go: rows' parts of `pitch` of them.
 struct Sums {
-  float* p;
   uint32_t pitch;
-  int unit, half;      // columns from unit to unit, from a unit's first half to its second
-  int limit, counted;  // j * unit + column + (half & counted) is below limit where a column is there
+  int unit, half;    // columns from unit to unit, from a unit's first half to its second
+  int limit, inner;  // j * unit + column + (of the second half) inner is below limit where a column is there
 };
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -216,6 +245,11 @@ __device__ __forceinline__ void arrive(uint32_t bar) {
 __device__ __noinline__ void grid_barrier() { cooperative_groups::this_grid().sync(); }
 // Rows that a stage has room for (as many as a unit's instantiation computes).
 __device__ __forceinline__ int tile_rows(int rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok;
+}
 // A whole warp waits; the same answer in every lane.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const Ring& r) {
   if (__all_sync(MEP_FULL_MASK, mbar_try_wait_long(bar, parity))) return true;
@@ -235,6 +269,9 @@ template <int G, bool TILES> struct Stream {
   Phase p;
   Weights w;
   Rows x;
+  Sums o;
+  uint32_t run_part = 0;       // which part of its unit the run starts with
+  bool fresh = false;          // a part starts with this step
   uint32_t step = 0, end = 0;  // of the run
   uint32_t s, j, entry;        // step of the unit, unit of the expert, the expert's entry
   uint32_t tx;                 // bytes of a full step's weights
@@ -247,7 +284,7 @@ template <int G, bool TILES> struct Stream {
       : r(ring), expert(e_), start(s_) {}
   __device__ __forceinline__ void unit() {
     const int lane = threadIdx.x & 31, first = start[entry], panel = j * w.unit, pl = x.planes - 1;
-    rows_n = (start[entry + 1] - first) << pl, e = expert[entry];
+    rows_n = (start[entry + 1] - first) << pl, e = expert[entry], fresh = true;
     if (TILES) rows_n = tile_rows(rows_n);
     const int count = (w.columns + kW4Cols - 1) / kW4Cols - panel;
     panels = w.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
@@ -268,21 +305,29 @@ template <int G, bool TILES> struct Stream {
     if (step >= end) return;
     const uint32_t u = p.by_ks(step);
     s = step - u * p.ks, entry = p.by_nb(u), j = u - entry * p.nb;
+    run_part = p.parts == 1 ? 0 : run - run_at(p, u * p.ks);
     unit();
   }
-  __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_) {
-    p = p_, w = w_, x = x_;
+  __device__ __forceinline__ void own(const Phase& p_, const Weights& w_, const Rows& x_, const Sums& o_) {
+    p = p_, w = w_, x = x_, o = o_;
     seek(blockIdx.x);
   }
   __device__ __forceinline__ void next() {
+    fresh = false;
     if (++step == end || ++s < p.ks) return;
-    s = 0;
+    s = 0, run_part = 0;
     if (++j == p.nb) j = 0, ++entry;
     unit();
   }
   __device__ __forceinline__ void weights(int slot) const {  // one lane
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
-    r.step[slot] = step;
+    if (fresh) {
+      const int first = start[entry], n = (start[entry + 1] - first) * x.planes;
+      Part part;
+      part.steps = min(p.ks - s, end - step), part.left = w.K - int(s * BK), part.rows = n, part.columns = o.limit - int(j) * o.unit;
+      part.to = ((long long)first * p.parts + run_part) * o.pitch + j * o.unit, part.none = 0;
+      r.part[slot] = part;
+    }
     if (G == 0) {
       constexpr uint32_t bytes = step_rows(G) * kPanelRow;
       const int col = j * w.unit * kW4Cols, k = s * BK;
@@ -369,7 +414,7 @@ template <int G, bool TILES> struct Stream {
     }
     if (!warp_wait(r.empty + 8 * c.slot, c.parity ^ 1, r)) return;
     if (lane == 0) {
-      r.step[c.slot] = kEnd;
+      r.part[c.slot].steps = 0;
       arrive(r.full + 8 * c.slot);
       arrive(r.full + 8 * c.slot);
     }
@@ -459,38 +504,31 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
       }
     }
   } else {
-    // Everything that a block of 128 rows needs of the stage is asked for at once
-    // (with more than 32 columns the block is gone through again), with eight
-    // columns both blocks' at once.
+    // Everything that a block of 128 rows needs of the stage is asked for at once;
+    // with more than 32 rows of x the block is gone through again.
     constexpr int NS = NT < 4 ? NT : 4, block = w4_block_bytes(G > 0 ? G : 128), per = G > 0 ? G / 32 : 1;  // groups: per * 32 rows
-    constexpr int ahead = 1;
-    uint4 w[ahead][2][2];
-    uint32_t x[ahead][4][NT <= 2 ? NS : 1][4], scale[ahead][4][2];
+    constexpr bool early = NT <= 2;                                                                       // x too
+    uint4 w[2][2];
+    uint32_t x[early ? 4 : 1][early ? NS : 1][4], scale[4][2];
 #pragma unroll
     for (int i = 0; i < 2 * (NT / NS); ++i) {
-      const int n0 = (i >> 1) * NS;
-      if ((i & 1) >= blocks) continue;
+      const int n0 = (i >> 1) * NS, b = i & 1;
+      if (b >= blocks) continue;
+      const uint32_t wb = stage + (warp >> 2) * 2 * block + b * block;
+      const uint32_t at = wb + ((warp & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((warp & 3) * 8 + (lane >> 2)) * 4;
 #pragma unroll
-      for (int o = 0; o < ahead; ++o) {
-        const int b = (i & 1) + o;
-        if (ahead == 2 && i > 0) break;
-        const uint32_t wb = stage + (warp >> 2) * 2 * block + b * block;
-        const uint32_t at = wb + ((warp & 3) * 32 + lane) * 16, sb = wb + kW4Pairs + ((warp & 3) * 8 + (lane >> 2)) * 4;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[o][h][0] = lds128(at + 2048 * h), w[o][h][1] = lds128(at + 2048 * h + 4 * block);
-        if (NT <= 2) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int n = 0; n < NS; ++n) ldmatrix4(x[o][k][n], x_at(n0 + n, 128 * b + 32 * k));
-        }
+      for (int h = 0; h < 2; ++h) w[h][0] = lds128(at + 2048 * h), w[h][1] = lds128(at + 2048 * h + 4 * block);
+      if (early) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if ((k + 1) % per == 0)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) scale[o][k][q] = lds32(sb + k / per * 128 + q * 4 * block);
+          for (int n = 0; n < NS; ++n) ldmatrix4(x[k][n], x_at(n0 + n, 128 * b + 32 * k));
       }
-      const int o = ahead == 2 ? i & 1 : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if ((k + 1) % per == 0)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) scale[k][q] = lds32(sb + k / per * 128 + q * 4 * block);
       float sum[2][NS][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // 32 rows
@@ -499,13 +537,13 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
         for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const uint4& v = w[o][k >> 1][q];
+            const uint4& v = w[k >> 1][q];
             widen_q(k & 1 ? (s ? v.w : v.z) : (s ? v.y : v.x), a[q][s]);
           }
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-          if (NT > 2) ldmatrix4(x[0][0][0], x_at(n0 + n, 128 * (i & 1) + 32 * k));
-          const uint32_t(&f)[4] = NT <= 2 ? x[o][k][n] : x[0][0][0];
+          if (!early) ldmatrix4(x[0][0], x_at(n0 + n, 128 * b + 32 * k));
+          const uint32_t(&f)[4] = early ? x[k][n] : x[0][0];
 #pragma unroll
           for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -519,7 +557,7 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
         if ((k + 1) % per == 0) {  // a group ends
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float lo = __uint_as_float(scale[o][k][q] << 16), hi = __uint_as_float(scale[o][k][q] & 0xffff0000u);
+            const float lo = __uint_as_float(scale[k][q] << 16), hi = __uint_as_float(scale[k][q] & 0xffff0000u);
 #pragma unroll
             for (int n = 0; n < NS; ++n) {
               float(&to)[4] = acc[q][n0 + n];
@@ -535,12 +573,10 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
   }
 }
 
-// `steps` steps of one unit from its step s on, then their sums out. PUT(half,
-// column of the half, row, two values: of this row of x and the next one).
-// `dry`: see products().
+// The steps of a part, then their sums out. PUT(half, column of the half, row, two
+// values: of this row of x and the next one). `dry`: see products().
 template <int G, bool TILES, int NT, typename Put>
-__device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, const Ring& r, Cursor& c, int rows,
-                                             bool dry, Put put) {
+__device__ __forceinline__ bool unit_product(int steps, int left, const Ring& r, Cursor& c, int rows, bool dry, Put put) {
   constexpr int BK = step_rows(G);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float acc[2][NT][4];
@@ -548,10 +584,14 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[q][n][0] = acc[q][n][1] = acc[q][n][2] = acc[q][n][3] = 0.f;
+  bool there = true;  // the part's start has been waited for
 #pragma unroll 1
-  for (; steps > 0; --steps, ++s) {
-    if (!dry && !warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
-    const int blocks = G != 0 ? (K - int(s * BK) + kW4Rows - 1) / kW4Rows : 0;
+  for (; steps > 0; --steps, left -= BK) {
+    if (!dry && !__all_sync(MEP_FULL_MASK, there) && !warp_wait(r.full + 8 * c.slot, c.parity, r)) return false;
+    Cursor after = c;
+    after.next(r.stages);
+    there = !dry && steps > 1 && mbar_test(r.full + 8 * after.slot, after.parity);  // asked for while this step is worked on
+    const int blocks = G != 0 ? (left + kW4Rows - 1) / kW4Rows : 0;
     stage_product<G, TILES, NT>(acc, r.stage0 + c.slot * r.stage_bytes, r, warp, blocks, tile_rows(rows));
     __syncwarp();
     if (dry) continue;
@@ -575,38 +615,32 @@ __device__ __forceinline__ bool unit_product(uint32_t steps, uint32_t s, int K, 
   return true;
 }
 
-// All steps that this CTA is fed, of `planes` rows of x a token. PUT(first row of
-// the list, unit of the expert, part, rows, and as above). What a kernel executes
-// for the first time comes from far away, at some 25 ns an instruction: dry, the
-// code is run through once, on whatever the first stage holds and to no effect,
-// while that stage's bytes are on their way.
+// All steps that this CTA is fed, of up to `most` rows of x a unit. PUT(part, and
+// as above). What a kernel executes for the first time comes from far away, at
+// some 25 ns an instruction: dry, the code is run through once, on whatever the
+// first stage holds and to no effect, while that stage's bytes are on their way.
 enum Run { kReal, kDry, kDryThenReal };
 template <int G, bool TILES, int NTMAX, typename Put>
-__device__ __forceinline__ void products(const Phase& p, int K, int planes, const Ring& r, Cursor& c,
-                                         const uint16_t* start, Run how, int most, Put put) {
+__device__ __forceinline__ void products(const Ring& r, Cursor& c, Run how, int most, Put put) {
   bool dry = how != kReal;
 #pragma unroll 1
   while (true) {
-    uint32_t at = 0;
+    Part part = {1, step_rows(G), most, 0, 0, 0};
     if (!dry) {
       if (!warp_wait(r.full + 8 * c.slot, c.parity, r)) return;
-      at = r.step[c.slot];
-      if (at == kEnd) break;
+      part = r.part[c.slot];
+      if (part.steps == 0) break;
     }
-    const uint32_t u = p.by_ks(at), s = at - u * p.ks, run = p.parts == 1 ? 0 : run_at(p, at);
-    const uint32_t steps = dry ? 1 : p.parts == 1 ? p.ks - s : min(p.ks - s, run_start(p, run + 1) - at);
-    const uint32_t e = p.by_nb(u), j = u - e * p.nb, part = p.parts == 1 ? 0 : run - run_at(p, u * p.ks);
-    const int first = start[e], rows = planes * (dry ? most : start[e + 1] - first);
-    const auto f = [&](int q, int col, int row, float v0, float v1) { put(first, j, part, rows, q, col, row, v0, v1); };
+    const auto f = [&](int q, int col, int row, float v0, float v1) { put(part, q, col, row, v0, v1); };
     bool ok;
-    if (rows <= 8)
-      ok = unit_product<G, TILES, 1>(steps, s, K, r, c, rows, dry, f);
-    else if (rows <= 16)
-      ok = unit_product<G, TILES, 2>(steps, s, K, r, c, rows, dry, f);
-    else if (NTMAX <= 4 || rows <= 32)
-      ok = unit_product<G, TILES, 4>(steps, s, K, r, c, rows, dry, f);
+    if (part.rows <= 8)
+      ok = unit_product<G, TILES, 1>(part.steps, part.left, r, c, part.rows, dry, f);
+    else if (part.rows <= 16)
+      ok = unit_product<G, TILES, 2>(part.steps, part.left, r, c, part.rows, dry, f);
+    else if (NTMAX <= 4 || part.rows <= 32)
+      ok = unit_product<G, TILES, 4>(part.steps, part.left, r, c, part.rows, dry, f);
     else
-      ok = unit_product<G, TILES, NTMAX>(steps, s, K, r, c, rows, dry, f);
+      ok = unit_product<G, TILES, NTMAX>(part.steps, part.left, r, c, part.rows, dry, f);
     if (!ok || how == kDry) return;
     dry = false;
   }
@@ -625,7 +659,7 @@ template <int G, bool TILES> __device__ __forceinline__ void size_ring(Ring& r, 
 
 struct Head {  // start of shared memory
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint32_t step[kMaxStages];
+  Part part[kMaxStages];
   int warp_sums[32];
   int abort, bad, most, rows, go;
   Phase phase[2];
@@ -634,7 +668,7 @@ constexpr uint32_t kHeadBytes = 1024;
 
 __device__ __forceinline__ void init_names(Ring& r, Head* h, int32_t* status) {
   r.full = smem_u32(h->full), r.empty = smem_u32(h->empty);
-  r.step = h->step, r.abort = &h->abort, r.status = status;
+  r.part = h->part, r.abort = &h->abort, r.status = status;
 }
 __device__ __forceinline__ void init_ring(Ring& r, Head* h, int32_t* status) {
   init_names(r, h, status);
@@ -784,6 +818,8 @@ template <int G> __device__ __forceinline__ Weights first_weights(const LayerArg
   const long long m = G != 0 ? w4_matrix_bytes(a.H, a.F, G) : 0, q = G != 0 ? w4_panel_bytes(a.H, G) : 0;
   return {map, a.w1, 2 * m, q, m, 2, a.F, a.F, true, a.H};
 }
+__device__ __forceinline__ Sums first_sums(const LayerArgs& a) { return {2u * a.F, kUnit / 2, a.F, a.F, 0}; }
+__device__ __forceinline__ Sums second_sums(const LayerArgs& a) { return {uint32_t(a.H), kUnit, kUnit / 2, a.H, kUnit / 2}; }
 template <int G> __device__ __forceinline__ Weights second_weights(const LayerArgs& a, const CUtensorMap* map) {
   const long long m = G != 0 ? w4_matrix_bytes(a.F, a.H, G) : 0, q = G != 0 ? w4_panel_bytes(a.F, G) : 0;
   return {map, a.w2, m, q, 2 * q, 4, 2 * kW4Cols, a.H, false, a.F};
@@ -913,7 +949,8 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     const Phase &p1 = h->phase[0], &p2 = h->phase[1];
     Stream<G, false> t(r, l.expert, l.start);
     Cursor behind;
-    t.own(p1, first_weights<G>(a, &map1), {nullptr, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1});
+    t.own(p1, first_weights<G>(a, &map1), {nullptr, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1},
+          first_sums(a));
     t.ahead(c, true);
     if (counted) grid_barrier();
 #pragma unroll 1
@@ -921,7 +958,8 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
       t.feed(c, behind, phase == 1, a.counters + phase);
       if (phase == 0) {  // the ring fills while the activation is computed
         behind = c;
-        t.own(p2, second_weights<G>(a, &map2), {nullptr, reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2});
+        t.own(p2, second_weights<G>(a, &map2), {nullptr, reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2},
+              second_sums(a));
         t.ahead(c, false);
         grid_barrier();
       }
@@ -942,18 +980,17 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
       const bool dry = phase < -1, second = dry ? phase == -2 : phase == 1;
       const Phase& p = h->phase[second];
       if (!dry) {
-        const Sums o = second ? Sums{a.part2, uint32_t(a.H), kUnit, kUnit / 2, a.H, -1}
-                              : Sums{a.part1, 2u * a.F, kUnit / 2, a.F, a.F, 0};
-        products<G, false, kChunk / 4>(
-            p, second ? a.F : a.H, second ? 2 : 1, r, c, l.start, phase < 0 ? kDry : kReal, 1,
-            [&](int first, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
-              const int n = j * o.unit + col, off = q * o.half;
-              if (n + (off & o.counted) >= o.limit) return;
-              // the two rows: the activation's two of one token; else two tokens
-              float* to = o.p + ((long long)(first + (second ? row >> 1 : row)) * p.parts + part) * o.pitch + n + off;
-              *to = second ? v0 + v1 : v0;
-              if (!second && row + 1 < rows) to[p.parts * o.pitch] = v1;
-            });
+        const Sums o = second ? second_sums(a) : first_sums(a);
+        float* out = second ? a.part2 : a.part1;
+        const uint32_t pitch = p.parts * o.pitch;
+        products<G, false, kChunk / 4>(r, c, phase < 0 ? kDry : kReal, 1,
+                                       [&](const Part& part, int q, int col, int row, float v0, float v1) {
+                                         if (col + q * o.inner >= part.columns) return;
+                                         // the two rows: the activation's two of one token; else two tokens
+                                         float* to = out + part.to + (long long)(second ? row >> 1 : row) * pitch + q * o.half + col;
+                                         *to = second ? v0 + v1 : v0;
+                                         if (!second && row + 1 < part.rows) to[pitch] = v1;
+                                       });
         if (phase < 0) {
           list_made();
           if (counted) grid_barrier();
@@ -1035,12 +1072,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const __grid_constan
     }
     fence_async();
   };
+  const Sums o = {uint32_t(a.N), kUnit, kUnit / 2, a.N, kUnit / 2};
   Cursor c;
   if (producer) {
     Stream<G, true> t(r, expert, start);
     const Cursor behind;
     const long long panel = w4_panel_bytes(a.K, G);
-    t.own(p, {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K}, {&map_x, nullptr, nullptr, 0, K8, 1});
+    t.own(p, {nullptr, a.w4, 0, panel, 2 * panel, 4, 0, a.N, false, a.K}, {&map_x, nullptr, nullptr, 0, K8, 1}, o);
     t.ahead(c, !pad);
     if (pad) copy_rows();
     if (first_barrier) grid_barrier();
@@ -1049,19 +1087,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_w4_product(const __grid_constan
   } else {
     if (pad) copy_rows();
     if (first_barrier) grid_barrier();
-    products<G, true, NTMAX>(p, a.K, 1, r, c, start, kDryThenReal, a.T,
-                             [&](int, uint32_t j, uint32_t part, int rows, int q, int col, int row, float v0, float v1) {
-                               const int n = j * kUnit + q * (kUnit / 2) + col;
-                               if (n >= a.N) return;
-                               if (p.parts == 1) {
-                                 put_y(a, (long long)row * a.N + n, v0);
-                                 if (row + 1 < rows) put_y(a, (row + 1LL) * a.N + n, v1);
-                               } else {
-                                 float* to = a.part + ((long long)row * p.parts + part) * a.N + n;
-                                 *to = v0;
-                                 if (row + 1 < rows) to[(long long)p.parts * a.N] = v1;
-                               }
-                             });
+    const long long pitch = (long long)p.parts * a.N;
+    products<G, true, NTMAX>(r, c, kDryThenReal, a.T, [&](const Part& part, int q, int col, int row, float v0, float v1) {
+      if (col + q * o.inner >= part.columns) return;
+      const long long at = part.to + row * pitch + q * o.half + col;
+      if (!joined) {
+        put_y(a, at, v0);
+        if (row + 1 < part.rows) put_y(a, at + pitch, v1);
+      } else {
+        a.part[at] = v0;
+        if (row + 1 < part.rows) a.part[at + pitch] = v1;
+      }
+    });
   }
   if (joined) {
     grid_barrier();
@@ -1169,7 +1206,8 @@ bool layer_space(int T, int K, int E, long long H, long long F, int w_type, int 
 
 // Whether a product's runs are its units: where that leaves no more than a fifth
 // of the SMs idle in the last round, for partial sums cost a write and a read of
-// the output and a barrier ([64, 2048] x [2048, 65536]: DETAIL).
+// the output and a barrier ([64, 2048] x [2048, 65536]: 99 us with them, 74
+// without).
 bool whole_product(long long N) {
   const long long units = ceil_div(N, kUnit), rounds = ceil_div(units, kMaxCtas);
   return rounds * kMaxCtas * 4 <= units * 5;
@@ -1229,6 +1267,7 @@ extern "C" int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* sta
   const cuuint64_t dims[2] = {cuuint64_t(K8), cuuint64_t(T)}, strides[1] = {cuuint64_t(K8) * 2};
   const cuuint32_t box[2] = {64, T <= 8 ? 8u : T <= 16 ? 16u : T <= 32 ? 32u : 64u}, estr[2] = {1, 1};
   void* from = K % 8 == 0 ? const_cast<mep_bf16*>(x) : static_cast<void*>(p);
+  if (!on_current_device(from)) return MEP_ERR_INVALID_ARG;
   if (fn == nullptr || fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, from, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -1261,7 +1300,8 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
   char* p = static_cast<char*>(ws) + kCounters;
   const int bk = step_rows(w_type == MEP_W4 ? group : 0);
   const long long steps1 = ceil_div(H, bk) * ceil_div(F, kUnit / 2), steps2 = ceil_div(F, bk) * ceil_div(H, kUnit);
-  const int counted = max_entries(T, K, E) * (steps1 > steps2 ? steps1 : steps2) > kOneRun * (long long)ctas();
+  // fewer SMs take the runs that are sized for kMaxCtas as they come
+  const int counted = ctas() < kMaxCtas || max_entries(T, K, E) * (steps1 > steps2 ? steps1 : steps2) > kOneRun * (long long)kMaxCtas;
   const LayerArgs a = {reinterpret_cast<const __nv_bfloat16*>(x),
                        topk_idx,
                        topk_w,
