@@ -633,8 +633,8 @@ MEP_API int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* status
  *                            batch); a token without any gets zeros
  *   topk_w   fp32 [T, K]     used as given
  *   w1, w2   w_type MEP_BF16: bf16 [E, H, 2F] (gate columns, then up columns)
- *            and [E, F, H], as mep_grouped_gemm takes them (device memory of
- *            the current device); MEP_W4: uint8
+ *            and [E, F, H], as mep_grouped_gemm takes them (these, x and ws
+ *            device memory of the current device); MEP_W4: uint8
  *            [E, 2, mep_w4_bytes(H, F, group)] and [E, mep_w4_bytes(F, H, group)]
  *   group    of MEP_W4; not read for MEP_BF16
  *   status   int32 [1]       read on entry (nonzero: no-op); set to

@@ -204,8 +204,13 @@ struct Weights {
   bool gated;                       // the halves are gate and up columns, each counted to `columns`
   int K;                            // rows
 };
-// Rows of x: `planes` of them after one another (the activation's two). Given a
-// map, tiles of rows one after another instead of row by row.
+// Rows of x: `planes` of them after one another (the activation's two). They come
+// in tiles of 64 columns, 128-byte swizzled: in the product all rows in one copy
+// (x is the map's, its box the tile), in the layer from bf16 four rows of the list
+// in one or, of the activation, whose rows are in the list's order, eight (a lane
+// issues a copy in some 80 clocks: 64 tokens, 8 each of 32 experts, 7168 x 1408,
+// row by row 515 us, so 376). In 4 bits, where a step has four times the columns
+// and tiles would be four times as many copies, the layer copies row by row.
 struct Rows {
   const CUtensorMap* map;
   const char* p;
@@ -231,6 +236,14 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Four rows, 64 columns from x on.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], "
+      "[%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void bulk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -279,12 +292,18 @@ template <int G, bool TILES> struct Stream {
   const uint8_t* unit_w;       // 4 bits: the unit's first panel
   const char* row[2];          // this lane's rows of x
   uint32_t at[2];              // and where they go in a stage
+  int y[4];                    // rows of this lane's copy of a tile
 
   __device__ __forceinline__ Stream(const Ring& ring, const uint16_t* e_, const uint16_t* s_)
       : r(ring), expert(e_), start(s_) {}
   __device__ __forceinline__ void unit() {
     const int lane = threadIdx.x & 31, first = start[entry], panel = j * w.unit, pl = x.planes - 1;
     rows_n = (start[entry + 1] - first) << pl, e = expert[entry], fresh = true;
+    if (TILES && G == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // beyond the last row the last one again: products of a column that no one reads
+        y[i] = x.token != nullptr ? x.token[first + min(4 * lane + i, rows_n - 1)] : 2 * first + 8 * lane;
+    }
     if (TILES) rows_n = tile_rows(rows_n);
     const int count = (w.columns + kW4Cols - 1) / kW4Cols - panel;
     panels = w.gated ? (count > 1 ? 15 : 5) : count >= 4 ? 15 : (1 << count) - 1;
@@ -347,6 +366,15 @@ template <int G, bool TILES> struct Stream {
   __device__ __forceinline__ void rows(int slot) const {  // the warp
     const int lane = threadIdx.x & 31, k0 = s * BK, bytes = 2 * min(BK, x.K - k0);
     const uint32_t bar = r.full + 8 * slot, dst = r.stage0 + slot * r.stage_bytes;
+    if (TILES && G == 0) {
+      if (lane == 0) mbar_expect_tx(bar, rows_n * BK * 2);
+      if (x.token != nullptr) {
+        if (lane < rows_n / 4) tma_gather4(dst + r.x_at + lane * 512, x.map, k0, y, bar);
+      } else {
+        if (lane < rows_n / 8) tma_2d(dst + r.x_at + lane * 1024, x.map, k0, y[0], bar);
+      }
+      return;
+    }
     if (TILES) {  // zeros beyond the rows and the sum's end
       if (lane == 0) {
         mbar_expect_tx(bar, rows_n * BK * 2);
@@ -908,7 +936,9 @@ __device__ __forceinline__ void combine(const LayerArgs& a, const Phase& p, cons
 
 template <int G>
 __global__ void __launch_bounds__(kLayerThreads, 1)
-    k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2, const LayerArgs a) {
+    k_layer(const __grid_constant__ CUtensorMap map1, const __grid_constant__ CUtensorMap map2,
+            const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_act, const LayerArgs a) {
+  constexpr bool TILES = G == 0;
   extern __shared__ __align__(1024) char smem[];
   Head* h = reinterpret_cast<Head*>(smem);
   Lists l;
@@ -937,7 +967,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     asm volatile("barrier.sync 0;" ::: "memory");
     init_names(r, h, a.status);
     r.stage0 = smem_u32(smem + used);
-    size_ring<G, false>(r, kSmem - used, 2 * min(h->most, kChunk));
+    size_ring<G, TILES>(r, kSmem - used, 2 * min(h->most, kChunk));
   };
   // How many barriers there are does not depend on what is read: every CTA comes
   // to all of them, whatever another stream does to the status word meanwhile.
@@ -947,9 +977,9 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
     list_made();
     if (h->go && h->bad && threadIdx.x == 32 * kWarps) set_status(a.status, MEP_ERR_BAD_ROUTING);
     const Phase &p1 = h->phase[0], &p2 = h->phase[1];
-    Stream<G, false> t(r, l.expert, l.start);
+    Stream<G, TILES> t(r, l.expert, l.start);
     Cursor behind;
-    t.own(p1, first_weights<G>(a, &map1), {nullptr, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1},
+    t.own(p1, first_weights<G>(a, &map1), {&map_x, reinterpret_cast<const char*>(a.x), l.token, 2LL * a.H, a.H, 1},
           first_sums(a));
     t.ahead(c, true);
     if (counted) grid_barrier();
@@ -958,7 +988,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
       t.feed(c, behind, phase == 1, a.counters + phase);
       if (phase == 0) {  // the ring fills while the activation is computed
         behind = c;
-        t.own(p2, second_weights<G>(a, &map2), {nullptr, reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2},
+        t.own(p2, second_weights<G>(a, &map2), {&map_act, reinterpret_cast<const char*>(a.act), nullptr, 2LL * a.F, a.F, 2},
               second_sums(a));
         t.ahead(c, false);
         grid_barrier();
@@ -983,7 +1013,7 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
         const Sums o = second ? second_sums(a) : first_sums(a);
         float* out = second ? a.part2 : a.part1;
         const uint32_t pitch = p.parts * o.pitch;
-        products<G, false, kChunk / 4>(r, c, phase < 0 ? kDry : kReal, 1,
+        products<G, TILES, kChunk / 4>(r, c, phase < 0 ? kDry : kReal, 1,
                                        [&](const Part& part, int q, int col, int row, float v0, float v1) {
                                          if (col + q * o.inner >= part.columns) return;
                                          // the two rows: the activation's two of one token; else two tokens
@@ -1185,6 +1215,17 @@ bool make_map3(CUtensorMap* m, const void* p, long long E, long long K, long lon
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2D bf16 map over [rows, columns], box {64 columns, box_rows}, 128-byte swizzle; beyond the edges zeros.
+bool make_map2(CUtensorMap* m, const void* p, long long rows, long long columns, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(columns), cuuint64_t(rows)}, strides[1] = {cuuint64_t(columns) * 2};
+  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 constexpr size_t kCounters = 256;  // bytes at the start
 
 // The layer's workspace: counters, partial sums of the first product, the activation, partial sums of the second.
@@ -1223,11 +1264,14 @@ bool product_space(int T, long long K, long long N, int group, ProductSpace* s) 
   return true;
 }
 
+struct Maps {
+  CUtensorMap w1, w2, x, act;
+};
 template <int G>
-int launch_layer(const CUtensorMap& m1, const CUtensorMap& m2, const LayerArgs& a, cudaStream_t st) {
+int launch_layer(const Maps& m, const LayerArgs& a, cudaStream_t st) {
   const long long experts = max_entries(a.T, a.K, a.E), bk = step_rows(G);
   const long long n1 = experts * ceil_div(a.F, kUnit / 2) * ceil_div(a.H, bk), n2 = experts * ceil_div(a.H, kUnit) * ceil_div(a.F, bk);
-  return launch_all(k_layer<G>, n1 > n2 ? n1 : n2, kLayerThreads, st, m1, m2, a);
+  return launch_all(k_layer<G>, n1 > n2 ? n1 : n2, kLayerThreads, st, m.w1, m.w2, m.x, m.act, a);
 }
 template <int G> int launch_product(const CUtensorMap& x, const ProductArgs& a, cudaStream_t st) {
   const long long n = ceil_div(a.N, kUnit) * ceil_div(a.K, step_rows(G));
@@ -1260,18 +1304,10 @@ extern "C" int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* sta
                          shape_of(ceil_div(K, step_rows(128)), ceil_div(N, kUnit)), whole_product(N), static_cast<uint32_t*>(ws),
                          reinterpret_cast<__nv_bfloat16*>(p), reinterpret_cast<float*>(p + s.padded), y};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // x as tiles of all its rows and 64 columns, 128-byte swizzle; beyond its edges zeros
   CUtensorMap map = {};
-  EncodeTiledFn fn = encode_fn();
-  const long long K8 = ceil_div(K, 8) * 8;
-  const cuuint64_t dims[2] = {cuuint64_t(K8), cuuint64_t(T)}, strides[1] = {cuuint64_t(K8) * 2};
-  const cuuint32_t box[2] = {64, T <= 8 ? 8u : T <= 16 ? 16u : T <= 32 ? 32u : 64u}, estr[2] = {1, 1};
-  void* from = K % 8 == 0 ? const_cast<mep_bf16*>(x) : static_cast<void*>(p);
+  const void* from = K % 8 == 0 ? static_cast<const void*>(x) : p;
   if (!on_current_device(from)) return MEP_ERR_INVALID_ARG;
-  if (fn == nullptr || fn(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, from, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return MEP_ERR_CUDA;
+  if (!make_map2(&map, from, T, ceil_div(K, 8) * 8, T <= 8 ? 8 : T <= 16 ? 16 : T <= 32 ? 32 : 64)) return MEP_ERR_CUDA;
   return group == 32   ? launch_product<32>(map, a, st)
          : group == 64 ? launch_product<64>(map, a, st)
                        : launch_product<128>(map, a, st);
@@ -1323,12 +1359,14 @@ extern "C" int mep_expert_layer(const mep_bf16* x, const int32_t* topk_idx, cons
                        reinterpret_cast<__nv_bfloat16*>(p + s.part1),
                        reinterpret_cast<__nv_bfloat16*>(out)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CUtensorMap m1 = {}, m2 = {};
+  Maps m = {};
   if (w_type == MEP_W4)
-    return group == 32   ? launch_layer<32>(m1, m2, a, st)
-           : group == 64 ? launch_layer<64>(m1, m2, a, st)
-                         : launch_layer<128>(m1, m2, a, st);
-  if (!on_current_device(w1) || !on_current_device(w2)) return MEP_ERR_INVALID_ARG;
-  if (!make_map3(&m1, w1, E, H, 2 * F) || !make_map3(&m2, w2, E, F, H)) return MEP_ERR_CUDA;
-  return launch_layer<0>(m1, m2, a, st);
+    return group == 32   ? launch_layer<32>(m, a, st)
+           : group == 64 ? launch_layer<64>(m, a, st)
+                         : launch_layer<128>(m, a, st);
+  if (!on_current_device(w1) || !on_current_device(w2) || !on_current_device(x) || !on_current_device(ws)) return MEP_ERR_INVALID_ARG;
+  if (!make_map3(&m.w1, w1, E, H, 2 * F) || !make_map3(&m.w2, w2, E, F, H) || !make_map2(&m.x, x, T, H, 1) ||
+      !make_map2(&m.act, a.act, 2LL * T * K, F, 8))
+    return MEP_ERR_CUDA;
+  return launch_layer<0>(m, a, st);
 }

@@ -12,6 +12,14 @@
 // in shared memory, and the largest is taken K times.
 // Backward, the row is zeros but for K places: built in shared memory, which
 // stays zero otherwise, and written out in vectors; bound by those bytes.
+//
+// Measured, fp32 logits, L2 flushed before: [65536, 256], K 8: 37.5 us forward,
+// 21 backward, where 71 MB each way take 10.6 at the copy rate; [65536, 384], K 8:
+// 45.7 and 23; [32768, 64], K 6: 17 and 13. Steps of the first: the largest taken
+// K times out of shared memory 78 (384 experts, as every larger number still is),
+// out of registers with the lanes' best two kept 56, the bound and the ranking of
+// what reaches it 42, the next row's values on their way 39.6, orders in two
+// operations and the softmax's maximum by one reduction 37.5.
 
 #include <math.h>
 
