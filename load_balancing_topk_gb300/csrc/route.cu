@@ -13,13 +13,15 @@
 // Backward, the row is zeros but for K places: built in shared memory, which
 // stays zero otherwise, and written out in vectors; bound by those bytes.
 //
-// Measured, fp32 logits, L2 flushed before: [65536, 256], K 8: 37.5 us forward,
+// Measured, fp32 logits, L2 flushed before: [65536, 256], K 8: 36.1 us forward,
 // 21 backward, where 71 MB each way take 10.6 at the copy rate; [65536, 384], K 8:
-// 45.7 and 23; [32768, 64], K 6: 17 and 13. Steps of the first: the largest taken
+// 44.5 and 23; [32768, 64], K 6: 17 and 13. Steps of the first: the largest taken
 // K times out of shared memory 78 (384 experts, as every larger number still is),
 // out of registers with the lanes' best two kept 56, the bound and the ranking of
 // what reaches it 42, the next row's values on their way 39.6, orders in two
-// operations and the softmax's maximum by one reduction 37.5.
+// operations and the softmax's maximum by one reduction 37.5, four maxima of the
+// bound to a turn of its loop 36.1. In bf16 40.1: equal values send some rows the
+// long way.
 
 #include <math.h>
 
@@ -69,8 +71,13 @@ __device__ __forceinline__ void put_row(const float (&l)[2], const int (&at)[2],
   }
 }
 
-// Up to 32 NV experts, K <= 32: expert lane + 32 i is value i of the lane.
-template <typename T, int NV>
+// Up to 32 NV experts, K <= 32: expert lane + 32 i is value i of the lane, or with
+// rows of whole vectors four experts next to one another are four of its values:
+// in bf16, where loads of two bytes cost more than widening eight at once (E 384, K
+// 8: 66 us without, 50 with; 512, K 16: 112 and 103; 256, K 8: 42 both). In fp32 the
+// vectors' arrival together costs more than they save (256, K 8: 38 without, 40
+// with; 384: 46 and 54).
+template <typename T, int NV, bool VEC>
 __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ logits, const float* __restrict__ bias,
                                                         long long N, int E, int K, int skip_masked,
                                                         int32_t* __restrict__ idx, float* __restrict__ w) {
@@ -81,23 +88,33 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
   uint2* found = s_found[warp];
   const long long step = (long long)gridDim.x * kWarps;
   long long row = (long long)blockIdx.x * kWarps + warp;
+  const auto expert = [&](int i) { return VEC ? 128 * (i / 4) + 4 * lane + i % 4 : lane + 32 * i; };
   float v[NV];  // of the next row, on its way while this one is worked on
   const auto load = [&](long long r) {
+    if (VEC) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = r < N && lane + 32 * i < E ? to_f32(logits[r * E + lane + 32 * i]) : 0.f;
+      for (int i = 0; i < NV; i += 4) {
+        const uint2 f = r < N && expert(i) < E ? *reinterpret_cast<const uint2*>(logits + r * E + expert(i)) : make_uint2(0u, 0u);
+        v[i] = __uint_as_float(f.x << 16), v[i + 1] = __uint_as_float(f.x & 0xffff0000u);
+        v[i + 2] = __uint_as_float(f.y << 16), v[i + 3] = __uint_as_float(f.y & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] = r < N && expert(i) < E ? to_f32(logits[r * E + expert(i)]) : 0.f;
+    }
   };
   load(row);
   for (; row < N; row += step) {
     uint32_t key[NV], most = 0;  // 0: no expert
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
+      const int e = expert(i);
       key[i] = e < E ? order_of(bias == nullptr ? v[i] : v[i] + bias[e]) : 0u;
       most = max(most, key[i]);
     }
     load(row + step);
     uint32_t bound = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int k = 0; k < K; ++k) {
       bound = __reduce_max_sync(MEP_FULL_MASK, most);
       if (most == bound) most = 0;
@@ -114,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
       at -= count;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (key[i] >= bound) found[at++] = make_uint2(key[i], lane + 32 * i);
+        if (key[i] >= bound) found[at++] = make_uint2(key[i], expert(i));
       __syncwarp();
       const uint2 f = lane < all ? found[lane] : make_uint2(0u, 0u);
       mine = int(f.y), order = f.x, rank = lane < all ? 0 : 32;
@@ -133,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) k_route_few(const T* __restrict__ lo
         int e = 0x7fffffff;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int here = lane + 32 * i;
+          const int here = expert(i);
           if ((key[i] < last || (key[i] == last && here > last_at)) && key[i] > best) best = key[i], e = here;
         }
         last = __reduce_max_sync(MEP_FULL_MASK, best);
@@ -291,11 +308,13 @@ int route(const T* logits, const float* bias, int64_t N, int E, int K, int skip_
           cudaStream_t st) {
   const auto few = [&](auto kernel) { return launch_rows(kernel, N, 0, st, logits, bias, N, E, K, skip_masked, idx, w); };
   if (K > 32) return launch_rows(k_route<T>, N, kWarps * E * 4, st, logits, bias, N, E, K, skip_masked, idx, w);
-  if (E <= 32) return few(k_route_few<T, 1>);
-  if (E <= 64) return few(k_route_few<T, 2>);
-  if (E <= 128) return few(k_route_few<T, 4>);
-  if (E <= 256) return few(k_route_few<T, 8>);
-  if (E <= 512) return few(k_route_few<T, 16>);
+  if (E <= 32) return few(k_route_few<T, 1, false>);
+  if (E <= 64) return few(k_route_few<T, 2, false>);
+  constexpr bool V = sizeof(T) == 2;  // fp32 has no such form
+  const bool vec = V && E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % 8 == 0;
+  if (E <= 128) return few(vec ? k_route_few<T, 4, V> : k_route_few<T, 4, false>);
+  if (E <= 256) return few(vec ? k_route_few<T, 8, V> : k_route_few<T, 8, false>);
+  if (E <= 512) return few(vec ? k_route_few<T, 16, V> : k_route_few<T, 16, false>);
   return launch_rows(k_route<T>, N, kWarps * E * 4, st, logits, bias, N, E, K, skip_masked, idx, w);
 }
 template <typename T>
