@@ -67,3 +67,30 @@ def test_four_bits_stay_near_sixteen():
     places = torch.arange(16, device="cuda")
     a, b = four.step(x, places)[0], sixteen.step(x, places)[0]
     assert 0.02 < rel(a - x, b - x) < 0.4
+
+
+def test_tensors_that_are_mapped_must_be_the_devices_own():
+    """Host memory, even pinned, behind a tensor map is refused by the library before anything is enqueued."""
+    lib, T, K, N = mep.load_library(), 4, 64, 64
+    dev = dict(dtype=torch.bfloat16, device="cuda")
+    x, host = torch.zeros(T, K, **dev), torch.zeros(T, K, dtype=torch.bfloat16).pin_memory()
+    w4, y = mep.mep_w4_save(torch.zeros(K, N, device="cuda")), torch.full((T, N), 3.0, **dev)
+    ws = torch.empty(mep.w4_product_workspace_bytes(T, K, N), dtype=torch.uint8, device="cuda")
+    bad = mep.STATUS_CODE["MEP_ERR_INVALID_ARG"]
+
+    def product(x):
+        return lib.mep_w4_product(x.data_ptr(), w4.data_ptr(), None, T, K, N, 128, ws.data_ptr(), ws.numel(), 0, y.data_ptr(), None)
+
+    assert product(host) == bad and product(x) == 0
+    idx, w = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+    w1, w2, out = torch.zeros(2, K, 2 * N, **dev), torch.zeros(2, N, K, **dev), torch.empty(T, K, **dev)
+    need = mep.expert_layer_workspace_bytes(T, 1, 2, K, N)
+    room, host_room = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.empty(need, dtype=torch.uint8).pin_memory()
+
+    def layer(x, w1, ws):
+        return lib.mep_expert_layer(x.data_ptr(), idx.data_ptr(), w.data_ptr(), w1.data_ptr(), w2.data_ptr(), 0, 128, None, T, 1, 2, K, N,
+                                    ws.data_ptr(), ws.numel(), out.data_ptr(), None)
+
+    assert layer(host, w1, room) == bad and layer(x, w1.cpu().pin_memory(), room) == bad and layer(x, w1, host_room) == bad
+    assert layer(x, w1, room) == 0
+    torch.cuda.synchronize()
