@@ -36,15 +36,14 @@
 //
 // Measured, as one node of a graph, L2 flushed before it (back to back):
 //   64 tokens, 256 experts, 7168 x 1408, 8 each, bf16: 12.2 GB of weights in
-//     1750 to 1790 us (1710 to 1750), 6.8 to 7.1 TB/s; the same without the products.
-//   16 tokens of it in 4 bits: 1.24 GB in 281 us (265). Without the products the
-//     copies take 226, without the copies the products 244: a stage's 65536
-//     weights keep eight warps busy for some 1200 clocks, in which they issue
-//     nine operations for eight weights to widen them, and a unit's sums cost 700
-//     to 2000 more. Sixteen warps of half the columns each took 294, where eight
-//     took 283; both blocks of a stage in one go 308, where one after another took
-//     302.
-//   1 token in 4 bits: 125 MB in 48 us (43); 1 token, 64 experts, 2048 x 1408, 6
+//     1746 to 1790 us (1693 to 1750), 6.8 to 7.1 TB/s; the same without the products.
+//   16 tokens of it in 4 bits: 1.24 GB in 260 us (244). Without the products the
+//     copies take 226, and the products hide behind them but for a unit's start and
+//     its sums: a stage's 65536 weights keep eight warps busy for some 1000 clocks,
+//     in which they issue nine operations for eight weights to widen them. Sixteen
+//     warps of half the columns each took 294, where eight took 283; both blocks of
+//     a stage in one go 308, where one after another took 302.
+//   1 token in 4 bits: 125 MB in 48 us (42); 1 token, 64 experts, 2048 x 1408, 6
 //     each, bf16: 104 MB in 40 us (32). A launch with its first loads is some 5,
 //     the list 2.8, a barrier 1.3; the rest is the stream with its start and its
 //     slowest SM (some read a fifth slower than others).
@@ -209,7 +208,7 @@ struct Weights {
 // (x is the map's, its box the tile), in the layer from bf16 four rows of the list
 // in one or, of the activation, whose rows are in the list's order, eight (a lane
 // issues a copy in some 80 clocks: 64 tokens, 8 each of 32 experts, 7168 x 1408,
-// row by row 515 us, so 376). In 4 bits, where a step has four times the columns
+// row by row 515 us, so 370 to 376). In 4 bits, where a step has four times the columns
 // and tiles would be four times as many copies, the layer copies row by row.
 struct Rows {
   const CUtensorMap* map;
@@ -533,8 +532,12 @@ __device__ __forceinline__ void stage_product(float (&acc)[2][NT][4], uint32_t s
     }
   } else {
     // Everything that a block of 128 rows needs of the stage is asked for at once;
-    // with more than 32 rows of x the block is gone through again.
-    constexpr int NS = NT < 4 ? NT : 4, block = w4_block_bytes(G > 0 ? G : 128), per = G > 0 ? G / 32 : 1;  // groups: per * 32 rows
+    // with more than 32 rows of x the block is gone through again. In the layer, where
+    // that is rare, for every 16 of them: with 32 at once the registers ran short in
+    // the instantiations for fewer rows too (16 tokens, 256 experts, 7168 x 1408: 281
+    // us, 260 this way; 64 tokens, 6 each of 64, 2048 x 1408: 126 and 112). The
+    // product, of which 64 rows are no rare case, takes 32 (74 us; 87 by 16).
+    constexpr int NS = NT < 4 ? NT : NT == 8 && !TILES ? 2 : 4, block = w4_block_bytes(G > 0 ? G : 128), per = G > 0 ? G / 32 : 1;  // groups: per * 32 rows
     constexpr bool early = NT <= 2;                                                                       // x too
     uint4 w[2][2];
     uint32_t x[early ? 4 : 1][early ? NS : 1][4], scale[4][2];
