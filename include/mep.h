@@ -548,7 +548,8 @@ MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
  *   dtopk_w, topk_w  fp32 [N, K];  topk_idx int32 [N, K]
  *   status   int32 [1]             read on entry (nonzero: no-op); set to
  *                                  MEP_ERR_BAD_ROUTING if an index is outside
- *                                  [-1, E) (it counts as -1). May be NULL.
+ *                                  [-1, E) (it counts as -1), after the last row
+ *                                  is written, by a launch of its own. May be NULL.
  *   dlogits  bf16 or fp32 [N, E]   type; output, every element written
  * Outputs must not overlap the inputs or one another. N < 2^31.
  * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
