@@ -1019,9 +1019,11 @@ __global__ void __launch_bounds__(kLayerThreads, 1)
         products<G, TILES, kChunk / 4>(r, c, phase < 0 ? kDry : kReal, 1,
                                        [&](const Part& part, int q, int col, int row, float v0, float v1) {
                                          if (col + q * o.inner >= part.columns) return;
-                                         // the two rows: the activation's two of one token; else two tokens
+                                         // the two rows: the activation's two of one token; else two tokens. An
+                                         // infinite weight makes the first one's sum what it is to be, and the
+                                         // second's anything (infinity times 0 or times the other sign)
                                          float* to = out + part.to + (long long)(second ? row >> 1 : row) * pitch + q * o.half + col;
-                                         *to = second ? v0 + v1 : v0;
+                                         *to = second && isfinite(v0) ? v0 + v1 : v0;
                                          if (!second && row + 1 < part.rows) to[pitch] = v1;
                                        });
         if (phase < 0) {

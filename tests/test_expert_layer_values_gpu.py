@@ -1,0 +1,84 @@
+"""The layer's results where floating point ends: infinite weights and activations.
+
+Inputs are whole numbers, so that the formula's value is exact."""
+
+import pytest
+import torch
+
+import load_balancing_topk_gb300 as mep
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def layer(w1, w2, x, idx, w, **kw):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = mep.mep_expert_layer(x, idx, w, w1, w2, status, **kw)
+    assert int(status) == 0
+    return out
+
+
+def whole(H, F, T, seed, E=2):
+    """x, w1 and gates and ups in 64 bits: x[t, 0] = 1 and one more column of x is t's own, so that a gate is 20 + t % 8
+    (fp32's silu of it is itself) and an up runs through -120 .. 120 without 0; activations are whole, up to 3240."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.zeros(T, H)
+    x[:, 0] = 1
+    x[:, 1] = torch.arange(T) % 8
+    x[:, H - 1] = 1
+    w1 = torch.zeros(E, H, 2 * F)
+    w1[:, 0, :F] = 20
+    w1[:, 1, :F] = 1
+    up = torch.randint(1, 121, (E, F), generator=g) * (1 - 2 * torch.randint(0, 2, (E, F), generator=g))
+    w1[:, H - 1, F:] = up.float()
+    a = (20 + torch.arange(T) % 8)[None, :, None].double() * up[:, None, :].double()  # [E, T, F]
+    return x.bfloat16().cuda(), w1.bfloat16().cuda(), a.cuda()
+
+
+def same(got, want):
+    """bf16 values equal to 64-bit ones that fp32 holds; any NaN is a NaN."""
+    want = want.float().bfloat16()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got[~nan], want[~nan]), int((got[~nan] != want[~nan]).sum())
+
+
+@pytest.mark.parametrize("H,F,T", [(64, 32, 5), (256, 200, 40), (2048, 1408, 8), (7168, 1408, 3)])
+def test_an_infinite_weight_of_the_second_product(H, F, T):
+    """A single infinity in a column makes the result infinite, of the activation's sign times its own; two of opposite
+    signs make it NaN; the other columns are as they would be."""
+    x, w1, a = whole(H, F, T, 1)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w2 = torch.randint(-1, 2, (2, F, H), generator=g, device="cuda").bfloat16()
+    for h, rows in ((0, [0]), (1, [F - 1]), (H // 2, [F // 2]), (H - 1, [7]), (9, [0, F - 1]), (17, [3, 4])):
+        for n, f in enumerate(rows):
+            w2[0, f, h] = INF if (h + n) % 2 else -INF
+    w2[0, :, 25] = INF  # NaN where activations of both signs meet it
+    w2[1, 2, 30] = -INF
+    idx = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda").repeat(T, 1)
+    idx[-1, 0] = -1
+    w = torch.tensor([[1.0, 2.0]], device="cuda").repeat(T, 1)
+    got = layer(w1, w2, x, idx, w)
+    want = 2 * (a[1] @ w2[1].double())
+    want[:-1] += (a[0] @ w2[0].double())[:-1]
+    assert torch.isinf(want[0, [0, 1, H // 2, H - 1, 30]]).all() and torch.isnan(want[0, 25]) and torch.isfinite(want[-1, :30]).all()
+    same(got, want)
+
+
+@pytest.mark.parametrize("side", [1, -1])
+def test_an_infinite_activation(side):
+    """A gate times an up beyond fp32: the columns that it meets are infinite, nothing is NaN but where the weight is 0."""
+    H, F, T = 136, 72, 9
+    x, w1, a = whole(H, F, T, 3)
+    w1[0, 1, F + 5] = side * 3e38
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w2 = torch.randint(0, 2, (2, F, H), generator=g, device="cuda").mul(2).sub(1).bfloat16()
+    w2[0, 5, 11] = 0
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    got = layer(w1, w2, x, idx, torch.ones(T, 1, device="cuda"))
+    act = a[0].clone()
+    act[1:, 5] = side * INF  # x[t, 1] is 0 for tokens 0 and 8
+    act[8, 5] = a[0, 8, 5]
+    want = act @ w2[0].double()
+    assert torch.isinf(want[3]).sum() == H - 1 and torch.isnan(want[3, 11]) and torch.isfinite(want[[0, 8]]).all()
+    same(got, want)
