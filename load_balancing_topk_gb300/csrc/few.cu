@@ -856,6 +856,17 @@ template <int G> __device__ __forceinline__ Weights second_weights(const LayerAr
   return {map, a.w2, m, q, 2 * q, 4, 2 * kW4Cols, a.H, false, a.F};
 }
 
+// silu(g) * u. Below -88, where e^-g leaves fp32, 1 + e^-g is e^-g to 2^-126: g *
+// e^g * u, with e^g as the square of e^(g/2), u between the two factors, is what
+// fp32 holds of it (g = -100 and u = 1e38 make -3.7e-4; a quotient flushed to 0).
+__device__ __forceinline__ float silu_times(float g, float u) {
+  if (g < -88.f) {
+    const float h = expf(0.5f * g);
+    return g * h * u * h;
+  }
+  return g / (1.f + expf(-g)) * u;
+}
+
 // The activation of n quads of columns: the first product's parts added up, in
 // order, then silu(g) * u as two bf16.
 __device__ __forceinline__ void activate(const LayerArgs& a, const Phase& p, const Lists& l, uint32_t n, Spread s, bool dry) {
@@ -877,7 +888,7 @@ __device__ __forceinline__ void activate(const LayerArgs& a, const Phase& p, con
     __nv_bfloat16 hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float v = g[k] / (1.f + expf(-g[k])) * u[k];
+      const float v = silu_times(g[k], u[k]);
       hi[k] = __float2bfloat16_rn(v);
       const float rest = v - __bfloat162float(hi[k]);
       lo[k] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);  // an infinity stays one

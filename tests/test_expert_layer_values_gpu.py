@@ -1,6 +1,7 @@
-"""The layer's results where floating point ends: infinite weights and activations.
+"""The layer's results where floating point ends: infinite weights and activations, gates whose silu is tiny.
 
-Inputs are whole numbers, so that the formula's value is exact."""
+Inputs are whole numbers or powers of two where that makes the formula's value exact; elsewhere the bound is what the
+header promises: an activation off by 2^-16 of itself (2^-20 more for exp, division and products), a result by 2^-8."""
 
 import pytest
 import torch
@@ -82,3 +83,47 @@ def test_an_infinite_activation(side):
     want = act @ w2[0].double()
     assert torch.isinf(want[3]).sum() == H - 1 and torch.isnan(want[3, 11]) and torch.isfinite(want[[0, 8]]).all()
     same(got, want)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_gates_whose_sigmoid_is_tiny(group):
+    """From -87 down to -104 silu is 1e-37 to 1e-43 of 1, which an up of 1e38 makes an ordinary activation."""
+    H, F, T = 64, 128, 4
+    gates = -torch.linspace(86.5, 104, F).bfloat16().float()
+    x = torch.zeros(T, H).bfloat16().cuda()
+    x[:, 0], x[:, 40] = 1, torch.tensor([1, -1, 0.5, 2]).cuda()
+    w1 = torch.zeros(1, H, 2 * F)
+    w1[0, 0, :F], w1[0, 40, F:] = gates, 1e38
+    w2 = torch.zeros(1, F, H)
+    w2[0, torch.arange(F), torch.arange(F) % H] = torch.where(torch.arange(F) < H, 1.0, 0.0)
+    w2b = w2.roll(H, 1)  # the second half of the gates
+    w1 = w1.bfloat16().cuda()
+    kind, q1, v1 = {}, w1, w1
+    if group:
+        q1, kind = mep.mep_w4_save(w1, group, parts=2), dict(F=F, group=group)
+        v1 = mep.mep_w4_load(q1, H, 2 * F, group, dtype=torch.float32)
+    gu = x.double() @ v1[0].double()
+    g, u = gu[:, :F], gu[:, F:]
+    a = g / (1 + torch.exp(-g)) * u
+    idx, w = torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda")
+    for m in (w2, w2b):
+        q2 = v2 = m.bfloat16().cuda()
+        if group:
+            q2 = mep.mep_w4_save(q2, group)
+            v2 = mep.mep_w4_load(q2, F, H, group, dtype=torch.float32)
+        got = layer(q1, q2, x, idx, w, **kind)
+        want = a @ v2[0].double()
+        assert float(want.abs().min()) > 1e-6
+        assert ((got.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -16 + 2.0 ** -19) * want.abs()).all()
+
+
+def test_gates_further_out_are_zeros():
+    """Below that the activation leaves fp32: zeros, whatever the sign, never NaN."""
+    H, F, T = 64, 128, 2
+    x, w1 = torch.zeros(T, H, device="cuda").bfloat16(), torch.zeros(1, H, 2 * F, device="cuda").bfloat16()
+    x[:, 0] = torch.tensor([1, 2]).cuda()
+    w1[0, 0, :F] = -torch.logspace(2.7, 37.9, F, device="cuda")
+    w1[0, 0, F:] = 1e30
+    w2 = torch.ones(1, F, H, device="cuda").bfloat16()
+    got = layer(w1, w2, x, torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda"))
+    assert (got == 0).all()
