@@ -867,6 +867,8 @@ __device__ __forceinline__ float silu_times(float g, float u) {
   return g / (1.f + expf(-g)) * u;
 }
 
+constexpr float kTopBf16 = 255.f * 0x1p120f;  // bf16's largest number
+
 // The activation of n quads of columns: the first product's parts added up, in
 // order, then silu(g) * u as two bf16.
 __device__ __forceinline__ void activate(const LayerArgs& a, const Phase& p, const Lists& l, uint32_t n, Spread s, bool dry) {
@@ -889,7 +891,8 @@ __device__ __forceinline__ void activate(const LayerArgs& a, const Phase& p, con
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float v = silu_times(g[k], u[k]);
-      hi[k] = __float2bfloat16_rn(v);
+      const bool beyond = fabsf(v) > kTopBf16 && !isinf(v);  // a number in fp32, which rounding might make an infinity
+      hi[k] = __float2bfloat16_rn(beyond ? copysignf(kTopBf16, v) : v);
       const float rest = v - __bfloat162float(hi[k]);
       lo[k] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);  // an infinity stays one
     }

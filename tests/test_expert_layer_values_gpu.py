@@ -1,4 +1,5 @@
-"""The layer's results where floating point ends: infinite weights and activations, gates whose silu is tiny.
+"""The layer's results where floating point ends: infinite weights and activations, gates whose silu is tiny, activations
+between bf16's largest number and fp32's.
 
 Inputs are whole numbers or powers of two where that makes the formula's value exact; elsewhere the bound is what the
 header promises: an activation off by 2^-16 of itself (2^-20 more for exp, division and products), a result by 2^-8."""
@@ -127,3 +128,25 @@ def test_gates_further_out_are_zeros():
     w2 = torch.ones(1, F, H, device="cuda").bfloat16()
     got = layer(w1, w2, x, torch.zeros(T, 1, dtype=torch.int32, device="cuda"), torch.ones(T, 1, device="cuda"))
     assert (got == 0).all()
+
+
+def test_activations_between_the_largest_bf16_and_the_largest_fp32():
+    """3.3965e38 rounds to infinity in bf16 and is a number in fp32; times 2^-30 it is an ordinary result."""
+    H, F, T = 64, 8, 2
+    top_bf16, top = float(torch.finfo(torch.bfloat16).max), float(torch.finfo(torch.float32).max)
+    gates = torch.arange(17, 250).double()
+    ups = (torch.arange(128, 256).double() * 2.0 ** 113)[:, None] * 2.0 ** -torch.arange(0, 9).double()[None, :]
+    a = gates[:, None, None] * ups
+    at = torch.nonzero((a > (top_bf16 + 2.0 ** 128) / 2) & (a < top * (1 - 2.0 ** -10)))
+    at = at[torch.linspace(0, len(at) - 1, F).long()]
+    gate, up = gates[at[:, 0]], ups[at[:, 1], at[:, 2]]
+    x, w1, w2 = torch.zeros(T, H), torch.zeros(1, H, 2 * F), torch.zeros(1, F, H)
+    x[:, 0], x[0, 33], x[1, 33] = 1, 1, -1
+    w1[0, 0, :F], w1[0, 33, F:] = gate.float(), up.float()
+    w2[0, torch.arange(F), torch.arange(F)] = 2.0 ** -30
+    got = layer(w1.bfloat16().cuda(), w2.bfloat16().cuda(), x.bfloat16().cuda(), torch.zeros(T, 1, dtype=torch.int32, device="cuda"),
+                torch.ones(T, 1, device="cuda"))
+    want = (gate * up * 2.0 ** -30).cuda()
+    for t, sign in ((0, 1), (1, -1)):
+        assert ((got[t, :F].double() - sign * want).abs() <= (2.0 ** -8 + 2.0 ** -16 + 2.0 ** -20) * want).all(), got[t, :F]
+    assert (got[:, F:] == 0).all()
