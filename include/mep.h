@@ -256,7 +256,8 @@ MEP_API int mep_plan_static_scratch(const int32_t* topk_idx, int R, int S, int K
  *   dst_pos  int32 [R*S, K]    from mep_plan
  *   status   int32 [1]         read on entry (nonzero: no-op); set to
  *                              MEP_ERR_BAD_POSITION if an entry is out of
- *                              range (that row is skipped). May be NULL.
+ *                              range (that row is skipped; what of the output
+ *                              is written then is open). May be NULL.
  *   buf      bf16 [R*S*K, H]   output; must not overlap hidden
  * Host returns: MEP_OK, MEP_ERR_INVALID_ARG, MEP_ERR_CUDA.
  */
@@ -529,8 +530,8 @@ MEP_API int mep_grouped_wgrad(const void* x, int x_type, const mep_bf16* dy,
  *              everything;
  *   topk_w   = softmax over the chosen experts' logits (without the bias), in
  *              fp32.
- * A logit of -infinity masks its expert: it is chosen last and its weight is 0;
- * a token without any other logit has weights 0 throughout. With skip_masked
+ * A logit of -infinity masks its expert: its weight is 0, and where biases are
+ * finite (and keep the others' sums so) it is chosen last; a token without any other logit has weights 0 throughout. With skip_masked
  * a masked expert's index is -1, which mep_expert_layer passes over (mep_plan
  * wants K experts of every token). An infinity or a NaN among the chosen
  * makes the token's weights NaN.
@@ -565,7 +566,8 @@ MEP_API int mep_route_backward(const float* dtopk_w, const float* topk_w, const 
  * group of rows of a column, and their values back. (The pages keep weights in
  * one type; the format is this library's.) A column's rows are taken in groups
  * of 32, 64 or 128. With a = the group's largest magnitude its scale is
- * s = bf16_rn(a * (1/7)) (a product in fp32, by fp32's 1/7), q = w / s rounded
+ * s = bf16_rn(a * (1/7)) (a product in fp32, by fp32's 1/7: bf16_rn(a / 7) but
+ * for 140 of 2^24 fp32 magnitudes), q = w / s rounded
  * to nearest-even and kept within +-7, and the value is q * s (0 where s is 0;
  * NaN where the group holds an infinity or a NaN).
  * A matrix of K rows and N columns is mep_w4_bytes(K, N, group) bytes: panels
@@ -620,14 +622,15 @@ MEP_API int mep_w4_product(const mep_bf16* x, const uint8_t* w4, int32_t* status
  * of each of up to 64 sequences: what mep_plan .. mep_combine compute with the
  * two projections and mep_swiglu between them, from the home experts' weights,
  * without plan, buffer or slots (with so few tokens the path's time is the
- * weights' bytes, and every expert's are read once whatever the balance). With
+ * weights' bytes, and an expert's are read once for up to 32 of its tokens). With
  * e = topk_idx[t,k]:
  *   a[t,k] = silu(x[t] . w1[e][:, :F]) * (x[t] . w1[e][:, F:])
  *   out[t] = bf16_rn( sum_k topk_w[t,k] * (a[t,k] . w2[e]) )
  * with sums in fp32 (the tensor cores', order fixed: the same call gives the
  * same bits). The second product takes a as two bf16, the value rounded and
- * what that left over, so that a is off by 2^-16 of itself at most; nothing
- * else is rounded to fewer than 32 bits before out.
+ * what that left over, so that a is off by 2^-16 of itself or by 2^-134 at most;
+ * nothing else is rounded to fewer than 32 bits before out. Infinities and NaN go
+ * as in the formula, a below 2^-134 counting as 0.
  *   x        bf16 [T, H]     0 <= T <= MEP_MAX_FEW
  *   topk_idx int32 [T, K]    in [-1, E), distinct per row but for -1, which
  *                            stands for no expert (the empty places of a padded

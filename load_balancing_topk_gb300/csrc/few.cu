@@ -11,7 +11,7 @@
 // A unit of work is 256 columns of one expert (128 gate and the 128 matching up
 // columns, or 256 columns of the second product) times the expert's tokens, up
 // to 32 in the layer; a step is a stage's share of a unit's sum: 64 rows of bf16
-// (32 KB), 256 of 4 bits (34 to 40 KB). The steps of all units in a row are cut
+// (32 KB), 256 of 4 bits (33 to 36 KB). The steps of all units in a row are cut
 // into runs without regard to where units end, so that every SM reads about as
 // many bytes as the others whatever the number of experts and columns (Phase);
 // a unit that is cut leaves a partial sum for each of its runs, in fp32 in the
@@ -31,8 +31,11 @@
 // operand of four steps (w4.cuh): a mask and a packed multiply-add make two of
 // them q / 64 exactly, and the scale multiplies the group's fp32 sums.
 // The activation is kept as two bf16, the value rounded and what that left
-// over, and the second product takes both: it is then off by 2^-16 at most,
-// where one bf16 would be off by 2^-8. bf16 x bf16 is exact in fp32.
+// over, and the second product takes both: it is then off by 2^-17 of itself at
+// most (below 2^-117 by 2^-134, half of bf16's smallest number), where one bf16
+// would be off by 2^-8. bf16 x bf16 is exact in fp32. Of the results of 64 tokens of
+// the large layer 0.46% round to the other side than the 64-bit value does, 0.15%
+// with fp32 throughout; the error in the norm is 1.658e-3 for both, the rounding.
 //
 // Measured, as one node of a graph, L2 flushed before it (back to back):
 //   64 tokens, 256 experts, 7168 x 1408, 8 each, bf16: 12.2 GB of weights in
@@ -51,7 +54,9 @@
 //     that the code is run through before its data is there (products(), k_layer).
 //   [1, 7168] x [7168, 7168] in 4 bits 20 us (16.5), [64, 2048] x [2048, 65536]
 //     74 us (70), without the products 40: at 64 rows they are 34 us of the
-//     tensor pipe, and x comes from L2 once a step.
+//     tensor pipe, and x comes from L2 once a step. In groups of 64 rows it takes
+//     83, of 32 rows 91: more scales, and more registers than a thread has (88 to
+//     200 bytes of them spilled).
 
 #include <cooperative_groups.h>
 

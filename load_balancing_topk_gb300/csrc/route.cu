@@ -11,11 +11,14 @@
 // times. What bounds it is what a warp has to issue. More experts: the orders lie
 // in shared memory, and the largest is taken K times.
 // Backward, the row is zeros but for K places: built in shared memory, which
-// stays zero otherwise, and written out in vectors; bound by those bytes.
+// stays zero otherwise, and written out in vectors. What bounds it is again a
+// warp's row: half the issue slots are taken, and its bytes alone would take half
+// the time.
 //
-// Measured, fp32 logits, L2 flushed before: [65536, 256], K 8: 36.1 us forward,
-// 21 backward, where 71 MB each way take 10.6 at the copy rate; [65536, 384], K 8:
-// 44.5 and 23; [32768, 64], K 6: 17 and 13. Steps of the first: the largest taken
+// Measured, fp32 logits, L2 flushed before: [65536, 256], K 8: 36.4 us forward,
+// 21.6 backward, where 71 MB each way take 10.7 at the copy rate (bf16 40 and 19.6,
+// 5.6); [65536, 384], K 8: 46 and 26 (16); [32768, 64], K 6: 17.5 and 13.4 (1.5);
+// [65536, 640], K 8: 100 and 34 (26); [65536, 256], K 40: 194 and 138 (13). Steps of the first: the largest taken
 // K times out of shared memory 78 (384 experts, as every larger number still is),
 // out of registers with the lanes' best two kept 56, the bound and the ranking of
 // what reaches it 42, the next row's values on their way 39.6, orders in two

@@ -16,14 +16,20 @@
 //         a whole number, ties to even, and four of them become 16 bits of pairs
 //         by multiply-adds. Scales below 2^-100, whose reciprocal or remainder
 //         may leave fp32, divide, and keep within +-7, which others do anyway.
+//         The scale is a product by fp32's 1/7, not a quotient: that is what
+//         dividing a tensor by 7 is on the GPU in elementary tensor operations, whose
+//         bytes these are then. The two round to different bf16 for 140 of 2^24
+//         fp32 magnitudes, for none that a bf16 holds.
 //   load  In bf16 two weights at once: the bits of q + 8 are a bf16 of q / 64
 //         after one multiply-add (few.cu), and that times 64 s is rounded once.
 //         Scales from 2^120 on go the other way, through fp32, like fp32 output.
 //
 // Measured, L2 flushed before: bf16 [64, 2048, 2816] saved in 254 us and loaded in
 // 146, where 929 MB each way take 139 at the copy rate (55%, 95%); fp32 [16, 2048,
-// 2816] 103 and 68 (416 MB, 62: 60%, 91%); bf16 [16, 2047, 2817] 142 and 117 (232
-// MB, 35). Read by a lane from where its pairs' values lie, without the shared
+// 2816] 103 and 68 (416 MB, 62: 60%, 91%). Element by element, bf16 [16, 2047,
+// 2817] 143 and 118 (232 MB, 35), fp32 169 and 112 (62): bound by the accesses, two
+// or four bytes a lane; the aligned vectors that cover a row, shifted on their way
+// through shared memory, are not built. Read by a lane from where its pairs' values lie, without the shared
 // memory, the first took 1640 both ways; through it 558; with packed maxima,
 // corrected quotients and pairs by multiply-adds 400.
 
